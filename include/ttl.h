@@ -53,6 +53,9 @@ typedef uint16_t ttl_bf16;
 
 #define TTL_MAX_SHARDS 16     /* largest t (and g) accepted                             */
 
+#define TTL_T_BF16 0          /* element types of ttl_layer_norm_*                       */
+#define TTL_T_F32 1
+
 #define TTL_ACT_GELU_TANH 0   /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)))         */
 #define TTL_ACT_SWIGLU 1      /* SiLU(x Wg) * (x Wu), no bias                            */
 
@@ -90,6 +93,7 @@ int ttl_selftest_wait_timeout(int64_t timeout_us, void* stream);
 #define TTL_K_EMBED 9       /* vocab-parallel embedding lookup / gradient     */
 #define TTL_K_SOFTMAX 10    /* attention row softmax / softmax backward       */
 #define TTL_K_ATTN_CORE 11  /* fused attention cores (scores, softmax, P V)  */
+#define TTL_K_NORM 12       /* layer norm forward / backward                  */
 
 /* Starts (on != 0) or stops tracing on this process.  While on, every kernel launch the
  * library makes is bracketed by a pair of CUDA events recorded on the launch stream, and
@@ -379,6 +383,94 @@ int ttl_tp_attn_bwd(int t, int64_t T, int64_t h, int n_q, int n_kv, int d, const
                     const ttl_bf16* const* P_save, const ttl_bf16* const* O_save, ttl_bf16* const* dWq,
                     ttl_bf16* const* dWk, ttl_bf16* const* dWv, ttl_bf16* const* dWo, ttl_bf16* const* dX,
                     void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ layer norm */
+
+/* Layer norm with the residual sum in front, over t token slabs of `rows` rows each ([TPSP]
+ * "SP": LayerNorm and the residual run on the s/t tokens of each shard; t = 1 is the whole
+ * sequence).  For every row, s = x (or x + r, rounded to the stream's type) and
+ *   y = (s - mean) rstd gamma + beta,  rstd = 1 / sqrt(mean((s - mean)^2) + eps)
+ *   X[i], R[i]  [rows,h] row strides ldx, ldr (elements); R NULL = no residual
+ *   gamma, beta [h]      beta NULL = none
+ *   S[i]        [rows,h] out: the sum (given exactly when R is); the backward pass's X
+ *   Y[i]        [rows,h] out        mean[i], rstd[i] [rows] fp32 out, for the backward pass
+ * X, R, S and Y hold x_type elements, gamma and beta w_type (TTL_T_BF16 or TTL_T_F32).  Any
+ * h >= 1; pointers and strides need only their elements' alignment (16-byte aligned rows of a
+ * whole number of 16-byte words are faster).  Sums are fp32.  No output may alias an input or
+ * another output. */
+int ttl_layer_norm_fwd(int t, int64_t rows, int64_t h, int x_type, int w_type, const void* const* X, int64_t ldx,
+                       const void* const* R, int64_t ldr, const void* gamma, const void* beta, float eps,
+                       void* const* S, void* const* Y, float* const* mean, float* const* rstd, void* stream);
+
+/* Bytes of the workspace of ttl_layer_norm_bwd (partial weight gradients); 0 for bad arguments. */
+size_t ttl_layer_norm_bwd_workspace_size(int t, int64_t rows, int64_t h);
+
+/* Backward of ttl_layer_norm_fwd.  X is the normalised input (S where there was a residual).
+ * With xhat = (x - mean) rstd and g = dy gamma:
+ *   dX = rstd (g - mean(g) - xhat mean(g xhat)) (+ dS)     (also the residual's gradient)
+ *   dgamma (+)= sum over all slabs' rows of dy xhat, dbeta (+)= sum of dy
+ *   dY[i], dS[i] [rows,h] row strides lddy, ldds; dS NULL = none (the gradient that reaches the
+ *                sum past the block)
+ *   dX[i] [rows,h] out;  dgamma, dbeta [h] fp32 (dbeta NULL = not wanted), written, or added to
+ *                with accumulate = 1
+ * The weight gradients are summed in a fixed order: the same inputs give the same bits. */
+int ttl_layer_norm_bwd(int t, int64_t rows, int64_t h, int x_type, int w_type, const void* const* X, int64_t ldx,
+                       const void* const* dY, int64_t lddy, const void* const* dS, int64_t ldds, const void* gamma,
+                       const float* const* mean, const float* const* rstd, void* const* dX, float* dgamma,
+                       float* dbeta, int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ scaled embedding, sorted gradient */
+
+/* ttl_vocab_parallel_embedding_fwd (fused gather) with a factor: out[i][tok] = bf16(scale
+ * E[id(tok)]) in every one of the t buffers, one rounding.  An id outside [0,V) sets
+ * TTL_ERR_DEVICE in the status word and gives a zero row.  h a multiple of 8. */
+int ttl_vocab_parallel_embedding_scaled_fwd(int t, int64_t T, int64_t h, int64_t V, const int64_t* ids,
+                                            const ttl_bf16* const* E, float scale, ttl_bf16* const* out,
+                                            void* stream);
+
+/* Workspace bytes of ttl_vocab_parallel_embedding_sorted_bwd (the sorted tokens and the partial
+ * sums); 0 for bad arguments. */
+size_t ttl_vocab_parallel_embedding_sorted_bwd_workspace_size(int t, int64_t T, int64_t h, int64_t V);
+
+/* Its backward: dE[i][v - i V/t] (+)= scale sum over the tokens of id v of dY[tok], fp32.
+ * accumulate = 0 writes every row of dE (zeros where no token has the id), accumulate = 1 adds
+ * to the rows that have tokens.  The tokens are sorted by id and summed in a fixed order: the
+ * same inputs give the same bits.  dY [T,h] with row stride lddy (a multiple of 8).  Tokens
+ * with an id outside [0,V) set TTL_ERR_DEVICE and are left out. */
+int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t h, int64_t V, const int64_t* ids,
+                                            const ttl_bf16* dY, int64_t lddy, float scale, float* const* dE,
+                                            int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ packed attention */
+
+/* Causal attention with grouped heads over a pack of documents ([TPSP] "Attention:按 head 切":
+ * each shard finishes its own heads alone).  Document b holds tokens [cu_seqlens[b],
+ * cu_seqlens[b+1]) of the T; a query sees the keys of its own document up to itself.  Documents
+ * may be empty; tokens before the first or after the last document get O = 0, lse = -inf and
+ * zero gradients.  What the keys, values and gradients of tokens outside a row's document (or
+ * after it) hold, infinities and NaN among it, does not reach that row.
+ *   cu_seqlens [batch+1] int32, on the device, not decreasing, within [0,T]; anything else sets
+ *              TTL_ERR_DEVICE (the outputs then mean nothing, no access leaves the tensors)
+ *   Q[i] [T, n_q/t d], K[i], V[i] [T, n_kv/t d], head-major columns, row strides ldq, ldk, ldv
+ *              (multiples of 8; e.g. column ranges of one fused projection)
+ *   O[i] [T, n_q/t d] out, row stride ldo;  lse[i] [n_q/t, T] fp32 out: log sum exp(scale q.k)
+ *   ws   workspace of ttl_packed_attn_fwd_workspace_size() bytes (may be null where that is 0)
+ * t | n_q, t | n_kv, n_kv | n_q, d = 64 or 128, any T; scale > 0.  Memory use is linear in T. */
+size_t ttl_packed_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch);
+int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
+                        float scale, const ttl_bf16* const* Q, int64_t ldq, const ttl_bf16* const* K, int64_t ldk,
+                        const ttl_bf16* const* V, int64_t ldv, ttl_bf16* const* O, int64_t ldo, float* const* lse,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* Its backward pass from the saved O and lse: dQ[i], dK[i], dV[i] out with row strides lddq,
+ * lddk, lddv (the KV gradients summed over each group's query heads, in a fixed order). */
+size_t ttl_packed_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch);
+int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
+                        float scale, const ttl_bf16* const* dO, int64_t lddo, const ttl_bf16* const* Q, int64_t ldq,
+                        const ttl_bf16* const* K, int64_t ldk, const ttl_bf16* const* V, int64_t ldv,
+                        const ttl_bf16* const* O, int64_t ldo, const float* const* lse, ttl_bf16* const* dQ,
+                        int64_t lddq, ttl_bf16* const* dK, int64_t lddk, ttl_bf16* const* dV, int64_t lddv, void* ws,
+                        size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

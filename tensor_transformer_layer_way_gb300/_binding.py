@@ -28,6 +28,7 @@ TTL_MAX_SHARDS = 16
 ACT = {"gelu_tanh": 0, "swiglu": 1}
 CE_FP32_DLOGITS = 1
 CE_FORWARD_ONLY = 2
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}      # TTL_T_*
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -69,6 +70,21 @@ _SIGS = {
     "ttl_tp_attn_fwd": (_int, [_int, _i64, _i64, _int, _int, _int] + [_vp] * 11 + [_vp, ctypes.c_size_t, _vp]),
     "ttl_tp_attn_bwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int]),
     "ttl_tp_attn_bwd": (_int, [_int, _i64, _i64, _int, _int, _int] + [_vp] * 16 + [_vp, ctypes.c_size_t, _vp]),
+    "ttl_layer_norm_fwd": (_int, [_int, _i64, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_float, _vp,
+                                  _vp, _vp, _vp, _vp]),
+    "ttl_layer_norm_bwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _i64]),
+    "ttl_layer_norm_bwd": (_int, [_int, _i64, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
+                                  _vp, _vp, _int, _vp, ctypes.c_size_t, _vp]),
+    "ttl_vocab_parallel_embedding_scaled_fwd": (_int, [_int, _i64, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _vp]),
+    "ttl_vocab_parallel_embedding_sorted_bwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _i64, _i64]),
+    "ttl_vocab_parallel_embedding_sorted_bwd": (_int, [_int, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.c_float, _vp,
+                                                       _int, _vp, ctypes.c_size_t, _vp]),
+    "ttl_packed_attn_fwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int, _int]),
+    "ttl_packed_attn_fwd": (_int, [_int, _i64, _int, _int, _int, _int, _vp, ctypes.c_float]
+                            + [_vp, _i64] * 4 + [_vp, _vp, ctypes.c_size_t, _vp]),
+    "ttl_packed_attn_bwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int, _int]),
+    "ttl_packed_attn_bwd": (_int, [_int, _i64, _int, _int, _int, _int, _vp, ctypes.c_float]
+                            + [_vp, _i64] * 5 + [_vp] + [_vp, _i64] * 3 + [_vp, ctypes.c_size_t, _vp]),
 }
 
 _lib = None
@@ -166,7 +182,7 @@ def selftest_wait_timeout(timeout_us: int, stream=None) -> int:
 
 
 KERNEL_KINDS = ["gemm", "reduce", "gather", "gtp_gather", "finalize", "ce_stats", "ce_small", "ce_dlogits", "other",
-                "embed", "softmax", "attn_core"]
+                "embed", "softmax", "attn_core", "norm"]
 
 
 def trace_enable(on: bool = True, capacity: int = 65536):
@@ -572,4 +588,224 @@ def tp_attn_bwd(X, dY, Wq, Wk, Wv, Wo, fwd, *, n_q, n_kv, d, out=None, stream=No
                                  _arr(fwd["Q"]), _arr(fwd["K"]), _arr(fwd["V"]), _arr(fwd["P"]), _arr(fwd["O"]),
                                  _arr(out["dWq"]), _arr(out["dWk"]), _arr(out["dWv"]), _arr(out["dWo"]),
                                  _arr(out["dX"]), _p(ws), ws.numel(), _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ row-strided operands
+
+def _need_rows(ts, name, n, dtype, rows, cols):
+    """Checks n CUDA matrices [rows, cols] whose rows are contiguous and share one row stride;
+    returns that stride in elements."""
+    if not isinstance(ts, (list, tuple)) or len(ts) != n:
+        raise ValueError(f"{name} must be a list of {n} tensors")
+    ld = None
+    for x in ts:
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{name} must hold tensors")
+        if x.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+        if not x.is_cuda:
+            raise ValueError(f"{name} must be CUDA tensors")
+        if x.shape != (rows, cols):
+            raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {(rows, cols)}")
+        step, col = x.stride()
+        if col != 1 and cols > 1:
+            raise ValueError(f"{name}: rows must be contiguous")
+        if rows <= 1:
+            step = cols
+        if ld is None:
+            ld = step
+        elif step != ld:
+            raise ValueError(f"{name}: the tensors must share one row stride")
+    return ld
+
+
+# ------------------------------------------------------------------ layer norm
+
+def layer_norm_fwd_buffers(t, rows, h, dtype=torch.bfloat16, residual=False, device="cuda"):
+    """Output buffers of layer_norm_fwd."""
+    e = dict(device=device, dtype=dtype)
+    f = dict(device=device, dtype=torch.float32)
+    return {"Y": [torch.empty(rows, h, **e) for _ in range(t)],
+            "S": [torch.empty(rows, h, **e) for _ in range(t)] if residual else None,
+            "mean": [torch.empty(rows, **f) for _ in range(t)], "rstd": [torch.empty(rows, **f) for _ in range(t)]}
+
+
+def _stream_type(X, gamma):
+    if not isinstance(X, (list, tuple)) or not X or not isinstance(X[0], torch.Tensor) or X[0].dim() != 2:
+        raise ValueError("X must be a list of token slabs [rows, h]")
+    if X[0].dtype not in _TYPES or gamma.dtype not in _TYPES:
+        raise TypeError("layer norm takes bf16 or fp32 slabs and weights")
+    return len(X), X[0].shape[0], X[0].shape[1], X[0].dtype
+
+
+def layer_norm_fwd(X, gamma, beta=None, *, eps=1e-5, residual=None, out=None, stream=None):
+    """Layer norm of the token slabs X (a list of [rows, h], bf16 or fp32), of X + residual where
+    given.  Returns dict Y, S (the sums, None without a residual), mean, rstd (lists)."""
+    t, rows, h, dt = _stream_type(X, gamma)
+    ldx = _need_rows(X, "X", t, dt, rows, h)
+    ldr = h if residual is None else _need_rows(residual, "residual", t, dt, rows, h)
+    _need(gamma, "gamma", gamma.dtype, (h,))
+    if beta is not None:
+        _need(beta, "beta", gamma.dtype, (h,))
+    if out is None:
+        out = layer_norm_fwd_buffers(t, rows, h, dt, residual is not None, X[0].device)
+    _need_list(out["Y"], "Y", t, dt, (rows, h))
+    _need_list(out["mean"], "mean", t, torch.float32, (rows,))
+    _need_list(out["rstd"], "rstd", t, torch.float32, (rows,))
+    S = None
+    if residual is not None:
+        S = _need_list(out["S"], "S", t, dt, (rows, h))
+    _check(lib().ttl_layer_norm_fwd(t, rows, h, _TYPES[dt], _TYPES[gamma.dtype], _arr(X), ldx, _arr(residual), ldr,
+                                    _p(gamma), _p(beta), float(eps), _arr(S), _arr(out["Y"]), _arr(out["mean"]),
+                                    _arr(out["rstd"]), _stream(stream)))
+    return out
+
+
+def layer_norm_bwd_buffers(t, rows, h, dtype=torch.bfloat16, device="cuda"):
+    """Output and workspace buffers of layer_norm_bwd."""
+    ws = int(lib().ttl_layer_norm_bwd_workspace_size(t, rows, h))
+    return {"dX": [torch.empty(rows, h, device=device, dtype=dtype) for _ in range(t)],
+            "dgamma": torch.empty(h, device=device), "dbeta": torch.empty(h, device=device),
+            "ws": torch.empty(max(ws, 16), dtype=torch.uint8, device=device)}
+
+
+def layer_norm_bwd(X, dY, gamma, fwd, *, dS=None, accumulate=False, out=None, stream=None):
+    """Backward of layer_norm_fwd: X is the normalised input (fwd["S"] where there was a residual),
+    ``fwd`` holds its mean and rstd, dS is the gradient that reaches X past the block.  Returns dict
+    dX (list), dgamma, dbeta (fp32; with ``accumulate`` added to those of ``out``)."""
+    t, rows, h, dt = _stream_type(X, gamma)
+    ldx = _need_rows(X, "X", t, dt, rows, h)
+    lddy = _need_rows(dY, "dY", t, dt, rows, h)
+    ldds = h if dS is None else _need_rows(dS, "dS", t, dt, rows, h)
+    _need(gamma, "gamma", gamma.dtype, (h,))
+    _need_list(fwd["mean"], "mean", t, torch.float32, (rows,))
+    _need_list(fwd["rstd"], "rstd", t, torch.float32, (rows,))
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = layer_norm_bwd_buffers(t, rows, h, dt, X[0].device)
+    _need_list(out["dX"], "dX", t, dt, (rows, h))
+    _need(out["dgamma"], "dgamma", torch.float32, (h,))
+    if out["dbeta"] is not None:
+        _need(out["dbeta"], "dbeta", torch.float32, (h,))
+    ws = out["ws"]
+    _check(lib().ttl_layer_norm_bwd(t, rows, h, _TYPES[dt], _TYPES[gamma.dtype], _arr(X), ldx, _arr(dY), lddy,
+                                    _arr(dS), ldds, _p(gamma), _arr(fwd["mean"]), _arr(fwd["rstd"]), _arr(out["dX"]),
+                                    _p(out["dgamma"]), _p(out["dbeta"]), int(bool(accumulate)), _p(ws), ws.numel(),
+                                    _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ scaled embedding, sorted gradient
+
+def vocab_parallel_embedding_scaled_fwd(ids, E, scale, *, out=None, stream=None):
+    """Lookup times ``scale`` with the table split into len(E) vocab shards: the t output buffers
+    [T, h], each with every token's scaled row."""
+    t = len(E)
+    Vs, h = E[0].shape
+    T = ids.shape[0]
+    _need(ids, "ids", torch.int64, (T,))
+    _need_list(E, "E", t, shape=(Vs, h))
+    if out is None:
+        out = [torch.empty((T, h), device=ids.device, dtype=torch.bfloat16) for _ in range(t)]
+    _need_list(out, "out", t, shape=(T, h))
+    _check(lib().ttl_vocab_parallel_embedding_scaled_fwd(t, T, h, Vs * t, _p(ids), _arr(E), float(scale), _arr(out),
+                                                         _stream(stream)))
+    return out
+
+
+def embedding_sorted_bwd_workspace(t, T, h, V, device="cuda"):
+    """The workspace vocab_parallel_embedding_sorted_bwd needs."""
+    ws = int(lib().ttl_vocab_parallel_embedding_sorted_bwd_workspace_size(t, T, h, V))
+    return torch.empty(max(ws, 16), dtype=torch.uint8, device=device)
+
+
+def vocab_parallel_embedding_sorted_bwd(ids, dY, scale, dE, *, accumulate=False, ws=None, stream=None):
+    """Gradient of the scaled lookup into the fp32 shards dE ([V/t, h] each), summed by sorted
+    tokens: the same inputs give the same bits.  Every row is written, or with ``accumulate`` the
+    rows that have tokens are added to."""
+    t = len(dE)
+    Vs, h = dE[0].shape
+    T = ids.shape[0]
+    _need(ids, "ids", torch.int64, (T,))
+    lddy = _need_rows([dY], "dY", 1, torch.bfloat16, T, h)
+    _need_list(dE, "dE", t, torch.float32, (Vs, h))
+    if ws is None:
+        ws = embedding_sorted_bwd_workspace(t, T, h, Vs * t, ids.device)
+    _check(lib().ttl_vocab_parallel_embedding_sorted_bwd(t, T, h, Vs * t, _p(ids), _p(dY), lddy, float(scale),
+                                                         _arr(dE), int(bool(accumulate)), _p(ws), ws.numel(),
+                                                         _stream(stream)))
+    return dE
+
+
+# ------------------------------------------------------------------ packed attention
+
+def packed_attn_fwd_buffers(t, T, n_q, n_kv, d, batch, device="cuda"):
+    """Output and workspace buffers of packed_attn_fwd."""
+    qc = n_q // t * d
+    ws = int(lib().ttl_packed_attn_fwd_workspace_size(t, T, n_q, n_kv, d, batch))
+    return {"O": [torch.empty(T, qc, device=device, dtype=torch.bfloat16) for _ in range(t)],
+            "lse": [torch.empty(n_q // t, T, device=device) for _ in range(t)],
+            "ws": torch.empty(max(ws, 16), dtype=torch.uint8, device=device)}
+
+
+def packed_attn_fwd(Q, K, V, cu_seqlens, *, n_q, n_kv, d, scale=None, out=None, stream=None):
+    """Causal attention over a pack of documents: document b holds tokens
+    [cu_seqlens[b], cu_seqlens[b+1]) (int32, on the device).  Q, K, V are lists of t shards
+    [T, n_q/t d], [T, n_kv/t d] with contiguous rows of any stride; scale defaults to 1/sqrt(d).
+    Returns dict O ([T, n_q/t d] per shard) and lse ([n_q/t, T] fp32 per shard)."""
+    t = len(Q)
+    T = Q[0].shape[0]
+    qc, kc = n_q // t * d, n_kv // t * d
+    bf16 = torch.bfloat16
+    ldq, ldk = _need_rows(Q, "Q", t, bf16, T, qc), _need_rows(K, "K", t, bf16, T, kc)
+    ldv = _need_rows(V, "V", t, bf16, T, kc)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),))
+    batch = cu_seqlens.numel() - 1
+    if out is None:
+        out = packed_attn_fwd_buffers(t, T, n_q, n_kv, d, batch, Q[0].device)
+    ldo = _need_rows(out["O"], "O", t, bf16, T, qc)
+    _need_list(out["lse"], "lse", t, torch.float32, (n_q // t, T))
+    ws = out["ws"]
+    _check(lib().ttl_packed_attn_fwd(t, T, n_q, n_kv, d, batch, _p(cu_seqlens),
+                                     float(d ** -0.5 if scale is None else scale), _arr(Q), ldq, _arr(K), ldk,
+                                     _arr(V), ldv, _arr(out["O"]), ldo, _arr(out["lse"]), _p(ws), ws.numel(),
+                                     _stream(stream)))
+    return out
+
+
+def packed_attn_bwd_buffers(t, T, n_q, n_kv, d, batch, device="cuda"):
+    """Gradient and workspace buffers of packed_attn_bwd."""
+    qc, kc = n_q // t * d, n_kv // t * d
+    e = dict(device=device, dtype=torch.bfloat16)
+    ws = int(lib().ttl_packed_attn_bwd_workspace_size(t, T, n_q, n_kv, d, batch))
+    return {"dQ": [torch.empty(T, qc, **e) for _ in range(t)], "dK": [torch.empty(T, kc, **e) for _ in range(t)],
+            "dV": [torch.empty(T, kc, **e) for _ in range(t)],
+            "ws": torch.empty(max(ws, 16), dtype=torch.uint8, device=device)}
+
+
+def packed_attn_bwd(dO, Q, K, V, fwd, cu_seqlens, *, n_q, n_kv, d, scale=None, out=None, stream=None):
+    """Backward of packed_attn_fwd (``fwd`` holds its O and lse).  Returns dict dQ, dK, dV (lists);
+    the buffers of ``out`` may be column ranges of one fused gradient."""
+    t = len(Q)
+    T = Q[0].shape[0]
+    qc, kc = n_q // t * d, n_kv // t * d
+    bf16 = torch.bfloat16
+    lddo, ldq = _need_rows(dO, "dO", t, bf16, T, qc), _need_rows(Q, "Q", t, bf16, T, qc)
+    ldk, ldv = _need_rows(K, "K", t, bf16, T, kc), _need_rows(V, "V", t, bf16, T, kc)
+    ldo = _need_rows(fwd["O"], "O", t, bf16, T, qc)
+    _need_list(fwd["lse"], "lse", t, torch.float32, (n_q // t, T))
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),))
+    batch = cu_seqlens.numel() - 1
+    if out is None:
+        out = packed_attn_bwd_buffers(t, T, n_q, n_kv, d, batch, Q[0].device)
+    lddq = _need_rows(out["dQ"], "dQ", t, bf16, T, qc)
+    lddk, lddv = _need_rows(out["dK"], "dK", t, bf16, T, kc), _need_rows(out["dV"], "dV", t, bf16, T, kc)
+    ws = out["ws"]
+    _check(lib().ttl_packed_attn_bwd(t, T, n_q, n_kv, d, batch, _p(cu_seqlens),
+                                     float(d ** -0.5 if scale is None else scale), _arr(dO), lddo, _arr(Q), ldq,
+                                     _arr(K), ldk, _arr(V), ldv, _arr(fwd["O"]), ldo, _arr(fwd["lse"]),
+                                     _arr(out["dQ"]), lddq, _arr(out["dK"]), lddk, _arr(out["dV"]), lddv, _p(ws),
+                                     ws.numel(), _stream(stream)))
     return out

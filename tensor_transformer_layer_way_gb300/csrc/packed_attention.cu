@@ -1,0 +1,217 @@
+// Causal attention with grouped heads over a pack of documents, heads split across t shards.
+//
+// Source: "v4:Tensor Parallel 与 Sequence Parallel", section "Attention:按 head 切": each shard
+// finishes its own heads alone.  ttl_tp_attn_fwd computes one sequence and keeps the probabilities
+// (T^2 per head); here T tokens hold any number of documents, nothing of size T^2 reaches memory,
+// and the backward pass recomputes the probabilities from each row's log-sum-exp.
+//
+// For the query at token i of a document that starts at lo, head c reading KV head g = c / grp:
+//   s_j = scale q_i . k_j,  lse_i = log sum_{lo <= j <= i} exp(s_j),  p_j = exp(s_j - lse_i)
+//   o_i = sum_j p_j v_j
+//   D_i = do_i . o_i,  ds_j = p_j (do_i . v_j - D_i)
+//   dq_i = scale sum_j ds_j k_j,  dk_j = scale sum_{c, i} ds_j q_i,  dv_j = sum_{c, i} p_j do_i
+// A token of no document has o = 0, lse = -inf and zero gradients.
+
+#include "packed_attn.cuh"
+
+namespace ttl {
+namespace {
+
+constexpr int kRowWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kRowWarps * 32) pack_fwd_row_kernel(const __grid_constant__ PackArgs A) {
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_docs(A.cu, A.batch, A.T, A.status);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  if (i >= A.T) return;
+  const int shard = blockIdx.y / A.nql, c = blockIdx.y % A.nql;
+  fwd_row<D>(A, A.s[shard], c, static_cast<int>(i), doc_of(A.cu, A.batch, static_cast<int>(A.T), static_cast<int>(i)),
+             threadIdx.x & 31);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRowWarps * 32) pack_dq_row_kernel(const __grid_constant__ PackArgs A) {
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_docs(A.cu, A.batch, A.T, A.status);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  if (i >= A.T) return;
+  const int shard = blockIdx.y / A.nql, c = blockIdx.y % A.nql;
+  dq_row<D>(A, A.s[shard], shard, c, static_cast<int>(i),
+            doc_of(A.cu, A.batch, static_cast<int>(A.T), static_cast<int>(i)), threadIdx.x & 31);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRowWarps * 32) pack_dkv_row_kernel(const __grid_constant__ PackArgs A) {
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  if (j >= A.T) return;
+  const int shard = blockIdx.y / A.nkvl, g = blockIdx.y % A.nkvl;
+  dkv_row<D>(A, A.s[shard], shard, g, static_cast<int>(j),
+             doc_of(A.cu, A.batch, static_cast<int>(A.T), static_cast<int>(j)), threadIdx.x & 31);
+}
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int check_shape(int t, int64_t T, int n_q, int n_kv, int d, int batch, const char* name) {
+  if (t < 1 || t > kMaxShards) return set_error(TTL_ERR_ARG, "%s: t=%d outside [1,%d]", name, t, kMaxShards);
+  if (T < 0 || n_q < 1 || n_kv < 1 || d < 1 || batch < 0) return set_error(TTL_ERR_ARG, "%s: bad shape", name);
+  if (n_q % t || n_kv % t)
+    return set_error(TTL_ERR_SHAPE, "%s: t=%d must divide the head counts %d and %d", name, t, n_q, n_kv);
+  if (n_q % n_kv) return set_error(TTL_ERR_SHAPE, "%s: n_kv=%d must divide n_q=%d", name, n_kv, n_q);
+  if (d != 64 && d != 128) return set_error(TTL_ERR_SHAPE, "%s: head dimension %d is not 64 or 128", name, d);
+  if (T >= (int64_t(1) << 28) || n_q > 32768) return set_error(TTL_ERR_SHAPE, "%s: extent too large", name);
+  return TTL_OK;
+}
+
+// t matrices [T, cols] with row stride ld, 16-byte rows.
+int check_mats(const void* const* a, int t, int64_t cols, int64_t ld, const char* what, const char* name) {
+  if (!a) return set_error(TTL_ERR_ARG, "%s: %s: null shard array", name, what);
+  if (ld < cols) return set_error(TTL_ERR_SHAPE, "%s: %s: row stride smaller than its columns", name, what);
+  if (ld % 8) return set_error(TTL_ERR_ALIGN, "%s: %s: row stride not a multiple of 8", name, what);
+  if (ld >= (int64_t(1) << 31)) return set_error(TTL_ERR_SHAPE, "%s: %s: row stride too large", name, what);
+  for (int i = 0; i < t; ++i) {
+    if (!a[i]) return set_error(TTL_ERR_ARG, "%s: %s[%d] is null", name, what, i);
+    if (!aligned16(a[i])) return set_error(TTL_ERR_ALIGN, "%s: %s[%d] not 16-byte aligned", name, what, i);
+  }
+  return TTL_OK;
+}
+
+int check_lse(const float* const* lse, int t, const char* name) {
+  if (!lse) return set_error(TTL_ERR_ARG, "%s: lse: null shard array", name);
+  for (int i = 0; i < t; ++i) {
+    if (!lse[i]) return set_error(TTL_ERR_ARG, "%s: lse[%d] is null", name, i);
+    if (reinterpret_cast<uintptr_t>(lse[i]) & 3) return set_error(TTL_ERR_ALIGN, "%s: lse[%d] not 4-byte aligned", name, i);
+  }
+  return TTL_OK;
+}
+
+int check_cu(const int32_t* cu, float scale, const char* name) {
+  if (!cu) return set_error(TTL_ERR_ARG, "%s: cu_seqlens is null", name);
+  if (reinterpret_cast<uintptr_t>(cu) & 3) return set_error(TTL_ERR_ALIGN, "%s: cu_seqlens not 4-byte aligned", name);
+  if (!(scale > 0.0f && scale < INFINITY)) return set_error(TTL_ERR_ARG, "%s: scale must be positive and finite", name);
+  return TTL_OK;
+}
+
+const __nv_bfloat16* bf(const ttl_bf16* p) { return reinterpret_cast<const __nv_bfloat16*>(p); }
+__nv_bfloat16* bf(ttl_bf16* p) { return reinterpret_cast<__nv_bfloat16*>(p); }
+
+}  // namespace
+}  // namespace ttl
+
+using namespace ttl;
+
+extern "C" size_t ttl_packed_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
+  if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_fwd_workspace_size")) return 0;
+  return 0;   // scores and row statistics stay on chip
+}
+
+extern "C" size_t ttl_packed_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
+  if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_bwd_workspace_size")) return 0;
+  return round256(static_cast<size_t>(n_q) * T * 4);   // D
+}
+
+extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
+                                   float scale, const ttl_bf16* const* Q, int64_t ldq, const ttl_bf16* const* K,
+                                   int64_t ldk, const ttl_bf16* const* V, int64_t ldv, ttl_bf16* const* O, int64_t ldo,
+                                   float* const* lse, void* ws, size_t ws_bytes, void* stream) {
+  const char* name = "ttl_packed_attn_fwd";
+  int rc = check_shape(t, T, n_q, n_kv, d, batch, name);
+  if (rc) return rc;
+  if ((rc = check_cu(cu_seqlens, scale, name))) return rc;
+  const int64_t qc = static_cast<int64_t>(n_q / t) * d, kc = static_cast<int64_t>(n_kv / t) * d;
+  using CP = const void* const*;
+  if (T == 0) return TTL_OK;
+  if ((rc = check_mats(reinterpret_cast<CP>(Q), t, qc, ldq, "Q", name)) ||
+      (rc = check_mats(reinterpret_cast<CP>(K), t, kc, ldk, "K", name)) ||
+      (rc = check_mats(reinterpret_cast<CP>(V), t, kc, ldv, "V", name)) ||
+      (rc = check_mats(reinterpret_cast<CP>(O), t, qc, ldo, "O", name)) || (rc = check_lse(lse, t, name)))
+    return rc;
+  (void)ws;
+  (void)ws_bytes;
+  if ((rc = require_sm103())) return rc;
+  PackArgs A = {};
+  A.status = device_status_ptr();
+  if (!A.status) return TTL_ERR_CUDA;
+  for (int i = 0; i < t; ++i) {
+    A.s[i].q = bf(Q[i]);
+    A.s[i].k = bf(K[i]);
+    A.s[i].v = bf(V[i]);
+    A.s[i].o = bf(O[i]);
+    A.s[i].lse = lse[i];
+  }
+  A.t = t; A.nql = n_q / t; A.nkvl = n_kv / t; A.grp = n_q / n_kv; A.T = T;
+  A.ldq = ldq; A.ldk = ldk; A.ldv = ldv; A.ldo = ldo;
+  A.cu = cu_seqlens; A.batch = batch; A.scale = scale;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const double tri = static_cast<double>(T) * (T + 1) / 2.0;   // one document: the documents' lengths are on the device
+  TraceScope trace(s, TTL_K_ATTN_CORE, 4.0 * tri * d * n_q, 2.0 * T * d * (2.0 * n_q + 2.0 * n_kv));
+  const dim3 grid(static_cast<unsigned>((T + kRowWarps - 1) / kRowWarps), n_q);
+  if (d == 128)
+    pack_fwd_row_kernel<128><<<grid, kRowWarps * 32, 0, s>>>(A);
+  else
+    pack_fwd_row_kernel<64><<<grid, kRowWarps * 32, 0, s>>>(A);
+  return cuda_check(cudaGetLastError(), "packed attention forward launch");
+}
+
+extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
+                                   float scale, const ttl_bf16* const* dO, int64_t lddo, const ttl_bf16* const* Q,
+                                   int64_t ldq, const ttl_bf16* const* K, int64_t ldk, const ttl_bf16* const* V,
+                                   int64_t ldv, const ttl_bf16* const* O, int64_t ldo, const float* const* lse,
+                                   ttl_bf16* const* dQ, int64_t lddq, ttl_bf16* const* dK, int64_t lddk,
+                                   ttl_bf16* const* dV, int64_t lddv, void* ws, size_t ws_bytes, void* stream) {
+  const char* name = "ttl_packed_attn_bwd";
+  int rc = check_shape(t, T, n_q, n_kv, d, batch, name);
+  if (rc) return rc;
+  if ((rc = check_cu(cu_seqlens, scale, name))) return rc;
+  const int64_t qc = static_cast<int64_t>(n_q / t) * d, kc = static_cast<int64_t>(n_kv / t) * d;
+  using CP = const void* const*;
+  if (T == 0) return TTL_OK;
+  if ((rc = check_mats(reinterpret_cast<CP>(dO), t, qc, lddo, "dO", name)) ||
+      (rc = check_mats(reinterpret_cast<CP>(Q), t, qc, ldq, "Q", name)) ||
+      (rc = check_mats(reinterpret_cast<CP>(K), t, kc, ldk, "K", name)) ||
+      (rc = check_mats(reinterpret_cast<CP>(V), t, kc, ldv, "V", name)) ||
+      (rc = check_mats(reinterpret_cast<CP>(O), t, qc, ldo, "O", name)) || (rc = check_lse(lse, t, name)) ||
+      (rc = check_mats(reinterpret_cast<CP>(dQ), t, qc, lddq, "dQ", name)) ||
+      (rc = check_mats(reinterpret_cast<CP>(dK), t, kc, lddk, "dK", name)) ||
+      (rc = check_mats(reinterpret_cast<CP>(dV), t, kc, lddv, "dV", name)))
+    return rc;
+  const size_t need = ttl_packed_attn_bwd_workspace_size(t, T, n_q, n_kv, d, batch);
+  if (!ws || ws_bytes < need)
+    return set_error(TTL_ERR_ARG, "%s: workspace of %zu bytes needed, %zu given", name, need, ws_bytes);
+  if (!aligned16(ws)) return set_error(TTL_ERR_ALIGN, "%s: workspace not 16-byte aligned", name);
+  if ((rc = require_sm103())) return rc;
+  PackArgs A = {};
+  A.status = device_status_ptr();
+  if (!A.status) return TTL_ERR_CUDA;
+  for (int i = 0; i < t; ++i) {
+    A.s[i].q = bf(Q[i]);
+    A.s[i].k = bf(K[i]);
+    A.s[i].v = bf(V[i]);
+    A.s[i].o = const_cast<__nv_bfloat16*>(bf(O[i]));
+    A.s[i].lse = const_cast<float*>(lse[i]);
+    A.s[i].dO = bf(dO[i]);
+    A.s[i].dq = bf(dQ[i]);
+    A.s[i].dk = bf(dK[i]);
+    A.s[i].dv = bf(dV[i]);
+  }
+  A.t = t; A.nql = n_q / t; A.nkvl = n_kv / t; A.grp = n_q / n_kv; A.T = T;
+  A.ldq = ldq; A.ldk = ldk; A.ldv = ldv; A.ldo = ldo;
+  A.lddo = lddo; A.lddq = lddq; A.lddk = lddk; A.lddv = lddv;
+  A.cu = cu_seqlens; A.batch = batch; A.scale = scale;
+  A.D = static_cast<float*>(ws);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const double tri = static_cast<double>(T) * (T + 1) / 2.0;
+  const unsigned rows = static_cast<unsigned>((T + kRowWarps - 1) / kRowWarps);
+  {
+    TraceScope trace(s, TTL_K_ATTN_CORE, 6.0 * tri * d * n_q, 2.0 * T * d * (4.0 * n_q + 2.0 * n_kv));
+    if (d == 128)
+      pack_dq_row_kernel<128><<<dim3(rows, n_q), kRowWarps * 32, 0, s>>>(A);
+    else
+      pack_dq_row_kernel<64><<<dim3(rows, n_q), kRowWarps * 32, 0, s>>>(A);
+    if ((rc = cuda_check(cudaGetLastError(), "packed attention dQ launch"))) return rc;
+  }
+  TraceScope trace(s, TTL_K_ATTN_CORE, 4.0 * tri * d * n_q, 2.0 * T * d * (2.0 * n_q + 4.0 * n_kv));
+  if (d == 128)
+    pack_dkv_row_kernel<128><<<dim3(rows, n_kv), kRowWarps * 32, 0, s>>>(A);
+  else
+    pack_dkv_row_kernel<64><<<dim3(rows, n_kv), kRowWarps * 32, 0, s>>>(A);
+  return cuda_check(cudaGetLastError(), "packed attention dK dV launch");
+}

@@ -1,0 +1,195 @@
+// Packed causal attention: what its kernels share.  A pack is one axis of T tokens; document b holds
+// tokens [cu[b], cu[b+1]) and a query sees the keys of its own document up to itself.
+#pragma once
+
+#include <cmath>
+
+#include "ttl_device.cuh"
+#include "ttl_internal.h"
+
+namespace ttl {
+
+// One shard's operands.  Head c of a row-major [T, heads d] matrix starts at column c d.
+struct PackShard {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* o;            // forward: out; backward: in
+  float* lse;                  // [n_q/t, T], natural logarithm; forward: out; backward: in
+  const __nv_bfloat16* dO;
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+};
+
+struct PackArgs {
+  PackShard s[kMaxShards];
+  int t, nql, nkvl, grp;       // query and KV heads per shard, query heads per KV head
+  int64_t T;
+  int64_t ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;
+  const int32_t* cu;           // [batch + 1]
+  int batch;
+  float scale;
+  float* D;                    // backward: rowsum(dO o), [t][n_q/t][T]
+  int* status;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct DocRange {
+  int lo, hi;                  // the document's tokens [lo, hi); hi <= lo: the token is in none
+};
+
+// The document of token `tok`, by bisection.  Whatever cu holds, the answer stays inside [0, T): with
+// entries out of order it is some document cut to the pack, and the check kernel reports it.
+__device__ __forceinline__ DocRange doc_of(const int32_t* cu, int batch, int T, int tok) {
+  int l = 0, r = batch;        // cu[l] <= tok < cu[r] once both ends are checked
+  if (batch == 0 || tok < __ldg(cu) || tok >= __ldg(cu + batch)) return DocRange{0, 0};
+  while (r - l > 1) {
+    const int m = (l + r) >> 1;
+    if (__ldg(cu + m) <= tok) l = m; else r = m;
+  }
+  const int lo = __ldg(cu + l), hi = __ldg(cu + r);
+  return DocRange{lo < 0 ? 0 : lo, hi > T ? T : hi};
+}
+
+// Reports cu that does not start at 0 or above, decreases, or ends beyond T.
+__device__ __forceinline__ void check_docs(const int32_t* cu, int batch, int64_t T, int* status) {
+  bool bad = false;
+  for (int b = threadIdx.x; b <= batch; b += blockDim.x) {
+    const int c = __ldg(cu + b);
+    bad |= c < 0 || c > T || (b > 0 && __ldg(cu + b - 1) > c);
+  }
+  if (bad) atomicCAS(status, 0, TTL_ERR_DEVICE);
+}
+
+// ------------------------------------------------------------------ one row by one warp
+// Lane l holds columns [l D/32, (l + 1) D/32) of the head.  Every key or query of the range is read, and
+// nothing outside it, so what masked places hold (infinities, NaN) never enters.
+
+template <int D>
+struct RowVec {
+  float x[D / 32];
+};
+
+template <int D>
+__device__ __forceinline__ RowVec<D> row_load(const __nv_bfloat16* p, int lane) {
+  RowVec<D> r;
+  if constexpr (D == 128) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p + lane * 4);
+    r.x[0] = bf16_lo(w.x); r.x[1] = bf16_hi(w.x); r.x[2] = bf16_lo(w.y); r.x[3] = bf16_hi(w.y);
+  } else {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p + lane * 2);
+    r.x[0] = bf16_lo(w); r.x[1] = bf16_hi(w);
+  }
+  return r;
+}
+
+template <int D>
+__device__ __forceinline__ void row_store(__nv_bfloat16* p, const RowVec<D>& r, int lane) {
+  if constexpr (D == 128)
+    *reinterpret_cast<uint2*>(p + lane * 4) = make_uint2(pack_bf16x2(r.x[0], r.x[1]), pack_bf16x2(r.x[2], r.x[3]));
+  else
+    *reinterpret_cast<uint32_t*>(p + lane * 2) = pack_bf16x2(r.x[0], r.x[1]);
+}
+
+template <int D>
+__device__ __forceinline__ float row_dot(const RowVec<D>& a, const RowVec<D>& b) {
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) s = fmaf(a.x[j], b.x[j], s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+template <int D>
+__device__ __forceinline__ RowVec<D> row_zero() {
+  RowVec<D> r;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) r.x[j] = 0.0f;
+  return r;
+}
+
+// o_i and lse_i of query head c at token i: running maximum m and sum l, both in base 2.
+template <int D>
+__device__ __forceinline__ void fwd_row(const PackArgs& A, const PackShard& S, int c, int i, DocRange doc, int lane) {
+  const int g = c / A.grp;
+  RowVec<D> acc = row_zero<D>();
+  float lse = -INFINITY;
+  if (doc.hi > doc.lo) {
+    const RowVec<D> q = row_load<D>(S.q + i * A.ldq + c * D, lane);
+    const float k2 = A.scale * kLog2e;
+    float m = -INFINITY, l = 0.0f;
+    for (int j = doc.lo; j <= i; ++j) {
+      const float s = row_dot(q, row_load<D>(S.k + j * A.ldk + g * D, lane)) * k2;
+      const RowVec<D> v = row_load<D>(S.v + j * A.ldv + g * D, lane);
+      const float mn = fmaxf(m, s);
+      const float f = m == -INFINITY ? 0.0f : exp2f(m - mn), p = exp2f(s - mn);
+      l = l * f + p;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc.x[e] = fmaf(acc.x[e], f, p * v.x[e]);
+      m = mn;
+    }
+    const float inv = 1.0f / l;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc.x[e] *= inv;
+    lse = (m + log2f(l)) * kLn2;
+  }
+  row_store<D>(S.o + i * A.ldo + c * D, acc, lane);
+  if (lane == 0) S.lse[static_cast<int64_t>(c) * A.T + i] = lse;
+}
+
+// dq_i of query head c, and D_i = do_i . o_i.
+template <int D>
+__device__ __forceinline__ void dq_row(const PackArgs& A, const PackShard& S, int shard, int c, int i, DocRange doc,
+                                       int lane) {
+  const int g = c / A.grp;
+  RowVec<D> acc = row_zero<D>();
+  float Di = 0.0f;
+  if (doc.hi > doc.lo) {
+    const RowVec<D> q = row_load<D>(S.q + i * A.ldq + c * D, lane);
+    const RowVec<D> go = row_load<D>(S.dO + i * A.lddo + c * D, lane);
+    Di = row_dot(go, row_load<D>(S.o + i * A.ldo + c * D, lane));
+    const float k2 = A.scale * kLog2e, lse2 = S.lse[static_cast<int64_t>(c) * A.T + i] * kLog2e;
+    for (int j = doc.lo; j <= i; ++j) {
+      const RowVec<D> k = row_load<D>(S.k + j * A.ldk + g * D, lane);
+      const float p = exp2f(row_dot(q, k) * k2 - lse2);
+      const float dp = row_dot(go, row_load<D>(S.v + j * A.ldv + g * D, lane));
+      const float ds = p * (dp - Di) * A.scale;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc.x[e] = fmaf(ds, k.x[e], acc.x[e]);
+    }
+  }
+  row_store<D>(S.dq + i * A.lddq + c * D, acc, lane);
+  if (lane == 0) A.D[(static_cast<int64_t>(shard) * A.nql + c) * A.T + i] = Di;
+}
+
+// dk_j and dv_j of KV head g, summed over the group's query heads.
+template <int D>
+__device__ __forceinline__ void dkv_row(const PackArgs& A, const PackShard& S, int shard, int g, int j, DocRange doc,
+                                        int lane) {
+  RowVec<D> dk = row_zero<D>(), dv = row_zero<D>();
+  if (doc.hi > doc.lo) {
+    const RowVec<D> k = row_load<D>(S.k + j * A.ldk + g * D, lane);
+    const RowVec<D> v = row_load<D>(S.v + j * A.ldv + g * D, lane);
+    const float k2 = A.scale * kLog2e;
+    for (int c = g * A.grp; c < (g + 1) * A.grp; ++c)
+      for (int i = j; i < doc.hi; ++i) {
+        const RowVec<D> q = row_load<D>(S.q + i * A.ldq + c * D, lane);
+        const RowVec<D> go = row_load<D>(S.dO + i * A.lddo + c * D, lane);
+        const float p = exp2f(row_dot(q, k) * k2 - S.lse[static_cast<int64_t>(c) * A.T + i] * kLog2e);
+        const float ds = p * (row_dot(go, v) - A.D[(static_cast<int64_t>(shard) * A.nql + c) * A.T + i]) * A.scale;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+          dk.x[e] = fmaf(ds, q.x[e], dk.x[e]);
+          dv.x[e] = fmaf(p, go.x[e], dv.x[e]);
+        }
+      }
+  }
+  row_store<D>(S.dk + j * A.lddk + g * D, dk, lane);
+  row_store<D>(S.dv + j * A.lddv + g * D, dv, lane);
+}
+
+}  // namespace ttl

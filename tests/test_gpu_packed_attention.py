@@ -1,0 +1,296 @@
+"""Causal attention over packed documents vs a plain 64-bit implementation (GPU).
+
+Bounds, per element.  The probabilities and the score gradients are rounded to bf16 once before their
+product (half a step, 2^-8, of each term), the result once more; scores and statistics are fp32.  Hence
+  |O - o|    <= 2^-8 (sum p |v| + |o|),         |dV - dv| <= 2^-8 (sum p |do| + |dv|)
+  |dQ - dq|  <= 2^-8 (sum |ds k| + |dq|),       |dK - dk| <= 2^-8 (sum |ds q| + |dk|)
+plus the fp32 part: a score is off by at most 2 d u sum |q k| (u = 2^-24) and a few u of the exponential,
+which moves every probability, and p (dp - D), by that factor.  The backward reference takes the
+same O and lse as the kernels.
+"""
+import math
+
+import pytest
+import torch
+
+import tensor_transformer_layer_way_gb300 as ttl
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = 2.0 ** -8
+F8 = torch.float64
+BF16 = torch.bfloat16
+
+
+def _inputs(t, T, n_q, n_kv, d, lens, seed, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+
+    def mats(cols, s=1.0):
+        return [(torch.randn(T, cols, generator=g) * s).to(BF16).cuda() for _ in range(t)]
+
+    qc, kc = n_q // t * d, n_kv // t * d
+    x = {"Q": mats(qc, std), "K": mats(kc, std), "V": mats(kc), "dO": mats(qc)}
+    x["cu"] = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32).cuda()
+    return x
+
+
+def _reference(x, t, n_q, n_kv, d, lens, scale, fwd=None):
+    """Per shard: O, lse and (with fwd) dQ, dK, dV, each with its bound."""
+    grp, nql, nkl = n_q // n_kv, n_q // t, n_kv // t
+    out = []
+    for i in range(t):
+        T = x["Q"][i].shape[0]
+        q, k, v, do = (x[n][i].to(F8).view(T, -1, d) for n in ("Q", "K", "V", "dO"))
+        z = lambda h: torch.zeros(T, h, d, dtype=F8, device="cuda")   # noqa: E731
+        r = {"O": z(nql), "dO": z(nql), "lse": torch.full((nql, T), -math.inf, dtype=F8, device="cuda"),
+             "dlse": torch.zeros(nql, T, dtype=F8, device="cuda"), "dQ": z(nql), "eQ": z(nql), "dK": z(nkl),
+             "eK": z(nkl), "dV": z(nkl), "eV": z(nkl)}
+        a = 0
+        for n in lens:
+            s_ = slice(a, a + n)
+            a += n
+            if n == 0:
+                continue
+            hide = torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1)
+            for c in range(nql):
+                g = c // grp
+                qq, kk, vv, gg = q[s_, c], k[s_, g], v[s_, g], do[s_, c]
+                s = (scale * qq @ kk.T).masked_fill(hide, -math.inf)
+                e = (scale * 2 * d * U * qq.abs() @ kk.abs().T + 16 * U * (1 + s.abs())).masked_fill(hide, 0.0)
+                lse = torch.logsumexp(s, 1)
+                p = torch.exp(s - lse[:, None])
+                es = e.amax(1, keepdim=True) * 2 + n * U           # factor on the row's probabilities
+                r["lse"][c, s_] = lse
+                r["dlse"][c, s_] = es[:, 0] + 4 * U * lse.abs()
+                o, mag = p @ vv, p @ vv.abs()
+                r["O"][s_, c] = o
+                r["dO"][s_, c] = HALF * (mag + o.abs()) * 1.02 + es * mag * 2
+                if fwd is None:
+                    continue
+                oo = fwd["O"][i].to(F8).view(T, -1, d)[s_, c]
+                ll = fwd["lse"][i][c, s_].to(F8)
+                p = torch.exp(s - ll[:, None])
+                ep = (e + 8 * U * (1 + ll.abs()[:, None])).masked_fill(hide, 0.0)
+                dp, D = gg @ vv.T, (gg * oo).sum(1, keepdim=True)
+                ds = scale * p * (dp - D)
+                eds = scale * p * (ep * (dp - D).abs() + 2 * d * U * (gg.abs() @ vv.abs().T + (gg * oo).abs().sum(1, keepdim=True)))
+                r["dQ"][s_, c] = ds @ kk
+                r["eQ"][s_, c] = HALF * 1.02 * (ds.abs() @ kk.abs()) + 1.02 * eds @ kk.abs() + n * U * ds.abs() @ kk.abs()
+                r["dK"][s_, g] += ds.T @ qq
+                r["eK"][s_, g] += (HALF * 1.02 + n * grp * U) * (ds.abs().T @ qq.abs()) + 1.02 * eds.T @ qq.abs()
+                r["dV"][s_, g] += p.T @ gg
+                r["eV"][s_, g] += (HALF * 1.02 + n * grp * U) * (p.T @ gg.abs()) + 1.02 * (p * ep).T @ gg.abs()
+        for n_, e_ in (("dQ", "eQ"), ("dK", "eK"), ("dV", "eV")):
+            r[e_] = r[e_] * (1 + HALF) + HALF * r[n_].abs()
+        out.append(r)
+    return out
+
+
+def _near(got, ref, bound, name):
+    got = got.to(F8)
+    assert torch.isfinite(got).all(), f"{name}: not finite"
+    over = (got - ref).abs() - bound - 1e-30
+    assert (over <= 0).all(), f"{name}: {over.max().item():.3e} beyond the bound at {over.argmax().item()}"
+
+
+def _run(t, T, n_q, n_kv, d, lens, seed=0, std=1.0, scale=None, x=None, out_f=None, out_b=None):
+    x = _inputs(t, T, n_q, n_kv, d, lens, seed, std) if x is None else x
+    kw = dict(n_q=n_q, n_kv=n_kv, d=d, scale=scale)
+    fwd = ttl.packed_attn_fwd(x["Q"], x["K"], x["V"], x["cu"], out=out_f, **kw)
+    bwd = ttl.packed_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], fwd, x["cu"], out=out_b, **kw)
+    assert ttl.device_status() == 0
+    return x, fwd, bwd
+
+
+def _check(x, fwd, bwd, t, T, n_q, n_kv, d, lens, scale=None):
+    used = sum(lens)
+    ref = _reference(x, t, n_q, n_kv, d, lens, d ** -0.5 if scale is None else scale, fwd)
+    for i, r in enumerate(ref):
+        _near(fwd["O"][i].view(T, -1, d), r["O"], r["dO"], f"O[{i}]")
+        lse = fwd["lse"][i]
+        assert torch.isinf(lse[:, used:]).all() and (lse[:, used:] < 0).all()
+        _near(lse[:, :used], r["lse"][:, :used], r["dlse"][:, :used], f"lse[{i}]")
+        for n, e in (("dQ", "eQ"), ("dK", "eK"), ("dV", "eV")):
+            _near(bwd[n][i].view(T, -1, d), r[n], r[e], f"{n}[{i}]")
+            assert torch.count_nonzero(bwd[n][i][used:]) == 0
+        assert torch.count_nonzero(fwd["O"][i][used:]) == 0
+
+
+CASES = [
+    (1, 1, 1, 1, 64, [1]), (1, 5, 2, 1, 128, [5]), (1, 127, 2, 2, 64, [127]), (1, 128, 4, 1, 128, [128]),
+    (1, 129, 3, 1, 128, [129]), (2, 130, 4, 2, 64, [1, 64, 65]), (1, 256, 2, 1, 128, [100, 28, 128]),
+    (1, 257, 1, 1, 128, [257]), (2, 300, 6, 2, 128, [0, 17, 0, 200, 83, 0]), (1, 384, 5, 1, 64, [383, 1]),
+    (1, 400, 4, 4, 128, [1] * 400), (1, 500, 2, 1, 128, [3] * 100 + [150, 40]), (4, 513, 8, 4, 64, [256, 257]),
+    (1, 700, 8, 1, 128, [130, 570]), (8, 640, 16, 8, 128, [600]), (1, 333, 2, 1, 64, []), (1, 1025, 2, 1, 128, [1025]),
+    (1, 1500, 4, 2, 128, [700, 1, 2, 515, 100]), (1, 2100, 1, 1, 64, [2100]), (16, 200, 16, 16, 64, [99, 101]),
+]
+
+
+@pytest.mark.parametrize("t,T,n_q,n_kv,d,lens", CASES)
+def test_forward_and_backward(t, T, n_q, n_kv, d, lens):
+    x, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, seed=T)
+    _check(x, fwd, bwd, t, T, n_q, n_kv, d, lens)
+
+
+@pytest.mark.parametrize("std,scale", [(6.0, None), (1.0, 1.0), (0.01, 0.2), (3.0, 3.0)])
+def test_peaked_and_flat_scores(std, scale):
+    t, T, n_q, n_kv, d, lens = 1, 700, 4, 2, 128, [300, 400]
+    x, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, seed=9, std=std, scale=scale)
+    _check(x, fwd, bwd, t, T, n_q, n_kv, d, lens, scale)
+
+
+def test_growing_scores():
+    """Each key scores above all before it (the running maximum moves at every tile), and the reverse."""
+    t, T, n_q, n_kv, d, lens = 1, 900, 2, 1, 64, [900]
+    for sign in (1, -1):
+        x = _inputs(t, T, n_q, n_kv, d, lens, 1)
+        ramp = torch.linspace(-4, 4, T)[:, None] * sign
+        x["Q"][0][:] = 1.0
+        x["K"][0][:] = (ramp + 0.01 * torch.randn(T, d, generator=torch.Generator().manual_seed(2))).to(BF16).cuda()
+        x, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, x=x)
+        _check(x, fwd, bwd, t, T, n_q, n_kv, d, lens)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -3.3e38])
+def test_masked_places_do_not_reach_a_row(bad):
+    """Tokens of no document, another document's and later tokens hold values that would spread."""
+    t, T, n_q, n_kv, d, lens = 1, 600, 4, 2, 128, [150, 230, 100]
+    x, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, seed=4)
+    y = {k: [v.clone() for v in a] if k != "cu" else a for k, a in x.items()}
+    for n in ("Q", "K", "V", "dO"):
+        y[n][0][480:] = bad                # of no document
+        y[n][0][150:380] = bad             # the second document
+    _, f2, b2 = _run(t, T, n_q, n_kv, d, lens, x=y)
+    keep = torch.zeros(T, dtype=torch.bool, device="cuda")
+    keep[:150] = True
+    keep[380:480] = True
+    ref = _reference(x, t, n_q, n_kv, d, lens, d ** -0.5, fwd)[0]
+    _near(f2["O"][0].view(T, -1, d)[keep], ref["O"][keep], ref["dO"][keep], "O")
+    _near(f2["lse"][0][:, keep], ref["lse"][:, keep], ref["dlse"][:, keep], "lse")
+    for n, e in (("dQ", "eQ"), ("dK", "eK"), ("dV", "eV")):
+        # (the reference's O differs from f2's by no more than O's own bound: twice the bound covers it)
+        _near(b2[n][0].view(T, -1, d)[keep], ref[n][keep], 2 * ref[e][keep] + 1e-3 * ref[e].amax(), n)
+        assert torch.count_nonzero(b2[n][0][480:]) == 0
+    # a later key and value does not reach the queries before it
+    z = {k: [v.clone() for v in a] if k != "cu" else a for k, a in x.items()}
+    z["K"][0][140] = bad
+    z["V"][0][140] = bad
+    f3 = ttl.packed_attn_fwd(z["Q"], z["K"], z["V"], z["cu"], n_q=n_q, n_kv=n_kv, d=d)
+    _near(f3["O"][0].view(T, -1, d)[:140], ref["O"][:140], ref["dO"][:140], "O before")
+    _near(f3["O"][0].view(T, -1, d)[150:480], ref["O"][150:480], ref["dO"][150:480], "O of other documents")
+
+
+def test_bad_document_bounds_are_reported():
+    t, T, n_q, n_kv, d = 1, 200, 2, 1, 64
+    x = _inputs(t, T, n_q, n_kv, d, [200], 0)
+    for cu in ([0, 150, 100, 200], [-5, 100, 200], [0, 100, 5000], [300, 400], [200, 0]):
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        fwd = ttl.packed_attn_fwd(x["Q"], x["K"], x["V"], cu, n_q=n_q, n_kv=n_kv, d=d)
+        assert ttl.device_status() == ttl.TTL_ERR_DEVICE
+        ttl.packed_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], fwd, cu, n_q=n_q, n_kv=n_kv, d=d)
+        assert ttl.device_status() == ttl.TTL_ERR_DEVICE
+    _run(t, T, n_q, n_kv, d, [200])
+
+
+def test_documents_that_begin_late():
+    """cu_seqlens[0] > 0: the tokens before belong to no document."""
+    t, T, n_q, n_kv, d = 1, 300, 2, 1, 128
+    x = _inputs(t, T, n_q, n_kv, d, [300], 3)
+    x["cu"] = torch.tensor([40, 90, 250], dtype=torch.int32, device="cuda")
+    x, fwd, bwd = _run(t, T, n_q, n_kv, d, [], x=x)
+    part = {k: [v[40:250] for v in a] if k != "cu" else a for k, a in x.items()}
+    f = {"O": [fwd["O"][0][40:250]], "lse": [fwd["lse"][0][:, 40:250]]}
+    r = _reference(part, t, n_q, n_kv, d, [50, 160], d ** -0.5, f)[0]
+    _near(f["O"][0].view(210, -1, d), r["O"], r["dO"], "O")
+    for n, e in (("dQ", "eQ"), ("dK", "eK"), ("dV", "eV")):
+        _near(bwd[n][0][40:250].view(210, -1, d), r[n], r[e], n)
+        assert torch.count_nonzero(bwd[n][0][:40]) == 0 and torch.count_nonzero(bwd[n][0][250:]) == 0
+    assert torch.isinf(fwd["lse"][0][:, :40]).all()
+
+
+def test_fused_projection_strides():
+    """Q, K, V as column ranges of one matrix, the gradients into another: the same bits."""
+    t, T, n_q, n_kv, d, lens = 2, 333, 8, 4, 64, [200, 133]
+    x, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, seed=6)
+    qc, kc = n_q // t * d, n_kv // t * d
+    fused = [torch.cat([x["Q"][i], x["K"][i], x["V"][i]], 1) for i in range(t)]
+    grads = [torch.full_like(f, float("nan")) for f in fused]
+    cut = lambda m: ([f[:, :qc] for f in m], [f[:, qc:qc + kc] for f in m], [f[:, qc + kc:] for f in m])   # noqa: E731
+    q, k, v = cut(fused)
+    y = {"Q": q, "K": k, "V": v, "dO": x["dO"], "cu": x["cu"]}
+    out_b = ttl.packed_attn_bwd_buffers(t, T, n_q, n_kv, d, len(lens))
+    out_b["dQ"], out_b["dK"], out_b["dV"] = cut(grads)
+    _, f2, b2 = _run(t, T, n_q, n_kv, d, lens, x=y, out_b=out_b)
+    for i in range(t):
+        assert torch.equal(f2["O"][i], fwd["O"][i]) and torch.equal(f2["lse"][i], fwd["lse"][i])
+        for n in ("dQ", "dK", "dV"):
+            assert torch.equal(b2[n][i], bwd[n][i])
+
+
+def test_documents_do_not_see_their_place_in_the_pack():
+    """A document alone and the same document behind others give the same result (to the bounds)."""
+    t, n_q, n_kv, d = 1, 4, 1, 128
+    x, fwd, bwd = _run(t, 700, n_q, n_kv, d, [77, 310, 313], seed=12)
+    part = {k: [v[77:387].contiguous() for v in a] if k != "cu" else None for k, a in x.items()}
+    part["cu"] = torch.tensor([0, 310], dtype=torch.int32, device="cuda")
+    _, f2, b2 = _run(t, 310, n_q, n_kv, d, [310], x=part)
+    _check(part, f2, b2, t, 310, n_q, n_kv, d, [310])
+    f = {"O": [fwd["O"][0][77:387]], "lse": [fwd["lse"][0][:, 77:387]]}
+    r = _reference(part, t, n_q, n_kv, d, [310], d ** -0.5, f)[0]
+    for n, e in (("dQ", "eQ"), ("dK", "eK"), ("dV", "eV")):
+        _near(bwd[n][0][77:387].view(310, -1, d), r[n], r[e], n)
+
+
+def test_same_inputs_same_bits():
+    t, T, n_q, n_kv, d, lens = 2, 1200, 8, 2, 128, [500, 700]
+    x, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, seed=2)
+    for _ in range(4):
+        _, f2, b2 = _run(t, T, n_q, n_kv, d, lens, x=x)
+        for a, b in ((fwd, f2), (bwd, b2)):
+            for n in a:
+                if n != "ws":
+                    assert all(torch.equal(p, q) for p, q in zip(a[n], b[n])), n
+
+
+def test_gradient_against_differences():
+    """The directional derivative of the 64-bit forward against the kernels' gradients."""
+    t, T, n_q, n_kv, d, lens = 1, 150, 4, 2, 64, [60, 90]
+    x, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, seed=21)
+    gen = torch.Generator("cuda").manual_seed(5)
+    dirs = {n: torch.randn(x[n][0].shape, generator=gen, device="cuda", dtype=F8) for n in ("Q", "K", "V")}
+
+    def loss(e):
+        y = {n: [x[n][0].to(F8) + e * dirs[n]] for n in ("Q", "K", "V")}
+        y["dO"] = x["dO"]
+        o = _reference(y, t, n_q, n_kv, d, lens, d ** -0.5)[0]["O"]
+        return (o * x["dO"][0].to(F8).view(T, -1, d)).sum()
+
+    step = 1e-4
+    want = (loss(step) - loss(-step)) / (2 * step)
+    got = sum((bwd["d" + n][0].to(F8) * dirs[n]).sum() for n in ("Q", "K", "V"))
+    # Independent roundings of at most half a step in P or dS, O (through D) and the result: their
+    # 2-norm is at most 3 half steps of the gradient's, and a random direction sees 4 sigma of it.
+    size = sum((bwd["d" + n][0].to(F8).square().sum()) for n in ("Q", "K", "V")).sqrt()
+    assert (got - want).abs() <= 4 * 3 * HALF * size
+
+
+def test_graph_replay_on_a_side_stream():
+    t, T, n_q, n_kv, d, lens = 2, 400, 4, 2, 128, [150, 250]
+    x, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, seed=30)
+    f2 = ttl.packed_attn_fwd_buffers(t, T, n_q, n_kv, d, 2)
+    b2 = ttl.packed_attn_bwd_buffers(t, T, n_q, n_kv, d, 2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    kw = dict(n_q=n_q, n_kv=n_kv, d=d)
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        ttl.packed_attn_fwd(x["Q"], x["K"], x["V"], x["cu"], out=f2, **kw)
+        ttl.packed_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], f2, x["cu"], out=b2, **kw)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert ttl.device_status() == 0
+    for i in range(t):
+        assert torch.equal(f2["O"][i], fwd["O"][i])
+        for n in ("dQ", "dK", "dV"):
+            assert torch.equal(b2[n][i], bwd[n][i])
