@@ -20,16 +20,6 @@ namespace {
 constexpr int kRowWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kRowWarps * 32) pack_fwd_row_kernel(const __grid_constant__ PackArgs A) {
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_docs(A.cu, A.batch, A.T, A.status);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  if (i >= A.T) return;
-  const int shard = blockIdx.y / A.nql, c = blockIdx.y % A.nql;
-  fwd_row<D>(A, A.s[shard], c, static_cast<int>(i), doc_of(A.cu, A.batch, static_cast<int>(A.T), static_cast<int>(i)),
-             threadIdx.x & 31);
-}
-
-template <int D>
 __global__ void __launch_bounds__(kRowWarps * 32) pack_dq_row_kernel(const __grid_constant__ PackArgs A) {
   if (blockIdx.x == 0 && blockIdx.y == 0) check_docs(A.cu, A.batch, A.T, A.status);
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
@@ -141,14 +131,7 @@ extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, i
   A.ldq = ldq; A.ldk = ldk; A.ldv = ldv; A.ldo = ldo;
   A.cu = cu_seqlens; A.batch = batch; A.scale = scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const double tri = static_cast<double>(T) * (T + 1) / 2.0;   // one document: the documents' lengths are on the device
-  TraceScope trace(s, TTL_K_ATTN_CORE, 4.0 * tri * d * n_q, 2.0 * T * d * (2.0 * n_q + 2.0 * n_kv));
-  const dim3 grid(static_cast<unsigned>((T + kRowWarps - 1) / kRowWarps), n_q);
-  if (d == 128)
-    pack_fwd_row_kernel<128><<<grid, kRowWarps * 32, 0, s>>>(A);
-  else
-    pack_fwd_row_kernel<64><<<grid, kRowWarps * 32, 0, s>>>(A);
-  return cuda_check(cudaGetLastError(), "packed attention forward launch");
+  return pack_attn_fwd_launch(A, d, s);
 }
 
 extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,

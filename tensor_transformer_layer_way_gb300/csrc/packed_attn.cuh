@@ -34,6 +34,13 @@ struct PackArgs {
   int* status;
 };
 
+// Raises a kernel's dynamic shared-memory limit, once per kernel and device (thread-safe).
+enum PackKernelSlot { kPackFwd128, kPackFwd64, kPackDq128, kPackDq64, kPackDkv128, kPackDkv64, kPackKernelSlots };
+int set_core_smem_once(const void* fn, int slot, int bytes, const char* what);
+
+// Launches of the tensor-core kernels (arguments are checked; A.s holds every pointer they need).
+int pack_attn_fwd_launch(const PackArgs& A, int d, cudaStream_t stream);
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

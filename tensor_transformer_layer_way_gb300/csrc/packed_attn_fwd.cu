@@ -1,0 +1,533 @@
+// Forward kernel of packed causal attention on the tensor cores.
+//
+// The token axis is cut into 128-token tiles wherever documents begin: row i of a query tile
+// sees the keys [lo_i, i] of its own document, so a tile's key tiles run from the one that holds the
+// first row's lo to its own, and short documents share tiles.  One work item is two query tiles
+// that read the same K and V tiles (two heads of a group over the same tokens, or, where the group
+// has an odd number of heads, two neighbouring token tiles of one head): every K or V byte loaded
+// serves 256 rows, 32 bytes per MMA cycle and SM where one tile alone would need 64.
+//
+// Per item and key tile, for x in {0, 1}: S_x = Q_x K^T (fp32, tensor memory); one thread per
+// row takes the row's maximum, P = 2^(s k - m) as bf16 over S_x's own columns, O_x += P V with P
+// read from tensor memory.  The running maximum m only moves when a row's new maximum is more than
+// 8 above it (in base 2): P then stays below 2^8, which bf16 and the fp32 sums hold as exactly,
+// and the accumulator is rescaled rarely.  The row sum l is taken from the unrounded P.
+//
+// Roles (384 threads, persistent): warp 0 issues the TMA loads (Q_0, Q_1, then K_j, V_j through a ring),
+// warp 1 the MMAs, warps 4..7 and 8..11 are the softmax of tile 0 and 1.  A softmax thread holds a whole
+// row of 128 scores: its warpgroups take 208 registers a thread and the first leaves with 88 (together
+// the 384 x 168 of the launch).  Per tile x the order of MMAs is
+// S_x(j), P_x V(j), S_x(j + 1), and the two tiles alternate, so one tile's softmax runs under the
+// other's products; the next item's first S is issued before this item's epilogue.
+//
+// A masked place enters the product as P = 0, and 0 times an infinite or NaN value is NaN: a row whose
+// result is not finite is computed again by its warp over its own keys alone.
+
+#include <cstring>
+#include <mutex>
+
+#include "packed_attn.cuh"
+
+namespace ttl {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kRing = 5;
+constexpr int kFwdThreads = 384;
+constexpr int kTmemCols = 512;
+constexpr float kLazy = 8.0f;
+
+struct FwdParams {
+  CUtensorMap q[kMaxShards];   // box 64 x 128
+  CUtensorMap k[kMaxShards];
+  CUtensorMap v[kMaxShards];
+  PackArgs a;
+  int pair_heads;              // 1: an item is two heads of a group; 0: two token tiles of one head
+  int units;                   // token tiles (or pairs of them)
+  int lanes;                   // items per unit
+  uint64_t timeout_ns;
+};
+
+template <int D>
+struct FwdCfg {
+  static constexpr int KB = D / 64;
+  static constexpr int TILE = KB * kTile * 128;   // bytes of a Q, K or V tile
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_BAR = OFF_RING + kRing * TILE;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
+};
+
+// One query tile of an item: tokens [q0, q0 + 128) of head c, key tiles [jbeg, jend).
+struct QTile {
+  int c, q0, jbeg, jend;
+};
+struct Item {
+  int shard, g;
+  QTile x[2];
+  int jlo, jhi;                // union of the key tiles
+};
+
+// First token of the document of `tok` (or tok's range), found by the whole warp.
+__device__ __forceinline__ DocRange doc_of_warp(const int32_t* cu, int batch, int T, int tok) {
+  const int lane = threadIdx.x & 31;
+  int l = 0, r = batch;
+  while (r - l > 1) {
+    const int step = (r - l - 1 + 31) / 32;
+    const int at = l + step * (lane + 1);
+    const unsigned le = __ballot_sync(0xffffffffu, at < r && __ldg(cu + at) <= tok);
+    const int n = le == 0xffffffffu ? 32 : __ffs(~le) - 1;
+    l += step * n;
+    r = r < l + step ? r : l + step;
+  }
+  const int lo = __ldg(cu + l), hi = __ldg(cu + r);
+  return DocRange{lo < 0 ? 0 : lo, hi > T ? T : hi};
+}
+
+__device__ __forceinline__ void tile_range(const PackArgs& A, QTile& q) {
+  const int T = static_cast<int>(A.T);
+  q.jbeg = q.jend = 0;
+  if (A.batch == 0) return;
+  const int first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
+  const int v0 = q.q0 > first ? q.q0 : first;
+  int v1 = q.q0 + kTile < last ? q.q0 + kTile : last;
+  v1 = v1 < T ? v1 : T;
+  if (v0 >= v1) return;
+  q.jbeg = doc_of_warp(A.cu, A.batch, T, v0).lo / kTile;
+  q.jend = q.q0 / kTile + 1;
+}
+
+// The item of index `at` (heaviest token tiles of one long document first); every lane of a warp calls it.
+__device__ __forceinline__ Item item_of(const FwdParams& P, int at) {
+  const PackArgs& A = P.a;
+  const int unit = P.units - 1 - at / P.lanes;
+  int lane = at % P.lanes;
+  Item it;
+  if (P.pair_heads) {
+    const int half = A.nql / 2;
+    it.shard = lane / half;
+    const int c = (lane % half) * 2;
+    it.g = c / A.grp;
+    it.x[0].c = c;
+    it.x[1].c = c + 1;
+    it.x[0].q0 = it.x[1].q0 = unit * kTile;
+    tile_range(A, it.x[0]);
+    it.x[1].jbeg = it.x[0].jbeg;
+    it.x[1].jend = it.x[0].jend;
+    it.jlo = it.x[0].jbeg;
+    it.jhi = it.x[0].jend;
+  } else {
+    it.shard = lane / A.nql;
+    const int c = lane % A.nql;
+    it.g = c / A.grp;
+    it.x[0].c = it.x[1].c = c;
+    it.x[0].q0 = unit * 2 * kTile;
+    it.x[1].q0 = it.x[0].q0 + kTile;
+    tile_range(A, it.x[0]);
+    tile_range(A, it.x[1]);
+    const bool a = it.x[0].jend > it.x[0].jbeg, b = it.x[1].jend > it.x[1].jbeg;
+    it.jlo = a && (!b || it.x[0].jbeg < it.x[1].jbeg) ? it.x[0].jbeg : it.x[1].jbeg;
+    it.jhi = b ? it.x[1].jend : it.x[0].jend;
+  }
+  return it;
+}
+
+__device__ __forceinline__ bool active(const QTile& q, int j) { return j >= q.jbeg && j < q.jend; }
+
+// Rows whose result is not finite, again from their own keys (kept out of the main loop's registers).
+template <int D>
+__device__ __noinline__ void redo_rows(const PackArgs& A, int shard, int c, int q0, unsigned rows, int lane) {
+  while (rows) {
+    const int i = q0 + __ffs(rows) - 1;
+    rows &= rows - 1;
+    fwd_row<D>(A, A.s[shard], c, i, doc_of(A.cu, A.batch, static_cast<int>(A.T), i), lane);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_constant__ FwdParams P) {
+  using C = FwdCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sRing = smem + C::OFF_RING;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* ring_full = q_empty + 1;
+  uint64_t* ring_empty = ring_full + kRing;
+  uint64_t* s_full = ring_empty + kRing;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* done_bar = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 + 2 * kRing + 6 + 1) * 8 + 8 <= 256, "barrier area");
+
+  const PackArgs& A = P.a;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int total = P.units * P.lanes;
+  int* status = A.status;
+  const uint64_t tmo = P.timeout_ns;
+  // Round n of the persistent loop: blocks in turn, every other round in reverse, so that the block that
+  // took the heaviest item of a round takes the lightest of the next.
+  auto item_at = [&](int n) {
+    const int b = static_cast<int>(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    return n * static_cast<int>(gridDim.x) + b;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&ring_full[s], 1);
+      mbar_init(&ring_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);   // the tile's four softmax warps
+      mbar_init(&o_full[x], 1);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  if (blockIdx.x == 0) check_docs(A.cu, A.batch, A.T, status);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA loads
+    bool ok = true;
+    int pos = 0, nq = 0;
+    for (int n = 0; item_at(n) < total; ++n) {
+      const Item it = item_of(P, item_at(n));
+      if (it.jhi <= it.jlo) continue;
+      if (lane == 0 && ok) {
+        ok = mbar_wait(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
+        if (ok) {
+          const bool two = it.x[1].jend > it.x[1].jbeg, one = it.x[0].jend > it.x[0].jbeg;
+          mbar_arrive_expect_tx(q_full, (two ? C::TILE : 0) + (one ? C::TILE : 0));
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (x ? two : one)
+              for (int kb = 0; kb < C::KB; ++kb)
+                tma_load_2d(sQ + x * C::TILE + kb * 16384, &P.q[it.shard], q_full, it.x[x].c * D + kb * 64, it.x[x].q0);
+          ++nq;
+        }
+        for (int j = it.jlo; ok && j < it.jhi; ++j)
+          for (int v = 0; ok && v < 2; ++v, ++pos) {
+            const int slot = pos % kRing;
+            ok = mbar_wait(&ring_empty[slot], (static_cast<uint32_t>(pos / kRing) & 1u) ^ 1u, abort_flag, status, tmo);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&ring_full[slot], C::TILE);
+            for (int kb = 0; kb < C::KB; ++kb)
+              tma_load_2d(sRing + slot * C::TILE + kb * 16384, v ? &P.v[it.shard] : &P.k[it.shard], &ring_full[slot],
+                          it.g * D + kb * 64, j * kTile);
+          }
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+    }
+    if (lane == 0) {
+      // No copy may still be landing when the CTA leaves: wait (bounded) for the last loads.
+      int dummy = 0;
+      volatile int* da = reinterpret_cast<volatile int*>(&dummy);
+      if (nq > 0) mbar_wait(q_full, static_cast<uint32_t>(nq - 1) & 1u, da, status, tmo);
+      const int pending = pos < kRing ? pos : kRing;
+      for (int i = pos - pending; i < pos; ++i)
+        mbar_wait(&ring_full[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, da, status, tmo);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    bool ok = true;
+    int pos = 0, nq = 0, np[2] = {0, 0};
+    const uint32_t ring0 = smem_u32(sRing);
+    const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+    const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
+    const uint32_t idesc_o = idesc_bf16_f32(kTile, D, false, true);
+    auto wait_slot = [&](int p) {
+      if (!mbar_wait(&ring_full[p % kRing], static_cast<uint32_t>(p / kRing) & 1u, abort_flag, status, tmo)) return false;
+      tc_fence_after_sync();
+      return true;
+    };
+    for (int n = 0; item_at(n) < total; ++n) {
+      const Item it = item_of(P, item_at(n));
+      if (it.jhi <= it.jlo) continue;
+      if (lane == 0 && ok) {
+        ok = mbar_wait(q_full, static_cast<uint32_t>(nq) & 1u, abort_flag, status, tmo);
+        tc_fence_after_sync();
+        ++nq;
+        // Step j issues P V of key tile j and then S of key tile j + 1, tile by tile; K_j is at ring
+        // position pos + 2 (j - jlo), V_j behind it.
+        for (int j = it.jlo - 1; ok && j < it.jhi; ++j) {
+          const int kp = pos + 2 * (j + 1 - it.jlo), vp = kp - 1;
+          bool got_k = false, got_v = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (ok && active(it.x[x], j)) {
+              if (!got_v) ok = wait_slot(vp);
+              got_v = true;
+              ok = ok && mbar_wait(&p_full[x], static_cast<uint32_t>(np[x]) & 1u, abort_flag, status, tmo);
+              if (!ok) continue;
+              tc_fence_after_sync();
+              ++np[x];
+              const uint64_t vd = smem_desc_sw128(ring0 + (vp % kRing) * C::TILE, 16384, 1024);
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                umma_bf16_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, desc_advance(vd, kk * 2048), idesc_o,
+                             (j > it.x[x].jbeg || kk) ? 1u : 0u);
+              if (j + 1 == it.x[x].jend) umma_commit(&o_full[x]);
+            }
+            if (ok && active(it.x[x], j + 1)) {
+              if (!got_k) ok = wait_slot(kp);
+              got_k = true;
+              if (!ok) continue;
+              const uint64_t kd = smem_desc_sw128(ring0 + (kp % kRing) * C::TILE, 16, 1024);
+              for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16(tmem + x * 128, desc_advance(qd, x * C::TILE + kb * 16384 + kk * 32),
+                            desc_advance(kd, kb * 16384 + kk * 32), idesc_s, (kb | kk) ? 1u : 0u);
+              umma_commit(&s_full[x]);
+            }
+          }
+          if (!ok) break;
+          if (j >= it.jlo) {
+            if (!got_v) ok = wait_slot(vp);            // a slot nobody read is still passed on in order
+            umma_commit(&ring_empty[vp % kRing]);
+          }
+          if (ok && j + 1 < it.jhi) {
+            if (!got_k) ok = wait_slot(kp);
+            umma_commit(&ring_empty[kp % kRing]);
+          }
+          if (j + 2 == it.jhi) umma_commit(q_empty);   // the last S of the item is issued
+        }
+        pos += 2 * (it.jhi - it.jlo);
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+    }
+    if (lane == 0) {
+      umma_commit(done_bar);   // every MMA issued here must finish before TMEM is released
+      int dummy = 0;
+      mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ softmax of tile x
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int quad = warp & 3;
+    const int x = (warp - 4) >> 2;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t s_col = lane_base + x * 128, o_col = lane_base + 256 + x * 128;
+    const float k2 = A.scale * kLog2e;
+    const int T = static_cast<int>(A.T);
+    bool ok = true;
+    uint32_t ns = 0, no = 0;
+    for (int n = 0; ok && item_at(n) < total; ++n) {
+      const Item it = item_of(P, item_at(n));
+      const QTile qt = x ? it.x[1] : it.x[0];
+      const PackShard& S = A.s[it.shard];
+      const int i = qt.q0 + r;
+      DocRange doc{0, 0};
+      if (qt.jend > qt.jbeg) doc = doc_of(A.cu, A.batch, T, i);
+      const bool in = doc.hi > doc.lo;           // a row of a document (so i < T)
+      const int lo = in ? doc.lo : 0x7fffffff, hi = in ? i : -1;      // its keys are lo..hi
+      const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
+      float m = -INFINITY, l = 0.0f;
+      for (int j = qt.jbeg; ok && j < qt.jend; ++j) {
+        ok = mbar_wait(&s_full[x], ns & 1u, abort_flag, status, tmo);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ++ns;
+        tc_fence_after_sync();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) tmem_ld_32x32b_x32(s_col + u * 32, s[u]);
+        tmem_ld_wait();
+        const int k0 = j * kTile;
+        if (k0 < lo_max || k0 + kTile - 1 > hi_min) {   // some row of the warp does not see every key
+          const int a = lo - k0, b = hi - k0;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              s[u][e] = (u * 32 + e >= a && u * 32 + e <= b) ? s[u][e] : 0xff800000u;
+        }
+        float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          x0 = fmax3(x0, __uint_as_float(s[0][e]), __uint_as_float(s[0][e + 1]));
+          x1 = fmax3(x1, __uint_as_float(s[1][e]), __uint_as_float(s[1][e + 1]));
+          x2 = fmax3(x2, __uint_as_float(s[2][e]), __uint_as_float(s[2][e + 1]));
+          x3 = fmax3(x3, __uint_as_float(s[3][e]), __uint_as_float(s[3][e + 1]));
+        }
+        const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * k2;
+        const bool move = mx > m + kLazy || (m == -INFINITY && mx > m);
+        if (__any_sync(0xffffffffu, move)) {
+          const float mn = move ? mx : m;
+          const float f = move ? ex2_approx(m - mn) : 1.0f;
+          l *= f;
+          m = mn;
+          if (j > qt.jbeg) {
+            // O_x holds the products up to key tile j - 1: they were issued before S_x(j), which is complete.
+            for (int u = 0; u < D / 32; ++u) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(o_col + u * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x32(o_col + u * 32, o);
+            }
+          }
+        }
+        const float nm = m == -INFINITY ? 0.0f : -m;
+        const uint64_t kk2 = f2_pack(k2, k2), nm2 = f2_pack(nm, nm);
+        uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 a = f2_unpack(ffma2(f2_pack(__uint_as_float(s[2 * h][e]), __uint_as_float(s[2 * h][e + 1])), kk2, nm2));
+            const float2 b =
+                f2_unpack(ffma2(f2_pack(__uint_as_float(s[2 * h + 1][e]), __uint_as_float(s[2 * h + 1][e + 1])), kk2, nm2));
+            const float a0 = ex2_approx(a.x), a1 = ex2_approx(a.y), b0 = ex2_approx(b.x), b1 = ex2_approx(b.y);
+            sum0 = fadd2(sum0, f2_pack(a0, a1));
+            sum1 = fadd2(sum1, f2_pack(b0, b1));
+            p[e >> 1] = pack_bf16x2(a0, a1);
+            p[16 + (e >> 1)] = pack_bf16x2(b0, b1);
+          }
+          tmem_st_32x32b_x32(s_col + h * 32, p);
+        }
+        const float2 t0 = f2_unpack(sum0), t1 = f2_unpack(sum1);
+        l += (t0.x + t0.y) + (t1.x + t1.y);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      // ---- the row's result
+      const bool computed = qt.jend > qt.jbeg;
+      if (computed) {
+        ok = mbar_wait(&o_full[x], no & 1u, abort_flag, status, tmo);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ++no;
+        tc_fence_after_sync();
+      }
+      const float inv = in ? 1.0f / l : 0.0f;
+      bool fine = true;
+      __nv_bfloat16* out = S.o + static_cast<int64_t>(i < T ? i : 0) * A.ldo + qt.c * D;
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) {
+        uint32_t o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+        if (computed) {
+          tmem_ld_32x32b_x32(o_col + u * 32, o);
+          tmem_ld_wait();
+        }
+        if (!in) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float v = __uint_as_float(o[e]) * inv;
+          fine &= fabsf(v) < INFINITY;
+          o[e] = __float_as_uint(v);
+        }
+        if (i < T) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            *reinterpret_cast<uint4*>(out + u * 32 + w * 8) = make_uint4(
+                pack_bf16x2(__uint_as_float(o[w * 8 + 0]), __uint_as_float(o[w * 8 + 1])),
+                pack_bf16x2(__uint_as_float(o[w * 8 + 2]), __uint_as_float(o[w * 8 + 3])),
+                pack_bf16x2(__uint_as_float(o[w * 8 + 4]), __uint_as_float(o[w * 8 + 5])),
+                pack_bf16x2(__uint_as_float(o[w * 8 + 6]), __uint_as_float(o[w * 8 + 7])));
+        }
+      }
+      tc_fence_before_sync();
+      if (i < T) S.lse[static_cast<int64_t>(qt.c) * A.T + i] = in ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      const unsigned again = __ballot_sync(0xffffffffu, in && !fine);
+      __syncwarp();   // the rows' stores above come before those of the redo
+      if (again) redo_rows<D>(A, it.shard, qt.c, qt.q0 + quad * 32, again, lane);
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+int set_core_smem_once(const void* fn, int slot, int bytes, const char* what) {
+  static std::mutex mu;
+  static bool done[kPackKernelSlots][64] = {};
+  int dev = 0;
+  int rc = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc) return rc;
+  if (dev < 0 || dev >= 64) return set_error(TTL_ERR_CUDA, "device index %d out of range", dev);
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[slot][dev]) return TTL_OK;
+  rc = cuda_check(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), what);
+  if (!rc) done[slot][dev] = true;
+  return rc;
+}
+
+int pack_attn_fwd_launch(const PackArgs& A, int d, cudaStream_t stream) {
+  FwdParams P;
+  std::memset(static_cast<void*>(&P), 0, sizeof(P));
+  P.a = A;
+  const int64_t qc = static_cast<int64_t>(A.nql) * d, kc = static_cast<int64_t>(A.nkvl) * d;
+  int rc = TTL_OK;
+  for (int i = 0; i < A.t; ++i) {
+    if ((rc = encode_map_bf16(&P.q[i], A.s[i].q, A.T, qc, A.ldq, 64, kTile)) ||
+        (rc = encode_map_bf16(&P.k[i], A.s[i].k, A.T, kc, A.ldk, 64, kTile)) ||
+        (rc = encode_map_bf16(&P.v[i], A.s[i].v, A.T, kc, A.ldv, 64, kTile)))
+      return rc;
+  }
+  const int tiles = static_cast<int>((A.T + kTile - 1) / kTile);
+  P.pair_heads = A.grp % 2 == 0;
+  P.units = P.pair_heads ? tiles : (tiles + 1) / 2;
+  P.lanes = P.pair_heads ? A.t * A.nql / 2 : A.t * A.nql;
+  P.timeout_ns = 2000000000ull;
+  const int64_t items = static_cast<int64_t>(P.units) * P.lanes;
+  if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many query tiles");
+  const int sms = num_sms();
+  const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
+  const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
+  TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * tri * d * A.nql * A.t,
+                   2.0 * A.T * (2.0 * qc + 2.0 * kc) * A.t);
+  if (d == 128) {
+    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_fwd_kernel<128>), kPackFwd128, FwdCfg<128>::SMEM,
+                                 "cudaFuncSetAttribute(packed attention forward)")))
+      return rc;
+    pack_fwd_kernel<128><<<grid, kFwdThreads, FwdCfg<128>::SMEM, stream>>>(P);
+  } else {
+    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_fwd_kernel<64>), kPackFwd64, FwdCfg<64>::SMEM,
+                                 "cudaFuncSetAttribute(packed attention forward)")))
+      return rc;
+    pack_fwd_kernel<64><<<grid, kFwdThreads, FwdCfg<64>::SMEM, stream>>>(P);
+  }
+  return cuda_check(cudaGetLastError(), "pack_fwd_kernel launch");
+}
+
+}  // namespace ttl
