@@ -17,27 +17,6 @@
 namespace ttl {
 namespace {
 
-constexpr int kRowWarps = 8;
-
-template <int D>
-__global__ void __launch_bounds__(kRowWarps * 32) pack_dq_row_kernel(const __grid_constant__ PackArgs A) {
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_docs(A.cu, A.batch, A.T, A.status);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  if (i >= A.T) return;
-  const int shard = blockIdx.y / A.nql, c = blockIdx.y % A.nql;
-  dq_row<D>(A, A.s[shard], shard, c, static_cast<int>(i),
-            doc_of(A.cu, A.batch, static_cast<int>(A.T), static_cast<int>(i)), threadIdx.x & 31);
-}
-
-template <int D>
-__global__ void __launch_bounds__(kRowWarps * 32) pack_dkv_row_kernel(const __grid_constant__ PackArgs A) {
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  if (j >= A.T) return;
-  const int shard = blockIdx.y / A.nkvl, g = blockIdx.y % A.nkvl;
-  dkv_row<D>(A, A.s[shard], shard, g, static_cast<int>(j),
-             doc_of(A.cu, A.batch, static_cast<int>(A.T), static_cast<int>(j)), threadIdx.x & 31);
-}
-
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int check_shape(int t, int64_t T, int n_q, int n_kv, int d, int batch, const char* name) {
@@ -181,20 +160,6 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
   A.cu = cu_seqlens; A.batch = batch; A.scale = scale;
   A.D = static_cast<float*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const double tri = static_cast<double>(T) * (T + 1) / 2.0;
-  const unsigned rows = static_cast<unsigned>((T + kRowWarps - 1) / kRowWarps);
-  {
-    TraceScope trace(s, TTL_K_ATTN_CORE, 6.0 * tri * d * n_q, 2.0 * T * d * (4.0 * n_q + 2.0 * n_kv));
-    if (d == 128)
-      pack_dq_row_kernel<128><<<dim3(rows, n_q), kRowWarps * 32, 0, s>>>(A);
-    else
-      pack_dq_row_kernel<64><<<dim3(rows, n_q), kRowWarps * 32, 0, s>>>(A);
-    if ((rc = cuda_check(cudaGetLastError(), "packed attention dQ launch"))) return rc;
-  }
-  TraceScope trace(s, TTL_K_ATTN_CORE, 4.0 * tri * d * n_q, 2.0 * T * d * (2.0 * n_q + 4.0 * n_kv));
-  if (d == 128)
-    pack_dkv_row_kernel<128><<<dim3(rows, n_kv), kRowWarps * 32, 0, s>>>(A);
-  else
-    pack_dkv_row_kernel<64><<<dim3(rows, n_kv), kRowWarps * 32, 0, s>>>(A);
-  return cuda_check(cudaGetLastError(), "packed attention dK dV launch");
+  if ((rc = pack_attn_dq_launch(A, d, s))) return rc;
+  return pack_attn_dkv_launch(A, d, s);
 }

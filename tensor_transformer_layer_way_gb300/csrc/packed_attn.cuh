@@ -40,7 +40,11 @@ int set_core_smem_once(const void* fn, int slot, int bytes, const char* what);
 
 // Launches of the tensor-core kernels (arguments are checked; A.s holds every pointer they need).
 int pack_attn_fwd_launch(const PackArgs& A, int d, cudaStream_t stream);
+int pack_attn_dq_launch(const PackArgs& A, int d, cudaStream_t stream);    // dQ and D
+int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream);   // dK and dV, after D
 
+constexpr int kTile = 128;       // tokens per query or key tile
+constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -56,6 +60,22 @@ __device__ __forceinline__ DocRange doc_of(const int32_t* cu, int batch, int T, 
   while (r - l > 1) {
     const int m = (l + r) >> 1;
     if (__ldg(cu + m) <= tok) l = m; else r = m;
+  }
+  const int lo = __ldg(cu + l), hi = __ldg(cu + r);
+  return DocRange{lo < 0 ? 0 : lo, hi > T ? T : hi};
+}
+
+// The same for one token of a document (cu[0] <= tok < cu[batch]), by a whole warp: 32 bounds at a time.
+__device__ __forceinline__ DocRange doc_of_warp(const int32_t* cu, int batch, int T, int tok) {
+  const int lane = threadIdx.x & 31;
+  int l = 0, r = batch;
+  while (r - l > 1) {
+    const int step = (r - l - 1 + 31) / 32;
+    const int at = l + step * (lane + 1);
+    const unsigned le = __ballot_sync(0xffffffffu, at < r && __ldg(cu + at) <= tok);
+    const int n = le == 0xffffffffu ? 32 : __ffs(~le) - 1;
+    l += step * n;
+    r = r < l + step ? r : l + step;
   }
   const int lo = __ldg(cu + l), hi = __ldg(cu + r);
   return DocRange{lo < 0 ? 0 : lo, hi > T ? T : hi};
@@ -173,11 +193,11 @@ __device__ __forceinline__ void dq_row(const PackArgs& A, const PackShard& S, in
   if (lane == 0) A.D[(static_cast<int64_t>(shard) * A.nql + c) * A.T + i] = Di;
 }
 
-// dk_j and dv_j of KV head g, summed over the group's query heads.
+// dk_j (want_k) or dv_j of KV head g, summed over the group's query heads.
 template <int D>
 __device__ __forceinline__ void dkv_row(const PackArgs& A, const PackShard& S, int shard, int g, int j, DocRange doc,
-                                        int lane) {
-  RowVec<D> dk = row_zero<D>(), dv = row_zero<D>();
+                                        bool want_k, int lane) {
+  RowVec<D> acc = row_zero<D>();
   if (doc.hi > doc.lo) {
     const RowVec<D> k = row_load<D>(S.k + j * A.ldk + g * D, lane);
     const RowVec<D> v = row_load<D>(S.v + j * A.ldv + g * D, lane);
@@ -189,14 +209,10 @@ __device__ __forceinline__ void dkv_row(const PackArgs& A, const PackShard& S, i
         const float p = exp2f(row_dot(q, k) * k2 - S.lse[static_cast<int64_t>(c) * A.T + i] * kLog2e);
         const float ds = p * (row_dot(go, v) - A.D[(static_cast<int64_t>(shard) * A.nql + c) * A.T + i]) * A.scale;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-          dk.x[e] = fmaf(ds, q.x[e], dk.x[e]);
-          dv.x[e] = fmaf(p, go.x[e], dv.x[e]);
-        }
+        for (int e = 0; e < D / 32; ++e) acc.x[e] = want_k ? fmaf(ds, q.x[e], acc.x[e]) : fmaf(p, go.x[e], acc.x[e]);
       }
   }
-  row_store<D>(S.dk + j * A.lddk + g * D, dk, lane);
-  row_store<D>(S.dv + j * A.lddv + g * D, dv, lane);
+  row_store<D>((want_k ? S.dk + j * A.lddk : S.dv + j * A.lddv) + g * D, acc, lane);
 }
 
 }  // namespace ttl

@@ -1,0 +1,533 @@
+// dK and dV of packed causal attention on the tensor cores.
+//
+// One work item is a 128-token key tile of one KV head; it meets the query tiles from its own to the one
+// that holds the last token of its last key's document, each with every query head of the group
+// (step n: query tile, head), the last query tile first.  With the keys as rows:
+//   S^T = K Q^T, dP^T = V dO^T (fp32, tensor memory), P^T = 2^(s k - lse), dS^T = P^T (dP^T - D),
+//   dV += P^T dO, dK += dS^T Q, dK scaled once at the end.
+// P^T and dS^T go back to tensor memory as bf16 over the columns of S^T and dP^T, where they are the A
+// operands; the Q and dO tiles are read K-major for the scores and MN-major for the sums.  Nothing but
+// the four operand tiles passes through shared memory.
+//
+// S^T, dP^T, dK and dV fill tensor memory (4 x 128 columns), so the order of the products is what keeps the
+// tensor pipe busy: S(n+1), dK(n), dP(n+1), dV(n+1), S(n+2), ...  While the elementwise warps turn S(n+1)
+// into P, dK(n) and dP(n+1) run; while they form dS(n+1), dV(n+1) and S(n+2) do.
+//
+// Roles (384 threads, persistent): warp 0 the TMA loads, warp 1 the MMAs, warp 2 brings each step's lse and D
+// to shared memory, warps 4..11 the elementwise work: a key row per thread, each warpgroup on 64 of the queries.
+
+#include <cstring>
+
+#include "packed_attn.cuh"
+
+namespace ttl {
+namespace {
+
+constexpr int kKvThreads = 384;
+constexpr int kSlots = 2;      // Q and dO tiles
+constexpr int kStat = 2;       // lse and D stages
+
+struct KvParams {
+  CUtensorMap q[kMaxShards];   // box 64 x 128
+  CUtensorMap k[kMaxShards];
+  CUtensorMap v[kMaxShards];
+  CUtensorMap dO[kMaxShards];
+  PackArgs a;
+  int tiles, lanes;
+  uint64_t timeout_ns;
+};
+
+template <int D>
+struct KvCfg {
+  static constexpr int KB = D / 64;
+  static constexpr int TILE = KB * kTile * 128;
+  static constexpr int OFF_V = TILE;
+  static constexpr int OFF_Q = 2 * TILE;
+  static constexpr int OFF_DO = OFF_Q + kSlots * TILE;
+  static constexpr int OFF_STAT = OFF_DO + kSlots * TILE;   // float [kStat][2][128]: -lse log2(e), -D
+  static constexpr int OFF_BAR = OFF_STAT + kStat * 1024;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
+};
+
+struct KvItem {
+  int shard, g, k0, qt_first, qt_last, steps;   // query tiles [qt_first, qt_last], steps = tiles x group
+};
+
+__device__ __forceinline__ KvItem kv_item(const KvParams& P, int at) {
+  const PackArgs& A = P.a;
+  const int tile = at / P.lanes, ln = at % P.lanes;
+  KvItem it;
+  it.shard = ln / A.nkvl;
+  it.g = ln % A.nkvl;
+  it.k0 = tile * kTile;
+  it.qt_first = tile;
+  it.qt_last = tile - 1;
+  it.steps = 0;
+  if (A.batch > 0) {
+    const int T = static_cast<int>(A.T);
+    const int first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
+    const int v0 = it.k0 > first ? it.k0 : first;
+    int v1 = it.k0 + kTile < last ? it.k0 + kTile : last;
+    v1 = v1 < T ? v1 : T;
+    if (v0 < v1) {
+      const int hi = doc_of_warp(A.cu, A.batch, T, v1 - 1).hi;   // > v1 - 1
+      it.qt_last = (hi > v1 ? hi - 1 : v1 - 1) / kTile;
+      it.steps = (it.qt_last - tile + 1) * A.grp;
+    }
+  }
+  return it;
+}
+
+template <int D>
+__device__ __noinline__ void redo_dkv(const PackArgs& A, int shard, int g, int k0, unsigned rows, bool want_k, int lane) {
+  while (rows) {
+    const int j = k0 + __ffs(rows) - 1;
+    rows &= rows - 1;
+    dkv_row<D>(A, A.s[shard], shard, g, j, doc_of(A.cu, A.batch, static_cast<int>(A.T), j), want_k, lane);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_constant__ KvParams P) {
+  using C = KvCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + C::OFF_V;
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sDO = smem + C::OFF_DO;
+  float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* k_empty = k_full + 1;
+  uint64_t* v_full = k_empty + 1;
+  uint64_t* v_empty = v_full + 1;
+  uint64_t* q_full = v_empty + 1;
+  uint64_t* q_empty = q_full + kSlots;
+  uint64_t* do_full = q_empty + kSlots;
+  uint64_t* do_empty = do_full + kSlots;
+  uint64_t* st_full = do_empty + kSlots;
+  uint64_t* st_empty = st_full + kStat;
+  uint64_t* s_full = st_empty + kStat;
+  uint64_t* p_full = s_full + 1;
+  uint64_t* dp_full = p_full + 1;
+  uint64_t* ds_full = dp_full + 1;
+  uint64_t* acc_full = ds_full + 1;
+  uint64_t* done_bar = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((4 + 4 * kSlots + 2 * kStat + 6) * 8 + 8 <= 256, "barrier area");
+  constexpr uint32_t T_DP = 128, T_DK = 256, T_DV = 384;
+
+  const PackArgs& A = P.a;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int total = P.tiles * P.lanes;
+  int* status = A.status;
+  const uint64_t tmo = P.timeout_ns;
+  auto item_at = [&](int n) {
+    const int b = static_cast<int>(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    return n * static_cast<int>(gridDim.x) + b;
+  };
+  // Step n of an item: the last query tile first, the group's heads in turn.
+  auto step_q0 = [&](const KvItem& it, int n) { return (it.qt_last - n / A.grp) * kTile; };
+  auto step_head = [&](const KvItem& it, int n) { return it.g * A.grp + n % A.grp; };
+
+  if (threadIdx.x == 0) {
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
+    mbar_init(v_full, 1);
+    mbar_init(v_empty, 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&do_full[s], 1);
+      mbar_init(&do_empty[s], 1);
+    }
+    for (int s = 0; s < kStat; ++s) {
+      mbar_init(&st_full[s], 1);
+      mbar_init(&st_empty[s], 8);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 8);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 8);
+    mbar_init(acc_full, 1);
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA loads
+    bool ok = true;
+    int nk = 0, nv = 0, nq = 0, nd = 0;   // loads started: K, V, Q, dO tiles
+    for (int n = 0; item_at(n) < total; ++n) {
+      const KvItem it = kv_item(P, item_at(n));
+      if (it.steps == 0) continue;
+      if (lane == 0 && ok) {
+        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint32_t phase, int x, int y) {
+          if (!mbar_wait(empty, (phase & 1u) ^ 1u, abort_flag, status, tmo)) return false;
+          mbar_arrive_expect_tx(full, C::TILE);
+          for (int kb = 0; kb < C::KB; ++kb) tma_load_2d(dst + kb * 16384, map, full, x + kb * 64, y);
+          return true;
+        };
+        for (int t = 0; ok && t < it.steps; ++t) {
+          const int qs = nq % kSlots, ds = nd % kSlots;
+          if (t == 0) {
+            ok = load(sK, &P.k[it.shard], k_full, k_empty, nk, it.g * D, it.k0);
+            nk += ok;
+          }
+          if (ok) {
+            ok = load(sQ + qs * C::TILE, &P.q[it.shard], &q_full[qs], &q_empty[qs], nq / kSlots, step_head(it, t) * D,
+                      step_q0(it, t));
+            nq += ok;
+          }
+          if (ok && t == 0) {
+            ok = load(sV, &P.v[it.shard], v_full, v_empty, nv, it.g * D, it.k0);
+            nv += ok;
+          }
+          if (ok) {
+            ok = load(sDO + ds * C::TILE, &P.dO[it.shard], &do_full[ds], &do_empty[ds], nd / kSlots,
+                      step_head(it, t) * D, step_q0(it, t));
+            nd += ok;
+          }
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+    }
+    if (lane == 0) {
+      // No copy may still be landing when the CTA leaves: wait (bounded) for the last loads.
+      int dummy = 0;
+      volatile int* da = reinterpret_cast<volatile int*>(&dummy);
+      if (nk > 0) mbar_wait(k_full, static_cast<uint32_t>(nk - 1) & 1u, da, status, tmo);
+      if (nv > 0) mbar_wait(v_full, static_cast<uint32_t>(nv - 1) & 1u, da, status, tmo);
+      for (int i = nq > kSlots ? nq - kSlots : 0; i < nq; ++i)
+        mbar_wait(&q_full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u, da, status, tmo);
+      for (int i = nd > kSlots ? nd - kSlots : 0; i < nd; ++i)
+        mbar_wait(&do_full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u, da, status, tmo);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    bool ok = true;
+    int ni = 0, pos = 0;
+    const uint64_t kd = smem_desc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t vd = smem_desc_sw128(smem_u32(sV), 16, 1024);
+    const uint32_t qa = smem_u32(sQ), doa = smem_u32(sDO);
+    const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
+    const uint32_t idesc_acc = idesc_bf16_f32(kTile, D, false, true);
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      if (!mbar_wait(bar, phase & 1u, abort_flag, status, tmo)) return false;
+      tc_fence_after_sync();
+      return true;
+    };
+    // [keys x queries] = A B^T, both K-major tiles of D columns
+    auto scores = [&](uint32_t dst, uint64_t ad, uint32_t baddr) {
+      const uint64_t bd = smem_desc_sw128(baddr, 16, 1024);
+      for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16(dst, desc_advance(ad, kb * 16384 + kk * 32), desc_advance(bd, kb * 16384 + kk * 32), idesc_s,
+                    (kb | kk) ? 1u : 0u);
+    };
+    // [keys x D] += A B: A from tensor memory (queries [64 w, 64 w + 64) at columns 64 w ..), B read MN-major
+    auto sum = [&](uint32_t dst, uint32_t acol, uint32_t baddr, bool first) {
+      const uint64_t bd = smem_desc_sw128(baddr, 16384, 1024);
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        umma_bf16_ts(dst, acol + (kk >> 2) * 64 + (kk & 3) * 8, desc_advance(bd, kk * 2048), idesc_acc,
+                     (!first || kk) ? 1u : 0u);
+    };
+    for (int n = 0; item_at(n) < total; ++n) {
+      const KvItem it = kv_item(P, item_at(n));
+      if (it.steps == 0) continue;
+      if (lane == 0 && ok) {
+        ok = wait(k_full, ni);
+        // S^T of step t overwrites P^T of the step before, whose dV product was issued before it (the tensor
+        // pipe runs one thread's products in order); likewise dP^T and dK.
+        for (int t = -1; ok && t < it.steps; ++t) {
+          const int p = pos + t, p1 = p + 1;
+          if (t + 1 < it.steps) {
+            if (!(ok = wait(&q_full[p1 % kSlots], p1 / kSlots))) break;
+            scores(tmem, kd, qa + (p1 % kSlots) * C::TILE);
+            umma_commit(s_full);
+            if (t + 2 == it.steps) umma_commit(k_empty);
+          }
+          if (t >= 0) {
+            if (!(ok = wait(ds_full, p))) break;
+            sum(tmem + T_DK, tmem + T_DP, qa + (p % kSlots) * C::TILE, t == 0);
+            umma_commit(&q_empty[p % kSlots]);
+          }
+          if (t + 1 < it.steps) {
+            if (t < 0 && !(ok = wait(v_full, ni))) break;
+            if (!(ok = wait(&do_full[p1 % kSlots], p1 / kSlots))) break;
+            scores(tmem + T_DP, vd, doa + (p1 % kSlots) * C::TILE);
+            umma_commit(dp_full);
+            if (t + 2 == it.steps) umma_commit(v_empty);
+            if (!(ok = wait(p_full, p1))) break;
+            sum(tmem + T_DV, tmem, doa + (p1 % kSlots) * C::TILE, t < 0);
+            umma_commit(&do_empty[p1 % kSlots]);
+          }
+        }
+        if (ok) umma_commit(acc_full);
+        ++ni;
+        pos += it.steps;
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+    }
+    if (lane == 0) {
+      umma_commit(done_bar);   // every MMA issued here must finish before TMEM is released
+      int dummy = 0;
+      mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ lse and D of each step's queries
+    bool ok = true;
+    int pos = 0;
+    for (int n = 0; ok && item_at(n) < total; ++n) {
+      const KvItem it = kv_item(P, item_at(n));
+      const float* lse = A.s[it.shard].lse;
+      const float* Dr = A.D + static_cast<int64_t>(it.shard) * A.nql * A.T;
+      for (int t = 0; t < it.steps; ++t, ++pos) {
+        const int st = pos % kStat;
+        const int64_t row = static_cast<int64_t>(step_head(it, t)) * A.T;
+        const int q0 = step_q0(it, t);
+        float a[4], b[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int q = q0 + u * 32 + lane;
+          a[u] = q < A.T ? -__ldg(lse + row + q) * kLog2e : 0.0f;
+          b[u] = q < A.T ? -__ldg(Dr + row + q) : 0.0f;
+        }
+        ok = mbar_wait(&st_empty[st], (static_cast<uint32_t>(pos / kStat) & 1u) ^ 1u, abort_flag, status, tmo);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          stat[st * 256 + u * 32 + lane] = a[u];
+          stat[st * 256 + 128 + u * 32 + lane] = b[u];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st_full[st]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ P^T and dS^T
+    const int quad = warp & 3;
+    const int half = (warp - 4) >> 2;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const float k2 = A.scale * kLog2e;
+    const uint64_t kk2 = f2_pack(k2, k2);
+    const int T = static_cast<int>(A.T);
+    bool ok = true;
+    int pos = 0, ni = 0;
+    for (int n = 0; ok && item_at(n) < total; ++n) {
+      const KvItem it = kv_item(P, item_at(n));
+      const PackShard& S = A.s[it.shard];
+      const int key = it.k0 + r;
+      DocRange doc{0, 0};
+      if (it.steps > 0) doc = doc_of(A.cu, A.batch, T, key);
+      const bool in = doc.hi > doc.lo;
+      const int lo = in ? key : 0x7fffffff, hi = in ? doc.hi - 1 : -1;     // the queries that see the key
+      const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
+      for (int t = 0; ok && t < it.steps; ++t, ++pos) {
+        const int st = pos % kStat;
+        const int q0 = step_q0(it, t) + half * 64;
+        const bool masked = q0 < lo_max || q0 + 63 > hi_min;
+        const float4* nl = reinterpret_cast<const float4*>(stat + st * 256 + half * 64);
+        const float4* nD = reinterpret_cast<const float4*>(stat + st * 256 + 128 + half * 64);
+        ok = mbar_wait(&st_full[st], static_cast<uint32_t>(pos / kStat) & 1u, abort_flag, status, tmo) &&
+             mbar_wait(s_full, static_cast<uint32_t>(pos) & 1u, abort_flag, status, tmo);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        uint32_t s[2][32];
+        tmem_ld_32x32b_x32(lane_base + half * 64, s[0]);
+        tmem_ld_32x32b_x32(lane_base + half * 64 + 32, s[1]);
+        tmem_ld_wait();
+        const int a = lo - q0, b = hi - q0;
+        uint32_t pk[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 n4 = nl[(h * 32 + e) >> 2];
+            const float2 u = f2_unpack(
+                ffma2(f2_pack(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1])), kk2, f2_pack(n4.x, n4.y)));
+            const float2 w = f2_unpack(
+                ffma2(f2_pack(__uint_as_float(s[h][e + 2]), __uint_as_float(s[h][e + 3])), kk2, f2_pack(n4.z, n4.w)));
+            s[h][e] = __float_as_uint(ex2_approx(u.x));
+            s[h][e + 1] = __float_as_uint(ex2_approx(u.y));
+            s[h][e + 2] = __float_as_uint(ex2_approx(w.x));
+            s[h][e + 3] = __float_as_uint(ex2_approx(w.y));
+          }
+        if (masked) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[h][e] = (h * 32 + e >= a && h * 32 + e <= b) ? s[h][e] : 0u;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            pk[h * 16 + (e >> 1)] = pack_bf16x2(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]));
+        tmem_st_32x32b_x32(lane_base + half * 64, pk);   // over this thread's own columns of S^T
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        ok = mbar_wait(dp_full, static_cast<uint32_t>(pos) & 1u, abort_flag, status, tmo);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        uint32_t dp[2][32];
+        tmem_ld_32x32b_x32(lane_base + T_DP + half * 64, dp[0]);
+        tmem_ld_32x32b_x32(lane_base + T_DP + half * 64 + 32, dp[1]);
+        tmem_ld_wait();
+        if (masked) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) dp[h][e] = (h * 32 + e >= a && h * 32 + e <= b) ? dp[h][e] : 0u;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float4 n4 = nD[(h * 32 + e) >> 2];
+            if (masked) {   // a hidden query's D may be anything
+              n4.x = h * 32 + e >= a && h * 32 + e <= b ? n4.x : 0.0f;
+              n4.y = h * 32 + e + 1 >= a && h * 32 + e + 1 <= b ? n4.y : 0.0f;
+              n4.z = h * 32 + e + 2 >= a && h * 32 + e + 2 <= b ? n4.z : 0.0f;
+              n4.w = h * 32 + e + 3 >= a && h * 32 + e + 3 <= b ? n4.w : 0.0f;
+            }
+            const float2 u = f2_unpack(fmul2(
+                fadd2(f2_pack(__uint_as_float(dp[h][e]), __uint_as_float(dp[h][e + 1])), f2_pack(n4.x, n4.y)),
+                f2_pack(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]))));
+            const float2 w = f2_unpack(fmul2(
+                fadd2(f2_pack(__uint_as_float(dp[h][e + 2]), __uint_as_float(dp[h][e + 3])), f2_pack(n4.z, n4.w)),
+                f2_pack(__uint_as_float(s[h][e + 2]), __uint_as_float(s[h][e + 3]))));
+            pk[h * 16 + (e >> 1)] = pack_bf16x2(u.x, u.y);
+            pk[h * 16 + (e >> 1) + 1] = pack_bf16x2(w.x, w.y);
+          }
+        tmem_st_32x32b_x32(lane_base + T_DP + half * 64, pk);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(ds_full);
+          mbar_arrive(&st_empty[st]);
+        }
+      }
+      if (!ok) break;
+      // ---- the first warpgroup stores dK, the second dV
+      const bool computed = it.steps > 0;
+      if (computed) {
+        ok = mbar_wait(acc_full, static_cast<uint32_t>(ni) & 1u, abort_flag, status, tmo);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ++ni;
+        tc_fence_after_sync();
+      }
+      bool fine = true;
+      const float f = half ? 1.0f : A.scale;
+      const int64_t off = (half ? A.lddv : A.lddk) * static_cast<int64_t>(key < T ? key : 0) + it.g * D;
+      __nv_bfloat16* out = (half ? S.dv : S.dk) + off;
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) {
+        uint32_t o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+        if (computed) {
+          tmem_ld_32x32b_x32(lane_base + (half ? T_DV : T_DK) + u * 32, o);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float v = in ? __uint_as_float(o[e]) * f : 0.0f;
+          fine &= fabsf(v) < INFINITY;
+          o[e] = __float_as_uint(v);
+        }
+        if (key < T) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            *reinterpret_cast<uint4*>(out + u * 32 + w * 8) = make_uint4(
+                pack_bf16x2(__uint_as_float(o[w * 8 + 0]), __uint_as_float(o[w * 8 + 1])),
+                pack_bf16x2(__uint_as_float(o[w * 8 + 2]), __uint_as_float(o[w * 8 + 3])),
+                pack_bf16x2(__uint_as_float(o[w * 8 + 4]), __uint_as_float(o[w * 8 + 5])),
+                pack_bf16x2(__uint_as_float(o[w * 8 + 6]), __uint_as_float(o[w * 8 + 7])));
+        }
+      }
+      tc_fence_before_sync();
+      const unsigned again = __ballot_sync(0xffffffffu, in && !fine);
+      __syncwarp();   // the rows' stores above come before those of the redo
+      if (again) redo_dkv<D>(A, it.shard, it.g, it.k0 + quad * 32, again, half == 0, lane);
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream) {
+  KvParams P;
+  std::memset(static_cast<void*>(&P), 0, sizeof(P));
+  P.a = A;
+  const int64_t qc = static_cast<int64_t>(A.nql) * d, kc = static_cast<int64_t>(A.nkvl) * d;
+  int rc = TTL_OK;
+  for (int i = 0; i < A.t; ++i) {
+    if ((rc = encode_map_bf16(&P.q[i], A.s[i].q, A.T, qc, A.ldq, 64, kTile)) ||
+        (rc = encode_map_bf16(&P.k[i], A.s[i].k, A.T, kc, A.ldk, 64, kTile)) ||
+        (rc = encode_map_bf16(&P.v[i], A.s[i].v, A.T, kc, A.ldv, 64, kTile)) ||
+        (rc = encode_map_bf16(&P.dO[i], A.s[i].dO, A.T, qc, A.lddo, 64, kTile)))
+      return rc;
+  }
+  P.tiles = static_cast<int>((A.T + kTile - 1) / kTile);
+  P.lanes = A.t * A.nkvl;
+  P.timeout_ns = 2000000000ull;
+  const int64_t items = static_cast<int64_t>(P.tiles) * P.lanes;
+  if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many key tiles");
+  const int sms = num_sms();
+  const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
+  const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
+  TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * tri * d * A.nql * A.t, 2.0 * A.T * (2.0 * qc + 4.0 * kc) * A.t);
+  if (d == 128) {
+    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dkv_kernel<128>), kPackDkv128, KvCfg<128>::SMEM,
+                                 "cudaFuncSetAttribute(packed attention dK dV)")))
+      return rc;
+    pack_dkv_kernel<128><<<grid, kKvThreads, KvCfg<128>::SMEM, stream>>>(P);
+  } else {
+    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dkv_kernel<64>), kPackDkv64, KvCfg<64>::SMEM,
+                                 "cudaFuncSetAttribute(packed attention dK dV)")))
+      return rc;
+    pack_dkv_kernel<64><<<grid, kKvThreads, KvCfg<64>::SMEM, stream>>>(P);
+  }
+  return cuda_check(cudaGetLastError(), "pack_dkv_kernel launch");
+}
+
+}  // namespace ttl

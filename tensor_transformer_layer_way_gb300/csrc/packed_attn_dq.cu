@@ -1,0 +1,502 @@
+// dQ of packed causal attention on the tensor cores, and D = rowsum(dO O) for the dK and dV kernel.
+//
+// One work item is a 128-token query tile of one head; its key tiles are those of the forward kernel.
+// Per key tile:  S = Q K^T and dP = dO V^T (fp32, tensor memory), P = 2^(s k - lse), dS = P (dP - D) as
+// bf16 in tensor memory, dQ += dS K with dS as the A operand; dQ is scaled once at the end.  dQ and
+// (dK, dV) are two kernels, so every sum has one owner and a fixed order: the price is S and dP twice
+// (7 products where one kernel with atomic additions into dQ would need 5).
+//
+// Roles (384 threads, persistent): warp 0 the TMA loads (K three slots deep, read by S_j and again by dQ_j;
+// V two), warp 1 the MMAs in the order S_(j+1), dP_(j+1), dQ_j, so that two products run while the
+// elementwise warps form dS_j; warps 4..11 that: a row per thread, each warpgroup on 64 of the keys.
+// S, dP and dQ take 384 columns of tensor memory and two dS buffers the rest.
+
+#include <cstring>
+
+#include "packed_attn.cuh"
+
+namespace ttl {
+namespace {
+
+constexpr int kDqThreads = 384;
+constexpr int kKSlots = 3;
+constexpr int kVSlots = 2;
+
+struct DqParams {
+  CUtensorMap q[kMaxShards];   // box 64 x 128
+  CUtensorMap k[kMaxShards];
+  CUtensorMap v[kMaxShards];
+  CUtensorMap dO[kMaxShards];
+  PackArgs a;
+  int tiles, lanes;
+  uint64_t timeout_ns;
+};
+
+template <int D>
+struct DqCfg {
+  static constexpr int KB = D / 64;
+  static constexpr int TILE = KB * kTile * 128;
+  static constexpr int OFF_DO = TILE;
+  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int OFF_V = OFF_K + kKSlots * TILE;
+  static constexpr int OFF_X = OFF_V + kVSlots * TILE;   // float [2][128]: the two halves of D; int [128]: flags
+  static constexpr int OFF_BAR = OFF_X + 1536;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
+};
+
+struct DqItem {
+  int shard, c, g, q0, jbeg, jend;
+};
+
+__device__ __forceinline__ DqItem dq_item(const DqParams& P, int at) {
+  const PackArgs& A = P.a;
+  const int tile = P.tiles - 1 - at / P.lanes, ln = at % P.lanes;
+  DqItem it;
+  it.shard = ln / A.nql;
+  it.c = ln % A.nql;
+  it.g = it.c / A.grp;
+  it.q0 = tile * kTile;
+  it.jbeg = it.jend = 0;
+  if (A.batch > 0) {
+    const int T = static_cast<int>(A.T);
+    const int first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
+    const int v0 = it.q0 > first ? it.q0 : first;
+    int v1 = it.q0 + kTile < last ? it.q0 + kTile : last;
+    v1 = v1 < T ? v1 : T;
+    if (v0 < v1) {
+      it.jbeg = doc_of_warp(A.cu, A.batch, T, v0).lo / kTile;
+      it.jend = tile + 1;
+    }
+  }
+  return it;
+}
+
+template <int D>
+__device__ __noinline__ void redo_dq(const PackArgs& A, int shard, int c, int q0, unsigned rows, int lane) {
+  while (rows) {
+    const int i = q0 + __ffs(rows) - 1;
+    rows &= rows - 1;
+    dq_row<D>(A, A.s[shard], shard, c, i, doc_of(A.cu, A.batch, static_cast<int>(A.T), i), lane);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_constant__ DqParams P) {
+  using C = DqCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sDO = smem + C::OFF_DO;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  float* xch = reinterpret_cast<float*>(smem + C::OFF_X);
+  int* flags = reinterpret_cast<int*>(smem + C::OFF_X + 1024);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* k_full = q_empty + 1;
+  uint64_t* k_empty = k_full + kKSlots;
+  uint64_t* v_full = k_empty + kKSlots;
+  uint64_t* v_empty = v_full + kVSlots;
+  uint64_t* s_full = v_empty + kVSlots;
+  uint64_t* s_empty = s_full + 1;
+  uint64_t* dp_full = s_empty + 1;
+  uint64_t* dp_empty = dp_full + 1;
+  uint64_t* ds_full = dp_empty + 1;    // [2]
+  uint64_t* ds_empty = ds_full + 2;    // [2]
+  uint64_t* dq_full = ds_empty + 2;
+  uint64_t* dq_empty = dq_full + 1;
+  uint64_t* x_bar = dq_empty + 1;      // the eight elementwise warps meet
+  uint64_t* done_bar = x_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 + 2 * kKSlots + 2 * kVSlots + 12) * 8 + 8 <= 256, "barrier area");
+  constexpr uint32_t T_DP = 128, T_DQ = 256, T_DS = 384;
+
+  const PackArgs& A = P.a;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int total = P.tiles * P.lanes;
+  int* status = A.status;
+  const uint64_t tmo = P.timeout_ns;
+  auto item_at = [&](int n) {
+    const int b = static_cast<int>(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    return n * static_cast<int>(gridDim.x) + b;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < kKSlots; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < kVSlots; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, 8);
+    mbar_init(dp_full, 1);
+    mbar_init(dp_empty, 8);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ds_full[b], 8);
+      mbar_init(&ds_empty[b], 1);
+    }
+    mbar_init(dq_full, 1);
+    mbar_init(dq_empty, 8);
+    mbar_init(x_bar, 8);
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  if (blockIdx.x == 0) check_docs(A.cu, A.batch, A.T, status);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA loads
+    bool ok = true;
+    int pos = 0, nq = 0;    // key tiles and items started
+    for (int n = 0; item_at(n) < total; ++n) {
+      const DqItem it = dq_item(P, item_at(n));
+      if (it.jend <= it.jbeg) continue;
+      if (lane == 0 && ok) {
+        ok = mbar_wait(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
+        if (ok) {
+          mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+          for (int kb = 0; kb < C::KB; ++kb) {
+            tma_load_2d(sQ + kb * 16384, &P.q[it.shard], q_full, it.c * D + kb * 64, it.q0);
+            tma_load_2d(sDO + kb * 16384, &P.dO[it.shard], q_full, it.c * D + kb * 64, it.q0);
+          }
+          ++nq;
+        }
+        for (int j = it.jbeg; ok && j < it.jend; ++j, ++pos) {
+          const int ks = pos % kKSlots, vs = pos % kVSlots;
+          ok = mbar_wait(&k_empty[ks], (static_cast<uint32_t>(pos / kKSlots) & 1u) ^ 1u, abort_flag, status, tmo);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&k_full[ks], C::TILE);
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_2d(sK + ks * C::TILE + kb * 16384, &P.k[it.shard], &k_full[ks], it.g * D + kb * 64, j * kTile);
+          // (K was started: from here the position counts as started even if the wait for V fails)
+          ok = mbar_wait(&v_empty[vs], (static_cast<uint32_t>(pos / kVSlots) & 1u) ^ 1u, abort_flag, status, tmo);
+          if (!ok) {
+            int dummy = 0;
+            mbar_wait(&k_full[ks], static_cast<uint32_t>(pos / kKSlots) & 1u, reinterpret_cast<volatile int*>(&dummy),
+                      status, tmo);
+            break;
+          }
+          mbar_arrive_expect_tx(&v_full[vs], C::TILE);
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_2d(sV + vs * C::TILE + kb * 16384, &P.v[it.shard], &v_full[vs], it.g * D + kb * 64, j * kTile);
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+    }
+    if (lane == 0) {
+      // No copy may still be landing when the CTA leaves: wait (bounded) for the last loads.
+      int dummy = 0;
+      volatile int* da = reinterpret_cast<volatile int*>(&dummy);
+      if (nq > 0) mbar_wait(q_full, static_cast<uint32_t>(nq - 1) & 1u, da, status, tmo);
+      for (int i = pos > kKSlots ? pos - kKSlots : 0; i < pos; ++i)
+        mbar_wait(&k_full[i % kKSlots], static_cast<uint32_t>(i / kKSlots) & 1u, da, status, tmo);
+      for (int i = pos > kVSlots ? pos - kVSlots : 0; i < pos; ++i)
+        mbar_wait(&v_full[i % kVSlots], static_cast<uint32_t>(i / kVSlots) & 1u, da, status, tmo);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    bool ok = true;
+    int pos = 0, nq = 0;
+    const uint32_t k0a = smem_u32(sK), v0a = smem_u32(sV);
+    const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dod = smem_desc_sw128(smem_u32(sDO), 16, 1024);
+    const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
+    const uint32_t idesc_dq = idesc_bf16_f32(kTile, D, false, true);
+    for (int n = 0; item_at(n) < total; ++n) {
+      const DqItem it = dq_item(P, item_at(n));
+      const int nt = it.jend - it.jbeg;
+      if (nt <= 0) continue;
+      if (lane == 0 && ok) {
+        ok = mbar_wait(q_full, static_cast<uint32_t>(nq) & 1u, abort_flag, status, tmo);
+        tc_fence_after_sync();
+        ++nq;
+        for (int j = -1; ok && j < nt; ++j) {
+          if (j + 1 < nt) {
+            const int p = pos + j + 1;
+            const int ks = p % kKSlots, vs = p % kVSlots;
+            ok = mbar_wait(&k_full[ks], static_cast<uint32_t>(p / kKSlots) & 1u, abort_flag, status, tmo) &&
+                 mbar_wait(s_empty, (static_cast<uint32_t>(p) & 1u) ^ 1u, abort_flag, status, tmo);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint64_t kd = smem_desc_sw128(k0a + ks * C::TILE, 16, 1024);
+            for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(tmem, desc_advance(qd, kb * 16384 + kk * 32), desc_advance(kd, kb * 16384 + kk * 32), idesc_s,
+                          (kb | kk) ? 1u : 0u);
+            umma_commit(s_full);
+            ok = mbar_wait(&v_full[vs], static_cast<uint32_t>(p / kVSlots) & 1u, abort_flag, status, tmo) &&
+                 mbar_wait(dp_empty, (static_cast<uint32_t>(p) & 1u) ^ 1u, abort_flag, status, tmo);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint64_t vd = smem_desc_sw128(v0a + vs * C::TILE, 16, 1024);
+            for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(tmem + T_DP, desc_advance(dod, kb * 16384 + kk * 32), desc_advance(vd, kb * 16384 + kk * 32),
+                          idesc_s, (kb | kk) ? 1u : 0u);
+            umma_commit(dp_full);
+            umma_commit(&v_empty[vs]);
+            if (j + 2 == nt) umma_commit(q_empty);   // the item's last read of Q and dO
+          }
+          if (j >= 0) {
+            const int p = pos + j, ks = p % kKSlots, b = p & 1;
+            ok = mbar_wait(&ds_full[b], static_cast<uint32_t>(p >> 1) & 1u, abort_flag, status, tmo);
+            // the previous item's dQ has been read before this one's first product overwrites it
+            if (ok && j == 0)
+              ok = mbar_wait(dq_empty, (static_cast<uint32_t>(nq - 1) & 1u) ^ 1u, abort_flag, status, tmo);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint64_t kd = smem_desc_sw128(k0a + ks * C::TILE, 16384, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_bf16_ts(tmem + T_DQ, tmem + T_DS + b * 64 + kk * 8, desc_advance(kd, kk * 2048), idesc_dq,
+                           (j | kk) ? 1u : 0u);
+            umma_commit(&ds_empty[b]);
+            umma_commit(&k_empty[ks]);
+            if (j + 1 == nt) umma_commit(dq_full);
+          }
+        }
+        pos += nt;
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+    }
+    if (lane == 0) {
+      umma_commit(done_bar);   // every MMA issued here must finish before TMEM is released
+      int dummy = 0;
+      mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ dS
+    const int quad = warp & 3;
+    const int half = (warp - 4) >> 2;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const float k2 = A.scale * kLog2e;
+    const int T = static_cast<int>(A.T);
+    bool ok = true;
+    int pos = 0, no = 0;
+    uint32_t met = 0;
+    // All eight warps meet (a bounded wait, unlike a hardware barrier).
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x_bar);
+      const bool in_time = mbar_wait(x_bar, met & 1u, abort_flag, status, tmo);
+      ++met;
+      return static_cast<bool>(__all_sync(0xffffffffu, in_time));
+    };
+    for (int n = 0; ok && item_at(n) < total; ++n) {
+      const DqItem it = dq_item(P, item_at(n));
+      const PackShard& S = A.s[it.shard];
+      const int i = it.q0 + r;
+      DocRange doc{0, 0};
+      if (it.jend > it.jbeg) doc = doc_of(A.cu, A.batch, T, i);
+      const bool in = doc.hi > doc.lo;
+      // D_i: this thread's half of the head's columns, the other half from the other warpgroup
+      float part = 0.0f;
+      if (in) {
+        const uint4* go = reinterpret_cast<const uint4*>(S.dO + i * A.lddo + it.c * D + half * (D / 2));
+        const uint4* oo = reinterpret_cast<const uint4*>(S.o + i * A.ldo + it.c * D + half * (D / 2));
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+          const uint4 a = __ldg(go + u), b = __ldg(oo + u);
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) part = fmaf(bf16_lo(aw[w]), bf16_lo(bw[w]), fmaf(bf16_hi(aw[w]), bf16_hi(bw[w]), part));
+        }
+      }
+      xch[half * kTile + r] = part;   // (the last item's were read before the warps met at its end)
+      if (!(ok = meet())) break;
+      const float Di = xch[r] + xch[kTile + r];
+      const int64_t stat = static_cast<int64_t>(it.c) * A.T + (i < T ? i : 0);
+      if (half == 0 && i < T) A.D[static_cast<int64_t>(it.shard) * A.nql * A.T + stat] = Di;
+      const float nl = in ? -S.lse[stat] * kLog2e : 0.0f;
+      const int lo = in ? doc.lo : 0x7fffffff, hi = in ? i : -1;
+      const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
+      const uint64_t kk2 = f2_pack(k2, k2), nl2 = f2_pack(nl, nl), nD2 = f2_pack(-Di, -Di);
+      for (int j = it.jbeg; ok && j < it.jend; ++j, ++pos) {
+        ok = mbar_wait(s_full, static_cast<uint32_t>(pos) & 1u, abort_flag, status, tmo);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        uint32_t s[2][32];
+        tmem_ld_32x32b_x32(lane_base + half * 64, s[0]);
+        tmem_ld_32x32b_x32(lane_base + half * 64 + 32, s[1]);
+        tmem_ld_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(s_empty);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 a = f2_unpack(ffma2(f2_pack(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1])), kk2, nl2));
+            s[h][e] = __float_as_uint(ex2_approx(a.x));
+            s[h][e + 1] = __float_as_uint(ex2_approx(a.y));
+          }
+        ok = mbar_wait(dp_full, static_cast<uint32_t>(pos) & 1u, abort_flag, status, tmo);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        uint32_t dp[2][32];
+        tmem_ld_32x32b_x32(lane_base + T_DP + half * 64, dp[0]);
+        tmem_ld_32x32b_x32(lane_base + T_DP + half * 64 + 32, dp[1]);
+        tmem_ld_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(dp_empty);
+        const int k0 = j * kTile + half * 64;
+        if (k0 < lo_max || k0 + 63 > hi_min) {   // some row of the warp does not see every key
+          const int a = lo - k0, b = hi - k0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const bool see = h * 32 + e >= a && h * 32 + e <= b;
+              s[h][e] = see ? s[h][e] : 0u;
+              dp[h][e] = see ? dp[h][e] : 0u;
+            }
+        }
+        uint32_t ds[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t d2 = fadd2(f2_pack(__uint_as_float(dp[h][e]), __uint_as_float(dp[h][e + 1])), nD2);
+            const float2 v = f2_unpack(fmul2(d2, f2_pack(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]))));
+            ds[h * 16 + (e >> 1)] = pack_bf16x2(v.x, v.y);
+          }
+        const int b = pos & 1;
+        ok = mbar_wait(&ds_empty[b], (static_cast<uint32_t>(pos >> 1) & 1u) ^ 1u, abort_flag, status, tmo);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        tmem_st_32x32b_x32(lane_base + T_DS + b * 64 + half * 32, ds);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ds_full[b]);
+      }
+      if (!ok) break;
+      const bool computed = it.jend > it.jbeg;
+      if (computed) {
+        ok = mbar_wait(dq_full, static_cast<uint32_t>(no) & 1u, abort_flag, status, tmo);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ++no;
+        tc_fence_after_sync();
+      }
+      bool fine = true;
+      __nv_bfloat16* out = S.dq + static_cast<int64_t>(i < T ? i : 0) * A.lddq + it.c * D + half * (D / 2);
+#pragma unroll
+      for (int u = 0; u < D / 64; ++u) {
+        uint32_t o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+        if (computed) {
+          tmem_ld_32x32b_x32(lane_base + T_DQ + half * (D / 2) + u * 32, o);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float v = in ? __uint_as_float(o[e]) * A.scale : 0.0f;
+          fine &= fabsf(v) < INFINITY;
+          o[e] = __float_as_uint(v);
+        }
+        if (i < T) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            *reinterpret_cast<uint4*>(out + u * 32 + w * 8) = make_uint4(
+                pack_bf16x2(__uint_as_float(o[w * 8 + 0]), __uint_as_float(o[w * 8 + 1])),
+                pack_bf16x2(__uint_as_float(o[w * 8 + 2]), __uint_as_float(o[w * 8 + 3])),
+                pack_bf16x2(__uint_as_float(o[w * 8 + 4]), __uint_as_float(o[w * 8 + 5])),
+                pack_bf16x2(__uint_as_float(o[w * 8 + 6]), __uint_as_float(o[w * 8 + 7])));
+        }
+      }
+      if (computed) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(dq_empty);
+      }
+      // A row is redone, by the first warpgroup, if either found its half not finite, after both have stored.
+      if (half == 1) flags[r] = in && !fine;
+      if (!(ok = meet())) break;
+      if (half == 0) {
+        const unsigned again = __ballot_sync(0xffffffffu, in && (!fine || flags[r]));
+        if (again) redo_dq<D>(A, it.shard, it.c, it.q0 + quad * 32, again, lane);
+      }
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+int pack_attn_dq_launch(const PackArgs& A, int d, cudaStream_t stream) {
+  DqParams P;
+  std::memset(static_cast<void*>(&P), 0, sizeof(P));
+  P.a = A;
+  const int64_t qc = static_cast<int64_t>(A.nql) * d, kc = static_cast<int64_t>(A.nkvl) * d;
+  int rc = TTL_OK;
+  for (int i = 0; i < A.t; ++i) {
+    if ((rc = encode_map_bf16(&P.q[i], A.s[i].q, A.T, qc, A.ldq, 64, kTile)) ||
+        (rc = encode_map_bf16(&P.k[i], A.s[i].k, A.T, kc, A.ldk, 64, kTile)) ||
+        (rc = encode_map_bf16(&P.v[i], A.s[i].v, A.T, kc, A.ldv, 64, kTile)) ||
+        (rc = encode_map_bf16(&P.dO[i], A.s[i].dO, A.T, qc, A.lddo, 64, kTile)))
+      return rc;
+  }
+  P.tiles = static_cast<int>((A.T + kTile - 1) / kTile);
+  P.lanes = A.t * A.nql;
+  P.timeout_ns = 2000000000ull;
+  const int64_t items = static_cast<int64_t>(P.tiles) * P.lanes;
+  if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many query tiles");
+  const int sms = num_sms();
+  const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
+  const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
+  TraceScope trace(stream, TTL_K_ATTN_CORE, 6.0 * tri * d * A.nql * A.t, 2.0 * A.T * (4.0 * qc + 2.0 * kc) * A.t);
+  if (d == 128) {
+    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dq_kernel<128>), kPackDq128, DqCfg<128>::SMEM,
+                                 "cudaFuncSetAttribute(packed attention dQ)")))
+      return rc;
+    pack_dq_kernel<128><<<grid, kDqThreads, DqCfg<128>::SMEM, stream>>>(P);
+  } else {
+    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dq_kernel<64>), kPackDq64, DqCfg<64>::SMEM,
+                                 "cudaFuncSetAttribute(packed attention dQ)")))
+      return rc;
+    pack_dq_kernel<64><<<grid, kDqThreads, DqCfg<64>::SMEM, stream>>>(P);
+  }
+  return cuda_check(cudaGetLastError(), "pack_dq_kernel launch");
+}
+
+}  // namespace ttl

@@ -31,10 +31,8 @@
 namespace ttl {
 namespace {
 
-constexpr int kTile = 128;
 constexpr int kRing = 5;
 constexpr int kFwdThreads = 384;
-constexpr int kTmemCols = 512;
 constexpr float kLazy = 8.0f;
 
 struct FwdParams {
@@ -67,22 +65,6 @@ struct Item {
   QTile x[2];
   int jlo, jhi;                // union of the key tiles
 };
-
-// First token of the document of `tok` (or tok's range), found by the whole warp.
-__device__ __forceinline__ DocRange doc_of_warp(const int32_t* cu, int batch, int T, int tok) {
-  const int lane = threadIdx.x & 31;
-  int l = 0, r = batch;
-  while (r - l > 1) {
-    const int step = (r - l - 1 + 31) / 32;
-    const int at = l + step * (lane + 1);
-    const unsigned le = __ballot_sync(0xffffffffu, at < r && __ldg(cu + at) <= tok);
-    const int n = le == 0xffffffffu ? 32 : __ffs(~le) - 1;
-    l += step * n;
-    r = r < l + step ? r : l + step;
-  }
-  const int lo = __ldg(cu + l), hi = __ldg(cu + r);
-  return DocRange{lo < 0 ? 0 : lo, hi > T ? T : hi};
-}
 
 __device__ __forceinline__ void tile_range(const PackArgs& A, QTile& q) {
   const int T = static_cast<int>(A.T);
