@@ -591,23 +591,60 @@ def tp_attn_bwd(X, dY, Wq, Wk, Wv, Wo, fwd, *, n_q, n_kv, d, out=None, stream=No
     return out
 
 
-# ------------------------------------------------------------------ row-strided operands
+# ------------------------------------------------------------------ checks and pointers in one pass
+# The operators below are also called on a few tokens, where the time of the call is the host's: each tensor
+# is looked at once, and the slow path that words an error runs only when there is one.
 
-def _need_rows(ts, name, n, dtype, rows, cols):
-    """Checks n CUDA matrices [rows, cols] whose rows are contiguous and share one row stride;
-    returns that stride in elements."""
-    if not isinstance(ts, (list, tuple)) or len(ts) != n:
-        raise ValueError(f"{name} must be a list of {n} tensors")
+_ARRS = [None] + [ctypes.c_void_p * n for n in range(1, TTL_MAX_SHARDS + 1)]
+
+
+def _refuse(x, name, dtype, shape):
+    """Raises what is wrong with x."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must hold tensors")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _list_of(ts, name, n):
+    if not isinstance(ts, (list, tuple)) or len(ts) != n or not 1 <= n <= TTL_MAX_SHARDS:
+        raise ValueError(f"{name} must be a list of {n} tensors (1 to {TTL_MAX_SHARDS})")
+
+
+def _ptr(x, name, dtype, shape):
+    """The pointer of one contiguous CUDA tensor."""
+    if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.shape != shape or not x.is_cuda or not x.is_contiguous():
+        _refuse(x, name, dtype, shape)
+    return x.data_ptr()
+
+
+def _ptrs(ts, name, n, dtype, shape):
+    """The pointers of n contiguous CUDA tensors as a host array."""
+    _list_of(ts, name, n)
+    out = _ARRS[n]()
+    for i, x in enumerate(ts):
+        if (not isinstance(x, torch.Tensor) or x.dtype != dtype or x.shape != shape or not x.is_cuda
+                or not x.is_contiguous()):
+            _refuse(x, name, dtype, shape)
+        out[i] = x.data_ptr()
+    return out
+
+
+def _rows(ts, name, n, dtype, rows, cols):
+    """The pointers of n CUDA matrices [rows, cols] whose rows are contiguous and share one row
+    stride, and that stride in elements."""
+    _list_of(ts, name, n)
+    out = _ARRS[n]()
+    shape = (rows, cols)
     ld = None
-    for x in ts:
-        if not isinstance(x, torch.Tensor):
-            raise TypeError(f"{name} must hold tensors")
-        if x.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-        if not x.is_cuda:
-            raise ValueError(f"{name} must be CUDA tensors")
-        if x.shape != (rows, cols):
-            raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {(rows, cols)}")
+    for i, x in enumerate(ts):
+        if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.shape != shape or not x.is_cuda:
+            _refuse(x, name, dtype, shape)
         step, col = x.stride()
         if col != 1 and cols > 1:
             raise ValueError(f"{name}: rows must be contiguous")
@@ -617,7 +654,15 @@ def _need_rows(ts, name, n, dtype, rows, cols):
             ld = step
         elif step != ld:
             raise ValueError(f"{name}: the tensors must share one row stride")
-    return ld
+        out[i] = x.data_ptr()
+    return out, ld
+
+
+def _queue(x, stream):
+    """The raw stream: the given one, or the current one of x's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(x.get_device())
 
 
 # ------------------------------------------------------------------ layer norm
@@ -634,31 +679,29 @@ def layer_norm_fwd_buffers(t, rows, h, dtype=torch.bfloat16, residual=False, dev
 def _stream_type(X, gamma):
     if not isinstance(X, (list, tuple)) or not X or not isinstance(X[0], torch.Tensor) or X[0].dim() != 2:
         raise ValueError("X must be a list of token slabs [rows, h]")
-    if X[0].dtype not in _TYPES or gamma.dtype not in _TYPES:
+    x = X[0]
+    dt, wt = _TYPES.get(x.dtype), _TYPES.get(gamma.dtype)
+    if dt is None or wt is None:
         raise TypeError("layer norm takes bf16 or fp32 slabs and weights")
-    return len(X), X[0].shape[0], X[0].shape[1], X[0].dtype
+    rows, h = x.shape
+    return len(X), rows, h, x.dtype, dt, wt
 
 
 def layer_norm_fwd(X, gamma, beta=None, *, eps=1e-5, residual=None, out=None, stream=None):
     """Layer norm of the token slabs X (a list of [rows, h], bf16 or fp32), of X + residual where
     given.  Returns dict Y, S (the sums, None without a residual), mean, rstd (lists)."""
-    t, rows, h, dt = _stream_type(X, gamma)
-    ldx = _need_rows(X, "X", t, dt, rows, h)
-    ldr = h if residual is None else _need_rows(residual, "residual", t, dt, rows, h)
-    _need(gamma, "gamma", gamma.dtype, (h,))
-    if beta is not None:
-        _need(beta, "beta", gamma.dtype, (h,))
+    t, rows, h, dtype, dt, wt = _stream_type(X, gamma)
+    x, ldx = _rows(X, "X", t, dtype, rows, h)
+    r, ldr = (None, h) if residual is None else _rows(residual, "residual", t, dtype, rows, h)
+    g = _ptr(gamma, "gamma", gamma.dtype, (h,))
+    b = None if beta is None else _ptr(beta, "beta", gamma.dtype, (h,))
     if out is None:
-        out = layer_norm_fwd_buffers(t, rows, h, dt, residual is not None, X[0].device)
-    _need_list(out["Y"], "Y", t, dt, (rows, h))
-    _need_list(out["mean"], "mean", t, torch.float32, (rows,))
-    _need_list(out["rstd"], "rstd", t, torch.float32, (rows,))
-    S = None
-    if residual is not None:
-        S = _need_list(out["S"], "S", t, dt, (rows, h))
-    _check(lib().ttl_layer_norm_fwd(t, rows, h, _TYPES[dt], _TYPES[gamma.dtype], _arr(X), ldx, _arr(residual), ldr,
-                                    _p(gamma), _p(beta), float(eps), _arr(S), _arr(out["Y"]), _arr(out["mean"]),
-                                    _arr(out["rstd"]), _stream(stream)))
+        out = layer_norm_fwd_buffers(t, rows, h, dtype, residual is not None, X[0].device)
+    s = None if residual is None else _ptrs(out["S"], "S", t, dtype, (rows, h))
+    f = torch.float32
+    _check(lib().ttl_layer_norm_fwd(t, rows, h, dt, wt, x, ldx, r, ldr, g, b, eps, s,
+                                    _ptrs(out["Y"], "Y", t, dtype, (rows, h)), _ptrs(out["mean"], "mean", t, f, (rows,)),
+                                    _ptrs(out["rstd"], "rstd", t, f, (rows,)), _queue(X[0], stream)))
     return out
 
 
@@ -674,26 +717,22 @@ def layer_norm_bwd(X, dY, gamma, fwd, *, dS=None, accumulate=False, out=None, st
     """Backward of layer_norm_fwd: X is the normalised input (fwd["S"] where there was a residual),
     ``fwd`` holds its mean and rstd, dS is the gradient that reaches X past the block.  Returns dict
     dX (list), dgamma, dbeta (fp32; with ``accumulate`` added to those of ``out``)."""
-    t, rows, h, dt = _stream_type(X, gamma)
-    ldx = _need_rows(X, "X", t, dt, rows, h)
-    lddy = _need_rows(dY, "dY", t, dt, rows, h)
-    ldds = h if dS is None else _need_rows(dS, "dS", t, dt, rows, h)
-    _need(gamma, "gamma", gamma.dtype, (h,))
-    _need_list(fwd["mean"], "mean", t, torch.float32, (rows,))
-    _need_list(fwd["rstd"], "rstd", t, torch.float32, (rows,))
+    t, rows, h, dtype, dt, wt = _stream_type(X, gamma)
+    x, ldx = _rows(X, "X", t, dtype, rows, h)
+    dy, lddy = _rows(dY, "dY", t, dtype, rows, h)
+    ds, ldds = (None, h) if dS is None else _rows(dS, "dS", t, dtype, rows, h)
+    f = torch.float32
+    g = _ptr(gamma, "gamma", gamma.dtype, (h,))
+    mean, rstd = _ptrs(fwd["mean"], "mean", t, f, (rows,)), _ptrs(fwd["rstd"], "rstd", t, f, (rows,))
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = layer_norm_bwd_buffers(t, rows, h, dt, X[0].device)
-    _need_list(out["dX"], "dX", t, dt, (rows, h))
-    _need(out["dgamma"], "dgamma", torch.float32, (h,))
-    if out["dbeta"] is not None:
-        _need(out["dbeta"], "dbeta", torch.float32, (h,))
-    ws = out["ws"]
-    _check(lib().ttl_layer_norm_bwd(t, rows, h, _TYPES[dt], _TYPES[gamma.dtype], _arr(X), ldx, _arr(dY), lddy,
-                                    _arr(dS), ldds, _p(gamma), _arr(fwd["mean"]), _arr(fwd["rstd"]), _arr(out["dX"]),
-                                    _p(out["dgamma"]), _p(out["dbeta"]), int(bool(accumulate)), _p(ws), ws.numel(),
-                                    _stream(stream)))
+        out = layer_norm_bwd_buffers(t, rows, h, dtype, X[0].device)
+    ws, dbeta = out["ws"], out["dbeta"]
+    _check(lib().ttl_layer_norm_bwd(t, rows, h, dt, wt, x, ldx, dy, lddy, ds, ldds, g, mean, rstd,
+                                    _ptrs(out["dX"], "dX", t, dtype, (rows, h)), _ptr(out["dgamma"], "dgamma", f, (h,)),
+                                    None if dbeta is None else _ptr(dbeta, "dbeta", f, (h,)), 1 if accumulate else 0,
+                                    ws.data_ptr(), ws.numel(), _queue(X[0], stream)))
     return out
 
 
@@ -705,13 +744,13 @@ def vocab_parallel_embedding_scaled_fwd(ids, E, scale, *, out=None, stream=None)
     t = len(E)
     Vs, h = E[0].shape
     T = ids.shape[0]
-    _need(ids, "ids", torch.int64, (T,))
-    _need_list(E, "E", t, shape=(Vs, h))
+    bf16 = torch.bfloat16
+    i = _ptr(ids, "ids", torch.int64, (T,))
+    e = _ptrs(E, "E", t, bf16, (Vs, h))
     if out is None:
-        out = [torch.empty((T, h), device=ids.device, dtype=torch.bfloat16) for _ in range(t)]
-    _need_list(out, "out", t, shape=(T, h))
-    _check(lib().ttl_vocab_parallel_embedding_scaled_fwd(t, T, h, Vs * t, _p(ids), _arr(E), float(scale), _arr(out),
-                                                         _stream(stream)))
+        out = [torch.empty((T, h), device=ids.device, dtype=bf16) for _ in range(t)]
+    _check(lib().ttl_vocab_parallel_embedding_scaled_fwd(t, T, h, Vs * t, i, e, scale,
+                                                         _ptrs(out, "out", t, bf16, (T, h)), _queue(ids, stream)))
     return out
 
 
@@ -728,14 +767,14 @@ def vocab_parallel_embedding_sorted_bwd(ids, dY, scale, dE, *, accumulate=False,
     t = len(dE)
     Vs, h = dE[0].shape
     T = ids.shape[0]
-    _need(ids, "ids", torch.int64, (T,))
-    lddy = _need_rows([dY], "dY", 1, torch.bfloat16, T, h)
-    _need_list(dE, "dE", t, torch.float32, (Vs, h))
+    i = _ptr(ids, "ids", torch.int64, (T,))
+    dy, lddy = _rows([dY], "dY", 1, torch.bfloat16, T, h)
+    de = _ptrs(dE, "dE", t, torch.float32, (Vs, h))
     if ws is None:
         ws = embedding_sorted_bwd_workspace(t, T, h, Vs * t, ids.device)
-    _check(lib().ttl_vocab_parallel_embedding_sorted_bwd(t, T, h, Vs * t, _p(ids), _p(dY), lddy, float(scale),
-                                                         _arr(dE), int(bool(accumulate)), _p(ws), ws.numel(),
-                                                         _stream(stream)))
+    _check(lib().ttl_vocab_parallel_embedding_sorted_bwd(t, T, h, Vs * t, i, dy[0], lddy, scale, de,
+                                                         1 if accumulate else 0, ws.data_ptr(), ws.numel(),
+                                                         _queue(ids, stream)))
     return dE
 
 
@@ -757,21 +796,21 @@ def packed_attn_fwd(Q, K, V, cu_seqlens, *, n_q, n_kv, d, scale=None, out=None, 
     Returns dict O ([T, n_q/t d] per shard) and lse ([n_q/t, T] fp32 per shard)."""
     t = len(Q)
     T = Q[0].shape[0]
-    qc, kc = n_q // t * d, n_kv // t * d
+    nql = n_q // t
+    qc, kc = nql * d, n_kv // t * d
     bf16 = torch.bfloat16
-    ldq, ldk = _need_rows(Q, "Q", t, bf16, T, qc), _need_rows(K, "K", t, bf16, T, kc)
-    ldv = _need_rows(V, "V", t, bf16, T, kc)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),))
-    batch = cu_seqlens.numel() - 1
+    q, ldq = _rows(Q, "Q", t, bf16, T, qc)
+    k, ldk = _rows(K, "K", t, bf16, T, kc)
+    v, ldv = _rows(V, "V", t, bf16, T, kc)
+    bounds = cu_seqlens.numel()
+    cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (bounds,))
     if out is None:
-        out = packed_attn_fwd_buffers(t, T, n_q, n_kv, d, batch, Q[0].device)
-    ldo = _need_rows(out["O"], "O", t, bf16, T, qc)
-    _need_list(out["lse"], "lse", t, torch.float32, (n_q // t, T))
+        out = packed_attn_fwd_buffers(t, T, n_q, n_kv, d, bounds - 1, Q[0].device)
+    o, ldo = _rows(out["O"], "O", t, bf16, T, qc)
     ws = out["ws"]
-    _check(lib().ttl_packed_attn_fwd(t, T, n_q, n_kv, d, batch, _p(cu_seqlens),
-                                     float(d ** -0.5 if scale is None else scale), _arr(Q), ldq, _arr(K), ldk,
-                                     _arr(V), ldv, _arr(out["O"]), ldo, _arr(out["lse"]), _p(ws), ws.numel(),
-                                     _stream(stream)))
+    _check(lib().ttl_packed_attn_fwd(t, T, n_q, n_kv, d, bounds - 1, cu, d ** -0.5 if scale is None else scale, q, ldq,
+                                     k, ldk, v, ldv, o, ldo, _ptrs(out["lse"], "lse", t, torch.float32, (nql, T)),
+                                     ws.data_ptr(), ws.numel(), _queue(Q[0], stream)))
     return out
 
 
@@ -790,22 +829,24 @@ def packed_attn_bwd(dO, Q, K, V, fwd, cu_seqlens, *, n_q, n_kv, d, scale=None, o
     the buffers of ``out`` may be column ranges of one fused gradient."""
     t = len(Q)
     T = Q[0].shape[0]
-    qc, kc = n_q // t * d, n_kv // t * d
+    nql = n_q // t
+    qc, kc = nql * d, n_kv // t * d
     bf16 = torch.bfloat16
-    lddo, ldq = _need_rows(dO, "dO", t, bf16, T, qc), _need_rows(Q, "Q", t, bf16, T, qc)
-    ldk, ldv = _need_rows(K, "K", t, bf16, T, kc), _need_rows(V, "V", t, bf16, T, kc)
-    ldo = _need_rows(fwd["O"], "O", t, bf16, T, qc)
-    _need_list(fwd["lse"], "lse", t, torch.float32, (n_q // t, T))
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),))
-    batch = cu_seqlens.numel() - 1
+    do, lddo = _rows(dO, "dO", t, bf16, T, qc)
+    q, ldq = _rows(Q, "Q", t, bf16, T, qc)
+    k, ldk = _rows(K, "K", t, bf16, T, kc)
+    v, ldv = _rows(V, "V", t, bf16, T, kc)
+    o, ldo = _rows(fwd["O"], "O", t, bf16, T, qc)
+    bounds = cu_seqlens.numel()
+    cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (bounds,))
     if out is None:
-        out = packed_attn_bwd_buffers(t, T, n_q, n_kv, d, batch, Q[0].device)
-    lddq = _need_rows(out["dQ"], "dQ", t, bf16, T, qc)
-    lddk, lddv = _need_rows(out["dK"], "dK", t, bf16, T, kc), _need_rows(out["dV"], "dV", t, bf16, T, kc)
+        out = packed_attn_bwd_buffers(t, T, n_q, n_kv, d, bounds - 1, Q[0].device)
+    dq, lddq = _rows(out["dQ"], "dQ", t, bf16, T, qc)
+    dk, lddk = _rows(out["dK"], "dK", t, bf16, T, kc)
+    dv, lddv = _rows(out["dV"], "dV", t, bf16, T, kc)
     ws = out["ws"]
-    _check(lib().ttl_packed_attn_bwd(t, T, n_q, n_kv, d, batch, _p(cu_seqlens),
-                                     float(d ** -0.5 if scale is None else scale), _arr(dO), lddo, _arr(Q), ldq,
-                                     _arr(K), ldk, _arr(V), ldv, _arr(fwd["O"]), ldo, _arr(fwd["lse"]),
-                                     _arr(out["dQ"]), lddq, _arr(out["dK"]), lddk, _arr(out["dV"]), lddv, _p(ws),
-                                     ws.numel(), _stream(stream)))
+    _check(lib().ttl_packed_attn_bwd(t, T, n_q, n_kv, d, bounds - 1, cu, d ** -0.5 if scale is None else scale, do, lddo,
+                                     q, ldq, k, ldk, v, ldv, o, ldo,
+                                     _ptrs(fwd["lse"], "lse", t, torch.float32, (nql, T)), dq, lddq, dk, lddk, dv, lddv,
+                                     ws.data_ptr(), ws.numel(), _queue(Q[0], stream)))
     return out

@@ -12,6 +12,8 @@
 //   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
 // All statistics and sums are fp32; the variance is taken about the mean (no E[x^2] - mean^2).
 
+#include <mutex>
+
 #include "ttl_device.cuh"
 #include "ttl_internal.h"
 
@@ -34,6 +36,7 @@ struct NormFwd {
   int64_t total;               // t rows
   float eps;
   int wtype;
+  int* status;
 };
 
 struct NormBwd {
@@ -48,6 +51,7 @@ struct NormBwd {
   int64_t rows, h, ldx, lddy, ldds;
   int64_t total;
   int wtype;
+  int* status;
 };
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -78,6 +82,666 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += red[w];
   return s;
 }
+
+// A group's place: row k of slab i, moved on by a fixed number of rows (no division per row).
+struct Cursor {
+  int i;
+  int64_t k;
+  __device__ __forceinline__ Cursor(int64_t row, int64_t rows) {
+    i = 0;
+    k = row;
+    fold(rows);
+  }
+  __device__ __forceinline__ void fold(int64_t rows) {
+    while (k >= rows && i < kMaxShards) {   // past the last slab the place is not used
+      k -= rows;
+      ++i;
+    }
+  }
+  __device__ __forceinline__ void move(int64_t step, int64_t rows) {
+    k += step;
+    fold(rows);
+  }
+};
+
+// ------------------------------------------------------------------ rows held in registers
+// Short rows, and rows that do not start on 16 bytes: a row belongs to W warps; each thread holds NV words of B
+// bytes of it (16 where every row starts on 16 bytes and holds whole words, else 4 or 2), so the row is read once and the weights stay in registers over
+// the persistent loop.  The next row's words are loaded before this one's sums.  A CTA of narrow rows has
+// several groups of W warps, each with rows of its own.
+
+template <int B> struct Word;
+template <> struct Word<16> { using type = uint4; };
+template <> struct Word<4> { using type = uint32_t; };
+template <> struct Word<2> { using type = uint16_t; };
+
+template <typename T, int B>
+__device__ __forceinline__ void unpack(const typename Word<B>::type& w, float* f) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (B == 16) {
+      f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y); f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
+    } else {
+      f[0] = __uint_as_float(w);
+    }
+  } else if constexpr (B == 16) {
+    f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x); f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);
+    f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z); f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
+  } else if constexpr (B == 4) {
+    f[0] = bf16_lo(w); f[1] = bf16_hi(w);
+  } else {
+    f[0] = __uint_as_float(static_cast<uint32_t>(w) << 16);
+  }
+}
+
+template <typename T, int B>
+__device__ __forceinline__ typename Word<B>::type pack(const float* f) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (B == 16)
+      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    else
+      return __float_as_uint(f[0]);
+  } else if constexpr (B == 16) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  } else if constexpr (B == 4) {
+    return pack_bf16x2(f[0], f[1]);
+  } else {
+    return static_cast<uint16_t>(pack_bf16x2(f[0], 0.0f) & 0xffffu);
+  }
+}
+
+constexpr int kMaxWarps = 16;    // warps per row
+
+// The W warps of a group meet (each group has its own hardware barrier; all its warps take the same rows).
+__device__ __forceinline__ void group_sync(int group, int W) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(W * 32) : "memory");
+}
+
+template <typename T, int B, int NV>
+__global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_kernel(const __grid_constant__ NormFwd P, int W, int G) {
+  using Wd = typename Word<B>::type;
+  constexpr int E = B / sizeof(T);
+  __shared__ float2 red[2][kMaxWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / W, gw = warp % W;
+  const int words = static_cast<int>(P.h / E);
+  const int v0 = gw * 32 + lane, vs = W * 32;     // this thread's words: v0 + u vs
+  float ga[NV * E], be[NV * E];
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool in = v0 + u * vs < words;
+      const int64_t c = static_cast<int64_t>(v0 + u * vs) * E + e;
+      ga[u * E + e] = in ? load_w(P.gamma, P.wtype, c) : 0.0f;
+      be[u * E + e] = in && P.beta ? load_w(P.beta, P.wtype, c) : 0.0f;
+    }
+  const float inv_h = 1.0f / static_cast<float>(P.h);
+  Wd xw[NV], rw[NV];
+  auto fetch = [&](const Cursor& at) {
+    const int i = at.i;
+    const int64_t k = at.k;
+    const Wd* x = reinterpret_cast<const Wd*>(static_cast<const T*>(P.x[i]) + k * P.ldx);
+    const Wd* r = P.r[i] ? reinterpret_cast<const Wd*>(static_cast<const T*>(P.r[i]) + k * P.ldr) : nullptr;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (v0 + u * vs < words) {
+        xw[u] = __ldcs(x + v0 + u * vs);
+        if (r) rw[u] = __ldcs(r + v0 + u * vs);
+      }
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
+  Cursor ahead(row, P.rows);
+  if (row < P.total) fetch(ahead);
+  for (int it = 0; row < P.total; row += step, it ^= 1) {
+    const int i = ahead.i;
+    const int64_t k = ahead.k;
+    ahead.move(step, P.rows);
+    const bool res = P.r[i] != nullptr;
+    float x[NV * E];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const bool in = v0 + u * vs < words;
+      if (in) {
+        unpack<T, B>(xw[u], x + u * E);
+        if (res) {
+          float r[E];
+          unpack<T, B>(rw[u], r);
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[u * E + e] += r[e];
+          const Wd w = pack<T, B>(x + u * E);      // the stream's type: what is normalised is what is kept
+          unpack<T, B>(w, x + u * E);
+          __stcs(reinterpret_cast<Wd*>(static_cast<T*>(P.s[i]) + k * P.h) + v0 + u * vs, w);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[u * E + e] = 0.0f;
+      }
+    }
+    if (row + step < P.total) fetch(ahead);
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < NV * E; ++e) sum += x[e];
+    sum = warp_sum(sum);
+    // The warp's own mean and the squares about it; the warps are joined with the exact shift
+    // sum (s - mean)^2 = sum (s - mean_w)^2 + n_w (mean_w - mean)^2, so one exchange is enough.
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int left = words - (gw * 32 + u * vs);
+      mine += left <= 0 ? 0 : (left < 32 ? left : 32);
+    }
+    const float nw = static_cast<float>(mine * E);
+    float mean = mine > 0 ? sum / nw : 0.0f;
+    float sq = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (v0 + u * vs < words) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float d = x[u * E + e] - mean;
+          sq = fmaf(d, d, sq);
+        }
+      }
+    sq = warp_sum(sq);
+    if (W > 1) {
+      // two buffers in turn: a warp can be one row ahead of another's reads, never two
+      if (lane == 0) red[it][warp] = make_float2(sum, sq);
+      group_sync(group, W);
+      float tot = 0.0f;
+      for (int w = 0; w < W; ++w) tot += red[it][group * W + w].x;
+      mean = tot / static_cast<float>(P.h);   // divided, so that a row of one value has exactly that mean
+      sq = 0.0f;
+      for (int w = 0; w < W; ++w) {
+        const float2 o = red[it][group * W + w];
+        int cnt = 0;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+          const int left = words - (w * 32 + u * vs);
+          cnt += left <= 0 ? 0 : (left < 32 ? left : 32);
+        }
+        const float n = static_cast<float>(cnt * E);
+        const float d = cnt > 0 ? o.x / n - mean : 0.0f;
+        sq += fmaf(n * d, d, o.y);
+      }
+    }
+    const float rstd = rsqrtf(fmaf(sq, inv_h, P.eps));
+    Wd* y = reinterpret_cast<Wd*>(static_cast<T*>(P.y[i]) + k * P.h);
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (v0 + u * vs < words) {
+        float o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf((x[u * E + e] - mean) * rstd, ga[u * E + e], be[u * E + e]);
+        __stcs(y + v0 + u * vs, pack<T, B>(o));
+      }
+    if (gw == 0 && lane == 0) {
+      P.mean[i][k] = mean;
+      P.rstd[i][k] = rstd;
+    }
+  }
+}
+
+// The backward pass: each thread also keeps its columns' sums of dgamma and dbeta over the CTA's rows;
+// the groups of a CTA join theirs in shared memory, the CTAs in norm_join_kernel.
+template <typename T, int B, int NV>
+__global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_kernel(const __grid_constant__ NormBwd P, int W, int G) {
+  using Wd = typename Word<B>::type;
+  constexpr int E = B / sizeof(T);
+  __shared__ float2 red[2][kMaxWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / W, gw = warp % W;
+  const int words = static_cast<int>(P.h / E);
+  const int v0 = gw * 32 + lane, vs = W * 32;
+  float ga[NV * E], dg[NV * E], db[NV * E];
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool in = v0 + u * vs < words;
+      ga[u * E + e] = in ? load_w(P.gamma, P.wtype, static_cast<int64_t>(v0 + u * vs) * E + e) : 0.0f;
+      dg[u * E + e] = db[u * E + e] = 0.0f;
+    }
+  const float inv_h = 1.0f / static_cast<float>(P.h);
+  Wd xw[NV], dw[NV];
+  float mean = 0.0f, rstd = 0.0f;
+  auto fetch = [&](const Cursor& at) {
+    const int i = at.i;
+    const int64_t k = at.k;
+    const Wd* x = reinterpret_cast<const Wd*>(static_cast<const T*>(P.x[i]) + k * P.ldx);
+    const Wd* d = reinterpret_cast<const Wd*>(static_cast<const T*>(P.dy[i]) + k * P.lddy);
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (v0 + u * vs < words) {
+        xw[u] = __ldcs(x + v0 + u * vs);
+        dw[u] = __ldcs(d + v0 + u * vs);
+      }
+    mean = __ldg(P.mean[i] + k);
+    rstd = __ldg(P.rstd[i] + k);
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
+  Cursor ahead(row, P.rows);
+  if (row < P.total) fetch(ahead);
+  for (int it = 0; row < P.total; row += step, it ^= 1) {
+    const int i = ahead.i;
+    const int64_t k = ahead.k;
+    ahead.move(step, P.rows);
+    const bool more = P.ds[i] != nullptr;
+    const Wd* ds = more ? reinterpret_cast<const Wd*>(static_cast<const T*>(P.ds[i]) + k * P.ldds) : nullptr;
+    Wd sw[NV];
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+        if (v0 + u * vs < words) sw[u] = __ldcs(ds + v0 + u * vs);
+    }
+    float xh[NV * E], g[NV * E];
+    float s1 = 0.0f, s2 = 0.0f;
+    const float rs = rstd;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      if (v0 + u * vs < words) {
+        float d[E];
+        unpack<T, B>(xw[u], xh + u * E);
+        unpack<T, B>(dw[u], d);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int c = u * E + e;
+          xh[c] = (xh[c] - mean) * rs;
+          dg[c] = fmaf(d[e], xh[c], dg[c]);
+          db[c] += d[e];
+          g[c] = d[e] * ga[c];
+          s1 += g[c];
+          s2 = fmaf(g[c], xh[c], s2);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) xh[u * E + e] = g[u * E + e] = 0.0f;
+      }
+    }
+    if (row + step < P.total) fetch(ahead);
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (W > 1) {
+      if (lane == 0) red[it][warp] = make_float2(s1, s2);
+      group_sync(group, W);
+      s1 = s2 = 0.0f;
+      for (int w = 0; w < W; ++w) {
+        const float2 o = red[it][group * W + w];
+        s1 += o.x;
+        s2 += o.y;
+      }
+    }
+    const float c1 = s1 * inv_h, c2 = s2 * inv_h;
+    Wd* dx = reinterpret_cast<Wd*>(static_cast<T*>(P.dx[i]) + k * P.h);
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (v0 + u * vs < words) {
+        float o[E], d[E];
+        if (more) unpack<T, B>(sw[u], d);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int c = u * E + e;
+          o[e] = rs * (g[c] - c1 - xh[c] * c2);
+          if (more) o[e] += d[e];
+        }
+        __stcs(dx + v0 + u * vs, pack<T, B>(o));
+      }
+  }
+  // ---- the CTA's partial sums: group 0 first, the others added in order
+  extern __shared__ float sums[];                      // [2][h], only with several groups
+  float* pg = G > 1 ? sums : P.part + static_cast<int64_t>(blockIdx.x) * 2 * P.h;
+  for (int q = 0; q < G; ++q) {
+    if (q == group) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+        if (v0 + u * vs < words) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int64_t c = static_cast<int64_t>(v0 + u * vs) * E + e;
+            pg[c] = q ? pg[c] + dg[u * E + e] : dg[u * E + e];
+            pg[P.h + c] = q ? pg[P.h + c] + db[u * E + e] : db[u * E + e];
+          }
+        }
+    }
+    if (G > 1) __syncthreads();
+  }
+  if (G > 1) {
+    float* out = P.part + static_cast<int64_t>(blockIdx.x) * 2 * P.h;
+    for (int64_t c = threadIdx.x; c < 2 * P.h; c += blockDim.x) out[c] = sums[c];
+  }
+}
+
+// ------------------------------------------------------------------ rows through shared memory
+// Rows of 2 KiB and more on 16-byte boundaries: a ring of whole rows in shared memory, filled by bulk copies
+// that run several rows ahead, so the bytes in flight do not depend on how many registers the sums take.
+// The group's first thread starts the copy of row n + stages as soon as the group has met over row n's sums:
+// by then every thread holds its words.
+
+constexpr int kMaxStages = 6;
+constexpr uint64_t kNormTimeout = 2000000000ull;
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_ring_kernel(const __grid_constant__ NormFwd P, int W, int G,
+                                                                       int stages) {
+  constexpr int E = 16 / sizeof(T);
+  extern __shared__ __align__(16) uint8_t ring[];     // [G][stages][x, r]
+  __shared__ float2 red[2][kMaxWarps];
+  __shared__ float own_mean[2][kMaxWarps];
+  __shared__ float count[kMaxWarps];
+  __shared__ uint64_t full[8][kMaxStages];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / W, gw = warp % W;
+  const int words = static_cast<int>(P.h / E);
+  const int v0 = gw * 32 + lane, vs = W * 32;
+  const bool res = P.r[0] != nullptr;
+  const uint32_t row_bytes = static_cast<uint32_t>(words) * 16;
+  const uint32_t stage_bytes = row_bytes * (res ? 2 : 1);
+  uint8_t* mine = ring + static_cast<size_t>(group) * stages * stage_bytes;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * G + group;
+  volatile int* ab = &abort_flag;
+  Cursor ahead(first, P.rows);      // the next row to be copied (used by the group's first thread)
+  auto start = [&](int st) {
+    const int i = ahead.i;
+    const int64_t k = ahead.k;
+    ahead.move(step, P.rows);
+    mbar_arrive_expect_tx(&full[group][st], stage_bytes);
+    bulk_load(mine + st * stage_bytes, static_cast<const T*>(P.x[i]) + k * P.ldx, row_bytes, &full[group][st]);
+    if (res)
+      bulk_load(mine + st * stage_bytes + row_bytes, static_cast<const T*>(P.r[i]) + k * P.ldr, row_bytes,
+                &full[group][st]);
+  };
+  if (gw == 0 && lane == 0) {
+    for (int st = 0; st < stages; ++st) mbar_init(&full[group][st], 1);
+    if (group == 0) abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  if (gw == 0 && lane == 0)
+    for (int st = 0; st < stages; ++st)
+      if (first + st * step < P.total) start(st);
+  float ga[NV * E], be[NV * E];
+  float n_mine = 0.0f;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int left = words - (gw * 32 + u * vs);
+    n_mine += static_cast<float>(left <= 0 ? 0 : (left < 32 ? left : 32) * E);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool in = v0 + u * vs < words;
+      const int64_t c = static_cast<int64_t>(v0 + u * vs) * E + e;
+      ga[u * E + e] = in ? load_w(P.gamma, P.wtype, c) : 0.0f;
+      be[u * E + e] = in && P.beta ? load_w(P.beta, P.wtype, c) : 0.0f;
+    }
+  }
+  if (lane == 0) count[warp] = n_mine;
+  __syncthreads();
+  const float hf = static_cast<float>(P.h), inv_h = 1.0f / hf;
+  int st = 0, it = 0;
+  uint32_t ph = 0;
+  Cursor at(first, P.rows);
+  for (int64_t row = first; row < P.total; row += step, it ^= 1, at.move(step, P.rows)) {
+    const int i = at.i;
+    const int64_t k = at.k;
+    // (a wait that runs out is in the status word; the group goes on, so that all its warps keep meeting)
+    mbar_wait(&full[group][st], ph, ab, P.status, kNormTimeout);
+    const uint4* sx = reinterpret_cast<const uint4*>(mine + st * stage_bytes);
+    float x[NV * E];
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      if (v0 + u * vs < words) {
+        unpack<T, 16>(sx[v0 + u * vs], x + u * E);
+        if (res) {
+          float r[E];
+          unpack<T, 16>(sx[words + v0 + u * vs], r);
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[u * E + e] += r[e];
+          const uint4 w = pack<T, 16>(x + u * E);      // the stream's type: what is normalised is what is kept
+          unpack<T, 16>(w, x + u * E);
+          __stcs(reinterpret_cast<uint4*>(static_cast<T*>(P.s[i]) + k * P.h) + v0 + u * vs, w);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum += x[u * E + e];
+      }
+    }
+    sum = warp_sum(sum);
+    // The warp's own mean and the squares about it; the warps are joined with the exact shift
+    // sum (s - mean)^2 = sum (s - mean_w)^2 + n_w (mean_w - mean)^2, so one exchange is enough.
+    float mean = n_mine > 0.0f ? sum / n_mine : 0.0f;
+    float sq = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (v0 + u * vs < words) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float d = x[u * E + e] - mean;
+          sq = fmaf(d, d, sq);
+        }
+      }
+    sq = warp_sum(sq);
+    if (W > 1) {
+      if (lane == 0) {
+        red[it][warp] = make_float2(sum, sq);
+        own_mean[it][warp] = mean;
+      }
+      group_sync(group, W);
+      // lane w takes warp w's, the lanes join by shuffles
+      const bool has = lane < W;
+      const float2 o = has ? red[it][group * W + lane] : make_float2(0.0f, 0.0f);
+      const float n = has ? count[group * W + lane] : 0.0f, mw = has ? own_mean[it][group * W + lane] : 0.0f;
+      float tot = o.x;
+#pragma unroll
+      for (int q = kMaxWarps / 2; q > 0; q >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, q);
+      mean = __shfl_sync(0xffffffffu, tot, 0) / hf;   // divided: a row of one value has exactly that mean
+      const float d = mw - mean;
+      sq = fmaf(n * d, d, o.y);
+#pragma unroll
+      for (int q = kMaxWarps / 2; q > 0; q >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, q);
+      sq = __shfl_sync(0xffffffffu, sq, 0);
+    } else {
+      __syncwarp();
+    }
+    if (gw == 0 && lane == 0 && row + stages * step < P.total) start(st);
+    if (++st == stages) {
+      st = 0;
+      ph ^= 1;
+    }
+    const float rstd = rsqrtf(fmaf(sq, inv_h, P.eps));
+    uint4* y = reinterpret_cast<uint4*>(static_cast<T*>(P.y[i]) + k * P.h);
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (v0 + u * vs < words) {
+        float o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf((x[u * E + e] - mean) * rstd, ga[u * E + e], be[u * E + e]);
+        __stcs(y + v0 + u * vs, pack<T, 16>(o));
+      }
+    if (gw == 0 && lane == 0) {
+      P.mean[i][k] = mean;
+      P.rstd[i][k] = rstd;
+    }
+  }
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_ring_kernel(const __grid_constant__ NormBwd P, int W, int G,
+                                                                       int stages) {
+  constexpr int E = 16 / sizeof(T);
+  constexpr bool KEEP = NV * E <= 16;     // xhat and g stay in registers between the sums and dx
+  extern __shared__ __align__(16) uint8_t ring[];     // [G][stages][x, dy, ds], and then [2][h] sums
+  __shared__ float2 red[2][kMaxWarps];
+  __shared__ uint64_t full[8][kMaxStages];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / W, gw = warp % W;
+  const int words = static_cast<int>(P.h / E);
+  const int v0 = gw * 32 + lane, vs = W * 32;
+  const bool more = P.ds[0] != nullptr;
+  const uint32_t row_bytes = static_cast<uint32_t>(words) * 16;
+  const uint32_t stage_bytes = row_bytes * (more ? 3 : 2);
+  uint8_t* mine = ring + static_cast<size_t>(group) * stages * stage_bytes;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * G + group;
+  volatile int* ab = &abort_flag;
+  Cursor ahead(first, P.rows);      // the next row to be copied (used by the group's first thread)
+  auto start = [&](int st) {
+    const int i = ahead.i;
+    const int64_t k = ahead.k;
+    ahead.move(step, P.rows);
+    uint8_t* dst = mine + st * stage_bytes;
+    mbar_arrive_expect_tx(&full[group][st], stage_bytes);
+    bulk_load(dst, static_cast<const T*>(P.x[i]) + k * P.ldx, row_bytes, &full[group][st]);
+    bulk_load(dst + row_bytes, static_cast<const T*>(P.dy[i]) + k * P.lddy, row_bytes, &full[group][st]);
+    if (more)
+      bulk_load(dst + 2 * row_bytes, static_cast<const T*>(P.ds[i]) + k * P.ldds, row_bytes, &full[group][st]);
+  };
+  if (gw == 0 && lane == 0) {
+    for (int st = 0; st < stages; ++st) mbar_init(&full[group][st], 1);
+    if (group == 0) abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  if (gw == 0 && lane == 0)
+    for (int st = 0; st < stages; ++st)
+      if (first + st * step < P.total) start(st);
+  float ga[NV * E], dg[NV * E], db[NV * E];
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool in = v0 + u * vs < words;
+      ga[u * E + e] = in ? load_w(P.gamma, P.wtype, static_cast<int64_t>(v0 + u * vs) * E + e) : 0.0f;
+      dg[u * E + e] = db[u * E + e] = 0.0f;
+    }
+  const float inv_h = 1.0f / static_cast<float>(P.h);
+  int st = 0, it = 0;
+  uint32_t ph = 0;
+  Cursor at(first, P.rows);
+  float next_mean = 0.0f, next_rstd = 0.0f;   // of the coming row: loaded a row early
+  if (first < P.total) {
+    next_mean = __ldg(P.mean[at.i] + at.k);
+    next_rstd = __ldg(P.rstd[at.i] + at.k);
+  }
+  for (int64_t row = first; row < P.total; row += step, it ^= 1) {
+    const int i = at.i;
+    const int64_t k = at.k;
+    const float mean = next_mean, rs = next_rstd;
+    at.move(step, P.rows);
+    if (row + step < P.total) {
+      next_mean = __ldg(P.mean[at.i] + at.k);
+      next_rstd = __ldg(P.rstd[at.i] + at.k);
+    }
+    mbar_wait(&full[group][st], ph, ab, P.status, kNormTimeout);
+    const uint4* sx = reinterpret_cast<const uint4*>(mine + st * stage_bytes);
+    float xh[KEEP ? NV * E : 1], g[KEEP ? NV * E : 1];
+    uint4 sw[KEEP ? NV : 1];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (v0 + u * vs < words) {
+        float x[E], d[E];
+        unpack<T, 16>(sx[v0 + u * vs], x);
+        unpack<T, 16>(sx[words + v0 + u * vs], d);
+        if (KEEP && more) sw[KEEP ? u : 0] = sx[2 * words + v0 + u * vs];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int c = u * E + e;
+          const float n = (x[e] - mean) * rs, q = d[e] * ga[c];
+          dg[c] = fmaf(d[e], n, dg[c]);
+          db[c] += d[e];
+          s1 += q;
+          s2 = fmaf(q, n, s2);
+          if (KEEP) {
+            xh[KEEP ? c : 0] = n;
+            g[KEEP ? c : 0] = q;
+          }
+        }
+      }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (W > 1) {
+      if (lane == 0) red[it][warp] = make_float2(s1, s2);
+      group_sync(group, W);
+      s1 = s2 = 0.0f;
+#pragma unroll 4
+      for (int w = 0; w < W; ++w) {
+        const float2 o = red[it][group * W + w];
+        s1 += o.x;
+        s2 += o.y;
+      }
+    } else {
+      __syncwarp();
+    }
+    const bool next = row + stages * step < P.total;
+    if (KEEP && gw == 0 && lane == 0 && next) start(st);
+    const float c1 = s1 * inv_h, c2 = s2 * inv_h;
+    uint4* dx = reinterpret_cast<uint4*>(static_cast<T*>(P.dx[i]) + k * P.h);
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (v0 + u * vs < words) {
+        float o[E], n[E], q[E];
+        if (!KEEP) {
+          unpack<T, 16>(sx[v0 + u * vs], n);
+          unpack<T, 16>(sx[words + v0 + u * vs], q);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float nn = KEEP ? xh[KEEP ? u * E + e : 0] : (n[e] - mean) * rs;
+          const float qq = KEEP ? g[KEEP ? u * E + e : 0] : q[e] * ga[u * E + e];
+          o[e] = rs * (qq - c1 - nn * c2);
+        }
+        if (more) {
+          float d[E];
+          unpack<T, 16>(KEEP ? sw[KEEP ? u : 0] : sx[2 * words + v0 + u * vs], d);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += d[e];
+        }
+        __stcs(dx + v0 + u * vs, pack<T, 16>(o));
+      }
+    if (!KEEP) {   // the row was read twice: the group meets again before its buffer is filled
+      if (W > 1) group_sync(group, W); else __syncwarp();
+      if (gw == 0 && lane == 0 && next) start(st);
+    }
+    if (++st == stages) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+  // ---- the CTA's partial sums: group 0 first, the others added in order
+  float* sums = reinterpret_cast<float*>(ring + static_cast<size_t>(G) * stages * stage_bytes);
+  float* pg = G > 1 ? sums : P.part + static_cast<int64_t>(blockIdx.x) * 2 * P.h;
+  for (int q = 0; q < G; ++q) {
+    if (q == group) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+        if (v0 + u * vs < words) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int64_t c = static_cast<int64_t>(v0 + u * vs) * E + e;
+            pg[c] = q ? pg[c] + dg[u * E + e] : dg[u * E + e];
+            pg[P.h + c] = q ? pg[P.h + c] + db[u * E + e] : db[u * E + e];
+          }
+        }
+    }
+    if (G > 1) __syncthreads();
+  }
+  if (G > 1) {
+    float* out = P.part + static_cast<int64_t>(blockIdx.x) * 2 * P.h;
+    for (int64_t c = threadIdx.x; c < 2 * P.h; c += blockDim.x) out[c] = sums[c];
+  }
+}
+
+// ------------------------------------------------------------------ rows of any width
 
 // One row per CTA at a time, any width, stride and alignment; the row is read again for each step
 // (from L1 / L2).
@@ -166,6 +830,7 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const float* part, int n
   if (!out) return;
   float s = 0.0f;
   if (c < h)
+#pragma unroll 8
     for (int p = w; p < nparts; p += 8) s += part[(static_cast<int64_t>(p) * 2 + blockIdx.y) * h + c];
   red[w][lane] = s;
   __syncthreads();
@@ -209,6 +874,143 @@ bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t row
   return p < q + ((rows - 1) * ldb + h) * bytes && q < p + ((rows - 1) * lda + h) * bytes;
 }
 
+// How a row of h elements is spread: B bytes per word, NV words per thread, W warps per row, G rows at a
+// time per CTA; stages > 0: through the ring, with that many rows of a group in shared memory (smem bytes
+// in all).  W = 0: wider than all of these, the kernel that reads its row again takes it.
+struct Spread {
+  int B, NV, W, G, stages;
+  size_t smem;
+};
+
+// `inputs` rows (x, r, or x, dy, ds) come in for each row.
+Spread spread_of(int64_t h, int elem, int B, bool bwd, int inputs) {
+  Spread s = {B, 0, 0, 1, 0, 0};
+  const int64_t words = h * elem / B;
+  auto fit = [&](int nv, int warps) {
+    if (s.W || words > static_cast<int64_t>(nv) * 32 * warps) return;
+    s.NV = nv;
+    s.W = static_cast<int>((words + nv * 32 - 1) / (nv * 32));
+  };
+  if (B == 16 && h * elem >= 2048) {
+    // two words a thread (16 bf16 values), then up to four: the fewer values, the more rows in flight
+    fit(2, 8);
+    fit(2, kMaxWarps);
+    fit(3, kMaxWarps);
+    fit(4, kMaxWarps);
+    if (!s.W) return s;
+    if (s.W < 8) s.G = 8 / s.W;
+    const size_t stage = static_cast<size_t>(h) * elem * inputs * s.G;
+    const size_t sums = bwd && s.G > 1 ? static_cast<size_t>(h) * 8 : 0;
+    const size_t room = 112000 - 1024;                       // two CTAs on an SM
+    size_t n = (room - sums) / stage;
+    n = n < 2 ? 2 : (n > kMaxStages ? kMaxStages : n);
+    if (n * stage + sums > 220000) {                          // two rows do not fit
+      s.W = 0;
+      return s;
+    }
+    s.stages = static_cast<int>(n);
+    s.smem = n * stage + sums;
+    return s;
+  }
+  if (B == 16) {
+    fit(1, 1);
+    fit(2, 1);
+    fit(4, 1);
+  } else {
+    const int hi = bwd && B == 4 && elem == 2 ? 8 : 16;
+    const int caps[3] = {1, 8, kMaxWarps};
+    for (int c : caps)
+      for (int nv = 8; nv <= hi; nv *= 2) fit(nv, c);
+  }
+  if (s.W > 0 && s.W < 8) s.G = 8 / s.W;
+  if (bwd && s.G > 1) s.smem = static_cast<size_t>(h) * 8;
+  return s;
+}
+
+template <auto Kernel>
+int allow_smem(size_t bytes) {
+  static std::mutex mu;
+  static size_t done[64] = {};
+  int dev = 0;
+  int rc = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc || bytes <= 40 * 1024) return rc;   // (the limit of 48 KiB counts the static arrays too)
+  if (dev < 0 || dev >= 64) return set_error(TTL_ERR_CUDA, "device index %d out of range", dev);
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev] >= bytes) return TTL_OK;
+  rc = cuda_check(cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)),
+                  "cudaFuncSetAttribute(layer norm)");
+  if (!rc) done[dev] = bytes;
+  return rc;
+}
+
+template <typename T, int B, int NV>
+int launch_fwd(const NormFwd& P, const Spread& sp, cudaStream_t s) {
+  const int threads = sp.W * sp.G * 32;
+  const int64_t ctas = (P.total + sp.G - 1) / sp.G;
+  const int64_t cap = static_cast<int64_t>(num_sms()) * 2;
+  const unsigned grid = static_cast<unsigned>(ctas < cap ? ctas : cap);
+  if constexpr (B == 16) {
+    if (sp.stages > 0) {
+      if (int rc = allow_smem<norm_fwd_ring_kernel<T, NV>>(sp.smem)) return rc;
+      norm_fwd_ring_kernel<T, NV><<<grid, threads, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
+      return TTL_OK;
+    }
+  }
+  if constexpr (B != 16 || NV != 3) norm_fwd_kernel<T, B, NV><<<grid, threads, 0, s>>>(P, sp.W, sp.G);
+  return TTL_OK;
+}
+
+template <typename T, int B, int NV>
+int launch_bwd(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
+  const int threads = sp.W * sp.G * 32;
+  if constexpr (B == 16) {
+    if (sp.stages > 0) {
+      if (int rc = allow_smem<norm_bwd_ring_kernel<T, NV>>(sp.smem)) return rc;
+      norm_bwd_ring_kernel<T, NV><<<parts, threads, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
+      return TTL_OK;
+    }
+  }
+  if constexpr (B != 16 || NV != 3) norm_bwd_kernel<T, B, NV><<<parts, threads, sp.smem, s>>>(P, sp.W, sp.G);
+  return TTL_OK;
+}
+
+template <typename T, int B>
+int pick_fwd(const NormFwd& P, const Spread& sp, cudaStream_t s) {
+  if constexpr (B == 16) {
+    switch (sp.NV) {
+      case 1: return launch_fwd<T, B, 1>(P, sp, s);
+      case 2: return launch_fwd<T, B, 2>(P, sp, s);
+      case 3: return launch_fwd<T, B, 3>(P, sp, s);
+      default: return launch_fwd<T, B, 4>(P, sp, s);
+    }
+  } else {
+    return sp.NV == 8 ? launch_fwd<T, B, 8>(P, sp, s) : launch_fwd<T, B, 16>(P, sp, s);
+  }
+}
+
+template <typename T, int B>
+int pick_bwd(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
+  if constexpr (B == 16) {
+    switch (sp.NV) {
+      case 1: return launch_bwd<T, B, 1>(P, sp, parts, s);
+      case 2: return launch_bwd<T, B, 2>(P, sp, parts, s);
+      case 3: return launch_bwd<T, B, 3>(P, sp, parts, s);
+      default: return launch_bwd<T, B, 4>(P, sp, parts, s);
+    }
+  } else if constexpr (sizeof(T) == B) {
+    return sp.NV == 8 ? launch_bwd<T, B, 8>(P, sp, parts, s) : launch_bwd<T, B, 16>(P, sp, parts, s);
+  } else {
+    return launch_bwd<T, B, 8>(P, sp, parts, s);
+  }
+}
+
+// The widest word that every row is made of: 16 bytes, or 4, or the element.
+int word_of(uintptr_t ptrs, int64_t strides, int64_t h, int elem) {
+  const uintptr_t all = ptrs | static_cast<uintptr_t>(strides * elem) | static_cast<uintptr_t>(h * elem);
+  return all % 16 == 0 ? 16 : (all % 4 == 0 ? 4 : elem);
+}
+
 int parts_of(int64_t total) { return static_cast<int>(total < kNormParts ? total : kNormParts); }
 
 }  // namespace
@@ -244,6 +1046,8 @@ extern "C" int ttl_layer_norm_fwd(int t, int64_t rows, int64_t h, int x_type, in
         return set_error(TTL_ERR_ARG, "%s: an output aliases an input or another output", name);
   if ((rc = require_sm103())) return rc;
   NormFwd P = {};
+  P.status = device_status_ptr();
+  if (!P.status) return TTL_ERR_CUDA;
   for (int i = 0; i < t; ++i) {
     P.x[i] = X[i];
     P.r[i] = R ? R[i] : nullptr;
@@ -264,12 +1068,25 @@ extern "C" int ttl_layer_norm_fwd(int t, int64_t rows, int64_t h, int x_type, in
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const double n = static_cast<double>(P.total) * h;
   TraceScope trace(s, TTL_K_NORM, 0.0, n * xb * (R ? 4.0 : 2.0));
-  const int64_t cap = static_cast<int64_t>(num_sms()) * 8;
-  const unsigned grid = static_cast<unsigned>(P.total < cap ? P.total : cap);
-  if (x_type == TTL_T_F32)
-    norm_fwd_any_kernel<float><<<grid, kNormThreads, 0, s>>>(P);
-  else
-    norm_fwd_any_kernel<__nv_bfloat16><<<grid, kNormThreads, 0, s>>>(P);
+  uintptr_t ptrs = 0;
+  for (int i = 0; i < t; ++i)
+    ptrs |= reinterpret_cast<uintptr_t>(X[i]) | reinterpret_cast<uintptr_t>(Y[i]) |
+            (R ? reinterpret_cast<uintptr_t>(R[i]) | reinterpret_cast<uintptr_t>(S[i]) : 0);
+  const Spread sp = spread_of(h, xb, word_of(ptrs, ldx | (R ? ldr : 0), h, xb), false, R ? 2 : 1);
+  if (sp.W == 0) {
+    const int64_t cap = static_cast<int64_t>(num_sms()) * 8;
+    const unsigned grid = static_cast<unsigned>(P.total < cap ? P.total : cap);
+    if (x_type == TTL_T_F32) norm_fwd_any_kernel<float><<<grid, kNormThreads, 0, s>>>(P);
+    else norm_fwd_any_kernel<__nv_bfloat16><<<grid, kNormThreads, 0, s>>>(P);
+  } else if (x_type == TTL_T_F32) {
+    if (sp.B == 16) rc = pick_fwd<float, 16>(P, sp, s);
+    else rc = pick_fwd<float, 4>(P, sp, s);
+  } else {
+    if (sp.B == 16) rc = pick_fwd<__nv_bfloat16, 16>(P, sp, s);
+    else if (sp.B == 4) rc = pick_fwd<__nv_bfloat16, 4>(P, sp, s);
+    else rc = pick_fwd<__nv_bfloat16, 2>(P, sp, s);
+  }
+  if (rc) return rc;
   return cuda_check(cudaGetLastError(), "layer norm forward launch");
 }
 
@@ -316,6 +1133,8 @@ extern "C" int ttl_layer_norm_bwd(int t, int64_t rows, int64_t h, int x_type, in
   int parts = 0;
   if (rows > 0) {
     NormBwd P = {};
+    P.status = device_status_ptr();
+    if (!P.status) return TTL_ERR_CUDA;
     for (int i = 0; i < t; ++i) {
       P.x[i] = X[i];
       P.dy[i] = dY[i];
@@ -336,11 +1155,24 @@ extern "C" int ttl_layer_norm_bwd(int t, int64_t rows, int64_t h, int x_type, in
     parts = parts_of(P.total);
     const double n = static_cast<double>(P.total) * h;
     TraceScope trace(s, TTL_K_NORM, 0.0, n * xb * (dS ? 4.0 : 3.0));
-    if (x_type == TTL_T_F32)
-      norm_bwd_any_kernel<float><<<parts, kNormThreads, 0, s>>>(P);
-    else
-      norm_bwd_any_kernel<__nv_bfloat16><<<parts, kNormThreads, 0, s>>>(P);
-    if ((rc = cuda_check(cudaGetLastError(), "layer norm backward launch"))) return rc;
+    uintptr_t ptrs = 0;
+    for (int i = 0; i < t; ++i)
+      ptrs |= reinterpret_cast<uintptr_t>(X[i]) | reinterpret_cast<uintptr_t>(dY[i]) |
+              reinterpret_cast<uintptr_t>(dX[i]) | (dS ? reinterpret_cast<uintptr_t>(dS[i]) : 0);
+    const Spread sp = spread_of(h, xb, word_of(ptrs, ldx | lddy | (dS ? ldds : 0), h, xb), true, dS ? 3 : 2);
+    if (sp.W > 0) parts = static_cast<int>((P.total + sp.G - 1) / sp.G < parts ? (P.total + sp.G - 1) / sp.G : parts);
+    if (sp.W == 0) {
+      if (x_type == TTL_T_F32) norm_bwd_any_kernel<float><<<parts, kNormThreads, 0, s>>>(P);
+      else norm_bwd_any_kernel<__nv_bfloat16><<<parts, kNormThreads, 0, s>>>(P);
+    } else if (x_type == TTL_T_F32) {
+      if (sp.B == 16) rc = pick_bwd<float, 16>(P, sp, parts, s);
+      else rc = pick_bwd<float, 4>(P, sp, parts, s);
+    } else {
+      if (sp.B == 16) rc = pick_bwd<__nv_bfloat16, 16>(P, sp, parts, s);
+      else if (sp.B == 4) rc = pick_bwd<__nv_bfloat16, 4>(P, sp, parts, s);
+      else rc = pick_bwd<__nv_bfloat16, 2>(P, sp, parts, s);
+    }
+    if (rc || (rc = cuda_check(cudaGetLastError(), "layer norm backward launch"))) return rc;
   }
   TraceScope trace(s, TTL_K_NORM, 0.0, 8.0 * h * parts);
   norm_join_kernel<<<dim3(static_cast<unsigned>((h + 31) / 32), 2), 256, 0, s>>>(static_cast<const float*>(ws), parts,
