@@ -892,7 +892,11 @@ Spread spread_of(int64_t h, int elem, int B, bool bwd, int inputs) {
     s.W = static_cast<int>((words + nv * 32 - 1) / (nv * 32));
   };
   if (B == 16 && h * elem >= 2048) {
-    // two words a thread (16 bf16 values), then up to four: the fewer values, the more rows in flight
+    // 16 values a thread: fewer leave too little work between the row's exchanges, more hold the registers
+    // that other rows need (8192 x 4096: fp32 forward 45 us with four words, 53 with two; fp32 backward, which
+    // keeps two sums per value as well, 80 us with two words, 94 with four; bf16 forward 52 and 56, backward
+    // 72 and 103 us with two and four)
+    if (elem == 4 && !bwd) fit(4, 8);
     fit(2, 8);
     fit(2, kMaxWarps);
     fit(3, kMaxWarps);

@@ -91,6 +91,17 @@ __device__ __forceinline__ void check_docs(const int32_t* cu, int batch, int64_t
   if (bad) atomicCAS(status, 0, TTL_ERR_DEVICE);
 }
 
+// The warp's index as a value the compiler knows to be the same in all lanes: descriptors computed from it and
+// from loop counters stay in uniform registers, which is where the MMA instruction takes them from.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ------------------------------------------------------------------ one row by one warp
 // Lane l holds columns [l D/32, (l + 1) D/32) of the head.  Every key or query of the range is read, and
 // nothing outside it, so what masked places hold (infinities, NaN) never enters.

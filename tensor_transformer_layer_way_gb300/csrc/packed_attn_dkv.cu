@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   constexpr uint32_t T_DP = 128, T_DK = 256, T_DV = 384;
 
   const PackArgs& A = P.a;
-  const int warp = threadIdx.x >> 5;
+  const int warp = uniform_warp();
   const int lane = threadIdx.x & 31;
   const int total = P.tiles * P.lanes;
   int* status = A.status;
@@ -218,21 +218,23 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
-    bool ok = true;
-    int ni = 0, pos = 0;
+    // The whole warp runs this loop, one elected lane issues.  A wait that runs out is in the status word and raises
+    // the abort flag, after which every wait returns at once: the loop then ends over what is in memory.
+    int ni = 0, p = 0;                     // items; steps scored
     const uint64_t kd = smem_desc_sw128(smem_u32(sK), 16, 1024);
     const uint64_t vd = smem_desc_sw128(smem_u32(sV), 16, 1024);
-    const uint32_t qa = smem_u32(sQ), doa = smem_u32(sDO);
+    const uint64_t qk0 = smem_desc_sw128(smem_u32(sQ), 16, 1024), qn0 = smem_desc_sw128(smem_u32(sQ), 16384, 1024);
+    const uint64_t dk0 = smem_desc_sw128(smem_u32(sDO), 16, 1024), dn0 = smem_desc_sw128(smem_u32(sDO), 16384, 1024);
     const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
     const uint32_t idesc_acc = idesc_bf16_f32(kTile, D, false, true);
-    auto wait = [&](uint64_t* bar, uint32_t phase) {
-      if (!mbar_wait(bar, phase & 1u, abort_flag, status, tmo)) return false;
-      tc_fence_after_sync();
-      return true;
+    static_assert(kSlots == 2, "the Q and dO places are the parity of the step");
+    const bool leader = elect_one();
+    auto wait = [&](uint64_t* bar, int phase) {
+      mbar_wait(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
     };
     // [keys x queries] = A B^T, both K-major tiles of D columns
-    auto scores = [&](uint32_t dst, uint64_t ad, uint32_t baddr) {
-      const uint64_t bd = smem_desc_sw128(baddr, 16, 1024);
+    auto scores = [&](uint32_t dst, uint64_t ad, uint64_t bd) {
+#pragma unroll
       for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
@@ -240,55 +242,63 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
                     (kb | kk) ? 1u : 0u);
     };
     // [keys x D] += A B: A from tensor memory (queries [64 w, 64 w + 64) at columns 64 w ..), B read MN-major
-    auto sum = [&](uint32_t dst, uint32_t acol, uint32_t baddr, bool first) {
-      const uint64_t bd = smem_desc_sw128(baddr, 16384, 1024);
+    auto sum = [&](uint32_t dst, uint32_t acol, uint64_t bd, uint32_t more) {
 #pragma unroll
       for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_bf16_ts(dst, acol + (kk >> 2) * 64 + (kk & 3) * 8, desc_advance(bd, kk * 2048), idesc_acc,
-                     (!first || kk) ? 1u : 0u);
+        umma_bf16_ts(dst, acol + (kk >> 2) * 64 + (kk & 3) * 8, desc_advance(bd, kk * 2048), idesc_acc, kk ? 1u : more);
     };
     for (int n = 0; item_at(n) < total; ++n) {
       const KvItem it = kv_item(P, item_at(n));
       if (it.steps == 0) continue;
-      if (lane == 0 && ok) {
-        ok = wait(k_full, ni);
-        // S^T of step t overwrites P^T of the step before, whose dV product was issued before it (the tensor
-        // pipe runs one thread's products in order); likewise dP^T and dK.
-        for (int t = -1; ok && t < it.steps; ++t) {
-          const int p = pos + t, p1 = p + 1;
-          if (t + 1 < it.steps) {
-            if (!(ok = wait(&q_full[p1 % kSlots], p1 / kSlots))) break;
-            scores(tmem, kd, qa + (p1 % kSlots) * C::TILE);
+      wait(k_full, ni);
+      // S^T of step t overwrites P^T of the step before, whose dV product was issued before it (the tensor
+      // pipe runs one thread's products in order); likewise dP^T and dK.
+      for (int t = -1; t < it.steps; ++t) {
+        const int s = p & 1, o = s ^ 1;    // places of step t + 1 and of step t
+        if (t + 1 < it.steps) {
+          wait(&q_full[s], p >> 1);
+          tc_fence_after_sync();
+          if (leader) {
+            scores(tmem, kd, desc_advance(qk0, s * C::TILE));
             umma_commit(s_full);
             if (t + 2 == it.steps) umma_commit(k_empty);
           }
-          if (t >= 0) {
-            if (!(ok = wait(ds_full, p))) break;
-            sum(tmem + T_DK, tmem + T_DP, qa + (p % kSlots) * C::TILE, t == 0);
-            umma_commit(&q_empty[p % kSlots]);
-          }
-          if (t + 1 < it.steps) {
-            if (t < 0 && !(ok = wait(v_full, ni))) break;
-            if (!(ok = wait(&do_full[p1 % kSlots], p1 / kSlots))) break;
-            scores(tmem + T_DP, vd, doa + (p1 % kSlots) * C::TILE);
-            umma_commit(dp_full);
-            if (t + 2 == it.steps) umma_commit(v_empty);
-            if (!(ok = wait(p_full, p1))) break;
-            sum(tmem + T_DV, tmem, doa + (p1 % kSlots) * C::TILE, t < 0);
-            umma_commit(&do_empty[p1 % kSlots]);
+        }
+        if (t >= 0) {
+          wait(ds_full, p - 1);
+          tc_fence_after_sync();
+          if (leader) {
+            sum(tmem + T_DK, tmem + T_DP, desc_advance(qn0, o * C::TILE), t > 0 ? 1u : 0u);
+            umma_commit(&q_empty[o]);
           }
         }
-        if (ok) umma_commit(acc_full);
-        ++ni;
-        pos += it.steps;
+        if (t + 1 < it.steps) {
+          if (t < 0) wait(v_full, ni);
+          wait(&do_full[s], p >> 1);
+          tc_fence_after_sync();
+          if (leader) {
+            scores(tmem + T_DP, vd, desc_advance(dk0, s * C::TILE));
+            umma_commit(dp_full);
+            if (t + 2 == it.steps) umma_commit(v_empty);
+          }
+          wait(p_full, p);
+          tc_fence_after_sync();
+          if (leader) {
+            sum(tmem + T_DV, tmem, desc_advance(dn0, s * C::TILE), t >= 0 ? 1u : 0u);
+            umma_commit(&do_empty[s]);
+          }
+          ++p;
+        }
+        __syncwarp();
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      if (leader) umma_commit(acc_full);
+      __syncwarp();
+      ++ni;
     }
-    if (lane == 0) {
-      umma_commit(done_bar);   // every MMA issued here must finish before TMEM is released
-      int dummy = 0;
-      mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
-    }
+    if (leader) umma_commit(done_bar);   // every MMA issued here must finish before TMEM is released
+    __syncwarp();
+    int dummy = 0;
+    mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ lse and D of each step's queries

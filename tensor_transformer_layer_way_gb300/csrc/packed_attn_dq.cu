@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
   constexpr uint32_t T_DP = 128, T_DQ = 256, T_DS = 384;
 
   const PackArgs& A = P.a;
-  const int warp = threadIdx.x >> 5;
+  const int warp = uniform_warp();
   const int lane = threadIdx.x & 31;
   const int total = P.tiles * P.lanes;
   int* status = A.status;
@@ -212,41 +212,52 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
-    bool ok = true;
-    int pos = 0, nq = 0;
-    const uint32_t k0a = smem_u32(sK), v0a = smem_u32(sV);
+    // The whole warp runs this loop, one elected lane issues.  A wait that runs out is in the status word and raises
+    // the abort flag, after which every wait returns at once: the loop then ends over what is in memory.
+    int p = 0, nq = 0;                     // key tiles scored, items
+    int ks = 0, klap = 0, old = 0;         // K place of the tile about to be scored; of the one before
     const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 16, 1024);
     const uint64_t dod = smem_desc_sw128(smem_u32(sDO), 16, 1024);
+    const uint64_t kd0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t kn0 = smem_desc_sw128(smem_u32(sK), 16384, 1024);
+    const uint64_t vd0 = smem_desc_sw128(smem_u32(sV), 16, 1024);
     const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
     const uint32_t idesc_dq = idesc_bf16_f32(kTile, D, false, true);
+    static_assert(kVSlots == 2, "the V place is the parity of the key tile");
+    const bool leader = elect_one();
+    auto wait = [&](uint64_t* bar, int phase) {
+      mbar_wait(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
+    };
     for (int n = 0; item_at(n) < total; ++n) {
       const DqItem it = dq_item(P, item_at(n));
       const int nt = it.jend - it.jbeg;
       if (nt <= 0) continue;
-      if (lane == 0 && ok) {
-        ok = mbar_wait(q_full, static_cast<uint32_t>(nq) & 1u, abort_flag, status, tmo);
-        tc_fence_after_sync();
-        ++nq;
-        for (int j = -1; ok && j < nt; ++j) {
-          if (j + 1 < nt) {
-            const int p = pos + j + 1;
-            const int ks = p % kKSlots, vs = p % kVSlots;
-            ok = mbar_wait(&k_full[ks], static_cast<uint32_t>(p / kKSlots) & 1u, abort_flag, status, tmo) &&
-                 mbar_wait(s_empty, (static_cast<uint32_t>(p) & 1u) ^ 1u, abort_flag, status, tmo);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t kd = smem_desc_sw128(k0a + ks * C::TILE, 16, 1024);
+      wait(q_full, nq);
+      tc_fence_after_sync();
+      ++nq;
+      for (int j = -1; j < nt; ++j) {
+        const int ds = p - 1;              // the key tile of dS_j: the last one scored before this step
+        if (j + 1 < nt) {
+          const int vs = p & 1;
+          wait(&k_full[ks], klap);
+          wait(s_empty, p + 1);
+          tc_fence_after_sync();
+          const uint64_t kd = desc_advance(kd0, ks * C::TILE);
+          if (leader) {
+#pragma unroll
             for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 umma_bf16(tmem, desc_advance(qd, kb * 16384 + kk * 32), desc_advance(kd, kb * 16384 + kk * 32), idesc_s,
                           (kb | kk) ? 1u : 0u);
             umma_commit(s_full);
-            ok = mbar_wait(&v_full[vs], static_cast<uint32_t>(p / kVSlots) & 1u, abort_flag, status, tmo) &&
-                 mbar_wait(dp_empty, (static_cast<uint32_t>(p) & 1u) ^ 1u, abort_flag, status, tmo);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t vd = smem_desc_sw128(v0a + vs * C::TILE, 16, 1024);
+          }
+          wait(&v_full[vs], p >> 1);
+          wait(dp_empty, p + 1);
+          tc_fence_after_sync();
+          const uint64_t vd = desc_advance(vd0, vs * C::TILE);
+          if (leader) {
+#pragma unroll
             for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -256,33 +267,40 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
             umma_commit(&v_empty[vs]);
             if (j + 2 == nt) umma_commit(q_empty);   // the item's last read of Q and dO
           }
-          if (j >= 0) {
-            const int p = pos + j, ks = p % kKSlots, b = p & 1;
-            ok = mbar_wait(&ds_full[b], static_cast<uint32_t>(p >> 1) & 1u, abort_flag, status, tmo);
-            // the previous item's dQ has been read before this one's first product overwrites it
-            if (ok && j == 0)
-              ok = mbar_wait(dq_empty, (static_cast<uint32_t>(nq - 1) & 1u) ^ 1u, abort_flag, status, tmo);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t kd = smem_desc_sw128(k0a + ks * C::TILE, 16384, 1024);
+        }
+        if (j >= 0) {
+          const int b = ds & 1;
+          wait(&ds_full[b], ds >> 1);
+          // the previous item's dQ has been read before this one's first product overwrites it
+          if (j == 0) wait(dq_empty, nq);
+          tc_fence_after_sync();
+          const uint64_t kd = desc_advance(kn0, old * C::TILE);
+          const uint32_t more = j > 0 ? 1u : 0u;
+          if (leader) {
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
               umma_bf16_ts(tmem + T_DQ, tmem + T_DS + b * 64 + kk * 8, desc_advance(kd, kk * 2048), idesc_dq,
-                           (j | kk) ? 1u : 0u);
+                           kk ? 1u : more);
             umma_commit(&ds_empty[b]);
-            umma_commit(&k_empty[ks]);
+            umma_commit(&k_empty[old]);
             if (j + 1 == nt) umma_commit(dq_full);
           }
         }
-        pos += nt;
+        __syncwarp();
+        if (j + 1 < nt) {
+          ++p;
+          old = ks;
+          if (++ks == kKSlots) {
+            ks = 0;
+            ++klap;
+          }
+        }
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
     }
-    if (lane == 0) {
-      umma_commit(done_bar);   // every MMA issued here must finish before TMEM is released
-      int dummy = 0;
-      mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
-    }
+    if (leader) umma_commit(done_bar);   // every MMA issued here must finish before TMEM is released
+    __syncwarp();
+    int dummy = 0;
+    mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ dS
