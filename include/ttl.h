@@ -454,7 +454,7 @@ int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t h, int64_t
  *   Q[i] [T, n_q/t d], K[i], V[i] [T, n_kv/t d], head-major columns, row strides ldq, ldk, ldv
  *              (multiples of 8; e.g. column ranges of one fused projection)
  *   O[i] [T, n_q/t d] out, row stride ldo;  lse[i] [n_q/t, T] fp32 out: log sum exp(scale q.k)
- *   ws   workspace of ttl_packed_attn_fwd_workspace_size() bytes (may be null where that is 0)
+ *   ws   workspace of ttl_packed_attn_fwd_workspace_size() bytes
  * t | n_q, t | n_kv, n_kv | n_q, d = 64 or 128, any T; scale > 0.  Memory use is linear in T. */
 size_t ttl_packed_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch);
 int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,

@@ -59,6 +59,34 @@ int check_cu(const int32_t* cu, float scale, const char* name) {
   return TTL_OK;
 }
 
+int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
+
+// Backward workspace: D, the query tiles by work, the key items by work with their counts, the key tiles that
+// several items share, and those items' partial sums.
+struct BwdWs {
+  size_t q_list, kv_list, head, join, part, total;   // offsets after D
+};
+BwdWs bwd_ws(int64_t T, int n_q, int n_kv, int d) {
+  const int64_t tiles = tiles_of(T);
+  const int grp = n_q / n_kv;
+  // A cut leaves at most 2 steps / most parts of a tile and most >= all steps / kSplitItems: at most
+  // 2 kSplitItems parts in all; and no part is shorter than kSplitSteps / 2.
+  int64_t slots = 0;
+  if (pack_split(tiles, n_kv, grp)) {
+    slots = 2 * kSplitItems / n_kv + 1;
+    const int64_t most = tiles * (tiles * grp / kSplitSteps + 1);
+    if (slots > most) slots = most;
+  }
+  BwdWs w;
+  w.q_list = round256(static_cast<size_t>(n_q) * T * 4);
+  w.kv_list = w.q_list + round256(static_cast<size_t>(tiles) * 16);
+  w.head = w.kv_list + round256(static_cast<size_t>(tiles + slots) * 32);
+  w.join = w.head + 256;
+  w.part = w.join + round256(static_cast<size_t>(tiles) * 16);
+  w.total = w.part + static_cast<size_t>(slots) * n_kv * 2 * kTile * d * 4 + 256;   // (it starts on 256 bytes)
+  return w;
+}
+
 const __nv_bfloat16* bf(const ttl_bf16* p) { return reinterpret_cast<const __nv_bfloat16*>(p); }
 __nv_bfloat16* bf(ttl_bf16* p) { return reinterpret_cast<__nv_bfloat16*>(p); }
 
@@ -69,12 +97,12 @@ using namespace ttl;
 
 extern "C" size_t ttl_packed_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
   if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_fwd_workspace_size")) return 0;
-  return 0;   // scores and row statistics stay on chip
+  return round256(static_cast<size_t>(tiles_of(T)) * 16);   // the query tiles by work
 }
 
 extern "C" size_t ttl_packed_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
   if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_bwd_workspace_size")) return 0;
-  return round256(static_cast<size_t>(n_q) * T * 4);   // D
+  return bwd_ws(T, n_q, n_kv, d).total;
 }
 
 extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
@@ -93,8 +121,10 @@ extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, i
       (rc = check_mats(reinterpret_cast<CP>(V), t, kc, ldv, "V", name)) ||
       (rc = check_mats(reinterpret_cast<CP>(O), t, qc, ldo, "O", name)) || (rc = check_lse(lse, t, name)))
     return rc;
-  (void)ws;
-  (void)ws_bytes;
+  const size_t need = ttl_packed_attn_fwd_workspace_size(t, T, n_q, n_kv, d, batch);
+  if (!ws || ws_bytes < need)
+    return set_error(TTL_ERR_ARG, "%s: workspace of %zu bytes needed, %zu given", name, need, ws_bytes);
+  if (!aligned16(ws)) return set_error(TTL_ERR_ALIGN, "%s: workspace not 16-byte aligned", name);
   if ((rc = require_sm103())) return rc;
   PackArgs A = {};
   A.status = device_status_ptr();
@@ -110,7 +140,7 @@ extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, i
   A.ldq = ldq; A.ldk = ldk; A.ldv = ldv; A.ldo = ldo;
   A.cu = cu_seqlens; A.batch = batch; A.scale = scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return pack_attn_fwd_launch(A, d, s);
+  return pack_attn_fwd_launch(A, d, ws, s);
 }
 
 extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
@@ -158,8 +188,32 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
   A.ldq = ldq; A.ldk = ldk; A.ldv = ldv; A.ldo = ldo;
   A.lddo = lddo; A.lddq = lddq; A.lddk = lddk; A.lddv = lddv;
   A.cu = cu_seqlens; A.batch = batch; A.scale = scale;
-  A.D = static_cast<float*>(ws);
+  A.D = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = pack_attn_dq_launch(A, d, s))) return rc;
-  return pack_attn_dkv_launch(A, d, s);
+  // Work lists where there are more items than SMs, or key tiles long enough to be cut; a batch below that
+  // starts every item at once.
+  const int64_t tiles = tiles_of(T);
+  const bool split = pack_split(tiles, n_kv, A.grp);
+  const bool listed = split || tiles * n_q > num_sms();
+  if (listed) {
+    const BwdWs w = bwd_ws(T, n_q, n_kv, d);
+    char* base = reinterpret_cast<char*>(A.D);
+    PackPlan plan = {};
+    plan.q_list = reinterpret_cast<int4*>(base + w.q_list);
+    plan.q_units = plan.tiles = static_cast<int>(tiles);
+    plan.q_per = 1;
+    plan.kv_list = reinterpret_cast<int4*>(base + w.kv_list);
+    plan.kv_head = reinterpret_cast<int*>(base + w.head);
+    plan.join_list = reinterpret_cast<int4*>(base + w.join);
+    plan.lanes = n_kv;
+    plan.split = split;
+    if ((rc = pack_attn_plan_launch(A, plan, s))) return rc;
+    A.q_list = plan.q_list;
+    A.kv_list = plan.kv_list;
+    A.kv_head = plan.kv_head;
+    A.join_list = plan.join_list;
+    A.part = reinterpret_cast<float*>(base + w.part);
+  }
+  if ((rc = pack_attn_dq_launch(A, d, s)) || (rc = pack_attn_dkv_launch(A, d, s))) return rc;
+  return split ? pack_attn_join_launch(A, d, s) : TTL_OK;
 }

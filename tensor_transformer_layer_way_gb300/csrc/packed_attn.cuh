@@ -32,14 +32,45 @@ struct PackArgs {
   float scale;
   float* D;                    // backward: rowsum(dO o), [t][n_q/t][T]
   int* status;
+  // Work lists, heaviest first, written by the plan kernel (null: the kernels look their items up)
+  const int4* q_list;          // see QUnit
+  const int4* kv_list;         // see KvUnit, two words each
+  const int* kv_head;          // [0] entries of kv_list, [1] key tiles in join_list, [2] partial slots (per lane) taken
+  const int4* join_list;       // {key tile, first slot, parts, 0} of the key tiles that several items share
+  float* part;                 // partial dK and dV: [slot * KV heads + head][2][128][d]
 };
+
+// Two key-loop bounds of a query unit: {unit, first key tile of its first token tile, of its second, 0}; -1 for
+// a token tile without keys.  A tile's last key tile is its own.
+// A key unit: {key tile, last query tile, first step, end step} {slot or -1, 0, 0, 0}.
+
+// What the plan kernel writes for a launch (null: not wanted).
+struct PackPlan {
+  int4* q_list;
+  int q_units, q_per;          // token tiles per query unit
+  int4* kv_list;
+  int* kv_head;
+  int4* join_list;
+  int tiles, lanes;            // key tiles; KV heads over all shards
+  int split;                   // key tiles may be cut into several items
+};
+constexpr int kSplitItems = 456;   // items a cut aims at in all: three for each of 152 SMs
+constexpr int kSplitSteps = 8;     // and no shorter than this
+int pack_attn_plan_launch(const PackArgs& A, const PackPlan& plan, cudaStream_t stream);
+int pack_attn_join_launch(const PackArgs& A, int d, cudaStream_t stream);
+// Whether key tiles may be cut: few items, and long enough ones.  With eight items or more for each SM the
+// list's order alone evens the SMs out.
+inline bool pack_split(int64_t tiles, int lanes, int grp) {
+  return tiles * lanes < 8 * 152 && tiles * grp > 2 * kSplitSteps;
+}
 
 // Raises a kernel's dynamic shared-memory limit, once per kernel and device (thread-safe).
 enum PackKernelSlot { kPackFwd128, kPackFwd64, kPackDq128, kPackDq64, kPackDkv128, kPackDkv64, kPackKernelSlots };
 int set_core_smem_once(const void* fn, int slot, int bytes, const char* what);
 
 // Launches of the tensor-core kernels (arguments are checked; A.s holds every pointer they need).
-int pack_attn_fwd_launch(const PackArgs& A, int d, cudaStream_t stream);
+// `list`: room for one word of 16 bytes per 128 tokens.
+int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stream);
 int pack_attn_dq_launch(const PackArgs& A, int d, cudaStream_t stream);    // dQ and D
 int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream);   // dK and dV, after D
 
@@ -100,6 +131,21 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+// 32 fp32 bit patterns of a row as bf16 to 64 bytes of global memory: whole 32-byte sectors where the row allows.
+__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* out, const uint32_t (&o)[32]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+  if ((reinterpret_cast<uintptr_t>(out) & 31) == 0) {
+    st_global_v8(out, w);
+    st_global_v8(out + 16, w + 8);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<uint4*>(out + u * 8) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+  }
 }
 
 // ------------------------------------------------------------------ one row by one warp

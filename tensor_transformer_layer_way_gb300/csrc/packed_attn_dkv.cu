@@ -50,20 +50,33 @@ struct KvCfg {
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
 };
 
+// Steps [t0, t0 + steps) of a key tile: step n is query tile qt_last - n / group, head n % group of the group.
 struct KvItem {
-  int shard, g, k0, qt_first, qt_last, steps;   // query tiles [qt_first, qt_last], steps = tiles x group
+  int shard, g, k0, qt_last, t0, steps;
+  int slot;                    // >= 0: a part of the key tile's sums, for that place of the partial buffers
 };
 
 __device__ __forceinline__ KvItem kv_item(const KvParams& P, int at) {
   const PackArgs& A = P.a;
-  const int tile = at / P.lanes, ln = at % P.lanes;
+  const int ln = at % P.lanes;
   KvItem it;
   it.shard = ln / A.nkvl;
   it.g = ln % A.nkvl;
+  it.slot = -1;
+  if (A.kv_list) {
+    const int4 e = __ldg(A.kv_list + 2 * (at / P.lanes));
+    const int slot = __ldg(A.kv_list + 2 * (at / P.lanes) + 1).x;
+    it.k0 = e.x * kTile;
+    it.qt_last = e.y;
+    it.t0 = e.z;
+    it.steps = e.w - e.z;
+    if (slot >= 0) it.slot = slot * P.lanes + ln;
+    return it;
+  }
+  const int tile = at / P.lanes;
   it.k0 = tile * kTile;
-  it.qt_first = tile;
   it.qt_last = tile - 1;
-  it.steps = 0;
+  it.t0 = it.steps = 0;
   if (A.batch > 0) {
     const int T = static_cast<int>(A.T);
     const int first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
@@ -122,16 +135,16 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   const PackArgs& A = P.a;
   const int warp = uniform_warp();
   const int lane = threadIdx.x & 31;
-  const int total = P.tiles * P.lanes;
+  const int total = (A.kv_list ? __ldg(A.kv_head) : P.tiles) * P.lanes;
   int* status = A.status;
   const uint64_t tmo = P.timeout_ns;
   auto item_at = [&](int n) {
     const int b = static_cast<int>(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     return n * static_cast<int>(gridDim.x) + b;
   };
-  // Step n of an item: the last query tile first, the group's heads in turn.
-  auto step_q0 = [&](const KvItem& it, int n) { return (it.qt_last - n / A.grp) * kTile; };
-  auto step_head = [&](const KvItem& it, int n) { return it.g * A.grp + n % A.grp; };
+  // The item's n-th step: the last query tile first, the group's heads in turn.
+  auto step_q0 = [&](const KvItem& it, int n) { return (it.qt_last - (it.t0 + n) / A.grp) * kTile; };
+  auto step_head = [&](const KvItem& it, int n) { return it.g * A.grp + (it.t0 + n) % A.grp; };
 
   if (threadIdx.x == 0) {
     mbar_init(k_full, 1);
@@ -170,8 +183,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int nk = 0, nv = 0, nq = 0, nd = 0;   // loads started: K, V, Q, dO tiles
+    KvItem ahead = {};
+    if (item_at(0) < total) ahead = kv_item(P, item_at(0));   // the coming item is looked up while this one runs
     for (int n = 0; item_at(n) < total; ++n) {
-      const KvItem it = kv_item(P, item_at(n));
+      const KvItem it = ahead;
+      if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
       if (it.steps == 0) continue;
       if (lane == 0 && ok) {
         auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint32_t phase, int x, int y) {
@@ -247,8 +263,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       for (int kk = 0; kk < kTile / 16; ++kk)
         umma_bf16_ts(dst, acol + (kk >> 2) * 64 + (kk & 3) * 8, desc_advance(bd, kk * 2048), idesc_acc, kk ? 1u : more);
     };
+    KvItem ahead = {};
+    if (item_at(0) < total) ahead = kv_item(P, item_at(0));
     for (int n = 0; item_at(n) < total; ++n) {
-      const KvItem it = kv_item(P, item_at(n));
+      const KvItem it = ahead;
+      if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
       if (it.steps == 0) continue;
       wait(k_full, ni);
       // S^T of step t overwrites P^T of the step before, whose dV product was issued before it (the tensor
@@ -304,8 +323,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // ------------------------------------------------------------------ lse and D of each step's queries
     bool ok = true;
     int pos = 0;
+    KvItem ahead = {};
+    if (item_at(0) < total) ahead = kv_item(P, item_at(0));
     for (int n = 0; ok && item_at(n) < total; ++n) {
-      const KvItem it = kv_item(P, item_at(n));
+      const KvItem it = ahead;
+      if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
       const float* lse = A.s[it.shard].lse;
       const float* Dr = A.D + static_cast<int64_t>(it.shard) * A.nql * A.T;
       for (int t = 0; t < it.steps; ++t, ++pos) {
@@ -344,12 +366,19 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     const int T = static_cast<int>(A.T);
     bool ok = true;
     int pos = 0, ni = 0;
+    KvItem ahead = {};
+    DocRange next_doc{0, 0};
+    auto look_up = [&](int n) {            // the coming item and its keys' documents
+      ahead = kv_item(P, item_at(n));
+      next_doc = DocRange{0, 0};
+      if (ahead.steps > 0) next_doc = doc_of(A.cu, A.batch, T, ahead.k0 + r);
+    };
+    if (item_at(0) < total) look_up(0);
     for (int n = 0; ok && item_at(n) < total; ++n) {
-      const KvItem it = kv_item(P, item_at(n));
+      const KvItem it = ahead;
+      const DocRange doc = next_doc;
       const PackShard& S = A.s[it.shard];
       const int key = it.k0 + r;
-      DocRange doc{0, 0};
-      if (it.steps > 0) doc = doc_of(A.cu, A.batch, T, key);
       const bool in = doc.hi > doc.lo;
       const int lo = in ? key : 0x7fffffff, hi = in ? doc.hi - 1 : -1;     // the queries that see the key
       const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
@@ -448,7 +477,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         }
       }
       if (!ok) break;
-      // ---- the first warpgroup stores dK, the second dV
+      // ---- the first warpgroup stores dK, the second dV; the last products are running
+      if (item_at(n + 1) < total) look_up(n + 1);
       const bool computed = it.steps > 0;
       if (computed) {
         ok = mbar_wait(acc_full, static_cast<uint32_t>(ni) & 1u, abort_flag, status, tmo);
@@ -460,9 +490,10 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         tc_fence_after_sync();
       }
       bool fine = true;
-      const float f = half ? 1.0f : A.scale;
+      const float f = half || it.slot >= 0 ? 1.0f : A.scale;
       const int64_t off = (half ? A.lddv : A.lddk) * static_cast<int64_t>(key < T ? key : 0) + it.g * D;
       __nv_bfloat16* out = (half ? S.dv : S.dk) + off;
+      float* part = A.part + ((static_cast<int64_t>(it.slot < 0 ? 0 : it.slot) * 2 + half) * kTile + r) * D;
 #pragma unroll
       for (int u = 0; u < D / 32; ++u) {
         uint32_t o[32];
@@ -478,18 +509,15 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           fine &= fabsf(v) < INFINITY;
           o[e] = __float_as_uint(v);
         }
-        if (key < T) {
+        if (it.slot >= 0) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            *reinterpret_cast<uint4*>(out + u * 32 + w * 8) = make_uint4(
-                pack_bf16x2(__uint_as_float(o[w * 8 + 0]), __uint_as_float(o[w * 8 + 1])),
-                pack_bf16x2(__uint_as_float(o[w * 8 + 2]), __uint_as_float(o[w * 8 + 3])),
-                pack_bf16x2(__uint_as_float(o[w * 8 + 4]), __uint_as_float(o[w * 8 + 5])),
-                pack_bf16x2(__uint_as_float(o[w * 8 + 6]), __uint_as_float(o[w * 8 + 7])));
+          for (int w = 0; w < 4; ++w) st_global_v8(part + u * 32 + w * 8, o + w * 8);
+        } else if (key < T) {
+          store_bf16x32(out + u * 32, o);
         }
       }
       tc_fence_before_sync();
-      const unsigned again = __ballot_sync(0xffffffffu, in && !fine);
+      const unsigned again = __ballot_sync(0xffffffffu, in && !fine && it.slot < 0);
       __syncwarp();   // the rows' stores above come before those of the redo
       if (again) redo_dkv<D>(A, it.shard, it.g, it.k0 + quad * 32, again, half == 0, lane);
     }
@@ -502,7 +530,53 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   }
 }
 
+// Adds up the parts of the key tiles that several items shared, in the order of their steps: one warp per row
+// of dK or dV.
+template <int D>
+__global__ void __launch_bounds__(256) pack_join_kernel(const __grid_constant__ PackArgs A) {
+  const int lane = threadIdx.x & 31;
+  const int lanes = A.t * A.nkvl;
+  const int64_t rows = static_cast<int64_t>(__ldg(A.kv_head + 1)) * lanes * 2 * kTile;
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); w < rows; w += gridDim.x * 8) {
+    const int r = static_cast<int>(w % kTile), half = static_cast<int>(w / kTile) & 1;
+    const int64_t at = w / (2 * kTile);
+    const int ln = static_cast<int>(at % lanes);
+    const int4 e = __ldg(A.join_list + at / lanes);
+    const int key = e.x * kTile + r;
+    if (key >= A.T) continue;
+    RowVec<D> acc = row_zero<D>();
+    for (int p = 0; p < e.z; ++p) {
+      const float* src = A.part + ((static_cast<int64_t>(e.y + p) * lanes + ln) * 2 + half) * kTile * D +
+                         static_cast<int64_t>(r) * D + lane * (D / 32);
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) acc.x[u] += src[u];
+    }
+    bool fine = true;
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+      if (half == 0) acc.x[u] *= A.scale;
+      fine &= fabsf(acc.x[u]) < INFINITY;
+    }
+    const int shard = ln / A.nkvl, g = ln % A.nkvl;
+    const PackShard& S = A.s[shard];
+    if (__all_sync(0xffffffffu, fine))
+      row_store<D>((half ? S.dv + key * A.lddv : S.dk + key * A.lddk) + g * D, acc, lane);
+    else
+      dkv_row<D>(A, S, shard, g, key, doc_of(A.cu, A.batch, static_cast<int>(A.T), key), half == 0, lane);
+  }
+}
+
 }  // namespace
+
+int pack_attn_join_launch(const PackArgs& A, int d, cudaStream_t stream) {
+  TraceScope trace(stream, TTL_K_OTHER, 0.0, 0.0);
+  const unsigned grid = static_cast<unsigned>(num_sms()) * 4;
+  if (d == 128)
+    pack_join_kernel<128><<<grid, 256, 0, stream>>>(A);
+  else
+    pack_join_kernel<64><<<grid, 256, 0, stream>>>(A);
+  return cuda_check(cudaGetLastError(), "pack_join_kernel launch");
+}
 
 int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream) {
   KvParams P;
@@ -523,7 +597,7 @@ int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(P.tiles) * P.lanes;
   if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many key tiles");
   const int sms = num_sms();
-  const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
+  const unsigned grid = static_cast<unsigned>(items < sms && !A.kv_list ? items : sms);
   const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
   TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * tri * d * A.nql * A.t, 2.0 * A.T * (2.0 * qc + 4.0 * kc) * A.t);
   if (d == 128) {

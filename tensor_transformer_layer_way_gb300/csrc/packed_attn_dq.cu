@@ -51,13 +51,23 @@ struct DqItem {
 
 __device__ __forceinline__ DqItem dq_item(const DqParams& P, int at) {
   const PackArgs& A = P.a;
-  const int tile = P.tiles - 1 - at / P.lanes, ln = at % P.lanes;
+  const int ln = at % P.lanes;
   DqItem it;
   it.shard = ln / A.nql;
   it.c = ln % A.nql;
   it.g = it.c / A.grp;
-  it.q0 = tile * kTile;
   it.jbeg = it.jend = 0;
+  if (A.q_list) {
+    const int4 e = __ldg(A.q_list + at / P.lanes);
+    it.q0 = e.x * kTile;
+    if (e.y >= 0) {
+      it.jbeg = e.y;
+      it.jend = e.x + 1;
+    }
+    return it;
+  }
+  const int tile = P.tiles - 1 - at / P.lanes;
+  it.q0 = tile * kTile;
   if (A.batch > 0) {
     const int T = static_cast<int>(A.T);
     const int first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
@@ -164,8 +174,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int pos = 0, nq = 0;    // key tiles and items started
+    DqItem ahead = {};
+    if (item_at(0) < total) ahead = dq_item(P, item_at(0));   // the coming item is looked up while this one runs
     for (int n = 0; item_at(n) < total; ++n) {
-      const DqItem it = dq_item(P, item_at(n));
+      const DqItem it = ahead;
+      if (item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
       if (it.jend <= it.jbeg) continue;
       if (lane == 0 && ok) {
         ok = mbar_wait(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
@@ -228,8 +241,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     auto wait = [&](uint64_t* bar, int phase) {
       mbar_wait(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
     };
+    DqItem ahead = {};
+    if (item_at(0) < total) ahead = dq_item(P, item_at(0));
     for (int n = 0; item_at(n) < total; ++n) {
-      const DqItem it = dq_item(P, item_at(n));
+      const DqItem it = ahead;
+      if (item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
       const int nt = it.jend - it.jbeg;
       if (nt <= 0) continue;
       wait(q_full, nq);
@@ -321,32 +337,46 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
       ++met;
       return static_cast<bool>(__all_sync(0xffffffffu, in_time));
     };
-    for (int n = 0; ok && item_at(n) < total; ++n) {
-      const DqItem it = dq_item(P, item_at(n));
-      const PackShard& S = A.s[it.shard];
-      const int i = it.q0 + r;
-      DocRange doc{0, 0};
-      if (it.jend > it.jbeg) doc = doc_of(A.cu, A.batch, T, i);
-      const bool in = doc.hi > doc.lo;
-      // D_i: this thread's half of the head's columns, the other half from the other warpgroup
-      float part = 0.0f;
-      if (in) {
-        const uint4* go = reinterpret_cast<const uint4*>(S.dO + i * A.lddo + it.c * D + half * (D / 2));
-        const uint4* oo = reinterpret_cast<const uint4*>(S.o + i * A.ldo + it.c * D + half * (D / 2));
+    // The coming item, its rows' documents, this thread's half of D_i = do_i . o_i (the other half of the head's
+    // columns comes from the other warpgroup) and lse_i: all looked up while the last product of the item
+    // before runs.
+    DqItem ahead = {};
+    DocRange next_doc{0, 0};
+    float next_part = 0.0f, next_nl = 0.0f;
+    auto look_up = [&](int n) {
+      ahead = dq_item(P, item_at(n));
+      const PackShard& S = A.s[ahead.shard];
+      const int i = ahead.q0 + r;
+      next_doc = DocRange{0, 0};
+      if (ahead.jend > ahead.jbeg) next_doc = doc_of(A.cu, A.batch, T, i);
+      next_part = next_nl = 0.0f;
+      if (next_doc.hi > next_doc.lo) {
+        const uint4* go = reinterpret_cast<const uint4*>(S.dO + i * A.lddo + ahead.c * D + half * (D / 2));
+        const uint4* oo = reinterpret_cast<const uint4*>(S.o + i * A.ldo + ahead.c * D + half * (D / 2));
+        next_nl = -S.lse[static_cast<int64_t>(ahead.c) * A.T + i] * kLog2e;
 #pragma unroll
         for (int u = 0; u < D / 16; ++u) {
           const uint4 a = __ldg(go + u), b = __ldg(oo + u);
           const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) part = fmaf(bf16_lo(aw[w]), bf16_lo(bw[w]), fmaf(bf16_hi(aw[w]), bf16_hi(bw[w]), part));
+          for (int w = 0; w < 4; ++w)
+            next_part = fmaf(bf16_lo(aw[w]), bf16_lo(bw[w]), fmaf(bf16_hi(aw[w]), bf16_hi(bw[w]), next_part));
         }
       }
+    };
+    if (item_at(0) < total) look_up(0);
+    for (int n = 0; ok && item_at(n) < total; ++n) {
+      const DqItem it = ahead;
+      const DocRange doc = next_doc;
+      const float part = next_part, nl = next_nl;
+      const PackShard& S = A.s[it.shard];
+      const int i = it.q0 + r;
+      const bool in = doc.hi > doc.lo;
       xch[half * kTile + r] = part;   // (the last item's were read before the warps met at its end)
       if (!(ok = meet())) break;
       const float Di = xch[r] + xch[kTile + r];
       const int64_t stat = static_cast<int64_t>(it.c) * A.T + (i < T ? i : 0);
       if (half == 0 && i < T) A.D[static_cast<int64_t>(it.shard) * A.nql * A.T + stat] = Di;
-      const float nl = in ? -S.lse[stat] * kLog2e : 0.0f;
       const int lo = in ? doc.lo : 0x7fffffff, hi = in ? i : -1;
       const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
       const uint64_t kk2 = f2_pack(k2, k2), nl2 = f2_pack(nl, nl), nD2 = f2_pack(-Di, -Di);
@@ -420,6 +450,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&ds_full[b]);
       }
       if (!ok) break;
+      if (item_at(n + 1) < total) look_up(n + 1);
       const bool computed = it.jend > it.jbeg;
       if (computed) {
         ok = mbar_wait(dq_full, static_cast<uint32_t>(no) & 1u, abort_flag, status, tmo);
@@ -447,15 +478,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           fine &= fabsf(v) < INFINITY;
           o[e] = __float_as_uint(v);
         }
-        if (i < T) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            *reinterpret_cast<uint4*>(out + u * 32 + w * 8) = make_uint4(
-                pack_bf16x2(__uint_as_float(o[w * 8 + 0]), __uint_as_float(o[w * 8 + 1])),
-                pack_bf16x2(__uint_as_float(o[w * 8 + 2]), __uint_as_float(o[w * 8 + 3])),
-                pack_bf16x2(__uint_as_float(o[w * 8 + 4]), __uint_as_float(o[w * 8 + 5])),
-                pack_bf16x2(__uint_as_float(o[w * 8 + 6]), __uint_as_float(o[w * 8 + 7])));
-        }
+        if (i < T) store_bf16x32(out + u * 32, o);
       }
       if (computed) {
         tc_fence_before_sync();

@@ -66,51 +66,44 @@ struct Item {
   int jlo, jhi;                // union of the key tiles
 };
 
-__device__ __forceinline__ void tile_range(const PackArgs& A, QTile& q) {
+// First key tile of the query tile at token q0, or -1; found by the whole warp.
+__device__ __forceinline__ int first_key(const PackArgs& A, int q0) {
   const int T = static_cast<int>(A.T);
-  q.jbeg = q.jend = 0;
-  if (A.batch == 0) return;
+  if (A.batch == 0) return -1;
   const int first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
-  const int v0 = q.q0 > first ? q.q0 : first;
-  int v1 = q.q0 + kTile < last ? q.q0 + kTile : last;
+  const int v0 = q0 > first ? q0 : first;
+  int v1 = q0 + kTile < last ? q0 + kTile : last;
   v1 = v1 < T ? v1 : T;
-  if (v0 >= v1) return;
-  q.jbeg = doc_of_warp(A.cu, A.batch, T, v0).lo / kTile;
-  q.jend = q.q0 / kTile + 1;
+  return v0 < v1 ? doc_of_warp(A.cu, A.batch, T, v0).lo / kTile : -1;
 }
 
-// The item of index `at` (heaviest token tiles of one long document first); every lane of a warp calls it.
+// The item of index `at`: from the list, or without one the last token tiles first; every lane of a warp calls it.
 __device__ __forceinline__ Item item_of(const FwdParams& P, int at) {
   const PackArgs& A = P.a;
-  const int unit = P.units - 1 - at / P.lanes;
-  int lane = at % P.lanes;
-  Item it;
-  if (P.pair_heads) {
-    const int half = A.nql / 2;
-    it.shard = lane / half;
-    const int c = (lane % half) * 2;
-    it.g = c / A.grp;
-    it.x[0].c = c;
-    it.x[1].c = c + 1;
-    it.x[0].q0 = it.x[1].q0 = unit * kTile;
-    tile_range(A, it.x[0]);
-    it.x[1].jbeg = it.x[0].jbeg;
-    it.x[1].jend = it.x[0].jend;
-    it.jlo = it.x[0].jbeg;
-    it.jhi = it.x[0].jend;
+  const int lane = at % P.lanes;
+  int unit = P.units - 1 - at / P.lanes;
+  int4 e = make_int4(unit, -1, -1, 0);
+  if (A.q_list) {
+    e = __ldg(A.q_list + at / P.lanes);
+    unit = e.x;
   } else {
-    it.shard = lane / A.nql;
-    const int c = lane % A.nql;
-    it.g = c / A.grp;
-    it.x[0].c = it.x[1].c = c;
-    it.x[0].q0 = unit * 2 * kTile;
-    it.x[1].q0 = it.x[0].q0 + kTile;
-    tile_range(A, it.x[0]);
-    tile_range(A, it.x[1]);
-    const bool a = it.x[0].jend > it.x[0].jbeg, b = it.x[1].jend > it.x[1].jbeg;
-    it.jlo = a && (!b || it.x[0].jbeg < it.x[1].jbeg) ? it.x[0].jbeg : it.x[1].jbeg;
-    it.jhi = b ? it.x[1].jend : it.x[0].jend;
+    e.y = first_key(A, unit * (P.pair_heads ? 1 : 2) * kTile);
+    if (!P.pair_heads) e.z = first_key(A, (unit * 2 + 1) * kTile);
   }
+  Item it;
+  const int per = P.pair_heads ? A.nql / 2 : A.nql;
+  it.shard = lane / per;
+  const int c = (lane % per) * (P.pair_heads ? 2 : 1);
+  it.g = c / A.grp;
+  const int t0 = P.pair_heads ? unit : 2 * unit;
+  auto tile = [&](int head, int t, int first) {
+    return QTile{head, t * kTile, first < 0 ? 0 : first, first < 0 ? 0 : t + 1};
+  };
+  it.x[0] = tile(c, t0, e.y);
+  it.x[1] = P.pair_heads ? tile(c + 1, t0, e.y) : tile(c, t0 + 1, e.z);
+  const bool a = it.x[0].jend > 0, b = it.x[1].jend > 0;
+  it.jlo = a && (!b || it.x[0].jbeg < it.x[1].jbeg) ? it.x[0].jbeg : it.x[1].jbeg;
+  it.jhi = b ? it.x[1].jend : it.x[0].jend;
   return it;
 }
 
@@ -189,8 +182,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int pos = 0, nq = 0;
+    Item ahead = {};
+    if (item_at(0) < total) ahead = item_of(P, item_at(0));     // the coming item is looked up while this one runs
     for (int n = 0; item_at(n) < total; ++n) {
-      const Item it = item_of(P, item_at(n));
+      const Item it = ahead;
+      if (item_at(n + 1) < total) ahead = item_of(P, item_at(n + 1));
       if (it.jhi <= it.jlo) continue;
       if (lane == 0 && ok) {
         ok = mbar_wait(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
@@ -245,8 +241,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     auto wait = [&](uint64_t* bar, int phase) {
       mbar_wait(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
     };
+    Item ahead = {};
+    if (item_at(0) < total) ahead = item_of(P, item_at(0));
     for (int n = 0; item_at(n) < total; ++n) {
-      const Item it = item_of(P, item_at(n));
+      const Item it = ahead;
+      if (item_at(n + 1) < total) ahead = item_of(P, item_at(n + 1));
       if (it.jhi <= it.jlo) continue;
       wait(q_full, nq);
       tc_fence_after_sync();
@@ -318,13 +317,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     const int T = static_cast<int>(A.T);
     bool ok = true;
     uint32_t ns = 0, no = 0;
-    for (int n = 0; ok && item_at(n) < total; ++n) {
+    QTile next_qt = {};
+    int next_shard = 0;
+    DocRange next_doc{0, 0};
+    auto look_up = [&](int n) {                  // the coming item and its rows' documents
       const Item it = item_of(P, item_at(n));
-      const QTile qt = x ? it.x[1] : it.x[0];
-      const PackShard& S = A.s[it.shard];
+      next_qt = x ? it.x[1] : it.x[0];
+      next_shard = it.shard;
+      next_doc = DocRange{0, 0};
+      if (next_qt.jend > next_qt.jbeg) next_doc = doc_of(A.cu, A.batch, T, next_qt.q0 + r);
+    };
+    if (item_at(0) < total) look_up(0);
+    for (int n = 0; ok && item_at(n) < total; ++n) {
+      const QTile qt = next_qt;
+      const int shard = next_shard;
+      const DocRange doc = next_doc;
+      const PackShard& S = A.s[shard];
       const int i = qt.q0 + r;
-      DocRange doc{0, 0};
-      if (qt.jend > qt.jbeg) doc = doc_of(A.cu, A.batch, T, i);
       const bool in = doc.hi > doc.lo;           // a row of a document (so i < T)
       const int lo = in ? doc.lo : 0x7fffffff, hi = in ? i : -1;      // its keys are lo..hi
       const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
@@ -404,7 +413,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
-      // ---- the row's result
+      // ---- the row's result; its last product is running
+      if (item_at(n + 1) < total) look_up(n + 1);
       const bool computed = qt.jend > qt.jbeg;
       if (computed) {
         ok = mbar_wait(&o_full[x], no & 1u, abort_flag, status, tmo);
@@ -437,21 +447,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
           fine &= fabsf(v) < INFINITY;
           o[e] = __float_as_uint(v);
         }
-        if (i < T) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            *reinterpret_cast<uint4*>(out + u * 32 + w * 8) = make_uint4(
-                pack_bf16x2(__uint_as_float(o[w * 8 + 0]), __uint_as_float(o[w * 8 + 1])),
-                pack_bf16x2(__uint_as_float(o[w * 8 + 2]), __uint_as_float(o[w * 8 + 3])),
-                pack_bf16x2(__uint_as_float(o[w * 8 + 4]), __uint_as_float(o[w * 8 + 5])),
-                pack_bf16x2(__uint_as_float(o[w * 8 + 6]), __uint_as_float(o[w * 8 + 7])));
-        }
+        if (i < T) store_bf16x32(out + u * 32, o);
       }
       tc_fence_before_sync();
       if (i < T) S.lse[static_cast<int64_t>(qt.c) * A.T + i] = in ? (m + __log2f(l)) * kLn2 : -INFINITY;
       const unsigned again = __ballot_sync(0xffffffffu, in && !fine);
       __syncwarp();   // the rows' stores above come before those of the redo
-      if (again) redo_rows<D>(A, it.shard, qt.c, qt.q0 + quad * 32, again, lane);
+      if (again) redo_rows<D>(A, shard, qt.c, qt.q0 + quad * 32, again, lane);
     }
   }
 
@@ -478,7 +480,7 @@ int set_core_smem_once(const void* fn, int slot, int bytes, const char* what) {
   return rc;
 }
 
-int pack_attn_fwd_launch(const PackArgs& A, int d, cudaStream_t stream) {
+int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stream) {
   FwdParams P;
   std::memset(static_cast<void*>(&P), 0, sizeof(P));
   P.a = A;
@@ -499,6 +501,14 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, cudaStream_t stream) {
   if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many query tiles");
   const int sms = num_sms();
   const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
+  if (items > sms) {   // more than one round: the order counts
+    PackPlan plan = {};
+    plan.q_list = static_cast<int4*>(list);
+    plan.q_units = P.units;
+    plan.q_per = P.pair_heads ? 1 : 2;
+    if ((rc = pack_attn_plan_launch(A, plan, stream))) return rc;
+    P.a.q_list = plan.q_list;
+  }
   const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
   TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * tri * d * A.nql * A.t,
                    2.0 * A.T * (2.0 * qc + 2.0 * kc) * A.t);

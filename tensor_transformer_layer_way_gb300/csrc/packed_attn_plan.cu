@@ -1,0 +1,160 @@
+// Work lists of the packed attention kernels.
+//
+// A query tile's work is the number of key tiles it meets, a key tile's the number of (query tile, head) steps;
+// both depend on the documents, which only the device knows.  One CTA sorts the tiles by work, heaviest first
+// (a counting sort; tiles of equal work in any order), so that the persistent kernels, which take items in
+// turn, end together, and cuts the longest key tiles into several items where there are few.  Worth one small
+// launch only when there are more items than SMs; below that every item starts at once.
+
+#include "packed_attn.cuh"
+
+namespace ttl {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// First key tile that token tile `tile` meets, or -1.
+__device__ __forceinline__ int first_key_tile(const PackArgs& A, int tile) {
+  const int T = static_cast<int>(A.T);
+  if (A.batch == 0 || static_cast<int64_t>(tile) * kTile >= A.T) return -1;
+  const int q0 = tile * kTile, first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
+  const int v0 = q0 > first ? q0 : first;
+  int v1 = q0 + kTile < last ? q0 + kTile : last;
+  v1 = v1 < T ? v1 : T;
+  return v0 < v1 ? doc_of(A.cu, A.batch, T, v0).lo / kTile : -1;
+}
+
+// Last query tile that key tile `tile` meets, or tile - 1.
+__device__ __forceinline__ int last_query_tile(const PackArgs& A, int tile) {
+  const int T = static_cast<int>(A.T);
+  if (A.batch == 0) return tile - 1;
+  const int k0 = tile * kTile, first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
+  const int v0 = k0 > first ? k0 : first;
+  int v1 = k0 + kTile < last ? k0 + kTile : last;
+  v1 = v1 < T ? v1 : T;
+  if (v0 >= v1) return tile - 1;
+  const int hi = doc_of(A.cu, A.batch, T, v1 - 1).hi;
+  return (hi > v1 ? hi - 1 : v1 - 1) / kTile;
+}
+
+// hist[b] entries of work class b become places, the highest class first.  Every thread calls it.
+__device__ __forceinline__ void to_places(int* hist, int* warp_tot) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  __syncthreads();
+  const int mine = hist[kPlanThreads - 1 - threadIdx.x];
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) warp_tot[w] = inc;
+  __syncthreads();
+  int base = inc - mine;
+  for (int j = 0; j < w; ++j) base += warp_tot[j];
+  hist[kPlanThreads - 1 - threadIdx.x] = base;
+  __syncthreads();
+}
+
+__device__ __forceinline__ int work_class(int work, int shift) {
+  const int c = work >> shift;
+  return c < kPlanThreads ? c : kPlanThreads - 1;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_constant__ PackArgs A,
+                                                                 const __grid_constant__ PackPlan P, int q_shift,
+                                                                 int kv_shift) {
+  __shared__ int hist[kPlanThreads];
+  __shared__ int warp_tot[32];
+  __shared__ unsigned long long total;
+  __shared__ int taken, joins;
+  const int tid = threadIdx.x;
+  if (P.q_list) {
+    hist[tid] = 0;
+    __syncthreads();
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int u = tid; u < P.q_units; u += kPlanThreads) {
+        const int t0 = u * P.q_per;
+        const int a = first_key_tile(A, t0), b = P.q_per == 2 ? first_key_tile(A, t0 + 1) : -1;
+        const int work = (a < 0 ? 0 : t0 + 1 - a) + (b < 0 ? 0 : t0 + 2 - b);
+        const int at = atomicAdd(&hist[work_class(work, q_shift)], 1);
+        if (pass) P.q_list[at] = make_int4(u, a, b, 0);
+      }
+      if (pass == 0) to_places(hist, warp_tot);
+    }
+    __syncthreads();
+  }
+  if (P.kv_list) {
+    hist[tid] = 0;
+    if (tid == 0) {
+      total = 0;
+      taken = joins = 0;
+    }
+    __syncthreads();
+    unsigned long long sum = 0;
+    for (int t = tid; t < P.tiles; t += kPlanThreads)
+      sum += static_cast<unsigned long long>(last_query_tile(A, t) - t + 1) * A.grp;
+    atomicAdd(&total, sum);
+    __syncthreads();
+    // the longest item: a third of an SM's share of all steps
+    unsigned long long most = 0x7fffffffull;
+    if (P.split) {
+      most = (total * P.lanes + kSplitItems - 1) / kSplitItems;
+      if (most < kSplitSteps) most = kSplitSteps;
+    }
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int t = tid; t < P.tiles; t += kPlanThreads) {
+        const int last = last_query_tile(A, t);
+        const int steps = (last - t + 1) * A.grp;
+        const int parts = steps > 0 ? static_cast<int>((steps + most - 1) / most) : 1;
+        const int len = (steps + parts - 1) / parts;
+        const int at = atomicAdd(&hist[work_class(len, kv_shift)], parts);
+        if (pass) {
+          int slot = -1;
+          if (parts > 1) {
+            slot = atomicAdd(&taken, parts);
+            P.join_list[atomicAdd(&joins, 1)] = make_int4(t, slot, parts, 0);
+          }
+          for (int p = 0; p < parts; ++p) {
+            const int b = p * len, e = b + len < steps ? b + len : steps;
+            P.kv_list[2 * (at + p)] = make_int4(t, last, b < steps ? b : steps, e);
+            P.kv_list[2 * (at + p) + 1] = make_int4(slot < 0 ? -1 : slot + p, 0, 0, 0);
+          }
+        }
+      }
+      if (pass == 0) {
+        to_places(hist, warp_tot);
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      P.kv_head[1] = joins;
+      P.kv_head[2] = taken;
+    }
+    // the number of entries: all places given out
+    int entries = 0;
+    for (int t = tid; t < P.tiles; t += kPlanThreads) {
+      const int steps = (last_query_tile(A, t) - t + 1) * A.grp;
+      entries += steps > 0 ? static_cast<int>((steps + most - 1) / most) : 1;
+    }
+    if (tid == 0) taken = 0;
+    __syncthreads();
+    atomicAdd(&taken, entries);
+    __syncthreads();
+    if (tid == 0) P.kv_head[0] = taken;
+  }
+}
+
+}  // namespace
+
+int pack_attn_plan_launch(const PackArgs& A, const PackPlan& plan, cudaStream_t stream) {
+  const int tiles = static_cast<int>((A.T + kTile - 1) / kTile);
+  int q_shift = 0, kv_shift = 0;
+  while ((2 * static_cast<int64_t>(tiles) >> q_shift) >= kPlanThreads) ++q_shift;
+  while ((static_cast<int64_t>(tiles) * A.grp >> kv_shift) >= kPlanThreads) ++kv_shift;
+  TraceScope trace(stream, TTL_K_OTHER, 0.0, 32.0 * tiles);
+  pack_plan_kernel<<<1, kPlanThreads, 0, stream>>>(A, plan, q_shift, kv_shift);
+  return cuda_check(cudaGetLastError(), "pack_plan_kernel launch");
+}
+
+}  // namespace ttl
