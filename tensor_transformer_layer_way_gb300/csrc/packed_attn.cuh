@@ -133,6 +133,24 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// 32 lanes x 32 bits, 16 consecutive columns from registers.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Bits [a, b] of a word, for any a and b (none where b < a).
+__device__ __forceinline__ uint32_t bits_between(int a, int b) {
+  const int lo = a < 0 ? 0 : (a > 32 ? 32 : a), hi = b < -1 ? -1 : (b > 31 ? 31 : b);
+  uint32_t m;
+  asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(m) : "r"(lo), "r"(hi < lo ? 0 : hi - lo + 1));
+  return m;
+}
+
 // 32 fp32 bit patterns of a row as bf16 to 64 bytes of global memory: whole 32-byte sectors where the row allows.
 __device__ __forceinline__ void store_bf16x32(__nv_bfloat16* out, const uint32_t (&o)[32]) {
   uint32_t w[16];

@@ -14,7 +14,7 @@
 // into P, dK(n) and dP(n+1) run; while they form dS(n+1), dV(n+1) and S(n+2) do.
 //
 // Roles (384 threads, persistent): warp 0 the TMA loads, warp 1 the MMAs, warp 2 brings each step's lse and D
-// to shared memory, warps 4..11 the elementwise work: a key row per thread, each warpgroup on 64 of the queries.
+// to shared memory, warp 3 the documents of the coming item's keys, warps 4..11 the elementwise work: a key row per thread, each warpgroup on 64 of the queries.
 
 #include <cstring>
 
@@ -45,7 +45,8 @@ struct KvCfg {
   static constexpr int OFF_Q = 2 * TILE;
   static constexpr int OFF_DO = OFF_Q + kSlots * TILE;
   static constexpr int OFF_STAT = OFF_DO + kSlots * TILE;   // float [kStat][2][128]: -lse log2(e), -D
-  static constexpr int OFF_BAR = OFF_STAT + kStat * 1024;
+  static constexpr int OFF_ROWS = OFF_STAT + kStat * 1024;  // int [128]: the last query that sees a key
+  static constexpr int OFF_BAR = OFF_ROWS + 512;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
 };
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   uint8_t* sQ = smem + C::OFF_Q;
   uint8_t* sDO = smem + C::OFF_DO;
   float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT);
+  int* row_hi = reinterpret_cast<int*>(smem + C::OFF_ROWS);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* k_empty = k_full + 1;
   uint64_t* v_full = k_empty + 1;
@@ -126,10 +128,12 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   uint64_t* dp_full = p_full + 1;
   uint64_t* ds_full = dp_full + 1;
   uint64_t* acc_full = ds_full + 1;
-  uint64_t* done_bar = acc_full + 1;
+  uint64_t* rows_full = acc_full + 1;
+  uint64_t* rows_empty = rows_full + 1;
+  uint64_t* done_bar = rows_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((4 + 4 * kSlots + 2 * kStat + 6) * 8 + 8 <= 256, "barrier area");
+  static_assert((4 + 4 * kSlots + 2 * kStat + 8) * 8 + 8 <= 256, "barrier area");
   constexpr uint32_t T_DP = 128, T_DK = 256, T_DV = 384;
 
   const PackArgs& A = P.a;
@@ -166,6 +170,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     mbar_init(dp_full, 1);
     mbar_init(ds_full, 8);
     mbar_init(acc_full, 1);
+    mbar_init(rows_full, 1);
+    mbar_init(rows_empty, 8);
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -267,8 +273,10 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     if (item_at(0) < total) ahead = kv_item(P, item_at(0));
     for (int n = 0; item_at(n) < total; ++n) {
       const KvItem it = ahead;
-      if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
-      if (it.steps == 0) continue;
+      if (it.steps == 0) {
+        if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
+        continue;
+      }
       wait(k_full, ni);
       // S^T of step t overwrites P^T of the step before, whose dV product was issued before it (the tensor
       // pipe runs one thread's products in order); likewise dP^T and dK.
@@ -309,6 +317,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           ++p;
         }
         __syncwarp();
+        // the coming item is looked up once the first products run
+        if (t < 0 && item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
       }
       if (leader) umma_commit(acc_full);
       __syncwarp();
@@ -355,7 +365,26 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         if (lane == 0) mbar_arrive(&st_full[st]);
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------ last queries of the coming item's keys
+    bool ok = true;
+    for (int n = 0; ok && item_at(n) < total; ++n) {
+      const KvItem it = kv_item(P, item_at(n));
+      int hi[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        DocRange doc{0, 0};
+        if (it.steps > 0) doc = doc_of(A.cu, A.batch, static_cast<int>(A.T), it.k0 + u * 32 + lane);
+        hi[u] = doc.hi > doc.lo ? doc.hi - 1 : -1;   // a token of no document is seen by none
+      }
+      ok = mbar_wait(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
+      if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) row_hi[u * 32 + lane] = hi[u];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rows_full);
+    }
+  } else {
     // ------------------------------------------------------------------ P^T and dS^T
     const int quad = warp & 3;
     const int half = (warp - 4) >> 2;
@@ -367,20 +396,21 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     bool ok = true;
     int pos = 0, ni = 0;
     KvItem ahead = {};
-    DocRange next_doc{0, 0};
-    auto look_up = [&](int n) {            // the coming item and its keys' documents
-      ahead = kv_item(P, item_at(n));
-      next_doc = DocRange{0, 0};
-      if (ahead.steps > 0) next_doc = doc_of(A.cu, A.batch, T, ahead.k0 + r);
-    };
-    if (item_at(0) < total) look_up(0);
+    if (item_at(0) < total) ahead = kv_item(P, item_at(0));
     for (int n = 0; ok && item_at(n) < total; ++n) {
       const KvItem it = ahead;
-      const DocRange doc = next_doc;
       const PackShard& S = A.s[it.shard];
       const int key = it.k0 + r;
-      const bool in = doc.hi > doc.lo;
-      const int lo = in ? key : 0x7fffffff, hi = in ? doc.hi - 1 : -1;     // the queries that see the key
+      ok = mbar_wait(rows_full, static_cast<uint32_t>(n) & 1u, abort_flag, status, tmo);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const int hi = row_hi[r];                      // the queries lo..hi see the key
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rows_empty);
+      const bool in = hi >= 0;                       // a key of a document
+      const int lo = in ? key : 0x7fffffff;
       const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
       for (int t = 0; ok && t < it.steps; ++t, ++pos) {
         const int st = pos % kStat;
@@ -399,7 +429,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         tmem_ld_32x32b_x32(lane_base + half * 64, s[0]);
         tmem_ld_32x32b_x32(lane_base + half * 64 + 32, s[1]);
         tmem_ld_wait();
-        const int a = lo - q0, b = hi - q0;
+        const uint32_t see[2] = {bits_between(lo - q0, hi - q0), bits_between(lo - q0 - 32, hi - q0 - 32)};
         uint32_t pk[32];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -419,7 +449,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[h][e] = (h * 32 + e >= a && h * 32 + e <= b) ? s[h][e] : 0u;
+            for (int e = 0; e < 32; ++e) s[h][e] = (see[h] >> e) & 1u ? s[h][e] : 0u;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -441,23 +471,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         tmem_ld_32x32b_x32(lane_base + T_DP + half * 64, dp[0]);
         tmem_ld_32x32b_x32(lane_base + T_DP + half * 64 + 32, dp[1]);
         tmem_ld_wait();
-        if (masked) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) dp[h][e] = (h * 32 + e >= a && h * 32 + e <= b) ? dp[h][e] : 0u;
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            float4 n4 = nD[(h * 32 + e) >> 2];
-            if (masked) {   // a hidden query's D may be anything
-              n4.x = h * 32 + e >= a && h * 32 + e <= b ? n4.x : 0.0f;
-              n4.y = h * 32 + e + 1 >= a && h * 32 + e + 1 <= b ? n4.y : 0.0f;
-              n4.z = h * 32 + e + 2 >= a && h * 32 + e + 2 <= b ? n4.z : 0.0f;
-              n4.w = h * 32 + e + 3 >= a && h * 32 + e + 3 <= b ? n4.w : 0.0f;
-            }
+            const float4 n4 = nD[(h * 32 + e) >> 2];
             const float2 u = f2_unpack(fmul2(
                 fadd2(f2_pack(__uint_as_float(dp[h][e]), __uint_as_float(dp[h][e + 1])), f2_pack(n4.x, n4.y)),
                 f2_pack(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]))));
@@ -467,6 +485,13 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
             pk[h * 16 + (e >> 1)] = pack_bf16x2(u.x, u.y);
             pk[h * 16 + (e >> 1) + 1] = pack_bf16x2(w.x, w.y);
           }
+        if (masked) {   // a hidden query's dP and D may be anything: its dS is 0
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              pk[h * 16 + (e >> 1)] &= ((see[h] >> e) & 1u ? 0x0000ffffu : 0u) | ((see[h] >> (e + 1)) & 1u ? 0xffff0000u : 0u);
+        }
         tmem_st_32x32b_x32(lane_base + T_DP + half * 64, pk);
         tmem_st_wait();
         tc_fence_before_sync();
@@ -478,7 +503,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       }
       if (!ok) break;
       // ---- the first warpgroup stores dK, the second dV; the last products are running
-      if (item_at(n + 1) < total) look_up(n + 1);
+      if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
       const bool computed = it.steps > 0;
       if (computed) {
         ok = mbar_wait(acc_full, static_cast<uint32_t>(ni) & 1u, abort_flag, status, tmo);
@@ -489,7 +514,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         ++ni;
         tc_fence_after_sync();
       }
-      bool fine = true;
+      float bad = 0.0f;   // becomes NaN with the first value that is not finite
       const float f = half || it.slot >= 0 ? 1.0f : A.scale;
       const int64_t off = (half ? A.lddv : A.lddk) * static_cast<int64_t>(key < T ? key : 0) + it.g * D;
       __nv_bfloat16* out = (half ? S.dv : S.dk) + off;
@@ -506,7 +531,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const float v = in ? __uint_as_float(o[e]) * f : 0.0f;
-          fine &= fabsf(v) < INFINITY;
+          bad = fmaf(v, 0.0f, bad);
           o[e] = __float_as_uint(v);
         }
         if (it.slot >= 0) {
@@ -517,7 +542,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         }
       }
       tc_fence_before_sync();
-      const unsigned again = __ballot_sync(0xffffffffu, in && !fine && it.slot < 0);
+      const unsigned again = __ballot_sync(0xffffffffu, in && bad != 0.0f && it.slot < 0);
       __syncwarp();   // the rows' stores above come before those of the redo
       if (again) redo_dkv<D>(A, it.shard, it.g, it.k0 + quad * 32, again, half == 0, lane);
     }

@@ -8,7 +8,8 @@
 //
 // Roles (384 threads, persistent): warp 0 the TMA loads (K three slots deep, read by S_j and again by dQ_j;
 // V two), warp 1 the MMAs in the order S_(j+1), dP_(j+1), dQ_j, so that two products run while the
-// elementwise warps form dS_j; warps 4..11 that: a row per thread, each warpgroup on 64 of the keys.
+// elementwise warps form dS_j; warps 2 and 3 bring lse, D and the first key of the coming item's rows to shared
+// memory; warps 4..11 form dS: a row per thread, each warpgroup on 64 of the keys.
 // S, dP and dQ take 384 columns of tensor memory and two dS buffers the rest.
 
 #include <cstring>
@@ -39,7 +40,7 @@ struct DqCfg {
   static constexpr int OFF_DO = TILE;
   static constexpr int OFF_K = 2 * TILE;
   static constexpr int OFF_V = OFF_K + kKSlots * TILE;
-  static constexpr int OFF_X = OFF_V + kVSlots * TILE;   // float [2][128]: the two halves of D; int [128]: flags
+  static constexpr int OFF_X = OFF_V + kVSlots * TILE;   // of each row: -lse log2(e), D, first key
   static constexpr int OFF_BAR = OFF_X + 1536;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
@@ -100,8 +101,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
   uint8_t* sDO = smem + C::OFF_DO;
   uint8_t* sK = smem + C::OFF_K;
   uint8_t* sV = smem + C::OFF_V;
-  float* xch = reinterpret_cast<float*>(smem + C::OFF_X);
-  int* flags = reinterpret_cast<int*>(smem + C::OFF_X + 1024);
+  float* row_nl = reinterpret_cast<float*>(smem + C::OFF_X);
+  float* row_D = row_nl + kTile;
+  int* row_lo = reinterpret_cast<int*>(row_D + kTile);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_empty = q_full + 1;
   uint64_t* k_full = q_empty + 1;
@@ -117,10 +119,13 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
   uint64_t* dq_full = ds_empty + 2;
   uint64_t* dq_empty = dq_full + 1;
   uint64_t* x_bar = dq_empty + 1;      // the eight elementwise warps meet
-  uint64_t* done_bar = x_bar + 1;
+  uint64_t* rows_full = x_bar + 1;
+  uint64_t* rows_empty = rows_full + 1;
+  uint64_t* done_bar = rows_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 + 2 * kKSlots + 2 * kVSlots + 12) * 8 + 8 <= 256, "barrier area");
+  uint32_t* flags = tmem_slot + 2;     // [4]: rows of a quadrant to be done again
+  static_assert((2 + 2 * kKSlots + 2 * kVSlots + 14) * 8 + 24 <= 256, "barrier area");
   constexpr uint32_t T_DP = 128, T_DQ = 256, T_DS = 384;
 
   const PackArgs& A = P.a;
@@ -156,6 +161,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     mbar_init(dq_full, 1);
     mbar_init(dq_empty, 8);
     mbar_init(x_bar, 8);
+    mbar_init(rows_full, 2);
+    mbar_init(rows_empty, 8);
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -245,9 +252,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     if (item_at(0) < total) ahead = dq_item(P, item_at(0));
     for (int n = 0; item_at(n) < total; ++n) {
       const DqItem it = ahead;
-      if (item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
       const int nt = it.jend - it.jbeg;
-      if (nt <= 0) continue;
+      if (nt <= 0) {
+        if (item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
+        continue;
+      }
       wait(q_full, nq);
       tc_fence_after_sync();
       ++nq;
@@ -303,6 +312,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           }
         }
         __syncwarp();
+        // the coming item is looked up once the first products run
+        if (j < 0 && item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
         if (j + 1 < nt) {
           ++p;
           old = ks;
@@ -318,7 +329,66 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     int dummy = 0;
     mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ lse, D and first keys of 64 rows
+    const int r0 = (warp - 2) * 64;
+    const int T = static_cast<int>(A.T);
+    constexpr int LANES = D / 8;                 // lanes that hold a row (16 bytes each)
+    constexpr int ROWS = 32 / LANES;             // rows a warp reads at a time
+    bool ok = true;
+    for (int n = 0; ok && item_at(n) < total; ++n) {
+      const DqItem it = dq_item(P, item_at(n));
+      const PackShard& S = A.s[it.shard];
+      int lo[2];
+      float nl[2], Dr[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = it.q0 + r0 + u * 32 + lane;
+        DocRange doc{0, 0};
+        if (it.jend > it.jbeg) doc = doc_of(A.cu, A.batch, T, i);
+        const bool in = doc.hi > doc.lo;
+        lo[u] = in ? doc.lo : 0x7fffffff;        // a token of no document has no keys
+        nl[u] = in ? -__ldg(S.lse + static_cast<int64_t>(it.c) * A.T + i) * kLog2e : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll 4
+        for (int q = 0; q < 32; q += ROWS) {
+          const int i = it.q0 + r0 + u * 32 + q + lane / LANES;
+          float d = 0.0f;
+          if (i < T) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(S.dO + i * A.lddo + it.c * D) + lane % LANES);
+            const uint4 b = __ldg(reinterpret_cast<const uint4*>(S.o + i * A.ldo + it.c * D) + lane % LANES);
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) d = fmaf(bf16_lo(aw[w]), bf16_lo(bw[w]), fmaf(bf16_hi(aw[w]), bf16_hi(bw[w]), d));
+          }
+#pragma unroll
+          for (int o = LANES / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+#pragma unroll
+          for (int k = 0; k < ROWS; ++k) {       // to the lane whose row it is
+            const float v = __shfl_sync(0xffffffffu, d, k * LANES);
+            if (lane == q + k) Dr[u] = v;
+          }
+        }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = it.q0 + r0 + u * 32 + lane;
+        if (lo[u] == 0x7fffffff) Dr[u] = 0.0f;
+        if (i < T) A.D[(static_cast<int64_t>(it.shard) * A.nql + it.c) * A.T + i] = Dr[u];
+      }
+      ok = mbar_wait(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
+      if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        row_lo[r0 + u * 32 + lane] = lo[u];
+        row_nl[r0 + u * 32 + lane] = nl[u];
+        row_D[r0 + u * 32 + lane] = Dr[u];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rows_full);
+    }
+  } else {
     // ------------------------------------------------------------------ dS
     const int quad = warp & 3;
     const int half = (warp - 4) >> 2;
@@ -337,47 +407,23 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
       ++met;
       return static_cast<bool>(__all_sync(0xffffffffu, in_time));
     };
-    // The coming item, its rows' documents, this thread's half of D_i = do_i . o_i (the other half of the head's
-    // columns comes from the other warpgroup) and lse_i: all looked up while the last product of the item
-    // before runs.
     DqItem ahead = {};
-    DocRange next_doc{0, 0};
-    float next_part = 0.0f, next_nl = 0.0f;
-    auto look_up = [&](int n) {
-      ahead = dq_item(P, item_at(n));
-      const PackShard& S = A.s[ahead.shard];
-      const int i = ahead.q0 + r;
-      next_doc = DocRange{0, 0};
-      if (ahead.jend > ahead.jbeg) next_doc = doc_of(A.cu, A.batch, T, i);
-      next_part = next_nl = 0.0f;
-      if (next_doc.hi > next_doc.lo) {
-        const uint4* go = reinterpret_cast<const uint4*>(S.dO + i * A.lddo + ahead.c * D + half * (D / 2));
-        const uint4* oo = reinterpret_cast<const uint4*>(S.o + i * A.ldo + ahead.c * D + half * (D / 2));
-        next_nl = -S.lse[static_cast<int64_t>(ahead.c) * A.T + i] * kLog2e;
-#pragma unroll
-        for (int u = 0; u < D / 16; ++u) {
-          const uint4 a = __ldg(go + u), b = __ldg(oo + u);
-          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            next_part = fmaf(bf16_lo(aw[w]), bf16_lo(bw[w]), fmaf(bf16_hi(aw[w]), bf16_hi(bw[w]), next_part));
-        }
-      }
-    };
-    if (item_at(0) < total) look_up(0);
+    if (item_at(0) < total) ahead = dq_item(P, item_at(0));
     for (int n = 0; ok && item_at(n) < total; ++n) {
       const DqItem it = ahead;
-      const DocRange doc = next_doc;
-      const float part = next_part, nl = next_nl;
       const PackShard& S = A.s[it.shard];
       const int i = it.q0 + r;
-      const bool in = doc.hi > doc.lo;
-      xch[half * kTile + r] = part;   // (the last item's were read before the warps met at its end)
-      if (!(ok = meet())) break;
-      const float Di = xch[r] + xch[kTile + r];
-      const int64_t stat = static_cast<int64_t>(it.c) * A.T + (i < T ? i : 0);
-      if (half == 0 && i < T) A.D[static_cast<int64_t>(it.shard) * A.nql * A.T + stat] = Di;
-      const int lo = in ? doc.lo : 0x7fffffff, hi = in ? i : -1;
+      ok = mbar_wait(rows_full, static_cast<uint32_t>(n) & 1u, abort_flag, status, tmo);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const int lo = row_lo[r];                      // the row sees the keys lo..hi
+      const float nl = row_nl[r], Di = row_D[r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rows_empty);
+      const bool in = lo != 0x7fffffff;              // a row of a document (so i < T)
+      const int hi = in ? i : -1;
       const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
       const uint64_t kk2 = f2_pack(k2, k2), nl2 = f2_pack(nl, nl), nD2 = f2_pack(-Di, -Di);
       for (int j = it.jbeg; ok && j < it.jend; ++j, ++pos) {
@@ -417,15 +463,15 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         if (lane == 0) mbar_arrive_relaxed(dp_empty);
         const int k0 = j * kTile + half * 64;
         if (k0 < lo_max || k0 + 63 > hi_min) {   // some row of the warp does not see every key
-          const int a = lo - k0, b = hi - k0;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t see = bits_between(lo - k0 - h * 32, hi - k0 - h * 32);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const bool see = h * 32 + e >= a && h * 32 + e <= b;
-              s[h][e] = see ? s[h][e] : 0u;
-              dp[h][e] = see ? dp[h][e] : 0u;
+              s[h][e] = (see >> e) & 1u ? s[h][e] : 0u;
+              dp[h][e] = (see >> e) & 1u ? dp[h][e] : 0u;
             }
+          }
         }
         uint32_t ds[32];
 #pragma unroll
@@ -450,7 +496,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&ds_full[b]);
       }
       if (!ok) break;
-      if (item_at(n + 1) < total) look_up(n + 1);
+      if (item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
       const bool computed = it.jend > it.jbeg;
       if (computed) {
         ok = mbar_wait(dq_full, static_cast<uint32_t>(no) & 1u, abort_flag, status, tmo);
@@ -461,7 +507,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         ++no;
         tc_fence_after_sync();
       }
-      bool fine = true;
+      float bad = 0.0f;   // becomes NaN with the first value that is not finite
       __nv_bfloat16* out = S.dq + static_cast<int64_t>(i < T ? i : 0) * A.lddq + it.c * D + half * (D / 2);
 #pragma unroll
       for (int u = 0; u < D / 64; ++u) {
@@ -475,7 +521,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const float v = in ? __uint_as_float(o[e]) * A.scale : 0.0f;
-          fine &= fabsf(v) < INFINITY;
+          bad = fmaf(v, 0.0f, bad);
           o[e] = __float_as_uint(v);
         }
         if (i < T) store_bf16x32(out + u * 32, o);
@@ -486,10 +532,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         if (lane == 0) mbar_arrive_relaxed(dq_empty);
       }
       // A row is redone, by the first warpgroup, if either found its half not finite, after both have stored.
-      if (half == 1) flags[r] = in && !fine;
+      const unsigned mine = __ballot_sync(0xffffffffu, in && bad != 0.0f);
+      if (half == 1 && lane == 0) flags[quad] = mine;
       if (!(ok = meet())) break;
       if (half == 0) {
-        const unsigned again = __ballot_sync(0xffffffffu, in && (!fine || flags[r]));
+        const unsigned again = mine | flags[quad];
         if (again) redo_dq<D>(A, it.shard, it.c, it.q0 + quad * 32, again, lane);
       }
     }

@@ -13,18 +13,21 @@
 // 8 above it (in base 2): P then stays below 2^8, which bf16 and the fp32 sums hold as exactly,
 // and the accumulator is rescaled rarely.  The row sum l is taken from the unrounded P.
 //
-// Roles (384 threads, persistent): warp 0 issues the TMA loads (Q_0, Q_1, then K_j, V_j through a ring),
-// warp 1 the MMAs, warps 4..7 and 8..11 are the softmax of tile 0 and 1.  A softmax thread holds a whole
-// row of 128 scores: its warpgroups take 208 registers a thread and the first leaves with 88 (together
-// the 384 x 168 of the launch).  Per tile x the order of MMAs is
-// S_x(j), P_x V(j), S_x(j + 1), and the two tiles alternate, so one tile's softmax runs under the
-// other's products; the next item's first S is issued before this item's epilogue.
+// Roles (384 threads, persistent): warp 0 issues the TMA loads (Q_0, Q_1, then K_j, V_j through a ring), warp 1
+// the MMAs, warps 2 and 3 look up the coming item and the documents of its rows, warps 4..7 and 8..11 are the
+// softmax of tile 0 and 1 and store its result.  A softmax thread holds a whole row of 128 scores: its warpgroups
+// take 208 registers a thread and the first leaves with 88 (together the 384 x 168 of the launch).  Per tile x
+// the order of MMAs is S_x(j), P_x V(j), S_x(j + 1), and the two tiles alternate, so one tile's softmax runs under
+// the other's products; the next item's first S is issued before this item's results are stored.  (A
+// warpgroup of its own for the results was slower: it leaves the softmax 176 registers, and a key tile of one
+// long document then takes 3200 cycles, with 208 it takes 2700.)
 //
 // A masked place enters the product as P = 0, and 0 times an infinite or NaN value is NaN: a row whose
 // result is not finite is computed again by its warp over its own keys alone.
 
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "packed_attn.cuh"
 
@@ -51,7 +54,8 @@ struct FwdCfg {
   static constexpr int KB = D / 64;
   static constexpr int TILE = KB * kTile * 128;   // bytes of a Q, K or V tile
   static constexpr int OFF_RING = 2 * TILE;
-  static constexpr int OFF_BAR = OFF_RING + kRing * TILE;
+  static constexpr int OFF_ROWS = OFF_RING + kRing * TILE;   // RowDocs [2]
+  static constexpr int OFF_BAR = OFF_ROWS + 96;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
 };
@@ -109,6 +113,24 @@ __device__ __forceinline__ Item item_of(const FwdParams& P, int at) {
 
 __device__ __forceinline__ bool active(const QTile& q, int j) { return j >= q.jbeg && j < q.jend; }
 
+// A query tile and the documents of its rows: rows [v0, v1) belong to some; the first of them to one that begins at
+// token lo, and bit r of `begins` is set where another begins at row r.
+struct RowDocs {
+  uint32_t begins[4];
+  int lo, v0, v1;
+  int shard;                   // the tile itself, for the warps that work on it
+  QTile tile;
+};
+static_assert(sizeof(RowDocs) == 48, "two of them in 96 bytes");
+
+// First token of row r's document.
+__device__ __forceinline__ int first_token(const RowDocs& d, int q0, int r) {
+  int w = r >> 5;
+  uint32_t m = d.begins[w] & (0xffffffffu >> (31 - (r & 31)));
+  while (m == 0 && w > 0) m = d.begins[--w];
+  return m ? q0 + w * 32 + 31 - __clz(m) : d.lo;
+}
+
 // Rows whose result is not finite, again from their own keys (kept out of the main loop's registers).
 template <int D>
 __device__ __noinline__ void redo_rows(const PackArgs& A, int shard, int c, int q0, unsigned rows, int lane) {
@@ -126,6 +148,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + C::OFF_RING;
+  RowDocs* docs = reinterpret_cast<RowDocs*>(smem + C::OFF_ROWS);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_empty = q_full + 1;
   uint64_t* ring_full = q_empty + 1;
@@ -133,10 +156,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
   uint64_t* s_full = ring_empty + kRing;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
-  uint64_t* done_bar = o_full + 2;
+  uint64_t* rows_full = o_full + 2;
+  uint64_t* rows_empty = rows_full + 1;
+  uint64_t* done_bar = rows_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 + 2 * kRing + 6 + 1) * 8 + 8 <= 256, "barrier area");
+  static_assert((2 + 2 * kRing + 8 + 1) * 8 + 8 <= 256, "barrier area");
 
   const PackArgs& A = P.a;
   const int warp = uniform_warp();
@@ -163,6 +188,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
       mbar_init(&p_full[x], 4);   // the tile's four softmax warps
       mbar_init(&o_full[x], 1);
     }
+    mbar_init(rows_full, 2);
+    mbar_init(rows_empty, 8);
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -189,7 +216,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
       if (item_at(n + 1) < total) ahead = item_of(P, item_at(n + 1));
       if (it.jhi <= it.jlo) continue;
       if (lane == 0 && ok) {
-        ok = mbar_wait(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
+        auto load = [&](const CUtensorMap* map, int j) {
+          const int slot = pos % kRing;
+          if (!mbar_wait(&ring_empty[slot], (static_cast<uint32_t>(pos / kRing) & 1u) ^ 1u, abort_flag, status, tmo))
+            return false;
+          mbar_arrive_expect_tx(&ring_full[slot], C::TILE);
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_2d(sRing + slot * C::TILE + kb * 16384, map, &ring_full[slot], it.g * D + kb * 64, j * kTile);
+          ++pos;
+          return true;
+        };
+        // the first K does not wait for the item before to be done with Q
+        ok = load(&P.k[it.shard], it.jlo) &&
+             mbar_wait(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
         if (ok) {
           const bool two = it.x[1].jend > it.x[1].jbeg, one = it.x[0].jend > it.x[0].jbeg;
           mbar_arrive_expect_tx(q_full, (two ? C::TILE : 0) + (one ? C::TILE : 0));
@@ -200,16 +239,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
                 tma_load_2d(sQ + x * C::TILE + kb * 16384, &P.q[it.shard], q_full, it.x[x].c * D + kb * 64, it.x[x].q0);
           ++nq;
         }
-        for (int j = it.jlo; ok && j < it.jhi; ++j)
-          for (int v = 0; ok && v < 2; ++v, ++pos) {
-            const int slot = pos % kRing;
-            ok = mbar_wait(&ring_empty[slot], (static_cast<uint32_t>(pos / kRing) & 1u) ^ 1u, abort_flag, status, tmo);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&ring_full[slot], C::TILE);
-            for (int kb = 0; kb < C::KB; ++kb)
-              tma_load_2d(sRing + slot * C::TILE + kb * 16384, v ? &P.v[it.shard] : &P.k[it.shard], &ring_full[slot],
-                          it.g * D + kb * 64, j * kTile);
-          }
+        ok = ok && load(&P.v[it.shard], it.jlo);
+        for (int j = it.jlo + 1; ok && j < it.jhi; ++j) ok = load(&P.k[it.shard], j) && load(&P.v[it.shard], j);
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
     }
@@ -245,8 +276,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     if (item_at(0) < total) ahead = item_of(P, item_at(0));
     for (int n = 0; item_at(n) < total; ++n) {
       const Item it = ahead;
-      if (item_at(n + 1) < total) ahead = item_of(P, item_at(n + 1));
-      if (it.jhi <= it.jlo) continue;
+      if (it.jhi <= it.jlo) {
+        if (item_at(n + 1) < total) ahead = item_of(P, item_at(n + 1));
+        continue;
+      }
       wait(q_full, nq);
       tc_fence_after_sync();
       ++nq;
@@ -291,6 +324,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
           if (j + 2 == it.jhi) umma_commit(q_empty);   // the last S of the item is issued
         }
         __syncwarp();
+        // the coming item is looked up once the first scores run
+        if (j < it.jlo && item_at(n + 1) < total) ahead = item_of(P, item_at(n + 1));
         if (j + 1 < it.jhi) {              // on to K_(j + 2), past V_(j + 1)
           slot += 2;
           if (slot >= kRing) {
@@ -305,7 +340,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     int dummy = 0;
     mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ documents of the rows of tile x
+    const int x = warp - 2;
+    bool ok = true;
+    for (int n = 0; ok && item_at(n) < total; ++n) {
+      const Item it = item_of(P, item_at(n));
+      const QTile qt = x ? it.x[1] : it.x[0];
+      RowDocs d = {{0, 0, 0, 0}, 0, 0, 0, it.shard, qt};
+      if (qt.jend > qt.jbeg) {
+        const int T = static_cast<int>(A.T);
+        const int first = __ldg(A.cu), last = min(__ldg(A.cu + A.batch), T);
+        d.v0 = max(qt.q0, first);
+        d.v1 = min(qt.q0 + kTile, last);
+        d.lo = doc_of(A.cu, A.batch, T, d.v0).lo;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = qt.q0 + u * 32 + lane;
+          const bool begins = i > d.v0 && i < d.v1 && doc_of(A.cu, A.batch, T, i).lo == i;
+          d.begins[u] = __ballot_sync(0xffffffffu, begins);
+        }
+      }
+      ok = mbar_wait(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) docs[x] = d;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rows_full);
+    }
+  } else {
     // ------------------------------------------------------------------ softmax of tile x
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int quad = warp & 3;
@@ -317,26 +379,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     const int T = static_cast<int>(A.T);
     bool ok = true;
     uint32_t ns = 0, no = 0;
-    QTile next_qt = {};
-    int next_shard = 0;
-    DocRange next_doc{0, 0};
-    auto look_up = [&](int n) {                  // the coming item and its rows' documents
-      const Item it = item_of(P, item_at(n));
-      next_qt = x ? it.x[1] : it.x[0];
-      next_shard = it.shard;
-      next_doc = DocRange{0, 0};
-      if (next_qt.jend > next_qt.jbeg) next_doc = doc_of(A.cu, A.batch, T, next_qt.q0 + r);
-    };
-    if (item_at(0) < total) look_up(0);
     for (int n = 0; ok && item_at(n) < total; ++n) {
-      const QTile qt = next_qt;
-      const int shard = next_shard;
-      const DocRange doc = next_doc;
+      ok = mbar_wait(rows_full, static_cast<uint32_t>(n) & 1u, abort_flag, status, tmo);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const QTile qt = docs[x].tile;
+      const int shard = docs[x].shard;
       const PackShard& S = A.s[shard];
       const int i = qt.q0 + r;
-      const bool in = doc.hi > doc.lo;           // a row of a document (so i < T)
-      const int lo = in ? doc.lo : 0x7fffffff, hi = in ? i : -1;      // its keys are lo..hi
+      const bool in = i >= docs[x].v0 && i < docs[x].v1;        // a row of a document (so i < T)
+      const int lo = in ? first_token(docs[x], qt.q0, r) : 0x7fffffff, hi = in ? i : -1;   // it sees the keys lo..hi
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rows_empty);
       const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
+      const int lo_min = __reduce_min_sync(0xffffffffu, lo), hi_max = __reduce_max_sync(0xffffffffu, hi);
       float m = -INFINITY, l = 0.0f;
       for (int j = qt.jbeg; ok && j < qt.jend; ++j) {
         ok = mbar_wait(&s_full[x], ns & 1u, abort_flag, status, tmo);
@@ -346,75 +404,102 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         }
         ++ns;
         tc_fence_after_sync();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) tmem_ld_32x32b_x32(s_col + u * 32, s[u]);
-        tmem_ld_wait();
+        // A tile that every row of the warp sees whole takes straight-line code; else 32 keys at a time, seen by
+        // every row, by some (the others' scores become -inf), or by none (their P is 0 without a look).
         const int k0 = j * kTile;
-        if (k0 < lo_max || k0 + kTile - 1 > hi_min) {   // some row of the warp does not see every key
-          const int a = lo - k0, b = hi - k0;
+        auto tile = [&](auto whole) {
+          constexpr bool WHOLE = decltype(whole)::value;
+          auto live = [&](int) { return true; };
+          uint32_t s[4][32];
+          auto read_scores = [&]() {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u) tmem_ld_32x32b_x32(s_col + u * 32, s[u]);
+            tmem_ld_wait();
+            if (k0 < lo_max || k0 + kTile - 1 > hi_min) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              s[u][e] = (u * 32 + e >= a && u * 32 + e <= b) ? s[u][e] : 0xff800000u;
-        }
-        float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+              for (int u = 0; u < 4; ++u) {
+                const int c0 = k0 + u * 32;
+                if (live(u) && (c0 < lo_max || c0 + 31 > hi_min)) {
+                  const uint32_t see = bits_between(lo - c0, hi - c0);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          x0 = fmax3(x0, __uint_as_float(s[0][e]), __uint_as_float(s[0][e + 1]));
-          x1 = fmax3(x1, __uint_as_float(s[1][e]), __uint_as_float(s[1][e + 1]));
-          x2 = fmax3(x2, __uint_as_float(s[2][e]), __uint_as_float(s[2][e + 1]));
-          x3 = fmax3(x3, __uint_as_float(s[3][e]), __uint_as_float(s[3][e + 1]));
-        }
-        const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * k2;
-        const bool move = mx > m + kLazy || (m == -INFINITY && mx > m);
-        if (__any_sync(0xffffffffu, move)) {
-          const float mn = move ? mx : m;
-          const float f = move ? ex2_approx(m - mn) : 1.0f;
-          l *= f;
-          m = mn;
-          if (j > qt.jbeg) {
-            // O_x holds the products up to key tile j - 1: they were issued before S_x(j), which is complete.
-            for (int u = 0; u < D / 32; ++u) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(o_col + u * 32, o);
-              tmem_ld_wait();
+                  for (int e = 0; e < 32; ++e) s[u][e] = (see >> e) & 1u ? s[u][e] : 0xff800000u;
+                }
+              }
+            }
+          };
+          read_scores();
+          float mxs[4];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st_32x32b_x32(o_col + u * 32, o);
+          for (int u = 0; u < 4; ++u) {
+            mxs[u] = -INFINITY;
+            if (live(u)) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                mxs[u] = fmax3(mxs[u], __uint_as_float(s[u][e]), __uint_as_float(s[u][e + 1]));
             }
           }
-        }
-        const float nm = m == -INFINITY ? 0.0f : -m;
-        const uint64_t kk2 = f2_pack(k2, k2), nm2 = f2_pack(nm, nm);
-        uint64_t sum0 = 0, sum1 = 0;
+          const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * k2;
+          const bool move = mx > m + kLazy || (m == -INFINITY && mx > m);
+          if (__any_sync(0xffffffffu, move)) {
+            const float mn = move ? mx : m;
+            const float f = move ? ex2_approx(m - mn) : 1.0f;
+            l *= f;
+            m = mn;
+            if (j > qt.jbeg) {
+              // O_x holds the products up to key tile j - 1: they were issued before S_x(j), which is complete.
+#pragma unroll 1
+              for (int u = 0; u < D / 32; ++u) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(o_col + u * 32, o);
+                tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 a = f2_unpack(ffma2(f2_pack(__uint_as_float(s[2 * h][e]), __uint_as_float(s[2 * h][e + 1])), kk2, nm2));
-            const float2 b =
-                f2_unpack(ffma2(f2_pack(__uint_as_float(s[2 * h + 1][e]), __uint_as_float(s[2 * h + 1][e + 1])), kk2, nm2));
-            const float a0 = ex2_approx(a.x), a1 = ex2_approx(a.y), b0 = ex2_approx(b.x), b1 = ex2_approx(b.y);
-            sum0 = fadd2(sum0, f2_pack(a0, a1));
-            sum1 = fadd2(sum1, f2_pack(b0, b1));
-            p[e >> 1] = pack_bf16x2(a0, a1);
-            p[16 + (e >> 1)] = pack_bf16x2(b0, b1);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st_32x32b_x32(o_col + u * 32, o);
+              }
+              read_scores();   // again: their registers are O's meanwhile
+            }
           }
-          tmem_st_32x32b_x32(s_col + h * 32, p);
-        }
-        const float2 t0 = f2_unpack(sum0), t1 = f2_unpack(sum1);
-        l += (t0.x + t0.y) + (t1.x + t1.y);
+          const float nm = m == -INFINITY ? 0.0f : -m;
+          const uint64_t kk2 = f2_pack(k2, k2), nm2 = f2_pack(nm, nm);
+          uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              if (live(2 * h + q)) {
+                const uint32_t(&c)[32] = s[2 * h + q];
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const float2 a = f2_unpack(ffma2(f2_pack(__uint_as_float(c[e]), __uint_as_float(c[e + 1])), kk2, nm2));
+                  const float2 b =
+                      f2_unpack(ffma2(f2_pack(__uint_as_float(c[e + 2]), __uint_as_float(c[e + 3])), kk2, nm2));
+                  const float a0 = ex2_approx(a.x), a1 = ex2_approx(a.y), b0 = ex2_approx(b.x), b1 = ex2_approx(b.y);
+                  sum0 = fadd2(sum0, f2_pack(a0, a1));
+                  sum1 = fadd2(sum1, f2_pack(b0, b1));
+                  p[q * 16 + (e >> 1)] = pack_bf16x2(a0, a1);
+                  p[q * 16 + (e >> 1) + 1] = pack_bf16x2(b0, b1);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) p[q * 16 + e] = 0;
+              }
+            }
+            tmem_st_32x32b_x32(s_col + h * 32, p);
+          }
+          const float2 t0 = f2_unpack(sum0), t1 = f2_unpack(sum1);
+          l += (t0.x + t0.y) + (t1.x + t1.y);
+        };
+        tile(std::false_type{});
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
-      // ---- the row's result; its last product is running
-      if (item_at(n + 1) < total) look_up(n + 1);
+      // ---- the row's result
+      if (i < T) S.lse[static_cast<int64_t>(qt.c) * A.T + i] = in ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      const float inv = in ? 1.0f / l : 0.0f;
       const bool computed = qt.jend > qt.jbeg;
       if (computed) {
         ok = mbar_wait(&o_full[x], no & 1u, abort_flag, status, tmo);
@@ -425,33 +510,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         ++no;
         tc_fence_after_sync();
       }
-      const float inv = in ? 1.0f / l : 0.0f;
-      bool fine = true;
+      float bad = 0.0f;   // becomes NaN with the first value that is not finite
       __nv_bfloat16* out = S.o + static_cast<int64_t>(i < T ? i : 0) * A.ldo + qt.c * D;
 #pragma unroll
-      for (int u = 0; u < D / 32; ++u) {
-        uint32_t o[32];
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t o[2][32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0;
+        for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = 0;
         if (computed) {
-          tmem_ld_32x32b_x32(o_col + u * 32, o);
+          tmem_ld_32x32b_x32(o_col + h * 64, o[0]);
+          tmem_ld_32x32b_x32(o_col + h * 64 + 32, o[1]);
           tmem_ld_wait();
         }
-        if (!in) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0;
-        }
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float v = __uint_as_float(o[e]) * inv;
-          fine &= fabsf(v) < INFINITY;
-          o[e] = __float_as_uint(v);
+          for (int e = 0; e < 32; ++e) {
+            const float v = in ? __uint_as_float(o[u][e]) * inv : 0.0f;
+            bad = fmaf(v, 0.0f, bad);
+            o[u][e] = __float_as_uint(v);
+          }
+          if (i < T) store_bf16x32(out + h * 64 + u * 32, o[u]);
         }
-        if (i < T) store_bf16x32(out + u * 32, o);
       }
       tc_fence_before_sync();
-      if (i < T) S.lse[static_cast<int64_t>(qt.c) * A.T + i] = in ? (m + __log2f(l)) * kLn2 : -INFINITY;
-      const unsigned again = __ballot_sync(0xffffffffu, in && !fine);
+      const unsigned again = __ballot_sync(0xffffffffu, in && bad != 0.0f);
       __syncwarp();   // the rows' stores above come before those of the redo
       if (again) redo_rows<D>(A, shard, qt.c, qt.q0 + quad * 32, again, lane);
     }
