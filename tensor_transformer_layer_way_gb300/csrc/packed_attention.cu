@@ -195,10 +195,10 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
   const int64_t tiles = tiles_of(T);
   const bool split = pack_split(tiles, n_kv, A.grp);
   const bool listed = split || tiles * n_q > num_sms();
+  PackPlan plan = {};
   if (listed) {
     const BwdWs w = bwd_ws(T, n_q, n_kv, d);
     char* base = reinterpret_cast<char*>(A.D);
-    PackPlan plan = {};
     plan.q_list = reinterpret_cast<int4*>(base + w.q_list);
     plan.q_units = plan.tiles = static_cast<int>(tiles);
     plan.q_per = 1;
@@ -207,13 +207,12 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
     plan.join_list = reinterpret_cast<int4*>(base + w.join);
     plan.lanes = n_kv;
     plan.split = split;
-    if ((rc = pack_attn_plan_launch(A, plan, s))) return rc;
     A.q_list = plan.q_list;
     A.kv_list = plan.kv_list;
     A.kv_head = plan.kv_head;
     A.join_list = plan.join_list;
     A.part = reinterpret_cast<float*>(base + w.part);
   }
-  if ((rc = pack_attn_dq_launch(A, d, s)) || (rc = pack_attn_dkv_launch(A, d, s))) return rc;
+  if ((rc = pack_attn_plan_launch(A, plan, d, s)) || (rc = pack_attn_dq_launch(A, d, s)) || (rc = pack_attn_dkv_launch(A, d, s))) return rc;
   return split ? pack_attn_join_launch(A, d, s) : TTL_OK;
 }

@@ -56,7 +56,8 @@ struct PackPlan {
 };
 constexpr int kSplitItems = 456;   // items a cut aims at in all: three for each of 152 SMs
 constexpr int kSplitSteps = 8;     // and no shorter than this
-int pack_attn_plan_launch(const PackArgs& A, const PackPlan& plan, cudaStream_t stream);
+// d > 0: the launch also takes A.D.
+int pack_attn_plan_launch(const PackArgs& A, const PackPlan& plan, int d, cudaStream_t stream);
 int pack_attn_join_launch(const PackArgs& A, int d, cudaStream_t stream);
 // Whether key tiles may be cut: few items, and long enough ones.  With eight items or more for each SM the
 // list's order alone evens the SMs out.
@@ -71,7 +72,7 @@ int set_core_smem_once(const void* fn, int slot, int bytes, const char* what);
 // Launches of the tensor-core kernels (arguments are checked; A.s holds every pointer they need).
 // `list`: room for one word of 16 bytes per 128 tokens.
 int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stream);
-int pack_attn_dq_launch(const PackArgs& A, int d, cudaStream_t stream);    // dQ and D
+int pack_attn_dq_launch(const PackArgs& A, int d, cudaStream_t stream);    // dQ, after D
 int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream);   // dK and dV, after D
 
 constexpr int kTile = 128;       // tokens per query or key tile
@@ -120,6 +121,38 @@ __device__ __forceinline__ void check_docs(const int32_t* cu, int batch, int64_t
     bad |= c < 0 || c > T || (b > 0 && __ldg(cu + b - 1) > c);
   }
   if (bad) atomicCAS(status, 0, TTL_ERR_DEVICE);
+}
+
+// mbar_wait with its polling loop out of line: these kernels wait in some thirty places, and the loop's code
+// in each of them would crowd the instruction cache at every change of item.
+static __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
+                                                uint64_t timeout_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity)
+          : "memory");
+      if (ok) return true;
+    }
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > timeout_ns) {
+      if (status) atomicCAS(status, 0, TTL_ERR_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
+                                        uint64_t timeout_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_longer(smem_u32(bar), parity, abort, status, timeout_ns);
 }
 
 // The warp's index as a value the compiler knows to be the same in all lanes: descriptors computed from it and
@@ -243,17 +276,16 @@ __device__ __forceinline__ void fwd_row(const PackArgs& A, const PackShard& S, i
   if (lane == 0) S.lse[static_cast<int64_t>(c) * A.T + i] = lse;
 }
 
-// dq_i of query head c, and D_i = do_i . o_i.
+// dq_i of query head c.
 template <int D>
 __device__ __forceinline__ void dq_row(const PackArgs& A, const PackShard& S, int shard, int c, int i, DocRange doc,
                                        int lane) {
   const int g = c / A.grp;
   RowVec<D> acc = row_zero<D>();
-  float Di = 0.0f;
   if (doc.hi > doc.lo) {
     const RowVec<D> q = row_load<D>(S.q + i * A.ldq + c * D, lane);
     const RowVec<D> go = row_load<D>(S.dO + i * A.lddo + c * D, lane);
-    Di = row_dot(go, row_load<D>(S.o + i * A.ldo + c * D, lane));
+    const float Di = A.D[(static_cast<int64_t>(shard) * A.nql + c) * A.T + i];
     const float k2 = A.scale * kLog2e, lse2 = S.lse[static_cast<int64_t>(c) * A.T + i] * kLog2e;
     for (int j = doc.lo; j <= i; ++j) {
       const RowVec<D> k = row_load<D>(S.k + j * A.ldk + g * D, lane);
@@ -265,7 +297,6 @@ __device__ __forceinline__ void dq_row(const PackArgs& A, const PackShard& S, in
     }
   }
   row_store<D>(S.dq + i * A.lddq + c * D, acc, lane);
-  if (lane == 0) A.D[(static_cast<int64_t>(shard) * A.nql + c) * A.T + i] = Di;
 }
 
 // dk_j (want_k) or dv_j of KV head g, summed over the group's query heads.

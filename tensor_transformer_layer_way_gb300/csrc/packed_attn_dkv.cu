@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       if (it.steps == 0) continue;
       if (lane == 0 && ok) {
         auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint32_t phase, int x, int y) {
-          if (!mbar_wait(empty, (phase & 1u) ^ 1u, abort_flag, status, tmo)) return false;
+          if (!wait_on(empty, (phase & 1u) ^ 1u, abort_flag, status, tmo)) return false;
           mbar_arrive_expect_tx(full, C::TILE);
           for (int kb = 0; kb < C::KB; ++kb) tma_load_2d(dst + kb * 16384, map, full, x + kb * 64, y);
           return true;
@@ -230,12 +230,12 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       // No copy may still be landing when the CTA leaves: wait (bounded) for the last loads.
       int dummy = 0;
       volatile int* da = reinterpret_cast<volatile int*>(&dummy);
-      if (nk > 0) mbar_wait(k_full, static_cast<uint32_t>(nk - 1) & 1u, da, status, tmo);
-      if (nv > 0) mbar_wait(v_full, static_cast<uint32_t>(nv - 1) & 1u, da, status, tmo);
+      if (nk > 0) wait_on(k_full, static_cast<uint32_t>(nk - 1) & 1u, da, status, tmo);
+      if (nv > 0) wait_on(v_full, static_cast<uint32_t>(nv - 1) & 1u, da, status, tmo);
       for (int i = nq > kSlots ? nq - kSlots : 0; i < nq; ++i)
-        mbar_wait(&q_full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u, da, status, tmo);
+        wait_on(&q_full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u, da, status, tmo);
       for (int i = nd > kSlots ? nd - kSlots : 0; i < nd; ++i)
-        mbar_wait(&do_full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u, da, status, tmo);
+        wait_on(&do_full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u, da, status, tmo);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     static_assert(kSlots == 2, "the Q and dO places are the parity of the step");
     const bool leader = elect_one();
     auto wait = [&](uint64_t* bar, int phase) {
-      mbar_wait(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
+      wait_on(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
     };
     // [keys x queries] = A B^T, both K-major tiles of D columns
     auto scores = [&](uint32_t dst, uint64_t ad, uint64_t bd) {
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     if (leader) umma_commit(done_bar);   // every MMA issued here must finish before TMEM is released
     __syncwarp();
     int dummy = 0;
-    mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
+    wait_on(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ lse and D of each step's queries
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           a[u] = q < A.T ? -__ldg(lse + row + q) * kLog2e : 0.0f;
           b[u] = q < A.T ? -__ldg(Dr + row + q) : 0.0f;
         }
-        ok = mbar_wait(&st_empty[st], (static_cast<uint32_t>(pos / kStat) & 1u) ^ 1u, abort_flag, status, tmo);
+        ok = wait_on(&st_empty[st], (static_cast<uint32_t>(pos / kStat) & 1u) ^ 1u, abort_flag, status, tmo);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         if (it.steps > 0) doc = doc_of(A.cu, A.batch, static_cast<int>(A.T), it.k0 + u * 32 + lane);
         hi[u] = doc.hi > doc.lo ? doc.hi - 1 : -1;   // a token of no document is seen by none
       }
-      ok = mbar_wait(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
+      ok = wait_on(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
       if (!__all_sync(0xffffffffu, ok)) break;
 #pragma unroll
       for (int u = 0; u < 4; ++u) row_hi[u * 32 + lane] = hi[u];

@@ -1,4 +1,4 @@
-// dQ of packed causal attention on the tensor cores, and D = rowsum(dO O) for the dK and dV kernel.
+// dQ of packed causal attention on the tensor cores.
 //
 // One work item is a 128-token query tile of one head; its key tiles are those of the forward kernel.
 // Per key tile:  S = Q K^T and dP = dO V^T (fp32, tensor memory), P = 2^(s k - lse), dS = P (dP - D) as
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
       if (item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
       if (it.jend <= it.jbeg) continue;
       if (lane == 0 && ok) {
-        ok = mbar_wait(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
+        ok = wait_on(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
         if (ok) {
           mbar_arrive_expect_tx(q_full, 2 * C::TILE);
           for (int kb = 0; kb < C::KB; ++kb) {
@@ -199,16 +199,16 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         }
         for (int j = it.jbeg; ok && j < it.jend; ++j, ++pos) {
           const int ks = pos % kKSlots, vs = pos % kVSlots;
-          ok = mbar_wait(&k_empty[ks], (static_cast<uint32_t>(pos / kKSlots) & 1u) ^ 1u, abort_flag, status, tmo);
+          ok = wait_on(&k_empty[ks], (static_cast<uint32_t>(pos / kKSlots) & 1u) ^ 1u, abort_flag, status, tmo);
           if (!ok) break;
           mbar_arrive_expect_tx(&k_full[ks], C::TILE);
           for (int kb = 0; kb < C::KB; ++kb)
             tma_load_2d(sK + ks * C::TILE + kb * 16384, &P.k[it.shard], &k_full[ks], it.g * D + kb * 64, j * kTile);
           // (K was started: from here the position counts as started even if the wait for V fails)
-          ok = mbar_wait(&v_empty[vs], (static_cast<uint32_t>(pos / kVSlots) & 1u) ^ 1u, abort_flag, status, tmo);
+          ok = wait_on(&v_empty[vs], (static_cast<uint32_t>(pos / kVSlots) & 1u) ^ 1u, abort_flag, status, tmo);
           if (!ok) {
             int dummy = 0;
-            mbar_wait(&k_full[ks], static_cast<uint32_t>(pos / kKSlots) & 1u, reinterpret_cast<volatile int*>(&dummy),
+            wait_on(&k_full[ks], static_cast<uint32_t>(pos / kKSlots) & 1u, reinterpret_cast<volatile int*>(&dummy),
                       status, tmo);
             break;
           }
@@ -223,11 +223,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
       // No copy may still be landing when the CTA leaves: wait (bounded) for the last loads.
       int dummy = 0;
       volatile int* da = reinterpret_cast<volatile int*>(&dummy);
-      if (nq > 0) mbar_wait(q_full, static_cast<uint32_t>(nq - 1) & 1u, da, status, tmo);
+      if (nq > 0) wait_on(q_full, static_cast<uint32_t>(nq - 1) & 1u, da, status, tmo);
       for (int i = pos > kKSlots ? pos - kKSlots : 0; i < pos; ++i)
-        mbar_wait(&k_full[i % kKSlots], static_cast<uint32_t>(i / kKSlots) & 1u, da, status, tmo);
+        wait_on(&k_full[i % kKSlots], static_cast<uint32_t>(i / kKSlots) & 1u, da, status, tmo);
       for (int i = pos > kVSlots ? pos - kVSlots : 0; i < pos; ++i)
-        mbar_wait(&v_full[i % kVSlots], static_cast<uint32_t>(i / kVSlots) & 1u, da, status, tmo);
+        wait_on(&v_full[i % kVSlots], static_cast<uint32_t>(i / kVSlots) & 1u, da, status, tmo);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     static_assert(kVSlots == 2, "the V place is the parity of the key tile");
     const bool leader = elect_one();
     auto wait = [&](uint64_t* bar, int phase) {
-      mbar_wait(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
+      wait_on(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
     };
     DqItem ahead = {};
     if (item_at(0) < total) ahead = dq_item(P, item_at(0));
@@ -327,20 +327,18 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     if (leader) umma_commit(done_bar);   // every MMA issued here must finish before TMEM is released
     __syncwarp();
     int dummy = 0;
-    mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
+    wait_on(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
     __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------------ lse, D and first keys of 64 rows
     const int r0 = (warp - 2) * 64;
     const int T = static_cast<int>(A.T);
-    constexpr int LANES = D / 8;                 // lanes that hold a row (16 bytes each)
-    constexpr int ROWS = 32 / LANES;             // rows a warp reads at a time
     bool ok = true;
     for (int n = 0; ok && item_at(n) < total; ++n) {
       const DqItem it = dq_item(P, item_at(n));
       const PackShard& S = A.s[it.shard];
       int lo[2];
-      float nl[2], Dr[2] = {0.0f, 0.0f};
+      float nl[2], Dr[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int i = it.q0 + r0 + u * 32 + lane;
@@ -348,36 +346,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         if (it.jend > it.jbeg) doc = doc_of(A.cu, A.batch, T, i);
         const bool in = doc.hi > doc.lo;
         lo[u] = in ? doc.lo : 0x7fffffff;        // a token of no document has no keys
-        nl[u] = in ? -__ldg(S.lse + static_cast<int64_t>(it.c) * A.T + i) * kLog2e : 0.0f;
+        const int64_t row = static_cast<int64_t>(it.c) * A.T + i;
+        nl[u] = in ? -__ldg(S.lse + row) * kLog2e : 0.0f;
+        Dr[u] = in ? __ldg(A.D + static_cast<int64_t>(it.shard) * A.nql * A.T + row) : 0.0f;
       }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll 4
-        for (int q = 0; q < 32; q += ROWS) {
-          const int i = it.q0 + r0 + u * 32 + q + lane / LANES;
-          float d = 0.0f;
-          if (i < T) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(S.dO + i * A.lddo + it.c * D) + lane % LANES);
-            const uint4 b = __ldg(reinterpret_cast<const uint4*>(S.o + i * A.ldo + it.c * D) + lane % LANES);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int w = 0; w < 4; ++w) d = fmaf(bf16_lo(aw[w]), bf16_lo(bw[w]), fmaf(bf16_hi(aw[w]), bf16_hi(bw[w]), d));
-          }
-#pragma unroll
-          for (int o = LANES / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-#pragma unroll
-          for (int k = 0; k < ROWS; ++k) {       // to the lane whose row it is
-            const float v = __shfl_sync(0xffffffffu, d, k * LANES);
-            if (lane == q + k) Dr[u] = v;
-          }
-        }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = it.q0 + r0 + u * 32 + lane;
-        if (lo[u] == 0x7fffffff) Dr[u] = 0.0f;
-        if (i < T) A.D[(static_cast<int64_t>(it.shard) * A.nql + it.c) * A.T + i] = Dr[u];
-      }
-      ok = mbar_wait(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
+      ok = wait_on(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
       if (!__all_sync(0xffffffffu, ok)) break;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {

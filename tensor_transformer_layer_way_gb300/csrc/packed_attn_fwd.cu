@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
       if (lane == 0 && ok) {
         auto load = [&](const CUtensorMap* map, int j) {
           const int slot = pos % kRing;
-          if (!mbar_wait(&ring_empty[slot], (static_cast<uint32_t>(pos / kRing) & 1u) ^ 1u, abort_flag, status, tmo))
+          if (!wait_on(&ring_empty[slot], (static_cast<uint32_t>(pos / kRing) & 1u) ^ 1u, abort_flag, status, tmo))
             return false;
           mbar_arrive_expect_tx(&ring_full[slot], C::TILE);
           for (int kb = 0; kb < C::KB; ++kb)
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         };
         // the first K does not wait for the item before to be done with Q
         ok = load(&P.k[it.shard], it.jlo) &&
-             mbar_wait(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
+             wait_on(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
         if (ok) {
           const bool two = it.x[1].jend > it.x[1].jbeg, one = it.x[0].jend > it.x[0].jbeg;
           mbar_arrive_expect_tx(q_full, (two ? C::TILE : 0) + (one ? C::TILE : 0));
@@ -248,10 +248,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
       // No copy may still be landing when the CTA leaves: wait (bounded) for the last loads.
       int dummy = 0;
       volatile int* da = reinterpret_cast<volatile int*>(&dummy);
-      if (nq > 0) mbar_wait(q_full, static_cast<uint32_t>(nq - 1) & 1u, da, status, tmo);
+      if (nq > 0) wait_on(q_full, static_cast<uint32_t>(nq - 1) & 1u, da, status, tmo);
       const int pending = pos < kRing ? pos : kRing;
       for (int i = pos - pending; i < pos; ++i)
-        mbar_wait(&ring_full[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, da, status, tmo);
+        wait_on(&ring_full[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, da, status, tmo);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     const uint32_t idesc_o = idesc_bf16_f32(kTile, D, false, true);
     const bool leader = elect_one();
     auto wait = [&](uint64_t* bar, int phase) {
-      mbar_wait(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
+      wait_on(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
     };
     Item ahead = {};
     if (item_at(0) < total) ahead = item_of(P, item_at(0));
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     if (leader) umma_commit(done_bar);   // every MMA issued here must finish before TMEM is released
     __syncwarp();
     int dummy = 0;
-    mbar_wait(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
+    wait_on(done_bar, 0, reinterpret_cast<volatile int*>(&dummy), status, tmo);
     __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------------ documents of the rows of tile x
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
           d.begins[u] = __ballot_sync(0xffffffffu, begins);
         }
       }
-      ok = mbar_wait(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
+      ok = wait_on(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) docs[x] = d;
       __syncwarp();
@@ -409,13 +409,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         const int k0 = j * kTile;
         auto tile = [&](auto whole) {
           constexpr bool WHOLE = decltype(whole)::value;
-          auto live = [&](int) { return true; };
+          auto live = [&](int u) { return WHOLE || (k0 + u * 32 <= hi_max && k0 + u * 32 + 31 >= lo_min); };
           uint32_t s[4][32];
           auto read_scores = [&]() {
 #pragma unroll
             for (int u = 0; u < 4; ++u) tmem_ld_32x32b_x32(s_col + u * 32, s[u]);
             tmem_ld_wait();
-            if (k0 < lo_max || k0 + kTile - 1 > hi_min) {
+            if constexpr (!WHOLE) {
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
                 const int c0 = k0 + u * 32;
@@ -490,7 +490,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
           const float2 t0 = f2_unpack(sum0), t1 = f2_unpack(sum1);
           l += (t0.x + t0.y) + (t1.x + t1.y);
         };
-        tile(std::false_type{});
+        if (k0 < lo_max || k0 + kTile - 1 > hi_min) tile(std::false_type{});
+        else tile(std::true_type{});
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
@@ -589,7 +590,7 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stre
     plan.q_list = static_cast<int4*>(list);
     plan.q_units = P.units;
     plan.q_per = P.pair_heads ? 1 : 2;
-    if ((rc = pack_attn_plan_launch(A, plan, stream))) return rc;
+    if ((rc = pack_attn_plan_launch(A, plan, 0, stream))) return rc;
     P.a.q_list = plan.q_list;
   }
   const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device

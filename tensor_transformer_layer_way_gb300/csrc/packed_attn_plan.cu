@@ -3,8 +3,9 @@
 // A query tile's work is the number of key tiles it meets, a key tile's the number of (query tile, head) steps;
 // both depend on the documents, which only the device knows.  One CTA sorts the tiles by work, heaviest first
 // (a counting sort; tiles of equal work in any order), so that the persistent kernels, which take items in
-// turn, end together, and cuts the longest key tiles into several items where there are few.  Worth one small
-// launch only when there are more items than SMs; below that every item starts at once.
+// turn, end together, and cuts the longest key tiles into several items where there are few.  Worth it only
+// when there are more items than SMs; below that every item starts at once.  The backward pass's launch also takes
+// D = rowsum(dO o) of every row and head, in the other CTAs: the sort is hidden under it.
 
 #include "packed_attn.cuh"
 
@@ -61,14 +62,39 @@ __device__ __forceinline__ int work_class(int work, int shift) {
   return c < kPlanThreads ? c : kPlanThreads - 1;
 }
 
+// D of one token of one shard, all its heads, by a warp: 256 columns at a time, d / 8 lanes for each head.
+__device__ __forceinline__ void row_dots(const PackArgs& A, int shard, int64_t i, int d) {
+  const int lane = threadIdx.x & 31;
+  const PackShard& S = A.s[shard];
+  const int cols = A.nql * d, lph = d / 8;
+  for (int base = 0; base < cols; base += 256) {
+    const int c = base + lane * 8;
+    float acc = 0.0f;
+    if (c < cols) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(S.dO + i * A.lddo + c));
+      const uint4 b = __ldg(reinterpret_cast<const uint4*>(S.o + i * A.ldo + c));
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) acc = fmaf(bf16_lo(aw[w]), bf16_lo(bw[w]), fmaf(bf16_hi(aw[w]), bf16_hi(bw[w]), acc));
+    }
+    for (int o = lph >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (c < cols && (lane & (lph - 1)) == 0) A.D[(static_cast<int64_t>(shard) * A.nql + c / d) * A.T + i] = acc;
+  }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_constant__ PackArgs A,
                                                                  const __grid_constant__ PackPlan P, int q_shift,
-                                                                 int kv_shift) {
+                                                                 int kv_shift, int d) {
   __shared__ int hist[kPlanThreads];
   __shared__ int warp_tot[32];
   __shared__ unsigned long long total;
   __shared__ int taken, joins;
   const int tid = threadIdx.x;
+  if (blockIdx.x > 0) {
+    const int64_t w = static_cast<int64_t>(blockIdx.x - 1) * (kPlanThreads / 32) + (tid >> 5);
+    if (w < A.t * A.T) row_dots(A, static_cast<int>(w / A.T), w % A.T, d);
+    return;
+  }
   if (P.q_list) {
     hist[tid] = 0;
     __syncthreads();
@@ -147,13 +173,16 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
 
 }  // namespace
 
-int pack_attn_plan_launch(const PackArgs& A, const PackPlan& plan, cudaStream_t stream) {
+int pack_attn_plan_launch(const PackArgs& A, const PackPlan& plan, int d, cudaStream_t stream) {
   const int tiles = static_cast<int>((A.T + kTile - 1) / kTile);
   int q_shift = 0, kv_shift = 0;
   while ((2 * static_cast<int64_t>(tiles) >> q_shift) >= kPlanThreads) ++q_shift;
   while ((static_cast<int64_t>(tiles) * A.grp >> kv_shift) >= kPlanThreads) ++kv_shift;
-  TraceScope trace(stream, TTL_K_OTHER, 0.0, 32.0 * tiles);
-  pack_plan_kernel<<<1, kPlanThreads, 0, stream>>>(A, plan, q_shift, kv_shift);
+  // d > 0: with D, one warp per (shard, token)
+  const int64_t rows = d > 0 ? A.t * A.T : 0;
+  TraceScope trace(stream, TTL_K_OTHER, 0.0, 32.0 * tiles + 4.0 * rows * A.nql * d);
+  const unsigned grid = 1 + static_cast<unsigned>((rows + kPlanThreads / 32 - 1) / (kPlanThreads / 32));
+  pack_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(A, plan, q_shift, kv_shift, d);
   return cuda_check(cudaGetLastError(), "pack_plan_kernel launch");
 }
 
