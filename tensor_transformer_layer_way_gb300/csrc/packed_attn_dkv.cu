@@ -13,8 +13,10 @@
 // tensor pipe busy: S(n+1), dK(n), dP(n+1), dV(n+1), S(n+2), ...  While the elementwise warps turn S(n+1)
 // into P, dK(n) and dP(n+1) run; while they form dS(n+1), dV(n+1) and S(n+2) do.
 //
-// Roles (384 threads, persistent): warp 0 the TMA loads, warp 1 the MMAs, warp 2 brings each step's lse and D
-// to shared memory, warp 3 the documents of the coming item's keys, warps 4..11 the elementwise work: a key row per thread, each warpgroup on 64 of the queries.
+// Roles (640 threads, persistent): warp 0 the TMA loads, warp 1 the MMAs, warp 2 brings each step's lse and D to
+// shared memory, warp 3 the documents of the coming item's keys, warps 4..19 the elementwise work: a key row per
+// thread, each of the four warpgroups on 32 of the queries (on 64 each, two warpgroups took 1450 cycles from
+// S to P, longer than dK and dP run).
 
 #include <cstring>
 
@@ -23,7 +25,8 @@
 namespace ttl {
 namespace {
 
-constexpr int kKvThreads = 384;
+constexpr int kKvThreads = 640;
+constexpr int kKvWarps = 16;   // elementwise warps
 constexpr int kSlots = 2;      // Q and dO tiles
 constexpr int kStat = 2;       // lse and D stages
 
@@ -130,10 +133,12 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   uint64_t* acc_full = ds_full + 1;
   uint64_t* rows_full = acc_full + 1;
   uint64_t* rows_empty = rows_full + 1;
-  uint64_t* done_bar = rows_empty + 1;
+  uint64_t* x_bar = rows_empty + 1;    // the elementwise warps meet
+  uint64_t* done_bar = x_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((4 + 4 * kSlots + 2 * kStat + 8) * 8 + 8 <= 256, "barrier area");
+  uint32_t* flags = tmem_slot + 2;     // [2][4]: rows of a quadrant to be done again, of dK and of dV
+  static_assert((4 + 4 * kSlots + 2 * kStat + 9) * 8 + 40 <= 256, "barrier area");
   constexpr uint32_t T_DP = 128, T_DK = 256, T_DV = 384;
 
   const PackArgs& A = P.a;
@@ -163,16 +168,18 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     }
     for (int s = 0; s < kStat; ++s) {
       mbar_init(&st_full[s], 1);
-      mbar_init(&st_empty[s], 8);
+      mbar_init(&st_empty[s], kKvWarps);
     }
     mbar_init(s_full, 1);
-    mbar_init(p_full, 8);
+    mbar_init(p_full, kKvWarps);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
+    mbar_init(ds_full, kKvWarps);
     mbar_init(acc_full, 1);
     mbar_init(rows_full, 1);
-    mbar_init(rows_empty, 8);
+    mbar_init(rows_empty, kKvWarps);
+    mbar_init(x_bar, kKvWarps);
     mbar_init(done_bar, 1);
+    for (int q = 0; q < 8; ++q) flags[q] = 0;
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -263,11 +270,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           umma_bf16(dst, desc_advance(ad, kb * 16384 + kk * 32), desc_advance(bd, kb * 16384 + kk * 32), idesc_s,
                     (kb | kk) ? 1u : 0u);
     };
-    // [keys x D] += A B: A from tensor memory (queries [64 w, 64 w + 64) at columns 64 w ..), B read MN-major
+    // [keys x D] += A B: A from tensor memory (queries [32 w, 32 w + 32) at columns 32 w ..), B read MN-major
     auto sum = [&](uint32_t dst, uint32_t acol, uint64_t bd, uint32_t more) {
 #pragma unroll
       for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_bf16_ts(dst, acol + (kk >> 2) * 64 + (kk & 3) * 8, desc_advance(bd, kk * 2048), idesc_acc, kk ? 1u : more);
+        umma_bf16_ts(dst, acol + (kk >> 1) * 32 + (kk & 1) * 8, desc_advance(bd, kk * 2048), idesc_acc, kk ? 1u : more);
     };
     KvItem ahead = {};
     if (item_at(0) < total) ahead = kv_item(P, item_at(0));
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   } else {
     // ------------------------------------------------------------------ P^T and dS^T
     const int quad = warp & 3;
-    const int half = (warp - 4) >> 2;
+    const int w = (warp - 4) >> 2;             // queries [32 w, 32 w + 32) of each tile
     const int r = quad * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float k2 = A.scale * kLog2e;
@@ -395,6 +402,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     const int T = static_cast<int>(A.T);
     bool ok = true;
     int pos = 0, ni = 0;
+    uint32_t met = 0;
     KvItem ahead = {};
     if (item_at(0) < total) ahead = kv_item(P, item_at(0));
     for (int n = 0; ok && item_at(n) < total; ++n) {
@@ -414,10 +422,10 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
       for (int t = 0; ok && t < it.steps; ++t, ++pos) {
         const int st = pos % kStat;
-        const int q0 = step_q0(it, t) + half * 64;
-        const bool masked = q0 < lo_max || q0 + 63 > hi_min;
-        const float4* nl = reinterpret_cast<const float4*>(stat + st * 256 + half * 64);
-        const float4* nD = reinterpret_cast<const float4*>(stat + st * 256 + 128 + half * 64);
+        const int q0 = step_q0(it, t) + w * 32;
+        const bool masked = q0 < lo_max || q0 + 31 > hi_min;
+        const float4* nl = reinterpret_cast<const float4*>(stat + st * 256 + w * 32);
+        const float4* nD = reinterpret_cast<const float4*>(stat + st * 256 + 128 + w * 32);
         ok = mbar_wait(&st_full[st], static_cast<uint32_t>(pos / kStat) & 1u, abort_flag, status, tmo) &&
              mbar_wait(s_full, static_cast<uint32_t>(pos) & 1u, abort_flag, status, tmo);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -425,38 +433,33 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           break;
         }
         tc_fence_after_sync();
-        uint32_t s[2][32];
-        tmem_ld_32x32b_x32(lane_base + half * 64, s[0]);
-        tmem_ld_32x32b_x32(lane_base + half * 64 + 32, s[1]);
+        uint32_t s[32];
+        tmem_ld_32x32b_x32(lane_base + w * 32, s);
         tmem_ld_wait();
-        const uint32_t see[2] = {bits_between(lo - q0, hi - q0), bits_between(lo - q0 - 32, hi - q0 - 32)};
-        uint32_t pk[32];
+        uint32_t pk[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 n4 = nl[(h * 32 + e) >> 2];
-            const float2 u = f2_unpack(
-                ffma2(f2_pack(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1])), kk2, f2_pack(n4.x, n4.y)));
-            const float2 w = f2_unpack(
-                ffma2(f2_pack(__uint_as_float(s[h][e + 2]), __uint_as_float(s[h][e + 3])), kk2, f2_pack(n4.z, n4.w)));
-            s[h][e] = __float_as_uint(ex2_approx(u.x));
-            s[h][e + 1] = __float_as_uint(ex2_approx(u.y));
-            s[h][e + 2] = __float_as_uint(ex2_approx(w.x));
-            s[h][e + 3] = __float_as_uint(ex2_approx(w.y));
-          }
-        if (masked) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[h][e] = (see[h] >> e) & 1u ? s[h][e] : 0u;
+        for (int e = 0; e < 32; e += 4) {
+          const float4 n4 = nl[e >> 2];
+          const float2 u =
+              f2_unpack(ffma2(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), kk2, f2_pack(n4.x, n4.y)));
+          const float2 v =
+              f2_unpack(ffma2(f2_pack(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), kk2, f2_pack(n4.z, n4.w)));
+          s[e] = __float_as_uint(ex2_approx(u.x));
+          s[e + 1] = __float_as_uint(ex2_approx(u.y));
+          s[e + 2] = __float_as_uint(ex2_approx(v.x));
+          s[e + 3] = __float_as_uint(ex2_approx(v.y));
+          pk[e >> 1] = pack_bf16x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          pk[(e >> 1) + 1] = pack_bf16x2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        // hidden queries: P and, whatever dP and D hold, dS are 0
+        const uint32_t see = masked ? bits_between(lo - q0, hi - q0) : 0xffffffffu;
+        auto hide = [&]() {
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
-            pk[h * 16 + (e >> 1)] = pack_bf16x2(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]));
-        tmem_st_32x32b_x32(lane_base + half * 64, pk);   // over this thread's own columns of S^T
+            pk[e >> 1] &= ((see >> e) & 1u ? 0x0000ffffu : 0u) | ((see >> (e + 1)) & 1u ? 0xffff0000u : 0u);
+        };
+        if (masked) hide();
+        tmem_st_32x32b_x16(lane_base + w * 32, pk);   // over this thread's own columns of S^T
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
@@ -467,32 +470,23 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           break;
         }
         tc_fence_after_sync();
-        uint32_t dp[2][32];
-        tmem_ld_32x32b_x32(lane_base + T_DP + half * 64, dp[0]);
-        tmem_ld_32x32b_x32(lane_base + T_DP + half * 64 + 32, dp[1]);
+        uint32_t dp[32];
+        tmem_ld_32x32b_x32(lane_base + T_DP + w * 32, dp);
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 n4 = nD[(h * 32 + e) >> 2];
-            const float2 u = f2_unpack(fmul2(
-                fadd2(f2_pack(__uint_as_float(dp[h][e]), __uint_as_float(dp[h][e + 1])), f2_pack(n4.x, n4.y)),
-                f2_pack(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]))));
-            const float2 w = f2_unpack(fmul2(
-                fadd2(f2_pack(__uint_as_float(dp[h][e + 2]), __uint_as_float(dp[h][e + 3])), f2_pack(n4.z, n4.w)),
-                f2_pack(__uint_as_float(s[h][e + 2]), __uint_as_float(s[h][e + 3]))));
-            pk[h * 16 + (e >> 1)] = pack_bf16x2(u.x, u.y);
-            pk[h * 16 + (e >> 1) + 1] = pack_bf16x2(w.x, w.y);
-          }
-        if (masked) {   // a hidden query's dP and D may be anything: its dS is 0
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              pk[h * 16 + (e >> 1)] &= ((see[h] >> e) & 1u ? 0x0000ffffu : 0u) | ((see[h] >> (e + 1)) & 1u ? 0xffff0000u : 0u);
+        for (int e = 0; e < 32; e += 4) {
+          const float4 n4 = nD[e >> 2];
+          const float2 u = f2_unpack(
+              fmul2(fadd2(f2_pack(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), f2_pack(n4.x, n4.y)),
+                    f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1]))));
+          const float2 v = f2_unpack(
+              fmul2(fadd2(f2_pack(__uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3])), f2_pack(n4.z, n4.w)),
+                    f2_pack(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]))));
+          pk[e >> 1] = pack_bf16x2(u.x, u.y);
+          pk[(e >> 1) + 1] = pack_bf16x2(v.x, v.y);
         }
-        tmem_st_32x32b_x32(lane_base + T_DP + half * 64, pk);
+        if (masked) hide();
+        tmem_st_32x32b_x16(lane_base + T_DP + w * 32, pk);
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
@@ -502,8 +496,9 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         }
       }
       if (!ok) break;
-      // ---- the first warpgroup stores dK, the second dV; the last products are running
+      // ---- two warpgroups store dK, two dV; the last products are running
       if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
+      const int kind = w >> 1, col = (w & 1) * (D / 2);
       const bool computed = it.steps > 0;
       if (computed) {
         ok = mbar_wait(acc_full, static_cast<uint32_t>(ni) & 1u, abort_flag, status, tmo);
@@ -515,17 +510,17 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         tc_fence_after_sync();
       }
       float bad = 0.0f;   // becomes NaN with the first value that is not finite
-      const float f = half || it.slot >= 0 ? 1.0f : A.scale;
-      const int64_t off = (half ? A.lddv : A.lddk) * static_cast<int64_t>(key < T ? key : 0) + it.g * D;
-      __nv_bfloat16* out = (half ? S.dv : S.dk) + off;
-      float* part = A.part + ((static_cast<int64_t>(it.slot < 0 ? 0 : it.slot) * 2 + half) * kTile + r) * D;
+      const float f = kind || it.slot >= 0 ? 1.0f : A.scale;
+      const int64_t off = (kind ? A.lddv : A.lddk) * static_cast<int64_t>(key < T ? key : 0) + it.g * D + col;
+      __nv_bfloat16* out = (kind ? S.dv : S.dk) + off;
+      float* part = A.part + ((static_cast<int64_t>(it.slot < 0 ? 0 : it.slot) * 2 + kind) * kTile + r) * D + col;
 #pragma unroll
-      for (int u = 0; u < D / 32; ++u) {
+      for (int u = 0; u < D / 64; ++u) {
         uint32_t o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0;
         if (computed) {
-          tmem_ld_32x32b_x32(lane_base + (half ? T_DV : T_DK) + u * 32, o);
+          tmem_ld_32x32b_x32(lane_base + (kind ? T_DV : T_DK) + col + u * 32, o);
           tmem_ld_wait();
         }
 #pragma unroll
@@ -536,15 +531,29 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         }
         if (it.slot >= 0) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) st_global_v8(part + u * 32 + w * 8, o + w * 8);
+          for (int q = 0; q < 4; ++q) st_global_v8(part + u * 32 + q * 8, o + q * 8);
         } else if (key < T) {
           store_bf16x32(out + u * 32, o);
         }
       }
       tc_fence_before_sync();
-      const unsigned again = __ballot_sync(0xffffffffu, in && bad != 0.0f && it.slot < 0);
-      __syncwarp();   // the rows' stores above come before those of the redo
-      if (again) redo_dkv<D>(A, it.shard, it.g, it.k0 + quad * 32, again, half == 0, lane);
+      // A row is redone, by one of its two warpgroups, if either found its columns not finite, after both have
+      // stored.  (All sixteen warps meet, with a bounded wait, unlike a hardware barrier.)
+      const unsigned mine = __ballot_sync(0xffffffffu, in && bad != 0.0f && it.slot < 0);
+      if (mine && lane == 0) atomicOr(&flags[kind * 4 + quad], mine);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x_bar);
+      ok = mbar_wait(x_bar, met & 1u, abort_flag, status, tmo);
+      ++met;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if ((w & 1) == 0) {
+        const unsigned again = flags[kind * 4 + quad];
+        __syncwarp();
+        if (again) {
+          if (lane == 0) flags[kind * 4 + quad] = 0;
+          redo_dkv<D>(A, it.shard, it.g, it.k0 + quad * 32, again, kind == 0, lane);
+        }
+      }
     }
   }
 

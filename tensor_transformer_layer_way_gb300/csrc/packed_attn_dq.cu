@@ -6,10 +6,11 @@
 // (dK, dV) are two kernels, so every sum has one owner and a fixed order: the price is S and dP twice
 // (7 products where one kernel with atomic additions into dQ would need 5).
 //
-// Roles (384 threads, persistent): warp 0 the TMA loads (K three slots deep, read by S_j and again by dQ_j;
-// V two), warp 1 the MMAs in the order S_(j+1), dP_(j+1), dQ_j, so that two products run while the
-// elementwise warps form dS_j; warps 2 and 3 bring lse, D and the first key of the coming item's rows to shared
-// memory; warps 4..11 form dS: a row per thread, each warpgroup on 64 of the keys.
+// Roles (640 threads, persistent): warp 0 the TMA loads (K three slots deep, read by S_j and again by dQ_j; V two),
+// warp 1 the MMAs in the order S_(j+1), dP_(j+1), dQ_j, so that two products run while the elementwise warps
+// form dS_j; warps 2 and 3 bring lse, D and the first key of the coming item's rows to shared memory; warps 4..19
+// form dS: a row per thread, each of the four warpgroups on 32 of the keys (on 64 each, two warpgroups took
+// longer over a tile than the products they run under).
 // S, dP and dQ take 384 columns of tensor memory and two dS buffers the rest.
 
 #include <cstring>
@@ -19,7 +20,8 @@
 namespace ttl {
 namespace {
 
-constexpr int kDqThreads = 384;
+constexpr int kDqThreads = 640;
+constexpr int kDqWarps = 16;   // elementwise warps
 constexpr int kKSlots = 3;
 constexpr int kVSlots = 2;
 
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
   uint64_t* ds_empty = ds_full + 2;    // [2]
   uint64_t* dq_full = ds_empty + 2;
   uint64_t* dq_empty = dq_full + 1;
-  uint64_t* x_bar = dq_empty + 1;      // the eight elementwise warps meet
+  uint64_t* x_bar = dq_empty + 1;      // the elementwise warps meet
   uint64_t* rows_full = x_bar + 1;
   uint64_t* rows_empty = rows_full + 1;
   uint64_t* done_bar = rows_empty + 1;
@@ -151,19 +153,20 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
       mbar_init(&v_empty[s], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_empty, 8);
+    mbar_init(s_empty, kDqWarps);
     mbar_init(dp_full, 1);
-    mbar_init(dp_empty, 8);
+    mbar_init(dp_empty, kDqWarps);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&ds_full[b], 8);
+      mbar_init(&ds_full[b], kDqWarps);
       mbar_init(&ds_empty[b], 1);
     }
     mbar_init(dq_full, 1);
-    mbar_init(dq_empty, 8);
-    mbar_init(x_bar, 8);
+    mbar_init(dq_empty, kDqWarps);
+    mbar_init(x_bar, kDqWarps);
     mbar_init(rows_full, 2);
-    mbar_init(rows_empty, 8);
+    mbar_init(rows_empty, kDqWarps);
     mbar_init(done_bar, 1);
+    for (int q = 0; q < 4; ++q) flags[q] = 0;
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
   } else {
     // ------------------------------------------------------------------ dS
     const int quad = warp & 3;
-    const int half = (warp - 4) >> 2;
+    const int g = (warp - 4) >> 2;             // keys [32 g, 32 g + 32) of each tile
     const int r = quad * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float k2 = A.scale * kLog2e;
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     bool ok = true;
     int pos = 0, no = 0;
     uint32_t met = 0;
-    // All eight warps meet (a bounded wait, unlike a hardware barrier).
+    // All elementwise warps meet (a bounded wait, unlike a hardware barrier).
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(x_bar);
@@ -406,55 +409,44 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           break;
         }
         tc_fence_after_sync();
-        uint32_t s[2][32];
-        tmem_ld_32x32b_x32(lane_base + half * 64, s[0]);
-        tmem_ld_32x32b_x32(lane_base + half * 64 + 32, s[1]);
+        uint32_t s[32];
+        tmem_ld_32x32b_x32(lane_base + g * 32, s);
         tmem_ld_wait();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive_relaxed(s_empty);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 a = f2_unpack(ffma2(f2_pack(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1])), kk2, nl2));
-            s[h][e] = __float_as_uint(ex2_approx(a.x));
-            s[h][e + 1] = __float_as_uint(ex2_approx(a.y));
-          }
+        for (int e = 0; e < 32; e += 2) {
+          const float2 a = f2_unpack(ffma2(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), kk2, nl2));
+          s[e] = __float_as_uint(ex2_approx(a.x));
+          s[e + 1] = __float_as_uint(ex2_approx(a.y));
+        }
         ok = mbar_wait(dp_full, static_cast<uint32_t>(pos) & 1u, abort_flag, status, tmo);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        uint32_t dp[2][32];
-        tmem_ld_32x32b_x32(lane_base + T_DP + half * 64, dp[0]);
-        tmem_ld_32x32b_x32(lane_base + T_DP + half * 64 + 32, dp[1]);
+        uint32_t dp[32];
+        tmem_ld_32x32b_x32(lane_base + T_DP + g * 32, dp);
         tmem_ld_wait();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive_relaxed(dp_empty);
-        const int k0 = j * kTile + half * 64;
-        if (k0 < lo_max || k0 + 63 > hi_min) {   // some row of the warp does not see every key
+        uint32_t ds[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t see = bits_between(lo - k0 - h * 32, hi - k0 - h * 32);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              s[h][e] = (see >> e) & 1u ? s[h][e] : 0u;
-              dp[h][e] = (see >> e) & 1u ? dp[h][e] : 0u;
-            }
-          }
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t d2 = fadd2(f2_pack(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nD2);
+          const float2 v = f2_unpack(fmul2(d2, f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1]))));
+          ds[e >> 1] = pack_bf16x2(v.x, v.y);
         }
-        uint32_t ds[32];
+        const int k0 = j * kTile + g * 32;
+        if (k0 < lo_max || k0 + 31 > hi_min) {   // some row of the warp does not see every key: its dS is 0
+          const uint32_t see = bits_between(lo - k0, hi - k0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const uint64_t d2 = fadd2(f2_pack(__uint_as_float(dp[h][e]), __uint_as_float(dp[h][e + 1])), nD2);
-            const float2 v = f2_unpack(fmul2(d2, f2_pack(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]))));
-            ds[h * 16 + (e >> 1)] = pack_bf16x2(v.x, v.y);
-          }
+          for (int e = 0; e < 32; e += 2)
+            ds[e >> 1] &= ((see >> e) & 1u ? 0x0000ffffu : 0u) | ((see >> (e + 1)) & 1u ? 0xffff0000u : 0u);
+        }
         const int b = pos & 1;
         ok = mbar_wait(&ds_empty[b], (static_cast<uint32_t>(pos >> 1) & 1u) ^ 1u, abort_flag, status, tmo);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -462,7 +454,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           break;
         }
         tc_fence_after_sync();
-        tmem_st_32x32b_x32(lane_base + T_DS + b * 64 + half * 32, ds);
+        tmem_st_32x32b_x16(lane_base + T_DS + b * 64 + g * 16, ds);
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
@@ -481,14 +473,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         tc_fence_after_sync();
       }
       float bad = 0.0f;   // becomes NaN with the first value that is not finite
-      __nv_bfloat16* out = S.dq + static_cast<int64_t>(i < T ? i : 0) * A.lddq + it.c * D + half * (D / 2);
-#pragma unroll
-      for (int u = 0; u < D / 64; ++u) {
+      if (g < D / 32) {   // 32 of the head's columns
         uint32_t o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0;
         if (computed) {
-          tmem_ld_32x32b_x32(lane_base + T_DQ + half * (D / 2) + u * 32, o);
+          tmem_ld_32x32b_x32(lane_base + T_DQ + g * 32, o);
           tmem_ld_wait();
         }
 #pragma unroll
@@ -497,20 +487,24 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           bad = fmaf(v, 0.0f, bad);
           o[e] = __float_as_uint(v);
         }
-        if (i < T) store_bf16x32(out + u * 32, o);
+        if (i < T) store_bf16x32(S.dq + i * A.lddq + it.c * D + g * 32, o);
       }
       if (computed) {
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive_relaxed(dq_empty);
       }
-      // A row is redone, by the first warpgroup, if either found its half not finite, after both have stored.
+      // A row is redone, by the first warpgroup, if any found its columns not finite, after all have stored.
       const unsigned mine = __ballot_sync(0xffffffffu, in && bad != 0.0f);
-      if (half == 1 && lane == 0) flags[quad] = mine;
+      if (mine && lane == 0) atomicOr(&flags[quad], mine);
       if (!(ok = meet())) break;
-      if (half == 0) {
-        const unsigned again = mine | flags[quad];
-        if (again) redo_dq<D>(A, it.shard, it.c, it.q0 + quad * 32, again, lane);
+      if (g == 0) {
+        const unsigned again = flags[quad];
+        __syncwarp();
+        if (again) {
+          if (lane == 0) flags[quad] = 0;
+          redo_dq<D>(A, it.shard, it.c, it.q0 + quad * 32, again, lane);
+        }
       }
     }
   }
