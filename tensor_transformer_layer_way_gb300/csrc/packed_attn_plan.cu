@@ -67,6 +67,7 @@ __device__ __forceinline__ void row_dots(const PackArgs& A, int shard, int64_t i
   const int lane = threadIdx.x & 31;
   const PackShard& S = A.s[shard];
   const int cols = A.nql * d, lph = d / 8;
+#pragma unroll 2
   for (int base = 0; base < cols; base += 256) {
     const int c = base + lane * 8;
     float acc = 0.0f;
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
   __shared__ int hist[kPlanThreads];
   __shared__ int warp_tot[32];
   __shared__ unsigned long long total;
-  __shared__ int taken, joins;
+  __shared__ int taken, joins, longest;
   const int tid = threadIdx.x;
   if (blockIdx.x > 0) {
     const int64_t w = static_cast<int64_t>(blockIdx.x - 1) * (kPlanThreads / 32) + (tid >> 5);
@@ -114,17 +115,24 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     hist[tid] = 0;
     if (tid == 0) {
       total = 0;
-      taken = joins = 0;
+      taken = joins = longest = 0;
     }
     __syncthreads();
     unsigned long long sum = 0;
-    for (int t = tid; t < P.tiles; t += kPlanThreads)
-      sum += static_cast<unsigned long long>(last_query_tile(A, t) - t + 1) * A.grp;
+    int most_here = 0;
+    for (int t = tid; t < P.tiles; t += kPlanThreads) {
+      const int steps = (last_query_tile(A, t) - t + 1) * A.grp;
+      sum += static_cast<unsigned long long>(steps);
+      most_here = steps > most_here ? steps : most_here;
+    }
     atomicAdd(&total, sum);
+    atomicMax(&longest, most_here);
     __syncthreads();
-    // the longest item: a third of an SM's share of all steps
+    // Where a whole key tile would be more than an SM's share of all steps, no item is longer than a third of
+    // that share.  (A part costs a write and a read of its fp32 sums: with every tile below the share,
+    // cutting took 24 us and won nothing.)
     unsigned long long most = 0x7fffffffull;
-    if (P.split) {
+    if (P.split && 3ull * static_cast<unsigned long long>(longest) * kSplitItems > 9ull * total * P.lanes) {
       most = (total * P.lanes + kSplitItems - 1) / kSplitItems;
       if (most < kSplitSteps) most = kSplitSteps;
     }
