@@ -7,8 +7,15 @@
 // Backward:  dE[v] (+)= scale sum over the tokens of id v of dY[tok], in fp32.
 // The token indices are sorted by id (a stable radix sort, so the tokens of one id stay in
 // token order); a run of equal ids is then summed by whole CTAs in chunks of fixed length, and the
-// partial sums of a run that crosses chunks are joined in chunk order.  No atomic adds: the same
-// inputs give the same bits, and a row of the gradient is written once.
+// partial sums of a run that crosses chunks are joined in a fixed order.  No atomic adds to the gradient: the
+// same inputs give the same bits, and a row of the gradient is written once.
+//
+// What bounds it: the table's bytes where every row is written (8192 tokens, 151936 x 4096: 2.5 GB), else the
+// tokens' rows; the sort is latency.  Up to 16384 tokens it is one CTA in shared memory, and the other CTAs of
+// the same launch write the zeros of the rows that no token has meanwhile; beyond that three launches per
+// digit, and zeros everywhere first.
+
+#include <mutex>
 
 #include "ttl_device.cuh"
 #include "ttl_internal.h"
@@ -84,7 +91,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int64_t*
 }
 
 // Exclusive prefix sums of the n counts, in place; one CTA, each thread a contiguous range.
-__global__ void __launch_bounds__(1024) sort_scan_kernel(uint32_t* counts, int64_t n) {
+__global__ void __launch_bounds__(1024) sort_scan_kernel(uint32_t* counts, int64_t n, uint32_t* runs) {
+  if (threadIdx.x == 0) runs[0] = 0;   // the list of long runs, filled by the sums
   __shared__ uint32_t warp_tot[32];
   const int64_t per = (n + 1023) / 1024;
   const int64_t lo = threadIdx.x * per < n ? threadIdx.x * per : n, hi = lo + per < n ? lo + per : n;
@@ -160,85 +168,270 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const int64_t* 
   }
 }
 
+// ------------------------------------------------------------------ sort in one CTA, zeros in the others
+
+constexpr int kOneThreads = 1024;
+constexpr int kOneWarps = kOneThreads / 32;
+constexpr int kOneMost = 16384;      // tokens: two buffers of keys and of 16-bit tokens, and a count per warp and digit
+constexpr size_t kOneSmem = 2 * kOneMost * 4 + 2 * kOneMost * 2 + kOneWarps * kRadix * 2;
+
+// CTA 0: the stable radix sort of the T keys, `bits` bits at a time; a warp owns rounds x 32 consecutive keys.
+__device__ void sort_one(const int64_t* ids, int T, int64_t V, int passes, int bits, uint32_t* keys_out,
+                         uint32_t* toks_out, int* status, uint8_t* smem) {
+  uint32_t* key[2] = {reinterpret_cast<uint32_t*>(smem), reinterpret_cast<uint32_t*>(smem) + kOneMost};
+  uint16_t* tok[2] = {reinterpret_cast<uint16_t*>(key[1] + kOneMost), reinterpret_cast<uint16_t*>(key[1] + kOneMost) + kOneMost};
+  uint16_t* at = tok[1] + kOneMost;                          // [warp][digit]
+  __shared__ uint32_t warp_tot[kRadix / 32];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int rounds = (T + kOneThreads - 1) / kOneThreads;    // at most 16
+  for (int k = tid; k < T; k += kOneThreads) {
+    key[0][k] = key_of(ids, nullptr, k, V, status);
+    tok[0][k] = static_cast<uint16_t>(k);
+  }
+  const uint32_t mask = (1u << bits) - 1u;
+  const int base = w * rounds * 32;
+  for (int pass = 0; pass < passes; ++pass) {
+    const uint32_t* ki = key[pass & 1];
+    const uint16_t* ti = tok[pass & 1];
+    uint32_t* ko = key[(pass & 1) ^ 1];
+    uint16_t* to = tok[(pass & 1) ^ 1];
+    const int shift = pass * bits;
+    for (int d = lane; d < kRadix; d += 32) at[w * kRadix + d] = 0;
+    __syncthreads();                                         // the keys are in place, the counts zero
+    for (int r = 0; r < rounds; ++r) {
+      const int k = base + r * 32 + lane;
+      const uint32_t d = k < T ? (ki[k] >> shift) & mask : kRadix;
+      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+      if (k < T && lane == __ffs(peers) - 1) at[w * kRadix + d] += static_cast<uint16_t>(__popc(peers));
+      __syncwarp();
+    }
+    __syncthreads();
+    // first place of warp w's keys of digit d: all smaller digits, then this digit's in the warps before
+    uint32_t mine = 0, inc = 0;
+    if (tid < kRadix) {
+      for (int j = 0; j < kOneWarps; ++j) mine += at[j * kRadix + tid];
+      inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (lane == 31) warp_tot[w] = inc;
+    }
+    __syncthreads();
+    if (tid < kRadix) {
+      uint32_t run = inc - mine;
+      for (int j = 0; j < w; ++j) run += warp_tot[j];
+      for (int j = 0; j < kOneWarps; ++j) {
+        const uint32_t c = at[j * kRadix + tid];
+        at[j * kRadix + tid] = static_cast<uint16_t>(run);
+        run += c;
+      }
+    }
+    __syncthreads();
+    for (int r = 0; r < rounds; ++r) {
+      const int k = base + r * 32 + lane;
+      const bool in = k < T;
+      const uint32_t key_k = in ? ki[k] : 0u;
+      const uint32_t d = in ? (key_k >> shift) & mask : kRadix;
+      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+      uint32_t place = 0;
+      if (in) place = at[w * kRadix + d] + __popc(peers & ((1u << lane) - 1u));
+      __syncwarp();
+      if (in && lane == __ffs(peers) - 1) at[w * kRadix + d] += static_cast<uint16_t>(__popc(peers));
+      __syncwarp();
+      if (in) {
+        if (pass + 1 == passes) {
+          keys_out[place] = key_k;
+          toks_out[place] = ti[k];
+        } else {
+          ko[place] = key_k;
+          to[place] = ti[k];
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// The other CTAs: zeros for the rows of a slice of the vocabulary that no token has.
+__device__ void fill_slice(const GradTables& G, const int64_t* ids, int T, int64_t V, int64_t Vs, int64_t h, int cta,
+                           int ctas, uint8_t* smem) {
+  uint32_t* seen = reinterpret_cast<uint32_t*>(smem);
+  const int64_t per = (V + ctas - 1) / ctas;
+  const int64_t lo = cta * per < V ? cta * per : V, hi = lo + per < V ? lo + per : V;
+  const int words = static_cast<int>((hi - lo + 31) / 32);
+  for (int k = threadIdx.x; k < words; k += kOneThreads) seen[k] = 0;
+  __syncthreads();
+  for (int k = threadIdx.x; k < T; k += kOneThreads) {
+    const int64_t id = ids[k];
+    if (id >= lo && id < hi) atomicOr(&seen[(id - lo) >> 5], 1u << ((id - lo) & 31));
+  }
+  __syncthreads();
+  // a warp per row
+  const int64_t h4 = h / 4;
+  for (int64_t v = lo + (threadIdx.x >> 5); v < hi; v += kOneWarps) {
+    if ((seen[(v - lo) >> 5] >> ((v - lo) & 31)) & 1u) continue;
+    const int i = static_cast<int>(v / Vs);
+    float4* row = reinterpret_cast<float4*>(G.g[i] + (v - i * Vs) * h);
+    for (int64_t k = threadIdx.x & 31; k < h4; k += 32) __stcs(row + k, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+  }
+}
+
+__global__ void __launch_bounds__(kOneThreads) sort_fill_kernel(const __grid_constant__ GradTables G,
+                                                                const int64_t* ids, int T, int64_t V, int64_t Vs,
+                                                                int64_t h, int passes, int bits, uint32_t* keys_out,
+                                                                uint32_t* toks_out, uint32_t* runs, int* status) {
+  extern __shared__ __align__(16) uint8_t one_smem[];
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) runs[0] = 0;
+    sort_one(ids, T, V, passes, bits, keys_out, toks_out, status, one_smem);
+  } else {
+    fill_slice(G, ids, T, V, Vs, h, blockIdx.x - 1, gridDim.x - 1, one_smem);
+  }
+}
+
 // ------------------------------------------------------------------ sums over runs of equal ids
 
 constexpr int kSumThreads = 256;
+constexpr int kMaxChunk = 1 << 20;   // places per chunk
 
-__device__ __forceinline__ void row_out(const GradTables& G, uint32_t key, int64_t Vs, int64_t h, int64_t col,
-                                        const float (&a)[8], float scale, int accumulate) {
-  const int i = static_cast<int>(key / Vs);
-  float4* dst = reinterpret_cast<float4*>(G.g[i] + (key - i * Vs) * h + col);
-  float4 u = make_float4(a[0] * scale, a[1] * scale, a[2] * scale, a[3] * scale);
-  float4 v = make_float4(a[4] * scale, a[5] * scale, a[6] * scale, a[7] * scale);
-  if (accumulate) {
-    const float4 p = dst[0], q = dst[1];
-    u = make_float4(u.x + p.x, u.y + p.y, u.z + p.z, u.w + p.w);
-    v = make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w);
-  }
-  dst[0] = u;
-  dst[1] = v;
+__device__ __forceinline__ float* row_of(const GradTables& G, uint32_t key, int64_t Vs, int64_t h) {
+  const uint32_t i = key / static_cast<uint32_t>(Vs);
+  return G.g[i] + static_cast<int64_t>(key - i * static_cast<uint32_t>(Vs)) * h;
 }
 
-// Chunk b = sorted places [b C, (b + 1) C); each thread sums 8 columns.  A run that begins and ends in
-// the chunk goes to its row of dE.  A run that began earlier leaves its sum in head[b]; one that
-// begins here and goes on leaves its sum in tail[b].
+// Eight columns of a finished row: 32 bytes, written (or added to) once.
+__device__ __forceinline__ void row_out(float* dst, const float (&a)[8], float scale, int accumulate) {
+  uint32_t w[8];
+  float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q = p;
+  if (accumulate) {
+    p = reinterpret_cast<const float4*>(dst)[0];
+    q = reinterpret_cast<const float4*>(dst)[1];
+  }
+  const float old[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(accumulate ? fmaf(a[j], scale, old[j]) : a[j] * scale);
+  if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+    st_global_v8(dst, w);
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// Chunk b = sorted places [b C, (b + 1) C); each thread sums 8 columns, the rows of eight places loaded ahead of
+// their sums.  A run that begins and ends in the chunk goes to its row of dE.  A run that began earlier leaves its
+// sum in head[b]; one that begins here and goes on leaves its sum in tail[b], and the chunk in runs.
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_constant__ GradTables G,
                                                                 const uint32_t* keys, const uint32_t* toks,
                                                                 const __nv_bfloat16* dY, int64_t lddy, int64_t T,
                                                                 int64_t h, int64_t Vs, int64_t V, int C, float scale,
-                                                                int accumulate, float* head, float* tail) {
-  const int64_t col = (static_cast<int64_t>(blockIdx.y) * kSumThreads + threadIdx.x) * 8;
-  if (col >= h) return;
+                                                                int accumulate, float* head, float* tail,
+                                                                uint32_t* runs) {
+  constexpr int W = 128;                                     // places looked at together
+  __shared__ const __nv_bfloat16* src[W];
+  __shared__ float* dst[W];                                  // where the run that ends at the place goes; null: it goes on
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * C, hi = lo + C < T ? lo + C : T;
+  const int64_t col = (static_cast<int64_t>(blockIdx.y) * kSumThreads + threadIdx.x) * 8;
+  const uint32_t first = keys[lo], last = keys[hi - 1];
+  bool began = lo == 0 || keys[lo - 1] != first;
+  if (blockIdx.y == 0 && threadIdx.x == 0 && last < V && hi < T && keys[hi] == last && (began || first != last))
+    runs[1 + atomicAdd(runs, 1u)] = blockIdx.x;              // (their order does not matter)
   float a[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) a[j] = 0.0f;
-  bool began = lo == 0 || keys[lo - 1] != keys[lo];
-  for (int64_t k = lo; k < hi; ++k) {
-    const uint32_t key = keys[k];
-    if (key >= V) break;   // ids out of range are last
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(dY + static_cast<int64_t>(toks[k]) * lddy + col));
-    a[0] += bf16_lo(v.x); a[1] += bf16_hi(v.x); a[2] += bf16_lo(v.y); a[3] += bf16_hi(v.y);
-    a[4] += bf16_lo(v.z); a[5] += bf16_hi(v.z); a[6] += bf16_lo(v.w); a[7] += bf16_hi(v.w);
-    const bool ends = k + 1 == T || keys[k + 1] != key;
-    if (ends || k + 1 == hi) {
-      if (began && ends) {
-        row_out(G, key, Vs, h, col, a, scale, accumulate);
-      } else {
-        float4* p = reinterpret_cast<float4*>((began ? tail : head) + static_cast<int64_t>(blockIdx.x) * h + col);
-        p[0] = make_float4(a[0], a[1], a[2], a[3]);
-        p[1] = make_float4(a[4], a[5], a[6], a[7]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = 0.0f;
-      began = true;
+  for (int64_t w0 = lo; w0 < hi; w0 += W) {
+    const int n = static_cast<int>(hi - w0 < W ? hi - w0 : W);
+    if (w0 > lo) __syncthreads();
+    if (static_cast<int>(threadIdx.x) < n) {
+      const int64_t k = w0 + threadIdx.x;
+      const uint32_t key = keys[k];
+      const bool valid = key < V;                            // ids out of range are last
+      src[threadIdx.x] = valid ? dY + static_cast<int64_t>(toks[k]) * lddy : nullptr;
+      dst[threadIdx.x] = valid && (k + 1 == T || keys[k + 1] != key) ? row_of(G, key, Vs, h) : nullptr;
     }
+    __syncthreads();
+    if (col < h) {
+      for (int k0 = 0; k0 < n; k0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const __nv_bfloat16* from = k0 + j < n ? src[k0 + j] : nullptr;
+          v[j] = from ? __ldcs(reinterpret_cast<const uint4*>(from + col)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          a[0] += bf16_lo(v[j].x); a[1] += bf16_hi(v[j].x); a[2] += bf16_lo(v[j].y); a[3] += bf16_hi(v[j].y);
+          a[4] += bf16_lo(v[j].z); a[5] += bf16_hi(v[j].z); a[6] += bf16_lo(v[j].w); a[7] += bf16_hi(v[j].w);
+          float* to = k0 + j < n ? dst[k0 + j] : nullptr;
+          if (to) {
+            if (began) {
+              row_out(to + col, a, scale, accumulate);
+            } else {
+              float4* p = reinterpret_cast<float4*>(head + static_cast<int64_t>(blockIdx.x) * h + col);
+              p[0] = make_float4(a[0], a[1], a[2], a[3]);
+              p[1] = make_float4(a[4], a[5], a[6], a[7]);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) a[q] = 0.0f;
+            began = true;
+          }
+        }
+      }
+    }
+  }
+  if (col < h && last < V && hi < T && keys[hi] == last) {   // a run goes on past the chunk
+    float4* p = reinterpret_cast<float4*>((began ? tail : head) + static_cast<int64_t>(blockIdx.x) * h + col);
+    p[0] = make_float4(a[0], a[1], a[2], a[3]);
+    p[1] = make_float4(a[4], a[5], a[6], a[7]);
   }
 }
 
-// Joins the runs that go on past their chunk: the chunk in which the run began adds the heads of the
-// following ones, in order.
+// Joins the runs that go on past their chunk.  A CTA takes 128 columns of one run: sixteen lanes hold the columns,
+// sixteen groups each every sixteenth partial sum, and the groups are added in order.
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const __grid_constant__ GradTables G,
                                                                  const uint32_t* keys, int64_t T, int64_t h,
                                                                  int64_t Vs, int64_t V, int C, float scale,
-                                                                 int accumulate, const float* head, const float* tail) {
-  const int64_t b = blockIdx.x, lo = b * C, hi = lo + C;
-  if (hi >= T) return;                                     // the last chunk goes on nowhere
-  const uint32_t key = keys[hi - 1];
-  if (key >= V || keys[hi] != key) return;                 // ends with the chunk
-  if (keys[lo] == key && lo > 0 && keys[lo - 1] == key) return;   // began in an earlier chunk
-  const int64_t col = (static_cast<int64_t>(blockIdx.y) * kSumThreads + threadIdx.x) * 8;
-  if (col >= h) return;
-  float a[8];
-  auto add = [&](const float* p, bool first) {
-    const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
-    const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+                                                                 int accumulate, const float* head, const float* tail,
+                                                                 const uint32_t* runs) {
+  __shared__ float red[16][16][9];
+  const int vec = threadIdx.x & 15, part = threadIdx.x >> 4;
+  const int64_t blocks = (h + 127) / 128;
+  const int64_t items = static_cast<int64_t>(runs[0]) * blocks;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t b = runs[1 + it / blocks];
+    const int64_t col = (it % blocks) * 128 + vec * 8;
+    const uint32_t key = keys[(b + 1) * C];
+    // the last chunk that the run enters: places are sorted, so by bisection
+    int64_t l = b + 1, r = (T - 1) / C + 1;                  // keys[l C] == key; r: not, or past the end
+    while (r - l > 1) {
+      const int64_t m = (l + r) >> 1;
+      if (keys[m * C] == key) l = m; else r = m;
+    }
+    float a[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = first ? w[j] : a[j] + w[j];
-  };
-  add(tail + b * h + col, true);
-  for (int64_t n = b + 1; n * C < T && keys[n * C] == key; ++n) add(head + n * h + col, false);
-  row_out(G, key, Vs, h, col, a, scale, accumulate);
+    for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+    if (col < h) {
+#pragma unroll 4
+      for (int64_t n = b + part; n <= l; n += 16) {
+        const float4* p = reinterpret_cast<const float4*>((n == b ? tail : head) + n * h + col);
+        const float4 u = p[0], v = p[1];
+        a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
+        a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[part][vec][j] = a[j];
+    __syncthreads();
+    if (part == 0 && col < h) {
+      for (int p = 1; p < 16; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] += red[p][vec][j];
+      row_out(row_of(G, key, Vs, h) + col, a, scale, accumulate);
+    }
+    __syncthreads();
+  }
 }
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -247,22 +440,40 @@ struct SortPlan {
   int64_t nb;        // sort blocks
   int C;             // sorted places per sum chunk
   int64_t chunks;
-  size_t keys, counts, part;   // bytes of one key array, of the counts, of one partial array
+  size_t keys, counts, part, runs;   // bytes of one key array, of the counts, of one partial array, of the run list
 };
 
-// A chunk is 32 places, or longer so that there are at most 2048 of them: a run of any length is
-// then joined from at most 2048 partial sums.
+// A chunk is 16 places, or longer so that there are at most 2048 of them up to kMaxChunk: with 8192 tokens of 4096
+// columns that is 1024 CTAs of two batches of loads.
 SortPlan plan_of(int64_t T, int64_t h) {
   SortPlan p;
   p.nb = (T + kSortBlock - 1) / kSortBlock;
-  int64_t C = 32;
-  while ((T + C - 1) / C > 2048) C *= 2;
+  int64_t C = 16;
+  while (C < kMaxChunk && (T + C - 1) / C > 2048) C *= 2;
   p.C = static_cast<int>(C);
   p.chunks = (T + C - 1) / C;
   p.keys = round256(static_cast<size_t>(T) * 4);
   p.counts = round256(static_cast<size_t>(kRadix) * p.nb * 4);
   p.part = round256(static_cast<size_t>(p.chunks) * h * 4);
+  p.runs = round256(static_cast<size_t>(p.chunks + 1) * 4);
   return p;
+}
+
+// Raises sort_fill_kernel's dynamic shared-memory limit, once per device (thread-safe).
+int one_smem_once() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  int rc = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc) return rc;
+  if (dev < 0 || dev >= 64) return set_error(TTL_ERR_CUDA, "device index %d out of range", dev);
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return TTL_OK;
+  rc = cuda_check(cudaFuncSetAttribute(reinterpret_cast<const void*>(sort_fill_kernel),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOneSmem)),
+                  "cudaFuncSetAttribute(sort_fill_kernel)");
+  if (!rc) done[dev] = true;
+  return rc;
 }
 
 int check_common(int t, int64_t T, int64_t h, int64_t V, const char* name) {
@@ -326,7 +537,7 @@ extern "C" int ttl_vocab_parallel_embedding_scaled_fwd(int t, int64_t T, int64_t
 extern "C" size_t ttl_vocab_parallel_embedding_sorted_bwd_workspace_size(int t, int64_t T, int64_t h, int64_t V) {
   if (check_common(t, T, h, V, "ttl_vocab_parallel_embedding_sorted_bwd_workspace_size")) return 0;
   const SortPlan p = plan_of(T, h);
-  return 4 * p.keys + p.counts + 2 * p.part;
+  return 4 * p.keys + p.counts + 2 * p.part + p.runs;
 }
 
 extern "C" int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t h, int64_t V, const int64_t* ids,
@@ -358,7 +569,10 @@ extern "C" int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t
   const int64_t Vs = V / t;
   GradTables G = {};
   for (int i = 0; i < t; ++i) G.g[i] = dE[i];
-  if (!accumulate) {
+  // one launch for the sort and the zeros, where the tokens fit one CTA and a slice's marks its shared memory
+  const int sms = num_sms();
+  const bool one = T > 0 && T <= kOneMost && sms > 1 && V / (sms - 1) / 8 + 64 < static_cast<int64_t>(kOneSmem);
+  if (!accumulate && !one) {
     TraceScope trace(s, TTL_K_OTHER, 0.0, 4.0 * V * h);
     for (int i = 0; i < t; ++i)
       if ((rc = fill_zero(dE[i], static_cast<size_t>(Vs) * h * 4, s))) return rc;
@@ -372,15 +586,27 @@ extern "C" int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t
   uint32_t* counts = reinterpret_cast<uint32_t*>(base + 4 * p.keys);
   float* head = reinterpret_cast<float*>(base + 4 * p.keys + p.counts);
   float* tail = reinterpret_cast<float*>(base + 4 * p.keys + p.counts + p.part);
+  uint32_t* runs = reinterpret_cast<uint32_t*>(base + 4 * p.keys + p.counts + 2 * p.part);
+  int width = 0;   // bits of the largest key, which is V
+  while (width < 32 && (V >> width) > 0) ++width;
   const uint32_t* k_in = nullptr;
   const uint32_t* t_in = nullptr;
-  {
+  if (one) {
+    const int passes = (width + 7) / 8, bits = (width + passes - 1) / passes;
+    TraceScope trace(s, TTL_K_EMBED, 0.0, 16.0 * T + (accumulate ? 0.0 : 4.0 * V * h));
+    if ((rc = one_smem_once())) return rc;
+    sort_fill_kernel<<<accumulate ? 1 : sms, kOneThreads, kOneSmem, s>>>(
+        G, ids, static_cast<int>(T), V, Vs, h, passes, bits, keys[0], toks[0], runs, status);
+    if ((rc = cuda_check(cudaGetLastError(), "sort_fill_kernel launch"))) return rc;
+    k_in = keys[0];
+    t_in = toks[0];
+  } else {
     TraceScope trace(s, TTL_K_EMBED, 0.0, 16.0 * T);
     int out = 0;
-    for (int shift = 0; shift < 32 && (shift == 0 || (V >> shift) > 0); shift += 8) {   // V itself is a key
+    for (int shift = 0; shift < width; shift += 8) {
       sort_count_kernel<<<static_cast<unsigned>(p.nb), kSortThreads, 0, s>>>(ids, k_in, T, V, shift, counts,
                                                                              static_cast<int>(p.nb), status);
-      sort_scan_kernel<<<1, 1024, 0, s>>>(counts, kRadix * p.nb);
+      sort_scan_kernel<<<1, 1024, 0, s>>>(counts, kRadix * p.nb, runs);
       sort_move_kernel<<<static_cast<unsigned>(p.nb), kSortThreads, 0, s>>>(
           ids, k_in, t_in, T, V, shift, counts, static_cast<int>(p.nb), keys[out], toks[out], status);
       k_in = keys[out];
@@ -392,7 +618,8 @@ extern "C" int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t
   TraceScope trace(s, TTL_K_EMBED, 0.0, static_cast<double>(T) * h * 2.0);
   const dim3 grid(static_cast<unsigned>(p.chunks), static_cast<unsigned>((h / 8 + kSumThreads - 1) / kSumThreads));
   embed_sum_kernel<<<grid, kSumThreads, 0, s>>>(G, k_in, t_in, reinterpret_cast<const __nv_bfloat16*>(dY), lddy, T, h,
-                                                Vs, V, p.C, scale, accumulate, head, tail);
-  embed_join_kernel<<<grid, kSumThreads, 0, s>>>(G, k_in, T, h, Vs, V, p.C, scale, accumulate, head, tail);
+                                                Vs, V, p.C, scale, accumulate, head, tail, runs);
+  embed_join_kernel<<<static_cast<unsigned>(sms) * 2, kSumThreads, 0, s>>>(G, k_in, T, h, Vs, V, p.C, scale, accumulate,
+                                                                          head, tail, runs);
   return cuda_check(cudaGetLastError(), "embedding gradient launch");
 }
