@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int64_t*
 
 // Exclusive prefix sums of the n counts, in place; one CTA, each thread a contiguous range.
 __global__ void __launch_bounds__(1024) sort_scan_kernel(uint32_t* counts, int64_t n, uint32_t* runs) {
-  if (threadIdx.x == 0) runs[0] = 0;   // the list of long runs, filled by the sums
+  if (threadIdx.x < 2) runs[threadIdx.x] = 0;   // the lists of runs to be joined, filled by the sums
   __shared__ uint32_t warp_tot[32];
   const int64_t per = (n + 1023) / 1024;
   const int64_t lo = threadIdx.x * per < n ? threadIdx.x * per : n, hi = lo + per < n ? lo + per : n;
@@ -175,7 +175,18 @@ constexpr int kOneWarps = kOneThreads / 32;
 constexpr int kOneMost = 16384;      // tokens: two buffers of keys and of 16-bit tokens, and a count per warp and digit
 constexpr size_t kOneSmem = 2 * kOneMost * 4 + 2 * kOneMost * 2 + kOneWarps * kRadix * 2;
 
-// CTA 0: the stable radix sort of the T keys, `bits` bits at a time; a warp owns rounds x 32 consecutive keys.
+// Lanes of the warp with the same `bits` low bits of d (one vote per bit), among the lanes of `in`.
+__device__ __forceinline__ uint32_t same_digit(uint32_t d, int bits, uint32_t in) {
+  uint32_t peers = in;
+  for (int b = 0; b < bits; ++b) {
+    const uint32_t m = __ballot_sync(0xffffffffu, (d >> b) & 1u);
+    peers &= (d >> b) & 1u ? m : ~m;
+  }
+  return peers;
+}
+
+// CTA 0: the stable radix sort of the T <= 1024 R keys, `bits` bits at a time; a warp owns 32 R consecutive keys.
+template <int R>
 __device__ void sort_one(const int64_t* ids, int T, int64_t V, int passes, int bits, uint32_t* keys_out,
                          uint32_t* toks_out, int* status, uint8_t* smem) {
   uint32_t* key[2] = {reinterpret_cast<uint32_t*>(smem), reinterpret_cast<uint32_t*>(smem) + kOneMost};
@@ -183,32 +194,44 @@ __device__ void sort_one(const int64_t* ids, int T, int64_t V, int passes, int b
   uint16_t* at = tok[1] + kOneMost;                          // [warp][digit]
   __shared__ uint32_t warp_tot[kRadix / 32];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int rounds = (T + kOneThreads - 1) / kOneThreads;    // at most 16
-  for (int k = tid; k < T; k += kOneThreads) {
-    key[0][k] = key_of(ids, nullptr, k, V, status);
-    tok[0][k] = static_cast<uint16_t>(k);
-  }
+  const int base = w * (32 * R);
   const uint32_t mask = (1u << bits) - 1u;
-  const int base = w * rounds * 32;
+  uint32_t k[R];
+  uint16_t tk[R];
+  {
+    int64_t id[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) id[r] = base + r * 32 + lane < T ? __ldg(ids + base + r * 32 + lane) : 0;
+    bool bad = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool in = base + r * 32 + lane < T, valid = id[r] >= 0 && id[r] < V;
+      bad |= in && !valid;
+      k[r] = static_cast<uint32_t>(valid ? id[r] : V);
+      tk[r] = static_cast<uint16_t>(base + r * 32 + lane);
+    }
+    if (bad) atomicCAS(status, 0, TTL_ERR_DEVICE);
+  }
   for (int pass = 0; pass < passes; ++pass) {
-    const uint32_t* ki = key[pass & 1];
-    const uint16_t* ti = tok[pass & 1];
-    uint32_t* ko = key[(pass & 1) ^ 1];
-    uint16_t* to = tok[(pass & 1) ^ 1];
     const int shift = pass * bits;
-    for (int d = lane; d < kRadix; d += 32) at[w * kRadix + d] = 0;
-    __syncthreads();                                         // the keys are in place, the counts zero
-    for (int r = 0; r < rounds; ++r) {
-      const int k = base + r * 32 + lane;
-      const uint32_t d = k < T ? (ki[k] >> shift) & mask : kRadix;
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
-      if (k < T && lane == __ffs(peers) - 1) at[w * kRadix + d] += static_cast<uint16_t>(__popc(peers));
+    uint32_t* ko = key[pass & 1];
+    uint16_t* to = tok[pass & 1];
+    for (int d = lane; d < kRadix / 2; d += 32) reinterpret_cast<uint32_t*>(at + w * kRadix)[d] = 0;
+    __syncwarp();
+    uint32_t peers[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool in = base + r * 32 + lane < T;
+      const uint32_t d = (k[r] >> shift) & mask;
+      peers[r] = same_digit(d, bits, __ballot_sync(0xffffffffu, in));
+      if (in && lane == __ffs(peers[r]) - 1) at[w * kRadix + d] += static_cast<uint16_t>(__popc(peers[r]));
       __syncwarp();
     }
     __syncthreads();
     // first place of warp w's keys of digit d: all smaller digits, then this digit's in the warps before
     uint32_t mine = 0, inc = 0;
     if (tid < kRadix) {
+#pragma unroll
       for (int j = 0; j < kOneWarps; ++j) mine += at[j * kRadix + tid];
       inc = mine;
 #pragma unroll
@@ -222,6 +245,7 @@ __device__ void sort_one(const int64_t* ids, int T, int64_t V, int passes, int b
     if (tid < kRadix) {
       uint32_t run = inc - mine;
       for (int j = 0; j < w; ++j) run += warp_tot[j];
+#pragma unroll
       for (int j = 0; j < kOneWarps; ++j) {
         const uint32_t c = at[j * kRadix + tid];
         at[j * kRadix + tid] = static_cast<uint16_t>(run);
@@ -229,28 +253,36 @@ __device__ void sort_one(const int64_t* ids, int T, int64_t V, int passes, int b
       }
     }
     __syncthreads();
-    for (int r = 0; r < rounds; ++r) {
-      const int k = base + r * 32 + lane;
-      const bool in = k < T;
-      const uint32_t key_k = in ? ki[k] : 0u;
-      const uint32_t d = in ? (key_k >> shift) & mask : kRadix;
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool in = base + r * 32 + lane < T;
+      const uint32_t d = (k[r] >> shift) & mask;
       uint32_t place = 0;
-      if (in) place = at[w * kRadix + d] + __popc(peers & ((1u << lane) - 1u));
+      if (in) place = at[w * kRadix + d] + __popc(peers[r] & ((1u << lane) - 1u));
       __syncwarp();
-      if (in && lane == __ffs(peers) - 1) at[w * kRadix + d] += static_cast<uint16_t>(__popc(peers));
+      if (in && lane == __ffs(peers[r]) - 1) at[w * kRadix + d] += static_cast<uint16_t>(__popc(peers[r]));
       __syncwarp();
       if (in) {
         if (pass + 1 == passes) {
-          keys_out[place] = key_k;
-          toks_out[place] = ti[k];
+          keys_out[place] = k[r];
+          toks_out[place] = tk[r];
         } else {
-          ko[place] = key_k;
-          to[place] = ti[k];
+          ko[place] = k[r];
+          to[place] = tk[r];
         }
       }
     }
-    __syncthreads();
+    if (pass + 1 < passes) {
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int i = base + r * 32 + lane;
+        if (i < T) {
+          k[r] = ko[i];
+          tk[r] = to[i];
+        }
+      }
+    }
   }
 }
 
@@ -284,8 +316,11 @@ __global__ void __launch_bounds__(kOneThreads) sort_fill_kernel(const __grid_con
                                                                 uint32_t* toks_out, uint32_t* runs, int* status) {
   extern __shared__ __align__(16) uint8_t one_smem[];
   if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) runs[0] = 0;
-    sort_one(ids, T, V, passes, bits, keys_out, toks_out, status, one_smem);
+    if (threadIdx.x < 2) runs[threadIdx.x] = 0;
+    if (T <= kOneThreads) sort_one<1>(ids, T, V, passes, bits, keys_out, toks_out, status, one_smem);
+    else if (T <= 4 * kOneThreads) sort_one<4>(ids, T, V, passes, bits, keys_out, toks_out, status, one_smem);
+    else if (T <= 8 * kOneThreads) sort_one<8>(ids, T, V, passes, bits, keys_out, toks_out, status, one_smem);
+    else sort_one<16>(ids, T, V, passes, bits, keys_out, toks_out, status, one_smem);
   } else {
     fill_slice(G, ids, T, V, Vs, h, blockIdx.x - 1, gridDim.x - 1, one_smem);
   }
@@ -295,6 +330,7 @@ __global__ void __launch_bounds__(kOneThreads) sort_fill_kernel(const __grid_con
 
 constexpr int kSumThreads = 256;
 constexpr int kMaxChunk = 1 << 20;   // places per chunk
+constexpr int kShortRun = 4;         // further chunks of a run that one thread adds up alone
 
 __device__ __forceinline__ float* row_of(const GradTables& G, uint32_t key, int64_t Vs, int64_t h) {
   const uint32_t i = key / static_cast<uint32_t>(Vs);
@@ -336,8 +372,11 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_con
   const int64_t col = (static_cast<int64_t>(blockIdx.y) * kSumThreads + threadIdx.x) * 8;
   const uint32_t first = keys[lo], last = keys[hi - 1];
   bool began = lo == 0 || keys[lo - 1] != first;
-  if (blockIdx.y == 0 && threadIdx.x == 0 && last < V && hi < T && keys[hi] == last && (began || first != last))
-    runs[1 + atomicAdd(runs, 1u)] = blockIdx.x;              // (their order does not matter)
+  if (blockIdx.y == 0 && threadIdx.x == 0 && last < V && hi < T && keys[hi] == last && (began || first != last)) {                                                          // (the lists' order does not matter)
+    const int64_t far = (static_cast<int64_t>(blockIdx.x) + 1 + kShortRun) * C;
+    if (far < T && keys[far] == last) runs[2 + gridDim.x - 1 - atomicAdd(runs + 1, 1u)] = blockIdx.x;
+    else runs[2 + atomicAdd(runs, 1u)] = blockIdx.x;
+  }
   float a[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) a[j] = 0.0f;
@@ -388,20 +427,44 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_con
   }
 }
 
-// Joins the runs that go on past their chunk.  A CTA takes 128 columns of one run: sixteen lanes hold the columns,
-// sixteen groups each every sixteenth partial sum, and the groups are added in order.
+// Joins the runs that go on past their chunk: first those that end within the next kShortRun chunks (eight columns per
+// thread, the partial sums one after the other), then the longer ones, 128 columns of one run per CTA: sixteen
+// lanes hold the columns, sixteen groups each every sixteenth partial sum, and the groups are added in order.
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const __grid_constant__ GradTables G,
                                                                  const uint32_t* keys, int64_t T, int64_t h,
-                                                                 int64_t Vs, int64_t V, int C, float scale,
-                                                                 int accumulate, const float* head, const float* tail,
-                                                                 const uint32_t* runs) {
+                                                                 int64_t Vs, int C, float scale, int accumulate,
+                                                                 const float* head, const float* tail,
+                                                                 const uint32_t* runs, int chunks) {
   __shared__ float red[16][16][9];
-  const int vec = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int64_t blocks = (h + 127) / 128;
-  const int64_t items = static_cast<int64_t>(runs[0]) * blocks;
+  const int64_t wide = (h + kSumThreads * 8 - 1) / (kSumThreads * 8), narrow = (h + 127) / 128;
+  const int64_t shorts = static_cast<int64_t>(runs[0]) * wide, items = shorts + static_cast<int64_t>(runs[1]) * narrow;
+  auto add = [&](float (&a)[8], int64_t b, int64_t n, int64_t col) {
+    const float4* p = reinterpret_cast<const float4*>((n == b ? tail : head) + n * h + col);
+    const float4 u = p[0], v = p[1];
+    a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
+    a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
+  };
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t b = runs[1 + it / blocks];
-    const int64_t col = (it % blocks) * 128 + vec * 8;
+    float a[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+    if (it < shorts) {
+      const int64_t b = runs[2 + it / wide];
+      const int64_t col = ((it % wide) * kSumThreads + threadIdx.x) * 8;
+      if (col >= h) continue;
+      const uint32_t key = keys[(b + 1) * C];
+      bool in[kShortRun + 1];
+#pragma unroll
+      for (int n = 0; n <= kShortRun; ++n) in[n] = n < 2 || ((b + n) * C < T && keys[(b + n) * C] == key);
+#pragma unroll
+      for (int n = 0; n <= kShortRun; ++n)
+        if (in[n]) add(a, b, b + n, col);
+      row_out(row_of(G, key, Vs, h) + col, a, scale, accumulate);
+      continue;
+    }
+    const int vec = threadIdx.x & 15, part = threadIdx.x >> 4;
+    const int64_t b = runs[2 + chunks - 1 - (it - shorts) / narrow];
+    const int64_t col = ((it - shorts) % narrow) * 128 + vec * 8;
     const uint32_t key = keys[(b + 1) * C];
     // the last chunk that the run enters: places are sorted, so by bisection
     int64_t l = b + 1, r = (T - 1) / C + 1;                  // keys[l C] == key; r: not, or past the end
@@ -409,17 +472,9 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const __grid_co
       const int64_t m = (l + r) >> 1;
       if (keys[m * C] == key) l = m; else r = m;
     }
-    float a[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = 0.0f;
     if (col < h) {
 #pragma unroll 4
-      for (int64_t n = b + part; n <= l; n += 16) {
-        const float4* p = reinterpret_cast<const float4*>((n == b ? tail : head) + n * h + col);
-        const float4 u = p[0], v = p[1];
-        a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
-        a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
-      }
+      for (int64_t n = b + part; n <= l; n += 16) add(a, b, n, col);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) red[part][vec][j] = a[j];
@@ -455,7 +510,7 @@ SortPlan plan_of(int64_t T, int64_t h) {
   p.keys = round256(static_cast<size_t>(T) * 4);
   p.counts = round256(static_cast<size_t>(kRadix) * p.nb * 4);
   p.part = round256(static_cast<size_t>(p.chunks) * h * 4);
-  p.runs = round256(static_cast<size_t>(p.chunks + 1) * 4);
+  p.runs = round256(static_cast<size_t>(p.chunks + 2) * 4);
   return p;
 }
 
@@ -619,7 +674,7 @@ extern "C" int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t
   const dim3 grid(static_cast<unsigned>(p.chunks), static_cast<unsigned>((h / 8 + kSumThreads - 1) / kSumThreads));
   embed_sum_kernel<<<grid, kSumThreads, 0, s>>>(G, k_in, t_in, reinterpret_cast<const __nv_bfloat16*>(dY), lddy, T, h,
                                                 Vs, V, p.C, scale, accumulate, head, tail, runs);
-  embed_join_kernel<<<static_cast<unsigned>(sms) * 2, kSumThreads, 0, s>>>(G, k_in, T, h, Vs, V, p.C, scale, accumulate,
-                                                                          head, tail, runs);
+  embed_join_kernel<<<static_cast<unsigned>(sms) * 2, kSumThreads, 0, s>>>(G, k_in, T, h, Vs, p.C, scale, accumulate,
+                                                                          head, tail, runs, static_cast<int>(p.chunks));
   return cuda_check(cudaGetLastError(), "embedding gradient launch");
 }
