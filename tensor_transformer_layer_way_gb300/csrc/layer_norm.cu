@@ -21,7 +21,7 @@ namespace ttl {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormParts = 304;   // partial sums of the weight gradients: two per SM of a 152-SM part
+constexpr int kNormParts = 456;   // partial sums of the weight gradients: at most three per SM of a 152-SM part
 
 struct NormFwd {
   const void* x[kMaxShards];
@@ -105,8 +105,8 @@ struct Cursor {
 };
 
 // ------------------------------------------------------------------ rows held in registers
-// Short rows, and rows that do not start on 16 bytes: a row belongs to W warps; each thread holds NV words of B
-// bytes of it (16 where every row starts on 16 bytes and holds whole words, else 4 or 2), so the row is read once and the weights stay in registers over
+// Rows below 1 KiB: a row belongs to W warps; each thread holds NV words of B bytes of it (16 where every row
+// starts on 16 bytes and holds whole words, else 4 or 2), so the row is read once and the weights stay in registers over
 // the persistent loop.  The next row's words are loaded before this one's sums.  A CTA of narrow rows has
 // several groups of W warps, each with rows of its own.
 
@@ -413,10 +413,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ rows through shared memory
-// Rows of 2 KiB and more on 16-byte boundaries: a ring of whole rows in shared memory, filled by bulk copies
-// that run several rows ahead, so the bytes in flight do not depend on how many registers the sums take.
-// The group's first thread starts the copy of row n + stages as soon as the group has met over row n's sums:
-// by then every thread holds its words.
+// Rows of 1 KiB and more: a ring of whole rows in shared memory, filled by bulk copies that run several rows ahead,
+// so the bytes in flight do not depend on how many registers the sums take.  A bulk copy moves whole 16-byte
+// pieces, so a row that does not start on one is copied with its neighbours' bytes (they belong to the same
+// slab; at the slab's own ends the copy is cut and the few elements outside it are stored beside it by hand), and
+// its words are read from shared memory at the row's own offset.
 
 constexpr int kMaxStages = 6;
 constexpr uint64_t kNormTimeout = 2000000000ull;
@@ -428,10 +429,77 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-template <typename T, int NV>
+// One input's row in shared memory.
+struct RowSpan {
+  const uint8_t* row;        // global address of the row
+  int skip;                  // bytes from the row's 16-byte piece to its start
+  int lo, hi;                // bytes of the row that the copy brings: [lo, hi)
+};
+
+// Row k of a slab of `rows` rows of row_bytes bytes every ld_bytes.
+template <int B>
+__device__ __forceinline__ RowSpan span_of(const void* slab, int64_t rows, int64_t ld_bytes, int row_bytes, int64_t k) {
+  RowSpan s;
+  const uint8_t* base = static_cast<const uint8_t*>(slab);
+  s.row = base + k * ld_bytes;
+  s.skip = B == 16 ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(s.row) & 15);
+  s.lo = 0;
+  s.hi = row_bytes;
+  if constexpr (B != 16) {
+    if (s.skip && k * ld_bytes < s.skip) s.lo = 16 - s.skip;              // the piece would begin before the slab
+    const int over = (s.skip + row_bytes) & 15;
+    if (over && (rows - 1 - k) * ld_bytes < 16 - over) s.hi = row_bytes - over;   // or end after it
+  }
+  return s;
+}
+
+// The whole pieces that hold bytes [lo, hi) of the row, to the place that its first piece has at dst.
+template <int B>
+__device__ __forceinline__ uint32_t span_bytes(const RowSpan& s) {
+  if constexpr (B == 16) return static_cast<uint32_t>(s.hi);
+  const int from = s.lo ? s.skip + s.lo : 0, to = (s.skip + s.hi + 15) & ~15;
+  return static_cast<uint32_t>(to - from);
+}
+template <int B>
+__device__ __forceinline__ void span_load(const RowSpan& s, uint8_t* dst, uint64_t* bar) {
+  const int from = B != 16 && s.lo ? s.skip + s.lo : 0;
+  bulk_load(dst + from, s.row - s.skip + from, span_bytes<B>(s), bar);
+}
+// Bytes that an input's row takes in a stage.
+template <int B>
+__host__ __device__ __forceinline__ uint32_t span_room(int64_t row_bytes) {
+  return static_cast<uint32_t>(B == 16 ? row_bytes : (row_bytes + 15 + 15) / 16 * 16);
+}
+
+// Whether the copy left bytes of the row out, and those bytes by hand (fewer than 16 at either end, by one warp).
+template <int B>
+__device__ __forceinline__ bool span_cut(const RowSpan& s, int row_bytes) {
+  return B != 16 && (s.lo > 0 || s.hi < row_bytes);
+}
+template <int B>
+__device__ __forceinline__ void span_mend(const RowSpan& s, uint8_t* at, int row_bytes) {
+  using Wd = typename Word<B>::type;
+  const int lane = threadIdx.x & 31;
+  const int c = lane < 16 ? lane * B : s.hi + (lane - 16) * B;
+  if (lane < 16 ? c < s.lo : c < row_bytes)
+    *reinterpret_cast<Wd*>(at + s.skip + c) = *reinterpret_cast<const Wd*>(s.row + c);
+  fence_proxy_async_smem();   // a later copy writes the same bytes
+}
+
+// Word v of the row.
+template <int B>
+__device__ __forceinline__ typename Word<B>::type span_word(const RowSpan& s, const uint8_t* at, int v) {
+  return *reinterpret_cast<const typename Word<B>::type*>(at + s.skip + v * B);
+}
+
+// The arithmetic runs on pairs of values (two fp32 operations per instruction): it is the number of instructions,
+// more than the bytes, that the row's chain of exchanges leaves no room for.  A value past the row's end is 0.
+
+template <typename T, int B, int NV>
 __global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_ring_kernel(const __grid_constant__ NormFwd P, int W, int G,
                                                                        int stages) {
-  constexpr int E = 16 / sizeof(T);
+  using Wd = typename Word<B>::type;
+  constexpr int E = B / sizeof(T);
   extern __shared__ __align__(16) uint8_t ring[];     // [G][stages][x, r]
   __shared__ float2 red[2][kMaxWarps];
   __shared__ float own_mean[2][kMaxWarps];
@@ -440,25 +508,28 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_ring_kernel(const __g
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / W, gw = warp % W;
-  const int words = static_cast<int>(P.h / E);
+  const int words = static_cast<int>(P.h / E), row_bytes = words * B;
   const int v0 = gw * 32 + lane, vs = W * 32;
   const bool res = P.r[0] != nullptr;
-  const uint32_t row_bytes = static_cast<uint32_t>(words) * 16;
-  const uint32_t stage_bytes = row_bytes * (res ? 2 : 1);
+  const int64_t ldx = P.ldx * static_cast<int64_t>(sizeof(T)), ldr = P.ldr * static_cast<int64_t>(sizeof(T));
+  const uint32_t room = span_room<B>(row_bytes), stage_bytes = room * (res ? 2 : 1);
   uint8_t* mine = ring + static_cast<size_t>(group) * stages * stage_bytes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * G + group;
   volatile int* ab = &abort_flag;
   Cursor ahead(first, P.rows);      // the next row to be copied (used by the group's first thread)
   auto start = [&](int st) {
-    const int i = ahead.i;
-    const int64_t k = ahead.k;
+    const RowSpan sx = span_of<B>(P.x[ahead.i], P.rows, ldx, row_bytes, ahead.k);
+    uint32_t bytes = span_bytes<B>(sx);
+    if (res) {
+      const RowSpan sr = span_of<B>(P.r[ahead.i], P.rows, ldr, row_bytes, ahead.k);
+      mbar_arrive_expect_tx(&full[group][st], bytes + span_bytes<B>(sr));
+      span_load<B>(sr, mine + st * stage_bytes + room, &full[group][st]);
+    } else {
+      mbar_arrive_expect_tx(&full[group][st], bytes);
+    }
+    span_load<B>(sx, mine + st * stage_bytes, &full[group][st]);
     ahead.move(step, P.rows);
-    mbar_arrive_expect_tx(&full[group][st], stage_bytes);
-    bulk_load(mine + st * stage_bytes, static_cast<const T*>(P.x[i]) + k * P.ldx, row_bytes, &full[group][st]);
-    if (res)
-      bulk_load(mine + st * stage_bytes + row_bytes, static_cast<const T*>(P.r[i]) + k * P.ldr, row_bytes,
-                &full[group][st]);
   };
   if (gw == 0 && lane == 0) {
     for (int st = 0; st < stages; ++st) mbar_init(&full[group][st], 1);
@@ -492,42 +563,65 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_ring_kernel(const __g
   for (int64_t row = first; row < P.total; row += step, it ^= 1, at.move(step, P.rows)) {
     const int i = at.i;
     const int64_t k = at.k;
+    const RowSpan sx = span_of<B>(P.x[i], P.rows, ldx, row_bytes, k);
+    const RowSpan sr = span_of<B>(res ? P.r[i] : P.x[i], P.rows, res ? ldr : ldx, row_bytes, k);
     // (a wait that runs out is in the status word; the group goes on, so that all its warps keep meeting)
     mbar_wait(&full[group][st], ph, ab, P.status, kNormTimeout);
-    const uint4* sx = reinterpret_cast<const uint4*>(mine + st * stage_bytes);
-    float x[NV * E];
-    float sum = 0.0f;
+    uint8_t* px = mine + st * stage_bytes;
+    if (span_cut<B>(sx, row_bytes) || span_cut<B>(sr, row_bytes)) {
+      if (gw == 0) {
+        span_mend<B>(sx, px, row_bytes);
+        if (res) span_mend<B>(sr, px + room, row_bytes);
+      }
+      if (W > 1) group_sync(group, W); else __syncwarp();
+    }
+    constexpr int N = NV * E;
+    float x[N];
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       if (v0 + u * vs < words) {
-        unpack<T, 16>(sx[v0 + u * vs], x + u * E);
+        unpack<T, B>(span_word<B>(sx, px, v0 + u * vs), x + u * E);
         if (res) {
           float r[E];
-          unpack<T, 16>(sx[words + v0 + u * vs], r);
+          unpack<T, B>(span_word<B>(sr, px + room, v0 + u * vs), r);
 #pragma unroll
           for (int e = 0; e < E; ++e) x[u * E + e] += r[e];
-          const uint4 w = pack<T, 16>(x + u * E);      // the stream's type: what is normalised is what is kept
-          unpack<T, 16>(w, x + u * E);
-          __stcs(reinterpret_cast<uint4*>(static_cast<T*>(P.s[i]) + k * P.h) + v0 + u * vs, w);
+          const Wd w = pack<T, B>(x + u * E);          // the stream's type: what is normalised is what is kept
+          unpack<T, B>(w, x + u * E);
+          __stcs(reinterpret_cast<Wd*>(static_cast<T*>(P.s[i]) + k * P.h) + v0 + u * vs, w);
         }
+      } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum += x[u * E + e];
+        for (int e = 0; e < E; ++e) x[u * E + e] = 0.0f;
       }
     }
-    sum = warp_sum(sum);
+    uint64_t acc0 = f2_pack(x[0], x[1]), acc1 = f2_pack(x[2], x[3]);
+#pragma unroll
+    for (int c = 4; c < N; c += 4) {
+      acc0 = fadd2(acc0, f2_pack(x[c], x[c + 1]));
+      acc1 = fadd2(acc1, f2_pack(x[c + 2], x[c + 3]));
+    }
+    const float2 pair = f2_unpack(fadd2(acc0, acc1));
+    const float sum = warp_sum(pair.x + pair.y);
     // The warp's own mean and the squares about it; the warps are joined with the exact shift
     // sum (s - mean)^2 = sum (s - mean_w)^2 + n_w (mean_w - mean)^2, so one exchange is enough.
     float mean = n_mine > 0.0f ? sum / n_mine : 0.0f;
-    float sq = 0.0f;
+    acc0 = acc1 = 0;
+    const uint64_t nm2 = f2_pack(-mean, -mean);
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
-      if (v0 + u * vs < words) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float d = x[u * E + e] - mean;
-          sq = fmaf(d, d, sq);
-        }
+    for (int c = 0; c < N; c += 2) {
+      // (a value past the end takes no part)
+      const bool in0 = v0 + (c / E) * vs < words, in1 = v0 + ((c + 1) / E) * vs < words;
+      uint64_t d = fadd2(f2_pack(x[c], x[c + 1]), nm2);
+      if (!in0 || !in1) {
+        const float2 f = f2_unpack(d);
+        d = f2_pack(in0 ? f.x : 0.0f, in1 ? f.y : 0.0f);
       }
+      if (c & 2) acc1 = ffma2(d, d, acc1);
+      else acc0 = ffma2(d, d, acc0);
+    }
+    const float2 sqp = f2_unpack(fadd2(acc0, acc1));
+    float sq = sqp.x + sqp.y;
     sq = warp_sum(sq);
     if (W > 1) {
       if (lane == 0) {
@@ -551,21 +645,25 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_ring_kernel(const __g
     } else {
       __syncwarp();
     }
+    // every thread of the group holds its words: the buffer is free
     if (gw == 0 && lane == 0 && row + stages * step < P.total) start(st);
     if (++st == stages) {
       st = 0;
       ph ^= 1;
     }
     const float rstd = rsqrtf(fmaf(sq, inv_h, P.eps));
-    uint4* y = reinterpret_cast<uint4*>(static_cast<T*>(P.y[i]) + k * P.h);
+    Wd* y = reinterpret_cast<Wd*>(static_cast<T*>(P.y[i]) + k * P.h);
+    const uint64_t m2 = f2_pack(-mean, -mean), r2 = f2_pack(rstd, rstd);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+      const float2 f = f2_unpack(ffma2(fmul2(fadd2(f2_pack(x[c], x[c + 1]), m2), r2), f2_pack(ga[c], ga[c + 1]),
+                                       f2_pack(be[c], be[c + 1])));
+      x[c] = f.x;
+      x[c + 1] = f.y;
+    }
 #pragma unroll
     for (int u = 0; u < NV; ++u)
-      if (v0 + u * vs < words) {
-        float o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf((x[u * E + e] - mean) * rstd, ga[u * E + e], be[u * E + e]);
-        __stcs(y + v0 + u * vs, pack<T, 16>(o));
-      }
+      if (v0 + u * vs < words) __stcs(y + v0 + u * vs, pack<T, B>(x + u * E));
     if (gw == 0 && lane == 0) {
       P.mean[i][k] = mean;
       P.rstd[i][k] = rstd;
@@ -573,37 +671,52 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_ring_kernel(const __g
   }
 }
 
-template <typename T, int NV>
+// The backward pass.  Up to 16 values a thread, xhat and g stay in registers between the sums and dx (KEEP) and the
+// row's buffer is free with the sums' exchange; with more, the words are read again, and the buffer is free once
+// the group has met over the next row's sums.
+template <typename T, int B, int NV>
 __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_ring_kernel(const __grid_constant__ NormBwd P, int W, int G,
                                                                        int stages) {
-  constexpr int E = 16 / sizeof(T);
-  constexpr bool KEEP = NV * E <= 16;     // xhat and g stay in registers between the sums and dx
+  constexpr bool KEEP = NV * B / sizeof(T) <= 16;
+  using Wd = typename Word<B>::type;
+  constexpr int E = B / sizeof(T);
   extern __shared__ __align__(16) uint8_t ring[];     // [G][stages][x, dy, ds], and then [2][h] sums
   __shared__ float2 red[2][kMaxWarps];
   __shared__ uint64_t full[8][kMaxStages];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / W, gw = warp % W;
-  const int words = static_cast<int>(P.h / E);
+  const int words = static_cast<int>(P.h / E), row_bytes = words * B;
   const int v0 = gw * 32 + lane, vs = W * 32;
   const bool more = P.ds[0] != nullptr;
-  const uint32_t row_bytes = static_cast<uint32_t>(words) * 16;
-  const uint32_t stage_bytes = row_bytes * (more ? 3 : 2);
+  const int64_t ldx = P.ldx * static_cast<int64_t>(sizeof(T)), ldd = P.lddy * static_cast<int64_t>(sizeof(T)),
+                lds = P.ldds * static_cast<int64_t>(sizeof(T));
+  const uint32_t room = span_room<B>(row_bytes), stage_bytes = room * (more ? 3 : 2);
   uint8_t* mine = ring + static_cast<size_t>(group) * stages * stage_bytes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * G + group;
   volatile int* ab = &abort_flag;
   Cursor ahead(first, P.rows);      // the next row to be copied (used by the group's first thread)
+  int64_t ahead_row = first;
   auto start = [&](int st) {
-    const int i = ahead.i;
-    const int64_t k = ahead.k;
-    ahead.move(step, P.rows);
-    uint8_t* dst = mine + st * stage_bytes;
-    mbar_arrive_expect_tx(&full[group][st], stage_bytes);
-    bulk_load(dst, static_cast<const T*>(P.x[i]) + k * P.ldx, row_bytes, &full[group][st]);
-    bulk_load(dst + row_bytes, static_cast<const T*>(P.dy[i]) + k * P.lddy, row_bytes, &full[group][st]);
-    if (more)
-      bulk_load(dst + 2 * row_bytes, static_cast<const T*>(P.ds[i]) + k * P.ldds, row_bytes, &full[group][st]);
+    if (ahead_row < P.total) {
+      uint8_t* dst = mine + st * stage_bytes;
+      uint64_t* bar = &full[group][st];
+      const RowSpan sx = span_of<B>(P.x[ahead.i], P.rows, ldx, row_bytes, ahead.k);
+      const RowSpan sd = span_of<B>(P.dy[ahead.i], P.rows, ldd, row_bytes, ahead.k);
+      const uint32_t bytes = span_bytes<B>(sx) + span_bytes<B>(sd);
+      if (more) {
+        const RowSpan ss = span_of<B>(P.ds[ahead.i], P.rows, lds, row_bytes, ahead.k);
+        mbar_arrive_expect_tx(bar, bytes + span_bytes<B>(ss));
+        span_load<B>(ss, dst + 2 * room, bar);
+      } else {
+        mbar_arrive_expect_tx(bar, bytes);
+      }
+      span_load<B>(sx, dst, bar);
+      span_load<B>(sd, dst + room, bar);
+      ahead.move(step, P.rows);
+    }
+    ahead_row += step;
   };
   if (gw == 0 && lane == 0) {
     for (int st = 0; st < stages; ++st) mbar_init(&full[group][st], 1);
@@ -612,8 +725,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_ring_kernel(const __g
   }
   __syncthreads();
   if (gw == 0 && lane == 0)
-    for (int st = 0; st < stages; ++st)
-      if (first + st * step < P.total) start(st);
+    for (int st = 0; st < stages; ++st) start(st);
   float ga[NV * E], dg[NV * E], db[NV * E];
 #pragma unroll
   for (int u = 0; u < NV; ++u)
@@ -641,77 +753,104 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_ring_kernel(const __g
       next_mean = __ldg(P.mean[at.i] + at.k);
       next_rstd = __ldg(P.rstd[at.i] + at.k);
     }
+    const RowSpan sx = span_of<B>(P.x[i], P.rows, ldx, row_bytes, k);
+    const RowSpan sd = span_of<B>(P.dy[i], P.rows, ldd, row_bytes, k);
     mbar_wait(&full[group][st], ph, ab, P.status, kNormTimeout);
-    const uint4* sx = reinterpret_cast<const uint4*>(mine + st * stage_bytes);
-    float xh[KEEP ? NV * E : 1], g[KEEP ? NV * E : 1];
-    uint4 sw[KEEP ? NV : 1];
-    float s1 = 0.0f, s2 = 0.0f;
+    uint8_t* px = mine + st * stage_bytes;
+    const RowSpan ss = span_of<B>(more ? P.ds[i] : P.x[i], P.rows, more ? lds : ldx, row_bytes, k);
+    if (span_cut<B>(sx, row_bytes) || span_cut<B>(sd, row_bytes) || span_cut<B>(ss, row_bytes)) {
+      if (gw == 0) {
+        span_mend<B>(sx, px, row_bytes);
+        span_mend<B>(sd, px + room, row_bytes);
+        if (more) span_mend<B>(ss, px + 2 * room, row_bytes);
+      }
+      if (W > 1) group_sync(group, W); else __syncwarp();
+    }
+    constexpr int N = NV * E;
+    // xhat = x rstd - mean rstd, g = dy gamma; 0 past the row's end, where gamma and dy are
+    const uint64_t rs2 = f2_pack(rs, rs), mr2 = f2_pack(-mean * rs, -mean * rs);
+    float n[N], q[N];
+    auto read = [&](bool sums_too, uint64_t& a1, uint64_t& a2) {
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
-      if (v0 + u * vs < words) {
-        float x[E], d[E];
-        unpack<T, 16>(sx[v0 + u * vs], x);
-        unpack<T, 16>(sx[words + v0 + u * vs], d);
-        if (KEEP && more) sw[KEEP ? u : 0] = sx[2 * words + v0 + u * vs];
+      for (int u = 0; u < NV; ++u) {
+        if (v0 + u * vs < words) {
+          unpack<T, B>(span_word<B>(sx, px, v0 + u * vs), n + u * E);
+          unpack<T, B>(span_word<B>(sd, px + room, v0 + u * vs), q + u * E);
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int c = u * E + e;
-          const float n = (x[e] - mean) * rs, q = d[e] * ga[c];
-          dg[c] = fmaf(d[e], n, dg[c]);
-          db[c] += d[e];
-          s1 += q;
-          s2 = fmaf(q, n, s2);
-          if (KEEP) {
-            xh[KEEP ? c : 0] = n;
-            g[KEEP ? c : 0] = q;
-          }
+          for (int e = 0; e < E; ++e) n[u * E + e] = q[u * E + e] = 0.0f;
         }
       }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const uint64_t d2 = f2_pack(q[c], q[c + 1]), n2 = ffma2(f2_pack(n[c], n[c + 1]), rs2, mr2);
+        const uint64_t g2 = fmul2(d2, f2_pack(ga[c], ga[c + 1]));
+        if (sums_too) {
+          const float2 fg = f2_unpack(ffma2(d2, n2, f2_pack(dg[c], dg[c + 1])));
+          const float2 fb = f2_unpack(fadd2(d2, f2_pack(db[c], db[c + 1])));
+          dg[c] = fg.x;
+          dg[c + 1] = fg.y;
+          db[c] = fb.x;
+          db[c + 1] = fb.y;
+          a1 = fadd2(a1, g2);
+          a2 = ffma2(g2, n2, a2);
+        }
+        const float2 fn = f2_unpack(n2), fq = f2_unpack(g2);
+        n[c] = fn.x;
+        n[c + 1] = fn.y;
+        q[c] = fq.x;
+        q[c + 1] = fq.y;
+      }
+    };
+    uint64_t a1 = 0, a2 = 0;
+    read(true, a1, a2);
+    Wd sw[KEEP ? NV : 1];
+    if (KEEP && more) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+        if (v0 + u * vs < words) sw[KEEP ? u : 0] = span_word<B>(ss, px + 2 * room, v0 + u * vs);
+    }
+    const float2 f1 = f2_unpack(a1), f2 = f2_unpack(a2);
+    float s1 = warp_sum(f1.x + f1.y), s2 = warp_sum(f2.x + f2.y);
     if (W > 1) {
       if (lane == 0) red[it][warp] = make_float2(s1, s2);
       group_sync(group, W);
-      s1 = s2 = 0.0f;
-#pragma unroll 4
-      for (int w = 0; w < W; ++w) {
-        const float2 o = red[it][group * W + w];
-        s1 += o.x;
-        s2 += o.y;
+      const float2 o = lane < W ? red[it][group * W + lane] : make_float2(0.0f, 0.0f);
+      s1 = o.x;
+      s2 = o.y;
+#pragma unroll
+      for (int q = kMaxWarps / 2; q > 0; q >>= 1) {
+        s1 += __shfl_xor_sync(0xffffffffu, s1, q);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, q);
       }
+      s1 = __shfl_sync(0xffffffffu, s1, 0);
+      s2 = __shfl_sync(0xffffffffu, s2, 0);
     } else {
       __syncwarp();
     }
-    const bool next = row + stages * step < P.total;
-    if (KEEP && gw == 0 && lane == 0 && next) start(st);
+    // the group is done with this row's buffer (or, without KEEP, with the one before): it is filled again
+    if (gw == 0 && lane == 0 && (KEEP || row > first)) start(KEEP ? st : (st == 0 ? stages - 1 : st - 1));
     const float c1 = s1 * inv_h, c2 = s2 * inv_h;
-    uint4* dx = reinterpret_cast<uint4*>(static_cast<T*>(P.dx[i]) + k * P.h);
+    Wd* dx = reinterpret_cast<Wd*>(static_cast<T*>(P.dx[i]) + k * P.h);
+    if (!KEEP) read(false, a1, a2);
+    const uint64_t k1 = f2_pack(-rs * c1, -rs * c1), k2 = f2_pack(-rs * c2, -rs * c2);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+      const float2 f = f2_unpack(ffma2(f2_pack(n[c], n[c + 1]), k2, ffma2(f2_pack(q[c], q[c + 1]), rs2, k1)));
+      q[c] = f.x;
+      q[c + 1] = f.y;
+    }
 #pragma unroll
     for (int u = 0; u < NV; ++u)
       if (v0 + u * vs < words) {
-        float o[E], n[E], q[E];
-        if (!KEEP) {
-          unpack<T, 16>(sx[v0 + u * vs], n);
-          unpack<T, 16>(sx[words + v0 + u * vs], q);
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float nn = KEEP ? xh[KEEP ? u * E + e : 0] : (n[e] - mean) * rs;
-          const float qq = KEEP ? g[KEEP ? u * E + e : 0] : q[e] * ga[u * E + e];
-          o[e] = rs * (qq - c1 - nn * c2);
-        }
         if (more) {
           float d[E];
-          unpack<T, 16>(KEEP ? sw[KEEP ? u : 0] : sx[2 * words + v0 + u * vs], d);
+          unpack<T, B>(KEEP ? sw[KEEP ? u : 0] : span_word<B>(ss, px + 2 * room, v0 + u * vs), d);
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] += d[e];
+          for (int e = 0; e < E; ++e) q[u * E + e] += d[e];
         }
-        __stcs(dx + v0 + u * vs, pack<T, 16>(o));
+        __stcs(dx + v0 + u * vs, pack<T, B>(q + u * E));
       }
-    if (!KEEP) {   // the row was read twice: the group meets again before its buffer is filled
-      if (W > 1) group_sync(group, W); else __syncwarp();
-      if (gw == 0 && lane == 0 && next) start(st);
-    }
     if (++st == stages) {
       st = 0;
       ph ^= 1;
@@ -875,40 +1014,41 @@ bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t row
 }
 
 // How a row of h elements is spread: B bytes per word, NV words per thread, W warps per row, G rows at a
-// time per CTA; stages > 0: through the ring, with that many rows of a group in shared memory (smem bytes
-// in all).  W = 0: wider than all of these, the kernel that reads its row again takes it.
+// time per CTA, `ctas` CTAs on an SM; stages > 0: through the ring, with that many rows of a group in shared memory
+// (smem bytes in all).  W = 0: wider than all of these, the kernel that reads its row again takes it.
 struct Spread {
-  int B, NV, W, G, stages;
+  int B, NV, W, G, stages, ctas;
   size_t smem;
 };
 
 // `inputs` rows (x, r, or x, dy, ds) come in for each row.
 Spread spread_of(int64_t h, int elem, int B, bool bwd, int inputs) {
-  Spread s = {B, 0, 0, 1, 0, 0};
+  Spread s = {B, 0, 0, 1, 0, 2, 0};
   const int64_t words = h * elem / B;
+  const int E = B / elem;
   auto fit = [&](int nv, int warps) {
     if (s.W || words > static_cast<int64_t>(nv) * 32 * warps) return;
     s.NV = nv;
     s.W = static_cast<int>((words + nv * 32 - 1) / (nv * 32));
   };
-  if (B == 16 && h * elem >= 2048) {
+  if (h * elem >= 1024) {
     // 16 values a thread: fewer leave too little work between the row's exchanges, more hold the registers
-    // that other rows need (8192 x 4096: fp32 forward 45 us with four words, 53 with two; fp32 backward, which
-    // keeps two sums per value as well, 80 us with two words, 94 with four; bf16 forward 52 and 56, backward
-    // 72 and 103 us with two and four)
-    if (elem == 4 && !bwd) fit(4, 8);
-    fit(2, 8);
-    fit(2, kMaxWarps);
-    fit(3, kMaxWarps);
-    fit(4, kMaxWarps);
+    // that other rows need (8192 x 4096: fp32 forward 45 us with 16 values, 53 with eight)
+    fit(16 / E, 8);
+    fit(16 / E, kMaxWarps);
+    fit(24 / E, kMaxWarps);
+    fit(32 / E, kMaxWarps);
     if (!s.W) return s;
     if (s.W < 8) s.G = 8 / s.W;
-    const size_t stage = static_cast<size_t>(h) * elem * inputs * s.G;
+    s.ctas = s.W * s.G <= 8 ? 2 : 1;
+    const size_t room = B == 16 ? h * elem : (h * elem + 30) / 16 * 16;
+    const size_t stage = room * inputs * s.G;
     const size_t sums = bwd && s.G > 1 ? static_cast<size_t>(h) * 8 : 0;
-    const size_t room = 112000 - 1024;                       // two CTAs on an SM
-    size_t n = (room - sums) / stage;
+    const size_t budget = 226000 / s.ctas - 2048;
+    size_t n = sums < budget ? (budget - sums) / stage : 0;
     n = n < 2 ? 2 : (n > kMaxStages ? kMaxStages : n);
-    if (n * stage + sums > 220000) {                          // two rows do not fit
+    if (bwd && s.NV * E > 16 && n < 3) n = 3;                 // one of them is the row that is being stored
+    if (n * stage + sums > 224000) {
       s.W = 0;
       return s;
     }
@@ -919,14 +1059,11 @@ Spread spread_of(int64_t h, int elem, int B, bool bwd, int inputs) {
   if (B == 16) {
     fit(1, 1);
     fit(2, 1);
-    fit(4, 1);
   } else {
-    const int hi = bwd && B == 4 && elem == 2 ? 8 : 16;
-    const int caps[3] = {1, 8, kMaxWarps};
-    for (int c : caps)
-      for (int nv = 8; nv <= hi; nv *= 2) fit(nv, c);
+    fit(8, 1);
+    fit(8, 2);
   }
-  if (s.W > 0 && s.W < 8) s.G = 8 / s.W;
+  if (s.W < 8) s.G = 8 / s.W;
   if (bwd && s.G > 1) s.smem = static_cast<size_t>(h) * 8;
   return s;
 }
@@ -952,61 +1089,55 @@ template <typename T, int B, int NV>
 int launch_fwd(const NormFwd& P, const Spread& sp, cudaStream_t s) {
   const int threads = sp.W * sp.G * 32;
   const int64_t ctas = (P.total + sp.G - 1) / sp.G;
-  const int64_t cap = static_cast<int64_t>(num_sms()) * 2;
+  const int64_t cap = static_cast<int64_t>(num_sms()) * sp.ctas;
   const unsigned grid = static_cast<unsigned>(ctas < cap ? ctas : cap);
-  if constexpr (B == 16) {
+  constexpr int E = B / sizeof(T);
+  if constexpr (NV * E == 16 || NV * E == 24 || NV * E == 32) {
     if (sp.stages > 0) {
-      if (int rc = allow_smem<norm_fwd_ring_kernel<T, NV>>(sp.smem)) return rc;
-      norm_fwd_ring_kernel<T, NV><<<grid, threads, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
+      if (int rc = allow_smem<norm_fwd_ring_kernel<T, B, NV>>(sp.smem)) return rc;
+      norm_fwd_ring_kernel<T, B, NV><<<grid, threads, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
       return TTL_OK;
     }
   }
-  if constexpr (B != 16 || NV != 3) norm_fwd_kernel<T, B, NV><<<grid, threads, 0, s>>>(P, sp.W, sp.G);
+  if constexpr (B == 16 ? NV <= 2 : NV == 8) norm_fwd_kernel<T, B, NV><<<grid, threads, 0, s>>>(P, sp.W, sp.G);
   return TTL_OK;
 }
 
 template <typename T, int B, int NV>
 int launch_bwd(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
   const int threads = sp.W * sp.G * 32;
-  if constexpr (B == 16) {
+  constexpr int E = B / sizeof(T);
+  if constexpr (NV * E == 16 || NV * E == 24 || NV * E == 32) {
     if (sp.stages > 0) {
-      if (int rc = allow_smem<norm_bwd_ring_kernel<T, NV>>(sp.smem)) return rc;
-      norm_bwd_ring_kernel<T, NV><<<parts, threads, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
+      if (int rc = allow_smem<norm_bwd_ring_kernel<T, B, NV>>(sp.smem)) return rc;
+      norm_bwd_ring_kernel<T, B, NV><<<parts, threads, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
       return TTL_OK;
     }
   }
-  if constexpr (B != 16 || NV != 3) norm_bwd_kernel<T, B, NV><<<parts, threads, sp.smem, s>>>(P, sp.W, sp.G);
+  if constexpr (B == 16 ? NV <= 2 : NV == 8) norm_bwd_kernel<T, B, NV><<<parts, threads, sp.smem, s>>>(P, sp.W, sp.G);
   return TTL_OK;
 }
 
 template <typename T, int B>
 int pick_fwd(const NormFwd& P, const Spread& sp, cudaStream_t s) {
-  if constexpr (B == 16) {
-    switch (sp.NV) {
-      case 1: return launch_fwd<T, B, 1>(P, sp, s);
-      case 2: return launch_fwd<T, B, 2>(P, sp, s);
-      case 3: return launch_fwd<T, B, 3>(P, sp, s);
-      default: return launch_fwd<T, B, 4>(P, sp, s);
-    }
-  } else {
-    return sp.NV == 8 ? launch_fwd<T, B, 8>(P, sp, s) : launch_fwd<T, B, 16>(P, sp, s);
+  constexpr int E = B / sizeof(T);
+  if (sp.stages > 0) {
+    if (sp.NV == 16 / E) return launch_fwd<T, B, 16 / E>(P, sp, s);
+    return sp.NV == 24 / E ? launch_fwd<T, B, 24 / E>(P, sp, s) : launch_fwd<T, B, 32 / E>(P, sp, s);
   }
+  if constexpr (B == 16) return sp.NV == 1 ? launch_fwd<T, B, 1>(P, sp, s) : launch_fwd<T, B, 2>(P, sp, s);
+  else return launch_fwd<T, B, 8>(P, sp, s);
 }
 
 template <typename T, int B>
 int pick_bwd(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
-  if constexpr (B == 16) {
-    switch (sp.NV) {
-      case 1: return launch_bwd<T, B, 1>(P, sp, parts, s);
-      case 2: return launch_bwd<T, B, 2>(P, sp, parts, s);
-      case 3: return launch_bwd<T, B, 3>(P, sp, parts, s);
-      default: return launch_bwd<T, B, 4>(P, sp, parts, s);
-    }
-  } else if constexpr (sizeof(T) == B) {
-    return sp.NV == 8 ? launch_bwd<T, B, 8>(P, sp, parts, s) : launch_bwd<T, B, 16>(P, sp, parts, s);
-  } else {
-    return launch_bwd<T, B, 8>(P, sp, parts, s);
+  constexpr int E = B / sizeof(T);
+  if (sp.stages > 0) {
+    if (sp.NV == 16 / E) return launch_bwd<T, B, 16 / E>(P, sp, parts, s);
+    return sp.NV == 24 / E ? launch_bwd<T, B, 24 / E>(P, sp, parts, s) : launch_bwd<T, B, 32 / E>(P, sp, parts, s);
   }
+  if constexpr (B == 16) return sp.NV == 1 ? launch_bwd<T, B, 1>(P, sp, parts, s) : launch_bwd<T, B, 2>(P, sp, parts, s);
+  else return launch_bwd<T, B, 8>(P, sp, parts, s);
 }
 
 // The widest word that every row is made of: 16 bytes, or 4, or the element.
@@ -1164,7 +1295,10 @@ extern "C" int ttl_layer_norm_bwd(int t, int64_t rows, int64_t h, int x_type, in
       ptrs |= reinterpret_cast<uintptr_t>(X[i]) | reinterpret_cast<uintptr_t>(dY[i]) |
               reinterpret_cast<uintptr_t>(dX[i]) | (dS ? reinterpret_cast<uintptr_t>(dS[i]) : 0);
     const Spread sp = spread_of(h, xb, word_of(ptrs, ldx | lddy | (dS ? ldds : 0), h, xb), true, dS ? 3 : 2);
-    if (sp.W > 0) parts = static_cast<int>((P.total + sp.G - 1) / sp.G < parts ? (P.total + sp.G - 1) / sp.G : parts);
+    if (sp.W > 0) {
+      const int64_t ctas = (P.total + sp.G - 1) / sp.G, cap = sp.ctas * (kNormParts / 3);
+      parts = static_cast<int>(ctas < cap ? ctas : cap);
+    }
     if (sp.W == 0) {
       if (x_type == TTL_T_F32) norm_bwd_any_kernel<float><<<parts, kNormThreads, 0, s>>>(P);
       else norm_bwd_any_kernel<__nv_bfloat16><<<parts, kNormThreads, 0, s>>>(P);
