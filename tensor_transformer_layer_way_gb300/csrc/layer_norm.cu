@@ -769,21 +769,24 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_ring_kernel(const __g
     constexpr int N = NV * E;
     // xhat = x rstd - mean rstd, g = dy gamma; 0 past the row's end, where gamma and dy are
     const uint64_t rs2 = f2_pack(rs, rs), mr2 = f2_pack(-mean * rs, -mean * rs);
-    float n[N], q[N];
-    auto read = [&](bool sums_too, uint64_t& a1, uint64_t& a2) {
+    float n[KEEP ? N : 2], q[KEEP ? N : 2];
+    // xhat and g of word u of this thread; E is 1 only where words are read in pairs
+    constexpr int U = E == 1 ? 2 : 1;            // words taken together
+    auto read = [&](int u, float (&nn)[U * E], float (&qq)[U * E], bool sums_too, uint64_t& a1, uint64_t& a2) {
 #pragma unroll
-      for (int u = 0; u < NV; ++u) {
-        if (v0 + u * vs < words) {
-          unpack<T, B>(span_word<B>(sx, px, v0 + u * vs), n + u * E);
-          unpack<T, B>(span_word<B>(sd, px + room, v0 + u * vs), q + u * E);
+      for (int w = 0; w < U; ++w) {
+        if (v0 + (u + w) * vs < words) {
+          unpack<T, B>(span_word<B>(sx, px, v0 + (u + w) * vs), nn + w * E);
+          unpack<T, B>(span_word<B>(sd, px + room, v0 + (u + w) * vs), qq + w * E);
         } else {
 #pragma unroll
-          for (int e = 0; e < E; ++e) n[u * E + e] = q[u * E + e] = 0.0f;
+          for (int e = 0; e < E; ++e) nn[w * E + e] = qq[w * E + e] = 0.0f;
         }
       }
 #pragma unroll
-      for (int c = 0; c < N; c += 2) {
-        const uint64_t d2 = f2_pack(q[c], q[c + 1]), n2 = ffma2(f2_pack(n[c], n[c + 1]), rs2, mr2);
+      for (int e = 0; e < U * E; e += 2) {
+        const int c = u * E + e;
+        const uint64_t d2 = f2_pack(qq[e], qq[e + 1]), n2 = ffma2(f2_pack(nn[e], nn[e + 1]), rs2, mr2);
         const uint64_t g2 = fmul2(d2, f2_pack(ga[c], ga[c + 1]));
         if (sums_too) {
           const float2 fg = f2_unpack(ffma2(d2, n2, f2_pack(dg[c], dg[c + 1])));
@@ -796,14 +799,25 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_ring_kernel(const __g
           a2 = ffma2(g2, n2, a2);
         }
         const float2 fn = f2_unpack(n2), fq = f2_unpack(g2);
-        n[c] = fn.x;
-        n[c + 1] = fn.y;
-        q[c] = fq.x;
-        q[c + 1] = fq.y;
+        nn[e] = fn.x;
+        nn[e + 1] = fn.y;
+        qq[e] = fq.x;
+        qq[e + 1] = fq.y;
       }
     };
     uint64_t a1 = 0, a2 = 0;
-    read(true, a1, a2);
+#pragma unroll
+    for (int u = 0; u < NV; u += U) {
+      float nn[U * E], qq[U * E];
+      read(u, nn, qq, true, a1, a2);
+      if constexpr (KEEP) {
+#pragma unroll
+        for (int e = 0; e < U * E; ++e) {
+          n[u * E + e] = nn[e];
+          q[u * E + e] = qq[e];
+        }
+      }
+    }
     Wd sw[KEEP ? NV : 1];
     if (KEEP && more) {
 #pragma unroll
@@ -832,25 +846,37 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_ring_kernel(const __g
     if (gw == 0 && lane == 0 && (KEEP || row > first)) start(KEEP ? st : (st == 0 ? stages - 1 : st - 1));
     const float c1 = s1 * inv_h, c2 = s2 * inv_h;
     Wd* dx = reinterpret_cast<Wd*>(static_cast<T*>(P.dx[i]) + k * P.h);
-    if (!KEEP) read(false, a1, a2);
     const uint64_t k1 = f2_pack(-rs * c1, -rs * c1), k2 = f2_pack(-rs * c2, -rs * c2);
 #pragma unroll
-    for (int c = 0; c < N; c += 2) {
-      const float2 f = f2_unpack(ffma2(f2_pack(n[c], n[c + 1]), k2, ffma2(f2_pack(q[c], q[c + 1]), rs2, k1)));
-      q[c] = f.x;
-      q[c + 1] = f.y;
-    }
+    for (int u = 0; u < NV; u += U) {
+      float nn[U * E], qq[U * E];
+      if constexpr (KEEP) {
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
-      if (v0 + u * vs < words) {
-        if (more) {
-          float d[E];
-          unpack<T, B>(KEEP ? sw[KEEP ? u : 0] : span_word<B>(ss, px + 2 * room, v0 + u * vs), d);
-#pragma unroll
-          for (int e = 0; e < E; ++e) q[u * E + e] += d[e];
+        for (int e = 0; e < U * E; ++e) {
+          nn[e] = n[u * E + e];
+          qq[e] = q[u * E + e];
         }
-        __stcs(dx + v0 + u * vs, pack<T, B>(q + u * E));
+      } else {
+        read(u, nn, qq, false, a1, a2);
       }
+#pragma unroll
+      for (int e = 0; e < U * E; e += 2) {
+        const float2 f = f2_unpack(ffma2(f2_pack(nn[e], nn[e + 1]), k2, ffma2(f2_pack(qq[e], qq[e + 1]), rs2, k1)));
+        qq[e] = f.x;
+        qq[e + 1] = f.y;
+      }
+#pragma unroll
+      for (int w = 0; w < U; ++w)
+        if (v0 + (u + w) * vs < words) {
+          if (more) {
+            float d[E];
+            unpack<T, B>(KEEP ? sw[KEEP ? u + w : 0] : span_word<B>(ss, px + 2 * room, v0 + (u + w) * vs), d);
+#pragma unroll
+            for (int e = 0; e < E; ++e) qq[w * E + e] += d[e];
+          }
+          __stcs(dx + v0 + (u + w) * vs, pack<T, B>(qq + w * E));
+        }
+    }
     if (++st == stages) {
       st = 0;
       ph ^= 1;
@@ -1033,7 +1059,10 @@ Spread spread_of(int64_t h, int elem, int B, bool bwd, int inputs) {
   };
   if (h * elem >= 1024) {
     // 16 values a thread: fewer leave too little work between the row's exchanges, more hold the registers
-    // that other rows need (8192 x 4096: fp32 forward 45 us with 16 values, 53 with eight)
+    // that other rows need (8192 x 4096: fp32 forward 45 us with 16 values, 53 with eight).  The backward pass
+    // holds five registers a value: eight where the words are fp32 or short (fp32 80 us with eight values, 83 with
+    // 16; 4099 x 1001 fp32 19 and 35).
+    if (bwd && (elem == 4 || B < 16)) fit(8 / E, kMaxWarps);
     fit(16 / E, 8);
     fit(16 / E, kMaxWarps);
     fit(24 / E, kMaxWarps);
@@ -1107,7 +1136,7 @@ template <typename T, int B, int NV>
 int launch_bwd(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
   const int threads = sp.W * sp.G * 32;
   constexpr int E = B / sizeof(T);
-  if constexpr (NV * E == 16 || NV * E == 24 || NV * E == 32) {
+  if constexpr (NV * E == 8 || NV * E == 16 || NV * E == 24 || NV * E == 32) {
     if (sp.stages > 0) {
       if (int rc = allow_smem<norm_bwd_ring_kernel<T, B, NV>>(sp.smem)) return rc;
       norm_bwd_ring_kernel<T, B, NV><<<parts, threads, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
@@ -1133,6 +1162,8 @@ template <typename T, int B>
 int pick_bwd(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
   constexpr int E = B / sizeof(T);
   if (sp.stages > 0) {
+    if constexpr (sizeof(T) == 4 || B < 16)
+      if (sp.NV == 8 / E) return launch_bwd<T, B, 8 / E>(P, sp, parts, s);
     if (sp.NV == 16 / E) return launch_bwd<T, B, 16 / E>(P, sp, parts, s);
     return sp.NV == 24 / E ? launch_bwd<T, B, 24 / E>(P, sp, parts, s) : launch_bwd<T, B, 32 / E>(P, sp, parts, s);
   }
