@@ -17,6 +17,7 @@
 
 #include <mutex>
 
+#include "launch_after.cuh"
 #include "ttl_device.cuh"
 #include "ttl_internal.h"
 
@@ -366,6 +367,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_con
                                                                 int accumulate, float* head, float* tail,
                                                                 uint32_t* runs) {
   constexpr int W = 128;                                     // places looked at together
+  await_previous();
   __shared__ const __nv_bfloat16* src[W];
   __shared__ float* dst[W];                                  // where the run that ends at the place goes; null: it goes on
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * C, hi = lo + C < T ? lo + C : T;
@@ -436,6 +438,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const __grid_co
                                                                  const float* head, const float* tail,
                                                                  const uint32_t* runs, int chunks) {
   __shared__ float red[16][16][9];
+  await_previous();
   const int64_t wide = (h + kSumThreads * 8 - 1) / (kSumThreads * 8), narrow = (h + 127) / 128;
   const int64_t shorts = static_cast<int64_t>(runs[0]) * wide, items = shorts + static_cast<int64_t>(runs[1]) * narrow;
   auto add = [&](float (&a)[8], int64_t b, int64_t n, int64_t col) {
@@ -672,9 +675,14 @@ extern "C" int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t
   }
   TraceScope trace(s, TTL_K_EMBED, 0.0, static_cast<double>(T) * h * 2.0);
   const dim3 grid(static_cast<unsigned>(p.chunks), static_cast<unsigned>((h / 8 + kSumThreads - 1) / kSumThreads));
-  embed_sum_kernel<<<grid, kSumThreads, 0, s>>>(G, k_in, t_in, reinterpret_cast<const __nv_bfloat16*>(dY), lddy, T, h,
-                                                Vs, V, p.C, scale, accumulate, head, tail, runs);
-  embed_join_kernel<<<static_cast<unsigned>(sms) * 2, kSumThreads, 0, s>>>(G, k_in, T, h, Vs, p.C, scale, accumulate,
-                                                                          head, tail, runs, static_cast<int>(p.chunks));
-  return cuda_check(cudaGetLastError(), "embedding gradient launch");
+  if ((rc = cuda_check(launch_after(embed_sum_kernel, grid, kSumThreads, 0, s, G, k_in, t_in,
+                                    reinterpret_cast<const __nv_bfloat16*>(dY), lddy, T, h, Vs, V, p.C, scale,
+                                    accumulate, head, tail, runs),
+                       "embed_sum_kernel launch")))
+    return rc;
+  return cuda_check(launch_after(embed_join_kernel, dim3(static_cast<unsigned>(sms) * 2), kSumThreads, 0, s, G, k_in, T, h,
+                                 Vs, p.C, scale, accumulate, static_cast<const float*>(head),
+                                 static_cast<const float*>(tail), static_cast<const uint32_t*>(runs),
+                                 static_cast<int>(p.chunks)),
+                    "embed_join_kernel launch");
 }

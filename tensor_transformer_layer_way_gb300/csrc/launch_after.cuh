@@ -1,0 +1,31 @@
+// Launches of a kernel that follows another of the same call on the same stream: its blocks may be brought up
+// while the last blocks of the one before still run, and await_previous() is where they wait for its results.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <utility>
+
+namespace ttl {
+
+// Every thread of the following kernel calls this before it reads what the kernel before wrote, and before it
+// writes anything that kernel may still read.
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
+                         Args&&... args) {
+  cudaLaunchAttribute overlap;
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = dim3(block);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  config.attrs = &overlap;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, std::forward<Args>(args)...);
+}
+
+}  // namespace ttl

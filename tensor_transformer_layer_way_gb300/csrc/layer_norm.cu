@@ -14,6 +14,7 @@
 
 #include <mutex>
 
+#include "launch_after.cuh"
 #include "ttl_device.cuh"
 #include "ttl_internal.h"
 
@@ -985,10 +986,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_any_kernel(const __grid
 }
 
 // dgamma and dbeta: the partial sums joined in the order of the CTAs.  One warp per 32 columns of
-// one of the two, eight warps of a CTA each taking every eighth part.
-__global__ void __launch_bounds__(256) norm_join_kernel(const float* part, int nparts, int64_t h, float* dgamma,
-                                                        float* dbeta, int accumulate) {
-  __shared__ float red[8][33];
+// one of the two, 32 warps of a CTA each taking every 32nd part.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const float* part, int nparts, int64_t h, float* dgamma,
+                                                         float* dbeta, int accumulate) {
+  __shared__ float red[32][33];
+  await_previous();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float* out = blockIdx.y ? dbeta : dgamma;
@@ -996,13 +998,13 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const float* part, int n
   float s = 0.0f;
   if (c < h)
 #pragma unroll 8
-    for (int p = w; p < nparts; p += 8) s += part[(static_cast<int64_t>(p) * 2 + blockIdx.y) * h + c];
+    for (int p = w; p < nparts; p += 32) s += part[(static_cast<int64_t>(p) * 2 + blockIdx.y) * h + c];
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < h) {
     float v = red[0][lane];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) v += red[j][lane];
+    for (int j = 1; j < 32; ++j) v += red[j][lane];
     out[c] = accumulate ? out[c] + v : v;
   }
 }
@@ -1344,7 +1346,7 @@ extern "C" int ttl_layer_norm_bwd(int t, int64_t rows, int64_t h, int x_type, in
     if (rc || (rc = cuda_check(cudaGetLastError(), "layer norm backward launch"))) return rc;
   }
   TraceScope trace(s, TTL_K_NORM, 0.0, 8.0 * h * parts);
-  norm_join_kernel<<<dim3(static_cast<unsigned>((h + 31) / 32), 2), 256, 0, s>>>(static_cast<const float*>(ws), parts,
-                                                                                 h, dgamma, dbeta, accumulate);
-  return cuda_check(cudaGetLastError(), "norm_join_kernel launch");
+  return cuda_check(launch_after(norm_join_kernel, dim3(static_cast<unsigned>((h + 31) / 32), 2), 1024, 0, s,
+                                 static_cast<const float*>(ws), parts, h, dgamma, dbeta, accumulate),
+                    "norm_join_kernel launch");
 }

@@ -4,6 +4,7 @@
 
 #include <cmath>
 
+#include "launch_after.cuh"
 #include "ttl_device.cuh"
 #include "ttl_internal.h"
 

@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   const PackArgs& A = P.a;
   const int warp = uniform_warp();
   const int lane = threadIdx.x & 31;
+  await_previous();   // (the dQ kernel; through it D and the list)
   const int total = (A.kv_list ? __ldg(A.kv_head) : P.tiles) * P.lanes;
   int* status = A.status;
   const uint64_t tmo = P.timeout_ns;
@@ -568,6 +569,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
 // of dK or dV.
 template <int D>
 __global__ void __launch_bounds__(256) pack_join_kernel(const __grid_constant__ PackArgs A) {
+  await_previous();
   const int lane = threadIdx.x & 31;
   const int lanes = A.t * A.nkvl;
   const int64_t rows = static_cast<int64_t>(__ldg(A.kv_head + 1)) * lanes * 2 * kTile;
@@ -606,10 +608,8 @@ int pack_attn_join_launch(const PackArgs& A, int d, cudaStream_t stream) {
   TraceScope trace(stream, TTL_K_OTHER, 0.0, 0.0);
   const unsigned grid = static_cast<unsigned>(num_sms()) * 4;
   if (d == 128)
-    pack_join_kernel<128><<<grid, 256, 0, stream>>>(A);
-  else
-    pack_join_kernel<64><<<grid, 256, 0, stream>>>(A);
-  return cuda_check(cudaGetLastError(), "pack_join_kernel launch");
+    return cuda_check(launch_after(pack_join_kernel<128>, dim3(grid), 256, 0, stream, A), "pack_join_kernel launch");
+  return cuda_check(launch_after(pack_join_kernel<64>, dim3(grid), 256, 0, stream, A), "pack_join_kernel launch");
 }
 
 int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream) {
@@ -638,14 +638,14 @@ int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream) {
     if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dkv_kernel<128>), kPackDkv128, KvCfg<128>::SMEM,
                                  "cudaFuncSetAttribute(packed attention dK dV)")))
       return rc;
-    pack_dkv_kernel<128><<<grid, kKvThreads, KvCfg<128>::SMEM, stream>>>(P);
+    rc = cuda_check(launch_after(pack_dkv_kernel<128>, dim3(grid), kKvThreads, KvCfg<128>::SMEM, stream, P), "pack_dkv_kernel launch");
   } else {
     if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dkv_kernel<64>), kPackDkv64, KvCfg<64>::SMEM,
                                  "cudaFuncSetAttribute(packed attention dK dV)")))
       return rc;
-    pack_dkv_kernel<64><<<grid, kKvThreads, KvCfg<64>::SMEM, stream>>>(P);
+    rc = cuda_check(launch_after(pack_dkv_kernel<64>, dim3(grid), kKvThreads, KvCfg<64>::SMEM, stream, P), "pack_dkv_kernel launch");
   }
-  return cuda_check(cudaGetLastError(), "pack_dkv_kernel launch");
+  return rc;
 }
 
 }  // namespace ttl

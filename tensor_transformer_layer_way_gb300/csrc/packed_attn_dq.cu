@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  await_previous();   // D and the list
   if (blockIdx.x == 0) check_docs(A.cu, A.batch, A.T, status);
   tc_fence_before_sync();
   __syncthreads();
@@ -544,14 +545,14 @@ int pack_attn_dq_launch(const PackArgs& A, int d, cudaStream_t stream) {
     if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dq_kernel<128>), kPackDq128, DqCfg<128>::SMEM,
                                  "cudaFuncSetAttribute(packed attention dQ)")))
       return rc;
-    pack_dq_kernel<128><<<grid, kDqThreads, DqCfg<128>::SMEM, stream>>>(P);
+    rc = cuda_check(launch_after(pack_dq_kernel<128>, dim3(grid), kDqThreads, DqCfg<128>::SMEM, stream, P), "pack_dq_kernel launch");
   } else {
     if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dq_kernel<64>), kPackDq64, DqCfg<64>::SMEM,
                                  "cudaFuncSetAttribute(packed attention dQ)")))
       return rc;
-    pack_dq_kernel<64><<<grid, kDqThreads, DqCfg<64>::SMEM, stream>>>(P);
+    rc = cuda_check(launch_after(pack_dq_kernel<64>, dim3(grid), kDqThreads, DqCfg<64>::SMEM, stream, P), "pack_dq_kernel launch");
   }
-  return cuda_check(cudaGetLastError(), "pack_dq_kernel launch");
+  return rc;
 }
 
 }  // namespace ttl

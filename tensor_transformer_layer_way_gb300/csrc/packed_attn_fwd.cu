@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  await_previous();   // the list, and with it whatever ran before it
   if (blockIdx.x == 0) check_docs(A.cu, A.batch, A.T, status);
   tc_fence_before_sync();
   __syncthreads();
@@ -600,14 +601,14 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stre
     if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_fwd_kernel<128>), kPackFwd128, FwdCfg<128>::SMEM,
                                  "cudaFuncSetAttribute(packed attention forward)")))
       return rc;
-    pack_fwd_kernel<128><<<grid, kFwdThreads, FwdCfg<128>::SMEM, stream>>>(P);
+    rc = cuda_check(launch_after(pack_fwd_kernel<128>, dim3(grid), kFwdThreads, FwdCfg<128>::SMEM, stream, P), "pack_fwd_kernel launch");
   } else {
     if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_fwd_kernel<64>), kPackFwd64, FwdCfg<64>::SMEM,
                                  "cudaFuncSetAttribute(packed attention forward)")))
       return rc;
-    pack_fwd_kernel<64><<<grid, kFwdThreads, FwdCfg<64>::SMEM, stream>>>(P);
+    rc = cuda_check(launch_after(pack_fwd_kernel<64>, dim3(grid), kFwdThreads, FwdCfg<64>::SMEM, stream, P), "pack_fwd_kernel launch");
   }
-  return cuda_check(cudaGetLastError(), "pack_fwd_kernel launch");
+  return rc;
 }
 
 }  // namespace ttl
