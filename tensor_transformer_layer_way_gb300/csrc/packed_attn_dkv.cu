@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kKvThreads = 640;
 constexpr int kKvWarps = 16;   // elementwise warps
-constexpr int kSlots = 2;      // Q and dO tiles
+constexpr int kRing = 5;       // places of the Q and dO tiles: Q_0, dO_0, Q_1, dO_1, ...
 constexpr int kStat = 2;       // lse and D stages
 
 struct KvParams {
@@ -45,12 +45,11 @@ struct KvCfg {
   static constexpr int KB = D / 64;
   static constexpr int TILE = KB * kTile * 128;
   static constexpr int OFF_V = TILE;
-  static constexpr int OFF_Q = 2 * TILE;
-  static constexpr int OFF_DO = OFF_Q + kSlots * TILE;
-  static constexpr int OFF_STAT = OFF_DO + kSlots * TILE;   // float [kStat][2][128]: -lse log2(e), -D
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_STAT = OFF_RING + kRing * TILE;   // float [kStat][2][128]: -lse log2(e), -D
   static constexpr int OFF_ROWS = OFF_STAT + kStat * 1024;  // int [128]: the last query that sees a key
   static constexpr int OFF_BAR = OFF_ROWS + 512;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int SMEM = OFF_BAR + 256;   // (the block begins on 1024 bytes; the kernel checks it)
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
 };
 
@@ -109,22 +108,19 @@ template <int D>
 __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_constant__ KvParams P) {
   using C = KvCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw;
   uint8_t* sK = smem;
   uint8_t* sV = smem + C::OFF_V;
-  uint8_t* sQ = smem + C::OFF_Q;
-  uint8_t* sDO = smem + C::OFF_DO;
+  uint8_t* sRing = smem + C::OFF_RING;
   float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT);
   int* row_hi = reinterpret_cast<int*>(smem + C::OFF_ROWS);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* k_empty = k_full + 1;
   uint64_t* v_full = k_empty + 1;
   uint64_t* v_empty = v_full + 1;
-  uint64_t* q_full = v_empty + 1;
-  uint64_t* q_empty = q_full + kSlots;
-  uint64_t* do_full = q_empty + kSlots;
-  uint64_t* do_empty = do_full + kSlots;
-  uint64_t* st_full = do_empty + kSlots;
+  uint64_t* ring_full = v_empty + 1;
+  uint64_t* ring_empty = ring_full + kRing;
+  uint64_t* st_full = ring_empty + kRing;
   uint64_t* st_empty = st_full + kStat;
   uint64_t* s_full = st_empty + kStat;
   uint64_t* p_full = s_full + 1;
@@ -138,12 +134,16 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* flags = tmem_slot + 2;     // [2][4]: rows of a quadrant to be done again, of dK and of dV
-  static_assert((4 + 4 * kSlots + 2 * kStat + 9) * 8 + 40 <= 256, "barrier area");
+  static_assert((4 + 2 * kRing + 2 * kStat + 9) * 8 + 40 <= 256, "barrier area");
   constexpr uint32_t T_DP = 128, T_DK = 256, T_DV = 384;
 
   const PackArgs& A = P.a;
   const int warp = uniform_warp();
   const int lane = threadIdx.x & 31;
+  if (smem_u32(smem_raw) & 1023u) {   // the tiles' swizzle needs it; every block of the launch ends here alike
+    if (threadIdx.x == 0) atomicCAS(A.status, 0, TTL_ERR_ALIGN);
+    return;
+  }
   await_previous();   // (the dQ kernel; through it D and the list)
   const int total = (A.kv_list ? __ldg(A.kv_head) : P.tiles) * P.lanes;
   int* status = A.status;
@@ -161,11 +161,9 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     mbar_init(k_empty, 1);
     mbar_init(v_full, 1);
     mbar_init(v_empty, 1);
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&q_full[s], 1);
-      mbar_init(&q_empty[s], 1);
-      mbar_init(&do_full[s], 1);
-      mbar_init(&do_empty[s], 1);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&ring_full[s], 1);
+      mbar_init(&ring_empty[s], 1);
     }
     for (int s = 0; s < kStat; ++s) {
       mbar_init(&st_full[s], 1);
@@ -196,7 +194,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
-    int nk = 0, nv = 0, nq = 0, nd = 0;   // loads started: K, V, Q, dO tiles
+    int nk = 0, nv = 0, pos = 0;   // loads started: K, V, ring places
     KvItem ahead = {};
     if (item_at(0) < total) ahead = kv_item(P, item_at(0));   // the coming item is looked up while this one runs
     for (int n = 0; item_at(n) < total; ++n) {
@@ -210,26 +208,23 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           for (int kb = 0; kb < C::KB; ++kb) tma_load_2d(dst + kb * 16384, map, full, x + kb * 64, y);
           return true;
         };
+        auto load_ring = [&](const CUtensorMap* map, int x, int y) {
+          const int slot = pos % kRing;
+          if (!load(sRing + slot * C::TILE, map, &ring_full[slot], &ring_empty[slot], pos / kRing, x, y)) return false;
+          ++pos;
+          return true;
+        };
         for (int t = 0; ok && t < it.steps; ++t) {
-          const int qs = nq % kSlots, ds = nd % kSlots;
           if (t == 0) {
             ok = load(sK, &P.k[it.shard], k_full, k_empty, nk, it.g * D, it.k0);
             nk += ok;
           }
-          if (ok) {
-            ok = load(sQ + qs * C::TILE, &P.q[it.shard], &q_full[qs], &q_empty[qs], nq / kSlots, step_head(it, t) * D,
-                      step_q0(it, t));
-            nq += ok;
-          }
+          ok = ok && load_ring(&P.q[it.shard], step_head(it, t) * D, step_q0(it, t));
           if (ok && t == 0) {
             ok = load(sV, &P.v[it.shard], v_full, v_empty, nv, it.g * D, it.k0);
             nv += ok;
           }
-          if (ok) {
-            ok = load(sDO + ds * C::TILE, &P.dO[it.shard], &do_full[ds], &do_empty[ds], nd / kSlots,
-                      step_head(it, t) * D, step_q0(it, t));
-            nd += ok;
-          }
+          ok = ok && load_ring(&P.dO[it.shard], step_head(it, t) * D, step_q0(it, t));
         }
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
@@ -240,10 +235,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       volatile int* da = reinterpret_cast<volatile int*>(&dummy);
       if (nk > 0) wait_on(k_full, static_cast<uint32_t>(nk - 1) & 1u, da, status, tmo);
       if (nv > 0) wait_on(v_full, static_cast<uint32_t>(nv - 1) & 1u, da, status, tmo);
-      for (int i = nq > kSlots ? nq - kSlots : 0; i < nq; ++i)
-        wait_on(&q_full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u, da, status, tmo);
-      for (int i = nd > kSlots ? nd - kSlots : 0; i < nd; ++i)
-        wait_on(&do_full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u, da, status, tmo);
+      for (int i = pos > kRing ? pos - kRing : 0; i < pos; ++i)
+        wait_on(&ring_full[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, da, status, tmo);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -251,13 +244,13 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // The whole warp runs this loop, one elected lane issues.  A wait that runs out is in the status word and raises
     // the abort flag, after which every wait returns at once: the loop then ends over what is in memory.
     int ni = 0, p = 0;                     // items; steps scored
+    int qs = 0, lap = 0, old = 0;          // ring place of Q_(t + 1), its round; place of Q_t
     const uint64_t kd = smem_desc_sw128(smem_u32(sK), 16, 1024);
     const uint64_t vd = smem_desc_sw128(smem_u32(sV), 16, 1024);
-    const uint64_t qk0 = smem_desc_sw128(smem_u32(sQ), 16, 1024), qn0 = smem_desc_sw128(smem_u32(sQ), 16384, 1024);
-    const uint64_t dk0 = smem_desc_sw128(smem_u32(sDO), 16, 1024), dn0 = smem_desc_sw128(smem_u32(sDO), 16384, 1024);
+    const uint64_t rk0 = smem_desc_sw128(smem_u32(sRing), 16, 1024);      // K-major
+    const uint64_t rn0 = smem_desc_sw128(smem_u32(sRing), 16384, 1024);   // MN-major
     const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
     const uint32_t idesc_acc = idesc_bf16_f32(kTile, D, false, true);
-    static_assert(kSlots == 2, "the Q and dO places are the parity of the step");
     const bool leader = elect_one();
     auto wait = [&](uint64_t* bar, int phase) {
       wait_on(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
@@ -289,12 +282,12 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       // S^T of step t overwrites P^T of the step before, whose dV product was issued before it (the tensor
       // pipe runs one thread's products in order); likewise dP^T and dK.
       for (int t = -1; t < it.steps; ++t) {
-        const int s = p & 1, o = s ^ 1;    // places of step t + 1 and of step t
+        const int ds = qs + 1 == kRing ? 0 : qs + 1;   // place of dO_(t + 1): the one behind Q_(t + 1)
         if (t + 1 < it.steps) {
-          wait(&q_full[s], p >> 1);
+          wait(&ring_full[qs], lap);
           tc_fence_after_sync();
           if (leader) {
-            scores(tmem, kd, desc_advance(qk0, s * C::TILE));
+            scores(tmem, kd, desc_advance(rk0, qs * C::TILE));
             umma_commit(s_full);
             if (t + 2 == it.steps) umma_commit(k_empty);
           }
@@ -303,26 +296,32 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           wait(ds_full, p - 1);
           tc_fence_after_sync();
           if (leader) {
-            sum(tmem + T_DK, tmem + T_DP, desc_advance(qn0, o * C::TILE), t > 0 ? 1u : 0u);
-            umma_commit(&q_empty[o]);
+            sum(tmem + T_DK, tmem + T_DP, desc_advance(rn0, old * C::TILE), t > 0 ? 1u : 0u);
+            umma_commit(&ring_empty[old]);
           }
         }
         if (t + 1 < it.steps) {
           if (t < 0) wait(v_full, ni);
-          wait(&do_full[s], p >> 1);
+          wait(&ring_full[ds], ds == 0 ? lap + 1 : lap);
           tc_fence_after_sync();
           if (leader) {
-            scores(tmem + T_DP, vd, desc_advance(dk0, s * C::TILE));
+            scores(tmem + T_DP, vd, desc_advance(rk0, ds * C::TILE));
             umma_commit(dp_full);
             if (t + 2 == it.steps) umma_commit(v_empty);
           }
           wait(p_full, p);
           tc_fence_after_sync();
           if (leader) {
-            sum(tmem + T_DV, tmem, desc_advance(dn0, s * C::TILE), t >= 0 ? 1u : 0u);
-            umma_commit(&do_empty[s]);
+            sum(tmem + T_DV, tmem, desc_advance(rn0, ds * C::TILE), t >= 0 ? 1u : 0u);
+            umma_commit(&ring_empty[ds]);
           }
           ++p;
+          old = qs;
+          qs += 2;
+          if (qs >= kRing) {
+            qs -= kRing;
+            ++lap;
+          }
         }
         __syncwarp();
         // the coming item is looked up once the first products run
