@@ -22,6 +22,11 @@
 // warpgroup of its own for the results was slower: it leaves the softmax 176 registers, and a key tile of one
 // long document then takes 3200 cycles, with 208 it takes 2700.)
 //
+// What bounds it: shared memory, which S_x = Q_x K^T reads at 128 bytes a cycle for 2000 of the 2700 cycles a
+// pair of key tiles takes.  Measured: one document of 32768 tokens, 4 query heads and 1 KV head of 128: 680 us, 1618
+// TFLOP/s; 8192 tokens in 12 documents, 32 query and 8 KV heads over 8 shards: 101 us.  With many short documents an
+// item costs about 10000 cycles beside its key tiles (masks, the wait for the last product, the result).
+//
 // A masked place enters the product as P = 0, and 0 times an infinite or NaN value is NaN: a row whose
 // result is not finite is computed again by its warp over its own keys alone.
 
@@ -34,7 +39,7 @@
 namespace ttl {
 namespace {
 
-constexpr int kRing = 5;
+constexpr int kRing = 4;       // (five places were no faster; the fifth's room stages the results)
 constexpr int kFwdThreads = 384;
 constexpr float kLazy = 8.0f;
 
@@ -42,6 +47,7 @@ struct FwdParams {
   CUtensorMap q[kMaxShards];   // box 64 x 128
   CUtensorMap k[kMaxShards];
   CUtensorMap v[kMaxShards];
+  CUtensorMap o[kMaxShards];   // box 64 x 32
   PackArgs a;
   int pair_heads;              // 1: an item is two heads of a group; 0: two token tiles of one head
   int units;                   // token tiles (or pairs of them)
@@ -54,7 +60,8 @@ struct FwdCfg {
   static constexpr int KB = D / 64;
   static constexpr int TILE = KB * kTile * 128;   // bytes of a Q, K or V tile
   static constexpr int OFF_RING = 2 * TILE;
-  static constexpr int OFF_ROWS = OFF_RING + kRing * TILE;   // RowDocs [2]
+  static constexpr int OFF_OUT = OFF_RING + kRing * TILE;    // 32 rows x 64 columns of results per softmax warp
+  static constexpr int OFF_ROWS = OFF_OUT + 8 * 4096;        // RowDocs [2]
   static constexpr int OFF_BAR = OFF_ROWS + 96;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
@@ -376,6 +383,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     const int r = quad * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t s_col = lane_base + x * 128, o_col = lane_base + 256 + x * 128;
+    uint8_t* stage = smem + C::OFF_OUT + (warp - 4) * 4096;
     const float k2 = A.scale * kLog2e;
     const int T = static_cast<int>(A.T);
     bool ok = true;
@@ -513,7 +521,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         tc_fence_after_sync();
       }
       float bad = 0.0f;   // becomes NaN with the first value that is not finite
-      __nv_bfloat16* out = S.o + static_cast<int64_t>(i < T ? i : 0) * A.ldo + qt.c * D;
+      // 64 columns at a time: a row per thread into the warp's swizzled tile, which a TMA store takes to memory (rows
+      // past T are clipped).  Stored by the threads, 64 bytes of 32 different rows at a time, it took 3100
+      // cycles an item.
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
         uint32_t o[2][32];
@@ -524,22 +534,38 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
           tmem_ld_32x32b_x32(o_col + h * 64 + 32, o[1]);
           tmem_ld_wait();
         }
+        if (lane == 0) bulk_wait_group_read<0>();   // the tile's last store has read it
+        __syncwarp();
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 8; ++u) {
+          uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float v = in ? __uint_as_float(o[u][e]) * inv : 0.0f;
-            bad = fmaf(v, 0.0f, bad);
-            o[u][e] = __float_as_uint(v);
+          for (int e = 0; e < 4; ++e) {
+            const int c = u * 8 + 2 * e;
+            const float lo_v = in ? __uint_as_float(o[c >> 5][c & 31]) * inv : 0.0f;
+            const float hi_v = in ? __uint_as_float(o[c >> 5][(c & 31) + 1]) * inv : 0.0f;
+            bad = fmaf(lo_v, 0.0f, fmaf(hi_v, 0.0f, bad));
+            w[e] = pack_bf16x2(lo_v, hi_v);
           }
-          if (i < T) store_bf16x32(out + h * 64 + u * 32, o[u]);
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&P.o[shard], stage, qt.c * D + h * 64, qt.q0 + quad * 32);
+          bulk_commit_group();
         }
       }
       tc_fence_before_sync();
       const unsigned again = __ballot_sync(0xffffffffu, in && bad != 0.0f);
-      __syncwarp();   // the rows' stores above come before those of the redo
-      if (again) redo_rows<D>(A, shard, qt.c, qt.q0 + quad * 32, again, lane);
+      if (again) {
+        if (lane == 0) bulk_wait_group_all();   // the rows' stores above come before those of the redo
+        __syncwarp();
+        redo_rows<D>(A, shard, qt.c, qt.q0 + quad * 32, again, lane);
+      }
     }
+    if (lane == 0) bulk_wait_group_all();   // every store complete before the CTA's shared memory goes away
+    __syncwarp();
   }
 
   __syncthreads();
@@ -574,7 +600,8 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stre
   for (int i = 0; i < A.t; ++i) {
     if ((rc = encode_map_bf16(&P.q[i], A.s[i].q, A.T, qc, A.ldq, 64, kTile)) ||
         (rc = encode_map_bf16(&P.k[i], A.s[i].k, A.T, kc, A.ldk, 64, kTile)) ||
-        (rc = encode_map_bf16(&P.v[i], A.s[i].v, A.T, kc, A.ldv, 64, kTile)))
+        (rc = encode_map_bf16(&P.v[i], A.s[i].v, A.T, kc, A.ldv, 64, kTile)) ||
+        (rc = encode_map_bf16(&P.o[i], A.s[i].o, A.T, qc, A.ldo, 64, 32)))
       return rc;
   }
   const int tiles = static_cast<int>((A.T + kTile - 1) / kTile);
