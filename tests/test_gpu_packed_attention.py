@@ -295,3 +295,68 @@ def test_graph_replay_on_a_side_stream():
         assert torch.equal(f2["O"][i], fwd["O"][i])
         for n in ("dQ", "dK", "dV"):
             assert torch.equal(b2[n][i], bwd[n][i])
+
+
+def _ragged(total, n, seed):
+    """n lengths of any size, empty ones among them, `total` tokens together."""
+    cuts = torch.randint(0, total + 1, (n - 1,), generator=torch.Generator().manual_seed(seed)).sort()[0].tolist()
+    return [b - a for a, b in zip([0] + cuts, cuts + [total])]
+
+
+# More items than SMs (they are then taken by work): heads paired (even groups) and token tiles paired (odd
+# groups), both head widths, one long document among short ones, one alone, hundreds of short ones.
+MANY_ITEMS = [
+    (1, 3000, 16, 4, 128, [2100] + _ragged(800, 9, 1)), (1, 4000, 10, 10, 64, _ragged(3990, 7, 2)),
+    (1, 4000, 10, 10, 128, [4000]), (2, 3333, 24, 8, 64, _ragged(3300, 300, 3)), (1, 4100, 16, 2, 64, [4097]),
+    (1, 2500, 20, 4, 128, _ragged(2500, 700, 4)),
+]
+
+
+@pytest.mark.parametrize("t,T,n_q,n_kv,d,lens", MANY_ITEMS)
+def test_more_items_than_sms(t, T, n_q, n_kv, d, lens):
+    x, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, seed=T)
+    _check(x, fwd, bwd, t, T, n_q, n_kv, d, lens)
+
+
+@pytest.mark.parametrize("t,T,n_q,n_kv,d,lens", [(1, 2000, 16, 1, 128, [1500, 200, 100]), (1, 2600, 4, 1, 64, [100, 2300])])
+def test_masked_places_in_key_tiles_that_several_items_share(t, T, n_q, n_kv, d, lens):
+    """A long document's key tiles are summed in parts: NaN before and behind it stays outside."""
+    x, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, seed=8)
+    first = lens.index(max(lens))
+    a, b = sum(lens[:first]), sum(lens[:first + 1])
+    y = {k: [v.clone() for v in m] if k != "cu" else m for k, m in x.items()}
+    for n in ("Q", "K", "V", "dO"):
+        y[n][0][:a] = float("nan")
+        y[n][0][b:] = float("nan")
+    _, f2, b2 = _run(t, T, n_q, n_kv, d, lens, x=y)
+    part = {k: [v[a:b] for v in m] if k != "cu" else m for k, m in x.items()}
+    f = {"O": [f2["O"][0][a:b]], "lse": [f2["lse"][0][:, a:b]]}
+    r = _reference(part, t, n_q, n_kv, d, [b - a], d ** -0.5, f)[0]
+    _near(f["O"][0].view(b - a, -1, d), r["O"], r["dO"], "O")
+    _near(f["lse"][0], r["lse"], r["dlse"], "lse")
+    for n, e in (("dQ", "eQ"), ("dK", "eK"), ("dV", "eV")):
+        _near(b2[n][0][a:b].view(b - a, -1, d), r[n], r[e], n)
+
+
+@pytest.mark.parametrize("T,n_q,n_kv,d", [(45, 2, 1, 64), (161, 3, 1, 128), (3001, 16, 4, 128)])
+def test_results_in_a_wider_buffer(T, n_q, n_kv, d):
+    """O as columns of a larger matrix: the columns beside it and the rows behind it keep their values."""
+    lens = [T // 3, T - T // 3 - 5]
+    x, fwd, bwd = _run(1, T, n_q, n_kv, d, lens, seed=T)
+    big = torch.full((T + 70, n_q * d + 24), 7.0, dtype=BF16, device="cuda")
+    out = ttl.packed_attn_fwd_buffers(1, T, n_q, n_kv, d, len(lens))
+    out["O"] = [big[:T, 16:16 + n_q * d]]
+    _, f2, b2 = _run(1, T, n_q, n_kv, d, lens, x=x, out_f=out)
+    assert torch.equal(f2["O"][0], fwd["O"][0]) and torch.equal(b2["dQ"][0], bwd["dQ"][0])
+    assert (big[T:] == 7).all() and (big[:, :16] == 7).all() and (big[:, 16 + n_q * d:] == 7).all()
+
+
+def test_bad_document_bounds_with_many_items():
+    t, T, n_q, n_kv, d = 1, 3000, 16, 4, 64
+    x = _inputs(t, T, n_q, n_kv, d, [3000], 0)
+    for cu in ([0, 2500, 100, 3000], [-5, 1000, 2000], [0, 1000, 50000], [4000, 5000], [2000, 0]):
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        fwd = ttl.packed_attn_fwd(x["Q"], x["K"], x["V"], cu, n_q=n_q, n_kv=n_kv, d=d)
+        assert ttl.device_status() == ttl.TTL_ERR_DEVICE
+        ttl.packed_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], fwd, cu, n_q=n_q, n_kv=n_kv, d=d)
+        assert ttl.device_status() == ttl.TTL_ERR_DEVICE
