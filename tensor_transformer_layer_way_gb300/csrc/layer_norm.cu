@@ -1068,7 +1068,7 @@ Spread spread_of(int64_t h, int elem, int B, bool bwd, int inputs) {
     fit(16 / E, 8);
     fit(16 / E, kMaxWarps);
     fit(24 / E, kMaxWarps);
-    fit(32 / E, kMaxWarps);
+    if (!bwd || elem == 2) fit(32 / E, kMaxWarps);            // (fp32 rows that wide do not fit below)
     if (!s.W) return s;
     if (s.W < 8) s.G = 8 / s.W;
     s.ctas = s.W * s.G <= 8 ? 2 : 1;
@@ -1116,36 +1116,35 @@ int allow_smem(size_t bytes) {
   return rc;
 }
 
-template <typename T, int B, int NV>
-int launch_fwd(const NormFwd& P, const Spread& sp, cudaStream_t s) {
-  const int threads = sp.W * sp.G * 32;
+unsigned fwd_grid(const NormFwd& P, const Spread& sp) {
   const int64_t ctas = (P.total + sp.G - 1) / sp.G;
   const int64_t cap = static_cast<int64_t>(num_sms()) * sp.ctas;
-  const unsigned grid = static_cast<unsigned>(ctas < cap ? ctas : cap);
-  constexpr int E = B / sizeof(T);
-  if constexpr (NV * E == 16 || NV * E == 24 || NV * E == 32) {
-    if (sp.stages > 0) {
-      if (int rc = allow_smem<norm_fwd_ring_kernel<T, B, NV>>(sp.smem)) return rc;
-      norm_fwd_ring_kernel<T, B, NV><<<grid, threads, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
-      return TTL_OK;
-    }
-  }
-  if constexpr (B == 16 ? NV <= 2 : NV == 8) norm_fwd_kernel<T, B, NV><<<grid, threads, 0, s>>>(P, sp.W, sp.G);
+  return static_cast<unsigned>(ctas < cap ? ctas : cap);
+}
+
+template <typename T, int B, int NV>
+int fwd_ring(const NormFwd& P, const Spread& sp, cudaStream_t s) {
+  if (int rc = allow_smem<norm_fwd_ring_kernel<T, B, NV>>(sp.smem)) return rc;
+  norm_fwd_ring_kernel<T, B, NV><<<fwd_grid(P, sp), sp.W * sp.G * 32, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
   return TTL_OK;
 }
 
 template <typename T, int B, int NV>
-int launch_bwd(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
-  const int threads = sp.W * sp.G * 32;
-  constexpr int E = B / sizeof(T);
-  if constexpr (NV * E == 8 || NV * E == 16 || NV * E == 24 || NV * E == 32) {
-    if (sp.stages > 0) {
-      if (int rc = allow_smem<norm_bwd_ring_kernel<T, B, NV>>(sp.smem)) return rc;
-      norm_bwd_ring_kernel<T, B, NV><<<parts, threads, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
-      return TTL_OK;
-    }
-  }
-  if constexpr (B == 16 ? NV <= 2 : NV == 8) norm_bwd_kernel<T, B, NV><<<parts, threads, sp.smem, s>>>(P, sp.W, sp.G);
+int fwd_regs(const NormFwd& P, const Spread& sp, cudaStream_t s) {
+  norm_fwd_kernel<T, B, NV><<<fwd_grid(P, sp), sp.W * sp.G * 32, 0, s>>>(P, sp.W, sp.G);
+  return TTL_OK;
+}
+
+template <typename T, int B, int NV>
+int bwd_ring(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
+  if (int rc = allow_smem<norm_bwd_ring_kernel<T, B, NV>>(sp.smem)) return rc;
+  norm_bwd_ring_kernel<T, B, NV><<<parts, sp.W * sp.G * 32, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
+  return TTL_OK;
+}
+
+template <typename T, int B, int NV>
+int bwd_regs(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
+  norm_bwd_kernel<T, B, NV><<<parts, sp.W * sp.G * 32, sp.smem, s>>>(P, sp.W, sp.G);
   return TTL_OK;
 }
 
@@ -1153,11 +1152,11 @@ template <typename T, int B>
 int pick_fwd(const NormFwd& P, const Spread& sp, cudaStream_t s) {
   constexpr int E = B / sizeof(T);
   if (sp.stages > 0) {
-    if (sp.NV == 16 / E) return launch_fwd<T, B, 16 / E>(P, sp, s);
-    return sp.NV == 24 / E ? launch_fwd<T, B, 24 / E>(P, sp, s) : launch_fwd<T, B, 32 / E>(P, sp, s);
+    if (sp.NV == 16 / E) return fwd_ring<T, B, 16 / E>(P, sp, s);
+    return sp.NV == 24 / E ? fwd_ring<T, B, 24 / E>(P, sp, s) : fwd_ring<T, B, 32 / E>(P, sp, s);
   }
-  if constexpr (B == 16) return sp.NV == 1 ? launch_fwd<T, B, 1>(P, sp, s) : launch_fwd<T, B, 2>(P, sp, s);
-  else return launch_fwd<T, B, 8>(P, sp, s);
+  if constexpr (B == 16) return sp.NV == 1 ? fwd_regs<T, B, 1>(P, sp, s) : fwd_regs<T, B, 2>(P, sp, s);
+  else return fwd_regs<T, B, 8>(P, sp, s);
 }
 
 template <typename T, int B>
@@ -1165,12 +1164,13 @@ int pick_bwd(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
   constexpr int E = B / sizeof(T);
   if (sp.stages > 0) {
     if constexpr (sizeof(T) == 4 || B < 16)
-      if (sp.NV == 8 / E) return launch_bwd<T, B, 8 / E>(P, sp, parts, s);
-    if (sp.NV == 16 / E) return launch_bwd<T, B, 16 / E>(P, sp, parts, s);
-    return sp.NV == 24 / E ? launch_bwd<T, B, 24 / E>(P, sp, parts, s) : launch_bwd<T, B, 32 / E>(P, sp, parts, s);
+      if (sp.NV == 8 / E) return bwd_ring<T, B, 8 / E>(P, sp, parts, s);
+    if constexpr (sizeof(T) == 2)
+      if (sp.NV == 32 / E) return bwd_ring<T, B, 32 / E>(P, sp, parts, s);
+    return sp.NV == 24 / E ? bwd_ring<T, B, 24 / E>(P, sp, parts, s) : bwd_ring<T, B, 16 / E>(P, sp, parts, s);
   }
-  if constexpr (B == 16) return sp.NV == 1 ? launch_bwd<T, B, 1>(P, sp, parts, s) : launch_bwd<T, B, 2>(P, sp, parts, s);
-  else return launch_bwd<T, B, 8>(P, sp, parts, s);
+  if constexpr (B == 16) return sp.NV == 1 ? bwd_regs<T, B, 1>(P, sp, parts, s) : bwd_regs<T, B, 2>(P, sp, parts, s);
+  else return bwd_regs<T, B, 8>(P, sp, parts, s);
 }
 
 // The widest word that every row is made of: 16 bytes, or 4, or the element.

@@ -34,16 +34,16 @@ struct PackArgs {
   float* D;                    // backward: rowsum(dO o), [t][n_q/t][T]
   int* status;
   // Work lists, heaviest first, written by the plan kernel (null: the kernels look their items up)
-  const int4* q_list;          // see QUnit
-  const int4* kv_list;         // see KvUnit, two words each
-  const int* kv_head;          // [0] entries of kv_list, [1] key tiles in join_list, [2] partial slots (per lane) taken
+  const int4* q_list;          // one word a query unit, below
+  const int4* kv_list;         // two words a key unit, below
+  const int* kv_head;          // [0] entries of kv_list, [1] key tiles in join_list
   const int4* join_list;       // {key tile, first slot, parts, 0} of the key tiles that several items share
   float* part;                 // partial dK and dV: [slot * KV heads + head][2][128][d]
 };
 
-// Two key-loop bounds of a query unit: {unit, first key tile of its first token tile, of its second, 0}; -1 for
-// a token tile without keys.  A tile's last key tile is its own.
-// A key unit: {key tile, last query tile, first step, end step} {slot or -1, 0, 0, 0}.
+// A query unit: {unit, first key tile of its first token tile, of its second, 0}, -1 for a token tile without
+// keys; a tile's last key tile is its own.
+// A key unit: {key tile, last query tile, first step, end step} {slot of its partial sums or -1, 0, 0, 0}.
 
 // What the plan kernel writes for a launch (null: not wanted).
 struct PackPlan {

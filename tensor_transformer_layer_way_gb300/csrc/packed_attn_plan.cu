@@ -161,10 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
       }
     }
     __syncthreads();
-    if (tid == 0) {
-      P.kv_head[1] = joins;
-      P.kv_head[2] = taken;
-    }
+    if (tid == 0) P.kv_head[1] = joins;
     // the number of entries: all places given out
     int entries = 0;
     for (int t = tid; t < P.tiles; t += kPlanThreads) {
