@@ -36,7 +36,7 @@ struct PackArgs {
   // Work lists, heaviest first, written by the plan kernel (null: the kernels look their items up)
   const int4* q_list;          // one word a query unit, below
   const int4* kv_list;         // two words a key unit, below
-  const int* kv_head;          // [0] entries of kv_list, [1] key tiles in join_list
+  const int* kv_head;          // [0] entries of kv_list, [1] key tiles in join_list, [2] 0
   const int4* join_list;       // {key tile, first slot, parts, 0} of the key tiles that several items share
   float* part;                 // partial dK and dV: [slot * KV heads + head][2][128][d]
 };

@@ -13,6 +13,10 @@
 // tensor pipe busy: S(n+1), dK(n), dP(n+1), dV(n+1), S(n+2), ...  While the elementwise warps turn S(n+1)
 // into P, dK(n) and dP(n+1) run; while they form dS(n+1), dV(n+1) and S(n+2) do.
 //
+// Blocks take items from the list, heaviest first, as they get to them; warp 0 takes one while its last tiles wait for
+// a place, and announces it to the others.  (Dealt out beforehand, in turn and back: 188 us for 12 documents
+// of 8192 tokens, 32 and 8 heads over 8 shards; taken: 145.)
+//
 // Roles (640 threads, persistent): warp 0 the TMA loads, warp 1 the MMAs, warp 2 brings each step's lse and D to
 // shared memory, warp 3 the documents of the coming item's keys, warps 4..19 the elementwise work: a key row per
 // thread, each of the four warpgroups on 32 of the queries (on 64 each, two warpgroups took 1450 cycles from
@@ -29,6 +33,8 @@ constexpr int kKvThreads = 640;
 constexpr int kKvWarps = 16;   // elementwise warps
 constexpr int kRing = 5;       // places of the Q and dO tiles: Q_0, dO_0, Q_1, dO_1, ...
 constexpr int kStat = 2;       // lse and D stages
+constexpr int kAhead = 4;      // items announced to the roles
+constexpr int kKvReaders = kKvWarps + 3;
 
 struct KvParams {
   CUtensorMap q[kMaxShards];   // box 64 x 128
@@ -36,6 +42,7 @@ struct KvParams {
   CUtensorMap v[kMaxShards];
   CUtensorMap dO[kMaxShards];
   PackArgs a;
+  int* taken;                  // items given out beyond the first of each block
   int tiles, lanes;
   uint64_t timeout_ns;
 };
@@ -49,15 +56,17 @@ struct KvCfg {
   static constexpr int OFF_STAT = OFF_RING + kRing * TILE;   // float [kStat][2][128]: -lse log2(e), -D
   static constexpr int OFF_ROWS = OFF_STAT + kStat * 1024;  // int [128]: the last query that sees a key
   static constexpr int OFF_BAR = OFF_ROWS + 512;
-  static constexpr int SMEM = OFF_BAR + 256;   // (the block begins on 1024 bytes; the kernel checks it)
+  static constexpr int SMEM = OFF_BAR + 320 + kAhead * 32;   // (the block begins on 1024 bytes; the kernel checks it)
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
 };
 
 // Steps [t0, t0 + steps) of a key tile: step n is query tile qt_last - n / group, head n % group of the group.
 struct KvItem {
-  int shard, g, k0, qt_last, t0, steps;
+  int shard, g, k0, qt_last, t0, steps;   // (shard < 0: no more items)
   int slot;                    // >= 0: a part of the key tile's sums, for that place of the partial buffers
+  int unused;
 };
+static_assert(sizeof(KvItem) == 32, "an item is two 16-byte words");
 
 __device__ __forceinline__ KvItem kv_item(const KvParams& P, int at) {
   const PackArgs& A = P.a;
@@ -66,6 +75,7 @@ __device__ __forceinline__ KvItem kv_item(const KvParams& P, int at) {
   it.shard = ln / A.nkvl;
   it.g = ln % A.nkvl;
   it.slot = -1;
+  it.unused = 0;
   if (A.kv_list) {
     const int4 e = __ldg(A.kv_list + 2 * (at / P.lanes));
     const int slot = __ldg(A.kv_list + 2 * (at / P.lanes) + 1).x;
@@ -131,10 +141,13 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   uint64_t* rows_empty = rows_full + 1;
   uint64_t* x_bar = rows_empty + 1;    // the elementwise warps meet
   uint64_t* done_bar = x_bar + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  uint64_t* item_full = done_bar + 1;
+  uint64_t* item_empty = item_full + kAhead;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_empty + kAhead);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* flags = tmem_slot + 2;     // [2][4]: rows of a quadrant to be done again, of dK and of dV
-  static_assert((4 + 2 * kRing + 2 * kStat + 9) * 8 + 40 <= 256, "barrier area");
+  static_assert((4 + 2 * kRing + 2 * kStat + 9 + 2 * kAhead) * 8 + 40 <= 320, "barrier area");
+  KvItem* items = reinterpret_cast<KvItem*>(smem + C::OFF_BAR + 320);   // [kAhead]
   constexpr uint32_t T_DP = 128, T_DK = 256, T_DV = 384;
 
   const PackArgs& A = P.a;
@@ -148,9 +161,15 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   const int total = (A.kv_list ? __ldg(A.kv_head) : P.tiles) * P.lanes;
   int* status = A.status;
   const uint64_t tmo = P.timeout_ns;
-  auto item_at = [&](int n) {
-    const int b = static_cast<int>(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    return n * static_cast<int>(gridDim.x) + b;
+  // The n-th item of this block, announced by warp 0, read by a whole warp; false where the wait ran out.
+  auto next_item = [&](int n, KvItem& it) {
+    const int a = n % kAhead;
+    const bool in_time = wait_on(&item_full[a], static_cast<uint32_t>(n / kAhead) & 1u, abort_flag, status, tmo);
+    if (!__all_sync(0xffffffffu, in_time)) return false;
+    it = items[a];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[a]);
+    return true;
   };
   // The item's n-th step: the last query tile first, the group's heads in turn.
   auto step_q0 = [&](const KvItem& it, int n) { return (it.qt_last - (it.t0 + n) / A.grp) * kTile; };
@@ -178,6 +197,10 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     mbar_init(rows_empty, kKvWarps);
     mbar_init(x_bar, kKvWarps);
     mbar_init(done_bar, 1);
+    for (int a = 0; a < kAhead; ++a) {
+      mbar_init(&item_full[a], 1);
+      mbar_init(&item_empty[a], kKvReaders);
+    }
     for (int q = 0; q < 8; ++q) flags[q] = 0;
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -195,12 +218,25 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int nk = 0, nv = 0, pos = 0;   // loads started: K, V, ring places
-    KvItem ahead = {};
-    if (item_at(0) < total) ahead = kv_item(P, item_at(0));   // the coming item is looked up while this one runs
-    for (int n = 0; item_at(n) < total; ++n) {
-      const KvItem it = ahead;
-      if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
-      if (it.steps == 0) continue;
+    auto take = [&]() { return static_cast<int>(gridDim.x) + atomicAdd(P.taken, 1); };
+    int at = static_cast<int>(blockIdx.x);
+    for (int n = 0;; ++n) {
+      KvItem it = {};
+      it.shard = -1;
+      if (at < total) it = kv_item(P, at);
+      if (lane == 0) {
+        const int a = n % kAhead;
+        ok = wait_on(&item_empty[a], (static_cast<uint32_t>(n / kAhead) & 1u) ^ 1u, abort_flag, status, tmo);
+        if (ok) {
+          items[a] = it;
+          mbar_arrive(&item_full[a]);
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0) || it.shard < 0) break;
+      // The next item is taken while this one's last tiles wait for their places: by then the blocks that end
+      // first have come back for more.
+      int next = total;
+      if (lane == 0 && it.steps == 0 && A.kv_list) next = take();
       if (lane == 0 && ok) {
         auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint32_t phase, int x, int y) {
           if (!wait_on(empty, (phase & 1u) ^ 1u, abort_flag, status, tmo)) return false;
@@ -215,6 +251,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           return true;
         };
         for (int t = 0; ok && t < it.steps; ++t) {
+          if (t + 1 == it.steps && A.kv_list) next = take();
           if (t == 0) {
             ok = load(sK, &P.k[it.shard], k_full, k_empty, nk, it.g * D, it.k0);
             nk += ok;
@@ -228,6 +265,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         }
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      at = __shfl_sync(0xffffffffu, next, 0);
     }
     if (lane == 0) {
       // No copy may still be landing when the CTA leaves: wait (bounded) for the last loads.
@@ -270,14 +308,9 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       for (int kk = 0; kk < kTile / 16; ++kk)
         umma_bf16_ts(dst, acol + (kk >> 1) * 32 + (kk & 1) * 8, desc_advance(bd, kk * 2048), idesc_acc, kk ? 1u : more);
     };
-    KvItem ahead = {};
-    if (item_at(0) < total) ahead = kv_item(P, item_at(0));
-    for (int n = 0; item_at(n) < total; ++n) {
-      const KvItem it = ahead;
-      if (it.steps == 0) {
-        if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
-        continue;
-      }
+    KvItem it;
+    for (int n = 0; next_item(n, it) && it.shard >= 0; ++n) {
+      if (it.steps == 0) continue;
       wait(k_full, ni);
       // S^T of step t overwrites P^T of the step before, whose dV product was issued before it (the tensor
       // pipe runs one thread's products in order); likewise dP^T and dK.
@@ -324,8 +357,6 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           }
         }
         __syncwarp();
-        // the coming item is looked up once the first products run
-        if (t < 0 && item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
       }
       if (leader) umma_commit(acc_full);
       __syncwarp();
@@ -340,11 +371,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // ------------------------------------------------------------------ lse and D of each step's queries
     bool ok = true;
     int pos = 0;
-    KvItem ahead = {};
-    if (item_at(0) < total) ahead = kv_item(P, item_at(0));
-    for (int n = 0; ok && item_at(n) < total; ++n) {
-      const KvItem it = ahead;
-      if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
+    KvItem it;
+    for (int n = 0; ok && next_item(n, it) && it.shard >= 0; ++n) {
       const float* lse = A.s[it.shard].lse;
       const float* Dr = A.D + static_cast<int64_t>(it.shard) * A.nql * A.T;
       for (int t = 0; t < it.steps; ++t, ++pos) {
@@ -375,8 +403,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   } else if (warp == 3) {
     // ------------------------------------------------------------------ last queries of the coming item's keys
     bool ok = true;
-    for (int n = 0; ok && item_at(n) < total; ++n) {
-      const KvItem it = kv_item(P, item_at(n));
+    KvItem it;
+    for (int n = 0; ok && next_item(n, it) && it.shard >= 0; ++n) {
       int hi[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -403,10 +431,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     bool ok = true;
     int pos = 0, ni = 0;
     uint32_t met = 0;
-    KvItem ahead = {};
-    if (item_at(0) < total) ahead = kv_item(P, item_at(0));
-    for (int n = 0; ok && item_at(n) < total; ++n) {
-      const KvItem it = ahead;
+    KvItem it;
+    for (int n = 0; ok && next_item(n, it) && it.shard >= 0; ++n) {
       const PackShard& S = A.s[it.shard];
       const int key = it.k0 + r;
       ok = mbar_wait(rows_full, static_cast<uint32_t>(n) & 1u, abort_flag, status, tmo);
@@ -497,7 +523,6 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       }
       if (!ok) break;
       // ---- two warpgroups store dK, two dV; the last products are running
-      if (item_at(n + 1) < total) ahead = kv_item(P, item_at(n + 1));
       const int kind = w >> 1, col = (w & 1) * (D / 2);
       const bool computed = it.steps > 0;
       if (computed) {
@@ -626,6 +651,7 @@ int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream) {
   }
   P.tiles = static_cast<int>((A.T + kTile - 1) / kTile);
   P.lanes = A.t * A.nkvl;
+  P.taken = A.kv_list ? const_cast<int*>(A.kv_head) + 2 : nullptr;
   P.timeout_ns = 2000000000ull;
   const int64_t items = static_cast<int64_t>(P.tiles) * P.lanes;
   if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many key tiles");

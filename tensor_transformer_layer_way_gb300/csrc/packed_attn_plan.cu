@@ -172,7 +172,10 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     __syncthreads();
     atomicAdd(&taken, entries);
     __syncthreads();
-    if (tid == 0) P.kv_head[0] = taken;
+    if (tid == 0) {
+      P.kv_head[0] = taken;
+      P.kv_head[2] = 0;
+    }
   }
 }
 
