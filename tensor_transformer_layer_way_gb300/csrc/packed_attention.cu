@@ -97,7 +97,7 @@ using namespace ttl;
 
 extern "C" size_t ttl_packed_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
   if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_fwd_workspace_size")) return 0;
-  return round256(static_cast<size_t>(tiles_of(T)) * 16);   // the query tiles by work
+  return round256(static_cast<size_t>(tiles_of(T) + 1) * 16);   // the query tiles by work, and how many were taken
 }
 
 extern "C" size_t ttl_packed_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
@@ -204,12 +204,16 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
     plan.q_per = 1;
     plan.kv_list = reinterpret_cast<int4*>(base + w.kv_list);
     plan.kv_head = reinterpret_cast<int*>(base + w.head);
+    plan.kv_taken = plan.kv_head + 2;
+    plan.q_taken = plan.kv_head + 3;
     plan.join_list = reinterpret_cast<int4*>(base + w.join);
     plan.lanes = n_kv;
     plan.split = split;
     A.q_list = plan.q_list;
     A.kv_list = plan.kv_list;
     A.kv_head = plan.kv_head;
+    A.q_taken = plan.q_taken;
+    A.kv_taken = plan.kv_taken;
     A.join_list = plan.join_list;
     A.part = reinterpret_cast<float*>(base + w.part);
   }

@@ -36,7 +36,9 @@ struct PackArgs {
   // Work lists, heaviest first, written by the plan kernel (null: the kernels look their items up)
   const int4* q_list;          // one word a query unit, below
   const int4* kv_list;         // two words a key unit, below
-  const int* kv_head;          // [0] entries of kv_list, [1] key tiles in join_list, [2] 0
+  const int* kv_head;          // [0] entries of kv_list, [1] key tiles in join_list
+  int* q_taken;                // items of a list that blocks took beyond their first; 0 at the start
+  int* kv_taken;
   const int4* join_list;       // {key tile, first slot, parts, 0} of the key tiles that several items share
   float* part;                 // partial dK and dV: [slot * KV heads + head][2][128][d]
 };
@@ -49,8 +51,10 @@ struct PackArgs {
 struct PackPlan {
   int4* q_list;
   int q_units, q_per;          // token tiles per query unit
+  int* q_taken;
   int4* kv_list;
   int* kv_head;
+  int* kv_taken;
   int4* join_list;
   int tiles, lanes;            // key tiles; KV heads over all shards
   int split;                   // key tiles may be cut into several items
@@ -71,7 +75,7 @@ enum PackKernelSlot { kPackFwd128, kPackFwd64, kPackDq128, kPackDq64, kPackDkv12
 int set_core_smem_once(const void* fn, int slot, int bytes, const char* what);
 
 // Launches of the tensor-core kernels (arguments are checked; A.s holds every pointer they need).
-// `list`: room for one word of 16 bytes per 128 tokens.
+// `list`: room for one word of 16 bytes per 128 tokens and one more.
 int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stream);
 int pack_attn_dq_launch(const PackArgs& A, int d, cudaStream_t stream);    // dQ, after D
 int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream);   // dK and dV, after D
@@ -155,6 +159,48 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
   if (mbar_try_wait(bar, parity)) return true;
   return wait_longer(smem_u32(bar), parity, abort, status, timeout_ns);
 }
+
+// The items of a persistent block after its first, announced by one of its warps and read by the others.  Blocks
+// take items from the work list, heaviest first, as they get to them.  One is taken kLead tiles before the loads
+// of the one before end: early enough that its documents are looked up by then, late enough that a block which
+// ends first finds items left.
+constexpr int kLead = 2;
+constexpr int kAhead = 4;        // items announced and not yet read
+constexpr int kQueueBars = 2 * kAhead;
+template <class Item>
+struct ItemQueue {
+  Item* items;                   // [kAhead], shared memory; shard < 0: no more items
+  uint64_t* bars;                // [kQueueBars]
+  volatile int* abort;
+  int* status;
+  uint64_t timeout_ns;
+
+  __device__ __forceinline__ void init(int readers) const {
+    for (int a = 0; a < kAhead; ++a) {
+      mbar_init(&bars[a], 1);
+      mbar_init(&bars[kAhead + a], readers);
+    }
+  }
+  // The n-th item (n >= 1), by one lane; false where the wait for its place ran out.
+  __device__ __forceinline__ bool announce(int n, const Item& it) const {
+    const int a = (n - 1) % kAhead;
+    if (!wait_on(&bars[kAhead + a], (static_cast<uint32_t>((n - 1) / kAhead) & 1u) ^ 1u, abort, status, timeout_ns)) return false;
+    items[a] = it;
+    mbar_arrive(&bars[a]);
+    return true;
+  }
+  // The n-th item (n >= 1), by a whole warp; false where the wait ran out.
+  __device__ __forceinline__ bool next(int n, Item& it) const {
+    if (n == 0) return true;     // (the first one each warp finds by itself)
+    const int a = (n - 1) % kAhead;
+    const bool in_time = wait_on(&bars[a], static_cast<uint32_t>((n - 1) / kAhead) & 1u, abort, status, timeout_ns);
+    if (!__all_sync(0xffffffffu, in_time)) return false;
+    it = items[a];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars[kAhead + a]);
+    return true;
+  }
+};
 
 // The warp's index as a value the compiler knows to be the same in all lanes: descriptors computed from it and
 // from loop counters stay in uniform registers, which is where the MMA instruction takes them from.

@@ -13,9 +13,12 @@
 // tensor pipe busy: S(n+1), dK(n), dP(n+1), dV(n+1), S(n+2), ...  While the elementwise warps turn S(n+1)
 // into P, dK(n) and dP(n+1) run; while they form dS(n+1), dV(n+1) and S(n+2) do.
 //
+// What bounds it: the turns of tensor pipe and elementwise warps, 3000 cycles a step where the products need 2050.
+// Measured: one document of 16384 tokens, 4 query heads and 1 KV head of 128: 375 us, 1470 TFLOP/s.
+//
 // Blocks take items from the list, heaviest first, as they get to them; warp 0 takes one while its last tiles wait for
-// a place, and announces it to the others.  (Dealt out beforehand, in turn and back: 188 us for 12 documents
-// of 8192 tokens, 32 and 8 heads over 8 shards; taken: 145.)
+// a place, and announces it to the others.  (Dealt out beforehand, in turn and back: 188 us for 12 documents of
+// 8192 tokens together, 32 and 8 heads over 8 shards; taken: 147.)
 //
 // Roles (640 threads, persistent): warp 0 the TMA loads, warp 1 the MMAs, warp 2 brings each step's lse and D to
 // shared memory, warp 3 the documents of the coming item's keys, warps 4..19 the elementwise work: a key row per
@@ -33,8 +36,6 @@ constexpr int kKvThreads = 640;
 constexpr int kKvWarps = 16;   // elementwise warps
 constexpr int kRing = 5;       // places of the Q and dO tiles: Q_0, dO_0, Q_1, dO_1, ...
 constexpr int kStat = 2;       // lse and D stages
-constexpr int kAhead = 4;      // items announced to the roles
-constexpr int kKvReaders = kKvWarps + 3;
 
 struct KvParams {
   CUtensorMap q[kMaxShards];   // box 64 x 128
@@ -42,9 +43,14 @@ struct KvParams {
   CUtensorMap v[kMaxShards];
   CUtensorMap dO[kMaxShards];
   PackArgs a;
-  int* taken;                  // items given out beyond the first of each block
   int tiles, lanes;
   uint64_t timeout_ns;
+};
+
+// Steps [t0, t0 + steps) of a key tile: step n is query tile qt_last - n / group, head n % group of the group.
+struct KvItem {
+  int shard, g, k0, qt_last, t0, steps;   // (shard < 0: no more items)
+  int slot;                    // >= 0: a part of the key tile's sums, for that place of the partial buffers
 };
 
 template <int D>
@@ -56,40 +62,26 @@ struct KvCfg {
   static constexpr int OFF_STAT = OFF_RING + kRing * TILE;   // float [kStat][2][128]: -lse log2(e), -D
   static constexpr int OFF_ROWS = OFF_STAT + kStat * 1024;  // int [128]: the last query that sees a key
   static constexpr int OFF_BAR = OFF_ROWS + 512;
-  static constexpr int SMEM = OFF_BAR + 320 + kAhead * 32;   // (the block begins on 1024 bytes; the kernel checks it)
+  static constexpr int SMEM = OFF_BAR + 320 + kAhead * static_cast<int>(sizeof(KvItem));   // (the block begins on 1024 bytes; the kernel checks it)
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
 };
 
-// Steps [t0, t0 + steps) of a key tile: step n is query tile qt_last - n / group, head n % group of the group.
-struct KvItem {
-  int shard, g, k0, qt_last, t0, steps;   // (shard < 0: no more items)
-  int slot;                    // >= 0: a part of the key tile's sums, for that place of the partial buffers
-  int unused;
-};
-static_assert(sizeof(KvItem) == 32, "an item is two 16-byte words");
-
-__device__ __forceinline__ KvItem kv_item(const KvParams& P, int at) {
+// The listed item of index `at`.
+__device__ __forceinline__ KvItem listed_item(const KvParams& P, int at) {
   const PackArgs& A = P.a;
   const int ln = at % P.lanes;
-  KvItem it;
-  it.shard = ln / A.nkvl;
-  it.g = ln % A.nkvl;
-  it.slot = -1;
-  it.unused = 0;
-  if (A.kv_list) {
-    const int4 e = __ldg(A.kv_list + 2 * (at / P.lanes));
-    const int slot = __ldg(A.kv_list + 2 * (at / P.lanes) + 1).x;
-    it.k0 = e.x * kTile;
-    it.qt_last = e.y;
-    it.t0 = e.z;
-    it.steps = e.w - e.z;
-    if (slot >= 0) it.slot = slot * P.lanes + ln;
-    return it;
-  }
-  const int tile = at / P.lanes;
-  it.k0 = tile * kTile;
-  it.qt_last = tile - 1;
-  it.t0 = it.steps = 0;
+  const int4 e = __ldg(A.kv_list + 2 * (at / P.lanes));
+  const int slot = __ldg(A.kv_list + 2 * (at / P.lanes) + 1).x;
+  return KvItem{ln / A.nkvl, ln % A.nkvl, e.x * kTile, e.y, e.z, e.w - e.z, slot < 0 ? -1 : slot * P.lanes + ln};
+}
+
+// A block's first item (of `total`), found by a whole warp.
+__device__ __forceinline__ KvItem first_item(const KvParams& P, int total) {
+  const PackArgs& A = P.a;
+  const int at = static_cast<int>(blockIdx.x), ln = at % P.lanes, tile = at / P.lanes;
+  if (at >= total) return KvItem{-1, 0, 0, 0, 0, 0, -1};
+  if (A.kv_list) return listed_item(P, at);
+  KvItem it = {ln / A.nkvl, ln % A.nkvl, tile * kTile, tile - 1, 0, 0, -1};
   if (A.batch > 0) {
     const int T = static_cast<int>(A.T);
     const int first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
@@ -141,13 +133,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   uint64_t* rows_empty = rows_full + 1;
   uint64_t* x_bar = rows_empty + 1;    // the elementwise warps meet
   uint64_t* done_bar = x_bar + 1;
-  uint64_t* item_full = done_bar + 1;
-  uint64_t* item_empty = item_full + kAhead;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_empty + kAhead);
+  uint64_t* item_bars = done_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bars + kQueueBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* flags = tmem_slot + 2;     // [2][4]: rows of a quadrant to be done again, of dK and of dV
-  static_assert((4 + 2 * kRing + 2 * kStat + 9 + 2 * kAhead) * 8 + 40 <= 320, "barrier area");
-  KvItem* items = reinterpret_cast<KvItem*>(smem + C::OFF_BAR + 320);   // [kAhead]
+  static_assert((4 + 2 * kRing + 2 * kStat + 9 + kQueueBars) * 8 + 40 <= 320, "barrier area");
   constexpr uint32_t T_DP = 128, T_DK = 256, T_DV = 384;
 
   const PackArgs& A = P.a;
@@ -161,16 +151,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   const int total = (A.kv_list ? __ldg(A.kv_head) : P.tiles) * P.lanes;
   int* status = A.status;
   const uint64_t tmo = P.timeout_ns;
-  // The n-th item of this block, announced by warp 0, read by a whole warp; false where the wait ran out.
-  auto next_item = [&](int n, KvItem& it) {
-    const int a = n % kAhead;
-    const bool in_time = wait_on(&item_full[a], static_cast<uint32_t>(n / kAhead) & 1u, abort_flag, status, tmo);
-    if (!__all_sync(0xffffffffu, in_time)) return false;
-    it = items[a];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&item_empty[a]);
-    return true;
-  };
+  const ItemQueue<KvItem> queue{reinterpret_cast<KvItem*>(smem + C::OFF_BAR + 320), item_bars, abort_flag, status, tmo};
   // The item's n-th step: the last query tile first, the group's heads in turn.
   auto step_q0 = [&](const KvItem& it, int n) { return (it.qt_last - (it.t0 + n) / A.grp) * kTile; };
   auto step_head = [&](const KvItem& it, int n) { return it.g * A.grp + (it.t0 + n) % A.grp; };
@@ -197,12 +178,12 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     mbar_init(rows_empty, kKvWarps);
     mbar_init(x_bar, kKvWarps);
     mbar_init(done_bar, 1);
-    for (int a = 0; a < kAhead; ++a) {
-      mbar_init(&item_full[a], 1);
-      mbar_init(&item_empty[a], kKvReaders);
-    }
     for (int q = 0; q < 8; ++q) flags[q] = 0;
     *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (threadIdx.x == 64) {
+    queue.init(kKvWarps + 3);
     fence_mbarrier_init();
   }
   if (warp == 1) {
@@ -218,26 +199,21 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int nk = 0, nv = 0, pos = 0;   // loads started: K, V, ring places
-    auto take = [&]() { return static_cast<int>(gridDim.x) + atomicAdd(P.taken, 1); };
-    int at = static_cast<int>(blockIdx.x);
-    for (int n = 0;; ++n) {
-      KvItem it = {};
-      it.shard = -1;
-      if (at < total) it = kv_item(P, at);
-      if (lane == 0) {
-        const int a = n % kAhead;
-        ok = wait_on(&item_empty[a], (static_cast<uint32_t>(n / kAhead) & 1u) ^ 1u, abort_flag, status, tmo);
-        if (ok) {
-          items[a] = it;
-          mbar_arrive(&item_full[a]);
+    KvItem it = first_item(P, total);
+    for (int n = 0; lane == 0 && ok && it.shard >= 0; ++n) {
+      KvItem coming = {};
+      coming.shard = -1;
+      auto announce = [&]() {
+        if (A.kv_list) {
+          const int at = static_cast<int>(gridDim.x) + atomicAdd(A.kv_taken, 1);
+          if (at < total) coming = listed_item(P, at);
         }
-      }
-      if (!__shfl_sync(0xffffffffu, ok, 0) || it.shard < 0) break;
-      // The next item is taken while this one's last tiles wait for their places: by then the blocks that end
-      // first have come back for more.
-      int next = total;
-      if (lane == 0 && it.steps == 0 && A.kv_list) next = take();
-      if (lane == 0 && ok) {
+        ok = queue.announce(n + 1, coming);
+      };
+      const int when = max(0, it.steps - kLead);
+      if (it.steps == 0) {
+        announce();
+      } else {
         auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint32_t phase, int x, int y) {
           if (!wait_on(empty, (phase & 1u) ^ 1u, abort_flag, status, tmo)) return false;
           mbar_arrive_expect_tx(full, C::TILE);
@@ -251,7 +227,6 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           return true;
         };
         for (int t = 0; ok && t < it.steps; ++t) {
-          if (t + 1 == it.steps && A.kv_list) next = take();
           if (t == 0) {
             ok = load(sK, &P.k[it.shard], k_full, k_empty, nk, it.g * D, it.k0);
             nk += ok;
@@ -262,10 +237,10 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
             nv += ok;
           }
           ok = ok && load_ring(&P.dO[it.shard], step_head(it, t) * D, step_q0(it, t));
+          if (ok && t == when) announce();
         }
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      at = __shfl_sync(0xffffffffu, next, 0);
+      it = coming;
     }
     if (lane == 0) {
       // No copy may still be landing when the CTA leaves: wait (bounded) for the last loads.
@@ -308,8 +283,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       for (int kk = 0; kk < kTile / 16; ++kk)
         umma_bf16_ts(dst, acol + (kk >> 1) * 32 + (kk & 1) * 8, desc_advance(bd, kk * 2048), idesc_acc, kk ? 1u : more);
     };
-    KvItem it;
-    for (int n = 0; next_item(n, it) && it.shard >= 0; ++n) {
+    KvItem it = first_item(P, total);
+    for (int n = 0; queue.next(n, it) && it.shard >= 0; ++n) {
       if (it.steps == 0) continue;
       wait(k_full, ni);
       // S^T of step t overwrites P^T of the step before, whose dV product was issued before it (the tensor
@@ -371,8 +346,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // ------------------------------------------------------------------ lse and D of each step's queries
     bool ok = true;
     int pos = 0;
-    KvItem it;
-    for (int n = 0; ok && next_item(n, it) && it.shard >= 0; ++n) {
+    KvItem it = first_item(P, total);
+    for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       const float* lse = A.s[it.shard].lse;
       const float* Dr = A.D + static_cast<int64_t>(it.shard) * A.nql * A.T;
       for (int t = 0; t < it.steps; ++t, ++pos) {
@@ -403,8 +378,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   } else if (warp == 3) {
     // ------------------------------------------------------------------ last queries of the coming item's keys
     bool ok = true;
-    KvItem it;
-    for (int n = 0; ok && next_item(n, it) && it.shard >= 0; ++n) {
+    KvItem it = first_item(P, total);
+    for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       int hi[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -431,8 +406,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     bool ok = true;
     int pos = 0, ni = 0;
     uint32_t met = 0;
-    KvItem it;
-    for (int n = 0; ok && next_item(n, it) && it.shard >= 0; ++n) {
+    KvItem it = first_item(P, total);
+    for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       const PackShard& S = A.s[it.shard];
       const int key = it.k0 + r;
       ok = mbar_wait(rows_full, static_cast<uint32_t>(n) & 1u, abort_flag, status, tmo);
@@ -651,7 +626,6 @@ int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream) {
   }
   P.tiles = static_cast<int>((A.T + kTile - 1) / kTile);
   P.lanes = A.t * A.nkvl;
-  P.taken = A.kv_list ? const_cast<int*>(A.kv_head) + 2 : nullptr;
   P.timeout_ns = 2000000000ull;
   const int64_t items = static_cast<int64_t>(P.tiles) * P.lanes;
   if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many key tiles");

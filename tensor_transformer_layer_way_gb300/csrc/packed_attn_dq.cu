@@ -12,6 +12,10 @@
 // form dS: a row per thread, each of the four warpgroups on 32 of the keys (on 64 each, two warpgroups took
 // longer over a tile than the products they run under).
 // S, dP and dQ take 384 columns of tensor memory and two dS buffers the rest.
+//
+// What bounds it: the products' reads of shared memory, 1750 of the 2340 cycles a key tile takes.  Measured: one
+// document of 16384 tokens, 4 query heads and 1 KV head of 128: 270 us, 1530 TFLOP/s; 8192 tokens in 12
+// documents, 32 and 8 heads over 8 shards: 129 us.
 
 #include <cstring>
 
@@ -35,6 +39,10 @@ struct DqParams {
   uint64_t timeout_ns;
 };
 
+struct DqItem {
+  int shard, c, g, q0, jbeg, jend;
+};
+
 template <int D>
 struct DqCfg {
   static constexpr int KB = D / 64;
@@ -44,45 +52,45 @@ struct DqCfg {
   static constexpr int OFF_V = OFF_K + kKSlots * TILE;
   static constexpr int OFF_X = OFF_V + kVSlots * TILE;   // of each row: -lse log2(e), D, first key
   static constexpr int OFF_BAR = OFF_X + 1536;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int SMEM = OFF_BAR + 320 + kAhead * static_cast<int>(sizeof(DqItem)) + 1024;
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
 };
 
-struct DqItem {
-  int shard, c, g, q0, jbeg, jend;
-};
-
-__device__ __forceinline__ DqItem dq_item(const DqParams& P, int at) {
-  const PackArgs& A = P.a;
+// The item of index `at` whose query tile is `tile` and first key tile `first` (-1: none).
+__device__ __forceinline__ DqItem item_from(const DqParams& P, int at, int tile, int first) {
   const int ln = at % P.lanes;
   DqItem it;
-  it.shard = ln / A.nql;
-  it.c = ln % A.nql;
-  it.g = it.c / A.grp;
-  it.jbeg = it.jend = 0;
-  if (A.q_list) {
-    const int4 e = __ldg(A.q_list + at / P.lanes);
-    it.q0 = e.x * kTile;
-    if (e.y >= 0) {
-      it.jbeg = e.y;
-      it.jend = e.x + 1;
-    }
-    return it;
-  }
-  const int tile = P.tiles - 1 - at / P.lanes;
+  it.shard = ln / P.a.nql;
+  it.c = ln % P.a.nql;
+  it.g = it.c / P.a.grp;
   it.q0 = tile * kTile;
+  it.jbeg = first < 0 ? 0 : first;
+  it.jend = first < 0 ? 0 : tile + 1;
+  return it;
+}
+
+// The listed item of index `at`.
+__device__ __forceinline__ DqItem listed_item(const DqParams& P, int at) {
+  const int4 e = __ldg(P.a.q_list + at / P.lanes);
+  return item_from(P, at, e.x, e.y);
+}
+
+// A block's first item, found by a whole warp.
+__device__ __forceinline__ DqItem first_item(const DqParams& P) {
+  const PackArgs& A = P.a;
+  const int at = static_cast<int>(blockIdx.x);
+  if (A.q_list) return listed_item(P, at);
+  const int tile = P.tiles - 1 - at / P.lanes, q0 = tile * kTile;
+  int first_tile = -1;
   if (A.batch > 0) {
     const int T = static_cast<int>(A.T);
     const int first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
-    const int v0 = it.q0 > first ? it.q0 : first;
-    int v1 = it.q0 + kTile < last ? it.q0 + kTile : last;
+    const int v0 = q0 > first ? q0 : first;
+    int v1 = q0 + kTile < last ? q0 + kTile : last;
     v1 = v1 < T ? v1 : T;
-    if (v0 < v1) {
-      it.jbeg = doc_of_warp(A.cu, A.batch, T, v0).lo / kTile;
-      it.jend = tile + 1;
-    }
+    if (v0 < v1) first_tile = doc_of_warp(A.cu, A.batch, T, v0).lo / kTile;
   }
-  return it;
+  return item_from(P, at, tile, first_tile);
 }
 
 template <int D>
@@ -124,10 +132,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
   uint64_t* rows_full = x_bar + 1;
   uint64_t* rows_empty = rows_full + 1;
   uint64_t* done_bar = rows_empty + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  uint64_t* item_bars = done_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bars + kQueueBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* flags = tmem_slot + 2;     // [4]: rows of a quadrant to be done again
-  static_assert((2 + 2 * kKSlots + 2 * kVSlots + 14) * 8 + 24 <= 256, "barrier area");
+  static_assert((2 + 2 * kKSlots + 2 * kVSlots + 14 + kQueueBars) * 8 + 24 <= 320, "barrier area");
   constexpr uint32_t T_DP = 128, T_DQ = 256, T_DS = 384;
 
   const PackArgs& A = P.a;
@@ -136,10 +145,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
   const int total = P.tiles * P.lanes;
   int* status = A.status;
   const uint64_t tmo = P.timeout_ns;
-  auto item_at = [&](int n) {
-    const int b = static_cast<int>(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    return n * static_cast<int>(gridDim.x) + b;
-  };
+  const ItemQueue<DqItem> queue{reinterpret_cast<DqItem*>(smem + C::OFF_BAR + 320), item_bars, abort_flag, status, tmo};
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -170,6 +176,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     *abort_flag = 0;
     fence_mbarrier_init();
   }
+  if (threadIdx.x == 64) {
+    queue.init(kDqWarps + 3);
+    fence_mbarrier_init();
+  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
@@ -185,13 +195,21 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int pos = 0, nq = 0;    // key tiles and items started
-    DqItem ahead = {};
-    if (item_at(0) < total) ahead = dq_item(P, item_at(0));   // the coming item is looked up while this one runs
-    for (int n = 0; item_at(n) < total; ++n) {
-      const DqItem it = ahead;
-      if (item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
-      if (it.jend <= it.jbeg) continue;
-      if (lane == 0 && ok) {
+    DqItem it = first_item(P);
+    for (int n = 0; lane == 0 && ok && it.shard >= 0; ++n) {
+      DqItem coming = {};
+      coming.shard = -1;
+      auto announce = [&]() {
+        if (A.q_list) {
+          const int at = static_cast<int>(gridDim.x) + atomicAdd(A.q_taken, 1);
+          if (at < total) coming = listed_item(P, at);
+        }
+        ok = queue.announce(n + 1, coming);
+      };
+      const int when = max(it.jbeg, it.jend - kLead);
+      if (it.jend <= it.jbeg) {
+        announce();
+      } else {
         ok = wait_on(q_empty, (static_cast<uint32_t>(nq) & 1u) ^ 1u, abort_flag, status, tmo);
         if (ok) {
           mbar_arrive_expect_tx(q_full, 2 * C::TILE);
@@ -219,9 +237,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           mbar_arrive_expect_tx(&v_full[vs], C::TILE);
           for (int kb = 0; kb < C::KB; ++kb)
             tma_load_2d(sV + vs * C::TILE + kb * 16384, &P.v[it.shard], &v_full[vs], it.g * D + kb * 64, j * kTile);
+          if (j == when) announce();
         }
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      it = coming;
     }
     if (lane == 0) {
       // No copy may still be landing when the CTA leaves: wait (bounded) for the last loads.
@@ -252,15 +271,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     auto wait = [&](uint64_t* bar, int phase) {
       wait_on(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
     };
-    DqItem ahead = {};
-    if (item_at(0) < total) ahead = dq_item(P, item_at(0));
-    for (int n = 0; item_at(n) < total; ++n) {
-      const DqItem it = ahead;
+    DqItem it = first_item(P);
+    for (int n = 0; queue.next(n, it) && it.shard >= 0; ++n) {
       const int nt = it.jend - it.jbeg;
-      if (nt <= 0) {
-        if (item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
-        continue;
-      }
+      if (nt <= 0) continue;
       wait(q_full, nq);
       tc_fence_after_sync();
       ++nq;
@@ -316,8 +330,6 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           }
         }
         __syncwarp();
-        // the coming item is looked up once the first products run
-        if (j < 0 && item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
         if (j + 1 < nt) {
           ++p;
           old = ks;
@@ -338,8 +350,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     const int r0 = (warp - 2) * 64;
     const int T = static_cast<int>(A.T);
     bool ok = true;
-    for (int n = 0; ok && item_at(n) < total; ++n) {
-      const DqItem it = dq_item(P, item_at(n));
+    DqItem it = first_item(P);
+    for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       const PackShard& S = A.s[it.shard];
       int lo[2];
       float nl[2], Dr[2];
@@ -384,10 +396,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
       ++met;
       return static_cast<bool>(__all_sync(0xffffffffu, in_time));
     };
-    DqItem ahead = {};
-    if (item_at(0) < total) ahead = dq_item(P, item_at(0));
-    for (int n = 0; ok && item_at(n) < total; ++n) {
-      const DqItem it = ahead;
+    DqItem it = first_item(P);
+    for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       const PackShard& S = A.s[it.shard];
       const int i = it.q0 + r;
       ok = mbar_wait(rows_full, static_cast<uint32_t>(n) & 1u, abort_flag, status, tmo);
@@ -462,7 +472,6 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&ds_full[b]);
       }
       if (!ok) break;
-      if (item_at(n + 1) < total) ahead = dq_item(P, item_at(n + 1));
       const bool computed = it.jend > it.jbeg;
       if (computed) {
         ok = mbar_wait(dq_full, static_cast<uint32_t>(no) & 1u, abort_flag, status, tmo);

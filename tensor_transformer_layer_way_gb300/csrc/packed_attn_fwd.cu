@@ -24,7 +24,8 @@
 //
 // What bounds it: shared memory, which S_x = Q_x K^T reads at 128 bytes a cycle for 2000 of the 2700 cycles a
 // pair of key tiles takes.  Measured: one document of 32768 tokens, 4 query heads and 1 KV head of 128: 680 us, 1618
-// TFLOP/s; 8192 tokens in 12 documents, 32 query and 8 KV heads over 8 shards: 101 us.  With many short documents an
+// TFLOP/s; 8192 tokens in 12 documents, 32 query and 8 KV heads over 8 shards: 96 us (101
+// with items dealt out beforehand).  With many short documents an
 // item costs about 10000 cycles beside its key tiles (masks, the wait for the last product, the result).
 //
 // A masked place enters the product as P = 0, and 0 times an infinite or NaN value is NaN: a row whose
@@ -55,6 +56,16 @@ struct FwdParams {
   uint64_t timeout_ns;
 };
 
+// One query tile of an item: tokens [q0, q0 + 128) of head c, key tiles [jbeg, jend).
+struct QTile {
+  int c, q0, jbeg, jend;
+};
+struct Item {
+  int shard, g;                // shard < 0: no more items
+  QTile x[2];
+  int jlo, jhi;                // union of the key tiles
+};
+
 template <int D>
 struct FwdCfg {
   static constexpr int KB = D / 64;
@@ -63,18 +74,8 @@ struct FwdCfg {
   static constexpr int OFF_OUT = OFF_RING + kRing * TILE;    // 32 rows x 64 columns of results per softmax warp
   static constexpr int OFF_ROWS = OFF_OUT + 8 * 4096;        // RowDocs [2]
   static constexpr int OFF_BAR = OFF_ROWS + 96;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int SMEM = OFF_BAR + 256 + kAhead * static_cast<int>(sizeof(Item)) + 1024;
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
-};
-
-// One query tile of an item: tokens [q0, q0 + 128) of head c, key tiles [jbeg, jend).
-struct QTile {
-  int c, q0, jbeg, jend;
-};
-struct Item {
-  int shard, g;
-  QTile x[2];
-  int jlo, jhi;                // union of the key tiles
 };
 
 // First key tile of the query tile at token q0, or -1; found by the whole warp.
@@ -88,25 +89,16 @@ __device__ __forceinline__ int first_key(const PackArgs& A, int q0) {
   return v0 < v1 ? doc_of_warp(A.cu, A.batch, T, v0).lo / kTile : -1;
 }
 
-// The item of index `at`: from the list, or without one the last token tiles first; every lane of a warp calls it.
-__device__ __forceinline__ Item item_of(const FwdParams& P, int at) {
+// The item of index `at` whose unit and first keys are e.
+__device__ __forceinline__ Item item_from(const FwdParams& P, int at, int4 e) {
   const PackArgs& A = P.a;
   const int lane = at % P.lanes;
-  int unit = P.units - 1 - at / P.lanes;
-  int4 e = make_int4(unit, -1, -1, 0);
-  if (A.q_list) {
-    e = __ldg(A.q_list + at / P.lanes);
-    unit = e.x;
-  } else {
-    e.y = first_key(A, unit * (P.pair_heads ? 1 : 2) * kTile);
-    if (!P.pair_heads) e.z = first_key(A, (unit * 2 + 1) * kTile);
-  }
   Item it;
   const int per = P.pair_heads ? A.nql / 2 : A.nql;
   it.shard = lane / per;
   const int c = (lane % per) * (P.pair_heads ? 2 : 1);
   it.g = c / A.grp;
-  const int t0 = P.pair_heads ? unit : 2 * unit;
+  const int t0 = P.pair_heads ? e.x : 2 * e.x;
   auto tile = [&](int head, int t, int first) {
     return QTile{head, t * kTile, first < 0 ? 0 : first, first < 0 ? 0 : t + 1};
   };
@@ -118,6 +110,18 @@ __device__ __forceinline__ Item item_of(const FwdParams& P, int at) {
   return it;
 }
 
+// A block's first item, found by a whole warp: from the list, or without one the last token tiles first.
+__device__ __forceinline__ Item first_item(const FwdParams& P) {
+  const PackArgs& A = P.a;
+  const int at = static_cast<int>(blockIdx.x);
+  if (A.q_list) return item_from(P, at, __ldg(A.q_list + at / P.lanes));
+  const int unit = P.units - 1 - at / P.lanes;
+  int4 e = make_int4(unit, -1, -1, 0);
+  e.y = first_key(A, unit * (P.pair_heads ? 1 : 2) * kTile);
+  if (!P.pair_heads) e.z = first_key(A, (unit * 2 + 1) * kTile);
+  return item_from(P, at, e);
+}
+
 __device__ __forceinline__ bool active(const QTile& q, int j) { return j >= q.jbeg && j < q.jend; }
 
 // A query tile and the documents of its rows: rows [v0, v1) belong to some; the first of them to one that begins at
@@ -125,7 +129,7 @@ __device__ __forceinline__ bool active(const QTile& q, int j) { return j >= q.jb
 struct RowDocs {
   uint32_t begins[4];
   int lo, v0, v1;
-  int shard;                   // the tile itself, for the warps that work on it
+  int shard;                   // the tile itself, for the warps that work on it (< 0: no more)
   QTile tile;
 };
 static_assert(sizeof(RowDocs) == 48, "two of them in 96 bytes");
@@ -166,9 +170,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
   uint64_t* rows_full = o_full + 2;
   uint64_t* rows_empty = rows_full + 1;
   uint64_t* done_bar = rows_empty + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  uint64_t* item_bars = done_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bars + kQueueBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 + 2 * kRing + 8 + 1) * 8 + 8 <= 256, "barrier area");
+  static_assert((2 + 2 * kRing + 8 + 1 + kQueueBars) * 8 + 8 <= 256, "barrier area");
 
   const PackArgs& A = P.a;
   const int warp = uniform_warp();
@@ -176,12 +181,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
   const int total = P.units * P.lanes;
   int* status = A.status;
   const uint64_t tmo = P.timeout_ns;
-  // Round n of the persistent loop: blocks in turn, every other round in reverse, so that the block that
-  // took the heaviest item of a round takes the lightest of the next.
-  auto item_at = [&](int n) {
-    const int b = static_cast<int>(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    return n * static_cast<int>(gridDim.x) + b;
-  };
+  const ItemQueue<Item> queue{reinterpret_cast<Item*>(smem + C::OFF_BAR + 256), item_bars, abort_flag, status, tmo};
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -201,6 +201,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     *abort_flag = 0;
     fence_mbarrier_init();
   }
+  if (threadIdx.x == 64) {
+    queue.init(3);
+    fence_mbarrier_init();
+  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
@@ -217,13 +221,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int pos = 0, nq = 0;
-    Item ahead = {};
-    if (item_at(0) < total) ahead = item_of(P, item_at(0));     // the coming item is looked up while this one runs
-    for (int n = 0; item_at(n) < total; ++n) {
-      const Item it = ahead;
-      if (item_at(n + 1) < total) ahead = item_of(P, item_at(n + 1));
-      if (it.jhi <= it.jlo) continue;
-      if (lane == 0 && ok) {
+    Item it = first_item(P);
+    for (int n = 0; lane == 0 && ok && it.shard >= 0; ++n) {
+      Item coming = {};
+      coming.shard = -1;
+      auto announce = [&]() {
+        if (A.q_list) {
+          const int at = static_cast<int>(gridDim.x) + atomicAdd(A.q_taken, 1);
+          if (at < total) coming = item_from(P, at, __ldg(A.q_list + at / P.lanes));
+        }
+        ok = queue.announce(n + 1, coming);
+      };
+      const int when = max(it.jlo, it.jhi - kLead);
+      if (it.jhi <= it.jlo) {
+        announce();
+      } else {
         auto load = [&](const CUtensorMap* map, int j) {
           const int slot = pos % kRing;
           if (!wait_on(&ring_empty[slot], (static_cast<uint32_t>(pos / kRing) & 1u) ^ 1u, abort_flag, status, tmo))
@@ -248,9 +260,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
           ++nq;
         }
         ok = ok && load(&P.v[it.shard], it.jlo);
-        for (int j = it.jlo + 1; ok && j < it.jhi; ++j) ok = load(&P.k[it.shard], j) && load(&P.v[it.shard], j);
+        if (ok && it.jlo == when) announce();
+        for (int j = it.jlo + 1; ok && j < it.jhi; ++j) {
+          ok = load(&P.k[it.shard], j) && load(&P.v[it.shard], j);
+          if (ok && j == when) announce();
+        }
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      it = coming;
     }
     if (lane == 0) {
       // No copy may still be landing when the CTA leaves: wait (bounded) for the last loads.
@@ -280,14 +296,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     auto wait = [&](uint64_t* bar, int phase) {
       wait_on(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
     };
-    Item ahead = {};
-    if (item_at(0) < total) ahead = item_of(P, item_at(0));
-    for (int n = 0; item_at(n) < total; ++n) {
-      const Item it = ahead;
-      if (it.jhi <= it.jlo) {
-        if (item_at(n + 1) < total) ahead = item_of(P, item_at(n + 1));
-        continue;
-      }
+    Item it = first_item(P);
+    for (int n = 0; queue.next(n, it) && it.shard >= 0; ++n) {
+      if (it.jhi <= it.jlo) continue;
       wait(q_full, nq);
       tc_fence_after_sync();
       ++nq;
@@ -332,8 +343,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
           if (j + 2 == it.jhi) umma_commit(q_empty);   // the last S of the item is issued
         }
         __syncwarp();
-        // the coming item is looked up once the first scores run
-        if (j < it.jlo && item_at(n + 1) < total) ahead = item_of(P, item_at(n + 1));
         if (j + 1 < it.jhi) {              // on to K_(j + 2), past V_(j + 1)
           slot += 2;
           if (slot >= kRing) {
@@ -352,8 +361,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     // ------------------------------------------------------------------ documents of the rows of tile x
     const int x = warp - 2;
     bool ok = true;
-    for (int n = 0; ok && item_at(n) < total; ++n) {
-      const Item it = item_of(P, item_at(n));
+    Item it = first_item(P);
+    for (int n = 0; ok && it.shard >= 0 && queue.next(n, it); ++n) {   // (the end is passed on too)
       const QTile qt = x ? it.x[1] : it.x[0];
       RowDocs d = {{0, 0, 0, 0}, 0, 0, 0, it.shard, qt};
       if (qt.jend > qt.jbeg) {
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     const int T = static_cast<int>(A.T);
     bool ok = true;
     uint32_t ns = 0, no = 0;
-    for (int n = 0; ok && item_at(n) < total; ++n) {
+    for (int n = 0; ok; ++n) {
       ok = mbar_wait(rows_full, static_cast<uint32_t>(n) & 1u, abort_flag, status, tmo);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -396,6 +405,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
       }
       const QTile qt = docs[x].tile;
       const int shard = docs[x].shard;
+      if (shard < 0) break;
       const PackShard& S = A.s[shard];
       const int i = qt.q0 + r;
       const bool in = i >= docs[x].v0 && i < docs[x].v1;        // a row of a document (so i < T)
@@ -618,8 +628,10 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stre
     plan.q_list = static_cast<int4*>(list);
     plan.q_units = P.units;
     plan.q_per = P.pair_heads ? 1 : 2;
+    plan.q_taken = reinterpret_cast<int*>(plan.q_list + tiles);
     if ((rc = pack_attn_plan_launch(A, plan, 0, stream))) return rc;
     P.a.q_list = plan.q_list;
+    P.a.q_taken = plan.q_taken;
   }
   const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
   TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * tri * d * A.nql * A.t,

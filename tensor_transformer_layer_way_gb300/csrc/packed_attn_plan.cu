@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     return;
   }
   if (P.q_list) {
+    if (tid == 0) *P.q_taken = 0;
     hist[tid] = 0;
     __syncthreads();
     for (int pass = 0; pass < 2; ++pass) {
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     __syncthreads();
     if (tid == 0) {
       P.kv_head[0] = taken;
-      P.kv_head[2] = 0;
+      *P.kv_taken = 0;
     }
   }
 }
