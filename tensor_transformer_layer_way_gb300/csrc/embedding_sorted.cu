@@ -10,10 +10,10 @@
 // partial sums of a run that crosses chunks are joined in a fixed order.  No atomic adds to the gradient: the
 // same inputs give the same bits, and a row of the gradient is written once.
 //
-// What bounds it: the table's bytes where every row is written (8192 tokens, 151936 x 4096: 2.5 GB), else the
-// tokens' rows; the sort is latency.  Up to 16384 tokens it is one CTA in shared memory, and the other CTAs of
-// the same launch write the zeros of the rows that no token has meanwhile; beyond that three launches per
-// digit, and zeros everywhere first.
+// What bounds it: the table's bytes where every row is written (8192 tokens, 151936 x 4096: 2.5 GB, 400 us, 94% of
+// the copy rate), else the tokens' rows; the sort is latency.  Up to 16384 tokens it is one CTA in shared memory, and
+// the other CTAs of the same launch write the zeros of the rows that no token has meanwhile; beyond that three
+// launches per digit, and zeros everywhere first.  A few tokens of few columns need no sort: one launch.
 
 #include <mutex>
 
@@ -492,6 +492,121 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const __grid_co
   }
 }
 
+// ------------------------------------------------------------------ few tokens: no sort
+// Each CTA owns a slice of the vocabulary and picks the tokens of its rows out of all ids, in token order.  A warp
+// sums a row of few tokens, all warps one of many, each a part of the list, and the parts are added in order.  One launch
+// where the sorted path takes three, but a slice's rows are one CTA's work: for calls whose tokens' rows are few
+// bytes in all and the slices short.  Measured, this and the sorted path (us): 128 tokens x 256 columns, 2048 rows
+// 5.2 and 11.3; 1024 x 256, half of them one id, 11.3 and 15.4; 1000 x 256, 65000 rows 19.6 and 22.1; 256 x
+// 1024, half of them one id, 17.5 and 13.4; 1024 x 64, 200000 rows 33 and 27.
+
+constexpr int kDirectThreads = 512;
+constexpr int kDirectWarps = kDirectThreads / 32;
+constexpr int kDirectMost = 1024;       // tokens
+constexpr int kDirectWide = 512;        // columns
+constexpr int kDirectRows = 65536;
+constexpr int64_t kDirectWork = 1 << 18;   // tokens x columns
+constexpr int kDirectFew = 8;           // tokens that one warp sums alone
+
+// Adds columns [col, col + 8) of the row's tokens among entries [from, to) of the list, eight loads before their sums.
+__device__ __forceinline__ void direct_sum(float (&a)[8], const uint32_t* list, int from, int to, uint32_t row,
+                                           const __nv_bfloat16* dY, int64_t lddy, int64_t col, int64_t h) {
+  const int lane = threadIdx.x & 31;
+  for (int e0 = from; e0 < to; e0 += 32) {
+    const uint32_t e = e0 + lane < to ? list[e0 + lane] : 0;
+    unsigned m = __ballot_sync(0xffffffffu, e0 + lane < to && e / kDirectMost == row);
+    while (m) {
+      uint4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int at = m ? __ffs(m) - 1 : 32;
+        m &= m - 1;
+        const uint32_t tok = __shfl_sync(0xffffffffu, e, at & 31) % kDirectMost;
+        v[u] = at < 32 && col < h ? __ldg(reinterpret_cast<const uint4*>(dY + static_cast<int64_t>(tok) * lddy + col))
+                                  : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        a[0] += bf16_lo(v[u].x); a[1] += bf16_hi(v[u].x); a[2] += bf16_lo(v[u].y); a[3] += bf16_hi(v[u].y);
+        a[4] += bf16_lo(v[u].z); a[5] += bf16_hi(v[u].z); a[6] += bf16_lo(v[u].w); a[7] += bf16_hi(v[u].w);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kDirectThreads) embed_direct_kernel(const __grid_constant__ GradTables G,
+                                                                      const int64_t* ids, int T, int64_t V, int64_t Vs,
+                                                                      int64_t h, const __nv_bfloat16* dY, int64_t lddy,
+                                                                      float scale, int accumulate, int* status) {
+  __shared__ uint32_t list[kDirectMost];                   // row of the slice * kDirectMost + token
+  __shared__ uint32_t many[kDirectMost / kDirectFew];      // rows of more than kDirectFew tokens
+  __shared__ int found[kDirectWarps];
+  __shared__ int many_n;
+  __shared__ float4 part[kDirectWarps][2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t per = (V + gridDim.x - 1) / gridDim.x;
+  const int64_t lo = blockIdx.x * per, hi = lo + per < V ? lo + per : V;
+  if (threadIdx.x == 0) many_n = 0;
+  int n = 0;                                               // entries
+  for (int k0 = 0; k0 < T; k0 += kDirectThreads) {
+    const int k = k0 + static_cast<int>(threadIdx.x);
+    const int64_t id = k < T ? ids[k] : -1;
+    if (blockIdx.x == 0 && k < T && (id < 0 || id >= V)) atomicCAS(status, 0, TTL_ERR_DEVICE);
+    const bool mine = id >= lo && id < hi;
+    const unsigned m = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) found[warp] = __popc(m);
+    __syncthreads();
+    int at = n;
+#pragma unroll
+    for (int w = 0; w < kDirectWarps; ++w) {
+      at += w < warp ? found[w] : 0;
+      n += found[w];
+    }
+    if (mine) list[at + __popc(m & ((1u << lane) - 1))] = static_cast<uint32_t>(id - lo) * kDirectMost + k;
+    __syncthreads();
+  }
+  auto out = [&](int64_t r, int64_t col, const float (&a)[8]) {
+    row_out(row_of(G, static_cast<uint32_t>(lo + r), Vs, h) + col, a, scale, accumulate);
+  };
+  for (int64_t r = warp; r < hi - lo; r += kDirectWarps) {
+    int tokens = 0;
+    for (int e0 = 0; e0 < n; e0 += 32)
+      tokens += __popc(__ballot_sync(0xffffffffu, e0 + lane < n && list[e0 + lane] / kDirectMost == static_cast<uint32_t>(r)));
+    if (tokens > kDirectFew) {
+      if (lane == 0) many[atomicAdd(&many_n, 1)] = static_cast<uint32_t>(r);   // (their order does not matter)
+      continue;
+    }
+    if (tokens == 0 && accumulate) continue;
+    for (int64_t c0 = 0; c0 < h; c0 += 256) {
+      const int64_t col = c0 + lane * 8;
+      float a[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (tokens > 0) direct_sum(a, list, 0, n, static_cast<uint32_t>(r), dY, lddy, col, h);
+      if (col < h) out(r, col, a);
+    }
+  }
+  __syncthreads();
+  const int share = (n + kDirectWarps - 1) / kDirectWarps, from = warp * share, to = min(n, from + share);
+  for (int i = 0; i < many_n; ++i)
+    for (int64_t c0 = 0; c0 < h; c0 += 256) {
+      const int64_t col = c0 + lane * 8;
+      float a[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      direct_sum(a, list, from, to, many[i], dY, lddy, col, h);
+      part[warp][0][lane] = make_float4(a[0], a[1], a[2], a[3]);
+      part[warp][1][lane] = make_float4(a[4], a[5], a[6], a[7]);
+      __syncthreads();
+      if (warp == 0 && col < h) {
+#pragma unroll
+        for (int w = 1; w < kDirectWarps; ++w) {
+          const float4 p = part[w][0][lane], q = part[w][1][lane];
+          a[0] += p.x; a[1] += p.y; a[2] += p.z; a[3] += p.w;
+          a[4] += q.x; a[5] += q.y; a[6] += q.z; a[7] += q.w;
+        }
+        out(many[i], col, a);
+      }
+      __syncthreads();
+    }
+}
+
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct SortPlan {
@@ -630,12 +745,22 @@ extern "C" int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t
   // one launch for the sort and the zeros, where the tokens fit one CTA and a slice's marks its shared memory
   const int sms = num_sms();
   const bool one = T > 0 && T <= kOneMost && sms > 1 && V / (sms - 1) / 8 + 64 < static_cast<int64_t>(kOneSmem);
-  if (!accumulate && !one) {
+  const bool direct = T <= kDirectMost && h <= kDirectWide && V <= kDirectRows && T * h <= kDirectWork;
+  if (!accumulate && (T == 0 || !(one || direct))) {
     TraceScope trace(s, TTL_K_OTHER, 0.0, 4.0 * V * h);
     for (int i = 0; i < t; ++i)
       if ((rc = fill_zero(dE[i], static_cast<size_t>(Vs) * h * 4, s))) return rc;
   }
   if (T == 0) return TTL_OK;
+  if (direct) {
+    TraceScope trace(s, TTL_K_EMBED, 0.0, static_cast<double>(T) * h * 2.0 + (accumulate ? 0.0 : 4.0 * V * h));
+    const int64_t most = (V + kDirectThreads / 32 - 1) / (kDirectThreads / 32);   // a row per warp at least
+    const unsigned grid = static_cast<unsigned>(most < 2 * sms ? most : 2 * sms);
+    embed_direct_kernel<<<grid, kDirectThreads, 0, s>>>(G, ids, static_cast<int>(T), V, Vs, h,
+                                                        reinterpret_cast<const __nv_bfloat16*>(dY), lddy, scale,
+                                                        accumulate, status);
+    return cuda_check(cudaGetLastError(), "embed_direct_kernel launch");
+  }
 
   const SortPlan p = plan_of(T, h);
   char* base = static_cast<char*>(ws);

@@ -158,3 +158,31 @@ def test_graph_replay_on_a_side_stream():
     torch.cuda.synchronize()
     for a, b in zip(want, dE):
         assert torch.equal(a, b)
+
+
+# Few tokens of few columns: one launch, each CTA a slice of the rows.  The largest of each, one row, one column
+# block past a warp's, more tokens of one id than one warp sums alone, slices of one row.
+@pytest.mark.parametrize("kind", ["uniform", "half", "same"])
+@pytest.mark.parametrize("t,T,h,V", [(1, 1024, 256, 2000), (2, 1000, 72, 2 * 30000), (1, 512, 512, 5), (4, 700, 264, 4 * 1000),
+                                     (1, 1024, 8, 65536), (1, 9, 512, 1), (2, 8, 504, 2), (8, 100, 256, 8 * 8192)])
+def test_gradient_of_few_tokens(t, T, h, V, kind):
+    test_gradient(t, T, h, V, kind)
+
+
+@pytest.mark.parametrize("T,h", [(700, 64), (2000, 64), (700, 1024)])
+def test_strided_rows_and_bad_ids_at_each_size(T, h):
+    t, V = 2, 2 * 300
+    ids = _ids("half", T, V, T)
+    bad = ids.clone()
+    keep = torch.rand(T, generator=torch.Generator().manual_seed(1)) < 0.9
+    bad[~keep] = V + 5
+    dY = torch.randn(T, 3 * h, device="cuda").to(torch.bfloat16)[:, 2 * h:]
+    dE = [torch.empty(V // t, h, device="cuda") for _ in range(t)]
+    ttl.vocab_parallel_embedding_sorted_bwd(bad.cuda(), dY, 1.5, dE)
+    assert ttl.device_status() == ttl.TTL_ERR_DEVICE
+    _check(ids[keep].cuda(), dY[keep.cuda()], 1.5, dE, V)
+    base = torch.randn(V, h, device="cuda")
+    acc = [b.clone() for b in base.chunk(t)]
+    ttl.vocab_parallel_embedding_sorted_bwd(bad.cuda(), dY, 1.5, acc, accumulate=True)
+    assert ttl.device_status() == ttl.TTL_ERR_DEVICE
+    _check(ids[keep].cuda(), dY[keep.cuda()], 1.5, acc, V, base)
