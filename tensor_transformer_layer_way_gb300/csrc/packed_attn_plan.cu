@@ -63,37 +63,45 @@ __device__ __forceinline__ int work_class(int work, int shift) {
 }
 
 // D of one token of one shard, all its heads, by a warp: 256 columns at a time, d / 8 lanes for each head.
-__device__ __forceinline__ void row_dots(const PackArgs& A, int shard, int64_t i, int d) {
+template <int D>
+__device__ __forceinline__ void row_dots(const PackArgs& A, int shard, int64_t i) {
+  constexpr int kLanes = D / 8, kHeads = 256 / D;   // lanes of a head, heads of 256 columns
   const int lane = threadIdx.x & 31;
   const PackShard& S = A.s[shard];
-  const int cols = A.nql * d, lph = d / 8;
+  const __nv_bfloat16* a_at = S.dO + i * A.lddo + lane * 8;
+  const __nv_bfloat16* b_at = S.o + i * A.ldo + lane * 8;
+  int head = lane / kLanes;
+  float* out = A.D + (static_cast<int64_t>(shard) * A.nql + head) * A.T + i;
 #pragma unroll 2
-  for (int base = 0; base < cols; base += 256) {
-    const int c = base + lane * 8;
+  for (; head - lane / kLanes < A.nql; head += kHeads, a_at += 256, b_at += 256, out += kHeads * A.T) {
     float acc = 0.0f;
-    if (c < cols) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(S.dO + i * A.lddo + c));
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(S.o + i * A.ldo + c));
+    if (head < A.nql) {
+      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(a_at)), b = __ldcs(reinterpret_cast<const uint4*>(b_at));
       const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int w = 0; w < 4; ++w) acc = fmaf(bf16_lo(aw[w]), bf16_lo(bw[w]), fmaf(bf16_hi(aw[w]), bf16_hi(bw[w]), acc));
     }
-    for (int o = lph >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (c < cols && (lane & (lph - 1)) == 0) A.D[(static_cast<int64_t>(shard) * A.nql + c / d) * A.T + i] = acc;
+#pragma unroll
+    for (int o = kLanes >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (head < A.nql && lane % kLanes == 0) *out = acc;
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_constant__ PackArgs A,
                                                                  const __grid_constant__ PackPlan P, int q_shift,
-                                                                 int kv_shift, int d) {
+                                                                 int kv_shift, int d, unsigned blocks) {
   __shared__ int hist[kPlanThreads];
   __shared__ int warp_tot[32];
   __shared__ unsigned long long total;
   __shared__ int taken, joins, longest;
   const int tid = threadIdx.x;
   if (blockIdx.x > 0) {
-    const int64_t w = static_cast<int64_t>(blockIdx.x - 1) * (kPlanThreads / 32) + (tid >> 5);
-    if (w < A.t * A.T) row_dots(A, static_cast<int>(w / A.T), w % A.T, d);
+    const unsigned shard = (blockIdx.x - 1) / blocks;
+    const int64_t i = static_cast<int64_t>(blockIdx.x - 1 - shard * blocks) * (kPlanThreads / 32) + (tid >> 5);
+    if (i < A.T) {
+      if (d == 128) row_dots<128>(A, static_cast<int>(shard), i);
+      else row_dots<64>(A, static_cast<int>(shard), i);
+    }
     return;
   }
   if (P.q_list) {
@@ -187,11 +195,12 @@ int pack_attn_plan_launch(const PackArgs& A, const PackPlan& plan, int d, cudaSt
   int q_shift = 0, kv_shift = 0;
   while ((2 * static_cast<int64_t>(tiles) >> q_shift) >= kPlanThreads) ++q_shift;
   while ((static_cast<int64_t>(tiles) * A.grp >> kv_shift) >= kPlanThreads) ++kv_shift;
-  // d > 0: with D, one warp per (shard, token)
+  // d > 0: with D, one warp per (shard, token) and `blocks` blocks a shard
   const int64_t rows = d > 0 ? A.t * A.T : 0;
   TraceScope trace(stream, TTL_K_OTHER, 0.0, 32.0 * tiles + 4.0 * rows * A.nql * d);
-  const unsigned grid = 1 + static_cast<unsigned>((rows + kPlanThreads / 32 - 1) / (kPlanThreads / 32));
-  pack_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(A, plan, q_shift, kv_shift, d);
+  const unsigned blocks = d > 0 ? static_cast<unsigned>((A.T + kPlanThreads / 32 - 1) / (kPlanThreads / 32)) : 0;
+  const unsigned grid = 1 + blocks * A.t;
+  pack_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(A, plan, q_shift, kv_shift, d, blocks);
   return cuda_check(cudaGetLastError(), "pack_plan_kernel launch");
 }
 
