@@ -217,6 +217,15 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
     A.join_list = plan.join_list;
     A.part = reinterpret_cast<float*>(base + w.part);
   }
-  if ((rc = pack_attn_plan_launch(A, plan, d, s)) || (rc = pack_attn_dq_launch(A, d, s)) || (rc = pack_attn_dkv_launch(A, d, s))) return rc;
+  PackMaps maps = {};
+  for (int i = 0; i < t; ++i)
+    if ((rc = encode_map_bf16(&maps.q[i], A.s[i].q, T, qc, ldq, 64, kTile)) ||
+        (rc = encode_map_bf16(&maps.k[i], A.s[i].k, T, kc, ldk, 64, kTile)) ||
+        (rc = encode_map_bf16(&maps.v[i], A.s[i].v, T, kc, ldv, 64, kTile)) ||
+        (rc = encode_map_bf16(&maps.dO[i], A.s[i].dO, T, qc, lddo, 64, kTile)))
+      return rc;
+  if ((rc = pack_attn_plan_launch(A, plan, d, s)) || (rc = pack_attn_dq_launch(A, maps, d, s)) ||
+      (rc = pack_attn_dkv_launch(A, maps, d, s)))
+    return rc;
   return split ? pack_attn_join_launch(A, d, s) : TTL_OK;
 }

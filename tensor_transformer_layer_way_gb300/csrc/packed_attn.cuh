@@ -47,6 +47,11 @@ struct PackArgs {
 // keys; a tile's last key tile is its own.
 // A key unit: {key tile, last query tile, first step, end step} {slot of its partial sums or -1, 0, 0, 0}.
 
+// The operands that both kernels of the backward pass load, in boxes of 64 x 128, made once for both.
+struct PackMaps {
+  CUtensorMap q[kMaxShards], k[kMaxShards], v[kMaxShards], dO[kMaxShards];
+};
+
 // What the plan kernel writes for a launch (null: not wanted).
 struct PackPlan {
   int4* q_list;
@@ -77,8 +82,8 @@ int set_core_smem_once(const void* fn, int slot, int bytes, const char* what);
 // Launches of the tensor-core kernels (arguments are checked; A.s holds every pointer they need).
 // `list`: room for one word of 16 bytes per 128 tokens and one more.
 int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stream);
-int pack_attn_dq_launch(const PackArgs& A, int d, cudaStream_t stream);    // dQ, after D
-int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream);   // dK and dV, after D
+int pack_attn_dq_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStream_t stream);    // dQ, after D
+int pack_attn_dkv_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStream_t stream);   // dK and dV, after D
 
 constexpr int kTile = 128;       // tokens per query or key tile
 constexpr int kTmemCols = 512;

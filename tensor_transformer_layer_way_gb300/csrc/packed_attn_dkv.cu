@@ -25,8 +25,6 @@
 // thread, each of the four warpgroups on 32 of the queries (on 64 each, two warpgroups took 1450 cycles from
 // S to P, longer than dK and dP run).
 
-#include <cstring>
-
 #include "packed_attn.cuh"
 
 namespace ttl {
@@ -38,10 +36,7 @@ constexpr int kRing = 5;       // places of the Q and dO tiles: Q_0, dO_0, Q_1, 
 constexpr int kStat = 2;       // lse and D stages
 
 struct KvParams {
-  CUtensorMap q[kMaxShards];   // box 64 x 128
-  CUtensorMap k[kMaxShards];
-  CUtensorMap v[kMaxShards];
-  CUtensorMap dO[kMaxShards];
+  PackMaps m;
   PackArgs a;
   int tiles, lanes;
   uint64_t timeout_ns;
@@ -228,15 +223,15 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         };
         for (int t = 0; ok && t < it.steps; ++t) {
           if (t == 0) {
-            ok = load(sK, &P.k[it.shard], k_full, k_empty, nk, it.g * D, it.k0);
+            ok = load(sK, &P.m.k[it.shard], k_full, k_empty, nk, it.g * D, it.k0);
             nk += ok;
           }
-          ok = ok && load_ring(&P.q[it.shard], step_head(it, t) * D, step_q0(it, t));
+          ok = ok && load_ring(&P.m.q[it.shard], step_head(it, t) * D, step_q0(it, t));
           if (ok && t == 0) {
-            ok = load(sV, &P.v[it.shard], v_full, v_empty, nv, it.g * D, it.k0);
+            ok = load(sV, &P.m.v[it.shard], v_full, v_empty, nv, it.g * D, it.k0);
             nv += ok;
           }
-          ok = ok && load_ring(&P.dO[it.shard], step_head(it, t) * D, step_q0(it, t));
+          ok = ok && load_ring(&P.m.dO[it.shard], step_head(it, t) * D, step_q0(it, t));
           if (ok && t == when) announce();
         }
       }
@@ -611,19 +606,12 @@ int pack_attn_join_launch(const PackArgs& A, int d, cudaStream_t stream) {
   return cuda_check(launch_after(pack_join_kernel<64>, dim3(grid), 256, 0, stream, A), "pack_join_kernel launch");
 }
 
-int pack_attn_dkv_launch(const PackArgs& A, int d, cudaStream_t stream) {
+int pack_attn_dkv_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStream_t stream) {
   KvParams P;
-  std::memset(static_cast<void*>(&P), 0, sizeof(P));
   P.a = A;
+  P.m = maps;
   const int64_t qc = static_cast<int64_t>(A.nql) * d, kc = static_cast<int64_t>(A.nkvl) * d;
   int rc = TTL_OK;
-  for (int i = 0; i < A.t; ++i) {
-    if ((rc = encode_map_bf16(&P.q[i], A.s[i].q, A.T, qc, A.ldq, 64, kTile)) ||
-        (rc = encode_map_bf16(&P.k[i], A.s[i].k, A.T, kc, A.ldk, 64, kTile)) ||
-        (rc = encode_map_bf16(&P.v[i], A.s[i].v, A.T, kc, A.ldv, 64, kTile)) ||
-        (rc = encode_map_bf16(&P.dO[i], A.s[i].dO, A.T, qc, A.lddo, 64, kTile)))
-      return rc;
-  }
   P.tiles = static_cast<int>((A.T + kTile - 1) / kTile);
   P.lanes = A.t * A.nkvl;
   P.timeout_ns = 2000000000ull;

@@ -17,8 +17,6 @@
 // document of 16384 tokens, 4 query heads and 1 KV head of 128: 270 us, 1530 TFLOP/s; 8192 tokens in 12
 // documents, 32 and 8 heads over 8 shards: 129 us.
 
-#include <cstring>
-
 #include "packed_attn.cuh"
 
 namespace ttl {
@@ -30,10 +28,7 @@ constexpr int kKSlots = 3;
 constexpr int kVSlots = 2;
 
 struct DqParams {
-  CUtensorMap q[kMaxShards];   // box 64 x 128
-  CUtensorMap k[kMaxShards];
-  CUtensorMap v[kMaxShards];
-  CUtensorMap dO[kMaxShards];
+  PackMaps m;
   PackArgs a;
   int tiles, lanes;
   uint64_t timeout_ns;
@@ -214,8 +209,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         if (ok) {
           mbar_arrive_expect_tx(q_full, 2 * C::TILE);
           for (int kb = 0; kb < C::KB; ++kb) {
-            tma_load_2d(sQ + kb * 16384, &P.q[it.shard], q_full, it.c * D + kb * 64, it.q0);
-            tma_load_2d(sDO + kb * 16384, &P.dO[it.shard], q_full, it.c * D + kb * 64, it.q0);
+            tma_load_2d(sQ + kb * 16384, &P.m.q[it.shard], q_full, it.c * D + kb * 64, it.q0);
+            tma_load_2d(sDO + kb * 16384, &P.m.dO[it.shard], q_full, it.c * D + kb * 64, it.q0);
           }
           ++nq;
         }
@@ -225,7 +220,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           if (!ok) break;
           mbar_arrive_expect_tx(&k_full[ks], C::TILE);
           for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_2d(sK + ks * C::TILE + kb * 16384, &P.k[it.shard], &k_full[ks], it.g * D + kb * 64, j * kTile);
+            tma_load_2d(sK + ks * C::TILE + kb * 16384, &P.m.k[it.shard], &k_full[ks], it.g * D + kb * 64, j * kTile);
           // (K was started: from here the position counts as started even if the wait for V fails)
           ok = wait_on(&v_empty[vs], (static_cast<uint32_t>(pos / kVSlots) & 1u) ^ 1u, abort_flag, status, tmo);
           if (!ok) {
@@ -236,7 +231,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           }
           mbar_arrive_expect_tx(&v_full[vs], C::TILE);
           for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_2d(sV + vs * C::TILE + kb * 16384, &P.v[it.shard], &v_full[vs], it.g * D + kb * 64, j * kTile);
+            tma_load_2d(sV + vs * C::TILE + kb * 16384, &P.m.v[it.shard], &v_full[vs], it.g * D + kb * 64, j * kTile);
           if (j == when) announce();
         }
       }
@@ -528,19 +523,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
 
 }  // namespace
 
-int pack_attn_dq_launch(const PackArgs& A, int d, cudaStream_t stream) {
+int pack_attn_dq_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStream_t stream) {
   DqParams P;
-  std::memset(static_cast<void*>(&P), 0, sizeof(P));
   P.a = A;
+  P.m = maps;
   const int64_t qc = static_cast<int64_t>(A.nql) * d, kc = static_cast<int64_t>(A.nkvl) * d;
   int rc = TTL_OK;
-  for (int i = 0; i < A.t; ++i) {
-    if ((rc = encode_map_bf16(&P.q[i], A.s[i].q, A.T, qc, A.ldq, 64, kTile)) ||
-        (rc = encode_map_bf16(&P.k[i], A.s[i].k, A.T, kc, A.ldk, 64, kTile)) ||
-        (rc = encode_map_bf16(&P.v[i], A.s[i].v, A.T, kc, A.ldv, 64, kTile)) ||
-        (rc = encode_map_bf16(&P.dO[i], A.s[i].dO, A.T, qc, A.lddo, 64, kTile)))
-      return rc;
-  }
   P.tiles = static_cast<int>((A.T + kTile - 1) / kTile);
   P.lanes = A.t * A.nql;
   P.timeout_ns = 2000000000ull;
