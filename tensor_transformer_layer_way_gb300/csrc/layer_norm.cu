@@ -21,7 +21,8 @@
 namespace ttl {
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 512;
+constexpr size_t kAnySums = 220000;   // bytes
 constexpr int kNormParts = 456;   // partial sums of the weight gradients: at most three per SM of a 152-SM part
 
 struct NormFwd {
@@ -54,12 +55,6 @@ struct NormBwd {
   int wtype;
   int* status;
 };
-
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 __device__ __forceinline__ float load_w(const void* w, int wtype, int64_t i) {
   return wtype == TTL_T_F32 ? static_cast<const float*>(w)[i]
@@ -109,7 +104,8 @@ struct Cursor {
 // Rows below 1 KiB: a row belongs to W warps; each thread holds NV words of B bytes of it (16 where every row
 // starts on 16 bytes and holds whole words, else 4 or 2), so the row is read once and the weights stay in registers over
 // the persistent loop.  The next row's words are loaded before this one's sums.  A CTA of narrow rows has
-// several groups of W warps, each with rows of its own.
+// several groups of W warps, each with rows of its own.  Measured, 65536 rows of 256 bf16: forward 28 us (2.4 TB/s),
+// backward 39 us (2.6 TB/s); bound by a row's chain of loads, sums and stores.
 
 template <int B> struct Word;
 template <> struct Word<16> { using type = uint4; };
@@ -419,6 +415,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_kernel(const __grid_c
 // pieces, so a row that does not start on one is copied with its neighbours' bytes (they belong to the same
 // slab; at the slab's own ends the copy is cut and the few elements outside it are stored beside it by hand), and
 // its words are read from shared memory at the row's own offset.
+// Measured, 8192 rows of 4096: fp32 forward 44 us (6.1 TB/s, 90% of the copy rate), backward 71 us (83%); bf16
+// with a residual 50 us (5.3 TB/s, 79%) and 61 us (4.4 TB/s, 65%), 7 of them the join of the weight gradients.
+// Rows of 4001 bf16, whose words are single values: 81 and 95 us.
 
 constexpr int kMaxStages = 6;
 constexpr uint64_t kNormTimeout = 2000000000ull;
@@ -909,37 +908,89 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_ring_kernel(const __g
 
 // ------------------------------------------------------------------ rows of any width
 
-// One row per CTA at a time, any width, stride and alignment; the row is read again for each step
-// (from L1 / L2).
-template <typename T>
+// E weights from column c on (a multiple of E), in wide loads where they start on 16 bytes.
+template <int E>
+__device__ __forceinline__ void load_weights(const void* w, int wtype, int64_t c, float (&f)[E]) {
+  const bool wide = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+  if constexpr (E >= 4) {
+    if (wide && wtype == TTL_T_F32) {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + e);
+        f[e] = v.x; f[e + 1] = v.y; f[e + 2] = v.z; f[e + 3] = v.w;
+      }
+      return;
+    }
+    if (wide) {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + c + e);
+        f[e] = bf16_lo(v.x); f[e + 1] = bf16_hi(v.x); f[e + 2] = bf16_lo(v.y); f[e + 3] = bf16_hi(v.y);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) f[e] = load_w(w, wtype, c + e);
+}
+
+// One row per CTA at a time, any width, stride and alignment; the row is read again for each step (from L1 / L2), by
+// words of 16 bytes where every row is made of them, else value by value.  Measured, 2048 rows of 20000 bf16: forward
+// 52 us (3.2 TB/s), backward 132 us (1.9 TB/s; 241 with its sums value by value); 2730 rows of 12288 fp32 with ds,
+// too wide for the ring's three rows: 129 us (4.2 TB/s), of 12287: 277.
+template <typename T, int B>
 __global__ void __launch_bounds__(kNormThreads) norm_fwd_any_kernel(const __grid_constant__ NormFwd P) {
+  using Wd = typename Word<B>::type;
+  constexpr int E = B / sizeof(T);
   __shared__ float red[kNormThreads / 32];
+  const int64_t words = P.h / E;
   for (int64_t row = blockIdx.x; row < P.total; row += gridDim.x) {
     const int i = static_cast<int>(row / P.rows);
     const int64_t k = row - i * P.rows;
-    const T* x = static_cast<const T*>(P.x[i]) + k * P.ldx;
-    const T* r = P.r[i] ? static_cast<const T*>(P.r[i]) + k * P.ldr : nullptr;
-    T* s = r ? static_cast<T*>(P.s[i]) + k * P.h : nullptr;
-    T* y = static_cast<T*>(P.y[i]) + k * P.h;
-    auto at = [&](int64_t c) {
-      return r ? to_f(from_f<T>(to_f(x[c]) + to_f(r[c]))) : to_f(x[c]);
-    };
+    const Wd* x = reinterpret_cast<const Wd*>(static_cast<const T*>(P.x[i]) + k * P.ldx);
+    const Wd* r = P.r[i] ? reinterpret_cast<const Wd*>(static_cast<const T*>(P.r[i]) + k * P.ldr) : nullptr;
+    Wd* s = r ? reinterpret_cast<Wd*>(static_cast<T*>(P.s[i]) + k * P.h) : nullptr;
+    Wd* y = reinterpret_cast<Wd*>(static_cast<T*>(P.y[i]) + k * P.h);
     float sum = 0.0f;
-    for (int64_t c = threadIdx.x; c < P.h; c += kNormThreads) {
-      const float v = at(c);
-      if (s) s[c] = from_f<T>(v);
-      sum += v;
+#pragma unroll 4
+    for (int64_t v = threadIdx.x; v < words; v += kNormThreads) {
+      float f[E];
+      unpack<T, B>(x[v], f);
+      if (r) {
+        float g[E];
+        unpack<T, B>(r[v], g);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] += g[e];
+        const Wd w = pack<T, B>(f);                        // the stream's type: what is normalised is what is kept
+        unpack<T, B>(w, f);
+        s[v] = w;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum += f[e];
     }
+    const Wd* in = r ? s : x;                              // (each thread reads the words that it wrote)
     const float mean = block_sum(sum, red) / static_cast<float>(P.h);
     float sq = 0.0f;
-    for (int64_t c = threadIdx.x; c < P.h; c += kNormThreads) {
-      const float v = at(c) - mean;
-      sq = fmaf(v, v, sq);
+#pragma unroll 4
+    for (int64_t v = threadIdx.x; v < words; v += kNormThreads) {
+      float f[E];
+      unpack<T, B>(in[v], f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sq = fmaf(f[e] - mean, f[e] - mean, sq);
     }
     const float rstd = 1.0f / sqrtf(block_sum(sq, red) / static_cast<float>(P.h) + P.eps);
-    for (int64_t c = threadIdx.x; c < P.h; c += kNormThreads) {
-      const float b = P.beta ? load_w(P.beta, P.wtype, c) : 0.0f;
-      y[c] = from_f<T>(fmaf((at(c) - mean) * rstd, load_w(P.gamma, P.wtype, c), b));
+#pragma unroll 2
+    for (int64_t v = threadIdx.x; v < words; v += kNormThreads) {
+      float f[E];
+      unpack<T, B>(in[v], f);
+      float ga[E], be[E];
+      load_weights<E>(P.gamma, P.wtype, v * E, ga);
+#pragma unroll
+      for (int e = 0; e < E; ++e) be[e] = 0.0f;
+      if (P.beta) load_weights<E>(P.beta, P.wtype, v * E, be);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = fmaf((f[e] - mean) * rstd, ga[e], be[e]);
+      y[v] = pack<T, B>(f);
     }
     if (threadIdx.x == 0) {
       P.mean[i][k] = mean;
@@ -948,40 +999,91 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_any_kernel(const __grid
   }
 }
 
-// The same for the backward pass.  CTA b takes rows b, b + grid, ...; each thread owns its columns'
-// partial sums of dgamma and dbeta, in the CTA's slice of the workspace.
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads) norm_bwd_any_kernel(const __grid_constant__ NormBwd P) {
+// The same for the backward pass.  CTA b takes rows b, b + grid, ...; each thread owns its columns' sums of dgamma
+// and dbeta, in shared memory where they fit (`near`), else in the CTA's slice of the workspace.
+template <typename T, int B>
+__global__ void __launch_bounds__(kNormThreads) norm_bwd_any_kernel(const __grid_constant__ NormBwd P, int near) {
+  using Wd = typename Word<B>::type;
+  constexpr int E = B / sizeof(T);
+  extern __shared__ __align__(16) float any_sums[];        // [2][h]
   __shared__ float red[kNormThreads / 32];
-  float* pg = P.part + static_cast<int64_t>(blockIdx.x) * 2 * P.h;
+  const int64_t words = P.h / E;
+  float* part = P.part + static_cast<int64_t>(blockIdx.x) * 2 * P.h;
+  float* pg = near ? any_sums : part;
   float* pb = pg + P.h;
-  for (int64_t c = threadIdx.x; c < P.h; c += kNormThreads) pg[c] = pb[c] = 0.0f;
+  for (int64_t v = threadIdx.x; v < words; v += kNormThreads)
+#pragma unroll
+    for (int e = 0; e < E; ++e) pg[v * E + e] = pb[v * E + e] = 0.0f;
   for (int64_t row = blockIdx.x; row < P.total; row += gridDim.x) {
     const int i = static_cast<int>(row / P.rows);
     const int64_t k = row - i * P.rows;
-    const T* x = static_cast<const T*>(P.x[i]) + k * P.ldx;
-    const T* dy = static_cast<const T*>(P.dy[i]) + k * P.lddy;
-    const T* ds = P.ds[i] ? static_cast<const T*>(P.ds[i]) + k * P.ldds : nullptr;
-    T* dx = static_cast<T*>(P.dx[i]) + k * P.h;
+    const Wd* x = reinterpret_cast<const Wd*>(static_cast<const T*>(P.x[i]) + k * P.ldx);
+    const Wd* dy = reinterpret_cast<const Wd*>(static_cast<const T*>(P.dy[i]) + k * P.lddy);
+    const Wd* ds = P.ds[i] ? reinterpret_cast<const Wd*>(static_cast<const T*>(P.ds[i]) + k * P.ldds) : nullptr;
+    Wd* dx = reinterpret_cast<Wd*>(static_cast<T*>(P.dx[i]) + k * P.h);
     const float mean = P.mean[i][k], rstd = P.rstd[i][k];
     float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t c = threadIdx.x; c < P.h; c += kNormThreads) {
-      const float d = to_f(dy[c]), xh = (to_f(x[c]) - mean) * rstd;
-      const float g = d * load_w(P.gamma, P.wtype, c);
-      s1 += g;
-      s2 = fmaf(g, xh, s2);
-      pg[c] = fmaf(d, xh, pg[c]);
-      pb[c] += d;
+#pragma unroll 2
+    for (int64_t v = threadIdx.x; v < words; v += kNormThreads) {
+      float f[E], d[E];
+      unpack<T, B>(x[v], f);
+      unpack<T, B>(dy[v], d);
+      float ga[E];
+      load_weights<E>(P.gamma, P.wtype, v * E, ga);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float g = d[e] * ga[e];
+        f[e] = (f[e] - mean) * rstd;
+        s1 += g;
+        s2 = fmaf(g, f[e], s2);
+      }
+      if constexpr (E >= 4) {
+        float4* a = reinterpret_cast<float4*>(pg + v * E);
+        float4* b = reinterpret_cast<float4*>(pb + v * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          float4 p = a[e / 4], q = b[e / 4];
+          p.x = fmaf(d[e], f[e], p.x);
+          p.y = fmaf(d[e + 1], f[e + 1], p.y);
+          p.z = fmaf(d[e + 2], f[e + 2], p.z);
+          p.w = fmaf(d[e + 3], f[e + 3], p.w);
+          q.x += d[e];
+          q.y += d[e + 1];
+          q.z += d[e + 2];
+          q.w += d[e + 3];
+          a[e / 4] = p;
+          b[e / 4] = q;
+        }
+      } else {
+        pg[v] = fmaf(d[0], f[0], pg[v]);
+        pb[v] += d[0];
+      }
     }
     const float c1 = block_sum(s1, red) / static_cast<float>(P.h);
     const float c2 = block_sum(s2, red) / static_cast<float>(P.h);
-    for (int64_t c = threadIdx.x; c < P.h; c += kNormThreads) {
-      const float xh = (to_f(x[c]) - mean) * rstd;
-      const float g = to_f(dy[c]) * load_w(P.gamma, P.wtype, c);
-      float v = rstd * (g - c1 - xh * c2);
-      if (ds) v += to_f(ds[c]);
-      dx[c] = from_f<T>(v);
+#pragma unroll 2
+    for (int64_t v = threadIdx.x; v < words; v += kNormThreads) {
+      float f[E], d[E];
+      unpack<T, B>(x[v], f);
+      unpack<T, B>(dy[v], d);
+      float ga[E];
+      load_weights<E>(P.gamma, P.wtype, v * E, ga);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float xh = (f[e] - mean) * rstd;
+        f[e] = rstd * (d[e] * ga[e] - c1 - xh * c2);
+      }
+      if (ds) {
+        unpack<T, B>(ds[v], d);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] += d[e];
+      }
+      dx[v] = pack<T, B>(f);
     }
+  }
+  if (near) {
+    __syncthreads();
+    for (int64_t c = threadIdx.x; c < 2 * P.h; c += kNormThreads) part[c] = any_sums[c];
   }
 }
 
@@ -1148,6 +1250,17 @@ int bwd_regs(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
   return TTL_OK;
 }
 
+// Up to 220 KB of sums stay in shared memory; the partial rows are as many as the CTAs that fit then.
+template <typename T, int B>
+int bwd_any(const NormBwd& P, int parts, cudaStream_t s) {
+  const size_t sums = static_cast<size_t>(P.h) * 8;
+  const int near = sums <= kAnySums;
+  if (near)
+    if (int rc = allow_smem<norm_bwd_any_kernel<T, B>>(sums)) return rc;
+  norm_bwd_any_kernel<T, B><<<parts, kNormThreads, near ? sums : 0, s>>>(P, near);
+  return TTL_OK;
+}
+
 template <typename T, int B>
 int pick_fwd(const NormFwd& P, const Spread& sp, cudaStream_t s) {
   constexpr int E = B / sizeof(T);
@@ -1244,8 +1357,13 @@ extern "C" int ttl_layer_norm_fwd(int t, int64_t rows, int64_t h, int x_type, in
   if (sp.W == 0) {
     const int64_t cap = static_cast<int64_t>(num_sms()) * 8;
     const unsigned grid = static_cast<unsigned>(P.total < cap ? P.total : cap);
-    if (x_type == TTL_T_F32) norm_fwd_any_kernel<float><<<grid, kNormThreads, 0, s>>>(P);
-    else norm_fwd_any_kernel<__nv_bfloat16><<<grid, kNormThreads, 0, s>>>(P);
+    if (x_type == TTL_T_F32) {
+      if (sp.B == 16) norm_fwd_any_kernel<float, 16><<<grid, kNormThreads, 0, s>>>(P);
+      else norm_fwd_any_kernel<float, 4><<<grid, kNormThreads, 0, s>>>(P);
+    } else {
+      if (sp.B == 16) norm_fwd_any_kernel<__nv_bfloat16, 16><<<grid, kNormThreads, 0, s>>>(P);
+      else norm_fwd_any_kernel<__nv_bfloat16, 2><<<grid, kNormThreads, 0, s>>>(P);
+    }
   } else if (x_type == TTL_T_F32) {
     if (sp.B == 16) rc = pick_fwd<float, 16>(P, sp, s);
     else rc = pick_fwd<float, 4>(P, sp, s);
@@ -1333,8 +1451,12 @@ extern "C" int ttl_layer_norm_bwd(int t, int64_t rows, int64_t h, int x_type, in
       parts = static_cast<int>(ctas < cap ? ctas : cap);
     }
     if (sp.W == 0) {
-      if (x_type == TTL_T_F32) norm_bwd_any_kernel<float><<<parts, kNormThreads, 0, s>>>(P);
-      else norm_bwd_any_kernel<__nv_bfloat16><<<parts, kNormThreads, 0, s>>>(P);
+      // one CTA per SM where its sums take more than half of the shared memory, else two, or three without sums in it
+      const size_t sums = static_cast<size_t>(h) * 8;
+      const int cap = (sums > kAnySums ? 3 : (sums > kAnySums / 2 ? 1 : 2)) * (kNormParts / 3);
+      parts = static_cast<int>(P.total < cap ? P.total : cap);
+      if (x_type == TTL_T_F32) rc = sp.B == 16 ? bwd_any<float, 16>(P, parts, s) : bwd_any<float, 4>(P, parts, s);
+      else rc = sp.B == 16 ? bwd_any<__nv_bfloat16, 16>(P, parts, s) : bwd_any<__nv_bfloat16, 2>(P, parts, s);
     } else if (x_type == TTL_T_F32) {
       if (sp.B == 16) rc = pick_bwd<float, 16>(P, sp, parts, s);
       else rc = pick_bwd<float, 4>(P, sp, parts, s);

@@ -213,3 +213,12 @@ def test_side_stream_and_graph_replay():
     torch.cuda.synchronize()
     assert torch.equal(torch.cat(fwd["Y"]), torch.cat(f2["Y"])) and torch.equal(torch.cat(bwd["dX"]), torch.cat(b2["dX"]))
     assert torch.equal(bwd["dgamma"], b2["dgamma"])
+
+
+# Rows beyond the ring (its widths, or the shared memory that its stages take): more rows than CTAs, sums of the
+# weight gradients in shared memory and beyond it, whole words and single values.
+@pytest.mark.parametrize("t,rows,h,dt", [(1, 700, 16400, torch.bfloat16), (2, 200, 16403, torch.bfloat16),
+                                         (1, 400, 12288, torch.float32), (1, 330, 9401, torch.float32),
+                                         (1, 170, 27504, torch.bfloat16), (1, 500, 27600, torch.float32)])
+def test_rows_beyond_the_ring(t, rows, h, dt):
+    test_residual_no_beta_and_accumulation(t, rows, h, dt)
