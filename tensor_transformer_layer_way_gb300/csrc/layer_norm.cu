@@ -101,10 +101,10 @@ struct Cursor {
 };
 
 // ------------------------------------------------------------------ rows held in registers
-// Rows below 1 KiB: a row belongs to W warps; each thread holds NV words of B bytes of it (16 where every row
+// Short rows (spread_of has the bounds): a row belongs to one warp or two; each thread holds NV words of B bytes of it (16 where every row
 // starts on 16 bytes and holds whole words, else 4 or 2), so the row is read once and the weights stay in registers over
 // the persistent loop.  The next row's words are loaded before this one's sums.  A CTA of narrow rows has
-// several groups of W warps, each with rows of its own.  Measured, 65536 rows of 256 bf16: forward 28 us (2.4 TB/s),
+// several groups of warps, each with rows of its own.  Measured, 65536 rows of 256 bf16: forward 20 us (3.4 TB/s),
 // backward 39 us (2.6 TB/s); bound by a row's chain of loads, sums and stores.
 
 template <int B> struct Word;
@@ -154,14 +154,12 @@ __device__ __forceinline__ void group_sync(int group, int W) {
 }
 
 template <typename T, int B, int NV>
-__global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_kernel(const __grid_constant__ NormFwd P, int W, int G) {
+__global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_kernel(const __grid_constant__ NormFwd P, int G) {
   using Wd = typename Word<B>::type;
   constexpr int E = B / sizeof(T);
-  __shared__ float2 red[2][kMaxWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = warp / W, gw = warp % W;
+  const int group = threadIdx.x >> 5, v0 = threadIdx.x & 31;
   const int words = static_cast<int>(P.h / E);
-  const int v0 = gw * 32 + lane, vs = W * 32;     // this thread's words: v0 + u vs
+  constexpr int vs = 32;                           // this thread's words: v0 + u vs
   float ga[NV * E], be[NV * E];
 #pragma unroll
   for (int u = 0; u < NV; ++u)
@@ -190,7 +188,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_kernel(const __grid_c
   int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
   Cursor ahead(row, P.rows);
   if (row < P.total) fetch(ahead);
-  for (int it = 0; row < P.total; row += step, it ^= 1) {
+  for (; row < P.total; row += step) {
     const int i = ahead.i;
     const int64_t k = ahead.k;
     ahead.move(step, P.rows);
@@ -220,16 +218,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_kernel(const __grid_c
 #pragma unroll
     for (int e = 0; e < NV * E; ++e) sum += x[e];
     sum = warp_sum(sum);
-    // The warp's own mean and the squares about it; the warps are joined with the exact shift
-    // sum (s - mean)^2 = sum (s - mean_w)^2 + n_w (mean_w - mean)^2, so one exchange is enough.
-    int mine = 0;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int left = words - (gw * 32 + u * vs);
-      mine += left <= 0 ? 0 : (left < 32 ? left : 32);
-    }
-    const float nw = static_cast<float>(mine * E);
-    float mean = mine > 0 ? sum / nw : 0.0f;
+    const float mean = sum / static_cast<float>(P.h);   // divided, so that a row of one value has exactly that mean
     float sq = 0.0f;
 #pragma unroll
     for (int u = 0; u < NV; ++u)
@@ -241,27 +230,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_kernel(const __grid_c
         }
       }
     sq = warp_sum(sq);
-    if (W > 1) {
-      // two buffers in turn: a warp can be one row ahead of another's reads, never two
-      if (lane == 0) red[it][warp] = make_float2(sum, sq);
-      group_sync(group, W);
-      float tot = 0.0f;
-      for (int w = 0; w < W; ++w) tot += red[it][group * W + w].x;
-      mean = tot / static_cast<float>(P.h);   // divided, so that a row of one value has exactly that mean
-      sq = 0.0f;
-      for (int w = 0; w < W; ++w) {
-        const float2 o = red[it][group * W + w];
-        int cnt = 0;
-#pragma unroll
-        for (int u = 0; u < NV; ++u) {
-          const int left = words - (w * 32 + u * vs);
-          cnt += left <= 0 ? 0 : (left < 32 ? left : 32);
-        }
-        const float n = static_cast<float>(cnt * E);
-        const float d = cnt > 0 ? o.x / n - mean : 0.0f;
-        sq += fmaf(n * d, d, o.y);
-      }
-    }
     const float rstd = rsqrtf(fmaf(sq, inv_h, P.eps));
     Wd* y = reinterpret_cast<Wd*>(static_cast<T*>(P.y[i]) + k * P.h);
 #pragma unroll
@@ -272,7 +240,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_fwd_kernel(const __grid_c
         for (int e = 0; e < E; ++e) o[e] = fmaf((x[u * E + e] - mean) * rstd, ga[u * E + e], be[u * E + e]);
         __stcs(y + v0 + u * vs, pack<T, B>(o));
       }
-    if (gw == 0 && lane == 0) {
+    if (v0 == 0) {
       P.mean[i][k] = mean;
       P.rstd[i][k] = rstd;
     }
@@ -410,7 +378,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ rows through shared memory
-// Rows of 1 KiB and more: a ring of whole rows in shared memory, filled by bulk copies that run several rows ahead,
+// Longer rows: a ring of whole rows in shared memory, filled by bulk copies that run several rows ahead,
 // so the bytes in flight do not depend on how many registers the sums take.  A bulk copy moves whole 16-byte
 // pieces, so a row that does not start on one is copied with its neighbours' bytes (they belong to the same
 // slab; at the slab's own ends the copy is cut and the few elements outside it are stored beside it by hand), and
@@ -1161,7 +1129,9 @@ Spread spread_of(int64_t h, int elem, int B, bool bwd, int inputs) {
     s.NV = nv;
     s.W = static_cast<int>((words + nv * 32 - 1) / (nv * 32));
   };
-  if (h * elem >= 1024) {
+  // (32768 rows, forward: 800 bytes fp32 with a residual 20 us through the ring, 31 in registers; 602 bytes of single
+  // values 36 and 77; 512 bytes, 65536 rows, 30 and 21.  Backward: 800 bytes 29 and 26, 602 bytes 52 and 40)
+  if (h * elem > (bwd ? 1023 : 512)) {
     // 16 values a thread: fewer leave too little work between the row's exchanges, more hold the registers
     // that other rows need (8192 x 4096: fp32 forward 45 us with 16 values, 53 with eight).  The backward pass
     // holds five registers a value: eight where the words are fp32 or short (fp32 80 us with eight values, 83 with
@@ -1189,14 +1159,15 @@ Spread spread_of(int64_t h, int elem, int B, bool bwd, int inputs) {
     s.smem = n * stage + sums;
     return s;
   }
-  if (B == 16) {
-    fit(1, 1);
-    fit(2, 1);
-  } else {
-    fit(8, 1);
-    fit(8, 2);
+  fit(B == 16 ? 1 : (bwd ? 8 : 16 / B), 1);
+  if (bwd) {
+    if (B == 16) fit(2, 1);
+    else fit(8, 2);
   }
   if (s.W < 8) s.G = 8 / s.W;
+  // (65536 rows of 256 bf16: forward 28 us with two CTAs an SM, 21 with four, 24 with six; the backward pass has
+  // registers for two)
+  if (!bwd) s.ctas = 4;
   if (bwd && s.G > 1) s.smem = static_cast<size_t>(h) * 8;
   return s;
 }
@@ -1233,7 +1204,7 @@ int fwd_ring(const NormFwd& P, const Spread& sp, cudaStream_t s) {
 
 template <typename T, int B, int NV>
 int fwd_regs(const NormFwd& P, const Spread& sp, cudaStream_t s) {
-  norm_fwd_kernel<T, B, NV><<<fwd_grid(P, sp), sp.W * sp.G * 32, 0, s>>>(P, sp.W, sp.G);
+  norm_fwd_kernel<T, B, NV><<<fwd_grid(P, sp), sp.G * 32, 0, s>>>(P, sp.G);
   return TTL_OK;
 }
 
@@ -1268,8 +1239,7 @@ int pick_fwd(const NormFwd& P, const Spread& sp, cudaStream_t s) {
     if (sp.NV == 16 / E) return fwd_ring<T, B, 16 / E>(P, sp, s);
     return sp.NV == 24 / E ? fwd_ring<T, B, 24 / E>(P, sp, s) : fwd_ring<T, B, 32 / E>(P, sp, s);
   }
-  if constexpr (B == 16) return sp.NV == 1 ? fwd_regs<T, B, 1>(P, sp, s) : fwd_regs<T, B, 2>(P, sp, s);
-  else return fwd_regs<T, B, 8>(P, sp, s);
+  return fwd_regs<T, B, B == 16 ? 1 : 16 / B>(P, sp, s);   // (16 / B words of 32 lanes: 512 bytes)
 }
 
 template <typename T, int B>
