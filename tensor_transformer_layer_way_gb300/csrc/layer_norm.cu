@@ -1159,15 +1159,16 @@ Spread spread_of(int64_t h, int elem, int B, bool bwd, int inputs) {
     s.smem = n * stage + sums;
     return s;
   }
-  fit(B == 16 ? 1 : (bwd ? 8 : 16 / B), 1);
+  fit(B == 16 ? 1 : (bwd ? 4 : 16 / B), 1);
   if (bwd) {
-    if (B == 16) fit(2, 1);
-    else fit(8, 2);
+    fit(B == 16 ? 2 : 8, 1);
+    if (B < 16) fit(8, 2);
   }
   if (s.W < 8) s.G = 8 / s.W;
   // (65536 rows of 256 bf16: forward 28 us with two CTAs an SM, 21 with four, 24 with six; the backward pass has
-  // registers for two)
+  // registers for two, with four values a thread for three: 32768 rows of 77 fp32 26 and 23 us)
   if (!bwd) s.ctas = 4;
+  else if (s.NV * E <= 4) s.ctas = 3;
   if (bwd && s.G > 1) s.smem = static_cast<size_t>(h) * 8;
   return s;
 }
@@ -1253,7 +1254,7 @@ int pick_bwd(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
     return sp.NV == 24 / E ? bwd_ring<T, B, 24 / E>(P, sp, parts, s) : bwd_ring<T, B, 16 / E>(P, sp, parts, s);
   }
   if constexpr (B == 16) return sp.NV == 1 ? bwd_regs<T, B, 1>(P, sp, parts, s) : bwd_regs<T, B, 2>(P, sp, parts, s);
-  else return bwd_regs<T, B, 8>(P, sp, parts, s);
+  else return sp.NV == 4 ? bwd_regs<T, B, 4>(P, sp, parts, s) : bwd_regs<T, B, 8>(P, sp, parts, s);
 }
 
 // The widest word that every row is made of: 16 bytes, or 4, or the element.
