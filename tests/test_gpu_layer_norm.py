@@ -222,3 +222,12 @@ def test_side_stream_and_graph_replay():
                                          (1, 170, 27504, torch.bfloat16), (1, 500, 27600, torch.float32)])
 def test_rows_beyond_the_ring(t, rows, h, dt):
     test_residual_no_beta_and_accumulation(t, rows, h, dt)
+
+
+# Short rows: around the widths at which the words, the warps of a row and the ring change.
+@pytest.mark.parametrize("t,rows,h", [(3, 50, 77), (2, 41, 128), (2, 40, 150), (1, 90, 200), (1, 17, 255), (1, 9, 257),
+                                      (2, 333, 301), (1, 20, 384), (4, 15, 511), (1, 2500, 129)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_short_rows(t, rows, h, dt):
+    test_forward_and_backward(t, rows, h, dt, torch.float32)
+    test_residual_no_beta_and_accumulation(t, rows, h, dt)
