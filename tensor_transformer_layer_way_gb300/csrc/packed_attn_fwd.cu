@@ -22,8 +22,9 @@
 // warpgroup of its own for the results was slower: it leaves the softmax 176 registers, and a key tile of one
 // long document then takes 3200 cycles, with 208 it takes 2700.)
 //
-// What bounds it: shared memory, which S_x = Q_x K^T reads at 128 bytes a cycle for 2000 of the 2700 cycles a
-// pair of key tiles takes.  Measured: one document of 32768 tokens, 4 query heads and 1 KV head of 128: 680 us, 1618
+// What bounds it: the turn of a tile, 2700 cycles (clock stamps: softmax 1300, product and next scores 1100, the rest
+// hand-overs), which the other tile's turn fills up to the products' 2050; tensor memory has no columns left in
+// which the next scores could wait.  Measured: one document of 32768 tokens, 4 query heads and 1 KV head of 128: 680 us, 1618
 // TFLOP/s; 8192 tokens in 12 documents, 32 query and 8 KV heads over 8 shards: 96 us (101
 // with items dealt out beforehand).  With many short documents an
 // item costs about 10000 cycles beside its key tiles (masks, the wait for the last product, the result).
