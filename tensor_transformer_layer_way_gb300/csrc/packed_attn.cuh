@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "launch_after.cuh"
+#include "pack_docs.h"
 #include "ttl_device.cuh"
 #include "ttl_internal.h"
 
@@ -90,24 +91,7 @@ constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-struct DocRange {
-  int lo, hi;                  // the document's tokens [lo, hi); hi <= lo: the token is in none
-};
-
-// The document of token `tok`, by bisection.  Whatever cu holds, the answer stays inside [0, T): with
-// entries out of order it is some document cut to the pack, and the check kernel reports it.
-__device__ __forceinline__ DocRange doc_of(const int32_t* cu, int batch, int T, int tok) {
-  int l = 0, r = batch;        // cu[l] <= tok < cu[r] once both ends are checked
-  if (batch == 0 || tok < __ldg(cu) || tok >= __ldg(cu + batch)) return DocRange{0, 0};
-  while (r - l > 1) {
-    const int m = (l + r) >> 1;
-    if (__ldg(cu + m) <= tok) l = m; else r = m;
-  }
-  const int lo = __ldg(cu + l), hi = __ldg(cu + r);
-  return DocRange{lo < 0 ? 0 : lo, hi > T ? T : hi};
-}
-
-// The same for one token of a document (cu[0] <= tok < cu[batch]), by a whole warp: 32 bounds at a time.
+// doc_of for one token of a document (0 <= tok < T, cu[0] <= tok < cu[batch]), by a whole warp: 32 bounds at a time.
 __device__ __forceinline__ DocRange doc_of_warp(const int32_t* cu, int batch, int T, int tok) {
   const int lane = threadIdx.x & 31;
   int l = 0, r = batch;

@@ -360,3 +360,41 @@ def test_bad_document_bounds_with_many_items():
         assert ttl.device_status() == ttl.TTL_ERR_DEVICE
         ttl.packed_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], fwd, cu, n_q=n_q, n_kv=n_kv, d=d)
         assert ttl.device_status() == ttl.TTL_ERR_DEVICE
+
+
+@pytest.mark.parametrize("T,n_q,n_kv,d,cu", [(200, 2, 1, 64, [40, 5000]), (200, 4, 2, 128, [0, 100, 5000]), (129, 2, 2, 64, [3, 300]),
+                                             (3000, 16, 4, 64, [700, 1000, 50000]), (2500, 4, 1, 128, [5, 9000])])
+def test_documents_beyond_the_pack_leave_the_rows_behind_it_alone(T, n_q, n_kv, d, cu):
+    """cu_seqlens that end beyond T are reported, and nothing behind the T rows is read into a result or written."""
+    x = _inputs(1, T, n_q, n_kv, d, [T], T)
+    guard = 140
+    wide = {n: torch.full((T + guard, x[n][0].shape[1]), float("nan"), dtype=BF16, device="cuda") for n in ("Q", "K", "V", "dO")}
+    for n, m in wide.items():
+        m[:T] = x[n][0]
+    y = {n: [m[:T]] for n, m in wide.items()}
+    y["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    cut = cu[:-1] + [T]
+    y["ok"] = torch.tensor(cut, dtype=torch.int32, device="cuda")
+    kw = dict(n_q=n_q, n_kv=n_kv, d=d)
+    rows = {n: torch.full((T + guard, c), 7.0, dtype=BF16, device="cuda")
+            for n, c in (("O", n_q * d), ("dQ", n_q * d), ("dK", n_kv * d), ("dV", n_kv * d))}
+    lse = torch.full((n_q * T + guard,), 7.0, device="cuda")
+    out_f = ttl.packed_attn_fwd_buffers(1, T, n_q, n_kv, d, len(cu) - 1)
+    out_b = ttl.packed_attn_bwd_buffers(1, T, n_q, n_kv, d, len(cu) - 1)
+    out_f["O"], out_f["lse"] = [rows["O"][:T]], [lse[:n_q * T].view(n_q, T)]
+    for n in ("dQ", "dK", "dV"):
+        out_b[n] = [rows[n][:T]]
+    ttl.packed_attn_fwd(y["Q"], y["K"], y["V"], y["cu"], out=out_f, **kw)
+    assert ttl.device_status() == ttl.TTL_ERR_DEVICE
+    ttl.packed_attn_bwd(y["dO"], y["Q"], y["K"], y["V"], out_f, y["cu"], out=out_b, **kw)
+    assert ttl.device_status() == ttl.TTL_ERR_DEVICE
+    for n, m in rows.items():
+        assert (m[T:] == 7).all(), n
+    assert (lse[n_q * T:] == 7).all()
+    # the last document cut to the pack is what the kernels take such bounds for: the same bits
+    f2 = ttl.packed_attn_fwd(y["Q"], y["K"], y["V"], y["ok"], **kw)
+    b2 = ttl.packed_attn_bwd(y["dO"], y["Q"], y["K"], y["V"], f2, y["ok"], **kw)
+    assert ttl.device_status() == 0
+    assert torch.equal(f2["O"][0], out_f["O"][0]) and torch.equal(f2["lse"][0], out_f["lse"][0])
+    for n in ("dQ", "dK", "dV"):
+        assert torch.equal(b2[n][0], out_b[n][0]), n
