@@ -735,8 +735,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_ring_kernel(const __g
       if (W > 1) group_sync(group, W); else __syncwarp();
     }
     constexpr int N = NV * E;
-    // xhat = x rstd - mean rstd, g = dy gamma; 0 past the row's end, where gamma and dy are
-    const uint64_t rs2 = f2_pack(rs, rs), mr2 = f2_pack(-mean * rs, -mean * rs);
+    // xhat = (x - mean) rstd, the difference first: it is exact near the mean, where x rstd - round(mean rstd) leaves half
+    // a step of the product in every xhat of the row (a row of one value has xhat 0).  g = dy gamma, 0 past the row's end.
+    const uint64_t rs2 = f2_pack(rs, rs), nm2 = f2_pack(-mean, -mean);
     float n[KEEP ? N : 2], q[KEEP ? N : 2];
     // xhat and g of word u of this thread; E is 1 only where words are read in pairs
     constexpr int U = E == 1 ? 2 : 1;            // words taken together
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) norm_bwd_ring_kernel(const __g
 #pragma unroll
       for (int e = 0; e < U * E; e += 2) {
         const int c = u * E + e;
-        const uint64_t d2 = f2_pack(qq[e], qq[e + 1]), n2 = ffma2(f2_pack(nn[e], nn[e + 1]), rs2, mr2);
+        const uint64_t d2 = f2_pack(qq[e], qq[e + 1]), n2 = fmul2(fadd2(f2_pack(nn[e], nn[e + 1]), nm2), rs2);
         const uint64_t g2 = fmul2(d2, f2_pack(ga[c], ga[c + 1]));
         if (sums_too) {
           const float2 fg = f2_unpack(ffma2(d2, n2, f2_pack(dg[c], dg[c + 1])));

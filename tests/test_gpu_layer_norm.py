@@ -231,3 +231,49 @@ def test_rows_beyond_the_ring(t, rows, h, dt):
 def test_short_rows(t, rows, h, dt):
     test_forward_and_backward(t, rows, h, dt, torch.float32)
     test_residual_no_beta_and_accumulation(t, rows, h, dt)
+
+
+# Each way a row is taken: registers, the ring with 16-byte words and single values, with xhat kept and read again, and
+# beyond the ring.
+BWD_WIDTHS = [(h, dt) for h, dt in [(77, torch.float32), (256, torch.bfloat16), (256, torch.float32), (1000, torch.bfloat16),
+                                    (1001, torch.float32), (1001, torch.bfloat16), (4001, torch.bfloat16), (4096, torch.bfloat16),
+                                    (4096, torch.float32), (9001, torch.bfloat16), (12288, torch.bfloat16),
+                                    (12288, torch.float32), (20000, torch.bfloat16)]]
+
+
+@pytest.mark.parametrize("h,dt", BWD_WIDTHS)
+def test_gradient_of_constant_rows(h, dt):
+    """A row of one value has xhat = 0: it adds nothing to dgamma, and dx = rstd (g - mean(g))."""
+    d = _inputs(1, 5, h, dt, dt, seed=h)
+    d["X"] = [torch.full((5, h), 7.0, device="cuda", dtype=dt)]
+    fwd = ttl.layer_norm_fwd(d["X"], d["gamma"], d["beta"])
+    assert (fwd["mean"][0] == 7.0).all()
+    out = ttl.layer_norm_bwd(d["X"], d["dY"], d["gamma"], fwd)
+    assert torch.count_nonzero(out["dgamma"]) == 0
+    g = d["dY"][0].to(F8) * d["gamma"].to(F8)
+    rstd, c1 = fwd["rstd"][0].to(F8)[:, None], g.mean(1, keepdim=True)
+    dx = rstd * (g - c1)
+    off = rstd * (4 * U * g.abs() + _chain(h) * g.abs().mean(1, keepdim=True) + 4 * U * c1.abs()) + 4 * U * dx.abs()
+    assert ((out["dX"][0].to(F8) - dx).abs() <= off + HALF[dt] * (dx.abs() + off)).all()
+
+
+@pytest.mark.parametrize("h", sorted({h for h, dt in BWD_WIDTHS if dt == torch.float32} | {4099, 9401}))
+def test_gradient_with_a_large_mean(h):
+    """A mean 4096 times the spread.  x - mean is exact to u of itself and xhat to 3 u, so the sums are off by their
+    chains' u of the terms' magnitudes and by no multiple of |mean| rstd."""
+    rows = 9
+    d = _inputs(1, rows, h, torch.float32, torch.float32, seed=h)
+    x = (torch.randn(rows, h, generator=torch.Generator().manual_seed(h)) + 4096.0).cuda()
+    fwd = ttl.layer_norm_fwd([x], d["gamma"], d["beta"])
+    out = ttl.layer_norm_bwd([x], d["dY"], d["gamma"], fwd)
+    mean, rstd = fwd["mean"][0].to(F8)[:, None], fwd["rstd"][0].to(F8)[:, None]
+    n, dy = (x.to(F8) - mean) * rstd, d["dY"][0].to(F8)
+    g = dy * d["gamma"].to(F8)
+    c1, c2 = g.mean(1, keepdim=True), (g * n).mean(1, keepdim=True)
+    dx = rstd * (g - c1 - n * c2)
+    c, n_off = _chain(h), 4 * U * n.abs()
+    off = rstd * (4 * U * g.abs() + c * g.abs().mean(1, keepdim=True) + 4 * U * c1.abs() + n_off * c2.abs()
+                  + n.abs() * (c + 4 * U) * (g * n).abs().mean(1, keepdim=True)) + 4 * U * dx.abs()
+    assert ((out["dX"][0].to(F8) - dx).abs() <= off + U * (dx.abs() + off)).all()
+    mag = (dy * n).abs().sum(0)
+    assert ((out["dgamma"].to(F8) - (dy * n).sum(0)).abs() <= (rows + 8) * U * mag).all()
