@@ -61,10 +61,16 @@ int check_cu(const int32_t* cu, float scale, const char* name) {
 
 int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
 
+// Room to list the rows that are computed again: of every query head, or of dK and dV of every KV head.
+size_t redo_bytes(int64_t T, int heads) { return static_cast<size_t>(heads) * tiles_of(T) * 4 * sizeof(RedoEntry); }
+
+// Forward workspace: the query tiles by work and how many were taken, and the rows that are computed again.
+size_t fwd_list_bytes(int64_t T) { return round256(static_cast<size_t>(tiles_of(T) + 1) * 16); }
+
 // Backward workspace: D, the query tiles by work, the key items by work with their counts, the key tiles that
-// several items share, and those items' partial sums.
+// several items share, those items' partial sums, and the rows that are computed again.
 struct BwdWs {
-  size_t q_list, kv_list, head, join, part, total;   // offsets after D
+  size_t q_list, kv_list, head, join, part, redo, total;   // offsets after D
 };
 BwdWs bwd_ws(int64_t T, int n_q, int n_kv, int d) {
   const int64_t tiles = tiles_of(T);
@@ -83,7 +89,8 @@ BwdWs bwd_ws(int64_t T, int n_q, int n_kv, int d) {
   w.head = w.kv_list + round256(static_cast<size_t>(tiles + slots) * 32);
   w.join = w.head + 256;
   w.part = w.join + round256(static_cast<size_t>(tiles) * 16);
-  w.total = w.part + static_cast<size_t>(slots) * n_kv * 2 * kTile * d * 4 + 256;   // (it starts on 256 bytes)
+  w.redo = w.part + static_cast<size_t>(slots) * n_kv * 2 * kTile * d * 4;
+  w.total = w.redo + redo_bytes(T, n_q > 2 * n_kv ? n_q : 2 * n_kv) + 256;   // (it starts on 256 bytes)
   return w;
 }
 
@@ -97,7 +104,7 @@ using namespace ttl;
 
 extern "C" size_t ttl_packed_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
   if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_fwd_workspace_size")) return 0;
-  return round256(static_cast<size_t>(tiles_of(T) + 1) * 16);   // the query tiles by work, and how many were taken
+  return fwd_list_bytes(T) + redo_bytes(T, n_q);
 }
 
 extern "C" size_t ttl_packed_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
@@ -139,6 +146,7 @@ extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, i
   A.t = t; A.nql = n_q / t; A.nkvl = n_kv / t; A.grp = n_q / n_kv; A.T = T;
   A.ldq = ldq; A.ldk = ldk; A.ldv = ldv; A.ldo = ldo;
   A.cu = cu_seqlens; A.batch = batch; A.scale = scale;
+  A.redo = reinterpret_cast<RedoEntry*>(static_cast<char*>(ws) + fwd_list_bytes(T));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return pack_attn_fwd_launch(A, d, ws, s);
 }
@@ -196,9 +204,10 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
   const bool split = pack_split(tiles, n_kv, A.grp);
   const bool listed = split || tiles * n_q > num_sms();
   PackPlan plan = {};
+  const BwdWs w = bwd_ws(T, n_q, n_kv, d);
+  char* base = reinterpret_cast<char*>(A.D);
+  A.redo = reinterpret_cast<RedoEntry*>(base + w.redo);
   if (listed) {
-    const BwdWs w = bwd_ws(T, n_q, n_kv, d);
-    char* base = reinterpret_cast<char*>(A.D);
     plan.q_list = reinterpret_cast<int4*>(base + w.q_list);
     plan.q_units = plan.tiles = static_cast<int>(tiles);
     plan.q_per = 1;

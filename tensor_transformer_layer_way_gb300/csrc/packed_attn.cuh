@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cmath>
+#include <type_traits>
 
 #include "launch_after.cuh"
 #include "pack_docs.h"
@@ -42,6 +43,7 @@ struct PackArgs {
   int* kv_taken;
   const int4* join_list;       // {key tile, first slot, parts, 0} of the key tiles that several items share
   float* part;                 // partial dK and dV: [slot * KV heads + head][2][128][d]
+  struct RedoEntry* redo;      // room for the rows that are computed again
 };
 
 // A query unit: {unit, first key tile of its first token tile, of its second, 0}, -1 for a token tile without
@@ -81,7 +83,8 @@ enum PackKernelSlot { kPackFwd128, kPackFwd64, kPackDq128, kPackDq64, kPackDkv12
 int set_core_smem_once(const void* fn, int slot, int bytes, const char* what);
 
 // Launches of the tensor-core kernels (arguments are checked; A.s holds every pointer they need).
-// `list`: room for one word of 16 bytes per 128 tokens and one more.
+// `list`: room for one word of 16 bytes per 128 tokens and one more; A.redo: for 4 words of 8 bytes per 128 tokens and
+// query head (backward: and twice as many per KV head, if that is more).
 int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stream);
 int pack_attn_dq_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStream_t stream);    // dQ, after D
 int pack_attn_dkv_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStream_t stream);   // dK and dV, after D
@@ -235,27 +238,63 @@ __device__ __forceinline__ void store_bf16x32(__nv_bfloat16* out, const uint32_t
   }
 }
 
-// ------------------------------------------------------------------ one row by one warp
-// Lane l holds columns [l D/32, (l + 1) D/32) of the head.  Every key or query of the range is read, and
-// nothing outside it, so what masked places hold (infinities, NaN) never enters.
+// ------------------------------------------------------------------ rows that are computed again
+// A masked place enters a product as 0, and 0 times an infinite or NaN value is NaN, so a row whose result is not
+// finite may owe that to places that it does not see.  A block lists such rows while it runs and computes them again
+// when its items are done, from what they see alone: nothing waits for that, however long it takes.  It is only
+// done where a masked place of the row's first or last tile (no other tile has places that it does not see) holds such
+// a value: a row that is not finite by what it sees keeps the product's result.
+// Measured, 8192 tokens in 12 documents, 32 and 8 heads of 128 over 8 shards (131 us forward, 328 us backward): NaN inside the
+// longest document 1.0 and 2.0 to 3.6 ms, NaN in all rows behind the documents 0.5 and 14 ms; row by row at the
+// end of the item they took 23, 72 to 100, 4.2 and 80 ms.
+
+// Rows [32 slot', 32 slot' + 32) of one head: which of them, and the block's next listed slot.
+struct RedoEntry {
+  uint32_t rows, next;
+};
+constexpr uint32_t kRedoNone = 0xffffffffu;
+// Slot of rows [q0 + 32 quad, + 32) of head `head` (over all shards; dK and dV: of two heads per KV head).
+__device__ __forceinline__ uint32_t redo_slot(int head, int64_t T, int q0, int quad) {
+  return (static_cast<uint32_t>(head) * static_cast<uint32_t>((T + kTile - 1) / kTile) + static_cast<uint32_t>(q0 / kTile)) * 4u +
+         static_cast<uint32_t>(quad);
+}
+struct RedoPlace {
+  int head, row0;
+};
+__device__ __forceinline__ RedoPlace redo_place(uint32_t slot, int64_t T) {
+  const uint32_t groups = static_cast<uint32_t>((T + kTile - 1) / kTile) * 4u;
+  return RedoPlace{static_cast<int>(slot / groups), static_cast<int>(slot % groups) * 32};
+}
+// By one lane.
+__device__ __forceinline__ void redo_later(RedoEntry* list, uint32_t* head, uint32_t slot, uint32_t rows) {
+  list[slot] = RedoEntry{rows, atomicExch(head, slot)};
+}
+// Up to R of the rows in `mask`, taken out of it, as numbers from row0; the last one again where there are fewer.
+template <int R>
+__device__ __forceinline__ int redo_take(uint32_t& mask, int row0, int (&i)[R]) {
+  int n = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (mask) {
+      i[r] = row0 + __ffs(mask) - 1;
+      mask &= mask - 1;
+      ++n;
+    } else {
+      i[r] = i[r > 0 ? r - 1 : 0];
+    }
+  }
+  return n;
+}
+
+// The work of one warp: kRedoRows rows together, 32 keys (or queries) at a time.  A lane takes the scores of one of
+// them, and lane l sums columns [l D/32, (l + 1) D/32) of the results.  The rows' ranges differ by a few places (or a
+// document); what a row does not see is left out of its sums, not multiplied by 0.
+constexpr int kRedoRows = 4;
 
 template <int D>
 struct RowVec {
   float x[D / 32];
 };
-
-template <int D>
-__device__ __forceinline__ RowVec<D> row_load(const __nv_bfloat16* p, int lane) {
-  RowVec<D> r;
-  if constexpr (D == 128) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p + lane * 4);
-    r.x[0] = bf16_lo(w.x); r.x[1] = bf16_hi(w.x); r.x[2] = bf16_lo(w.y); r.x[3] = bf16_hi(w.y);
-  } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p + lane * 2);
-    r.x[0] = bf16_lo(w); r.x[1] = bf16_hi(w);
-  }
-  return r;
-}
 
 template <int D>
 __device__ __forceinline__ void row_store(__nv_bfloat16* p, const RowVec<D>& r, int lane) {
@@ -266,16 +305,6 @@ __device__ __forceinline__ void row_store(__nv_bfloat16* p, const RowVec<D>& r, 
 }
 
 template <int D>
-__device__ __forceinline__ float row_dot(const RowVec<D>& a, const RowVec<D>& b) {
-  float s = 0.0f;
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j) s = fmaf(a.x[j], b.x[j], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-template <int D>
 __device__ __forceinline__ RowVec<D> row_zero() {
   RowVec<D> r;
 #pragma unroll
@@ -283,78 +312,282 @@ __device__ __forceinline__ RowVec<D> row_zero() {
   return r;
 }
 
-// o_i and lse_i of query head c at token i: running maximum m and sum l, both in base 2.
-template <int D>
-__device__ __forceinline__ void fwd_row(const PackArgs& A, const PackShard& S, int c, int i, DocRange doc, int lane) {
-  const int g = c / A.grp;
-  RowVec<D> acc = row_zero<D>();
-  float lse = -INFINITY;
-  if (doc.hi > doc.lo) {
-    const RowVec<D> q = row_load<D>(S.q + i * A.ldq + c * D, lane);
-    const float k2 = A.scale * kLog2e;
-    float m = -INFINITY, l = 0.0f;
-    for (int j = doc.lo; j <= i; ++j) {
-      const float s = row_dot(q, row_load<D>(S.k + j * A.ldk + g * D, lane)) * k2;
-      const RowVec<D> v = row_load<D>(S.v + j * A.ldv + g * D, lane);
-      const float mn = fmaxf(m, s);
-      const float f = m == -INFINITY ? 0.0f : exp2f(m - mn), p = exp2f(s - mn);
-      l = l * f + p;
+// s[r] = a[r] . b by one lane, rows of D values (a is the same in all lanes).  (Eight lanes to a row, whose loads take whole
+// lines, were no faster: the instructions of the products bound it.)
+template <int D, int R>
+__device__ __forceinline__ void lane_dots(float (&s)[R], const __nv_bfloat16* const (&a)[R], const __nv_bfloat16* b) {
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc.x[e] = fmaf(acc.x[e], f, p * v.x[e]);
-      m = mn;
-    }
-    const float inv = 1.0f / l;
+  for (int r = 0; r < R; ++r) s[r] = 0.0f;
+#pragma unroll 2
+  for (int u = 0; u < D; u += 8) {
+    const uint4 y = __ldg(reinterpret_cast<const uint4*>(b + u));
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc.x[e] *= inv;
-    lse = (m + log2f(l)) * kLn2;
-  }
-  row_store<D>(S.o + i * A.ldo + c * D, acc, lane);
-  if (lane == 0) S.lse[static_cast<int64_t>(c) * A.T + i] = lse;
-}
-
-// dq_i of query head c.
-template <int D>
-__device__ __forceinline__ void dq_row(const PackArgs& A, const PackShard& S, int shard, int c, int i, DocRange doc,
-                                       int lane) {
-  const int g = c / A.grp;
-  RowVec<D> acc = row_zero<D>();
-  if (doc.hi > doc.lo) {
-    const RowVec<D> q = row_load<D>(S.q + i * A.ldq + c * D, lane);
-    const RowVec<D> go = row_load<D>(S.dO + i * A.lddo + c * D, lane);
-    const float Di = A.D[(static_cast<int64_t>(shard) * A.nql + c) * A.T + i];
-    const float k2 = A.scale * kLog2e, lse2 = S.lse[static_cast<int64_t>(c) * A.T + i] * kLog2e;
-    for (int j = doc.lo; j <= i; ++j) {
-      const RowVec<D> k = row_load<D>(S.k + j * A.ldk + g * D, lane);
-      const float p = exp2f(row_dot(q, k) * k2 - lse2);
-      const float dp = row_dot(go, row_load<D>(S.v + j * A.ldv + g * D, lane));
-      const float ds = p * (dp - Di) * A.scale;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc.x[e] = fmaf(ds, k.x[e], acc.x[e]);
+    for (int r = 0; r < R; ++r) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(a[r] + u));
+      s[r] = fmaf(bf16_lo(x.x), bf16_lo(y.x), s[r]);
+      s[r] = fmaf(bf16_hi(x.x), bf16_hi(y.x), s[r]);
+      s[r] = fmaf(bf16_lo(x.y), bf16_lo(y.y), s[r]);
+      s[r] = fmaf(bf16_hi(x.y), bf16_hi(y.y), s[r]);
+      s[r] = fmaf(bf16_lo(x.z), bf16_lo(y.z), s[r]);
+      s[r] = fmaf(bf16_hi(x.z), bf16_hi(y.z), s[r]);
+      s[r] = fmaf(bf16_lo(x.w), bf16_lo(y.w), s[r]);
+      s[r] = fmaf(bf16_hi(x.w), bf16_hi(y.w), s[r]);
     }
   }
-  row_store<D>(S.dq + i * A.lddq + c * D, acc, lane);
 }
 
-// dk_j (want_k) or dv_j of KV head g, summed over the group's query heads.
-template <int D>
-__device__ __forceinline__ void dkv_row(const PackArgs& A, const PackShard& S, int shard, int g, int j, DocRange doc,
-                                        bool want_k, int lane) {
-  RowVec<D> acc = row_zero<D>();
-  if (doc.hi > doc.lo) {
-    const RowVec<D> k = row_load<D>(S.k + j * A.ldk + g * D, lane);
-    const RowVec<D> v = row_load<D>(S.v + j * A.ldv + g * D, lane);
-    const float k2 = A.scale * kLog2e;
-    for (int c = g * A.grp; c < (g + 1) * A.grp; ++c)
-      for (int i = j; i < doc.hi; ++i) {
-        const RowVec<D> q = row_load<D>(S.q + i * A.ldq + c * D, lane);
-        const RowVec<D> go = row_load<D>(S.dO + i * A.lddo + c * D, lane);
-        const float p = exp2f(row_dot(q, k) * k2 - S.lse[static_cast<int64_t>(c) * A.T + i] * kLog2e);
-        const float ds = p * (row_dot(go, v) - A.D[(static_cast<int64_t>(shard) * A.nql + c) * A.T + i]) * A.scale;
+// acc[r] += w[r] of place e times row e of m (row stride ld) for e in [from[r], to[r]); e < n <= 32, lane e holds place
+// e's weights.
+template <int D, int R>
+__device__ __forceinline__ void add_rows(RowVec<D> (&acc)[R], const float (&w)[R], const int (&from)[R], const int (&to)[R],
+                                         const __nv_bfloat16* m, int64_t ld, int n, int lane) {
+  constexpr int kBatch = 4;     // rows loaded ahead of their products
+  using Words = typename std::conditional<D == 128, uint2, uint32_t>::type;
+  const __nv_bfloat16* at = m + lane * (D / 32);
+#pragma unroll 1
+  for (int e0 = 0; e0 < n; e0 += kBatch) {
+    Words v[kBatch];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc.x[e] = want_k ? fmaf(ds, q.x[e], acc.x[e]) : fmaf(p, go.x[e], acc.x[e]);
+    for (int u = 0; u < kBatch; ++u) v[u] = __ldg(reinterpret_cast<const Words*>(at + (e0 + u < n ? e0 + u : n - 1) * ld));
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int e = e0 + u;
+      float f[D / 32];
+      if constexpr (D == 128) {
+        f[0] = bf16_lo(v[u].x); f[1] = bf16_hi(v[u].x); f[2] = bf16_lo(v[u].y); f[3] = bf16_hi(v[u].y);
+      } else {
+        f[0] = bf16_lo(v[u]); f[1] = bf16_hi(v[u]);
       }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float we = __shfl_sync(0xffffffffu, w[r], e & 31);
+        if (e >= from[r] && e < to[r]) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) acc[r].x[c] = fmaf(we, f[c], acc[r].x[c]);
+        }
+      }
+    }
   }
-  row_store<D>((want_k ? S.dk + j * A.lddk : S.dv + j * A.lddv) + g * D, acc, lane);
 }
+
+// o and lse of query head c at tokens i[0..n), whose documents begin at lo: running maximum m and sum l, in base 2.
+template <int D, int R>
+__device__ __forceinline__ void fwd_rows(const PackArgs& A, const PackShard& S, int c, const int (&i)[R], const int (&lo)[R],
+                                         int n, int lane) {
+  const int g = c / A.grp;
+  const float k2 = A.scale * kLog2e;
+  RowVec<D> acc[R];
+  float m[R], l[R];                                // (l: this lane's part)
+  const __nv_bfloat16* q[R];
+  int begin = lo[0], last = i[0];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    acc[r] = row_zero<D>();
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+    q[r] = S.q + i[r] * A.ldq + c * D;
+    begin = min(begin, lo[r]);
+    last = max(last, i[r]);
+  }
+#pragma unroll 1
+  for (int j0 = begin; j0 <= last; j0 += 32) {
+    const int j = j0 + lane;
+    float s[R];
+    int from[R], to[R];
+    lane_dots<D, R>(s, q, S.k + min(j, last) * A.ldk + g * D);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[r] = j >= lo[r] && j <= i[r] ? s[r] * k2 : -INFINITY;
+      float mn = fmaxf(m[r], s[r]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      const float base = mn == -INFINITY ? 0.0f : mn;
+      const float f = exp2f(m[r] - base);
+      s[r] = exp2f(s[r] - base);
+      l[r] = l[r] * f + s[r];
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[r].x[e] *= f;
+      m[r] = mn;
+      from[r] = lo[r] - j0;
+      to[r] = i[r] + 1 - j0;
+    }
+    add_rows<D, R>(acc, s, from, to, S.v + j0 * A.ldv + g * D, A.ldv, min(32, last + 1 - j0), lane);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+    const float inv = 1.0f / l[r];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[r].x[e] *= inv;
+    if (r < n) {
+      row_store<D>(S.o + i[r] * A.ldo + c * D, acc[r], lane);
+      if (lane == 0) S.lse[static_cast<int64_t>(c) * A.T + i[r]] = (m[r] + log2f(l[r])) * kLn2;
+    }
+  }
+}
+
+// dq of query head c at tokens i[0..n).
+template <int D, int R>
+__device__ __forceinline__ void dq_rows(const PackArgs& A, const PackShard& S, int shard, int c, const int (&i)[R],
+                                        const int (&lo)[R], int n, int lane) {
+  const int g = c / A.grp;
+  const float k2 = A.scale * kLog2e;
+  RowVec<D> acc[R];
+  float lse2[R], Di[R];
+  const __nv_bfloat16* q[R];
+  const __nv_bfloat16* go[R];
+  int begin = lo[0], last = i[0];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    acc[r] = row_zero<D>();
+    q[r] = S.q + i[r] * A.ldq + c * D;
+    go[r] = S.dO + i[r] * A.lddo + c * D;
+    lse2[r] = S.lse[static_cast<int64_t>(c) * A.T + i[r]] * kLog2e;
+    Di[r] = A.D[(static_cast<int64_t>(shard) * A.nql + c) * A.T + i[r]];
+    begin = min(begin, lo[r]);
+    last = max(last, i[r]);
+  }
+#pragma unroll 1
+  for (int j0 = begin; j0 <= last; j0 += 32) {
+    const int at = min(j0 + lane, last);
+    float s[R], dp[R];
+    int from[R], to[R];
+    lane_dots<D, R>(s, q, S.k + at * A.ldk + g * D);
+    lane_dots<D, R>(dp, go, S.v + at * A.ldv + g * D);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[r] = exp2f(s[r] * k2 - lse2[r]) * (dp[r] - Di[r]) * A.scale;
+      from[r] = lo[r] - j0;
+      to[r] = i[r] + 1 - j0;
+    }
+    add_rows<D, R>(acc, s, from, to, S.k + j0 * A.ldk + g * D, A.ldk, min(32, last + 1 - j0), lane);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < n) row_store<D>(S.dq + i[r] * A.lddq + c * D, acc[r], lane);
+}
+
+// dk (want_k) or dv of KV head g at tokens j[0..n), whose documents end at hi, summed over the group's query heads.
+template <int D, int R>
+__device__ __forceinline__ void dkv_rows(const PackArgs& A, const PackShard& S, int shard, int g, const int (&j)[R],
+                                         const int (&hi)[R], int n, bool want_k, int lane) {
+  const float k2 = A.scale * kLog2e;
+  RowVec<D> acc[R];
+  const __nv_bfloat16* k[R];
+  const __nv_bfloat16* v[R];
+  int begin = j[0], end = hi[0];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    acc[r] = row_zero<D>();
+    k[r] = S.k + j[r] * A.ldk + g * D;
+    v[r] = S.v + j[r] * A.ldv + g * D;
+    begin = min(begin, j[r]);
+    end = max(end, hi[r]);
+  }
+  for (int c = g * A.grp; c < (g + 1) * A.grp; ++c) {
+    const float* lse = S.lse + static_cast<int64_t>(c) * A.T;
+    const float* Dr = A.D + (static_cast<int64_t>(shard) * A.nql + c) * A.T;
+#pragma unroll 1
+    for (int i0 = begin; i0 < end; i0 += 32) {
+      const int at = min(i0 + lane, end - 1);
+      float w[R];
+      int from[R], to[R];
+      lane_dots<D, R>(w, k, S.q + at * A.ldq + c * D);
+      const float lse2 = lse[at] * kLog2e;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        w[r] = exp2f(w[r] * k2 - lse2);
+        from[r] = j[r] - i0;
+        to[r] = hi[r] - i0;
+      }
+      if (want_k) {
+        float dp[R];
+        lane_dots<D, R>(dp, v, S.dO + at * A.lddo + c * D);
+#pragma unroll
+        for (int r = 0; r < R; ++r) w[r] *= (dp[r] - Dr[at]) * A.scale;
+      }
+      const __nv_bfloat16* m = want_k ? S.q + i0 * A.ldq + c * D : S.dO + i0 * A.lddo + c * D;
+      add_rows<D, R>(acc, w, from, to, m, want_k ? A.ldq : A.lddo, min(32, end - i0), lane);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < n) row_store<D>((want_k ? S.dk + j[r] * A.lddk : S.dv + j[r] * A.lddv) + g * D, acc[r], lane);
+}
+
+// ---- what the products of a tile's rows met beside what the rows see
+
+// Bit r: row k0 + r (below T) of some heads' columns holds a value that is not finite.
+struct BadRows {
+  uint32_t w[4];
+  // any row of [a, b), numbered from the tile's first
+  __device__ __forceinline__ bool any(int a, int b) const {
+    uint32_t hit = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) hit |= w[u] & bits_between(a - u * 32, b - 1 - u * 32);
+    return hit != 0;
+  }
+};
+template <int D>
+__device__ __forceinline__ void add_bad_rows(BadRows& b, const __nv_bfloat16* m, int64_t ld, int col, int k0, int64_t T, int lane) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = k0 + u * 32 + lane;
+    bool bad = false;
+    if (i < T) {
+      const uint4* p = reinterpret_cast<const uint4*>(m + i * ld + col);
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = __ldg(p + c);
+        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)     // an exponent of ones
+          bad |= (q[e] & 0x7f800000u) == 0x7f800000u || (q[e] & 0x7f80u) == 0x7f80u;
+      }
+    }
+    b.w[u] |= __ballot_sync(0xffffffffu, bad);
+  }
+}
+constexpr int kRedoShort = 2 * kTile;   // rows of fewer places are computed again without that look
+
+// For query rows: m is what the product sums over the keys (V or K).  Keys before row i's document in the first tile,
+// keys behind it in its own.  (A row of kRedoShort keys or more belongs to the document of its tile's first row.)
+struct QueryEdges {
+  BadRows first, own;
+  int first0, own0;
+  template <int D>
+  __device__ __forceinline__ void look(const __nv_bfloat16* m, int64_t ld, int col, int lo, int row0, int64_t T, int lane) {
+    first = own = BadRows{{0, 0, 0, 0}};
+    first0 = lo / kTile * kTile;
+    own0 = row0 / kTile * kTile;
+    add_bad_rows<D>(first, m, ld, col, first0, T, lane);
+    add_bad_rows<D>(own, m, ld, col, own0, T, lane);
+  }
+  __device__ __forceinline__ bool met(int lo, int i) const {
+    return first.any(0, lo - first0) || own.any(i + 1 - own0, kTile);
+  }
+};
+// For key rows: m is what the product sums over the queries (Q or dO), of the group's heads.  Queries before row j in its
+// own tile, queries behind its document in the last one.  (Of kRedoShort queries or more: the tile's last document.)
+struct KeyEdges {
+  BadRows own, last;
+  int own0, last0;
+  template <int D>
+  __device__ __forceinline__ void look(const PackArgs& A, const PackShard& S, int g, int row0, int hi, bool want_k, int lane) {
+    const __nv_bfloat16* m = want_k ? S.q : S.dO;
+    const int64_t ld = want_k ? A.ldq : A.lddo;
+    own = last = BadRows{{0, 0, 0, 0}};
+    own0 = row0 / kTile * kTile;
+    last0 = (hi - 1) / kTile * kTile;
+    for (int c = g * A.grp; c < (g + 1) * A.grp; ++c) {
+      add_bad_rows<D>(own, m, ld, c * D, own0, A.T, lane);
+      add_bad_rows<D>(last, m, ld, c * D, last0, A.T, lane);
+    }
+  }
+  __device__ __forceinline__ bool met(int j, int hi) const {
+    return own.any(0, j - own0) || last.any(hi - last0, kTile);
+  }
+};
 
 }  // namespace ttl

@@ -57,7 +57,7 @@ struct KvCfg {
   static constexpr int OFF_STAT = OFF_RING + kRing * TILE;   // float [kStat][2][128]: -lse log2(e), -D
   static constexpr int OFF_ROWS = OFF_STAT + kStat * 1024;  // int [128]: the last query that sees a key
   static constexpr int OFF_BAR = OFF_ROWS + 512;
-  static constexpr int SMEM = OFF_BAR + 320 + kAhead * static_cast<int>(sizeof(KvItem));   // (the block begins on 1024 bytes; the kernel checks it)
+  static constexpr int SMEM = OFF_BAR + 336 + kAhead * static_cast<int>(sizeof(KvItem));   // (the block begins on 1024 bytes; the kernel checks it)
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
 };
 
@@ -92,12 +92,49 @@ __device__ __forceinline__ KvItem first_item(const KvParams& P, int total) {
   return it;
 }
 
+// Those of the rows j of dK (want_k) or dV, whose sums are not finite, that masked places may have made so, again.
+// `edges` are looked at once for the rows of a tile.
+template <int D, int R>
+__device__ __noinline__ void redo_keys(const PackArgs& A, int shard, int g, int (&j)[R], bool want_k, KeyEdges& edges,
+                                          bool& looked, int lane) {
+  const PackShard& S = A.s[shard];
+  const int T = static_cast<int>(A.T), row0 = j[0] & ~31;
+  uint32_t again = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int hi = doc_of(A.cu, A.batch, T, j[r]).hi;
+    bool met = hi - j[r] < kRedoShort;
+    if (!met) {
+      if (!looked) edges.look<D>(A, S, g, row0, hi, want_k, lane);
+      looked = true;
+      met = edges.met(j[r], hi);
+    }
+    if (met) again |= 1u << (j[r] - row0);
+  }
+  if (again == 0) return;
+  const int m = redo_take(again, row0, j);
+  int hi[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) hi[r] = doc_of(A.cu, A.batch, T, j[r]).hi;
+  dkv_rows<D>(A, S, shard, g, j, hi, m, want_k, lane);
+}
+
+// The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
 template <int D>
-__device__ __noinline__ void redo_dkv(const PackArgs& A, int shard, int g, int k0, unsigned rows, bool want_k, int lane) {
-  while (rows) {
-    const int j = k0 + __ffs(rows) - 1;
-    rows &= rows - 1;
-    dkv_row<D>(A, A.s[shard], shard, g, j, doc_of(A.cu, A.batch, static_cast<int>(A.T), j), want_k, lane);
+__device__ __noinline__ void redo_rows(const PackArgs& A, uint32_t slot, int w, int warps, int lane) {
+  int turn = 0;
+  while (slot != kRedoNone) {
+    const RedoEntry e = A.redo[slot];
+    const RedoPlace at = redo_place(slot, A.T);
+    const int kv = at.head >> 1;
+    KeyEdges edges;
+    bool looked = false;
+    for (uint32_t rows = e.rows; rows;) {
+      int j[kRedoRows];
+      redo_take(rows, at.row0, j);
+      if (turn++ % warps == w) redo_keys<D>(A, kv / A.nkvl, kv % A.nkvl, j, (at.head & 1) == 0, edges, looked, lane);
+    }
+    slot = e.next;
   }
 }
 
@@ -132,7 +169,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bars + kQueueBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* flags = tmem_slot + 2;     // [2][4]: rows of a quadrant to be done again, of dK and of dV
-  static_assert((4 + 2 * kRing + 2 * kStat + 9 + kQueueBars) * 8 + 40 <= 320, "barrier area");
+  uint32_t* redo_head = flags + 8;     // the last listed slot
+  static_assert((4 + 2 * kRing + 2 * kStat + 9 + kQueueBars) * 8 + 44 <= 336, "barrier area");
   constexpr uint32_t T_DP = 128, T_DK = 256, T_DV = 384;
 
   const PackArgs& A = P.a;
@@ -146,7 +184,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   const int total = (A.kv_list ? __ldg(A.kv_head) : P.tiles) * P.lanes;
   int* status = A.status;
   const uint64_t tmo = P.timeout_ns;
-  const ItemQueue<KvItem> queue{reinterpret_cast<KvItem*>(smem + C::OFF_BAR + 320), item_bars, abort_flag, status, tmo};
+  const ItemQueue<KvItem> queue{reinterpret_cast<KvItem*>(smem + C::OFF_BAR + 336), item_bars, abort_flag, status, tmo};
   // The item's n-th step: the last query tile first, the group's heads in turn.
   auto step_q0 = [&](const KvItem& it, int n) { return (it.qt_last - (it.t0 + n) / A.grp) * kTile; };
   auto step_head = [&](const KvItem& it, int n) { return it.g * A.grp + (it.t0 + n) % A.grp; };
@@ -174,6 +212,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     mbar_init(x_bar, kKvWarps);
     mbar_init(done_bar, 1);
     for (int q = 0; q < 8; ++q) flags[q] = 0;
+    *redo_head = kRedoNone;
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -532,8 +571,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         }
       }
       tc_fence_before_sync();
-      // A row is redone, by one of its two warpgroups, if either found its columns not finite, after both have
-      // stored.  (All sixteen warps meet, with a bounded wait, unlike a hardware barrier.)
+      // A row is listed, by one of its two warpgroups, if either found its columns not finite.  (All sixteen warps
+      // meet, with a bounded wait, unlike a hardware barrier.)
       const unsigned mine = __ballot_sync(0xffffffffu, in && bad != 0.0f && it.slot < 0);
       if (mine && lane == 0) atomicOr(&flags[kind * 4 + quad], mine);
       __syncwarp();
@@ -544,9 +583,9 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       if ((w & 1) == 0) {
         const unsigned again = flags[kind * 4 + quad];
         __syncwarp();
-        if (again) {
-          if (lane == 0) flags[kind * 4 + quad] = 0;
-          redo_dkv<D>(A, it.shard, it.g, it.k0 + quad * 32, again, kind == 0, lane);
+        if (again && lane == 0) {
+          flags[kind * 4 + quad] = 0;
+          redo_later(A.redo, redo_head, redo_slot((it.shard * A.nkvl + it.g) * 2 + kind, A.T, it.k0, quad), again);
         }
       }
     }
@@ -557,42 +596,57 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (warp >= 4 && *redo_head != kRedoNone && !*abort_flag) redo_rows<D>(A, *redo_head, warp - 4, kKvWarps, lane);
 }
 
 // Adds up the parts of the key tiles that several items shared, in the order of their steps: one warp per row
-// of dK or dV.
+// of dK or dV, eight rows of a tile per block.
 template <int D>
-__global__ void __launch_bounds__(256) pack_join_kernel(const __grid_constant__ PackArgs A) {
+__global__ void __launch_bounds__(256, 4) pack_join_kernel(const __grid_constant__ PackArgs A) {
+  __shared__ uint32_t redo[2];       // rows of the eight whose sums are not finite; of the eight before, spent
   await_previous();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = A.t * A.nkvl;
   const int64_t rows = static_cast<int64_t>(__ldg(A.kv_head + 1)) * lanes * 2 * kTile;
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); w < rows; w += gridDim.x * 8) {
-    const int r = static_cast<int>(w % kTile), half = static_cast<int>(w / kTile) & 1;
-    const int64_t at = w / (2 * kTile);
+  if (threadIdx.x < 2) redo[threadIdx.x] = 0;
+  __syncthreads();
+  int now = 0;
+  for (int64_t w0 = static_cast<int64_t>(blockIdx.x) * 8; w0 < rows; w0 += gridDim.x * 8, now ^= 1) {
+    const int r0 = static_cast<int>(w0 % kTile), half = static_cast<int>(w0 / kTile) & 1, r = r0 + warp;
+    const int64_t at = w0 / (2 * kTile);
     const int ln = static_cast<int>(at % lanes);
     const int4 e = __ldg(A.join_list + at / lanes);
-    const int key = e.x * kTile + r;
-    if (key >= A.T) continue;
-    RowVec<D> acc = row_zero<D>();
-    for (int p = 0; p < e.z; ++p) {
-      const float* src = A.part + ((static_cast<int64_t>(e.y + p) * lanes + ln) * 2 + half) * kTile * D +
-                         static_cast<int64_t>(r) * D + lane * (D / 32);
-#pragma unroll
-      for (int u = 0; u < D / 32; ++u) acc.x[u] += src[u];
-    }
-    bool fine = true;
-#pragma unroll
-    for (int u = 0; u < D / 32; ++u) {
-      if (half == 0) acc.x[u] *= A.scale;
-      fine &= fabsf(acc.x[u]) < INFINITY;
-    }
+    const int key0 = e.x * kTile + r0, key = key0 + warp;
     const int shard = ln / A.nkvl, g = ln % A.nkvl;
     const PackShard& S = A.s[shard];
-    if (__all_sync(0xffffffffu, fine))
+    if (key < A.T) {
+      RowVec<D> acc = row_zero<D>();
+      for (int p = 0; p < e.z; ++p) {
+        const float* src = A.part + ((static_cast<int64_t>(e.y + p) * lanes + ln) * 2 + half) * kTile * D +
+                           static_cast<int64_t>(r) * D + lane * (D / 32);
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) acc.x[u] += src[u];
+      }
+      bool fine = true;
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) {
+        if (half == 0) acc.x[u] *= A.scale;
+        fine &= fabsf(acc.x[u]) < INFINITY;
+      }
       row_store<D>((half ? S.dv + key * A.lddv : S.dk + key * A.lddk) + g * D, acc, lane);
-    else
-      dkv_row<D>(A, S, shard, g, key, doc_of(A.cu, A.batch, static_cast<int>(A.T), key), half == 0, lane);
+      if (!__all_sync(0xffffffffu, fine) && lane == 0) atomicOr(&redo[now], 1u << warp);
+    }
+    __syncthreads();                 // (and all eight rows are stored)
+    uint32_t again = redo[now];
+    if (threadIdx.x == 0) redo[now ^ 1] = 0;
+    if (again && warp < 8 / kRedoRows) {
+      again &= ((1u << kRedoRows) - 1) << (warp * kRedoRows);
+      int j[kRedoRows];
+      KeyEdges edges;
+      bool looked = false;
+      if (redo_take(again, key0, j) > 0) redo_keys<D>(A, shard, g, j, half == 0, edges, looked, lane);
+    }
+    __syncthreads();
   }
 }
 

@@ -88,12 +88,40 @@ __device__ __forceinline__ DqItem first_item(const DqParams& P) {
   return item_from(P, at, tile, first_tile);
 }
 
+// The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
 template <int D>
-__device__ __noinline__ void redo_dq(const PackArgs& A, int shard, int c, int q0, unsigned rows, int lane) {
-  while (rows) {
-    const int i = q0 + __ffs(rows) - 1;
-    rows &= rows - 1;
-    dq_row<D>(A, A.s[shard], shard, c, i, doc_of(A.cu, A.batch, static_cast<int>(A.T), i), lane);
+__device__ __noinline__ void redo_rows(const PackArgs& A, uint32_t slot, int w, int warps, int lane) {
+  int turn = 0;
+  while (slot != kRedoNone) {
+    const RedoEntry e = A.redo[slot];
+    const RedoPlace at = redo_place(slot, A.T);
+    const int shard = at.head / A.nql, c = at.head % A.nql;
+    const PackShard& S = A.s[shard];
+    QueryEdges edges;
+    bool looked = false;
+    for (uint32_t rows = e.rows; rows;) {
+      int i[kRedoRows], lo[kRedoRows];
+      redo_take(rows, at.row0, i);
+      if (turn++ % warps != w) continue;
+      uint32_t again = 0;
+#pragma unroll
+      for (int r = 0; r < kRedoRows; ++r) {
+        const int first = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
+        bool met = i[r] - first < kRedoShort;
+        if (!met) {
+          if (!looked) edges.look<D>(S.k, A.ldk, c / A.grp * D, first, at.row0, A.T, lane);
+          looked = true;
+          met = edges.met(first, i[r]);
+        }
+        if (met) again |= 1u << (i[r] - at.row0);
+      }
+      if (again == 0) continue;
+      const int n = redo_take(again, at.row0, i);
+#pragma unroll
+      for (int r = 0; r < kRedoRows; ++r) lo[r] = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
+      dq_rows<D>(A, S, shard, c, i, lo, n, lane);
+    }
+    slot = e.next;
   }
 }
 
@@ -131,7 +159,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bars + kQueueBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* flags = tmem_slot + 2;     // [4]: rows of a quadrant to be done again
-  static_assert((2 + 2 * kKSlots + 2 * kVSlots + 14 + kQueueBars) * 8 + 24 <= 320, "barrier area");
+  uint32_t* redo_head = flags + 4;     // the last listed slot
+  static_assert((2 + 2 * kKSlots + 2 * kVSlots + 14 + kQueueBars) * 8 + 28 <= 320, "barrier area");
   constexpr uint32_t T_DP = 128, T_DQ = 256, T_DS = 384;
 
   const PackArgs& A = P.a;
@@ -168,6 +197,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     mbar_init(rows_empty, kDqWarps);
     mbar_init(done_bar, 1);
     for (int q = 0; q < 4; ++q) flags[q] = 0;
+    *redo_head = kRedoNone;
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -499,16 +529,16 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive_relaxed(dq_empty);
       }
-      // A row is redone, by the first warpgroup, if any found its columns not finite, after all have stored.
+      // A row is listed, by the first warpgroup, if any found its columns not finite.
       const unsigned mine = __ballot_sync(0xffffffffu, in && bad != 0.0f);
       if (mine && lane == 0) atomicOr(&flags[quad], mine);
       if (!(ok = meet())) break;
       if (g == 0) {
         const unsigned again = flags[quad];
         __syncwarp();
-        if (again) {
-          if (lane == 0) flags[quad] = 0;
-          redo_dq<D>(A, it.shard, it.c, it.q0 + quad * 32, again, lane);
+        if (again && lane == 0) {
+          flags[quad] = 0;
+          redo_later(A.redo, redo_head, redo_slot(it.shard * A.nql + it.c, A.T, it.q0, quad), again);
         }
       }
     }
@@ -519,6 +549,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (warp >= 4 && *redo_head != kRedoNone && !*abort_flag) redo_rows<D>(A, *redo_head, warp - 4, kDqWarps, lane);
 }
 
 }  // namespace

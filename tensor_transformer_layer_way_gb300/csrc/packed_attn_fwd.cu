@@ -30,7 +30,7 @@
 // item costs about 10000 cycles beside its key tiles (masks, the wait for the last product, the result).
 //
 // A masked place enters the product as P = 0, and 0 times an infinite or NaN value is NaN: a row whose
-// result is not finite is computed again by its warp over its own keys alone.
+// result is not finite for that reason is computed again over its own keys alone when the block's items are done.
 
 #include <cstring>
 #include <mutex>
@@ -143,13 +143,40 @@ __device__ __forceinline__ int first_token(const RowDocs& d, int q0, int r) {
   return m ? q0 + w * 32 + 31 - __clz(m) : d.lo;
 }
 
-// Rows whose result is not finite, again from their own keys (kept out of the main loop's registers).
+// The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
 template <int D>
-__device__ __noinline__ void redo_rows(const PackArgs& A, int shard, int c, int q0, unsigned rows, int lane) {
-  while (rows) {
-    const int i = q0 + __ffs(rows) - 1;
-    rows &= rows - 1;
-    fwd_row<D>(A, A.s[shard], c, i, doc_of(A.cu, A.batch, static_cast<int>(A.T), i), lane);
+__device__ __noinline__ void redo_rows(const PackArgs& A, uint32_t slot, int w, int warps, int lane) {
+  int turn = 0;
+  while (slot != kRedoNone) {
+    const RedoEntry e = A.redo[slot];
+    const RedoPlace at = redo_place(slot, A.T);
+    const PackShard& S = A.s[at.head / A.nql];
+    const int c = at.head % A.nql;
+    QueryEdges edges;
+    bool looked = false;
+    for (uint32_t rows = e.rows; rows;) {
+      int i[kRedoRows], lo[kRedoRows];
+      redo_take(rows, at.row0, i);
+      if (turn++ % warps != w) continue;
+      uint32_t again = 0;
+#pragma unroll
+      for (int r = 0; r < kRedoRows; ++r) {
+        const int first = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
+        bool met = i[r] - first < kRedoShort;
+        if (!met) {
+          if (!looked) edges.look<D>(S.v, A.ldv, c / A.grp * D, first, at.row0, A.T, lane);
+          looked = true;
+          met = edges.met(first, i[r]);
+        }
+        if (met) again |= 1u << (i[r] - at.row0);
+      }
+      if (again == 0) continue;
+      const int n = redo_take(again, at.row0, i);
+#pragma unroll
+      for (int r = 0; r < kRedoRows; ++r) lo[r] = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
+      fwd_rows<D>(A, S, c, i, lo, n, lane);
+    }
+    slot = e.next;
   }
 }
 
@@ -174,7 +201,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
   uint64_t* item_bars = done_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bars + kQueueBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 + 2 * kRing + 8 + 1 + kQueueBars) * 8 + 8 <= 256, "barrier area");
+  uint32_t* redo_head = tmem_slot + 2;   // the last listed slot
+  static_assert((2 + 2 * kRing + 8 + 1 + kQueueBars) * 8 + 12 <= 256, "barrier area");
 
   const PackArgs& A = P.a;
   const int warp = uniform_warp();
@@ -200,6 +228,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     mbar_init(rows_empty, 8);
     mbar_init(done_bar, 1);
     *abort_flag = 0;
+    *redo_head = kRedoNone;
     fence_mbarrier_init();
   }
   if (threadIdx.x == 64) {
@@ -569,11 +598,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
       }
       tc_fence_before_sync();
       const unsigned again = __ballot_sync(0xffffffffu, in && bad != 0.0f);
-      if (again) {
-        if (lane == 0) bulk_wait_group_all();   // the rows' stores above come before those of the redo
-        __syncwarp();
-        redo_rows<D>(A, shard, qt.c, qt.q0 + quad * 32, again, lane);
-      }
+      if (again && lane == 0) redo_later(A.redo, redo_head, redo_slot(shard * A.nql + qt.c, A.T, qt.q0, quad), again);
     }
     if (lane == 0) bulk_wait_group_all();   // every store complete before the CTA's shared memory goes away
     __syncwarp();
@@ -584,6 +609,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
+  // (by the warps that hold the registers for it; every store of these rows above is complete)
+  if (warp >= 4 && *redo_head != kRedoNone && !*abort_flag) redo_rows<D>(A, *redo_head, warp - 4, 8, lane);
 }
 
 }  // namespace

@@ -398,3 +398,130 @@ def test_documents_beyond_the_pack_leave_the_rows_behind_it_alone(T, n_q, n_kv, 
     assert torch.equal(f2["O"][0], out_f["O"][0]) and torch.equal(f2["lse"][0], out_f["lse"][0])
     for n in ("dQ", "dK", "dV"):
         assert torch.equal(b2[n][0], out_b[n][0]), n
+
+
+def _one_bad_value(T, n_q, n_kv, d, lens, which, at, bad=float("nan")):
+    """Inputs with one value of `which` (head 0, column 3) at token `at` that is not finite, and the clean ones."""
+    x = _inputs(1, T, n_q, n_kv, d, lens, T + at)
+    y = {k: [v.clone() for v in m] if k != "cu" else m for k, m in x.items()}
+    y[which][0][at, 3] = bad
+    return x, y
+
+
+# One work list and none, key tiles that several items share, both head widths, odd groups.
+BESIDE = [(1, 700, 2, 1, 64, [100, 530, 60]), (1, 2600, 16, 4, 128, [130, 2100, 300]), (1, 2600, 6, 2, 64, [2, 2500, 60]),
+          (1, 3000, 16, 1, 128, [2800, 150])]
+
+
+@pytest.mark.parametrize("t,T,n_q,n_kv,d,lens", BESIDE)
+@pytest.mark.parametrize("which", ["V", "K", "Q", "dO"])
+def test_a_value_that_is_not_finite_reaches_what_sees_it_and_nothing_else(t, T, n_q, n_kv, d, lens, which):
+    """One NaN inside the longest document, in a tile's middle: the rows (and columns) that see it are NaN, all others
+    are as near as without it."""
+    first = lens.index(max(lens))
+    a, b = sum(lens[:first]), sum(lens[:first + 1])
+    for at in (a + 3, (a + b) // 2 + 5, b - 2):
+        x, y = _one_bad_value(T, n_q, n_kv, d, lens, which, at)
+        _, fwd, bwd = _run(t, T, n_q, n_kv, d, lens, x=x)
+        _, f2, b2 = _run(t, T, n_q, n_kv, d, lens, x=y)
+        # (the backward reference takes this run's O and lse, where a row's are numbers)
+        own = {n: [torch.where(torch.isnan(f2[n][0]), fwd[n][0], f2[n][0])] for n in ("O", "lse")}
+        ref = _reference(x, t, n_q, n_kv, d, lens, d ** -0.5, own)[0]
+        grp, used = n_q // n_kv, sum(lens)
+        see = {n: torch.zeros(T, h, d, dtype=torch.bool, device="cuda") for n, h in
+               (("O", n_q), ("dQ", n_q), ("dK", n_kv), ("dV", n_kv))}
+        lse = torch.zeros(n_q, T, dtype=torch.bool, device="cuda")
+        if which == "V":        # column 3 of o; through dp and D: dq of those rows, dk of the keys that they see
+            see["O"][at:b, :grp, 3] = True
+            see["dQ"][at:b, :grp] = True
+            see["dK"][a:b, 0] = True
+        elif which == "K":      # scores of the rows at or behind it
+            see["O"][at:b, :grp] = True
+            lse[:grp, at:b] = True
+            see["dQ"][at:b, :grp] = True
+            see["dK"][a:b, 0] = True
+            see["dV"][a:b, 0] = True
+        elif which == "Q":      # its own row's scores
+            see["O"][at, 0] = True
+            lse[0, at] = True
+            see["dQ"][at, 0] = True
+            see["dK"][a:at + 1, 0] = True
+            see["dV"][a:at + 1, 0] = True
+        else:                   # its own row's D and dp, and column 3 of what it adds to dv
+            see["dQ"][at, 0] = True
+            see["dK"][a:at + 1, 0] = True
+            see["dV"][a:at + 1, 0, 3] = True
+        got = {"O": f2["O"][0], "dQ": b2["dQ"][0], "dK": b2["dK"][0], "dV": b2["dV"][0]}
+        for n, e in (("O", "dO"), ("dQ", "eQ"), ("dK", "eK"), ("dV", "eV")):
+            g = got[n].view(T, -1, d)
+            assert torch.isnan(g[see[n]]).all(), f"{n} at {at}"
+            _near(g[~see[n]], ref[n][~see[n]], 2 * ref[e][~see[n]], f"{n} at {at}")
+        assert torch.isnan(f2["lse"][0][lse]).all()
+        rest = ~lse
+        rest[:, used:] = False
+        _near(f2["lse"][0][rest], ref["lse"][rest], ref["dlse"][rest], "lse")
+
+
+@pytest.mark.parametrize("t,T,n_q,n_kv,d,lens,left", [(1, 2000, 16, 4, 128, [900, 700], 150), (2, 1000, 4, 2, 64, [500, 300], 77),
+                                                      (1, 3000, 4, 1, 64, [2500], 201)])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+def test_rows_of_no_document_hold_anything(t, T, n_q, n_kv, d, lens, left, bad):
+    """Uninitialised rows before and behind the documents."""
+    x = _inputs(t, T, n_q, n_kv, d, lens, T)
+    used = left + sum(lens)
+    x["cu"] += left
+    y = {k: [v.clone() for v in m] if k != "cu" else m for k, m in x.items()}
+    for n in ("Q", "K", "V", "dO"):
+        for m in y[n]:
+            m[:left] = bad
+            m[used:] = bad
+    _, f2, b2 = _run(t, T, n_q, n_kv, d, lens, x=y)
+    part = {k: [v[left:used].contiguous() for v in m] if k != "cu" else m for k, m in x.items()}
+    f = {"O": [o[left:used] for o in f2["O"]], "lse": [l[:, left:used] for l in f2["lse"]]}
+    n_ = used - left
+    for i, r in enumerate(_reference(part, t, n_q, n_kv, d, lens, d ** -0.5, f)):
+        _near(f["O"][i].reshape(n_, -1, d), r["O"], r["dO"], "O")
+        _near(f["lse"][i], r["lse"], r["dlse"], "lse")
+        for n, e in (("dQ", "eQ"), ("dK", "eK"), ("dV", "eV")):
+            _near(b2[n][i][left:used].reshape(n_, -1, d), r[n], r[e], n)
+            assert torch.count_nonzero(b2[n][i][:left]) == 0 and torch.count_nonzero(b2[n][i][used:]) == 0
+
+
+def test_long_document_beside_a_value_that_is_not_finite():
+    """65536 tokens, 16 query heads to a KV head, a NaN in dO at token 3: its tile's later keys are computed again over the
+    whole document, which no wait may run out over; all other tiles keep their bits."""
+    T, n_q, n_kv, d, at, grp = 65536, 48, 3, 64, 3, 16
+    g = torch.Generator("cuda").manual_seed(1)
+    mat = lambda c: [torch.randn(T, c, generator=g, device="cuda").to(BF16)]   # noqa: E731
+    q, k, v, do = mat(n_q * d), mat(n_kv * d), mat(n_kv * d), mat(n_q * d)
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    kw = dict(n_q=n_q, n_kv=n_kv, d=d)
+    fwd = ttl.packed_attn_fwd(q, k, v, cu, **kw)
+    clean = ttl.packed_attn_bwd(do, q, k, v, fwd, cu, **kw)
+    bad = [do[0].clone()]
+    bad[0][at, 3] = float("nan")
+    got = ttl.packed_attn_bwd(bad, q, k, v, fwd, cu, **kw)
+    assert ttl.device_status() == 0
+    for n in ("dK", "dV"):
+        a, b = clean[n][0].view(T, n_kv, d), got[n][0].view(T, n_kv, d)
+        assert torch.equal(a[128:], b[128:]) and torch.equal(a[:, 1:], b[:, 1:]), n
+    assert torch.isnan(got["dV"][0][:at + 1, 3]).all() and torch.isnan(got["dK"][0][:at + 1, :d]).all()
+    # the tile's keys behind the NaN, of KV head 0
+    rows = slice(at + 1, 128)
+    kk, vv = k[0][rows, :d].to(F8), v[0][rows, :d].to(F8)
+    hide = torch.arange(T, device="cuda")[:, None] < torch.arange(at + 1, 128, device="cuda")[None]
+    r = {n: 0 for n in ("dV", "eV", "dK", "eK")}
+    for c in range(grp):
+        cols = slice(c * d, (c + 1) * d)
+        qq, gg = q[0][:, cols].to(F8), do[0][:, cols].to(F8)
+        ll, D = fwd["lse"][0][c].to(F8)[:, None], (gg * fwd["O"][0][:, cols].to(F8)).sum(1, keepdim=True)
+        s = d ** -0.5 * qq @ kk.T
+        p = torch.exp(s - ll).masked_fill(hide, 0.0)
+        ep = d ** -0.5 * 2 * d * U * qq.abs() @ kk.abs().T + 16 * U * (1 + s.abs()) + 8 * U * (1 + ll.abs())
+        dp = gg @ vv.T
+        ds = d ** -0.5 * p * (dp - D)
+        eds = d ** -0.5 * p * (ep * (dp - D).abs() + 2 * d * U * (gg.abs() @ vv.abs().T + (gg * fwd["O"][0][:, cols].to(F8)).abs().sum(1, keepdim=True)))
+        r["dV"], r["eV"] = r["dV"] + p.T @ gg, r["eV"] + T * grp * U * p.T @ gg.abs() + (p * ep).T @ gg.abs()
+        r["dK"], r["eK"] = r["dK"] + ds.T @ qq, r["eK"] + T * grp * U * ds.abs().T @ qq.abs() + eds.T @ qq.abs()
+    for n, e in (("dV", "eV"), ("dK", "eK")):
+        _near(got[n][0][rows, :d], r[n], 1.02 * r[e] + HALF * (r[n].abs() + r[e]), n)
