@@ -39,4 +39,9 @@ TTL_HOST_DEVICE DocRange doc_of(const int32_t* cu, int batch, int T, int tok) {
   return DocRange{lo < 0 ? 0 : lo, hi > T ? T : hi};
 }
 
+// How long a wait may take, in ns.  Some warps wait for the whole of an item, whose steps (key tiles; for dK and dV query
+// tiles times heads of the group) are as many as the longest document makes them: 2 s for a wait that nothing ends, and
+// 20 us for each step, twelve times what one takes.
+inline uint64_t pack_wait_ns(int64_t steps) { return 2000000000ull + 20000ull * static_cast<uint64_t>(steps); }
+
 }  // namespace ttl

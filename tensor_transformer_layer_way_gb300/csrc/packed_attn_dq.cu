@@ -562,7 +562,7 @@ int pack_attn_dq_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStre
   int rc = TTL_OK;
   P.tiles = static_cast<int>((A.T + kTile - 1) / kTile);
   P.lanes = A.t * A.nql;
-  P.timeout_ns = 2000000000ull;
+  P.timeout_ns = pack_wait_ns(P.tiles);
   const int64_t items = static_cast<int64_t>(P.tiles) * P.lanes;
   if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many query tiles");
   const int sms = num_sms();

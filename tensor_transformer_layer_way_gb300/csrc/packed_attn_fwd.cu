@@ -646,7 +646,7 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stre
   P.pair_heads = A.grp % 2 == 0;
   P.units = P.pair_heads ? tiles : (tiles + 1) / 2;
   P.lanes = P.pair_heads ? A.t * A.nql / 2 : A.t * A.nql;
-  P.timeout_ns = 2000000000ull;
+  P.timeout_ns = pack_wait_ns(tiles);
   const int64_t items = static_cast<int64_t>(P.units) * P.lanes;
   if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many query tiles");
   const int sms = num_sms();

@@ -23,16 +23,20 @@ def look_up(tmp_path_factory):
     src = d / "docs.cpp"
     src.write_text('#include "pack_docs.h"\n'
                    'extern "C" void docs(const int32_t* cu, int batch, int T, int tok, int* out) {\n'
-                   "  const ttl::DocRange r = ttl::doc_of(cu, batch, T, tok);\n  out[0] = r.lo;\n  out[1] = r.hi;\n}\n")
+                   "  const ttl::DocRange r = ttl::doc_of(cu, batch, T, tok);\n  out[0] = r.lo;\n  out[1] = r.hi;\n}\n"
+                   'extern "C" uint64_t wait_ns(int64_t steps) { return ttl::pack_wait_ns(steps); }\n')
     lib = d / "docs.so"
     subprocess.run([cxx, "-std=c++17", "-O1", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(lib)], check=True)
-    f = ctypes.CDLL(str(lib)).docs
+    host = ctypes.CDLL(str(lib))
+    f = host.docs
+    host.wait_ns.restype, host.wait_ns.argtypes = ctypes.c_uint64, [ctypes.c_int64]
 
     def call(cu, T, tok):
         out = (ctypes.c_int * 2)()
         f((ctypes.c_int32 * len(cu))(*cu), len(cu) - 1, T, tok, out)
         return out[0], out[1]
 
+    call.wait_ns = host.wait_ns
     return call
 
 
@@ -70,3 +74,12 @@ def test_valid_bounds(look_up):
             want = next(((a, b) for a, b in zip(cu, cu[1:]) if a <= tok < b), None)
             lo, hi = look_up(cu, T, tok)
             assert (lo, hi) == want if want else hi <= lo
+
+
+@pytest.mark.parametrize("tokens,grp", [(1, 1), (8192, 4), (65536, 16), (4 << 20, 64)])
+def test_a_wait_may_take_as_long_as_an_item(look_up, tokens, grp):
+    """Some warps wait for a whole item: one step of 1.6 us per query tile and head of the group for the longest."""
+    steps = (tokens + 127) // 128 * grp
+    ns = look_up.wait_ns(steps)
+    assert ns >= 2_000_000_000 and ns >= 5 * 1600 * steps
+    assert ns <= 2_000_000_000 + 100_000 * steps          # and what nothing ends does end
