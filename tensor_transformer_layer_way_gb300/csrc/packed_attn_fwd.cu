@@ -664,16 +664,23 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stre
   const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
   TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * tri * d * A.nql * A.t,
                    2.0 * A.T * (2.0 * qc + 2.0 * kc) * A.t);
+  // Behind the plan its blocks may be brought up early.  Without one the kernel before is the caller's: a block that
+  // held all of tensor memory while one of that kernel's still had to allocate some would keep it from ending.
+  auto launch = [&](auto kernel, size_t smem) {
+    return cuda_check(P.a.q_list ? launch_after(kernel, dim3(grid), kFwdThreads, smem, stream, P)
+                                 : launch_first(kernel, dim3(grid), kFwdThreads, smem, stream, P),
+                      "pack_fwd_kernel launch");
+  };
   if (d == 128) {
     if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_fwd_kernel<128>), kPackFwd128, FwdCfg<128>::SMEM,
                                  "cudaFuncSetAttribute(packed attention forward)")))
       return rc;
-    rc = cuda_check(launch_after(pack_fwd_kernel<128>, dim3(grid), kFwdThreads, FwdCfg<128>::SMEM, stream, P), "pack_fwd_kernel launch");
+    rc = launch(pack_fwd_kernel<128>, FwdCfg<128>::SMEM);
   } else {
     if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_fwd_kernel<64>), kPackFwd64, FwdCfg<64>::SMEM,
                                  "cudaFuncSetAttribute(packed attention forward)")))
       return rc;
-    rc = cuda_check(launch_after(pack_fwd_kernel<64>, dim3(grid), kFwdThreads, FwdCfg<64>::SMEM, stream, P), "pack_fwd_kernel launch");
+    rc = launch(pack_fwd_kernel<64>, FwdCfg<64>::SMEM);
   }
   return rc;
 }

@@ -525,3 +525,33 @@ def test_long_document_beside_a_value_that_is_not_finite():
         r["dK"], r["eK"] = r["dK"] + ds.T @ qq, r["eK"] + T * grp * U * ds.abs().T @ qq.abs() + eds.T @ qq.abs()
     for n, e in (("dV", "eV"), ("dK", "eK")):
         _near(got[n][0][rows, :d], r[n], 1.02 * r[e] + HALF * (r[n].abs() + r[e]), n)
+
+
+def _edges_into_the_last_kernel(call):
+    """The types of the edges between the kernels of a captured call behind one kernel of the caller's: 0 an ordinary
+    dependency, 1 one that lets the later kernel's blocks be brought up early."""
+    import ctypes
+    x = torch.zeros(1000, device="cuda")
+    x.add_(1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        x.add_(1)
+        call()
+    cuda = ctypes.CDLL("libcuda.so.1")
+    n = ctypes.c_size_t(0)
+    raw = ctypes.c_void_p(graph.raw_cuda_graph())
+    assert cuda.cuGraphGetEdges_v2(raw, None, None, None, ctypes.byref(n)) == 0
+    a, b, data = (ctypes.c_void_p * n.value)(), (ctypes.c_void_p * n.value)(), (ctypes.c_ubyte * (8 * n.value))()
+    assert cuda.cuGraphGetEdges_v2(raw, a, b, data, ctypes.byref(n)) == 0
+    return [data[8 * i + 2] for i in range(n.value)]
+
+
+@pytest.mark.skipif(not hasattr(torch.cuda.CUDAGraph, "raw_cuda_graph"), reason="needs the graph itself")
+@pytest.mark.parametrize("T,n_q,n_kv,d,types", [(200, 2, 1, 64, [0]), (300, 4, 1, 128, [0]), (4000, 20, 4, 64, [0, 1])])
+def test_the_first_kernel_of_a_call_waits_for_the_callers(T, n_q, n_kv, d, types):
+    x = _inputs(1, T, n_q, n_kv, d, [T], 1)
+    out = ttl.packed_attn_fwd_buffers(1, T, n_q, n_kv, d, 1)
+    call = lambda: ttl.packed_attn_fwd(x["Q"], x["K"], x["V"], x["cu"], n_q=n_q, n_kv=n_kv, d=d, out=out)   # noqa: E731
+    call()
+    assert sorted(_edges_into_the_last_kernel(call)) == types
