@@ -396,8 +396,8 @@ int ttl_tp_attn_bwd(int t, int64_t T, int64_t h, int n_q, int n_kv, int d, const
  *   Y[i]        [rows,h] out        mean[i], rstd[i] [rows] fp32 out, for the backward pass
  * X, R, S and Y hold x_type elements, gamma and beta w_type (TTL_T_BF16 or TTL_T_F32).  Any
  * h >= 1; pointers and strides need only their elements' alignment (16-byte aligned rows of a
- * whole number of 16-byte words are faster).  Sums are fp32.  No output may alias an input or
- * another output. */
+ * whole number of 16-byte words are faster).  Sums are fp32.  No output (mean and rstd among
+ * them) may share memory with an input or another output: TTL_ERR_ARG. */
 int ttl_layer_norm_fwd(int t, int64_t rows, int64_t h, int x_type, int w_type, const void* const* X, int64_t ldx,
                        const void* const* R, int64_t ldr, const void* gamma, const void* beta, float eps,
                        void* const* S, void* const* Y, float* const* mean, float* const* rstd, void* stream);
@@ -413,7 +413,8 @@ size_t ttl_layer_norm_bwd_workspace_size(int t, int64_t rows, int64_t h);
  *                sum past the block)
  *   dX[i] [rows,h] out;  dgamma, dbeta [h] fp32 (dbeta NULL = not wanted), written, or added to
  *                with accumulate = 1
- * The weight gradients are summed in a fixed order: the same inputs give the same bits. */
+ * The weight gradients are summed in a fixed order: the same inputs give the same bits.  No
+ * output, nor the workspace, may share memory with an input or another output: TTL_ERR_ARG. */
 int ttl_layer_norm_bwd(int t, int64_t rows, int64_t h, int x_type, int w_type, const void* const* X, int64_t ldx,
                        const void* const* dY, int64_t lddy, const void* const* dS, int64_t ldds, const void* gamma,
                        const float* const* mean, const float* const* rstd, void* const* dX, float* dgamma,
@@ -423,7 +424,8 @@ int ttl_layer_norm_bwd(int t, int64_t rows, int64_t h, int x_type, int w_type, c
 
 /* ttl_vocab_parallel_embedding_fwd (fused gather) with a factor: out[i][tok] = bf16(scale
  * E[id(tok)]) in every one of the t buffers, one rounding.  An id outside [0,V) sets
- * TTL_ERR_DEVICE in the status word and gives a zero row.  h a multiple of 8. */
+ * TTL_ERR_DEVICE in the status word and gives a zero row.  h a multiple of 8.  The outputs may
+ * all be one buffer; otherwise no output may share memory with another or with an input. */
 int ttl_vocab_parallel_embedding_scaled_fwd(int t, int64_t T, int64_t h, int64_t V, const int64_t* ids,
                                             const ttl_bf16* const* E, float scale, ttl_bf16* const* out,
                                             void* stream);
@@ -436,7 +438,8 @@ size_t ttl_vocab_parallel_embedding_sorted_bwd_workspace_size(int t, int64_t T, 
  * accumulate = 0 writes every row of dE (zeros where no token has the id), accumulate = 1 adds
  * to the rows that have tokens.  The tokens are sorted by id and summed in a fixed order: the
  * same inputs give the same bits.  dY [T,h] with row stride lddy (a multiple of 8).  Tokens
- * with an id outside [0,V) set TTL_ERR_DEVICE and are left out. */
+ * with an id outside [0,V) set TTL_ERR_DEVICE and are left out.  Neither dE nor the workspace may
+ * share memory with an input or with each other: TTL_ERR_ARG. */
 int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t h, int64_t V, const int64_t* ids,
                                             const ttl_bf16* dY, int64_t lddy, float scale, float* const* dE,
                                             int accumulate, void* ws, size_t ws_bytes, void* stream);
@@ -455,7 +458,9 @@ int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t h, int64_t
  *              (multiples of 8; e.g. column ranges of one fused projection)
  *   O[i] [T, n_q/t d] out, row stride ldo;  lse[i] [n_q/t, T] fp32 out: log sum exp(scale q.k)
  *   ws   workspace of ttl_packed_attn_fwd_workspace_size() bytes
- * t | n_q, t | n_kv, n_kv | n_q, d = 64 or 128, any T; scale > 0.  Memory use is linear in T. */
+ * t | n_q, t | n_kv, n_kv | n_q, d = 64 or 128, any T; scale > 0.  Memory use is linear in T.
+ * No output, nor the workspace, may share memory with an input or another output (column ranges
+ * of one matrix do not share any): TTL_ERR_ARG. */
 size_t ttl_packed_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch);
 int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
                         float scale, const ttl_bf16* const* Q, int64_t ldq, const ttl_bf16* const* K, int64_t ldk,
@@ -463,7 +468,8 @@ int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, c
                         void* ws, size_t ws_bytes, void* stream);
 
 /* Its backward pass from the saved O and lse: dQ[i], dK[i], dV[i] out with row strides lddq,
- * lddk, lddv (the KV gradients summed over each group's query heads, in a fixed order). */
+ * lddk, lddv (the KV gradients summed over each group's query heads, in a fixed order).  The
+ * same rule about shared memory. */
 size_t ttl_packed_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch);
 int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
                         float scale, const ttl_bf16* const* dO, int64_t lddo, const ttl_bf16* const* Q, int64_t ldq,

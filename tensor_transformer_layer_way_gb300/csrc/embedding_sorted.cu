@@ -18,6 +18,7 @@
 #include <mutex>
 
 #include "launch_after.cuh"
+#include "operands.h"
 #include "ttl_device.cuh"
 #include "ttl_internal.h"
 
@@ -690,6 +691,15 @@ extern "C" int ttl_vocab_parallel_embedding_scaled_fwd(int t, int64_t T, int64_t
   if ((rc = check_ids(ids, name)) || (rc = check_array(reinterpret_cast<const void* const*>(E), t, "E", name)) ||
       (rc = check_array(reinterpret_cast<const void* const*>(out), t, "out", name)))
     return rc;
+  {
+    bool one = true;   // the shards' outputs hold the same: they may be one buffer
+    for (int i = 1; i < t; ++i) one &= out[i] == out[0];
+    const void* tok = ids;
+    const Operand outs = operand("out", reinterpret_cast<const void* const*>(out), one ? 1 : t, T * h * 2);
+    const Operand ins[2] = {operand("E", reinterpret_cast<const void* const*>(E), t, V / t * h * 2),
+                            operand("ids", &tok, 1, T * 8)};
+    if ((rc = check_alias(&outs, 1, ins, 2, name))) return rc;
+  }
   if ((rc = require_sm103())) return rc;
   int* status = device_status_ptr();
   if (!status) return TTL_ERR_CUDA;
@@ -734,6 +744,14 @@ extern "C" int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t
     if (!aligned16(ws)) return set_error(TTL_ERR_ALIGN, "%s: workspace not 16-byte aligned", name);
   } else if (accumulate) {
     return TTL_OK;
+  }
+  {
+    const void *tok = ids, *dy = dY, *space = ws;
+    const int given = T > 0 ? 1 : 0;
+    const Operand outs[2] = {operand("dE", reinterpret_cast<const void* const*>(dE), t, V / t * h * 4),
+                             operand("the workspace", &space, given, static_cast<int64_t>(need))};
+    const Operand ins[2] = {operand("dY", &dy, given, T, lddy * 2, h * 2), operand("ids", &tok, given, T * 8)};
+    if ((rc = check_alias(outs, 2, ins, 2, name))) return rc;
   }
   if ((rc = require_sm103())) return rc;
   int* status = device_status_ptr();

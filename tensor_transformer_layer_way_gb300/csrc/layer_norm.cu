@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "launch_after.cuh"
+#include "operands.h"
 #include "ttl_device.cuh"
 #include "ttl_internal.h"
 
@@ -1105,13 +1106,6 @@ int check_slabs(const void* const* a, int t, int bytes, const char* what, const 
   return TTL_OK;
 }
 
-// Rows [rows, h] with stride ld at a and at b share memory.
-bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t h, int bytes) {
-  const char* p = static_cast<const char*>(a);
-  const char* q = static_cast<const char*>(b);
-  return p < q + ((rows - 1) * ldb + h) * bytes && q < p + ((rows - 1) * lda + h) * bytes;
-}
-
 // How a row of h elements is spread: B bytes per word, NV words per thread, W warps per row, G rows at a
 // time per CTA, `ctas` CTAs on an SM; stages > 0: through the ring, with that many rows of a group in shared memory
 // (smem bytes in all).  W = 0: wider than all of these, the kernel that reads its row again takes it.
@@ -1291,12 +1285,16 @@ extern "C" int ttl_layer_norm_fwd(int t, int64_t rows, int64_t h, int x_type, in
       (rc = check_slabs(reinterpret_cast<CP>(rstd), t, 4, "rstd", name)) ||
       (rc = check_ptr(gamma, wb, "gamma", name)) || (beta && (rc = check_ptr(beta, wb, "beta", name))))
     return rc;
-  for (int i = 0; i < t; ++i)
-    for (int o = 0; o < t; ++o)
-      if (overlap(X[i], ldx, Y[o], h, rows, h, xb) || (R && overlap(R[i], ldr, Y[o], h, rows, h, xb)) ||
-          (S && (overlap(X[i], ldx, S[o], h, rows, h, xb) || overlap(R[i], ldr, S[o], h, rows, h, xb) ||
-                 overlap(S[i], h, Y[o], h, rows, h, xb))))
-        return set_error(TTL_ERR_ARG, "%s: an output aliases an input or another output", name);
+  {
+    const int64_t w = h * xb;
+    Operand outs[4] = {operand("Y", reinterpret_cast<CP>(Y), t, rows, w, w),
+                       operand("mean", reinterpret_cast<CP>(mean), t, rows * 4),
+                       operand("rstd", reinterpret_cast<CP>(rstd), t, rows * 4),
+                       operand("S", reinterpret_cast<CP>(S), t, rows, w, w)};
+    const Operand ins[4] = {operand("X", X, t, rows, ldx * xb, w), operand("gamma", &gamma, 1, h * wb),
+                            operand("beta", &beta, beta ? 1 : 0, h * wb), operand("R", R, R ? t : 0, rows, ldr * xb, w)};
+    if ((rc = check_alias(outs, S ? 4 : 3, ins, 4, name))) return rc;
+  }
   if ((rc = require_sm103())) return rc;
   NormFwd P = {};
   P.status = device_status_ptr();
@@ -1375,15 +1373,20 @@ extern "C" int ttl_layer_norm_bwd(int t, int64_t rows, int64_t h, int x_type, in
         (rc = check_slabs(reinterpret_cast<CP>(rstd), t, 4, "rstd", name)) ||
         (rc = check_ptr(gamma, wb, "gamma", name)))
       return rc;
-    for (int i = 0; i < t; ++i)
-      for (int o = 0; o < t; ++o)
-        if (overlap(X[i], ldx, dX[o], h, rows, h, xb) || overlap(dY[i], lddy, dX[o], h, rows, h, xb) ||
-            (dS && overlap(dS[i], ldds, dX[o], h, rows, h, xb)))
-          return set_error(TTL_ERR_ARG, "%s: dX aliases an input", name);
     const size_t need = ttl_layer_norm_bwd_workspace_size(t, rows, h);
     if (!ws || ws_bytes < need)
       return set_error(TTL_ERR_ARG, "%s: workspace of %zu bytes needed, %zu given", name, need, ws_bytes);
     if (!aligned16(ws)) return set_error(TTL_ERR_ALIGN, "%s: workspace not 16-byte aligned", name);
+    const int64_t w = h * xb;
+    const void *dg = dgamma, *db = dbeta, *space = ws;
+    const Operand outs[4] = {operand("dX", reinterpret_cast<CP>(dX), t, rows, w, w), operand("dgamma", &dg, 1, h * 4),
+                             operand("dbeta", &db, dbeta ? 1 : 0, h * 4),
+                             operand("the workspace", &space, 1, static_cast<int64_t>(need))};
+    const Operand ins[6] = {operand("X", X, t, rows, ldx * xb, w), operand("dY", dY, t, rows, lddy * xb, w),
+                            operand("gamma", &gamma, 1, h * wb), operand("mean", reinterpret_cast<CP>(mean), t, rows * 4),
+                            operand("rstd", reinterpret_cast<CP>(rstd), t, rows * 4),
+                            operand("dS", dS, dS ? t : 0, rows, ldds * xb, w)};
+    if ((rc = check_alias(outs, 4, ins, 6, name))) return rc;
   }
   if (rows == 0 && accumulate) return TTL_OK;
   if ((rc = require_sm103())) return rc;

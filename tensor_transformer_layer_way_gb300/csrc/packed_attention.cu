@@ -12,6 +12,7 @@
 //   dq_i = scale sum_j ds_j k_j,  dk_j = scale sum_{c, i} ds_j q_i,  dv_j = sum_{c, i} p_j do_i
 // A token of no document has o = 0, lse = -inf and zero gradients.
 
+#include "operands.h"
 #include "packed_attn.cuh"
 
 namespace ttl {
@@ -94,6 +95,10 @@ BwdWs bwd_ws(int64_t T, int n_q, int n_kv, int d) {
   return w;
 }
 
+Operand mats(const char* name, const ttl_bf16* const* at, int t, int64_t T, int64_t ld, int64_t cols) {
+  return operand(name, reinterpret_cast<const void* const*>(at), t, T, ld * 2, cols * 2);
+}
+
 const __nv_bfloat16* bf(const ttl_bf16* p) { return reinterpret_cast<const __nv_bfloat16*>(p); }
 __nv_bfloat16* bf(ttl_bf16* p) { return reinterpret_cast<__nv_bfloat16*>(p); }
 
@@ -132,6 +137,14 @@ extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, i
   if (!ws || ws_bytes < need)
     return set_error(TTL_ERR_ARG, "%s: workspace of %zu bytes needed, %zu given", name, need, ws_bytes);
   if (!aligned16(ws)) return set_error(TTL_ERR_ALIGN, "%s: workspace not 16-byte aligned", name);
+  {
+    const void *bounds = cu_seqlens, *space = ws;
+    const Operand outs[3] = {mats("O", O, t, T, ldo, qc), operand("lse", reinterpret_cast<CP>(lse), t, n_q / t * T * 4),
+                             operand("the workspace", &space, 1, static_cast<int64_t>(need))};
+    const Operand ins[4] = {mats("Q", Q, t, T, ldq, qc), mats("K", K, t, T, ldk, kc), mats("V", V, t, T, ldv, kc),
+                            operand("cu_seqlens", &bounds, 1, (int64_t(batch) + 1) * 4)};
+    if ((rc = check_alias(outs, 3, ins, 4, name))) return rc;
+  }
   if ((rc = require_sm103())) return rc;
   PackArgs A = {};
   A.status = device_status_ptr();
@@ -177,6 +190,16 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
   if (!ws || ws_bytes < need)
     return set_error(TTL_ERR_ARG, "%s: workspace of %zu bytes needed, %zu given", name, need, ws_bytes);
   if (!aligned16(ws)) return set_error(TTL_ERR_ALIGN, "%s: workspace not 16-byte aligned", name);
+  {
+    const void *bounds = cu_seqlens, *space = ws;
+    const Operand outs[4] = {mats("dQ", dQ, t, T, lddq, qc), mats("dK", dK, t, T, lddk, kc), mats("dV", dV, t, T, lddv, kc),
+                             operand("the workspace", &space, 1, static_cast<int64_t>(need))};
+    const Operand ins[7] = {mats("dO", dO, t, T, lddo, qc), mats("Q", Q, t, T, ldq, qc), mats("K", K, t, T, ldk, kc),
+                            mats("V", V, t, T, ldv, kc), mats("O", O, t, T, ldo, qc),
+                            operand("lse", reinterpret_cast<CP>(lse), t, n_q / t * T * 4),
+                            operand("cu_seqlens", &bounds, 1, (int64_t(batch) + 1) * 4)};
+    if ((rc = check_alias(outs, 4, ins, 7, name))) return rc;
+  }
   if ((rc = require_sm103())) return rc;
   PackArgs A = {};
   A.status = device_status_ptr();

@@ -158,3 +158,91 @@ def test_binding_refuses_host_tensors_and_wrong_types(lib):
         ttl.packed_attn_fwd([x], [x], [x], torch.zeros(2, dtype=torch.int32), n_q=1, n_kv=1, d=64)
     with pytest.raises(ValueError):
         ttl.vocab_parallel_embedding_scaled_fwd(torch.zeros(4, dtype=torch.int64), [x], 1.0)
+
+
+# ---- outputs that share memory (4 rows of 64 bf16: 512 bytes a slab, 16 a slab of mean or rstd)
+@pytest.mark.parametrize("change", [
+    dict(Y=_arr(0x400000, 0x400000)), dict(Y=_arr(0x400000, 0x400100)), dict(R=R2, S=_arr(0x300000, 0x300000)),
+    dict(R=R2, S=_arr(0x300000, 0x400000)), dict(R=R2, S=_arr(0x408000, 0x308000)), dict(R=R2, S=_arr(0x208000, 0x308000)),
+    dict(mean=I2), dict(mean=_arr(0x500000, 0x50000c)), dict(rstd=_arr(0x100000, 0x530000)), dict(mean=_arr(0x4000f0, 0x510000)),
+    dict(Y=_arr(0x600000, 0x408000)), dict(rstd=_arr(0x520000, 0x610040)),
+])
+def test_layer_norm_fwd_refuses_outputs_that_share_memory(lib, change):
+    assert _norm_fwd(lib, **change) == 1
+    assert b"shares memory" in lib.ttl_last_error()
+
+
+@pytest.mark.parametrize("change", [
+    dict(dX=_arr(0x400000, 0x400000)), dict(dX=_arr(0x100100, 0x408000)), dict(dgamma=0x710000), dict(dgamma=0x710080),
+    dict(dbeta=0x100010), dict(dgamma=0x600000), dict(dX=_arr(0x500000, 0x408000)), dict(dX=_arr(0x400000, 0x530000)),
+    dict(ws=0x400000), dict(ws=0x200000), dict(dS=S2, dX=_arr(0x400000, 0x308010)),
+])
+def test_layer_norm_bwd_refuses_outputs_that_share_memory(lib, change):
+    assert _norm_bwd(lib, **change) == 1
+    assert b"shares memory" in lib.ttl_last_error()
+
+
+@pytest.mark.parametrize("change", [
+    dict(dE=_arr(0x300000, 0x300000)), dict(dE=_arr(0x300000, 0x300ff0)), dict(dE=_arr(0x20010, 0x400000)),
+    dict(dE=_arr(0x10030, 0x400000)), dict(ws=0x300000), dict(ws=0x20000), dict(ws=0x10000),
+])
+def test_sorted_embedding_refuses_outputs_that_share_memory(lib, change):
+    assert _emb_bwd(lib, **change) == 1
+    assert b"shares memory" in lib.ttl_last_error()
+
+
+def test_scaled_embedding_refuses_outputs_that_share_memory(lib):
+    f = lib.ttl_vocab_parallel_embedding_scaled_fwd
+    for out in (E2, _arr(0x500000, 0x500010), _arr(0x1007f0, 0x600000), _arr(0x500000, 0x10030)):
+        assert f(2, 8, 64, 32, 0x10000, E2, 2.0, out, None) == 1
+        assert b"shares memory" in lib.ttl_last_error()
+
+
+# 16 tokens, rows of 128 and 64 bf16, two shards each
+A2, B2, C2, D2, F2, L2 = (_arr(a, a + 0x100000) for a in (0x1000000, 0x2000000, 0x3000000, 0x4000000, 0x5000000, 0x6000000))
+H2, I3, J2 = (_arr(a, a + 0x100000) for a in (0x7000000, 0x8000000, 0x9000000))
+
+
+def _apart(**change):
+    return dict(dict(dO=A2, Q=B2, K=C2, V=D2, O=F2, lse=L2, dQ=H2, dK=I3, dV=J2, ws=0xa000000, cu=0xb000000), **change)
+
+
+@pytest.mark.parametrize("change", [
+    dict(O=B2), dict(O=C2), dict(O=_arr(0x5000000, 0x5000000)), dict(lse=F2), dict(lse=_arr(0x6000000, 0x600007c)),
+    dict(O=_arr(0x5000000, 0x4100010)), dict(lse=_arr(0xb000000, 0x6100000)), dict(ws=0x2100000), dict(ws=0x5000000),
+    dict(ldo=192, ldq=192, O=_arr(0x5000000, 0x2100000 + 112)),         # 8 columns into Q's
+])
+def test_packed_attn_fwd_refuses_outputs_that_share_memory(lib, change):
+    assert _attn_fwd(lib, **_apart(**change)) == 1
+    assert b"shares memory" in lib.ttl_last_error()
+
+
+@pytest.mark.parametrize("change", [
+    dict(dQ=A2), dict(dQ=B2), dict(dQ=F2), dict(dK=C2), dict(dV=D2), dict(dV=I3), dict(dK=_arr(0x8000000, 0x8000000)),
+    dict(dQ=_arr(0x7000000, 0x6100000)), dict(dV=_arr(0xb000000, 0x9100000)), dict(ws=0x7000000), dict(ws=0x6000000),
+    dict(lddq=256, lddk=256, dK=_arr(0x7000000 + 240, 0x8100000)),      # dK 8 columns into dQ's
+    dict(lddq=256, lddk=192, dK=_arr(0x7000000 + 256, 0x8100000)),      # two row strides in one place
+])
+def test_packed_attn_bwd_refuses_outputs_that_share_memory(lib, change):
+    assert _attn_bwd(lib, **_apart(**change)) == 1
+    assert b"shares memory" in lib.ttl_last_error()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are not memory: only where no kernel can be launched")
+def test_outputs_beside_each_other_are_taken(lib):
+    """Column ranges of one matrix, neighbours in memory, inputs that are the same: the calls get as far as the device."""
+    taken = lambda rc: rc not in (0, 1, 2, 3)     # noqa: E731
+    cols = lambda base, at: _arr(base + 2 * at, base + 0x100000 + 2 * at)   # noqa: E731
+    fused = dict(Q=cols(0x2000000, 0), K=cols(0x2000000, 128), V=cols(0x2000000, 192), ldq=256, ldk=256, ldv=256,
+                 dQ=cols(0x7000000, 0), dK=cols(0x7000000, 128), dV=cols(0x7000000, 192), lddq=256, lddk=256, lddv=256)
+    assert taken(_attn_bwd(lib, **_apart(**fused))) and taken(_attn_fwd(lib, **_apart(**fused)))
+    assert taken(_attn_fwd(lib, **_apart(K=D2))) and taken(_attn_bwd(lib, **_apart(dO=F2, K=D2)))
+    assert taken(_attn_fwd(lib, **_apart(O=_arr(0x5000000, 0x5000000 + 16 * 128 * 2))))
+    assert taken(_attn_fwd(lib, T=1, **_apart(O=_arr(0x5000000, 0x5000000 + 256))))
+    assert taken(_norm_fwd(lib, Y=_arr(0x400000, 0x400000 + 512), mean=_arr(0x500000, 0x500010), rstd=_arr(0x500020, 0x500030)))
+    assert taken(_norm_fwd(lib, X=_arr(0x100000, 0x100000)))
+    assert taken(_norm_bwd(lib, dY=X2, dS=X2)) and taken(_norm_bwd(lib, dbeta=0x700100))
+    assert taken(_emb_bwd(lib, dE=_arr(0x300000, 0x300000 + 16 * 64 * 4)))
+    f = lib.ttl_vocab_parallel_embedding_scaled_fwd
+    assert taken(f(2, 8, 64, 32, 0x10000, E2, 2.0, _arr(0x500000, 0x500000), None))
+    assert taken(f(2, 8, 64, 32, 0x10000, _arr(0x100000, 0x100000), 2.0, O2, None))
