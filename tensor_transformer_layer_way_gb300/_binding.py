@@ -658,6 +658,17 @@ def _rows(ts, name, n, dtype, rows, cols):
     return out, ld
 
 
+def _space(ws):
+    """The pointer and the bytes of a workspace: any contiguous CUDA tensor."""
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a tensor")
+    if not ws.is_cuda:
+        raise ValueError("ws must be a CUDA tensor")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _queue(x, stream):
     """The raw stream: the given one, or the current one of x's device."""
     if stream is not None:
@@ -728,11 +739,11 @@ def layer_norm_bwd(X, dY, gamma, fwd, *, dS=None, accumulate=False, out=None, st
         if accumulate:
             raise ValueError("accumulate needs out")
         out = layer_norm_bwd_buffers(t, rows, h, dtype, X[0].device)
-    ws, dbeta = out["ws"], out["dbeta"]
+    dbeta = out["dbeta"]
     _check(lib().ttl_layer_norm_bwd(t, rows, h, dt, wt, x, ldx, dy, lddy, ds, ldds, g, mean, rstd,
                                     _ptrs(out["dX"], "dX", t, dtype, (rows, h)), _ptr(out["dgamma"], "dgamma", f, (h,)),
                                     None if dbeta is None else _ptr(dbeta, "dbeta", f, (h,)), 1 if accumulate else 0,
-                                    ws.data_ptr(), ws.numel(), _queue(X[0], stream)))
+                                    *_space(out["ws"]), _queue(X[0], stream)))
     return out
 
 
@@ -773,8 +784,7 @@ def vocab_parallel_embedding_sorted_bwd(ids, dY, scale, dE, *, accumulate=False,
     if ws is None:
         ws = embedding_sorted_bwd_workspace(t, T, h, Vs * t, ids.device)
     _check(lib().ttl_vocab_parallel_embedding_sorted_bwd(t, T, h, Vs * t, i, dy[0], lddy, scale, de,
-                                                         1 if accumulate else 0, ws.data_ptr(), ws.numel(),
-                                                         _queue(ids, stream)))
+                                                         1 if accumulate else 0, *_space(ws), _queue(ids, stream)))
     return dE
 
 
@@ -807,10 +817,9 @@ def packed_attn_fwd(Q, K, V, cu_seqlens, *, n_q, n_kv, d, scale=None, out=None, 
     if out is None:
         out = packed_attn_fwd_buffers(t, T, n_q, n_kv, d, bounds - 1, Q[0].device)
     o, ldo = _rows(out["O"], "O", t, bf16, T, qc)
-    ws = out["ws"]
     _check(lib().ttl_packed_attn_fwd(t, T, n_q, n_kv, d, bounds - 1, cu, d ** -0.5 if scale is None else scale, q, ldq,
                                      k, ldk, v, ldv, o, ldo, _ptrs(out["lse"], "lse", t, torch.float32, (nql, T)),
-                                     ws.data_ptr(), ws.numel(), _queue(Q[0], stream)))
+                                     *_space(out["ws"]), _queue(Q[0], stream)))
     return out
 
 
@@ -844,9 +853,8 @@ def packed_attn_bwd(dO, Q, K, V, fwd, cu_seqlens, *, n_q, n_kv, d, scale=None, o
     dq, lddq = _rows(out["dQ"], "dQ", t, bf16, T, qc)
     dk, lddk = _rows(out["dK"], "dK", t, bf16, T, kc)
     dv, lddv = _rows(out["dV"], "dV", t, bf16, T, kc)
-    ws = out["ws"]
     _check(lib().ttl_packed_attn_bwd(t, T, n_q, n_kv, d, bounds - 1, cu, d ** -0.5 if scale is None else scale, do, lddo,
                                      q, ldq, k, ldk, v, ldv, o, ldo,
                                      _ptrs(fwd["lse"], "lse", t, torch.float32, (nql, T)), dq, lddq, dk, lddk, dv, lddv,
-                                     ws.data_ptr(), ws.numel(), _queue(Q[0], stream)))
+                                     *_space(out["ws"]), _queue(Q[0], stream)))
     return out

@@ -246,3 +246,11 @@ def test_outputs_beside_each_other_are_taken(lib):
     f = lib.ttl_vocab_parallel_embedding_scaled_fwd
     assert taken(f(2, 8, 64, 32, 0x10000, E2, 2.0, _arr(0x500000, 0x500000), None))
     assert taken(f(2, 8, 64, 32, 0x10000, _arr(0x100000, 0x100000), 2.0, O2, None))
+
+
+def test_binding_refuses_workspaces_that_are_no_device_memory(lib):
+    from tensor_transformer_layer_way_gb300 import _binding
+    for bad, error in ((torch.empty(64, dtype=torch.uint8), ValueError), (torch.empty(1 << 20, dtype=torch.uint8, device="meta"), ValueError),
+                       (None, TypeError), (1 << 20, TypeError)):
+        with pytest.raises(error):
+            _binding._space(bad)
