@@ -8,6 +8,7 @@ device memory, streams and events.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -669,6 +670,12 @@ def _space(ws):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _made_on(stream):
+    """Where buffers that a call makes itself are allocated: on the stream that the call's kernels run on, so that their
+    memory is neither still used by, nor given to, work of another stream while they run."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _queue(x, stream):
     """The raw stream: the given one, or the current one of x's device."""
     if stream is not None:
@@ -707,7 +714,8 @@ def layer_norm_fwd(X, gamma, beta=None, *, eps=1e-5, residual=None, out=None, st
     g = _ptr(gamma, "gamma", gamma.dtype, (h,))
     b = None if beta is None else _ptr(beta, "beta", gamma.dtype, (h,))
     if out is None:
-        out = layer_norm_fwd_buffers(t, rows, h, dtype, residual is not None, X[0].device)
+        with _made_on(stream):
+            out = layer_norm_fwd_buffers(t, rows, h, dtype, residual is not None, X[0].device)
     s = None if residual is None else _ptrs(out["S"], "S", t, dtype, (rows, h))
     f = torch.float32
     _check(lib().ttl_layer_norm_fwd(t, rows, h, dt, wt, x, ldx, r, ldr, g, b, eps, s,
@@ -738,7 +746,8 @@ def layer_norm_bwd(X, dY, gamma, fwd, *, dS=None, accumulate=False, out=None, st
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = layer_norm_bwd_buffers(t, rows, h, dtype, X[0].device)
+        with _made_on(stream):
+            out = layer_norm_bwd_buffers(t, rows, h, dtype, X[0].device)
     dbeta = out["dbeta"]
     _check(lib().ttl_layer_norm_bwd(t, rows, h, dt, wt, x, ldx, dy, lddy, ds, ldds, g, mean, rstd,
                                     _ptrs(out["dX"], "dX", t, dtype, (rows, h)), _ptr(out["dgamma"], "dgamma", f, (h,)),
@@ -759,7 +768,8 @@ def vocab_parallel_embedding_scaled_fwd(ids, E, scale, *, out=None, stream=None)
     i = _ptr(ids, "ids", torch.int64, (T,))
     e = _ptrs(E, "E", t, bf16, (Vs, h))
     if out is None:
-        out = [torch.empty((T, h), device=ids.device, dtype=bf16) for _ in range(t)]
+        with _made_on(stream):
+            out = [torch.empty((T, h), device=ids.device, dtype=bf16) for _ in range(t)]
     _check(lib().ttl_vocab_parallel_embedding_scaled_fwd(t, T, h, Vs * t, i, e, scale,
                                                          _ptrs(out, "out", t, bf16, (T, h)), _queue(ids, stream)))
     return out
@@ -782,7 +792,8 @@ def vocab_parallel_embedding_sorted_bwd(ids, dY, scale, dE, *, accumulate=False,
     dy, lddy = _rows([dY], "dY", 1, torch.bfloat16, T, h)
     de = _ptrs(dE, "dE", t, torch.float32, (Vs, h))
     if ws is None:
-        ws = embedding_sorted_bwd_workspace(t, T, h, Vs * t, ids.device)
+        with _made_on(stream):
+            ws = embedding_sorted_bwd_workspace(t, T, h, Vs * t, ids.device)
     _check(lib().ttl_vocab_parallel_embedding_sorted_bwd(t, T, h, Vs * t, i, dy[0], lddy, scale, de,
                                                          1 if accumulate else 0, *_space(ws), _queue(ids, stream)))
     return dE
@@ -815,7 +826,8 @@ def packed_attn_fwd(Q, K, V, cu_seqlens, *, n_q, n_kv, d, scale=None, out=None, 
     bounds = cu_seqlens.numel()
     cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (bounds,))
     if out is None:
-        out = packed_attn_fwd_buffers(t, T, n_q, n_kv, d, bounds - 1, Q[0].device)
+        with _made_on(stream):
+            out = packed_attn_fwd_buffers(t, T, n_q, n_kv, d, bounds - 1, Q[0].device)
     o, ldo = _rows(out["O"], "O", t, bf16, T, qc)
     _check(lib().ttl_packed_attn_fwd(t, T, n_q, n_kv, d, bounds - 1, cu, d ** -0.5 if scale is None else scale, q, ldq,
                                      k, ldk, v, ldv, o, ldo, _ptrs(out["lse"], "lse", t, torch.float32, (nql, T)),
@@ -849,7 +861,8 @@ def packed_attn_bwd(dO, Q, K, V, fwd, cu_seqlens, *, n_q, n_kv, d, scale=None, o
     bounds = cu_seqlens.numel()
     cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (bounds,))
     if out is None:
-        out = packed_attn_bwd_buffers(t, T, n_q, n_kv, d, bounds - 1, Q[0].device)
+        with _made_on(stream):
+            out = packed_attn_bwd_buffers(t, T, n_q, n_kv, d, bounds - 1, Q[0].device)
     dq, lddq = _rows(out["dQ"], "dQ", t, bf16, T, qc)
     dk, lddk = _rows(out["dK"], "dK", t, bf16, T, kc)
     dv, lddv = _rows(out["dV"], "dV", t, bf16, T, kc)
