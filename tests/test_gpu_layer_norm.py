@@ -277,3 +277,30 @@ def test_gradient_with_a_large_mean(h):
     assert ((out["dX"][0].to(F8) - dx).abs() <= off + U * (dx.abs() + off)).all()
     mag = (dy * n).abs().sum(0)
     assert ((out["dgamma"].to(F8) - (dy * n).sum(0)).abs() <= (rows + 8) * U * mag).all()
+
+
+# More rows to a group than its ring has places (and two more): every place is filled again, its barrier's phase turns,
+# and with rows above 8192 values (read again, released a row late) too.  304 groups at most of rows of 4096.
+@pytest.mark.parametrize("t,rows,h,dt", [(1, 20000, 1024, torch.bfloat16), (2, 2000, 4096, torch.bfloat16),
+                                         (1, 2500, 4001, torch.bfloat16), (1, 1000, 12288, torch.bfloat16),
+                                         (1, 1000, 9001, torch.bfloat16), (1, 8000, 1001, torch.float32),
+                                         (4, 750, 4096, torch.float32), (1, 30000, 513, torch.bfloat16)])
+def test_ring_places_are_filled_again(t, rows, h, dt):
+    test_forward_and_backward(t, rows, h, dt, torch.float32)
+    test_residual_no_beta_and_accumulation(t, rows, h, dt)
+
+
+@pytest.mark.parametrize("pad", [8, 64])
+@pytest.mark.parametrize("h", [256, 1000, 4096, 12288])
+def test_strided_rows_of_whole_words_give_the_same_bits(pad, h):
+    """Slabs that are column ranges of wider matrices, rows on 16 bytes: every output as from contiguous copies."""
+    d = _inputs(2, 700, h, torch.bfloat16, torch.bfloat16, seed=pad, residual=True, pad=pad)
+    flat = {k: [x.contiguous() for x in v] if isinstance(v, list) else v for k, v in d.items()}
+    a = ttl.layer_norm_fwd(d["X"], d["gamma"], d["beta"], residual=d["R"])
+    c = ttl.layer_norm_fwd(flat["X"], d["gamma"], d["beta"], residual=flat["R"])
+    e = ttl.layer_norm_bwd(d["X"], d["dY"], d["gamma"], a, dS=d["dS"])
+    f = ttl.layer_norm_bwd(flat["X"], flat["dY"], d["gamma"], a, dS=flat["dS"])
+    for n in ("Y", "S", "mean", "rstd"):
+        assert all(torch.equal(x, y) for x, y in zip(a[n], c[n])), n
+    assert all(torch.equal(x, y) for x, y in zip(e["dX"], f["dX"]))
+    assert torch.equal(e["dgamma"], f["dgamma"]) and torch.equal(e["dbeta"], f["dbeta"])
