@@ -253,21 +253,29 @@ struct RedoEntry {
   uint32_t rows, next;
 };
 constexpr uint32_t kRedoNone = 0xffffffffu;
+__host__ __device__ __forceinline__ uint32_t redo_slots(int heads, int64_t T) {
+  return static_cast<uint32_t>(heads) * static_cast<uint32_t>((T + kTile - 1) / kTile) * 4u;
+}
 // Slot of rows [q0 + 32 quad, + 32) of head `head` (over all shards; dK and dV: of two heads per KV head).
 __device__ __forceinline__ uint32_t redo_slot(int head, int64_t T, int q0, int quad) {
-  return (static_cast<uint32_t>(head) * static_cast<uint32_t>((T + kTile - 1) / kTile) + static_cast<uint32_t>(q0 / kTile)) * 4u +
-         static_cast<uint32_t>(quad);
+  return redo_slots(head, T) + static_cast<uint32_t>(q0 / kTile) * 4u + static_cast<uint32_t>(quad);
 }
 struct RedoPlace {
   int head, row0;
 };
 __device__ __forceinline__ RedoPlace redo_place(uint32_t slot, int64_t T) {
-  const uint32_t groups = static_cast<uint32_t>((T + kTile - 1) / kTile) * 4u;
+  const uint32_t groups = redo_slots(1, T);
   return RedoPlace{static_cast<int>(slot / groups), static_cast<int>(slot % groups) * 32};
 }
+// A block's list: the slot listed last and how many were, in shared memory.  The walk ends by the count and at a
+// slot that there is not, whatever the entries hold (a workspace that two calls write at once).
+struct RedoList {
+  uint32_t head, count;
+};
 // By one lane.
-__device__ __forceinline__ void redo_later(RedoEntry* list, uint32_t* head, uint32_t slot, uint32_t rows) {
-  list[slot] = RedoEntry{rows, atomicExch(head, slot)};
+__device__ __forceinline__ void redo_later(RedoEntry* entries, RedoList* list, uint32_t slot, uint32_t rows) {
+  entries[slot] = RedoEntry{rows, atomicExch(&list->head, slot)};
+  atomicAdd(&list->count, 1u);
 }
 // Up to R of the rows in `mask`, taken out of it, as numbers from row0; the last one again where there are fewer.
 template <int R>

@@ -121,9 +121,10 @@ __device__ __noinline__ void redo_keys(const PackArgs& A, int shard, int g, int 
 
 // The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
 template <int D>
-__device__ __noinline__ void redo_rows(const PackArgs& A, uint32_t slot, int w, int warps, int lane) {
+__device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, int warps, int lane) {
+  const uint32_t slots = redo_slots(A.t * A.nkvl * 2, A.T);
   int turn = 0;
-  while (slot != kRedoNone) {
+  for (uint32_t slot = list.head; slot < slots && list.count > 0; --list.count) {
     const RedoEntry e = A.redo[slot];
     const RedoPlace at = redo_place(slot, A.T);
     const int kv = at.head >> 1;
@@ -169,8 +170,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bars + kQueueBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* flags = tmem_slot + 2;     // [2][4]: rows of a quadrant to be done again, of dK and of dV
-  uint32_t* redo_head = flags + 8;     // the last listed slot
-  static_assert((4 + 2 * kRing + 2 * kStat + 9 + kQueueBars) * 8 + 44 <= 336, "barrier area");
+  RedoList* redo_list = reinterpret_cast<RedoList*>(flags + 8);
+  static_assert((4 + 2 * kRing + 2 * kStat + 9 + kQueueBars) * 8 + 48 <= 336, "barrier area");
   constexpr uint32_t T_DP = 128, T_DK = 256, T_DV = 384;
 
   const PackArgs& A = P.a;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     mbar_init(x_bar, kKvWarps);
     mbar_init(done_bar, 1);
     for (int q = 0; q < 8; ++q) flags[q] = 0;
-    *redo_head = kRedoNone;
+    *redo_list = RedoList{kRedoNone, 0};
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -585,7 +586,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         __syncwarp();
         if (again && lane == 0) {
           flags[kind * 4 + quad] = 0;
-          redo_later(A.redo, redo_head, redo_slot((it.shard * A.nkvl + it.g) * 2 + kind, A.T, it.k0, quad), again);
+          redo_later(A.redo, redo_list, redo_slot((it.shard * A.nkvl + it.g) * 2 + kind, A.T, it.k0, quad), again);
         }
       }
     }
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (warp >= 4 && *redo_head != kRedoNone && !*abort_flag) redo_rows<D>(A, *redo_head, warp - 4, kKvWarps, lane);
+  if (warp >= 4 && redo_list->count > 0 && !*abort_flag) redo_rows<D>(A, *redo_list, warp - 4, kKvWarps, lane);
 }
 
 // Adds up the parts of the key tiles that several items shared, in the order of their steps: one warp per row

@@ -90,9 +90,10 @@ __device__ __forceinline__ DqItem first_item(const DqParams& P) {
 
 // The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
 template <int D>
-__device__ __noinline__ void redo_rows(const PackArgs& A, uint32_t slot, int w, int warps, int lane) {
+__device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, int warps, int lane) {
+  const uint32_t slots = redo_slots(A.t * A.nql, A.T);
   int turn = 0;
-  while (slot != kRedoNone) {
+  for (uint32_t slot = list.head; slot < slots && list.count > 0; --list.count) {
     const RedoEntry e = A.redo[slot];
     const RedoPlace at = redo_place(slot, A.T);
     const int shard = at.head / A.nql, c = at.head % A.nql;
@@ -159,8 +160,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bars + kQueueBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* flags = tmem_slot + 2;     // [4]: rows of a quadrant to be done again
-  uint32_t* redo_head = flags + 4;     // the last listed slot
-  static_assert((2 + 2 * kKSlots + 2 * kVSlots + 14 + kQueueBars) * 8 + 28 <= 320, "barrier area");
+  RedoList* redo_list = reinterpret_cast<RedoList*>(flags + 4);
+  static_assert((2 + 2 * kKSlots + 2 * kVSlots + 14 + kQueueBars) * 8 + 32 <= 320, "barrier area");
   constexpr uint32_t T_DP = 128, T_DQ = 256, T_DS = 384;
 
   const PackArgs& A = P.a;
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     mbar_init(rows_empty, kDqWarps);
     mbar_init(done_bar, 1);
     for (int q = 0; q < 4; ++q) flags[q] = 0;
-    *redo_head = kRedoNone;
+    *redo_list = RedoList{kRedoNone, 0};
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         __syncwarp();
         if (again && lane == 0) {
           flags[quad] = 0;
-          redo_later(A.redo, redo_head, redo_slot(it.shard * A.nql + it.c, A.T, it.q0, quad), again);
+          redo_later(A.redo, redo_list, redo_slot(it.shard * A.nql + it.c, A.T, it.q0, quad), again);
         }
       }
     }
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (warp >= 4 && *redo_head != kRedoNone && !*abort_flag) redo_rows<D>(A, *redo_head, warp - 4, kDqWarps, lane);
+  if (warp >= 4 && redo_list->count > 0 && !*abort_flag) redo_rows<D>(A, *redo_list, warp - 4, kDqWarps, lane);
 }
 
 }  // namespace

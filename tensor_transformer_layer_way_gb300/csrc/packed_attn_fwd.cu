@@ -145,9 +145,10 @@ __device__ __forceinline__ int first_token(const RowDocs& d, int q0, int r) {
 
 // The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
 template <int D>
-__device__ __noinline__ void redo_rows(const PackArgs& A, uint32_t slot, int w, int warps, int lane) {
+__device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, int warps, int lane) {
+  const uint32_t slots = redo_slots(A.t * A.nql, A.T);
   int turn = 0;
-  while (slot != kRedoNone) {
+  for (uint32_t slot = list.head; slot < slots && list.count > 0; --list.count) {
     const RedoEntry e = A.redo[slot];
     const RedoPlace at = redo_place(slot, A.T);
     const PackShard& S = A.s[at.head / A.nql];
@@ -201,8 +202,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
   uint64_t* item_bars = done_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bars + kQueueBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* redo_head = tmem_slot + 2;   // the last listed slot
-  static_assert((2 + 2 * kRing + 8 + 1 + kQueueBars) * 8 + 12 <= 256, "barrier area");
+  RedoList* redo_list = reinterpret_cast<RedoList*>(tmem_slot + 2);
+  static_assert((2 + 2 * kRing + 8 + 1 + kQueueBars) * 8 + 16 <= 256, "barrier area");
 
   const PackArgs& A = P.a;
   const int warp = uniform_warp();
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     mbar_init(rows_empty, 8);
     mbar_init(done_bar, 1);
     *abort_flag = 0;
-    *redo_head = kRedoNone;
+    *redo_list = RedoList{kRedoNone, 0};
     fence_mbarrier_init();
   }
   if (threadIdx.x == 64) {
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
       }
       tc_fence_before_sync();
       const unsigned again = __ballot_sync(0xffffffffu, in && bad != 0.0f);
-      if (again && lane == 0) redo_later(A.redo, redo_head, redo_slot(shard * A.nql + qt.c, A.T, qt.q0, quad), again);
+      if (again && lane == 0) redo_later(A.redo, redo_list, redo_slot(shard * A.nql + qt.c, A.T, qt.q0, quad), again);
     }
     if (lane == 0) bulk_wait_group_all();   // every store complete before the CTA's shared memory goes away
     __syncwarp();
@@ -610,7 +611,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     tmem_dealloc(tmem, kTmemCols);
   }
   // (by the warps that hold the registers for it; every store of these rows above is complete)
-  if (warp >= 4 && *redo_head != kRedoNone && !*abort_flag) redo_rows<D>(A, *redo_head, warp - 4, 8, lane);
+  if (warp >= 4 && redo_list->count > 0 && !*abort_flag) redo_rows<D>(A, *redo_list, warp - 4, 8, lane);
 }
 
 }  // namespace
