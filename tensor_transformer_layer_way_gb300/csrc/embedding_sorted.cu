@@ -15,8 +15,6 @@
 // the other CTAs of the same launch write the zeros of the rows that no token has meanwhile; beyond that three
 // launches per digit, and zeros everywhere first.  A few tokens of few columns need no sort: one launch.
 
-#include <mutex>
-
 #include "launch_after.cuh"
 #include "operands.h"
 #include "ttl_device.cuh"
@@ -633,23 +631,6 @@ SortPlan plan_of(int64_t T, int64_t h) {
   return p;
 }
 
-// Raises sort_fill_kernel's dynamic shared-memory limit, once per device (thread-safe).
-int one_smem_once() {
-  static std::mutex mu;
-  static bool done[64] = {};
-  int dev = 0;
-  int rc = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
-  if (rc) return rc;
-  if (dev < 0 || dev >= 64) return set_error(TTL_ERR_CUDA, "device index %d out of range", dev);
-  std::lock_guard<std::mutex> lock(mu);
-  if (done[dev]) return TTL_OK;
-  rc = cuda_check(cudaFuncSetAttribute(reinterpret_cast<const void*>(sort_fill_kernel),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOneSmem)),
-                  "cudaFuncSetAttribute(sort_fill_kernel)");
-  if (!rc) done[dev] = true;
-  return rc;
-}
-
 int check_common(int t, int64_t T, int64_t h, int64_t V, const char* name) {
   if (t < 1 || t > kMaxShards) return set_error(TTL_ERR_ARG, "%s: t=%d outside [1,%d]", name, t, kMaxShards);
   if (T < 0 || h < 0 || V < 0) return set_error(TTL_ERR_ARG, "%s: negative shape", name);
@@ -795,7 +776,7 @@ extern "C" int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t
   if (one) {
     const int passes = (width + 7) / 8, bits = (width + passes - 1) / passes;
     TraceScope trace(s, TTL_K_EMBED, 0.0, 16.0 * T + (accumulate ? 0.0 : 4.0 * V * h));
-    if ((rc = one_smem_once())) return rc;
+    if ((rc = allow_smem<sort_fill_kernel>(kOneSmem, "cudaFuncSetAttribute(sort_fill_kernel)"))) return rc;
     sort_fill_kernel<<<accumulate ? 1 : sms, kOneThreads, kOneSmem, s>>>(
         G, ids, static_cast<int>(T), V, Vs, h, passes, bits, keys[0], toks[0], runs, status);
     if ((rc = cuda_check(cudaGetLastError(), "sort_fill_kernel launch"))) return rc;

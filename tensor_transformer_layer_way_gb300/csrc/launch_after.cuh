@@ -4,7 +4,10 @@
 
 #include <cuda_runtime.h>
 
+#include <mutex>
 #include <utility>
+
+#include "ttl_internal.h"
 
 namespace ttl {
 
@@ -38,6 +41,24 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, unsigned block, s
   config.attrs = &overlap;
   config.numAttrs = 1;
   return cudaLaunchKernelEx(&config, kernel, std::forward<Args>(args)...);
+}
+
+// Raises a kernel's dynamic shared-memory limit to `bytes`, once per device (thread-safe).
+template <auto Kernel>
+int allow_smem(size_t bytes, const char* what) {
+  static std::mutex mu;
+  static size_t done[64] = {};
+  int dev = 0;
+  int rc = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc || bytes <= 40 * 1024) return rc;   // (the limit of 48 KiB counts the static arrays too)
+  if (dev < 0 || dev >= 64) return set_error(TTL_ERR_CUDA, "device index %d out of range", dev);
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev] >= bytes) return TTL_OK;
+  rc = cuda_check(cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(bytes)),
+                  what);
+  if (!rc) done[dev] = bytes;
+  return rc;
 }
 
 }  // namespace ttl

@@ -12,8 +12,6 @@
 //   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
 // All statistics and sums are fp32; the variance is taken about the mean (no E[x^2] - mean^2).
 
-#include <mutex>
-
 #include "launch_after.cuh"
 #include "operands.h"
 #include "ttl_device.cuh"
@@ -1168,23 +1166,6 @@ Spread spread_of(int64_t h, int elem, int B, bool bwd, int inputs) {
   return s;
 }
 
-template <auto Kernel>
-int allow_smem(size_t bytes) {
-  static std::mutex mu;
-  static size_t done[64] = {};
-  int dev = 0;
-  int rc = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
-  if (rc || bytes <= 40 * 1024) return rc;   // (the limit of 48 KiB counts the static arrays too)
-  if (dev < 0 || dev >= 64) return set_error(TTL_ERR_CUDA, "device index %d out of range", dev);
-  std::lock_guard<std::mutex> lock(mu);
-  if (done[dev] >= bytes) return TTL_OK;
-  rc = cuda_check(cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)),
-                  "cudaFuncSetAttribute(layer norm)");
-  if (!rc) done[dev] = bytes;
-  return rc;
-}
-
 unsigned fwd_grid(const NormFwd& P, const Spread& sp) {
   const int64_t ctas = (P.total + sp.G - 1) / sp.G;
   const int64_t cap = static_cast<int64_t>(num_sms()) * sp.ctas;
@@ -1193,7 +1174,7 @@ unsigned fwd_grid(const NormFwd& P, const Spread& sp) {
 
 template <typename T, int B, int NV>
 int fwd_ring(const NormFwd& P, const Spread& sp, cudaStream_t s) {
-  if (int rc = allow_smem<norm_fwd_ring_kernel<T, B, NV>>(sp.smem)) return rc;
+  if (int rc = allow_smem<norm_fwd_ring_kernel<T, B, NV>>(sp.smem, "cudaFuncSetAttribute(layer norm)")) return rc;
   norm_fwd_ring_kernel<T, B, NV><<<fwd_grid(P, sp), sp.W * sp.G * 32, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
   return TTL_OK;
 }
@@ -1206,7 +1187,7 @@ int fwd_regs(const NormFwd& P, const Spread& sp, cudaStream_t s) {
 
 template <typename T, int B, int NV>
 int bwd_ring(const NormBwd& P, const Spread& sp, int parts, cudaStream_t s) {
-  if (int rc = allow_smem<norm_bwd_ring_kernel<T, B, NV>>(sp.smem)) return rc;
+  if (int rc = allow_smem<norm_bwd_ring_kernel<T, B, NV>>(sp.smem, "cudaFuncSetAttribute(layer norm)")) return rc;
   norm_bwd_ring_kernel<T, B, NV><<<parts, sp.W * sp.G * 32, sp.smem, s>>>(P, sp.W, sp.G, sp.stages);
   return TTL_OK;
 }
@@ -1223,7 +1204,7 @@ int bwd_any(const NormBwd& P, int parts, cudaStream_t s) {
   const size_t sums = static_cast<size_t>(P.h) * 8;
   const int near = sums <= kAnySums;
   if (near)
-    if (int rc = allow_smem<norm_bwd_any_kernel<T, B>>(sums)) return rc;
+    if (int rc = allow_smem<norm_bwd_any_kernel<T, B>>(sums, "cudaFuncSetAttribute(layer norm)")) return rc;
   norm_bwd_any_kernel<T, B><<<parts, kNormThreads, near ? sums : 0, s>>>(P, near);
   return TTL_OK;
 }

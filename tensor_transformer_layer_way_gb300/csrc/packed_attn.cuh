@@ -78,10 +78,6 @@ inline bool pack_split(int64_t tiles, int lanes, int grp) {
   return tiles * lanes < 8 * 152 && tiles * grp > 2 * kSplitSteps;
 }
 
-// Raises a kernel's dynamic shared-memory limit, once per kernel and device (thread-safe).
-enum PackKernelSlot { kPackFwd128, kPackFwd64, kPackDq128, kPackDq64, kPackDkv128, kPackDkv64, kPackKernelSlots };
-int set_core_smem_once(const void* fn, int slot, int bytes, const char* what);
-
 // Launches of the tensor-core kernels (arguments are checked; A.s holds every pointer they need).
 // `list`: room for one word of 16 bytes per 128 tokens and one more; A.redo: for 4 words of 8 bytes per 128 tokens and
 // query head (backward: and twice as many per KV head, if that is more).

@@ -677,13 +677,11 @@ int pack_attn_dkv_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStr
   const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
   TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * tri * d * A.nql * A.t, 2.0 * A.T * (2.0 * qc + 4.0 * kc) * A.t);
   if (d == 128) {
-    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dkv_kernel<128>), kPackDkv128, KvCfg<128>::SMEM,
-                                 "cudaFuncSetAttribute(packed attention dK dV)")))
+    if ((rc = allow_smem<pack_dkv_kernel<128>>(KvCfg<128>::SMEM, "cudaFuncSetAttribute(packed attention dK dV)")))
       return rc;
     rc = cuda_check(launch_after(pack_dkv_kernel<128>, dim3(grid), kKvThreads, KvCfg<128>::SMEM, stream, P), "pack_dkv_kernel launch");
   } else {
-    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dkv_kernel<64>), kPackDkv64, KvCfg<64>::SMEM,
-                                 "cudaFuncSetAttribute(packed attention dK dV)")))
+    if ((rc = allow_smem<pack_dkv_kernel<64>>(KvCfg<64>::SMEM, "cudaFuncSetAttribute(packed attention dK dV)")))
       return rc;
     rc = cuda_check(launch_after(pack_dkv_kernel<64>, dim3(grid), kKvThreads, KvCfg<64>::SMEM, stream, P), "pack_dkv_kernel launch");
   }

@@ -571,13 +571,11 @@ int pack_attn_dq_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStre
   const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
   TraceScope trace(stream, TTL_K_ATTN_CORE, 6.0 * tri * d * A.nql * A.t, 2.0 * A.T * (4.0 * qc + 2.0 * kc) * A.t);
   if (d == 128) {
-    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dq_kernel<128>), kPackDq128, DqCfg<128>::SMEM,
-                                 "cudaFuncSetAttribute(packed attention dQ)")))
+    if ((rc = allow_smem<pack_dq_kernel<128>>(DqCfg<128>::SMEM, "cudaFuncSetAttribute(packed attention dQ)")))
       return rc;
     rc = cuda_check(launch_after(pack_dq_kernel<128>, dim3(grid), kDqThreads, DqCfg<128>::SMEM, stream, P), "pack_dq_kernel launch");
   } else {
-    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_dq_kernel<64>), kPackDq64, DqCfg<64>::SMEM,
-                                 "cudaFuncSetAttribute(packed attention dQ)")))
+    if ((rc = allow_smem<pack_dq_kernel<64>>(DqCfg<64>::SMEM, "cudaFuncSetAttribute(packed attention dQ)")))
       return rc;
     rc = cuda_check(launch_after(pack_dq_kernel<64>, dim3(grid), kDqThreads, DqCfg<64>::SMEM, stream, P), "pack_dq_kernel launch");
   }

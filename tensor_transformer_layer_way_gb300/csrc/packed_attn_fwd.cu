@@ -33,7 +33,6 @@
 // result is not finite for that reason is computed again over its own keys alone when the block's items are done.
 
 #include <cstring>
-#include <mutex>
 #include <type_traits>
 
 #include "packed_attn.cuh"
@@ -616,20 +615,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
 
 }  // namespace
 
-int set_core_smem_once(const void* fn, int slot, int bytes, const char* what) {
-  static std::mutex mu;
-  static bool done[kPackKernelSlots][64] = {};
-  int dev = 0;
-  int rc = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
-  if (rc) return rc;
-  if (dev < 0 || dev >= 64) return set_error(TTL_ERR_CUDA, "device index %d out of range", dev);
-  std::lock_guard<std::mutex> lock(mu);
-  if (done[slot][dev]) return TTL_OK;
-  rc = cuda_check(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), what);
-  if (!rc) done[slot][dev] = true;
-  return rc;
-}
-
 int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stream) {
   FwdParams P;
   std::memset(static_cast<void*>(&P), 0, sizeof(P));
@@ -673,13 +658,11 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stre
                       "pack_fwd_kernel launch");
   };
   if (d == 128) {
-    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_fwd_kernel<128>), kPackFwd128, FwdCfg<128>::SMEM,
-                                 "cudaFuncSetAttribute(packed attention forward)")))
+    if ((rc = allow_smem<pack_fwd_kernel<128>>(FwdCfg<128>::SMEM, "cudaFuncSetAttribute(packed attention forward)")))
       return rc;
     rc = launch(pack_fwd_kernel<128>, FwdCfg<128>::SMEM);
   } else {
-    if ((rc = set_core_smem_once(reinterpret_cast<const void*>(pack_fwd_kernel<64>), kPackFwd64, FwdCfg<64>::SMEM,
-                                 "cudaFuncSetAttribute(packed attention forward)")))
+    if ((rc = allow_smem<pack_fwd_kernel<64>>(FwdCfg<64>::SMEM, "cudaFuncSetAttribute(packed attention forward)")))
       return rc;
     rc = launch(pack_fwd_kernel<64>, FwdCfg<64>::SMEM);
   }
