@@ -663,11 +663,9 @@ def _space(ws):
     """The pointer and the bytes of a workspace: any contiguous CUDA tensor."""
     if not isinstance(ws, torch.Tensor):
         raise TypeError("ws must be a tensor")
-    if not ws.is_cuda:
-        raise ValueError("ws must be a CUDA tensor")
-    if not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor")
+    return ws.data_ptr(), ws.nbytes
 
 
 def _made_on(stream):

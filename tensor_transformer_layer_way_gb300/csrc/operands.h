@@ -55,9 +55,14 @@ inline bool operands_meet(const Operand& a, const Operand& b) {
     bounds(b, blo, bhi);
     if (ahi <= blo || bhi <= alo) return false;
   }
-  for (int i = 0; i < a.n; ++i)
-    for (int j = self ? i + 1 : 0; j < b.n; ++j)
-      if (operands_share(a, a.at[i], b, b.at[j])) return true;
+  const uintptr_t sa = static_cast<uintptr_t>(operand_span(a)), sb = static_cast<uintptr_t>(operand_span(b));
+  for (int i = 0; i < a.n; ++i) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.at[i]);
+    for (int j = self ? i + 1 : 0; j < b.n; ++j) {
+      const uintptr_t pb = reinterpret_cast<uintptr_t>(b.at[j]);
+      if (pa < pb + sb && pb < pa + sa && operands_share(a, a.at[i], b, b.at[j])) return true;
+    }
+  }
   return false;
 }
 
