@@ -451,7 +451,8 @@ int ttl_vocab_parallel_embedding_sorted_bwd(int t, int64_t T, int64_t h, int64_t
  * cu_seqlens[b+1]) of the T; a query sees the keys of its own document up to itself.  Documents
  * may be empty; tokens before the first or after the last document get O = 0, lse = -inf and
  * zero gradients.  What the keys, values and gradients of tokens outside a row's document (or
- * after it) hold, infinities and NaN among it, does not reach that row.
+ * after it) hold, infinities and NaN among it, does not reach that row (a row that meets such
+ * values in its tiles is computed again without tensor cores, which is slow for long documents).
  *   cu_seqlens [batch+1] int32, on the device, not decreasing, within [0,T]; anything else sets
  *              TTL_ERR_DEVICE (the outputs then mean nothing, no access leaves the tensors)
  *   Q[i] [T, n_q/t d], K[i], V[i] [T, n_kv/t d], head-major columns, row strides ldq, ldk, ldv

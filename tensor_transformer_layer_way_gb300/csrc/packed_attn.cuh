@@ -240,9 +240,9 @@ __device__ __forceinline__ void store_bf16x32(__nv_bfloat16* out, const uint32_t
 // when its items are done, from what they see alone: nothing waits for that, however long it takes.  It is only
 // done where a masked place of the row's first or last tile (no other tile has places that it does not see) holds such
 // a value: a row that is not finite by what it sees keeps the product's result.
-// Measured, 8192 tokens in 12 documents, 32 and 8 heads of 128 over 8 shards (131 us forward, 328 us backward): NaN inside the
-// longest document 1.0 and 2.0 to 3.6 ms, NaN in all rows behind the documents 0.5 and 14 ms; row by row at the
-// end of the item they took 23, 72 to 100, 4.2 and 80 ms.
+// Measured, 8192 tokens in 12 documents, 32 and 8 heads of 128 over 8 shards (129 us forward, 329 us backward, calls one at a
+// time): one NaN inside the longest document 0.8 and 1.9 to 3.5 ms, NaN in all rows behind the documents 0.4 and 14 ms; row
+// by row at the end of the item they took 23, 72 to 100, 4.2 and 80 ms.
 
 // Rows [32 slot', 32 slot' + 32) of one head: which of them, and the block's next listed slot.
 struct RedoEntry {

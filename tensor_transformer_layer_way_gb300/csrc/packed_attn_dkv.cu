@@ -14,11 +14,12 @@
 // into P, dK(n) and dP(n+1) run; while they form dS(n+1), dV(n+1) and S(n+2) do.
 //
 // What bounds it: the turns of tensor pipe and elementwise warps, 3000 cycles a step where the products need 2050.
-// Measured: one document of 16384 tokens, 4 query heads and 1 KV head of 128: 375 us, 1470 TFLOP/s.
+// Measured: one document of 16384 tokens, 4 query heads and 1 KV head of 128: 370 us, 1490 TFLOP/s.  P^T and dS^T are
+// rounded to bf16 once, the type of dO and Q in their products.
 //
 // Blocks take items from the list, heaviest first, as they get to them; warp 0 takes one while its last tiles wait for
 // a place, and announces it to the others.  (Dealt out beforehand, in turn and back: 188 us for 12 documents of
-// 8192 tokens together, 32 and 8 heads over 8 shards; taken: 147.)
+// 8192 tokens together, 32 and 8 heads over 8 shards; taken: 145 to 149.)
 //
 // Roles (640 threads, persistent): warp 0 the TMA loads, warp 1 the MMAs, warp 2 brings each step's lse and D to
 // shared memory, warp 3 the documents of the coming item's keys, warps 4..19 the elementwise work: a key row per

@@ -11,7 +11,9 @@
 // row takes the row's maximum, P = 2^(s k - m) as bf16 over S_x's own columns, O_x += P V with P
 // read from tensor memory.  The running maximum m only moves when a row's new maximum is more than
 // 8 above it (in base 2): P then stays below 2^8, which bf16 and the fp32 sums hold as exactly,
-// and the accumulator is rescaled rarely.  The row sum l is taken from the unrounded P.
+// and the accumulator is rescaled rarely.  The row sum l is taken from the unrounded P.  P is rounded to bf16 once, as
+// the product's operands have one type and V is bf16 (error against 64 bits 1.8 to 2.0e-3, with P in fp32 1.5e-3;
+// P as two bf16 parts would cost the product twice).
 //
 // Roles (384 threads, persistent): warp 0 issues the TMA loads (Q_0, Q_1, then K_j, V_j through a ring), warp 1
 // the MMAs, warps 2 and 3 look up the coming item and the documents of its rows, warps 4..7 and 8..11 are the
@@ -24,9 +26,9 @@
 //
 // What bounds it: the turn of a tile, 2700 cycles (clock stamps: softmax 1300, product and next scores 1100, the rest
 // hand-overs), which the other tile's turn fills up to the products' 2050; tensor memory has no columns left in
-// which the next scores could wait.  Measured: one document of 32768 tokens, 4 query heads and 1 KV head of 128: 680 us, 1618
-// TFLOP/s; 8192 tokens in 12 documents, 32 query and 8 KV heads over 8 shards: 96 us (101
-// with items dealt out beforehand).  With many short documents an
+// which the next scores could wait.  Measured: one document of 32768 tokens, 4 query heads and 1 KV head of 128: 665 to 705 us,
+// 1560 to 1650 TFLOP/s; 8192 tokens in 12 documents, 32 query and 8 KV heads over 8 shards: 94 us (with items
+// dealt out beforehand 5 more); 16384 tokens, 8 and 2 heads of 64: 292 us.  With many short documents an
 // item costs about 10000 cycles beside its key tiles (masks, the wait for the last product, the result).
 //
 // A masked place enters the product as P = 0, and 0 times an infinite or NaN value is NaN: a row whose
