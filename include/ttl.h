@@ -93,7 +93,7 @@ int ttl_selftest_wait_timeout(int64_t timeout_us, void* stream);
 #define TTL_K_EMBED 9       /* vocab-parallel embedding lookup / gradient     */
 #define TTL_K_SOFTMAX 10    /* attention row softmax / softmax backward       */
 #define TTL_K_ATTN_CORE 11  /* fused attention cores (scores, softmax, P V)  */
-#define TTL_K_NORM 12       /* layer norm forward / backward                  */
+#define TTL_K_NORM 12       /* layer norm, head norm and rotation, both ways  */
 
 /* Starts (on != 0) or stops tracing on this process.  While on, every kernel launch the
  * library makes is bracketed by a pair of CUDA events recorded on the launch stream, and
@@ -478,6 +478,49 @@ int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, c
                         const ttl_bf16* const* O, int64_t ldo, const float* const* lse, ttl_bf16* const* dQ,
                         int64_t lddq, ttl_bf16* const* dK, int64_t lddk, ttl_bf16* const* dV, int64_t lddv, void* ws,
                         size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ norm and rotation of heads */
+
+/* Norm of every head of Q and K and its rotation by position, in one pass ([TPSP] "Attention:按 head 切":
+ * between the projection and the scores a head stays on its shard).  For one head x of a token:
+ *   y = x gamma / sqrt(mean(x^2) + eps)          (gamma_q, gamma_k NULL: y = x, no norm)
+ * and each pair (a, b) of y's first rot columns turns by its angle f = position[axis] freq:
+ *   (a cos f - b sin f, b cos f + a sin f); the columns behind stay.
+ *   rot         columns, a multiple of 16 up to d (0: the norm alone)
+ *   interleaved 0: pair i is columns i and rot/2 + i; 1: columns 2 i and 2 i + 1
+ *   freqs       [rot/2] host, radians per position, |freq| <= 2^20
+ *   pair_axis   [rot/2] host, the axis of each pair, in [0,axes) (NULL: all on axis 0); axes <= 8
+ *   positions   [axes,T] int32, on the device; any value.  NULL (one axis): a token's place in its
+ *               document, or in the pack without cu_seqlens
+ *   cu_seqlens  [batch+1] int32, on the device, as ttl_packed_attn_fwd takes it, or NULL.  A token of
+ *               no document has y = 0 (and a zero gradient), whatever its rows hold
+ *   gamma_q, gamma_k [d] of w_type (TTL_T_BF16 or TTL_T_F32), both or neither
+ *   Q[i] [T, n_q/t d], K[i] [T, n_kv/t d], head-major columns, row strides ldq, ldk (multiples of 8)
+ *   Qo[i], Ko[i] out, the same shapes, row strides ldqo, ldko
+ * t | n_q, t | n_kv, d a multiple of 16 up to 256, any T < 2^31 - 1.  Sums are fp32, one rounding;
+ * an angle is exact to 2^-24 of a half turn at any position.  Qo may be Q itself, and Ko K (the same pointers and
+ * stride); otherwise no output may share memory with an input or another output: TTL_ERR_ARG. */
+int ttl_head_norm_rotary_fwd(int t, int64_t T, int n_q, int n_kv, int d, int rot, int interleaved, const double* freqs,
+                             const int32_t* pair_axis, int axes, const int32_t* positions, int batch,
+                             const int32_t* cu_seqlens, int w_type, const void* gamma_q, const void* gamma_k, float eps,
+                             const ttl_bf16* const* Q, int64_t ldq, const ttl_bf16* const* K, int64_t ldk,
+                             ttl_bf16* const* Qo, int64_t ldqo, ttl_bf16* const* Ko, int64_t ldko, void* stream);
+
+/* Its backward pass from the outputs' gradients dY_q, dY_k and the inputs Q, K (not read, and may be
+ * NULL, without gamma):  with g = dY turned back, n = x / sqrt(mean(x^2) + eps), h = g gamma
+ *   dgamma (+)= sum over all tokens and heads of g n,   dQ, dK = (h - n mean(h n)) / sqrt(mean(x^2) + eps)
+ *   dgamma_q, dgamma_k [d] fp32 out (added to with accumulate = 1), NULL without gamma; summed in a
+ *               fixed order: the same inputs give the same bits
+ *   ws   workspace of ttl_head_norm_rotary_bwd_workspace_size() bytes, NULL without gamma
+ * dQ may be dY_q itself, and dK dY_k; the rule about other shared memory holds, for the workspace too. */
+size_t ttl_head_norm_rotary_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d);
+int ttl_head_norm_rotary_bwd(int t, int64_t T, int n_q, int n_kv, int d, int rot, int interleaved, const double* freqs,
+                             const int32_t* pair_axis, int axes, const int32_t* positions, int batch,
+                             const int32_t* cu_seqlens, int w_type, const void* gamma_q, const void* gamma_k, float eps,
+                             const ttl_bf16* const* dY_q, int64_t lddyq, const ttl_bf16* const* dY_k, int64_t lddyk,
+                             const ttl_bf16* const* Q, int64_t ldq, const ttl_bf16* const* K, int64_t ldk,
+                             ttl_bf16* const* dQ, int64_t lddq, ttl_bf16* const* dK, int64_t lddk, float* dgamma_q,
+                             float* dgamma_k, int accumulate, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

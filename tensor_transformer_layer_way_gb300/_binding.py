@@ -86,6 +86,11 @@ _SIGS = {
     "ttl_packed_attn_bwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int, _int]),
     "ttl_packed_attn_bwd": (_int, [_int, _i64, _int, _int, _int, _int, _vp, ctypes.c_float]
                             + [_vp, _i64] * 5 + [_vp] + [_vp, _i64] * 3 + [_vp, ctypes.c_size_t, _vp]),
+    "ttl_head_norm_rotary_fwd": (_int, [_int, _i64] + [_int] * 5 + [_vp, _vp, _int, _vp, _int, _vp, _int, _vp, _vp,
+                                        ctypes.c_float] + [_vp, _i64] * 4 + [_vp]),
+    "ttl_head_norm_rotary_bwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int]),
+    "ttl_head_norm_rotary_bwd": (_int, [_int, _i64] + [_int] * 5 + [_vp, _vp, _int, _vp, _int, _vp, _int, _vp, _vp,
+                                        ctypes.c_float] + [_vp, _i64] * 6 + [_vp, _vp, _int, _vp, ctypes.c_size_t, _vp]),
 }
 
 _lib = None
@@ -868,4 +873,137 @@ def packed_attn_bwd(dO, Q, K, V, fwd, cu_seqlens, *, n_q, n_kv, d, scale=None, o
                                      q, ldq, k, ldk, v, ldv, o, ldo,
                                      _ptrs(fwd["lse"], "lse", t, torch.float32, (nql, T)), dq, lddq, dk, lddk, dv, lddv,
                                      *_space(out["ws"]), _queue(Q[0], stream)))
+    return out
+
+
+# ------------------------------------------------------------------ norm and rotation of heads
+
+def rotary_freqs(rot, base=10000.0):
+    """Radians a position for the rot/2 pairs of a head's rotated columns: base^(-2 i / rot)."""
+    return [float(base) ** (-2.0 * i / rot) for i in range(rot // 2)]
+
+
+class Rotary:
+    """How heads are rotated, as a program keeps it: ``freqs``, radians a position for each pair of columns; ``axes``,
+    the axis of positions that each pair follows (all the first if None); ``interleaved``, whether a pair is two
+    neighbouring columns (else columns i and len(freqs) + i)."""
+
+    def __init__(self, freqs, *, axes=None, interleaved=False):
+        freqs = [float(f) for f in freqs]
+        axes = [0] * len(freqs) if axes is None else [int(a) for a in axes]
+        if len(axes) != len(freqs):
+            raise ValueError(f"axes has {len(axes)} entries, expected {len(freqs)}")
+        if any(a < 0 for a in axes):
+            raise ValueError("axes must not be negative")
+        self.rot = 2 * len(freqs)
+        self.axes = 1 + max(axes, default=0)
+        self.interleaved = bool(interleaved)
+        self._freqs = (ctypes.c_double * len(freqs))(*freqs)
+        self._pair_axis = (ctypes.c_int32 * len(axes))(*axes)
+
+
+def _rotary_args(rotary, T, d, n_q, n_kv, t, gamma_q, gamma_k, eps, positions, cu_seqlens):
+    """The arguments that both directions share, after t."""
+    if not isinstance(rotary, Rotary):
+        raise TypeError("rotary must be a Rotary")
+    pos = cu = gq = gk = None
+    axes, batch, wt = rotary.axes, 0, 0
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
+            raise ValueError("positions must be a tensor [axes, T] or [T]")
+        if positions.dim() == 2:
+            if positions.shape[0] < axes:
+                raise ValueError(f"positions has {positions.shape[0]} axes, the rotation {axes}")
+            axes = positions.shape[0]
+        elif axes != 1:
+            raise ValueError(f"positions has one axis, the rotation {axes}")
+        pos = _ptr(positions, "positions", torch.int32, (T,) if positions.dim() == 1 else (axes, T))
+    if cu_seqlens is not None:
+        bounds = cu_seqlens.numel()
+        cu, batch = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (bounds,)), bounds - 1
+    if (gamma_q is None) != (gamma_k is None):
+        raise ValueError("gamma_q and gamma_k go together")
+    if gamma_q is not None:
+        wt = _TYPES.get(gamma_q.dtype)
+        if wt is None:
+            raise TypeError("gamma must be bf16 or fp32")
+        gq, gk = _ptr(gamma_q, "gamma_q", gamma_q.dtype, (d,)), _ptr(gamma_k, "gamma_k", gamma_q.dtype, (d,))
+    return (t, T, n_q, n_kv, d, rotary.rot, 1 if rotary.interleaved else 0, rotary._freqs, rotary._pair_axis, axes, pos,
+            batch, cu, wt, gq, gk, eps)
+
+
+def head_norm_rotary_fwd_buffers(t, T, n_q, n_kv, d, device="cuda"):
+    """Output buffers of head_norm_rotary_fwd."""
+    e = dict(device=device, dtype=torch.bfloat16)
+    return {"Q": [torch.empty(T, n_q // t * d, **e) for _ in range(t)],
+            "K": [torch.empty(T, n_kv // t * d, **e) for _ in range(t)]}
+
+
+def head_norm_rotary_fwd(Q, K, rotary, *, n_q, n_kv, d, gamma_q=None, gamma_k=None, eps=1e-6, positions=None,
+                         cu_seqlens=None, out=None, stream=None):
+    """Norm (root mean square, weights gamma_q and gamma_k [d]; none without them) of every head of Q and K and its
+    rotation by position.  Q, K are lists of t shards [T, n_q/t d], [T, n_kv/t d] with contiguous rows of any stride;
+    positions int32 [axes, T] on the device, by default each token's place in its document of cu_seqlens (or in the
+    pack).  With cu_seqlens a token of no document gives zeros.  Returns dict Q, K (lists; ``out`` may hold the inputs)."""
+    t = len(Q)
+    T = Q[0].shape[0]
+    qc, kc = n_q // t * d, n_kv // t * d
+    bf16 = torch.bfloat16
+    q, ldq = _rows(Q, "Q", t, bf16, T, qc)
+    k, ldk = _rows(K, "K", t, bf16, T, kc)
+    args = _rotary_args(rotary, T, d, n_q, n_kv, t, gamma_q, gamma_k, eps, positions, cu_seqlens)
+    if out is None:
+        with _made_on(stream):
+            out = head_norm_rotary_fwd_buffers(t, T, n_q, n_kv, d, Q[0].device)
+    qo, ldqo = _rows(out["Q"], "Q", t, bf16, T, qc)
+    ko, ldko = _rows(out["K"], "K", t, bf16, T, kc)
+    _check(lib().ttl_head_norm_rotary_fwd(*args, q, ldq, k, ldk, qo, ldqo, ko, ldko, _queue(Q[0], stream)))
+    return out
+
+
+def head_norm_rotary_bwd_buffers(t, T, n_q, n_kv, d, norm=True, device="cuda"):
+    """Gradient and workspace buffers of head_norm_rotary_bwd."""
+    e = dict(device=device, dtype=torch.bfloat16)
+    out = {"dQ": [torch.empty(T, n_q // t * d, **e) for _ in range(t)],
+           "dK": [torch.empty(T, n_kv // t * d, **e) for _ in range(t)], "dgamma_q": None, "dgamma_k": None, "ws": None}
+    if norm:
+        ws = int(lib().ttl_head_norm_rotary_bwd_workspace_size(t, T, n_q, n_kv, d))
+        out.update(dgamma_q=torch.empty(d, device=device), dgamma_k=torch.empty(d, device=device),
+                   ws=torch.empty(max(ws, 16), dtype=torch.uint8, device=device))
+    return out
+
+
+def head_norm_rotary_bwd(dQ, dK, rotary, *, n_q, n_kv, d, Q=None, K=None, gamma_q=None, gamma_k=None, eps=1e-6,
+                         positions=None, cu_seqlens=None, accumulate=False, out=None, stream=None):
+    """Backward of head_norm_rotary_fwd: dQ and dK are its outputs' gradients, Q and K its inputs (needed with gamma
+    only), the rest as given to it.  Returns dict dQ, dK (lists; ``out`` may hold the incoming gradients) and, with
+    gamma, dgamma_q, dgamma_k (fp32; with ``accumulate`` added to those of ``out``)."""
+    t = len(dQ)
+    T = dQ[0].shape[0]
+    qc, kc = n_q // t * d, n_kv // t * d
+    bf16, f = torch.bfloat16, torch.float32
+    gq, ldgq = _rows(dQ, "dQ", t, bf16, T, qc)
+    gk, ldgk = _rows(dK, "dK", t, bf16, T, kc)
+    args = _rotary_args(rotary, T, d, n_q, n_kv, t, gamma_q, gamma_k, eps, positions, cu_seqlens)
+    norm = gamma_q is not None
+    (q, ldq), (k, ldk) = (None, qc), (None, kc)
+    if norm:
+        if Q is None or K is None:
+            raise ValueError("the norm's backward pass needs Q and K")
+        q, ldq = _rows(Q, "Q", t, bf16, T, qc)
+        k, ldk = _rows(K, "K", t, bf16, T, kc)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        with _made_on(stream):
+            out = head_norm_rotary_bwd_buffers(t, T, n_q, n_kv, d, norm, dQ[0].device)
+    oq, ldoq = _rows(out["dQ"], "dQ", t, bf16, T, qc)
+    ok, ldok = _rows(out["dK"], "dK", t, bf16, T, kc)
+    dgq = dgk = ws = None
+    ws_bytes = 0
+    if norm:
+        dgq, dgk = _ptr(out["dgamma_q"], "dgamma_q", f, (d,)), _ptr(out["dgamma_k"], "dgamma_k", f, (d,))
+        ws, ws_bytes = _space(out["ws"])
+    _check(lib().ttl_head_norm_rotary_bwd(*args, gq, ldgq, gk, ldgk, q, ldq, k, ldk, oq, ldoq, ok, ldok, dgq, dgk,
+                                          1 if accumulate else 0, ws, ws_bytes, _queue(dQ[0], stream)))
     return out
