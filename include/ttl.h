@@ -479,6 +479,32 @@ int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, c
                         int64_t lddq, ttl_bf16* const* dK, int64_t lddk, ttl_bf16* const* dV, int64_t lddv, void* ws,
                         size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ packed attention over a window */
+
+/* ttl_packed_attn_fwd where the query at token i of a document that begins at lo sees the keys
+ *   max(lo, i - window + 1) .. i, and before these lo .. lo + sinks - 1 (first tokens that stay visible)
+ * alone: window >= 1 keys up to itself, sinks >= 0; either may be any size (together T or more: the
+ * same as ttl_packed_attn_fwd).  All else as there: documents, strides, masked places, shared memory,
+ * errors.  Its time goes with T (window + sinks). */
+size_t ttl_packed_window_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch, int64_t window,
+                                                 int64_t sinks);
+int ttl_packed_window_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, int64_t window, int64_t sinks,
+                               const int32_t* cu_seqlens, float scale, const ttl_bf16* const* Q, int64_t ldq,
+                               const ttl_bf16* const* K, int64_t ldk, const ttl_bf16* const* V, int64_t ldv,
+                               ttl_bf16* const* O, int64_t ldo, float* const* lse, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* Its backward pass from the saved O and lse, with the same window and sinks; all else as
+ * ttl_packed_attn_bwd. */
+size_t ttl_packed_window_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch, int64_t window,
+                                                 int64_t sinks);
+int ttl_packed_window_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, int64_t window, int64_t sinks,
+                               const int32_t* cu_seqlens, float scale, const ttl_bf16* const* dO, int64_t lddo,
+                               const ttl_bf16* const* Q, int64_t ldq, const ttl_bf16* const* K, int64_t ldk,
+                               const ttl_bf16* const* V, int64_t ldv, const ttl_bf16* const* O, int64_t ldo,
+                               const float* const* lse, ttl_bf16* const* dQ, int64_t lddq, ttl_bf16* const* dK,
+                               int64_t lddk, ttl_bf16* const* dV, int64_t lddv, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ norm and rotation of heads */
 
 /* Norm of every head of Q and K and its rotation by position, in one pass ([TPSP] "Attention:按 head 切":

@@ -14,6 +14,7 @@ from ._binding import (  # noqa: F401
     Rotary, head_norm_rotary_bwd, head_norm_rotary_bwd_buffers, head_norm_rotary_fwd, head_norm_rotary_fwd_buffers, rotary_freqs,
     embedding_sorted_bwd_workspace, layer_norm_bwd, layer_norm_bwd_buffers, layer_norm_fwd, layer_norm_fwd_buffers,
     packed_attn_bwd, packed_attn_bwd_buffers, packed_attn_fwd, packed_attn_fwd_buffers,
+    packed_window_attn_bwd, packed_window_attn_bwd_buffers, packed_window_attn_fwd, packed_window_attn_fwd_buffers,
     mlp_fwd_buffers, selftest_wait_timeout, sp_mlp_bwd, sp_mlp_fwd, shard_all_gather, shard_all_reduce, shard_reduce_scatter, tp_mlp_bwd,
     tp_attn_bwd, tp_attn_fwd, tp_mlp_bwd_static_ws, tp_mlp_bwd_workspace_size, tp_mlp_fwd, trace_enable, trace_read, version,
     vocab_parallel_ce, vocab_parallel_embedding_bwd, vocab_parallel_embedding_fwd, vocab_parallel_embedding_scaled_fwd,

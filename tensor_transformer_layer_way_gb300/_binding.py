@@ -86,6 +86,12 @@ _SIGS = {
     "ttl_packed_attn_bwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int, _int]),
     "ttl_packed_attn_bwd": (_int, [_int, _i64, _int, _int, _int, _int, _vp, ctypes.c_float]
                             + [_vp, _i64] * 5 + [_vp] + [_vp, _i64] * 3 + [_vp, ctypes.c_size_t, _vp]),
+    "ttl_packed_window_attn_fwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int, _int, _i64, _i64]),
+    "ttl_packed_window_attn_fwd": (_int, [_int, _i64, _int, _int, _int, _int, _i64, _i64, _vp, ctypes.c_float]
+                                   + [_vp, _i64] * 4 + [_vp, _vp, ctypes.c_size_t, _vp]),
+    "ttl_packed_window_attn_bwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int, _int, _i64, _i64]),
+    "ttl_packed_window_attn_bwd": (_int, [_int, _i64, _int, _int, _int, _int, _i64, _i64, _vp, ctypes.c_float]
+                                   + [_vp, _i64] * 5 + [_vp] + [_vp, _i64] * 3 + [_vp, ctypes.c_size_t, _vp]),
     "ttl_head_norm_rotary_fwd": (_int, [_int, _i64] + [_int] * 5 + [_vp, _vp, _int, _vp, _int, _vp, _int, _vp, _vp,
                                         ctypes.c_float] + [_vp, _i64] * 4 + [_vp]),
     "ttl_head_norm_rotary_bwd_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int]),
@@ -873,6 +879,86 @@ def packed_attn_bwd(dO, Q, K, V, fwd, cu_seqlens, *, n_q, n_kv, d, scale=None, o
                                      q, ldq, k, ldk, v, ldv, o, ldo,
                                      _ptrs(fwd["lse"], "lse", t, torch.float32, (nql, T)), dq, lddq, dk, lddk, dv, lddv,
                                      *_space(out["ws"]), _queue(Q[0], stream)))
+    return out
+
+
+# ------------------------------------------------------------------ packed attention over a window
+
+def _window_size(entry, t, T, n_q, n_kv, d, batch, window, sinks):
+    """The workspace's bytes; raises what is wrong with the arguments."""
+    ws = int(entry(t, T, n_q, n_kv, d, batch, window, sinks))
+    if ws == 0:
+        raise TTLError(TTL_ERR_ARG, last_error())
+    return ws
+
+
+def packed_window_attn_fwd_buffers(t, T, n_q, n_kv, d, batch, window, sinks=0, device="cuda"):
+    """Output and workspace buffers of packed_window_attn_fwd."""
+    ws = _window_size(lib().ttl_packed_window_attn_fwd_workspace_size, t, T, n_q, n_kv, d, batch, window, sinks)
+    return {"O": [torch.empty(T, n_q // t * d, device=device, dtype=torch.bfloat16) for _ in range(t)],
+            "lse": [torch.empty(n_q // t, T, device=device) for _ in range(t)],
+            "ws": torch.empty(ws, dtype=torch.uint8, device=device)}
+
+
+def packed_window_attn_fwd(Q, K, V, cu_seqlens, *, window, sinks=0, n_q, n_kv, d, scale=None, out=None, stream=None):
+    """packed_attn_fwd where a query sees the last ``window`` keys of its document up to itself, and its document's first
+    ``sinks`` tokens.  Returns dict O and lse as there."""
+    t = len(Q)
+    T = Q[0].shape[0]
+    nql = n_q // t
+    qc, kc = nql * d, n_kv // t * d
+    bf16 = torch.bfloat16
+    q, ldq = _rows(Q, "Q", t, bf16, T, qc)
+    k, ldk = _rows(K, "K", t, bf16, T, kc)
+    v, ldv = _rows(V, "V", t, bf16, T, kc)
+    bounds = cu_seqlens.numel()
+    cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (bounds,))
+    if out is None:
+        with _made_on(stream):
+            out = packed_window_attn_fwd_buffers(t, T, n_q, n_kv, d, bounds - 1, window, sinks, Q[0].device)
+    o, ldo = _rows(out["O"], "O", t, bf16, T, qc)
+    _check(lib().ttl_packed_window_attn_fwd(t, T, n_q, n_kv, d, bounds - 1, window, sinks, cu,
+                                            d ** -0.5 if scale is None else scale, q, ldq, k, ldk, v, ldv, o, ldo,
+                                            _ptrs(out["lse"], "lse", t, torch.float32, (nql, T)), *_space(out["ws"]),
+                                            _queue(Q[0], stream)))
+    return out
+
+
+def packed_window_attn_bwd_buffers(t, T, n_q, n_kv, d, batch, window, sinks=0, device="cuda"):
+    """Gradient and workspace buffers of packed_window_attn_bwd."""
+    qc, kc = n_q // t * d, n_kv // t * d
+    e = dict(device=device, dtype=torch.bfloat16)
+    ws = _window_size(lib().ttl_packed_window_attn_bwd_workspace_size, t, T, n_q, n_kv, d, batch, window, sinks)
+    return {"dQ": [torch.empty(T, qc, **e) for _ in range(t)], "dK": [torch.empty(T, kc, **e) for _ in range(t)],
+            "dV": [torch.empty(T, kc, **e) for _ in range(t)], "ws": torch.empty(ws, dtype=torch.uint8, device=device)}
+
+
+def packed_window_attn_bwd(dO, Q, K, V, fwd, cu_seqlens, *, window, sinks=0, n_q, n_kv, d, scale=None, out=None,
+                           stream=None):
+    """Backward of packed_window_attn_fwd (``fwd`` holds its O and lse).  Returns dict dQ, dK, dV (lists); the buffers
+    of ``out`` may be column ranges of one fused gradient."""
+    t = len(Q)
+    T = Q[0].shape[0]
+    nql = n_q // t
+    qc, kc = nql * d, n_kv // t * d
+    bf16 = torch.bfloat16
+    do, lddo = _rows(dO, "dO", t, bf16, T, qc)
+    q, ldq = _rows(Q, "Q", t, bf16, T, qc)
+    k, ldk = _rows(K, "K", t, bf16, T, kc)
+    v, ldv = _rows(V, "V", t, bf16, T, kc)
+    o, ldo = _rows(fwd["O"], "O", t, bf16, T, qc)
+    bounds = cu_seqlens.numel()
+    cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (bounds,))
+    if out is None:
+        with _made_on(stream):
+            out = packed_window_attn_bwd_buffers(t, T, n_q, n_kv, d, bounds - 1, window, sinks, Q[0].device)
+    dq, lddq = _rows(out["dQ"], "dQ", t, bf16, T, qc)
+    dk, lddk = _rows(out["dK"], "dK", t, bf16, T, kc)
+    dv, lddv = _rows(out["dV"], "dV", t, bf16, T, kc)
+    _check(lib().ttl_packed_window_attn_bwd(t, T, n_q, n_kv, d, bounds - 1, window, sinks, cu,
+                                            d ** -0.5 if scale is None else scale, do, lddo, q, ldq, k, ldk, v, ldv, o, ldo,
+                                            _ptrs(fwd["lse"], "lse", t, torch.float32, (nql, T)), dq, lddq, dk, lddk,
+                                            dv, lddv, *_space(out["ws"]), _queue(Q[0], stream)))
     return out
 
 

@@ -11,6 +11,11 @@
 //   D_i = do_i . o_i,  ds_j = p_j (do_i . v_j - D_i)
 //   dq_i = scale sum_j ds_j k_j,  dk_j = scale sum_{c, i} ds_j q_i,  dv_j = sum_{c, i} p_j do_i
 // A token of no document has o = 0, lse = -inf and zero gradients.
+//
+// With a window the sums run over max(lo, i - window + 1) <= j <= i and lo <= j < lo + sinks (j <= i) alone.  The window
+// is a second instantiation of the same kernels: a query tile meets two ranges of key tiles, its window's and its
+// document's sinks; a key tile one range of query tiles, which ends a window behind it, or at its document's end
+// if it holds sinks.
 
 #include "operands.h"
 #include "packed_attn.cuh"
@@ -73,13 +78,13 @@ size_t fwd_list_bytes(int64_t T) { return round256(static_cast<size_t>(tiles_of(
 struct BwdWs {
   size_t q_list, kv_list, head, join, part, redo, total;   // offsets after D
 };
-BwdWs bwd_ws(int64_t T, int n_q, int n_kv, int d) {
+BwdWs bwd_ws(int64_t T, int n_q, int n_kv, int d, int sinks) {
   const int64_t tiles = tiles_of(T);
   const int grp = n_q / n_kv;
   // A cut leaves at most 2 steps / most parts of a tile and most >= all steps / kSplitItems: at most
   // 2 kSplitItems parts in all; and no part is shorter than kSplitSteps / 2.
   int64_t slots = 0;
-  if (pack_split(tiles, n_kv, grp)) {
+  if (pack_split(tiles, n_kv, grp, sinks)) {
     slots = 2 * kSplitItems / n_kv + 1;
     const int64_t most = tiles * (tiles * grp / kSplitSteps + 1);
     if (slots > most) slots = most;
@@ -102,28 +107,31 @@ Operand mats(const char* name, const ttl_bf16* const* at, int t, int64_t T, int6
 const __nv_bfloat16* bf(const ttl_bf16* p) { return reinterpret_cast<const __nv_bfloat16*>(p); }
 __nv_bfloat16* bf(ttl_bf16* p) { return reinterpret_cast<__nv_bfloat16*>(p); }
 
-}  // namespace
-}  // namespace ttl
+// Which keys a query sees beside the rule of documents: the last `window` up to itself, and the document's first
+// `sinks`; window 0: all.
+struct View {
+  int window, sinks;
+  int64_t asked_window, asked_sinks;           // as given; asked_window < 0: no window was asked for
+  static View all() { return View{0, 0, -1, 0}; }
+  static View of(int64_t window, int64_t sinks) { return View{0, 0, window < 0 ? 0 : window, sinks}; }
+  int check(int64_t T, const char* name) {
+    if (asked_window < 0) return TTL_OK;
+    if (asked_window < 1) return set_error(TTL_ERR_ARG, "%s: window must be at least 1", name);
+    if (asked_sinks < 0) return set_error(TTL_ERR_ARG, "%s: sinks must not be negative", name);
+    // No document is long enough to hide a key: the kernels without a window.  (Both are below T, 2^28, from here.)
+    if (asked_window >= T || asked_sinks >= T - asked_window) return TTL_OK;
+    window = static_cast<int>(asked_window);
+    sinks = static_cast<int>(asked_sinks);
+    return TTL_OK;
+  }
+};
 
-using namespace ttl;
-
-extern "C" size_t ttl_packed_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
-  if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_fwd_workspace_size")) return 0;
-  return fwd_list_bytes(T) + redo_bytes(T, n_q);
-}
-
-extern "C" size_t ttl_packed_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
-  if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_bwd_workspace_size")) return 0;
-  return bwd_ws(T, n_q, n_kv, d).total;
-}
-
-extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
-                                   float scale, const ttl_bf16* const* Q, int64_t ldq, const ttl_bf16* const* K,
-                                   int64_t ldk, const ttl_bf16* const* V, int64_t ldv, ttl_bf16* const* O, int64_t ldo,
-                                   float* const* lse, void* ws, size_t ws_bytes, void* stream) {
-  const char* name = "ttl_packed_attn_fwd";
+int attn_fwd(const char* name, View view, int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
+             float scale, const ttl_bf16* const* Q, int64_t ldq, const ttl_bf16* const* K, int64_t ldk,
+             const ttl_bf16* const* V, int64_t ldv, ttl_bf16* const* O, int64_t ldo, float* const* lse, void* ws,
+             size_t ws_bytes, void* stream) {
   int rc = check_shape(t, T, n_q, n_kv, d, batch, name);
-  if (rc) return rc;
+  if (rc || (rc = view.check(T, name))) return rc;
   if ((rc = check_cu(cu_seqlens, scale, name))) return rc;
   const int64_t qc = static_cast<int64_t>(n_q / t) * d, kc = static_cast<int64_t>(n_kv / t) * d;
   using CP = const void* const*;
@@ -133,7 +141,7 @@ extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, i
       (rc = check_mats(reinterpret_cast<CP>(V), t, kc, ldv, "V", name)) ||
       (rc = check_mats(reinterpret_cast<CP>(O), t, qc, ldo, "O", name)) || (rc = check_lse(lse, t, name)))
     return rc;
-  const size_t need = ttl_packed_attn_fwd_workspace_size(t, T, n_q, n_kv, d, batch);
+  const size_t need = fwd_list_bytes(T) + redo_bytes(T, n_q);
   if (!ws || ws_bytes < need)
     return set_error(TTL_ERR_ARG, "%s: workspace of %zu bytes needed, %zu given", name, need, ws_bytes);
   if (!aligned16(ws)) return set_error(TTL_ERR_ALIGN, "%s: workspace not 16-byte aligned", name);
@@ -159,20 +167,19 @@ extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, i
   A.t = t; A.nql = n_q / t; A.nkvl = n_kv / t; A.grp = n_q / n_kv; A.T = T;
   A.ldq = ldq; A.ldk = ldk; A.ldv = ldv; A.ldo = ldo;
   A.cu = cu_seqlens; A.batch = batch; A.scale = scale;
+  A.window = view.window; A.sinks = view.sinks;
   A.redo = reinterpret_cast<RedoEntry*>(static_cast<char*>(ws) + fwd_list_bytes(T));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return pack_attn_fwd_launch(A, d, ws, s);
 }
 
-extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
-                                   float scale, const ttl_bf16* const* dO, int64_t lddo, const ttl_bf16* const* Q,
-                                   int64_t ldq, const ttl_bf16* const* K, int64_t ldk, const ttl_bf16* const* V,
-                                   int64_t ldv, const ttl_bf16* const* O, int64_t ldo, const float* const* lse,
-                                   ttl_bf16* const* dQ, int64_t lddq, ttl_bf16* const* dK, int64_t lddk,
-                                   ttl_bf16* const* dV, int64_t lddv, void* ws, size_t ws_bytes, void* stream) {
-  const char* name = "ttl_packed_attn_bwd";
+int attn_bwd(const char* name, View view, int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
+             float scale, const ttl_bf16* const* dO, int64_t lddo, const ttl_bf16* const* Q, int64_t ldq,
+             const ttl_bf16* const* K, int64_t ldk, const ttl_bf16* const* V, int64_t ldv, const ttl_bf16* const* O,
+             int64_t ldo, const float* const* lse, ttl_bf16* const* dQ, int64_t lddq, ttl_bf16* const* dK, int64_t lddk,
+             ttl_bf16* const* dV, int64_t lddv, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_shape(t, T, n_q, n_kv, d, batch, name);
-  if (rc) return rc;
+  if (rc || (rc = view.check(T, name))) return rc;
   if ((rc = check_cu(cu_seqlens, scale, name))) return rc;
   const int64_t qc = static_cast<int64_t>(n_q / t) * d, kc = static_cast<int64_t>(n_kv / t) * d;
   using CP = const void* const*;
@@ -186,7 +193,8 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
       (rc = check_mats(reinterpret_cast<CP>(dK), t, kc, lddk, "dK", name)) ||
       (rc = check_mats(reinterpret_cast<CP>(dV), t, kc, lddv, "dV", name)))
     return rc;
-  const size_t need = ttl_packed_attn_bwd_workspace_size(t, T, n_q, n_kv, d, batch);
+  const BwdWs w = bwd_ws(T, n_q, n_kv, d, view.sinks);
+  const size_t need = w.total;
   if (!ws || ws_bytes < need)
     return set_error(TTL_ERR_ARG, "%s: workspace of %zu bytes needed, %zu given", name, need, ws_bytes);
   if (!aligned16(ws)) return set_error(TTL_ERR_ALIGN, "%s: workspace not 16-byte aligned", name);
@@ -219,15 +227,15 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
   A.ldq = ldq; A.ldk = ldk; A.ldv = ldv; A.ldo = ldo;
   A.lddo = lddo; A.lddq = lddq; A.lddk = lddk; A.lddv = lddv;
   A.cu = cu_seqlens; A.batch = batch; A.scale = scale;
+  A.window = view.window; A.sinks = view.sinks;
   A.D = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // Work lists where there are more items than SMs, or key tiles long enough to be cut; a batch below that
   // starts every item at once.
   const int64_t tiles = tiles_of(T);
-  const bool split = pack_split(tiles, n_kv, A.grp);
+  const bool split = pack_split(tiles, n_kv, A.grp, view.sinks);
   const bool listed = split || tiles * n_q > num_sms();
   PackPlan plan = {};
-  const BwdWs w = bwd_ws(T, n_q, n_kv, d);
   char* base = reinterpret_cast<char*>(A.D);
   A.redo = reinterpret_cast<RedoEntry*>(base + w.redo);
   if (listed) {
@@ -260,4 +268,68 @@ extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, i
       (rc = pack_attn_dkv_launch(A, maps, d, s)))
     return rc;
   return split ? pack_attn_join_launch(A, d, s) : TTL_OK;
+}
+
+}  // namespace
+}  // namespace ttl
+
+using namespace ttl;
+
+extern "C" size_t ttl_packed_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
+  if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_fwd_workspace_size")) return 0;
+  return fwd_list_bytes(T) + redo_bytes(T, n_q);
+}
+
+extern "C" size_t ttl_packed_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
+  if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_bwd_workspace_size")) return 0;
+  return bwd_ws(T, n_q, n_kv, d, 0).total;
+}
+
+extern "C" size_t ttl_packed_window_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch,
+                                                            int64_t window, int64_t sinks) {
+  const char* name = "ttl_packed_window_attn_fwd_workspace_size";
+  if (check_shape(t, T, n_q, n_kv, d, batch, name) || View::of(window, sinks).check(T, name)) return 0;
+  return fwd_list_bytes(T) + redo_bytes(T, n_q);
+}
+
+extern "C" size_t ttl_packed_window_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch,
+                                                            int64_t window, int64_t sinks) {
+  const char* name = "ttl_packed_window_attn_bwd_workspace_size";
+  View view = View::of(window, sinks);
+  if (check_shape(t, T, n_q, n_kv, d, batch, name) || view.check(T, name)) return 0;
+  return bwd_ws(T, n_q, n_kv, d, view.sinks).total;
+}
+
+extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
+             float scale, const ttl_bf16* const* Q, int64_t ldq, const ttl_bf16* const* K, int64_t ldk,
+             const ttl_bf16* const* V, int64_t ldv, ttl_bf16* const* O, int64_t ldo, float* const* lse, void* ws,
+             size_t ws_bytes, void* stream) {
+  return attn_fwd("ttl_packed_attn_fwd", View::all(), t, T, n_q, n_kv, d, batch, cu_seqlens, scale, Q, ldq, K, ldk, V, ldv, O, ldo, lse, ws,
+                  ws_bytes, stream);
+}
+
+extern "C" int ttl_packed_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,
+             float scale, const ttl_bf16* const* dO, int64_t lddo, const ttl_bf16* const* Q, int64_t ldq,
+             const ttl_bf16* const* K, int64_t ldk, const ttl_bf16* const* V, int64_t ldv, const ttl_bf16* const* O,
+             int64_t ldo, const float* const* lse, ttl_bf16* const* dQ, int64_t lddq, ttl_bf16* const* dK, int64_t lddk,
+             ttl_bf16* const* dV, int64_t lddv, void* ws, size_t ws_bytes, void* stream) {
+  return attn_bwd("ttl_packed_attn_bwd", View::all(), t, T, n_q, n_kv, d, batch, cu_seqlens, scale, dO, lddo, Q, ldq, K, ldk, V, ldv, O, ldo,
+                  lse, dQ, lddq, dK, lddk, dV, lddv, ws, ws_bytes, stream);
+}
+
+extern "C" int ttl_packed_window_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, int64_t window, int64_t sinks, const int32_t* cu_seqlens,
+             float scale, const ttl_bf16* const* Q, int64_t ldq, const ttl_bf16* const* K, int64_t ldk,
+             const ttl_bf16* const* V, int64_t ldv, ttl_bf16* const* O, int64_t ldo, float* const* lse, void* ws,
+             size_t ws_bytes, void* stream) {
+  return attn_fwd("ttl_packed_window_attn_fwd", View::of(window, sinks), t, T, n_q, n_kv, d, batch, cu_seqlens, scale, Q, ldq, K, ldk, V, ldv, O, ldo, lse, ws,
+                  ws_bytes, stream);
+}
+
+extern "C" int ttl_packed_window_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, int64_t window, int64_t sinks, const int32_t* cu_seqlens,
+             float scale, const ttl_bf16* const* dO, int64_t lddo, const ttl_bf16* const* Q, int64_t ldq,
+             const ttl_bf16* const* K, int64_t ldk, const ttl_bf16* const* V, int64_t ldv, const ttl_bf16* const* O,
+             int64_t ldo, const float* const* lse, ttl_bf16* const* dQ, int64_t lddq, ttl_bf16* const* dK, int64_t lddk,
+             ttl_bf16* const* dV, int64_t lddv, void* ws, size_t ws_bytes, void* stream) {
+  return attn_bwd("ttl_packed_window_attn_bwd", View::of(window, sinks), t, T, n_q, n_kv, d, batch, cu_seqlens, scale, dO, lddo, Q, ldq, K, ldk, V, ldv, O, ldo,
+                  lse, dQ, lddq, dK, lddk, dV, lddv, ws, ws_bytes, stream);
 }

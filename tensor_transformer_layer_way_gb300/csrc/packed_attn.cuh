@@ -1,5 +1,6 @@
 // Packed causal attention: what its kernels share.  A pack is one axis of T tokens; document b holds
-// tokens [cu[b], cu[b+1]) and a query sees the keys of its own document up to itself.
+// tokens [cu[b], cu[b+1]) and a query sees the keys of its own document up to itself, or with a window the last
+// `window` of these and the document's first `sinks`.
 #pragma once
 
 #include <cmath>
@@ -33,6 +34,7 @@ struct PackArgs {
   const int32_t* cu;           // [batch + 1]
   int batch;
   float scale;
+  int window, sinks;           // window 0: none
   float* D;                    // backward: rowsum(dO o), [t][n_q/t][T]
   int* status;
   // Work lists, heaviest first, written by the plan kernel (null: the kernels look their items up)
@@ -47,7 +49,8 @@ struct PackArgs {
 };
 
 // A query unit: {unit, first key tile of its first token tile, of its second, 0}, -1 for a token tile without
-// keys; a tile's last key tile is its own.
+// keys; a tile's last key tile is its own.  With a window, in place of a first key tile: the first token of the
+// document that the token tile begins in.
 // A key unit: {key tile, last query tile, first step, end step} {slot of its partial sums or -1, 0, 0, 0}.
 
 // The operands that both kernels of the backward pass load, in boxes of 64 x 128, made once for both.
@@ -73,9 +76,15 @@ constexpr int kSplitSteps = 8;     // and no shorter than this
 int pack_attn_plan_launch(const PackArgs& A, const PackPlan& plan, int d, cudaStream_t stream);
 int pack_attn_join_launch(const PackArgs& A, int d, cudaStream_t stream);
 // Whether key tiles may be cut: few items, and long enough ones.  With eight items or more for each SM the
-// list's order alone evens the SMs out.
-inline bool pack_split(int64_t tiles, int lanes, int grp) {
-  return tiles * lanes < 8 * 152 && tiles * grp > 2 * kSplitSteps;
+// list's order alone evens the SMs out, unless some keys are seen from everywhere and the others from a window.
+inline bool pack_split(int64_t tiles, int lanes, int grp, int sinks) {
+  return (tiles * lanes < 8 * 152 || sinks > 0) && tiles * grp > 2 * kSplitSteps;
+}
+// Pairs of a query and a key that it sees, in one document of T tokens (the lengths are on the device).
+inline double pack_pairs(const PackArgs& A) {
+  const double T = static_cast<double>(A.T), W = A.window ? A.window : T;
+  if (W >= T) return T * (T + 1) / 2;
+  return W * (W + 1) / 2 + (T - W) * (W + (A.sinks < T - W ? A.sinks : T - W));
 }
 
 // Launches of the tensor-core kernels (arguments are checked; A.s holds every pointer they need).
@@ -85,10 +94,64 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stre
 int pack_attn_dq_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStream_t stream);    // dQ, after D
 int pack_attn_dkv_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStream_t stream);   // dK and dV, after D
 
+template <int D>
+using Width = std::integral_constant<int, D>;   // a head's width, as an argument
+
 constexpr int kTile = 128;       // tokens per query or key tile
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// ---- windows
+// With a window (W) the query at token i of a document that begins at lo sees the keys [near, i] and, before these, the
+// sinks [lo, sink), sink <= near.  (window and sinks are at most T, below 2^28: no sum of theirs leaves 32 bits.)
+__device__ __forceinline__ int near_key(const PackArgs& A, int lo, int i) { return max(lo, i - A.window + 1); }
+__device__ __forceinline__ int sink_end(const PackArgs& A, int lo, int near) { return min(lo + A.sinks, near); }
+
+// The key tiles of the query tile at q0 whose first row's document begins at token lo: [beg, gap) with its sinks and
+// [wbeg, q0 / kTile]; other documents begin in the tile itself.  Neighbours are one range: gap = wbeg then.
+struct TileRange {
+  int beg, gap, wbeg;
+};
+__device__ __forceinline__ TileRange key_tiles(const PackArgs& A, int q0, int lo) {
+  TileRange r;
+  r.wbeg = near_key(A, lo, q0) / kTile;
+  r.beg = A.sinks > 0 ? lo / kTile : r.wbeg;
+  r.gap = A.sinks > 0 ? min((lo + A.sinks - 1) / kTile + 1, r.wbeg) : r.wbeg;
+  return r;
+}
+// The part of a work item that only windows have: key tiles [.., gap) and [wbeg, ..).
+template <bool W>
+struct Gap {};
+template <>
+struct Gap<true> {
+  int gap, wbeg;
+};
+// The item's key tile behind tile j.
+template <bool W>
+__device__ __forceinline__ int tile_after(const Gap<W>& it, int j) {
+  if constexpr (W) {
+    if (j + 1 == it.gap) return it.wbeg;
+  }
+  return j + 1;
+}
+
+// One past the last query that sees the key at token j of the document `doc`.
+template <bool W>
+__device__ __forceinline__ int query_end(const PackArgs& A, const DocRange& doc, int j) {
+  if constexpr (W) {
+    if (j - doc.lo >= A.sinks) return min(doc.hi, j + A.window);
+  }
+  return doc.hi;
+}
+// The last query tile that sees a key of tile k0 whose last token, v1 - 1, is of the document `doc`: documents that
+// end in the tile are seen from there.
+template <bool W>
+__device__ __forceinline__ int last_query_tile(const PackArgs& A, const DocRange& doc, int k0, int v1) {
+  // with a window: from the tile's last token, unless the document's sinks reach into the tile
+  const int hi = query_end<W>(A, doc, W && max(k0, doc.lo) - doc.lo < A.sinks ? doc.lo : v1 - 1);
+  return (hi > v1 ? hi - 1 : v1 - 1) / kTile;
+}
 
 // doc_of for one token of a document (0 <= tok < T, cu[0] <= tok < cu[batch]), by a whole warp: 32 bounds at a time.
 __device__ __forceinline__ DocRange doc_of_warp(const int32_t* cu, int batch, int T, int tok) {
@@ -374,8 +437,27 @@ __device__ __forceinline__ void add_rows(RowVec<D> (&acc)[R], const float (&w)[R
   }
 }
 
+// What rows see in turn: part 0 the keys lo..i, or with a window part 0 the sinks and part 1 the window.  Row r sees
+// [from[r], to[r]); [begin, end) holds them all.
+template <bool W, int R>
+__device__ __forceinline__ void row_keys(const PackArgs& A, int part, const int (&i)[R], const int (&lo)[R], int (&from)[R],
+                                         int (&to)[R], int& begin, int& end) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    from[r] = lo[r];
+    to[r] = i[r] + 1;
+    if constexpr (W) {
+      const int near = near_key(A, lo[r], i[r]);
+      if (part == 0) to[r] = sink_end(A, lo[r], near);
+      else from[r] = near;
+    }
+    begin = r ? min(begin, from[r]) : from[r];
+    end = r ? max(end, to[r]) : to[r];
+  }
+}
+
 // o and lse of query head c at tokens i[0..n), whose documents begin at lo: running maximum m and sum l, in base 2.
-template <int D, int R>
+template <int D, bool W, int R>
 __device__ __forceinline__ void fwd_rows(const PackArgs& A, const PackShard& S, int c, const int (&i)[R], const int (&lo)[R],
                                          int n, int lane) {
   const int g = c / A.grp;
@@ -383,39 +465,41 @@ __device__ __forceinline__ void fwd_rows(const PackArgs& A, const PackShard& S, 
   RowVec<D> acc[R];
   float m[R], l[R];                                // (l: this lane's part)
   const __nv_bfloat16* q[R];
-  int begin = lo[0], last = i[0];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     acc[r] = row_zero<D>();
     m[r] = -INFINITY;
     l[r] = 0.0f;
     q[r] = S.q + i[r] * A.ldq + c * D;
-    begin = min(begin, lo[r]);
-    last = max(last, i[r]);
   }
 #pragma unroll 1
-  for (int j0 = begin; j0 <= last; j0 += 32) {
-    const int j = j0 + lane;
-    float s[R];
-    int from[R], to[R];
-    lane_dots<D, R>(s, q, S.k + min(j, last) * A.ldk + g * D);
+  for (int part = 0; part < (W ? 2 : 1); ++part) {
+    int first[R], past[R], begin, end;
+    row_keys<W>(A, part, i, lo, first, past, begin, end);
+#pragma unroll 1
+    for (int j0 = begin; j0 < end; j0 += 32) {
+      const int j = j0 + lane;
+      float s[R];
+      int from[R], to[R];
+      lane_dots<D, R>(s, q, S.k + min(j, end - 1) * A.ldk + g * D);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      s[r] = j >= lo[r] && j <= i[r] ? s[r] * k2 : -INFINITY;
-      float mn = fmaxf(m[r], s[r]);
+      for (int r = 0; r < R; ++r) {
+        s[r] = j >= first[r] && j < past[r] ? s[r] * k2 : -INFINITY;
+        float mn = fmaxf(m[r], s[r]);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      const float base = mn == -INFINITY ? 0.0f : mn;
-      const float f = exp2f(m[r] - base);
-      s[r] = exp2f(s[r] - base);
-      l[r] = l[r] * f + s[r];
+        for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        const float base = mn == -INFINITY ? 0.0f : mn;
+        const float f = exp2f(m[r] - base);
+        s[r] = exp2f(s[r] - base);
+        l[r] = l[r] * f + s[r];
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[r].x[e] *= f;
-      m[r] = mn;
-      from[r] = lo[r] - j0;
-      to[r] = i[r] + 1 - j0;
+        for (int e = 0; e < D / 32; ++e) acc[r].x[e] *= f;
+        m[r] = mn;
+        from[r] = first[r] - j0;
+        to[r] = past[r] - j0;
+      }
+      add_rows<D, R>(acc, s, from, to, S.v + j0 * A.ldv + g * D, A.ldv, min(32, end - j0), lane);
     }
-    add_rows<D, R>(acc, s, from, to, S.v + j0 * A.ldv + g * D, A.ldv, min(32, last + 1 - j0), lane);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -432,7 +516,7 @@ __device__ __forceinline__ void fwd_rows(const PackArgs& A, const PackShard& S, 
 }
 
 // dq of query head c at tokens i[0..n).
-template <int D, int R>
+template <int D, bool W, int R>
 __device__ __forceinline__ void dq_rows(const PackArgs& A, const PackShard& S, int shard, int c, const int (&i)[R],
                                         const int (&lo)[R], int n, int lane) {
   const int g = c / A.grp;
@@ -441,7 +525,6 @@ __device__ __forceinline__ void dq_rows(const PackArgs& A, const PackShard& S, i
   float lse2[R], Di[R];
   const __nv_bfloat16* q[R];
   const __nv_bfloat16* go[R];
-  int begin = lo[0], last = i[0];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     acc[r] = row_zero<D>();
@@ -449,30 +532,33 @@ __device__ __forceinline__ void dq_rows(const PackArgs& A, const PackShard& S, i
     go[r] = S.dO + i[r] * A.lddo + c * D;
     lse2[r] = S.lse[static_cast<int64_t>(c) * A.T + i[r]] * kLog2e;
     Di[r] = A.D[(static_cast<int64_t>(shard) * A.nql + c) * A.T + i[r]];
-    begin = min(begin, lo[r]);
-    last = max(last, i[r]);
   }
 #pragma unroll 1
-  for (int j0 = begin; j0 <= last; j0 += 32) {
-    const int at = min(j0 + lane, last);
-    float s[R], dp[R];
-    int from[R], to[R];
-    lane_dots<D, R>(s, q, S.k + at * A.ldk + g * D);
-    lane_dots<D, R>(dp, go, S.v + at * A.ldv + g * D);
+  for (int part = 0; part < (W ? 2 : 1); ++part) {
+    int first[R], past[R], begin, end;
+    row_keys<W>(A, part, i, lo, first, past, begin, end);
+#pragma unroll 1
+    for (int j0 = begin; j0 < end; j0 += 32) {
+      const int at = min(j0 + lane, end - 1);
+      float s[R], dp[R];
+      int from[R], to[R];
+      lane_dots<D, R>(s, q, S.k + at * A.ldk + g * D);
+      lane_dots<D, R>(dp, go, S.v + at * A.ldv + g * D);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      s[r] = exp2f(s[r] * k2 - lse2[r]) * (dp[r] - Di[r]) * A.scale;
-      from[r] = lo[r] - j0;
-      to[r] = i[r] + 1 - j0;
+      for (int r = 0; r < R; ++r) {
+        s[r] = exp2f(s[r] * k2 - lse2[r]) * (dp[r] - Di[r]) * A.scale;
+        from[r] = first[r] - j0;
+        to[r] = past[r] - j0;
+      }
+      add_rows<D, R>(acc, s, from, to, S.k + j0 * A.ldk + g * D, A.ldk, min(32, end - j0), lane);
     }
-    add_rows<D, R>(acc, s, from, to, S.k + j0 * A.ldk + g * D, A.ldk, min(32, last + 1 - j0), lane);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r)
     if (r < n) row_store<D>(S.dq + i[r] * A.lddq + c * D, acc[r], lane);
 }
 
-// dk (want_k) or dv of KV head g at tokens j[0..n), whose documents end at hi, summed over the group's query heads.
+// dk (want_k) or dv of KV head g at tokens j[0..n), seen by the queries j to hi - 1, summed over the group's query heads.
 template <int D, int R>
 __device__ __forceinline__ void dkv_rows(const PackArgs& A, const PackShard& S, int shard, int g, const int (&j)[R],
                                          const int (&hi)[R], int n, bool want_k, int lane) {

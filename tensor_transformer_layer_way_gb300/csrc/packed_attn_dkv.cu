@@ -72,6 +72,7 @@ __device__ __forceinline__ KvItem listed_item(const KvParams& P, int at) {
 }
 
 // A block's first item (of `total`), found by a whole warp.
+template <bool W>
 __device__ __forceinline__ KvItem first_item(const KvParams& P, int total) {
   const PackArgs& A = P.a;
   const int at = static_cast<int>(blockIdx.x), ln = at % P.lanes, tile = at / P.lanes;
@@ -85,8 +86,7 @@ __device__ __forceinline__ KvItem first_item(const KvParams& P, int total) {
     int v1 = it.k0 + kTile < last ? it.k0 + kTile : last;
     v1 = v1 < T ? v1 : T;
     if (v0 < v1) {
-      const int hi = doc_of_warp(A.cu, A.batch, T, v1 - 1).hi;   // > v1 - 1
-      it.qt_last = (hi > v1 ? hi - 1 : v1 - 1) / kTile;
+      it.qt_last = last_query_tile<W>(A, doc_of_warp(A.cu, A.batch, T, v1 - 1), it.k0, v1);
       it.steps = (it.qt_last - tile + 1) * A.grp;
     }
   }
@@ -94,8 +94,8 @@ __device__ __forceinline__ KvItem first_item(const KvParams& P, int total) {
 }
 
 // Those of the rows j of dK (want_k) or dV, whose sums are not finite, that masked places may have made so, again.
-// `edges` are looked at once for the rows of a tile.
-template <int D, int R>
+// `edges` are looked at once for the rows of a tile.  (With a window without that look, as in the forward pass.)
+template <int D, bool W, int R>
 __device__ __noinline__ void redo_keys(const PackArgs& A, int shard, int g, int (&j)[R], bool want_k, KeyEdges& edges,
                                           bool& looked, int lane) {
   const PackShard& S = A.s[shard];
@@ -103,8 +103,8 @@ __device__ __noinline__ void redo_keys(const PackArgs& A, int shard, int g, int 
   uint32_t again = 0;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int hi = doc_of(A.cu, A.batch, T, j[r]).hi;
-    bool met = hi - j[r] < kRedoShort;
+    const int hi = query_end<W>(A, doc_of(A.cu, A.batch, T, j[r]), j[r]);
+    bool met = W || hi - j[r] < kRedoShort;
     if (!met) {
       if (!looked) edges.look<D>(A, S, g, row0, hi, want_k, lane);
       looked = true;
@@ -116,12 +116,12 @@ __device__ __noinline__ void redo_keys(const PackArgs& A, int shard, int g, int 
   const int m = redo_take(again, row0, j);
   int hi[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) hi[r] = doc_of(A.cu, A.batch, T, j[r]).hi;
+  for (int r = 0; r < R; ++r) hi[r] = query_end<W>(A, doc_of(A.cu, A.batch, T, j[r]), j[r]);
   dkv_rows<D>(A, S, shard, g, j, hi, m, want_k, lane);
 }
 
 // The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
-template <int D>
+template <int D, bool W>
 __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, int warps, int lane) {
   const uint32_t slots = redo_slots(A.t * A.nkvl * 2, A.T);
   int turn = 0;
@@ -134,13 +134,13 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
     for (uint32_t rows = e.rows; rows;) {
       int j[kRedoRows];
       redo_take(rows, at.row0, j);
-      if (turn++ % warps == w) redo_keys<D>(A, kv / A.nkvl, kv % A.nkvl, j, (at.head & 1) == 0, edges, looked, lane);
+      if (turn++ % warps == w) redo_keys<D, W>(A, kv / A.nkvl, kv % A.nkvl, j, (at.head & 1) == 0, edges, looked, lane);
     }
     slot = e.next;
   }
 }
 
-template <int D>
+template <int D, bool W>
 __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_constant__ KvParams P) {
   using C = KvCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int nk = 0, nv = 0, pos = 0;   // loads started: K, V, ring places
-    KvItem it = first_item(P, total);
+    KvItem it = first_item<W>(P, total);
     for (int n = 0; lane == 0 && ok && it.shard >= 0; ++n) {
       KvItem coming = {};
       coming.shard = -1;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       for (int kk = 0; kk < kTile / 16; ++kk)
         umma_bf16_ts(dst, acol + (kk >> 1) * 32 + (kk & 1) * 8, desc_advance(bd, kk * 2048), idesc_acc, kk ? 1u : more);
     };
-    KvItem it = first_item(P, total);
+    KvItem it = first_item<W>(P, total);
     for (int n = 0; queue.next(n, it) && it.shard >= 0; ++n) {
       if (it.steps == 0) continue;
       wait(k_full, ni);
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // ------------------------------------------------------------------ lse and D of each step's queries
     bool ok = true;
     int pos = 0;
-    KvItem it = first_item(P, total);
+    KvItem it = first_item<W>(P, total);
     for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       const float* lse = A.s[it.shard].lse;
       const float* Dr = A.D + static_cast<int64_t>(it.shard) * A.nql * A.T;
@@ -414,14 +414,15 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   } else if (warp == 3) {
     // ------------------------------------------------------------------ last queries of the coming item's keys
     bool ok = true;
-    KvItem it = first_item(P, total);
+    KvItem it = first_item<W>(P, total);
     for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       int hi[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         DocRange doc{0, 0};
         if (it.steps > 0) doc = doc_of(A.cu, A.batch, static_cast<int>(A.T), it.k0 + u * 32 + lane);
-        hi[u] = doc.hi > doc.lo ? doc.hi - 1 : -1;   // a token of no document is seen by none
+        // a token of no document is seen by none
+        hi[u] = doc.hi > doc.lo ? query_end<W>(A, doc, it.k0 + u * 32 + lane) - 1 : -1;
       }
       ok = wait_on(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     bool ok = true;
     int pos = 0, ni = 0;
     uint32_t met = 0;
-    KvItem it = first_item(P, total);
+    KvItem it = first_item<W>(P, total);
     for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       const PackShard& S = A.s[it.shard];
       const int key = it.k0 + r;
@@ -598,12 +599,12 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (warp >= 4 && redo_list->count > 0 && !*abort_flag) redo_rows<D>(A, *redo_list, warp - 4, kKvWarps, lane);
+  if (warp >= 4 && redo_list->count > 0 && !*abort_flag) redo_rows<D, W>(A, *redo_list, warp - 4, kKvWarps, lane);
 }
 
 // Adds up the parts of the key tiles that several items shared, in the order of their steps: one warp per row
 // of dK or dV, eight rows of a tile per block.
-template <int D>
+template <int D, bool W>
 __global__ void __launch_bounds__(256, 4) pack_join_kernel(const __grid_constant__ PackArgs A) {
   __shared__ uint32_t redo[2];       // rows of the eight whose sums are not finite; of the eight before, spent
   await_previous();
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(256, 4) pack_join_kernel(const __grid_constant
       int j[kRedoRows];
       KeyEdges edges;
       bool looked = false;
-      if (redo_take(again, key0, j) > 0) redo_keys<D>(A, shard, g, j, half == 0, edges, looked, lane);
+      if (redo_take(again, key0, j) > 0) redo_keys<D, W>(A, shard, g, j, half == 0, edges, looked, lane);
     }
     __syncthreads();
   }
@@ -657,9 +658,9 @@ __global__ void __launch_bounds__(256, 4) pack_join_kernel(const __grid_constant
 int pack_attn_join_launch(const PackArgs& A, int d, cudaStream_t stream) {
   TraceScope trace(stream, TTL_K_OTHER, 0.0, 0.0);
   const unsigned grid = static_cast<unsigned>(num_sms()) * 4;
-  if (d == 128)
-    return cuda_check(launch_after(pack_join_kernel<128>, dim3(grid), 256, 0, stream, A), "pack_join_kernel launch");
-  return cuda_check(launch_after(pack_join_kernel<64>, dim3(grid), 256, 0, stream, A), "pack_join_kernel launch");
+  auto run = [&](auto kernel) { return cuda_check(launch_after(kernel, dim3(grid), 256, 0, stream, A), "pack_join_kernel launch"); };
+  if (d == 128) return A.window ? run(pack_join_kernel<128, true>) : run(pack_join_kernel<128, false>);
+  return A.window ? run(pack_join_kernel<64, true>) : run(pack_join_kernel<64, false>);
 }
 
 int pack_attn_dkv_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStream_t stream) {
@@ -667,7 +668,6 @@ int pack_attn_dkv_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStr
   P.a = A;
   P.m = maps;
   const int64_t qc = static_cast<int64_t>(A.nql) * d, kc = static_cast<int64_t>(A.nkvl) * d;
-  int rc = TTL_OK;
   P.tiles = static_cast<int>((A.T + kTile - 1) / kTile);
   P.lanes = A.t * A.nkvl;
   P.timeout_ns = pack_wait_ns(static_cast<int64_t>(P.tiles) * A.grp);
@@ -675,18 +675,16 @@ int pack_attn_dkv_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStr
   if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many key tiles");
   const int sms = num_sms();
   const unsigned grid = static_cast<unsigned>(items < sms && !A.kv_list ? items : sms);
-  const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
-  TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * tri * d * A.nql * A.t, 2.0 * A.T * (2.0 * qc + 4.0 * kc) * A.t);
-  if (d == 128) {
-    if ((rc = allow_smem<pack_dkv_kernel<128>>(KvCfg<128>::SMEM, "cudaFuncSetAttribute(packed attention dK dV)")))
-      return rc;
-    rc = cuda_check(launch_after(pack_dkv_kernel<128>, dim3(grid), kKvThreads, KvCfg<128>::SMEM, stream, P), "pack_dkv_kernel launch");
-  } else {
-    if ((rc = allow_smem<pack_dkv_kernel<64>>(KvCfg<64>::SMEM, "cudaFuncSetAttribute(packed attention dK dV)")))
-      return rc;
-    rc = cuda_check(launch_after(pack_dkv_kernel<64>, dim3(grid), kKvThreads, KvCfg<64>::SMEM, stream, P), "pack_dkv_kernel launch");
-  }
-  return rc;
+  TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * pack_pairs(A) * d * A.nql * A.t, 2.0 * A.T * (2.0 * qc + 4.0 * kc) * A.t);
+  auto run = [&](auto width, auto window) {
+    constexpr int D = decltype(width)::value;
+    constexpr bool W = decltype(window)::value;
+    const int err = allow_smem<pack_dkv_kernel<D, W>>(KvCfg<D>::SMEM, "cudaFuncSetAttribute(packed attention dK dV)");
+    if (err) return err;
+    return cuda_check(launch_after(pack_dkv_kernel<D, W>, dim3(grid), kKvThreads, KvCfg<D>::SMEM, stream, P), "pack_dkv_kernel launch");
+  };
+  if (d == 128) return A.window ? run(Width<128>{}, std::true_type{}) : run(Width<128>{}, std::false_type{});
+  return A.window ? run(Width<64>{}, std::true_type{}) : run(Width<64>{}, std::false_type{});
 }
 
 }  // namespace ttl

@@ -35,11 +35,17 @@ struct DqParams {
   uint64_t timeout_ns;
 };
 
-struct DqItem {
+template <bool W>
+struct DqItem : Gap<W> {
   int shard, c, g, q0, jbeg, jend;
 };
+template <bool W>
+__device__ __forceinline__ int tiles_of(const DqItem<W>& it) {
+  if constexpr (W) return it.jend > it.jbeg ? it.gap - it.jbeg + it.jend - it.wbeg : 0;
+  else return it.jend - it.jbeg;
+}
 
-template <int D>
+template <int D, bool W>
 struct DqCfg {
   static constexpr int KB = D / 64;
   static constexpr int TILE = KB * kTile * 128;
@@ -48,34 +54,44 @@ struct DqCfg {
   static constexpr int OFF_V = OFF_K + kKSlots * TILE;
   static constexpr int OFF_X = OFF_V + kVSlots * TILE;   // of each row: -lse log2(e), D, first key
   static constexpr int OFF_BAR = OFF_X + 1536;
-  static constexpr int SMEM = OFF_BAR + 320 + kAhead * static_cast<int>(sizeof(DqItem)) + 1024;
+  static constexpr int SMEM = OFF_BAR + 320 + kAhead * static_cast<int>(sizeof(DqItem<W>)) + 1024;
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
 };
 
-// The item of index `at` whose query tile is `tile` and first key tile `first` (-1: none).
-__device__ __forceinline__ DqItem item_from(const DqParams& P, int at, int tile, int first) {
+// The item of index `at` whose query tile is `tile` and first key tile (with a window: first token of the document
+// that the tile begins in) `first` (-1: none).
+template <bool W>
+__device__ __forceinline__ DqItem<W> item_from(const DqParams& P, int at, int tile, int first) {
   const int ln = at % P.lanes;
-  DqItem it;
+  DqItem<W> it;
   it.shard = ln / P.a.nql;
   it.c = ln % P.a.nql;
   it.g = it.c / P.a.grp;
   it.q0 = tile * kTile;
   it.jbeg = first < 0 ? 0 : first;
   it.jend = first < 0 ? 0 : tile + 1;
+  if constexpr (W) {
+    const TileRange r = key_tiles(P.a, it.q0, it.jbeg);
+    it.jbeg = first < 0 ? 0 : r.beg;
+    it.gap = r.gap;
+    it.wbeg = r.wbeg;
+  }
   return it;
 }
 
 // The listed item of index `at`.
-__device__ __forceinline__ DqItem listed_item(const DqParams& P, int at) {
+template <bool W>
+__device__ __forceinline__ DqItem<W> listed_item(const DqParams& P, int at) {
   const int4 e = __ldg(P.a.q_list + at / P.lanes);
-  return item_from(P, at, e.x, e.y);
+  return item_from<W>(P, at, e.x, e.y);
 }
 
 // A block's first item, found by a whole warp.
-__device__ __forceinline__ DqItem first_item(const DqParams& P) {
+template <bool W>
+__device__ __forceinline__ DqItem<W> first_item(const DqParams& P) {
   const PackArgs& A = P.a;
   const int at = static_cast<int>(blockIdx.x);
-  if (A.q_list) return listed_item(P, at);
+  if (A.q_list) return listed_item<W>(P, at);
   const int tile = P.tiles - 1 - at / P.lanes, q0 = tile * kTile;
   int first_tile = -1;
   if (A.batch > 0) {
@@ -84,13 +100,14 @@ __device__ __forceinline__ DqItem first_item(const DqParams& P) {
     const int v0 = q0 > first ? q0 : first;
     int v1 = q0 + kTile < last ? q0 + kTile : last;
     v1 = v1 < T ? v1 : T;
-    if (v0 < v1) first_tile = doc_of_warp(A.cu, A.batch, T, v0).lo / kTile;
+    if (v0 < v1) first_tile = doc_of_warp(A.cu, A.batch, T, v0).lo / (W ? 1 : kTile);
   }
-  return item_from(P, at, tile, first_tile);
+  return item_from<W>(P, at, tile, first_tile);
 }
 
 // The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
-template <int D>
+// (With a window without a look at the masked places, as in the forward pass.)
+template <int D, bool W>
 __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, int warps, int lane) {
   const uint32_t slots = redo_slots(A.t * A.nql, A.T);
   int turn = 0;
@@ -109,7 +126,7 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
 #pragma unroll
       for (int r = 0; r < kRedoRows; ++r) {
         const int first = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
-        bool met = i[r] - first < kRedoShort;
+        bool met = W || i[r] - first < kRedoShort;
         if (!met) {
           if (!looked) edges.look<D>(S.k, A.ldk, c / A.grp * D, first, at.row0, A.T, lane);
           looked = true;
@@ -121,15 +138,15 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
       const int n = redo_take(again, at.row0, i);
 #pragma unroll
       for (int r = 0; r < kRedoRows; ++r) lo[r] = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
-      dq_rows<D>(A, S, shard, c, i, lo, n, lane);
+      dq_rows<D, W>(A, S, shard, c, i, lo, n, lane);
     }
     slot = e.next;
   }
 }
 
-template <int D>
+template <int D, bool W>
 __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_constant__ DqParams P) {
-  using C = DqCfg<D>;
+  using C = DqCfg<D, W>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
@@ -171,7 +188,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
   const int total = P.tiles * P.lanes;
   int* status = A.status;
   const uint64_t tmo = P.timeout_ns;
-  const ItemQueue<DqItem> queue{reinterpret_cast<DqItem*>(smem + C::OFF_BAR + 320), item_bars, abort_flag, status, tmo};
+  const ItemQueue<DqItem<W>> queue{reinterpret_cast<DqItem<W>*>(smem + C::OFF_BAR + 320), item_bars, abort_flag, status, tmo};
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -222,14 +239,14 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int pos = 0, nq = 0;    // key tiles and items started
-    DqItem it = first_item(P);
+    DqItem<W> it = first_item<W>(P);
     for (int n = 0; lane == 0 && ok && it.shard >= 0; ++n) {
-      DqItem coming = {};
+      DqItem<W> coming = {};
       coming.shard = -1;
       auto announce = [&]() {
         if (A.q_list) {
           const int at = static_cast<int>(gridDim.x) + atomicAdd(A.q_taken, 1);
-          if (at < total) coming = listed_item(P, at);
+          if (at < total) coming = listed_item<W>(P, at);
         }
         ok = queue.announce(n + 1, coming);
       };
@@ -246,7 +263,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           }
           ++nq;
         }
-        for (int j = it.jbeg; ok && j < it.jend; ++j, ++pos) {
+        bool told = false;
+        for (int j = it.jbeg; ok && j < it.jend; j = tile_after(it, j), ++pos) {
           const int ks = pos % kKSlots, vs = pos % kVSlots;
           ok = wait_on(&k_empty[ks], (static_cast<uint32_t>(pos / kKSlots) & 1u) ^ 1u, abort_flag, status, tmo);
           if (!ok) break;
@@ -264,7 +282,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           mbar_arrive_expect_tx(&v_full[vs], C::TILE);
           for (int kb = 0; kb < C::KB; ++kb)
             tma_load_2d(sV + vs * C::TILE + kb * 16384, &P.m.v[it.shard], &v_full[vs], it.g * D + kb * 64, j * kTile);
-          if (j == when) announce();
+          if (W ? !told && j >= when : j == when) {   // (`when` may lie in a window's gap)
+            announce();
+            told = true;
+          }
         }
       }
       it = coming;
@@ -298,9 +319,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     auto wait = [&](uint64_t* bar, int phase) {
       wait_on(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
     };
-    DqItem it = first_item(P);
+    DqItem<W> it = first_item<W>(P);
     for (int n = 0; queue.next(n, it) && it.shard >= 0; ++n) {
-      const int nt = it.jend - it.jbeg;
+      const int nt = tiles_of(it);
       if (nt <= 0) continue;
       wait(q_full, nq);
       tc_fence_after_sync();
@@ -377,7 +398,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     const int r0 = (warp - 2) * 64;
     const int T = static_cast<int>(A.T);
     bool ok = true;
-    DqItem it = first_item(P);
+    DqItem<W> it = first_item<W>(P);
     for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       const PackShard& S = A.s[it.shard];
       int lo[2];
@@ -423,7 +444,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
       ++met;
       return static_cast<bool>(__all_sync(0xffffffffu, in_time));
     };
-    DqItem it = first_item(P);
+    DqItem<W> it = first_item<W>(P);
     for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       const PackShard& S = A.s[it.shard];
       const int i = it.q0 + r;
@@ -438,9 +459,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
       if (lane == 0) mbar_arrive(rows_empty);
       const bool in = lo != 0x7fffffff;              // a row of a document (so i < T)
       const int hi = in ? i : -1;
-      const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
+      // (with a window: it sees near..hi, and lo..sink - 1)
+      const int near = W && in ? near_key(A, lo, i) : lo, sink = W && in ? sink_end(A, lo, near) : 0;
+      const int lo_max = __reduce_max_sync(0xffffffffu, near), hi_min = __reduce_min_sync(0xffffffffu, hi);
       const uint64_t kk2 = f2_pack(k2, k2), nl2 = f2_pack(nl, nl), nD2 = f2_pack(-Di, -Di);
-      for (int j = it.jbeg; ok && j < it.jend; ++j, ++pos) {
+      for (int j = it.jbeg; ok && j < it.jend; j = tile_after(it, j), ++pos) {
         ok = mbar_wait(s_full, static_cast<uint32_t>(pos) & 1u, abort_flag, status, tmo);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
@@ -480,7 +503,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         }
         const int k0 = j * kTile + g * 32;
         if (k0 < lo_max || k0 + 31 > hi_min) {   // some row of the warp does not see every key: its dS is 0
-          const uint32_t see = bits_between(lo - k0, hi - k0);
+          const uint32_t see = bits_between(near - k0, hi - k0) | (W ? bits_between(lo - k0, sink - 1 - k0) : 0u);
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
             ds[e >> 1] &= ((see >> e) & 1u ? 0x0000ffffu : 0u) | ((see >> (e + 1)) & 1u ? 0xffff0000u : 0u);
@@ -551,7 +574,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (warp >= 4 && redo_list->count > 0 && !*abort_flag) redo_rows<D>(A, *redo_list, warp - 4, kDqWarps, lane);
+  if (warp >= 4 && redo_list->count > 0 && !*abort_flag) redo_rows<D, W>(A, *redo_list, warp - 4, kDqWarps, lane);
 }
 
 }  // namespace
@@ -561,7 +584,6 @@ int pack_attn_dq_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStre
   P.a = A;
   P.m = maps;
   const int64_t qc = static_cast<int64_t>(A.nql) * d, kc = static_cast<int64_t>(A.nkvl) * d;
-  int rc = TTL_OK;
   P.tiles = static_cast<int>((A.T + kTile - 1) / kTile);
   P.lanes = A.t * A.nql;
   P.timeout_ns = pack_wait_ns(P.tiles);
@@ -569,18 +591,16 @@ int pack_attn_dq_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStre
   if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many query tiles");
   const int sms = num_sms();
   const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
-  const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
-  TraceScope trace(stream, TTL_K_ATTN_CORE, 6.0 * tri * d * A.nql * A.t, 2.0 * A.T * (4.0 * qc + 2.0 * kc) * A.t);
-  if (d == 128) {
-    if ((rc = allow_smem<pack_dq_kernel<128>>(DqCfg<128>::SMEM, "cudaFuncSetAttribute(packed attention dQ)")))
-      return rc;
-    rc = cuda_check(launch_after(pack_dq_kernel<128>, dim3(grid), kDqThreads, DqCfg<128>::SMEM, stream, P), "pack_dq_kernel launch");
-  } else {
-    if ((rc = allow_smem<pack_dq_kernel<64>>(DqCfg<64>::SMEM, "cudaFuncSetAttribute(packed attention dQ)")))
-      return rc;
-    rc = cuda_check(launch_after(pack_dq_kernel<64>, dim3(grid), kDqThreads, DqCfg<64>::SMEM, stream, P), "pack_dq_kernel launch");
-  }
-  return rc;
+  TraceScope trace(stream, TTL_K_ATTN_CORE, 6.0 * pack_pairs(A) * d * A.nql * A.t, 2.0 * A.T * (4.0 * qc + 2.0 * kc) * A.t);
+  auto run = [&](auto width, auto window) {
+    constexpr int D = decltype(width)::value;
+    constexpr bool W = decltype(window)::value;
+    const int err = allow_smem<pack_dq_kernel<D, W>>(DqCfg<D, W>::SMEM, "cudaFuncSetAttribute(packed attention dQ)");
+    if (err) return err;
+    return cuda_check(launch_after(pack_dq_kernel<D, W>, dim3(grid), kDqThreads, DqCfg<D, W>::SMEM, stream, P), "pack_dq_kernel launch");
+  };
+  if (d == 128) return A.window ? run(Width<128>{}, std::true_type{}) : run(Width<128>{}, std::false_type{});
+  return A.window ? run(Width<64>{}, std::true_type{}) : run(Width<64>{}, std::false_type{});
 }
 
 }  // namespace ttl

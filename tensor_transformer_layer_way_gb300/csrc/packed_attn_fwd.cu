@@ -58,29 +58,33 @@ struct FwdParams {
   uint64_t timeout_ns;
 };
 
-// One query tile of an item: tokens [q0, q0 + 128) of head c, key tiles [jbeg, jend).
-struct QTile {
+// One query tile of an item: tokens [q0, q0 + 128) of head c, key tiles [jbeg, jend) but for a window's gap.
+template <bool W>
+struct QTile : Gap<W> {
   int c, q0, jbeg, jend;
 };
-struct Item {
+template <bool W>
+struct Item : Gap<W> {
   int shard, g;                // shard < 0: no more items
-  QTile x[2];
+  QTile<W> x[2];
   int jlo, jhi;                // union of the key tiles
 };
 
-template <int D>
+template <int D, bool W>
 struct FwdCfg {
   static constexpr int KB = D / 64;
   static constexpr int TILE = KB * kTile * 128;   // bytes of a Q, K or V tile
   static constexpr int OFF_RING = 2 * TILE;
   static constexpr int OFF_OUT = OFF_RING + kRing * TILE;    // 32 rows x 64 columns of results per softmax warp
   static constexpr int OFF_ROWS = OFF_OUT + 8 * 4096;        // RowDocs [2]
-  static constexpr int OFF_BAR = OFF_ROWS + 96;
-  static constexpr int SMEM = OFF_BAR + 256 + kAhead * static_cast<int>(sizeof(Item)) + 1024;
+  static constexpr int OFF_BAR = OFF_ROWS + (W ? 112 : 96);
+  static constexpr int SMEM = OFF_BAR + 256 + kAhead * static_cast<int>(sizeof(Item<W>)) + 1024;
   static_assert(SMEM <= 232448, "shared memory beyond the per-CTA limit");
 };
 
-// First key tile of the query tile at token q0, or -1; found by the whole warp.
+// First key tile of the query tile at token q0 (with a window: the first token of the document it begins in), or -1;
+// found by the whole warp.
+template <bool W>
 __device__ __forceinline__ int first_key(const PackArgs& A, int q0) {
   const int T = static_cast<int>(A.T);
   if (A.batch == 0) return -1;
@@ -88,56 +92,89 @@ __device__ __forceinline__ int first_key(const PackArgs& A, int q0) {
   const int v0 = q0 > first ? q0 : first;
   int v1 = q0 + kTile < last ? q0 + kTile : last;
   v1 = v1 < T ? v1 : T;
-  return v0 < v1 ? doc_of_warp(A.cu, A.batch, T, v0).lo / kTile : -1;
+  if (v0 >= v1) return -1;
+  const int lo = doc_of_warp(A.cu, A.batch, T, v0).lo;
+  return W ? lo : lo / kTile;
 }
 
 // The item of index `at` whose unit and first keys are e.
-__device__ __forceinline__ Item item_from(const FwdParams& P, int at, int4 e) {
+template <bool W>
+__device__ __forceinline__ Item<W> item_from(const FwdParams& P, int at, int4 e) {
   const PackArgs& A = P.a;
   const int lane = at % P.lanes;
-  Item it;
+  Item<W> it;
   const int per = P.pair_heads ? A.nql / 2 : A.nql;
   it.shard = lane / per;
   const int c = (lane % per) * (P.pair_heads ? 2 : 1);
   it.g = c / A.grp;
   const int t0 = P.pair_heads ? e.x : 2 * e.x;
   auto tile = [&](int head, int t, int first) {
-    return QTile{head, t * kTile, first < 0 ? 0 : first, first < 0 ? 0 : t + 1};
+    QTile<W> q;
+    q.c = head;
+    q.q0 = t * kTile;
+    q.jbeg = first < 0 ? 0 : first;
+    q.jend = first < 0 ? 0 : t + 1;
+    if constexpr (W) {
+      const TileRange r = key_tiles(A, q.q0, q.jbeg);
+      q.jbeg = first < 0 ? 0 : r.beg;
+      q.gap = r.gap;
+      q.wbeg = r.wbeg;
+    }
+    return q;
   };
   it.x[0] = tile(c, t0, e.y);
   it.x[1] = P.pair_heads ? tile(c + 1, t0, e.y) : tile(c, t0 + 1, e.z);
   const bool a = it.x[0].jend > 0, b = it.x[1].jend > 0;
   it.jlo = a && (!b || it.x[0].jbeg < it.x[1].jbeg) ? it.x[0].jbeg : it.x[1].jbeg;
   it.jhi = b ? it.x[1].jend : it.x[0].jend;
+  if constexpr (W) {
+    // The gap is tile 0's where it has keys: of two neighbours tile 1 either is of the same document, with the same
+    // sinks and a window that begins no earlier, or its document begins in tile 0.  (Where bad bounds say otherwise,
+    // there is none: every tile that a softmax waits for is one that the products reach.)
+    const QTile<W>&p = it.x[0], &q = it.x[1];
+    it.gap = a ? p.gap : q.gap;
+    it.wbeg = a ? p.wbeg : q.wbeg;
+    if (a && b && !(q.wbeg >= p.wbeg && (q.gap <= q.jbeg || q.jbeg >= p.wbeg || (q.jbeg >= p.jbeg && q.gap <= p.gap))))
+      it.gap = it.wbeg = it.jlo;
+  }
   return it;
 }
 
 // A block's first item, found by a whole warp: from the list, or without one the last token tiles first.
-__device__ __forceinline__ Item first_item(const FwdParams& P) {
+template <bool W>
+__device__ __forceinline__ Item<W> first_item(const FwdParams& P) {
   const PackArgs& A = P.a;
   const int at = static_cast<int>(blockIdx.x);
-  if (A.q_list) return item_from(P, at, __ldg(A.q_list + at / P.lanes));
+  if (A.q_list) return item_from<W>(P, at, __ldg(A.q_list + at / P.lanes));
   const int unit = P.units - 1 - at / P.lanes;
   int4 e = make_int4(unit, -1, -1, 0);
-  e.y = first_key(A, unit * (P.pair_heads ? 1 : 2) * kTile);
-  if (!P.pair_heads) e.z = first_key(A, (unit * 2 + 1) * kTile);
-  return item_from(P, at, e);
+  e.y = first_key<W>(A, unit * (P.pair_heads ? 1 : 2) * kTile);
+  if (!P.pair_heads) e.z = first_key<W>(A, (unit * 2 + 1) * kTile);
+  return item_from<W>(P, at, e);
 }
 
-__device__ __forceinline__ bool active(const QTile& q, int j) { return j >= q.jbeg && j < q.jend; }
+template <bool W>
+__device__ __forceinline__ bool active(const QTile<W>& q, int j) {
+  if constexpr (W) {
+    if (j >= q.gap && j < q.wbeg) return false;
+  }
+  return j >= q.jbeg && j < q.jend;
+}
 
 // A query tile and the documents of its rows: rows [v0, v1) belong to some; the first of them to one that begins at
 // token lo, and bit r of `begins` is set where another begins at row r.
+template <bool W>
 struct RowDocs {
   uint32_t begins[4];
   int lo, v0, v1;
   int shard;                   // the tile itself, for the warps that work on it (< 0: no more)
-  QTile tile;
+  QTile<W> tile;
 };
-static_assert(sizeof(RowDocs) == 48, "two of them in 96 bytes");
+static_assert(sizeof(RowDocs<false>) == 48 && sizeof(RowDocs<true>) == 56, "two of them in 96 or 112 bytes");
 
 // First token of row r's document.
-__device__ __forceinline__ int first_token(const RowDocs& d, int q0, int r) {
+template <bool W>
+__device__ __forceinline__ int first_token(const RowDocs<W>& d, int q0, int r) {
   int w = r >> 5;
   uint32_t m = d.begins[w] & (0xffffffffu >> (31 - (r & 31)));
   while (m == 0 && w > 0) m = d.begins[--w];
@@ -145,7 +182,9 @@ __device__ __forceinline__ int first_token(const RowDocs& d, int q0, int r) {
 }
 
 // The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
-template <int D>
+// (With a window, whose tiles have masked places at both ends and among the sinks, without a look at them: a row's
+// keys are few.)
+template <int D, bool W>
 __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, int warps, int lane) {
   const uint32_t slots = redo_slots(A.t * A.nql, A.T);
   int turn = 0;
@@ -164,7 +203,7 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
 #pragma unroll
       for (int r = 0; r < kRedoRows; ++r) {
         const int first = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
-        bool met = i[r] - first < kRedoShort;
+        bool met = W || i[r] - first < kRedoShort;
         if (!met) {
           if (!looked) edges.look<D>(S.v, A.ldv, c / A.grp * D, first, at.row0, A.T, lane);
           looked = true;
@@ -176,20 +215,20 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
       const int n = redo_take(again, at.row0, i);
 #pragma unroll
       for (int r = 0; r < kRedoRows; ++r) lo[r] = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
-      fwd_rows<D>(A, S, c, i, lo, n, lane);
+      fwd_rows<D, W>(A, S, c, i, lo, n, lane);
     }
     slot = e.next;
   }
 }
 
-template <int D>
+template <int D, bool W>
 __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_constant__ FwdParams P) {
-  using C = FwdCfg<D>;
+  using C = FwdCfg<D, W>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + C::OFF_RING;
-  RowDocs* docs = reinterpret_cast<RowDocs*>(smem + C::OFF_ROWS);
+  RowDocs<W>* docs = reinterpret_cast<RowDocs<W>*>(smem + C::OFF_ROWS);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_empty = q_full + 1;
   uint64_t* ring_full = q_empty + 1;
@@ -212,7 +251,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
   const int total = P.units * P.lanes;
   int* status = A.status;
   const uint64_t tmo = P.timeout_ns;
-  const ItemQueue<Item> queue{reinterpret_cast<Item*>(smem + C::OFF_BAR + 256), item_bars, abort_flag, status, tmo};
+  const ItemQueue<Item<W>> queue{reinterpret_cast<Item<W>*>(smem + C::OFF_BAR + 256), item_bars, abort_flag, status, tmo};
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -253,14 +292,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int pos = 0, nq = 0;
-    Item it = first_item(P);
+    Item<W> it = first_item<W>(P);
     for (int n = 0; lane == 0 && ok && it.shard >= 0; ++n) {
-      Item coming = {};
+      Item<W> coming = {};
       coming.shard = -1;
       auto announce = [&]() {
         if (A.q_list) {
           const int at = static_cast<int>(gridDim.x) + atomicAdd(A.q_taken, 1);
-          if (at < total) coming = item_from(P, at, __ldg(A.q_list + at / P.lanes));
+          if (at < total) coming = item_from<W>(P, at, __ldg(A.q_list + at / P.lanes));
         }
         ok = queue.announce(n + 1, coming);
       };
@@ -293,9 +332,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         }
         ok = ok && load(&P.v[it.shard], it.jlo);
         if (ok && it.jlo == when) announce();
-        for (int j = it.jlo + 1; ok && j < it.jhi; ++j) {
+        bool told = it.jlo == when;              // (`when` may lie in a window's gap)
+        for (int j = tile_after(it, it.jlo); ok && j < it.jhi; j = tile_after(it, j)) {
           ok = load(&P.k[it.shard], j) && load(&P.v[it.shard], j);
-          if (ok && j == when) announce();
+          if (ok && (W ? !told && j >= when : j == when)) {
+            announce();
+            told = true;
+          }
         }
       }
       it = coming;
@@ -328,18 +371,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     auto wait = [&](uint64_t* bar, int phase) {
       wait_on(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, status, tmo);
     };
-    Item it = first_item(P);
+    Item<W> it = first_item<W>(P);
     for (int n = 0; queue.next(n, it) && it.shard >= 0; ++n) {
       if (it.jhi <= it.jlo) continue;
       wait(q_full, nq);
       tc_fence_after_sync();
       ++nq;
-      // Step j issues P V of key tile j and then S of key tile j + 1, tile by tile.
-      for (int j = it.jlo - 1; j < it.jhi; ++j) {
-        // V_j stands one place before K_(j + 1)
+      // Step j issues P V of key tile j and then S of the key tile jn behind it, tile by tile.
+      auto after = [&](int j) {
+        if constexpr (W) return j < it.jlo ? it.jlo : tile_after(it, j);
+        else return j + 1;
+      };
+      for (int j = it.jlo - 1; j < it.jhi; j = after(j)) {
+        const int jn = after(j);
+        // V_j stands one place before K_jn
         const int ks = slot, vs = slot == 0 ? kRing - 1 : slot - 1;
         if (j >= it.jlo) wait(&ring_full[vs], slot == 0 ? lap - 1 : lap);
-        if (j + 1 < it.jhi) wait(&ring_full[ks], lap);
+        if (jn < it.jhi) wait(&ring_full[ks], lap);
         const uint64_t kd = desc_advance(kd0, ks * C::TILE), vd = desc_advance(vd0, vs * C::TILE);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -356,7 +404,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
               if (j + 1 == it.x[x].jend) umma_commit(&o_full[x]);
             }
           }
-          if (active(it.x[x], j + 1)) {
+          if (active(it.x[x], jn)) {
             tc_fence_after_sync();
             if (leader) {
 #pragma unroll
@@ -371,11 +419,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         }
         if (leader) {
           if (j >= it.jlo) umma_commit(&ring_empty[vs]);
-          if (j + 1 < it.jhi) umma_commit(&ring_empty[ks]);
-          if (j + 2 == it.jhi) umma_commit(q_empty);   // the last S of the item is issued
+          if (jn < it.jhi) umma_commit(&ring_empty[ks]);
+          if (jn + 1 == it.jhi) umma_commit(q_empty);   // the last S of the item is issued
         }
         __syncwarp();
-        if (j + 1 < it.jhi) {              // on to K_(j + 2), past V_(j + 1)
+        if (jn < it.jhi) {                 // on to the next K, past V_jn
           slot += 2;
           if (slot >= kRing) {
             slot -= kRing;
@@ -393,10 +441,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     // ------------------------------------------------------------------ documents of the rows of tile x
     const int x = warp - 2;
     bool ok = true;
-    Item it = first_item(P);
+    Item<W> it = first_item<W>(P);
     for (int n = 0; ok && it.shard >= 0 && queue.next(n, it); ++n) {   // (the end is passed on too)
-      const QTile qt = x ? it.x[1] : it.x[0];
-      RowDocs d = {{0, 0, 0, 0}, 0, 0, 0, it.shard, qt};
+      const QTile<W> qt = x ? it.x[1] : it.x[0];
+      RowDocs<W> d = {{0, 0, 0, 0}, 0, 0, 0, it.shard, qt};
       if (qt.jend > qt.jbeg) {
         const int T = static_cast<int>(A.T);
         const int first = __ldg(A.cu), last = min(__ldg(A.cu + A.batch), T);
@@ -435,7 +483,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         ok = false;
         break;
       }
-      const QTile qt = docs[x].tile;
+      const QTile<W> qt = docs[x].tile;
       const int shard = docs[x].shard;
       if (shard < 0) break;
       const PackShard& S = A.s[shard];
@@ -444,10 +492,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
       const int lo = in ? first_token(docs[x], qt.q0, r) : 0x7fffffff, hi = in ? i : -1;   // it sees the keys lo..hi
       __syncwarp();
       if (lane == 0) mbar_arrive(rows_empty);
-      const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
-      const int lo_min = __reduce_min_sync(0xffffffffu, lo), hi_max = __reduce_max_sync(0xffffffffu, hi);
+      // (with a window: it sees near..hi, and lo..sink - 1)
+      const int near = W && in ? near_key(A, lo, i) : lo, sink = W && in ? sink_end(A, lo, near) : 0;
+      const int lo_max = __reduce_max_sync(0xffffffffu, near), hi_min = __reduce_min_sync(0xffffffffu, hi);
+      const int lo_min = __reduce_min_sync(0xffffffffu, near), hi_max = __reduce_max_sync(0xffffffffu, hi);
+      const int sink_lo = W ? __reduce_min_sync(0xffffffffu, lo) : 0, sink_hi = W ? __reduce_max_sync(0xffffffffu, sink) : 0;
       float m = -INFINITY, l = 0.0f;
-      for (int j = qt.jbeg; ok && j < qt.jend; ++j) {
+      for (int j = qt.jbeg; ok && j < qt.jend; j = tile_after(qt, j)) {
         ok = mbar_wait(&s_full[x], ns & 1u, abort_flag, status, tmo);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
@@ -460,7 +511,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         const int k0 = j * kTile;
         auto tile = [&](auto whole) {
           constexpr bool WHOLE = decltype(whole)::value;
-          auto live = [&](int u) { return WHOLE || (k0 + u * 32 <= hi_max && k0 + u * 32 + 31 >= lo_min); };
+          auto live = [&](int u) {
+            return WHOLE || (k0 + u * 32 <= hi_max && k0 + u * 32 + 31 >= lo_min) ||
+                   (W && k0 + u * 32 < sink_hi && k0 + u * 32 + 31 >= sink_lo);
+          };
           uint32_t s[4][32];
           auto read_scores = [&]() {
 #pragma unroll
@@ -471,7 +525,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
               for (int u = 0; u < 4; ++u) {
                 const int c0 = k0 + u * 32;
                 if (live(u) && (c0 < lo_max || c0 + 31 > hi_min)) {
-                  const uint32_t see = bits_between(lo - c0, hi - c0);
+                  const uint32_t see = bits_between(near - c0, hi - c0) | (W ? bits_between(lo - c0, sink - 1 - c0) : 0u);
 #pragma unroll
                   for (int e = 0; e < 32; ++e) s[u][e] = (see >> e) & 1u ? s[u][e] : 0xff800000u;
                 }
@@ -607,7 +661,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
     // The eight softmax warps, all of which come here, meet: the list is whole and every store of its rows complete.
     // (Within this branch, whose registers the code is given; behind the block's last barrier heads of 64 took 4% longer.)
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (redo_list->count > 0 && !*abort_flag) redo_rows<D>(A, *redo_list, warp - 4, 8, lane);
+    if (redo_list->count > 0 && !*abort_flag) redo_rows<D, W>(A, *redo_list, warp - 4, 8, lane);
   }
 
   __syncthreads();
@@ -651,8 +705,7 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stre
     P.a.q_list = plan.q_list;
     P.a.q_taken = plan.q_taken;
   }
-  const double tri = static_cast<double>(A.T) * (A.T + 1) / 2.0;   // one document: the lengths are on the device
-  TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * tri * d * A.nql * A.t,
+  TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * pack_pairs(A) * d * A.nql * A.t,
                    2.0 * A.T * (2.0 * qc + 2.0 * kc) * A.t);
   // Behind the plan its blocks may be brought up early.  Without one the kernel before is the caller's: a block that
   // held all of tensor memory while one of that kernel's still had to allocate some would keep it from ending.
@@ -661,16 +714,14 @@ int pack_attn_fwd_launch(const PackArgs& A, int d, void* list, cudaStream_t stre
                                  : launch_first(kernel, dim3(grid), kFwdThreads, smem, stream, P),
                       "pack_fwd_kernel launch");
   };
-  if (d == 128) {
-    if ((rc = allow_smem<pack_fwd_kernel<128>>(FwdCfg<128>::SMEM, "cudaFuncSetAttribute(packed attention forward)")))
-      return rc;
-    rc = launch(pack_fwd_kernel<128>, FwdCfg<128>::SMEM);
-  } else {
-    if ((rc = allow_smem<pack_fwd_kernel<64>>(FwdCfg<64>::SMEM, "cudaFuncSetAttribute(packed attention forward)")))
-      return rc;
-    rc = launch(pack_fwd_kernel<64>, FwdCfg<64>::SMEM);
-  }
-  return rc;
+  auto run = [&](auto width, auto window) {
+    constexpr int D = decltype(width)::value;
+    constexpr bool W = decltype(window)::value;
+    const int err = allow_smem<pack_fwd_kernel<D, W>>(FwdCfg<D, W>::SMEM, "cudaFuncSetAttribute(packed attention forward)");
+    return err ? err : launch(pack_fwd_kernel<D, W>, FwdCfg<D, W>::SMEM);
+  };
+  if (d == 128) return A.window ? run(Width<128>{}, std::true_type{}) : run(Width<128>{}, std::false_type{});
+  return A.window ? run(Width<64>{}, std::true_type{}) : run(Width<64>{}, std::false_type{});
 }
 
 }  // namespace ttl

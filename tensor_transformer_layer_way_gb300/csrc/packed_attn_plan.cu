@@ -15,19 +15,28 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
-// First key tile that token tile `tile` meets, or -1.
-__device__ __forceinline__ int first_key_tile(const PackArgs& A, int tile) {
+// First key tile that token tile `tile` meets (with a window: the first token of the document it begins in), or -1.
+__device__ __forceinline__ int first_of(const PackArgs& A, int tile) {
   const int T = static_cast<int>(A.T);
   if (A.batch == 0 || static_cast<int64_t>(tile) * kTile >= A.T) return -1;
   const int q0 = tile * kTile, first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
   const int v0 = q0 > first ? q0 : first;
   int v1 = q0 + kTile < last ? q0 + kTile : last;
   v1 = v1 < T ? v1 : T;
-  return v0 < v1 ? doc_of(A.cu, A.batch, T, v0).lo / kTile : -1;
+  if (v0 >= v1) return -1;
+  const int lo = doc_of(A.cu, A.batch, T, v0).lo;
+  return A.window ? lo : lo / kTile;
+}
+// Key tiles of token tile `tile`, of which first_of said `first`.
+__device__ __forceinline__ int tiles_met(const PackArgs& A, int tile, int first) {
+  if (first < 0) return 0;
+  if (!A.window) return tile + 1 - first;
+  const TileRange r = key_tiles(A, tile * kTile, first);
+  return r.gap - r.beg + tile + 1 - r.wbeg;
 }
 
 // Last query tile that key tile `tile` meets, or tile - 1.
-__device__ __forceinline__ int last_query_tile(const PackArgs& A, int tile) {
+__device__ __forceinline__ int last_tile_of(const PackArgs& A, int tile) {
   const int T = static_cast<int>(A.T);
   if (A.batch == 0) return tile - 1;
   const int k0 = tile * kTile, first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
@@ -35,8 +44,8 @@ __device__ __forceinline__ int last_query_tile(const PackArgs& A, int tile) {
   int v1 = k0 + kTile < last ? k0 + kTile : last;
   v1 = v1 < T ? v1 : T;
   if (v0 >= v1) return tile - 1;
-  const int hi = doc_of(A.cu, A.batch, T, v1 - 1).hi;
-  return (hi > v1 ? hi - 1 : v1 - 1) / kTile;
+  const DocRange doc = doc_of(A.cu, A.batch, T, v1 - 1);
+  return A.window ? last_query_tile<true>(A, doc, k0, v1) : last_query_tile<false>(A, doc, k0, v1);
 }
 
 // hist[b] entries of work class b become places, the highest class first.  Every thread calls it.
@@ -112,8 +121,8 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     for (int pass = 0; pass < 2; ++pass) {
       for (int u = tid; u < P.q_units; u += kPlanThreads) {
         const int t0 = u * P.q_per;
-        const int a = first_key_tile(A, t0), b = P.q_per == 2 ? first_key_tile(A, t0 + 1) : -1;
-        const int work = (a < 0 ? 0 : t0 + 1 - a) + (b < 0 ? 0 : t0 + 2 - b);
+        const int a = first_of(A, t0), b = P.q_per == 2 ? first_of(A, t0 + 1) : -1;
+        const int work = tiles_met(A, t0, a) + tiles_met(A, t0 + 1, b);
         const int at = atomicAdd(&hist[work_class(work, q_shift)], 1);
         if (pass) P.q_list[at] = make_int4(u, a, b, 0);
       }
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     unsigned long long sum = 0;
     int most_here = 0;
     for (int t = tid; t < P.tiles; t += kPlanThreads) {
-      const int steps = (last_query_tile(A, t) - t + 1) * A.grp;
+      const int steps = (last_tile_of(A, t) - t + 1) * A.grp;
       sum += static_cast<unsigned long long>(steps);
       most_here = steps > most_here ? steps : most_here;
     }
@@ -148,7 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     }
     for (int pass = 0; pass < 2; ++pass) {
       for (int t = tid; t < P.tiles; t += kPlanThreads) {
-        const int last = last_query_tile(A, t);
+        const int last = last_tile_of(A, t);
         const int steps = (last - t + 1) * A.grp;
         const int parts = steps > 0 ? static_cast<int>((steps + most - 1) / most) : 1;
         const int len = (steps + parts - 1) / parts;
@@ -175,7 +184,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     // the number of entries: all places given out
     int entries = 0;
     for (int t = tid; t < P.tiles; t += kPlanThreads) {
-      const int steps = (last_query_tile(A, t) - t + 1) * A.grp;
+      const int steps = (last_tile_of(A, t) - t + 1) * A.grp;
       entries += steps > 0 ? static_cast<int>((steps + most - 1) / most) : 1;
     }
     if (tid == 0) taken = 0;
