@@ -523,7 +523,7 @@ int ttl_packed_window_attn_bwd(int t, int64_t T, int n_q, int n_kv, int d, int b
  *   gamma_q, gamma_k [d] of w_type (TTL_T_BF16 or TTL_T_F32), both or neither
  *   Q[i] [T, n_q/t d], K[i] [T, n_kv/t d], head-major columns, row strides ldq, ldk (multiples of 8)
  *   Qo[i], Ko[i] out, the same shapes, row strides ldqo, ldko
- * t | n_q, t | n_kv, d a multiple of 16 up to 256, any T < 2^31 - 1.  Sums are fp32, one rounding;
+ * t | n_q, t | n_kv, d a multiple of 16 up to 256, any T < 2^31 - 64.  Sums are fp32, one rounding;
  * an angle is exact to 2^-24 of a half turn at any position.  Qo may be Q itself, and Ko K (the same pointers and
  * stride); otherwise no output may share memory with an input or another output: TTL_ERR_ARG. */
 int ttl_head_norm_rotary_fwd(int t, int64_t T, int n_q, int n_kv, int d, int rot, int interleaved, const double* freqs,

@@ -14,12 +14,18 @@
 //
 // Layout.  A lane holds 16 columns of a head as two 16-byte words whose columns pair up (columns c.. and rot/2 + c..,
 // or 16 neighbours), so a rotation exchanges nothing; the 1 to 16 lanes of a head share a token and join their squares
-// by shuffles.  A warp's tokens stay while it walks over a range of heads of all shards: the sines are taken once for
-// the range.
+// by shuffles.  A warp walks over an even share of all (token group, head) pairs, a group's heads of all shards in turn:
+// sines are taken once for a group.  A lane copies its words to a ring in shared memory, places ahead, and
+// reads there what it copied itself: no barrier, and the copies' depth costs no registers.  The arithmetic is on pairs
+// of values.
 //
-// What bounds it: bytes.
+// What bounds it: bytes, of which it moves 89% (forward) and 83% (backward) of what a plain copy of as many does.
+// Measured: 8192 tokens, 32 and 8 heads of 128 over 8 shards, forward 33 us (5.0 TB/s; one head's words a lane at a time
+// through registers took 51), backward with the weights' gradients 51 us, 3 of them the join of the blocks' sums.  A
+// look-up of a token's document in memory cost each token group microseconds: the bounds are in shared memory.
 
 #include <cmath>
+#include <type_traits>
 
 #include "launch_after.cuh"
 #include "operands.h"
@@ -33,6 +39,7 @@ namespace {
 constexpr int kMaxHead = 256;
 constexpr int kMaxPairs = kMaxHead / 2;
 constexpr int kMaxAxes = 8;
+constexpr int kNearDocs = 512;   // document bounds that a block keeps in shared memory
 constexpr int kWarps = 8;
 
 enum Mode : int {
@@ -58,40 +65,86 @@ struct HeadArgs {
   const void* gamma[2];
   int w_type;
   float eps;
-  float sign;                                // kTurn: -1 turns back
+  float sign;                                // -1: the turns go back
   float* part;                               // kBackward: [blocks][2][d]
-  int chunks, chunk;                         // ranges of heads a token group is cut into, heads of one
-  int64_t items;                             // token groups x chunks
+  int64_t groups;                            // of the tokens that a warp works on together
+  int64_t warps;                             // that share the pairs of a group and a head
   int* status;
 };
 
-__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
-
-// The 16 columns of two words as pairs (a[e], b[e]).
+// Eight pairs (a, b), two of them to a register pair: a[i] holds the a of pairs 2 i and 2 i + 1.
+struct Pairs {
+  uint64_t a[4], b[4];
+};
+__device__ __forceinline__ uint64_t widen(uint32_t w) { return f2_pack(bf16_lo(w), bf16_hi(w)); }
+// The 16 columns of two words.
 template <bool NEIGHBOURS>
-__device__ __forceinline__ void to_pairs(const uint4& u, const uint4& v, float (&a)[8], float (&b)[8]) {
+__device__ __forceinline__ Pairs to_pairs(const uint4& u, const uint4& v) {
   const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  Pairs p;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int i = 0; i < 4; ++i) {
     if constexpr (NEIGHBOURS) {
-      a[e] = bf16_lo(w[e]);
-      b[e] = bf16_hi(w[e]);
+      p.a[i] = f2_pack(bf16_lo(w[2 * i]), bf16_lo(w[2 * i + 1]));
+      p.b[i] = f2_pack(bf16_hi(w[2 * i]), bf16_hi(w[2 * i + 1]));
     } else {
-      a[e] = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-      b[e] = e & 1 ? bf16_hi(w[4 + (e >> 1)]) : bf16_lo(w[4 + (e >> 1)]);
+      p.a[i] = widen(w[i]);
+      p.b[i] = widen(w[4 + i]);
     }
   }
+  return p;
 }
 template <bool NEIGHBOURS>
-__device__ __forceinline__ void store_pairs(__nv_bfloat16* p0, __nv_bfloat16* p1, const float (&a)[8], const float (&b)[8]) {
+__device__ __forceinline__ void to_words(const Pairs& p, uint4& u, uint4& v) {
   uint32_t w[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if constexpr (NEIGHBOURS) w[e] = pack_bf16x2(a[e], b[e]);
-    else w[e] = e < 4 ? pack_bf16x2(a[2 * e], a[2 * e + 1]) : pack_bf16x2(b[2 * e - 8], b[2 * e - 7]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = f2_unpack(p.a[i]), b = f2_unpack(p.b[i]);
+    if constexpr (NEIGHBOURS) {
+      w[2 * i] = pack_bf16x2(a.x, b.x);
+      w[2 * i + 1] = pack_bf16x2(a.y, b.y);
+    } else {
+      w[i] = pack_bf16x2(a.x, a.y);
+      w[4 + i] = pack_bf16x2(b.x, b.y);
+    }
   }
-  *reinterpret_cast<uint4*>(p0) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(p1) = make_uint4(w[4], w[5], w[6], w[7]);
+  u = make_uint4(w[0], w[1], w[2], w[3]);
+  v = make_uint4(w[4], w[5], w[6], w[7]);
+}
+// Sum of the lanes of a head.
+template <int LANES>
+__device__ __forceinline__ float head_sum(uint64_t x) {
+  const float2 f = f2_unpack(x);
+  float s = f.x + f.y;
+#pragma unroll
+  for (int o = LANES >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// cos and sin of two angles, given as fractions of a turn in units of 2^-32: Taylor's series about the nearest quarter turn
+// (|x| <= pi / 4: up to x^9 for the sine, x^8 for the cosine, whose next terms are below 2^-29 and 2^-25).
+__device__ __forceinline__ void turn_of(uint32_t f0, uint32_t f1, float (&c)[2], float (&s)[2]) {
+  const uint32_t q[2] = {(f0 + 0x20000000u) >> 30, (f1 + 0x20000000u) >> 30};
+  const float unit = 1.4629180792671596e-9f;      // 2 pi / 2^32
+  const float x0 = static_cast<float>(static_cast<int32_t>(f0 - (q[0] << 30))) * unit;
+  const float x1 = static_cast<float>(static_cast<int32_t>(f1 - (q[1] << 30))) * unit;
+  auto both = [](float v) { return f2_pack(v, v); };
+  const uint64_t x = f2_pack(x0, x1), x2 = fmul2(x, x);
+  uint64_t p = ffma2(x2, both(1.0f / 362880.0f), both(-1.0f / 5040.0f));
+  p = ffma2(p, x2, both(1.0f / 120.0f));
+  p = ffma2(p, x2, both(-1.0f / 6.0f));
+  const float2 sn = f2_unpack(ffma2(fmul2(p, x2), x, x));
+  p = ffma2(x2, both(1.0f / 40320.0f), both(-1.0f / 720.0f));
+  p = ffma2(p, x2, both(1.0f / 24.0f));
+  p = ffma2(p, x2, both(-0.5f));
+  const float2 cs = f2_unpack(ffma2(p, x2, both(1.0f)));
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float sv = u ? sn.y : sn.x, cv = u ? cs.y : cs.x;
+    const float ps = q[u] & 1 ? cv : sv, pc = q[u] & 1 ? sv : cv;
+    s[u] = __uint_as_float(__float_as_uint(ps) ^ ((q[u] & 2u) << 30));
+    c[u] = __uint_as_float(__float_as_uint(pc) ^ (((q[u] + 1) & 2u) << 30));
+  }
 }
 
 // Reports document bounds that do not start at 0 or above, decrease, or end beyond T.
@@ -104,18 +157,48 @@ __device__ __forceinline__ void check_bounds(const HeadArgs& A) {
   if (bad) atomicCAS(A.status, 0, TTL_ERR_DEVICE);
 }
 
+// 16 bytes to shared memory, in the group that the thread commits next.
+__device__ __forceinline__ void copy16(void* dst, const __nv_bfloat16* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void await_copies() {   // all but the last N groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Places of a warp's ring: all but one of them hold heads on their way.  Blocks of an SM: with three (80 registers a thread) the
+// forward kernel spilled and took 37 us where two take 33; the backward kernel's one, whose sums leave half as many
+// rows to join, 51 where two took 53.  (8192 tokens, 40 heads of 128.)
+template <int MODE>
+constexpr int kStages = MODE == kBackward ? 4 : 5;
+template <int MODE>
+constexpr int kResident = MODE == kBackward ? 1 : 2;
+template <int MODE>
+constexpr int kWords = MODE == kBackward ? 4 : 2;   // of a lane and head
+template <int MODE>
+constexpr int kRingBytes = kWarps * kStages<MODE> * kWords<MODE> * 512;
+
 // LANES lanes to a head, each with two words of eight columns.
 template <int LANES, bool NEIGHBOURS, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, 2) head_rotary_kernel(const __grid_constant__ HeadArgs A) {
-  constexpr int kTokens = 32 / LANES;
-  __shared__ uint64_t turns[kMaxPairs];
-  __shared__ uint8_t axis[kMaxPairs];
-  __shared__ float gamma[MODE == kTurn ? 1 : 2][kMaxHead];
+__global__ void __launch_bounds__(kWarps * 32, kResident<MODE>) head_rotary_kernel(const __grid_constant__ HeadArgs A) {
+  constexpr int kTokens = 32 / LANES, S = kStages<MODE>;
+  extern __shared__ __align__(16) uint4 ring[];   // [warp][stage][word][lane]: a lane reads what it copied
+  __shared__ __align__(16) uint64_t turns[kMaxPairs];
+  __shared__ __align__(8) uint8_t axis[kMaxPairs];
+  __shared__ int32_t bounds[kNearDocs + 1];       // (looked up in memory they cost each token group a few microseconds)
+  __shared__ __align__(16) float gamma[MODE == kTurn ? 1 : 2][kMaxHead];
   __shared__ float sums[MODE == kBackward ? kWarps : 1][2][kMaxHead];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < A.rot / 2; i += kWarps * 32) {
-    turns[i] = A.turns[i];
+  if constexpr (MODE == kBackward) launch_next();   // (the join, which waits for all of this kernel)
+  uint4* mine_at = ring + warp * (S * kWords<MODE> * 32) + lane;
+  for (int i = threadIdx.x; i < kMaxPairs; i += kWarps * 32) {
+    turns[i] = A.turns[i];                        // (0 behind the rotated columns' pairs: no turn)
     axis[i] = A.axis[i];
+  }
+  const bool near = A.cu && A.batch <= kNearDocs;
+  if (near) {
+    for (int i = threadIdx.x; i <= A.batch; i += kWarps * 32) bounds[i] = __ldg(A.cu + i);
   }
   if constexpr (MODE != kTurn) {
     for (int i = threadIdx.x; i < 2 * A.d; i += kWarps * 32) {
@@ -130,139 +213,188 @@ __global__ void __launch_bounds__(kWarps * 32, 2) head_rotary_kernel(const __gri
   const int slot = lane % LANES;
   const bool mine = slot < A.d / 16;              // (a head whose 16-column slots are no power of two leaves lanes idle)
   // the slot's columns, and its pairs
-  int c0 = slot * 16, c1 = c0 + 8;
+  int c0 = slot * 16, step = 8;
   if (!NEIGHBOURS && slot < A.rot / 16) {
     c0 = slot * 8;
-    c1 = A.rot / 2 + c0;
+    step = A.rot / 2;
+  }
+  auto column = [&](bool second, int e) { return NEIGHBOURS ? c0 + 2 * e + second : c0 + e + (second ? step : 0); };
+  if (!mine) {                                    // idle lanes read zeros, which their heads' sums take in
+    for (int k = 0; k < S * kWords<MODE>; ++k) mine_at[k * 32] = make_uint4(0, 0, 0, 0);
   }
   const float inv_d = 1.0f / static_cast<float>(A.d);
-  float acc[2][16];
+  const int q_heads = A.t * A.heads[0], all = q_heads + A.t * A.heads[1];
+  Pairs acc[2];
   if constexpr (MODE == kBackward) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[0][e] = acc[1][e] = 0.0f;
+    for (int i = 0; i < 4; ++i) acc[0].a[i] = acc[0].b[i] = acc[1].a[i] = acc[1].b[i] = 0;
   }
 
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < A.items;
-       item += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t group = item / A.chunks;
-    const int h0 = static_cast<int>(item - group * A.chunks) * A.chunk;
-    const int all = A.t * (A.heads[0] + A.heads[1]);
-    const int h1 = h0 + A.chunk < all ? h0 + A.chunk : all;
-    const int64_t tok = group * kTokens + lane / LANES;
+  // The warp's share of all (token group, head) pairs: a group's heads of Q, shard by shard, then those of K.
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t total = A.groups * all, share = total / A.warps, more = total - share * A.warps;
+  // (an int: the results, 32 bytes a pair at least, share no memory, and a launch of many pairs has thousands of warps)
+  int left = w < A.warps ? static_cast<int>(share + (w < more)) : 0;
+  const int64_t from = w < A.warps ? w * share + (w < more ? w : more) : 0;
+  const int64_t group = from / all;
+  int h0 = static_cast<int>(from - group * all);
+  int tok = static_cast<int>(group) * kTokens + lane / LANES;
+  // Shard of head h of Q (kind 0) or K, counted from the kind's first; h becomes the head on the shard.
+  auto shard_of = [&](int kind, int& h) {
+    const int shard = A.magic[kind] ? static_cast<int>(__umulhi(static_cast<uint32_t>(h), A.magic[kind])) : h;
+    h -= shard * A.heads[kind];
+    return shard;
+  };
+  // What is fetched next: head `f_head` of shard f_shard, at f_in (and f_x), f_left of them in all.
+  int f_left = left, f_tok = tok;
+  int f_kind = h0 >= q_heads, f_head = f_kind ? h0 - q_heads : h0, f_shard = shard_of(f_kind, f_head);
+  int put = 0, get = 0;                           // places of the ring
+  const __nv_bfloat16 *f_in, *f_x;
+  auto locate = [&]() {
+    f_in = A.in[f_kind][f_shard] + static_cast<int64_t>(f_tok) * A.ld_in[f_kind] + f_head * A.d + c0;
+    if constexpr (MODE == kBackward) f_x = A.x[f_kind][f_shard] + static_cast<int64_t>(f_tok) * A.ld_x[f_kind] + f_head * A.d + c0;
+  };
+  locate();
+  auto fetch = [&]() {
+    if (f_left > 0) {
+      uint4* to = mine_at + put * (kWords<MODE> * 32);
+      if (mine && f_tok < A.T) {
+        copy16(to, f_in);
+        copy16(to + 32, f_in + step);
+        if constexpr (MODE == kBackward) {
+          copy16(to + 64, f_x);
+          copy16(to + 96, f_x + step);
+        }
+      }
+      --f_left;
+      put = put + 1 == S ? 0 : put + 1;
+      f_in += A.d;
+      if constexpr (MODE == kBackward) f_x += A.d;
+      if (++f_head == A.heads[f_kind]) {
+        f_head = 0;
+        if (++f_shard == A.t) {
+          f_shard = 0;
+          f_kind ^= 1;
+          if (f_kind == 0) f_tok += kTokens;
+        }
+        locate();
+      }
+    }
+    commit_copies();
+  };
+#pragma unroll
+  for (int k = 0; k < S - 1; ++k) fetch();
+
+  for (; left > 0; tok += kTokens, h0 = 0) {
+    const int h1 = left < all - h0 ? h0 + left : all;
+    left -= h1 - h0;
     const bool there = tok < A.T;
     DocRange doc{0, static_cast<int>(A.T)};
-    if (A.cu) doc = doc_of(A.cu, A.batch, static_cast<int>(A.T), there ? static_cast<int>(tok) : -1);
+    if (near) doc = doc_among([&](int b) { return bounds[b]; }, A.batch, static_cast<int>(A.T), there ? tok : -1);
+    else if (A.cu) doc = doc_of(A.cu, A.batch, static_cast<int>(A.T), there ? tok : -1);
     const bool counts = there && doc.hi > doc.lo;
-    float co[8], si[8];
+    const bool all_count = __all_sync(0xffffffffu, counts);
+    uint64_t co[4], si[4];
+    {
+      const uint2 on = *reinterpret_cast<const uint2*>(axis + slot * 8);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int pair = slot * 8 + e;
-      co[e] = 1.0f;
-      si[e] = 0.0f;
-      if (pair < A.rot / 2 && counts) {
-        const int64_t p = A.pos ? __ldg(A.pos + axis[pair] * A.T + tok) : tok - doc.lo;
-        const uint64_t turn = turns[pair] * static_cast<uint64_t>(p);
-        sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &si[e], &co[e]);
+      for (int i = 0; i < 4; ++i) {
+        const ulonglong2 per = *reinterpret_cast<const ulonglong2*>(turns + slot * 8 + i * 2);
+        const uint32_t two = ((i & 2) ? on.y : on.x) >> ((i & 1) * 16);
+        int p[2] = {tok - doc.lo, tok - doc.lo};
+        if (A.pos) {
+          p[0] = counts ? __ldg(A.pos + (two & 255u) * A.T + tok) : 0;
+          p[1] = counts ? __ldg(A.pos + (two >> 8 & 255u) * A.T + tok) : 0;
+        }
+        float c[2], s[2];
+        turn_of(static_cast<uint32_t>((per.x * static_cast<uint64_t>(static_cast<int64_t>(p[0]))) >> 32),
+                static_cast<uint32_t>((per.y * static_cast<uint64_t>(static_cast<int64_t>(p[1]))) >> 32), c, s);
+        co[i] = f2_pack(c[0], c[1]);
+        si[i] = f2_pack(s[0] * A.sign, s[1] * A.sign);
       }
-      if constexpr (MODE == kTurn) si[e] *= A.sign;
     }
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
-      const int base = kind ? A.t * A.heads[0] : 0;
-      const int begin = (h0 > base ? h0 : base) - base;
-      const int last = kind ? all : A.t * A.heads[0];
-      const int end = (h1 < last ? h1 : last) - base;
-      if (begin >= end) continue;
-      float ga[8], gb[8];
+      int at = kind ? (h0 > q_heads ? h0 - q_heads : 0) : h0;
+      int n = (kind ? h1 - q_heads : (h1 < q_heads ? h1 : q_heads)) - at;   // heads of this kind
+      if (n <= 0) continue;
+      Pairs ga;
       if constexpr (MODE != kTurn) {
+        float g[16];                              // (idle lanes: what is not used)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ga[e] = mine ? gamma[kind][NEIGHBOURS ? c0 + 2 * e : c0 + e] : 0.0f;
-          gb[e] = mine ? gamma[kind][NEIGHBOURS ? c0 + 2 * e + 1 : c1 + e] : 0.0f;
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(g + i * 4) =
+              *reinterpret_cast<const float4*>(gamma[kind] + (mine ? c0 + (i & 1) * 4 + (i >> 1) * step : i * 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ga.a[i] = NEIGHBOURS ? f2_pack(g[4 * i], g[4 * i + 2]) : f2_pack(g[2 * i], g[2 * i + 1]);
+          ga.b[i] = NEIGHBOURS ? f2_pack(g[4 * i + 1], g[4 * i + 3]) : f2_pack(g[8 + 2 * i], g[8 + 2 * i + 1]);
         }
       }
-      constexpr int kAtOnce = MODE == kBackward ? 1 : 2;   // heads whose words are loaded before the first is worked on
+      for (int shard = shard_of(kind, at); n > 0; ++shard, at = 0) {
+        __nv_bfloat16* out = A.out[kind][shard] + static_cast<int64_t>(tok) * A.ld_out[kind] + at * A.d + c0;
+        int here = A.heads[kind] - at;
+        here = here < n ? here : n;
+        n -= here;
 #pragma unroll 1
-      for (int h = begin; h < end; h += kAtOnce) {
-        uint4 u[kAtOnce], v[kAtOnce], xu[kAtOnce], xv[kAtOnce];
-        int shard[kAtOnce], col[kAtOnce];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          const int hk = h + k < end ? h + k : h;
-          shard[k] = A.magic[kind] ? static_cast<int>(__umulhi(static_cast<uint32_t>(hk), A.magic[kind])) : hk;
-          col[k] = (hk - shard[k] * A.heads[kind]) * A.d;
-          u[k] = v[k] = xu[k] = xv[k] = make_uint4(0, 0, 0, 0);
-          if (mine && counts) {
-            const __nv_bfloat16* p = A.in[kind][shard[k]] + tok * A.ld_in[kind] + col[k];
-            u[k] = load16(p + c0);
-            v[k] = load16(p + c1);
-            if constexpr (MODE == kBackward) {
-              const __nv_bfloat16* q = A.x[kind][shard[k]] + tok * A.ld_x[kind] + col[k];
-              xu[k] = load16(q + c0);
-              xv[k] = load16(q + c1);
-            }
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          float a[8], b[8], ya[8], yb[8];
-          to_pairs<NEIGHBOURS>(u[k], v[k], a, b);
+        for (; here > 0; --here, out += A.d) {
+          const uint4* ring_at = mine_at + get * (kWords<MODE> * 32);
+          get = get + 1 == S ? 0 : get + 1;
+          await_copies<S - 2>();
+          uint4 u = ring_at[0], v = ring_at[32];
+          const bool hide = !all_count && !counts;
+          if (MODE == kBackward && hide) u = v = make_uint4(0, 0, 0, 0);
+          Pairs y = to_pairs<NEIGHBOURS>(u, v);
           if constexpr (MODE == kForward) {
-            float ss = 0.0f;
+            uint64_t ss = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+            for (int i = 0; i < 4; ++i) ss = ffma2(y.a[i], y.a[i], ffma2(y.b[i], y.b[i], ss));
+            const float r = rsqrtf(fmaf(head_sum<LANES>(ss), inv_d, A.eps));
+            const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-            for (int o = LANES >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float r = rsqrtf(fmaf(ss, inv_d, A.eps));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              a[e] *= r * ga[e];
-              b[e] *= r * gb[e];
+            for (int i = 0; i < 4; ++i) {
+              y.a[i] = fmul2(fmul2(y.a[i], r2), ga.a[i]);
+              y.b[i] = fmul2(fmul2(y.b[i], r2), ga.b[i]);
             }
           }
-          if constexpr (MODE != kBackward) {
+          // the turn (backward: A.sign turned it back)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              ya[e] = fmaf(a[e], co[e], -b[e] * si[e]);
-              yb[e] = fmaf(b[e], co[e], a[e] * si[e]);
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t a = y.a[i], b = y.b[i];
+            y.a[i] = ffma2(a, co[i], fmul2(b, si[i] ^ 0x8000000080000000ull));
+            y.b[i] = ffma2(b, co[i], fmul2(a, si[i]));
+          }
+          if constexpr (MODE == kBackward) {
+            // y is g; with k = -r^2 mean(h n):  dx = (g r) gamma + x k,  dgamma += (g r) x
+            u = ring_at[64];
+            v = ring_at[96];
+            if (hide) u = v = make_uint4(0, 0, 0, 0);
+            const Pairs x = to_pairs<NEIGHBOURS>(u, v);
+            uint64_t ss = 0, dot = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ss = ffma2(x.a[i], x.a[i], ffma2(x.b[i], x.b[i], ss));
+              dot = ffma2(fmul2(y.a[i], ga.a[i]), x.a[i], ffma2(fmul2(y.b[i], ga.b[i]), x.b[i], dot));
             }
-          } else {
-            float na[8], nb[8];
-            to_pairs<NEIGHBOURS>(xu[k], xv[k], na, nb);
-            float ss = 0.0f, dot = 0.0f;
+            float r = rsqrtf(fmaf(head_sum<LANES>(ss), inv_d, A.eps));
+            if (hide) r = 0.0f;
+            const float k = -(head_sum<LANES>(dot) * inv_d) * r * r * r;
+            const uint64_t r2 = f2_pack(r, r), k2 = f2_pack(k, k);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float g0 = fmaf(a[e], co[e], b[e] * si[e]), g1 = fmaf(b[e], co[e], -a[e] * si[e]);
-              ss = fmaf(na[e], na[e], fmaf(nb[e], nb[e], ss));
-              a[e] = g0;
-              b[e] = g1;
-              dot = fmaf(g0 * ga[e], na[e], fmaf(g1 * gb[e], nb[e], dot));
-            }
-#pragma unroll
-            for (int o = LANES >> 1; o > 0; o >>= 1) {
-              ss += __shfl_xor_sync(0xffffffffu, ss, o);
-              dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            }
-            const float r = rsqrtf(fmaf(ss, inv_d, A.eps));
-            const float m = dot * r * inv_d;      // mean of h n
-            const bool add = counts && h + k < end;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              na[e] *= r;
-              nb[e] *= r;
-              acc[kind][e] += add ? a[e] * na[e] : 0.0f;
-              acc[kind][8 + e] += add ? b[e] * nb[e] : 0.0f;
-              ya[e] = r * fmaf(a[e], ga[e], -na[e] * m);
-              yb[e] = r * fmaf(b[e], gb[e], -nb[e] * m);
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t a = fmul2(y.a[i], r2), b = fmul2(y.b[i], r2);
+              acc[kind].a[i] = ffma2(a, x.a[i], acc[kind].a[i]);
+              acc[kind].b[i] = ffma2(b, x.b[i], acc[kind].b[i]);
+              y.a[i] = ffma2(a, ga.a[i], fmul2(x.a[i], k2));
+              y.b[i] = ffma2(b, ga.b[i], fmul2(x.b[i], k2));
             }
           }
-          if (!counts) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ya[e] = yb[e] = 0.0f;
-          }
-          if (mine && there && h + k < end) {
-            __nv_bfloat16* p = A.out[kind][shard[k]] + tok * A.ld_out[kind] + col[k];
-            store_pairs<NEIGHBOURS>(p + c0, p + c1, ya, yb);
+          fetch();                                // (into the place that was read a head ago)
+          to_words<NEIGHBOURS>(y, u, v);
+          if (hide) u = v = make_uint4(0, 0, 0, 0);
+          if (mine && there) {
+            *reinterpret_cast<uint4*>(out) = u;
+            *reinterpret_cast<uint4*>(out + step) = v;
           }
         }
       }
@@ -274,16 +406,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) head_rotary_kernel(const __gri
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float a = acc[kind][e], b = acc[kind][8 + e];
+      for (int i = 0; i < 8; ++i) {
+        float2 f = f2_unpack(i < 4 ? acc[kind].a[i] : acc[kind].b[i - 4]);
 #pragma unroll
         for (int o = 16; o >= LANES; o >>= 1) {
-          a += __shfl_xor_sync(0xffffffffu, a, o);
-          b += __shfl_xor_sync(0xffffffffu, b, o);
+          f.x += __shfl_xor_sync(0xffffffffu, f.x, o);
+          f.y += __shfl_xor_sync(0xffffffffu, f.y, o);
         }
         if (lane < LANES && mine) {
-          sums[warp][kind][NEIGHBOURS ? c0 + 2 * e : c0 + e] = a;
-          sums[warp][kind][NEIGHBOURS ? c0 + 2 * e + 1 : c1 + e] = b;
+          sums[warp][kind][column(i >= 4, i % 4 * 2)] = f.x;
+          sums[warp][kind][column(i >= 4, i % 4 * 2 + 1)] = f.y;
         }
       }
     __syncthreads();
@@ -291,26 +423,30 @@ __global__ void __launch_bounds__(kWarps * 32, 2) head_rotary_kernel(const __gri
       const int kind = i >= A.d, c = i - kind * A.d;
       float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += sums[w][kind][c];
+      for (int k = 0; k < kWarps; ++k) s += sums[k][kind][c];
       A.part[static_cast<int64_t>(blockIdx.x) * 2 * A.d + i] = s;
     }
   }
 }
 
-// dgamma from the blocks' sums, in their order: 32 columns a block, eight warps on every eighth row.
-__global__ void __launch_bounds__(256) head_join_kernel(const float* part, int rows, int d, float* dq, float* dk, int accumulate) {
-  __shared__ float sums[8][32];
+// dgamma from the blocks' sums: 32 columns a block, a warp on every 32nd row, the warps' sums in their order.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(kJoinWarps * 32) head_join_kernel(const float* part, int rows, int d, float* dq, float* dk,
+                                                                     int accumulate) {
+  __shared__ float sums[kJoinWarps][32];
   await_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.0f;
-  if (c < 2 * d)
-#pragma unroll 8
-    for (int r = warp; r < rows; r += 8) s += part[static_cast<int64_t>(r) * 2 * d + c];
+  if (c < 2 * d) {
+#pragma unroll 10
+    for (int r = warp; r < rows; r += kJoinWarps) s += __ldg(part + static_cast<int64_t>(r) * 2 * d + c);
+  }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < 2 * d) {
-    for (int w = 1; w < 8; ++w) s += sums[w][lane];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) s += sums[w][lane];
     float* out = c < d ? dq + c : dk + (c - d);
     *out = accumulate ? *out + s : s;
   }
@@ -322,38 +458,40 @@ int lanes_of(int d) {
   return l;
 }
 
-// Blocks of the backward launch, at most: what its workspace holds partial sums for.
-constexpr int kMaxBlocks = 2 * 152;
+// Blocks of a launch, at most: all that the card holds at once.
+template <int MODE>
+constexpr int kMaxBlocks = kResident<MODE> * 152;
 
-int blocks_of(int64_t items) {
-  const int64_t need = (items + kWarps - 1) / kWarps;
-  return static_cast<int>(need < kMaxBlocks ? need : kMaxBlocks);
-}
-
-// How the heads of a token group are cut: into ranges of no fewer than eight, more where the groups alone are too few
-// warps for the card.
-void cut_heads(HeadArgs& A) {
-  const int all = A.t * (A.heads[0] + A.heads[1]);
-  const int64_t groups = (A.T + 32 / lanes_of(A.d) - 1) / (32 / lanes_of(A.d));
-  const int64_t want = 152 * 2 * kWarps;
-  int64_t chunk = all * groups / want;
-  chunk = chunk < 2 ? 2 : (chunk > 8 ? 8 : chunk);
-  A.chunk = static_cast<int>(chunk < all ? chunk : all);
-  A.chunks = (all + A.chunk - 1) / A.chunk;
-  A.items = groups * A.chunks;
+// Deals out the work (fills A): returns the blocks.
+template <int MODE>
+unsigned deal(HeadArgs& A) {
+  const int tokens = 32 / lanes_of(A.d);
+  A.groups = (A.T + tokens - 1) / tokens;
+  const int64_t pairs = A.groups * A.t * (A.heads[0] + A.heads[1]), most = static_cast<int64_t>(kMaxBlocks<MODE>) * kWarps;
+  A.warps = pairs < most ? pairs : most;
+  return static_cast<unsigned>((A.warps + kWarps - 1) / kWarps);
 }
 
 template <int MODE>
-int launch(const HeadArgs& A, bool neighbours, unsigned grid, cudaStream_t s) {
+int launch(HeadArgs& A, bool neighbours, unsigned& grid, cudaStream_t s) {
+  grid = deal<MODE>(A);
   const double size = static_cast<double>(A.T) * A.t * (A.heads[0] + A.heads[1]) * A.d;
   TraceScope trace(s, TTL_K_NORM, 0.0, size * (MODE == kBackward ? 6.0 : 4.0));
-  auto go = [&](auto kernel) { return cuda_check(launch_first(kernel, dim3(grid), kWarps * 32, 0, s, A), "head_rotary_kernel launch"); };
+  auto go = [&](auto lanes) {
+    constexpr int L = decltype(lanes)::value;
+    auto run = [&](auto kernel) { return cuda_check(launch_first(kernel, dim3(grid), kWarps * 32, kRingBytes<MODE>, s, A), "head_rotary_kernel launch"); };
+    const char* what = "cudaFuncSetAttribute(head rotation)";
+    int rc = neighbours ? allow_smem<head_rotary_kernel<L, true, MODE>>(kRingBytes<MODE>, what)
+                        : allow_smem<head_rotary_kernel<L, false, MODE>>(kRingBytes<MODE>, what);
+    if (rc) return rc;
+    return neighbours ? run(head_rotary_kernel<L, true, MODE>) : run(head_rotary_kernel<L, false, MODE>);
+  };
   switch (lanes_of(A.d)) {
-    case 1: return neighbours ? go(head_rotary_kernel<1, true, MODE>) : go(head_rotary_kernel<1, false, MODE>);
-    case 2: return neighbours ? go(head_rotary_kernel<2, true, MODE>) : go(head_rotary_kernel<2, false, MODE>);
-    case 4: return neighbours ? go(head_rotary_kernel<4, true, MODE>) : go(head_rotary_kernel<4, false, MODE>);
-    case 8: return neighbours ? go(head_rotary_kernel<8, true, MODE>) : go(head_rotary_kernel<8, false, MODE>);
-    default: return neighbours ? go(head_rotary_kernel<16, true, MODE>) : go(head_rotary_kernel<16, false, MODE>);
+    case 1: return go(std::integral_constant<int, 1>{});
+    case 2: return go(std::integral_constant<int, 2>{});
+    case 4: return go(std::integral_constant<int, 4>{});
+    case 8: return go(std::integral_constant<int, 8>{});
+    default: return go(std::integral_constant<int, 16>{});
   }
 }
 
@@ -364,7 +502,7 @@ int check_shape(int t, int64_t T, int n_q, int n_kv, int d, const char* name) {
     return set_error(TTL_ERR_SHAPE, "%s: t=%d must divide the head counts %d and %d", name, t, n_q, n_kv);
   if (d % 16 || d > kMaxHead)
     return set_error(TTL_ERR_SHAPE, "%s: head dimension %d is not a multiple of 16 up to %d", name, d, kMaxHead);
-  if (T >= (int64_t(1) << 31) - 1 || n_q > 32768 || n_kv > 32768) return set_error(TTL_ERR_SHAPE, "%s: extent too large", name);
+  if (T >= (int64_t(1) << 31) - 64 || n_q > 32768 || n_kv > 32768) return set_error(TTL_ERR_SHAPE, "%s: extent too large", name);
   return TTL_OK;
 }
 
@@ -494,16 +632,14 @@ extern "C" int ttl_head_norm_rotary_fwd(int t, int64_t T, int n_q, int n_kv, int
   fill_mats(A, 0, Q, ldq, Qo, ldqo);
   fill_mats(A, 1, K, ldk, Ko, ldko);
   A.sign = 1.0f;
-  cut_heads(A);
-  const int64_t need = (A.items + kWarps - 1) / kWarps;
-  const unsigned grid = static_cast<unsigned>(need < (1 << 30) ? need : (1 << 30));
+  unsigned grid;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return gamma_q ? launch<kForward>(A, interleaved, grid, s) : launch<kTurn>(A, interleaved, grid, s);
 }
 
 extern "C" size_t ttl_head_norm_rotary_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d) {
   if (check_shape(t, T, n_q, n_kv, d, "ttl_head_norm_rotary_bwd_workspace_size")) return 0;
-  return static_cast<size_t>(kMaxBlocks) * 2 * d * 4;
+  return static_cast<size_t>(kMaxBlocks<kBackward>) * 2 * d * 4;
 }
 
 extern "C" int ttl_head_norm_rotary_bwd(int t, int64_t T, int n_q, int n_kv, int d, int rot, int interleaved,
@@ -582,11 +718,8 @@ extern "C" int ttl_head_norm_rotary_bwd(int t, int64_t T, int n_q, int n_kv, int
     if (!A.status) return TTL_ERR_CUDA;
     fill_mats(A, 0, dY_q, lddyq, dQ, lddq);
     fill_mats(A, 1, dY_k, lddyk, dK, lddk);
-    cut_heads(A);
+    A.sign = -1.0f;
     if (!norm) {
-      A.sign = -1.0f;
-      const int64_t need = (A.items + kWarps - 1) / kWarps;
-      grid = static_cast<unsigned>(need < (1 << 30) ? need : (1 << 30));
       return launch<kTurn>(A, interleaved, grid, s);
     }
     for (int i = 0; i < t; ++i) {
@@ -596,7 +729,6 @@ extern "C" int ttl_head_norm_rotary_bwd(int t, int64_t T, int n_q, int n_kv, int
     A.ld_x[0] = ldq;
     A.ld_x[1] = ldk;
     A.part = static_cast<float*>(ws);
-    grid = static_cast<unsigned>(blocks_of(A.items));
     if ((rc = launch<kBackward>(A, interleaved, grid, s))) return rc;
   }
   TraceScope trace(s, TTL_K_NORM, 0.0, 8.0 * d * grid);
@@ -604,7 +736,7 @@ extern "C" int ttl_head_norm_rotary_bwd(int t, int64_t T, int n_q, int n_kv, int
   const unsigned cols = static_cast<unsigned>((2 * d + 31) / 32);
   const float* part = A.part;
   const int rows = static_cast<int>(grid);
-  return cuda_check(grid ? launch_after(head_join_kernel, dim3(cols), 256, 0, s, part, rows, d, dgamma_q, dgamma_k, accumulate)
-                         : launch_first(head_join_kernel, dim3(cols), 256, 0, s, part, rows, d, dgamma_q, dgamma_k, accumulate),
+  return cuda_check(grid ? launch_after(head_join_kernel, dim3(cols), kJoinWarps * 32, 0, s, part, rows, d, dgamma_q, dgamma_k, accumulate)
+                         : launch_first(head_join_kernel, dim3(cols), kJoinWarps * 32, 0, s, part, rows, d, dgamma_q, dgamma_k, accumulate),
                     "head_join_kernel launch");
 }

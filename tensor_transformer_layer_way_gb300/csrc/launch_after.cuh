@@ -15,6 +15,10 @@ namespace ttl {
 // writes anything that kernel may still read.
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the following kernel's blocks be brought up from here on, where there is room for them; what they read still waits
+// for await_previous().
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A launch that begins when all before it is done: for the first kernel of a call, which knows nothing of the caller's.
 template <typename... Params, typename... Args>
 cudaError_t launch_first(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,

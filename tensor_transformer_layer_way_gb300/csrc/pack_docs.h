@@ -24,19 +24,27 @@ TTL_HOST_DEVICE int doc_bound(const int32_t* cu, int b) {
 #endif
 }
 
-// The document of token `tok` of a pack of T tokens, by bisection.  A token outside [0, T) is in none, also where the
+// The document of token `tok` of a pack of T tokens, by bisection of bounds that bound(b) reads.  A token outside [0, T) is in none, also where the
 // last document ends beyond T: a tile's rows behind the pack are asked for too.  Whatever cu holds, the answer is
 // empty or 0 <= lo <= tok < hi <= T: with entries out of order it is some document cut to the pack (the kernels
 // report such entries).
-TTL_HOST_DEVICE DocRange doc_of(const int32_t* cu, int batch, int T, int tok) {
-  if (batch == 0 || tok < 0 || tok >= T || tok < doc_bound(cu, 0) || tok >= doc_bound(cu, batch)) return DocRange{0, 0};
-  int l = 0, r = batch;        // cu[l] <= tok < cu[r]
+template <class Bound>
+TTL_HOST_DEVICE DocRange doc_among(const Bound& bound, int batch, int T, int tok) {
+  if (batch == 0 || tok < 0 || tok >= T || tok < bound(0) || tok >= bound(batch)) return DocRange{0, 0};
+  int l = 0, r = batch;        // bound(l) <= tok < bound(r)
   while (r - l > 1) {
     const int m = (l + r) >> 1;
-    if (doc_bound(cu, m) <= tok) l = m; else r = m;
+    if (bound(m) <= tok) l = m; else r = m;
   }
-  const int lo = doc_bound(cu, l), hi = doc_bound(cu, r);
+  const int lo = bound(l), hi = bound(r);
   return DocRange{lo < 0 ? 0 : lo, hi > T ? T : hi};
+}
+struct DocBounds {
+  const int32_t* cu;
+  TTL_HOST_DEVICE int operator()(int b) const { return doc_bound(cu, b); }
+};
+TTL_HOST_DEVICE DocRange doc_of(const int32_t* cu, int batch, int T, int tok) {
+  return doc_among(DocBounds{cu}, batch, T, tok);
 }
 
 // How long a wait may take, in ns.  Some warps wait for the whole of an item, whose steps (key tiles; for dK and dV query
