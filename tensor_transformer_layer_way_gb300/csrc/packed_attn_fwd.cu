@@ -450,13 +450,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         const int first = __ldg(A.cu), last = min(__ldg(A.cu + A.batch), T);
         d.v0 = max(qt.q0, first);
         d.v1 = min(qt.q0 + kTile, last);
-        d.lo = doc_of(A.cu, A.batch, T, d.v0).lo;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = qt.q0 + u * 32 + lane;
-          const bool begins = i > d.v0 && i < d.v1 && doc_of(A.cu, A.batch, T, i).lo == i;
-          d.begins[u] = __ballot_sync(0xffffffffu, begins);
-        }
+        const DocAt at = doc_at_warp(A.cu, A.batch, T, d.v0);
+        d.lo = at.range.lo;
+        begins_in_tile(A.cu, A.batch, at.doc, qt.q0, d.v0, d.v1, d.begins);
       }
       ok = wait_on(rows_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, abort_flag, status, tmo);
       if (!__all_sync(0xffffffffu, ok)) break;
