@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) head_join_kernel(const float*
   float s = 0.0f;
   if (c < 2 * d) {
 #pragma unroll 10
-    for (int r = warp; r < rows; r += kJoinWarps) s += __ldg(part + static_cast<int64_t>(r) * 2 * d + c);
+    for (int r = warp; r < rows; r += kJoinWarps) s += part[static_cast<int64_t>(r) * 2 * d + c];
   }
   sums[warp][lane] = s;
   __syncthreads();

@@ -74,28 +74,34 @@ size_t redo_bytes(int64_t T, int heads) { return static_cast<size_t>(heads) * ti
 size_t fwd_list_bytes(int64_t T) { return round256(static_cast<size_t>(tiles_of(T) + 1) * 16); }
 
 // Backward workspace: D, the query tiles by work, the key items by work with their counts, the key tiles that
-// several items share, those items' partial sums, and the rows that are computed again.
+// several items share, those items' partial sums, and the rows that are computed again; with a window the line of key
+// tiles too.
 struct BwdWs {
-  size_t q_list, kv_list, head, join, part, redo, total;   // offsets after D
+  size_t q_list, kv_list, head, shares, join, part, redo, total;   // offsets after D
 };
-BwdWs bwd_ws(int64_t T, int n_q, int n_kv, int d, int sinks) {
+BwdWs bwd_ws(int64_t T, int n_q, int n_kv, int d, int window, int sinks) {
   const int64_t tiles = tiles_of(T);
   const int grp = n_q / n_kv;
   // A cut leaves at most 2 steps / most parts of a tile and most >= all steps / kSplitItems: at most
   // 2 kSplitItems parts in all; and no part is shorter than kSplitSteps / 2.
   int64_t slots = 0;
-  if (pack_split(tiles, n_kv, grp, sinks)) {
+  if (pack_split(tiles, n_kv, grp)) {
     slots = 2 * kSplitItems / n_kv + 1;
     const int64_t most = tiles * (tiles * grp / kSplitSteps + 1);
     if (slots > most) slots = most;
   }
+  // (with a window: two parts a block)
+  const size_t parts = !window ? static_cast<size_t>(slots) * n_kv
+                               : (pack_shares(tiles, n_kv, grp, window, sinks) ? 2 * kShareBlocks : 0);
+  if (window) slots = 0;
   BwdWs w;
   w.q_list = round256(static_cast<size_t>(n_q) * T * 4);
   w.kv_list = w.q_list + round256(static_cast<size_t>(tiles) * 16);
   w.head = w.kv_list + round256(static_cast<size_t>(tiles + slots) * 32);
-  w.join = w.head + 256;
-  w.part = w.join + round256(static_cast<size_t>(tiles) * 16);
-  w.redo = w.part + static_cast<size_t>(slots) * n_kv * 2 * kTile * d * 4;
+  w.shares = w.head + 256;
+  w.join = w.shares + (window ? round256(sizeof(KvShares) + static_cast<size_t>(tiles + 1) * 8) : 0);
+  w.part = w.join + round256(static_cast<size_t>(window ? kShareBlocks : tiles) * 16);
+  w.redo = w.part + parts * 2 * kTile * d * 4;
   w.total = w.redo + redo_bytes(T, n_q > 2 * n_kv ? n_q : 2 * n_kv) + 256;   // (it starts on 256 bytes)
   return w;
 }
@@ -193,7 +199,7 @@ int attn_bwd(const char* name, View view, int t, int64_t T, int n_q, int n_kv, i
       (rc = check_mats(reinterpret_cast<CP>(dK), t, kc, lddk, "dK", name)) ||
       (rc = check_mats(reinterpret_cast<CP>(dV), t, kc, lddv, "dV", name)))
     return rc;
-  const BwdWs w = bwd_ws(T, n_q, n_kv, d, view.sinks);
+  const BwdWs w = bwd_ws(T, n_q, n_kv, d, view.window, view.sinks);
   const size_t need = w.total;
   if (!ws || ws_bytes < need)
     return set_error(TTL_ERR_ARG, "%s: workspace of %zu bytes needed, %zu given", name, need, ws_bytes);
@@ -233,7 +239,9 @@ int attn_bwd(const char* name, View view, int t, int64_t T, int n_q, int n_kv, i
   // Work lists where there are more items than SMs, or key tiles long enough to be cut; a batch below that
   // starts every item at once.
   const int64_t tiles = tiles_of(T);
-  const bool split = pack_split(tiles, n_kv, A.grp, view.sinks);
+  const bool window = view.window > 0;
+  const bool shares = window && pack_shares(tiles, n_kv, A.grp, view.window, view.sinks);
+  const bool split = window ? shares : pack_split(tiles, n_kv, A.grp);
   const bool listed = split || tiles * n_q > num_sms();
   PackPlan plan = {};
   char* base = reinterpret_cast<char*>(A.D);
@@ -242,13 +250,21 @@ int attn_bwd(const char* name, View view, int t, int64_t T, int n_q, int n_kv, i
     plan.q_list = reinterpret_cast<int4*>(base + w.q_list);
     plan.q_units = plan.tiles = static_cast<int>(tiles);
     plan.q_per = 1;
-    plan.kv_list = reinterpret_cast<int4*>(base + w.kv_list);
+    // (with a window whole tiles are a choice from two a block on; fewer never come out even)
+    if (!window || (shares && tiles * n_kv >= 2 * kShareBlocks)) plan.kv_list = reinterpret_cast<int4*>(base + w.kv_list);
     plan.kv_head = reinterpret_cast<int*>(base + w.head);
     plan.kv_taken = plan.kv_head + 2;
     plan.q_taken = plan.kv_head + 3;
     plan.join_list = reinterpret_cast<int4*>(base + w.join);
     plan.lanes = n_kv;
-    plan.split = split;
+    plan.split = split && !window;
+    if (shares) {
+      plan.cost = tile_cost(d);
+      plan.kv_shares = reinterpret_cast<KvShares*>(base + w.shares);
+      plan.kv_before = reinterpret_cast<long long*>(plan.kv_shares + 1);
+      plan.share_blocks = num_sms() < kShareBlocks ? num_sms() : kShareBlocks;
+      A.kv_shares = plan.kv_shares;
+    }
     A.q_list = plan.q_list;
     A.kv_list = plan.kv_list;
     A.kv_head = plan.kv_head;
@@ -282,7 +298,7 @@ extern "C" size_t ttl_packed_attn_fwd_workspace_size(int t, int64_t T, int n_q, 
 
 extern "C" size_t ttl_packed_attn_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch) {
   if (check_shape(t, T, n_q, n_kv, d, batch, "ttl_packed_attn_bwd_workspace_size")) return 0;
-  return bwd_ws(T, n_q, n_kv, d, 0).total;
+  return bwd_ws(T, n_q, n_kv, d, 0, 0).total;
 }
 
 extern "C" size_t ttl_packed_window_attn_fwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d, int batch,
@@ -297,7 +313,7 @@ extern "C" size_t ttl_packed_window_attn_bwd_workspace_size(int t, int64_t T, in
   const char* name = "ttl_packed_window_attn_bwd_workspace_size";
   View view = View::of(window, sinks);
   if (check_shape(t, T, n_q, n_kv, d, batch, name) || view.check(T, name)) return 0;
-  return bwd_ws(T, n_q, n_kv, d, view.sinks).total;
+  return bwd_ws(T, n_q, n_kv, d, view.window, view.sinks).total;
 }
 
 extern "C" int ttl_packed_attn_fwd(int t, int64_t T, int n_q, int n_kv, int d, int batch, const int32_t* cu_seqlens,

@@ -44,9 +44,25 @@ struct PackArgs {
   int* q_taken;                // items of a list that blocks took beyond their first; 0 at the start
   int* kv_taken;
   const int4* join_list;       // {key tile, first slot, parts, 0} of the key tiles that several items share
+  const struct KvShares* kv_shares;   // with a window, beside kv_list: the work as one line, cut evenly
   float* part;                 // partial dK and dV: [slot * KV heads + head][2][128][d]
   struct RedoEntry* redo;      // room for the rows that are computed again
 };
+
+// The key tiles of all KV heads, one head's after the other's, as a line of steps: tile t of a head lies at
+// [before[t], before[t + 1]), its own cost tile_cost(d) first and then its steps.  Block b of the launch works on an even share
+// [b total / blocks, (b + 1) total / blocks) of the line.  A tile that a border cuts is summed in parts: block b's
+// part of a tile that it continues has slot 2 b, of one that it begins and does not end slot 2 b + 1.
+struct KvShares {
+  long long head, total;       // a KV head's length, and all of them
+  int blocks, joins;           // 0 blocks: whole tiles from kv_list; cut tiles, in join_list: {key tile, slot of the first
+                               // part, parts, KV head}
+  int4 first[152];             // {KV head, key tile} where a block's share begins
+};
+constexpr int kShareBlocks = 152;
+// Of a tile beside its steps, in steps (measured: 8400 to 10400 of 2700 cycles, heads of 64 4800 of 3000).
+__host__ __device__ constexpr int tile_cost(int d) { return d == 128 ? 4 : 2; }
+constexpr int kLeastShare = 6; // and what a share is not cut below
 
 // A query unit: {unit, first key tile of its first token tile, of its second, 0}, -1 for a token tile without
 // keys; a tile's last key tile is its own.  With a window, in place of a first key tile: the first token of the
@@ -67,6 +83,10 @@ struct PackPlan {
   int* kv_head;
   int* kv_taken;
   int4* join_list;
+  KvShares* kv_shares;
+  long long* kv_before;        // [tiles + 1], behind kv_shares
+  int share_blocks;            // blocks of the dK, dV launch
+  int cost;                    // tile_cost
   int tiles, lanes;            // key tiles; KV heads over all shards
   int split;                   // key tiles may be cut into several items
 };
@@ -76,9 +96,9 @@ constexpr int kSplitSteps = 8;     // and no shorter than this
 int pack_attn_plan_launch(const PackArgs& A, const PackPlan& plan, int d, cudaStream_t stream);
 int pack_attn_join_launch(const PackArgs& A, int d, cudaStream_t stream);
 // Whether key tiles may be cut: few items, and long enough ones.  With eight items or more for each SM the
-// list's order alone evens the SMs out, unless some keys are seen from everywhere and the others from a window.
-inline bool pack_split(int64_t tiles, int lanes, int grp, int sinks) {
-  return (tiles * lanes < 8 * 152 || sinks > 0) && tiles * grp > 2 * kSplitSteps;
+// list's order alone evens the SMs out.
+inline bool pack_split(int64_t tiles, int lanes, int grp) {
+  return tiles * lanes < 8 * 152 && tiles * grp > 2 * kSplitSteps;
 }
 // Pairs of a query and a key that it sees, in one document of T tokens (the lengths are on the device).
 inline double pack_pairs(const PackArgs& A) {
@@ -101,6 +121,15 @@ constexpr int kTile = 128;       // tokens per query or key tile
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// With a window: whether the key tiles' work is dealt out in even shares.  Not where every tile has a block of its own and the
+// longest (of one document) is no longer than about a share, or short: a cut costs the write and the sum of its parts.
+inline bool pack_shares(int64_t tiles, int lanes, int grp, int window, int sinks) {
+  const int64_t seen = (window + kTile - 2) / kTile + 1;            // query tiles that see a key tile
+  const int64_t usual = (seen < tiles ? seen : tiles) * grp, longest = sinks > 0 ? tiles * grp : usual;
+  return tiles * lanes > kShareBlocks ||
+         (longest > 2 * kSplitSteps && 3 * longest * kShareBlocks > 4 * tiles * lanes * usual);
+}
 
 // ---- windows
 // With a window (W) the query at token i of a document that begins at lo sees the keys [near, i] and, before these, the
@@ -307,18 +336,33 @@ __device__ __forceinline__ uint32_t bits_between(int a, int b) {
   return m;
 }
 
-// 32 fp32 bit patterns of a row as bf16 to 64 bytes of global memory: whole 32-byte sectors where the row allows.
-__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* out, const uint32_t (&o)[32]) {
-  uint32_t w[16];
+// 32 rows of 32 fp32 values, a row a thread, as bf16 to rows of stride ld (16-byte aligned), of which the first `rows`
+// exist.  Groups of four lanes exchange their rows' 16-byte words, so that a store instruction covers 64 bytes of
+// eight rows.  (32 bytes of 32 rows at a time: 84 cycles an instruction, 2700 for a query tile's dQ of 128 columns.)
+__device__ __forceinline__ void store_rows_bf16x32(__nv_bfloat16* at, int64_t ld, int rows, const uint32_t (&o)[32]) {
+  const int lane = threadIdx.x & 31;
+  uint32_t w[4][4];                    // word q of the lane's row; then of row 4 (lane / 4) + q the lane's word
 #pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-  if ((reinterpret_cast<uintptr_t>(out) & 31) == 0) {
-    st_global_v8(out, w);
-    st_global_v8(out + 16, w + 8);
-  } else {
+  for (int e = 0; e < 16; ++e) w[e >> 2][e & 3] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      *reinterpret_cast<uint4*>(out + u * 8) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+  for (int far = 1; far <= 2; far <<= 1) {
+    const bool up = lane & far;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q & far) continue;           // places q and q + far
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[q][e] : w[q + far][e], far);
+        if (up) w[q][e] = got;
+        else w[q + far][e] = got;
+      }
+    }
+  }
+  at += (lane & 3) * 8;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = (lane & ~3) + q;
+    if (row < rows) *reinterpret_cast<uint4*>(at + row * ld) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
   }
 }
 

@@ -71,10 +71,46 @@ __device__ __forceinline__ KvItem listed_item(const KvParams& P, int at) {
   return KvItem{ln / A.nkvl, ln % A.nkvl, e.x * kTile, e.y, e.z, e.w - e.z, slot < 0 ? -1 : slot * P.lanes + ln};
 }
 
-// A block's first item (of `total`), found by a whole warp.
-template <bool W>
-__device__ __forceinline__ KvItem first_item(const KvParams& P, int total) {
+// The block's item in its share of the line at or behind key tile `tile` of KV head `head` (which become the place behind
+// it); shard < 0: none.
+template <int D>
+__device__ __forceinline__ KvItem share_item(const KvParams& P, int& head, int& tile) {
+  constexpr int kCost = tile_cost(D);
   const PackArgs& A = P.a;
+  const KvShares& S = *A.kv_shares;
+  const long long* before = reinterpret_cast<const long long*>(&S + 1);
+  const int b = static_cast<int>(blockIdx.x), blocks = __ldg(&S.blocks);
+  const long long total = __ldg(&S.total), per = __ldg(&S.head);
+  const long long p0 = total * b / blocks, p1 = total * (b + 1) / blocks;
+  while (b < blocks && head < P.lanes) {
+    const long long at = head * per + __ldg(before + tile), end = head * per + __ldg(before + tile + 1);
+    if (at >= p1) break;
+    const int k = tile, ln = head;
+    if (++tile == P.tiles) {
+      tile = 0;
+      ++head;
+    }
+    // the share's steps of the tile; a tile without steps belongs to the share in which it begins
+    const long long from = p0 - at - kCost, to = (p1 < end ? p1 : end) - at - kCost;
+    const int steps = static_cast<int>(end - at - kCost);
+    const int s0 = from > 0 ? static_cast<int>(from < steps ? from : steps) : 0, s1 = to > 0 ? static_cast<int>(to) : 0;
+    if (steps == 0 ? p0 <= at : s1 > s0) {
+      const int slot = s0 > 0 ? 2 * b : (s1 < steps ? 2 * b + 1 : -1);
+      return KvItem{ln / A.nkvl, ln % A.nkvl, k * kTile, k + steps / A.grp - 1, s0, s1 - s0, slot};
+    }
+  }
+  return KvItem{-1, 0, 0, 0, 0, 0, -1};
+}
+
+// A block's first item (of `total`), found by a whole warp.
+template <int D, bool W>
+__device__ __forceinline__ KvItem first_item(const KvParams& P, int total, bool shares) {
+  const PackArgs& A = P.a;
+  if (W && shares) {
+    const int4 e = __ldg(&A.kv_shares->first[blockIdx.x]);
+    int head = e.x, tile = e.y;
+    return share_item<D>(P, head, tile);
+  }
   const int at = static_cast<int>(blockIdx.x), ln = at % P.lanes, tile = at / P.lanes;
   if (at >= total) return KvItem{-1, 0, 0, 0, 0, 0, -1};
   if (A.kv_list) return listed_item(P, at);
@@ -184,6 +220,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   }
   await_previous();   // (the dQ kernel; through it D and the list)
   const int total = (A.kv_list ? __ldg(A.kv_head) : P.tiles) * P.lanes;
+  const bool shares = W && A.kv_shares && __ldg(&A.kv_shares->blocks) > 0;
   int* status = A.status;
   const uint64_t tmo = P.timeout_ns;
   const ItemQueue<KvItem> queue{reinterpret_cast<KvItem*>(smem + C::OFF_BAR + 336), item_bars, abort_flag, status, tmo};
@@ -235,12 +272,23 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // ------------------------------------------------------------------ TMA loads
     bool ok = true;
     int nk = 0, nv = 0, pos = 0;   // loads started: K, V, ring places
-    KvItem it = first_item<W>(P, total);
+    KvItem it = first_item<D, W>(P, total, shares);
+    int head = 0, tile = 0;        // behind `it` in the block's share
+    if (W && shares && it.shard >= 0) {
+      head = it.shard * A.nkvl + it.g;
+      tile = it.k0 / kTile + 1;
+      if (tile == P.tiles) {
+        tile = 0;
+        ++head;
+      }
+    }
     for (int n = 0; lane == 0 && ok && it.shard >= 0; ++n) {
       KvItem coming = {};
       coming.shard = -1;
       auto announce = [&]() {
-        if (A.kv_list) {
+        if (W && shares) {
+          coming = share_item<D>(P, head, tile);
+        } else if (A.kv_list) {
           const int at = static_cast<int>(gridDim.x) + atomicAdd(A.kv_taken, 1);
           if (at < total) coming = listed_item(P, at);
         }
@@ -319,7 +367,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       for (int kk = 0; kk < kTile / 16; ++kk)
         umma_bf16_ts(dst, acol + (kk >> 1) * 32 + (kk & 1) * 8, desc_advance(bd, kk * 2048), idesc_acc, kk ? 1u : more);
     };
-    KvItem it = first_item<W>(P, total);
+    KvItem it = first_item<D, W>(P, total, shares);
     for (int n = 0; queue.next(n, it) && it.shard >= 0; ++n) {
       if (it.steps == 0) continue;
       wait(k_full, ni);
@@ -382,7 +430,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     // ------------------------------------------------------------------ lse and D of each step's queries
     bool ok = true;
     int pos = 0;
-    KvItem it = first_item<W>(P, total);
+    KvItem it = first_item<D, W>(P, total, shares);
     for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       const float* lse = A.s[it.shard].lse;
       const float* Dr = A.D + static_cast<int64_t>(it.shard) * A.nql * A.T;
@@ -414,7 +462,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   } else if (warp == 3) {
     // ------------------------------------------------------------------ last queries of the coming item's keys
     bool ok = true;
-    KvItem it = first_item<W>(P, total);
+    KvItem it = first_item<D, W>(P, total, shares);
     for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       int hi[4];
 #pragma unroll
@@ -443,7 +491,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
     bool ok = true;
     int pos = 0, ni = 0;
     uint32_t met = 0;
-    KvItem it = first_item<W>(P, total);
+    KvItem it = first_item<D, W>(P, total, shares);
     for (int n = 0; ok && queue.next(n, it) && it.shard >= 0; ++n) {
       const PackShard& S = A.s[it.shard];
       const int key = it.k0 + r;
@@ -548,9 +596,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       }
       float bad = 0.0f;   // becomes NaN with the first value that is not finite
       const float f = kind || it.slot >= 0 ? 1.0f : A.scale;
-      const int64_t off = (kind ? A.lddv : A.lddk) * static_cast<int64_t>(key < T ? key : 0) + it.g * D + col;
-      __nv_bfloat16* out = (kind ? S.dv : S.dk) + off;
-      float* part = A.part + ((static_cast<int64_t>(it.slot < 0 ? 0 : it.slot) * 2 + kind) * kTile + r) * D + col;
+      const int row0 = it.k0 + quad * 32;
+      const int64_t ld = kind ? A.lddv : A.lddk;
+      __nv_bfloat16* out = (kind ? S.dv : S.dk) + ld * (row0 < T ? row0 : 0) + it.g * D + col;
+      // (partial sums: eight columns of all 128 rows lie together, a row's 32 bytes beside the next row's)
+      float* part = A.part + ((static_cast<int64_t>(it.slot < 0 ? 0 : it.slot) * 2 + kind) * D + col) * kTile + r * 8;
 #pragma unroll
       for (int u = 0; u < D / 64; ++u) {
         uint32_t o[32];
@@ -568,9 +618,9 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         }
         if (it.slot >= 0) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) st_global_v8(part + u * 32 + q * 8, o + q * 8);
-        } else if (key < T) {
-          store_bf16x32(out + u * 32, o);
+          for (int q = 0; q < 4; ++q) st_global_v8(part + (u * 32 + q * 8) * kTile, o + q * 8);
+        } else if (row0 < T) {
+          store_rows_bf16x32(out + u * 32, ld, T - row0, o);
         }
       }
       tc_fence_before_sync();
@@ -602,52 +652,69 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
   if (warp >= 4 && redo_list->count > 0 && !*abort_flag) redo_rows<D, W>(A, *redo_list, warp - 4, kKvWarps, lane);
 }
 
-// Adds up the parts of the key tiles that several items shared, in the order of their steps: one warp per row
-// of dK or dV, eight rows of a tile per block.
+// Adds up the parts of the key tiles that several items shared, in the order of their steps: 32 rows of dK or dV of a
+// tile per block, 16 columns of a row per thread.
 template <int D, bool W>
-__global__ void __launch_bounds__(256, 4) pack_join_kernel(const __grid_constant__ PackArgs A) {
-  __shared__ uint32_t redo[2];       // rows of the eight whose sums are not finite; of the eight before, spent
+__global__ void __launch_bounds__(2 * D) pack_join_kernel(const __grid_constant__ PackArgs A) {
+  constexpr int kRowWarps = 2 * D / 32;   // a warp's rows are the block's, its columns 16 of D
+  __shared__ uint32_t redo;               // rows whose sums are not finite
   await_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = A.t * A.nkvl;
-  const int64_t rows = static_cast<int64_t>(__ldg(A.kv_head + 1)) * lanes * 2 * kTile;
-  if (threadIdx.x < 2) redo[threadIdx.x] = 0;
-  __syncthreads();
-  int now = 0;
-  for (int64_t w0 = static_cast<int64_t>(blockIdx.x) * 8; w0 < rows; w0 += gridDim.x * 8, now ^= 1) {
-    const int r0 = static_cast<int>(w0 % kTile), half = static_cast<int>(w0 / kTile) & 1, r = r0 + warp;
-    const int64_t at = w0 / (2 * kTile);
-    const int ln = static_cast<int>(at % lanes);
-    const int4 e = __ldg(A.join_list + at / lanes);
-    const int key0 = e.x * kTile + r0, key = key0 + warp;
+  const bool shares = W && A.kv_shares;
+  const int64_t pieces = (shares ? static_cast<int64_t>(__ldg(&A.kv_shares->joins)) : static_cast<int64_t>(__ldg(A.kv_head + 1)) * lanes) * 8;
+  for (int64_t w = blockIdx.x; w < pieces; w += gridDim.x) {
+    const int r0 = static_cast<int>(w & 3) * 32, half = static_cast<int>(w >> 2) & 1;
+    const int64_t at = w >> 3;
+    const int4 e = __ldg(A.join_list + (shares ? at : at / lanes));
+    const int ln = shares ? e.w : static_cast<int>(at % lanes);
+    const int key0 = e.x * kTile + r0, key = key0 + lane;
     const int shard = ln / A.nkvl, g = ln % A.nkvl;
     const PackShard& S = A.s[shard];
-    if (key < A.T) {
-      RowVec<D> acc = row_zero<D>();
-      for (int p = 0; p < e.z; ++p) {
-        const float* src = A.part + ((static_cast<int64_t>(e.y + p) * lanes + ln) * 2 + half) * kTile * D +
-                           static_cast<int64_t>(r) * D + lane * (D / 32);
+    if (threadIdx.x == 0) redo = 0;
+    __syncthreads();
+    float acc[16];
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u) acc.x[u] += src[u];
-      }
-      bool fine = true;
+    for (int u = 0; u < 16; ++u) acc[u] = 0.0f;
+    // (the slots of a tile's parts: one for each KV head behind the other, or its blocks')
+    const int64_t size = 2 * kTile * D;
+    const float* first = A.part + (shares ? e.y : static_cast<int64_t>(e.y) * lanes + ln) * size + half * (kTile * D) +
+                         warp * (16 * kTile) + (r0 + lane) * 8;
+#pragma unroll 4
+    for (int p = 0; p < e.z; ++p) {
+      const float* src = first + (shares ? (p ? 2 * p - 1 : 0) : static_cast<int64_t>(p) * lanes) * size;
 #pragma unroll
-      for (int u = 0; u < D / 32; ++u) {
-        if (half == 0) acc.x[u] *= A.scale;
-        fine &= fabsf(acc.x[u]) < INFINITY;
+      for (int u = 0; u < 16; u += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src + (u >> 3) * (8 * kTile) + (u & 7));
+        acc[u] += v.x;
+        acc[u + 1] += v.y;
+        acc[u + 2] += v.z;
+        acc[u + 3] += v.w;
       }
-      row_store<D>((half ? S.dv + key * A.lddv : S.dk + key * A.lddk) + g * D, acc, lane);
-      if (!__all_sync(0xffffffffu, fine) && lane == 0) atomicOr(&redo[now], 1u << warp);
     }
-    __syncthreads();                 // (and all eight rows are stored)
-    uint32_t again = redo[now];
-    if (threadIdx.x == 0) redo[now ^ 1] = 0;
-    if (again && warp < 8 / kRedoRows) {
-      again &= ((1u << kRedoRows) - 1) << (warp * kRedoRows);
+    bool fine = true;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      if (half == 0) acc[u] *= A.scale;
+      fine &= fabsf(acc[u]) < INFINITY;
+    }
+    if (key < A.T) {
+      __nv_bfloat16* out = (half ? S.dv + key * A.lddv : S.dk + key * A.lddk) + g * D + warp * 16;
+#pragma unroll
+      for (int u = 0; u < 16; u += 8)
+        *reinterpret_cast<uint4*>(out + u) = make_uint4(pack_bf16x2(acc[u], acc[u + 1]), pack_bf16x2(acc[u + 2], acc[u + 3]),
+                                                        pack_bf16x2(acc[u + 4], acc[u + 5]), pack_bf16x2(acc[u + 6], acc[u + 7]));
+    }
+    const uint32_t bad = __ballot_sync(0xffffffffu, !fine && key < A.T);
+    if (bad && lane == 0) atomicOr(&redo, bad);
+    __syncthreads();                 // (and all rows are stored)
+    uint32_t again = redo;
+    KeyEdges edges;
+    bool looked = false;
+    for (int k = 0; again; ++k) {
       int j[kRedoRows];
-      KeyEdges edges;
-      bool looked = false;
-      if (redo_take(again, key0, j) > 0) redo_keys<D, W>(A, shard, g, j, half == 0, edges, looked, lane);
+      redo_take(again, key0, j);
+      if (k % kRowWarps == warp) redo_keys<D, W>(A, shard, g, j, half == 0, edges, looked, lane);
     }
     __syncthreads();
   }
@@ -658,7 +725,7 @@ __global__ void __launch_bounds__(256, 4) pack_join_kernel(const __grid_constant
 int pack_attn_join_launch(const PackArgs& A, int d, cudaStream_t stream) {
   TraceScope trace(stream, TTL_K_OTHER, 0.0, 0.0);
   const unsigned grid = static_cast<unsigned>(num_sms()) * 4;
-  auto run = [&](auto kernel) { return cuda_check(launch_after(kernel, dim3(grid), 256, 0, stream, A), "pack_join_kernel launch"); };
+  auto run = [&](auto kernel) { return cuda_check(launch_after(kernel, dim3(grid), 2 * d, 0, stream, A), "pack_join_kernel launch"); };
   if (d == 128) return A.window ? run(pack_join_kernel<128, true>) : run(pack_join_kernel<128, false>);
   return A.window ? run(pack_join_kernel<64, true>) : run(pack_join_kernel<64, false>);
 }
@@ -674,7 +741,8 @@ int pack_attn_dkv_launch(const PackArgs& A, const PackMaps& maps, int d, cudaStr
   const int64_t items = static_cast<int64_t>(P.tiles) * P.lanes;
   if (items >= (int64_t(1) << 30)) return set_error(TTL_ERR_SHAPE, "packed attention: too many key tiles");
   const int sms = num_sms();
-  const unsigned grid = static_cast<unsigned>(items < sms && !A.kv_list ? items : sms);
+  unsigned grid = static_cast<unsigned>(items < sms && !A.kv_list ? items : sms);
+  if (A.window) grid = static_cast<unsigned>(A.kv_shares ? (sms < kShareBlocks ? sms : kShareBlocks) : items);   // (items: kShareBlocks at most)
   TraceScope trace(stream, TTL_K_ATTN_CORE, 4.0 * pack_pairs(A) * d * A.nql * A.t, 2.0 * A.T * (2.0 * qc + 4.0 * kc) * A.t);
   auto run = [&](auto width, auto window) {
     constexpr int D = decltype(width)::value;

@@ -547,7 +547,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           bad = fmaf(v, 0.0f, bad);
           o[e] = __float_as_uint(v);
         }
-        if (i < T) store_bf16x32(S.dq + i * A.lddq + it.c * D + g * 32, o);
+        const int row0 = it.q0 + quad * 32;
+        if (row0 < T) store_rows_bf16x32(S.dq + row0 * A.lddq + it.c * D + g * 32, A.lddq, T - row0, o);
       }
       if (computed) {
         tc_fence_before_sync();

@@ -1,12 +1,17 @@
 // Work lists of the packed attention kernels.
 //
 // A query tile's work is the number of key tiles it meets, a key tile's the number of (query tile, head) steps;
-// both depend on the documents, which only the device knows.  One CTA sorts the tiles by work, heaviest first
-// (a counting sort; tiles of equal work in any order), so that the persistent kernels, which take items in
+// both depend on the documents, which only the device knows.  One CTA sorts the query tiles, one the key tiles, by work, heaviest
+// first (a counting sort; tiles of equal work in any order), so that the persistent kernels, which take items in
 // turn, end together, and cuts the longest key tiles into several items where there are few.  Worth it only
 // when there are more items than SMs; below that every item starts at once.  The backward pass's launch also takes
 // D = rowsum(dO o) of every row and head, in the other CTAs: the sort is hidden under it
 // (8192 tokens, 32 heads of 128: 134 MB in 23 us, 86% of the copy rate; the sort alone takes 5).
+//
+// With a window key tiles are also laid end to end and cut into even shares (KvShares): most are as long as the window,
+// so whole tiles may leave a part of the SMs idle at the end, and those with sinks are far longer.  Where whole
+// tiles in the list's order should end sooner than shares, which cost each block a part more, they are kept (8192
+// tokens in 12 documents, window 1024: dK, dV in 137 us, in shares 150).
 
 #include "packed_attn.cuh"
 
@@ -15,8 +20,16 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
+// Document bounds in shared memory, where there are few (a look-up in memory takes microseconds).
+constexpr int kNearDocs = 1024;
+__device__ __forceinline__ DocRange doc_near(const PackArgs& A, const int32_t* near, int tok) {
+  const int T = static_cast<int>(A.T);
+  if (A.batch > kNearDocs) return doc_of(A.cu, A.batch, T, tok);
+  return doc_among([&](int b) { return near[b]; }, A.batch, T, tok);
+}
+
 // First key tile that token tile `tile` meets (with a window: the first token of the document it begins in), or -1.
-__device__ __forceinline__ int first_of(const PackArgs& A, int tile) {
+__device__ __forceinline__ int first_of(const PackArgs& A, const int32_t* near, int tile) {
   const int T = static_cast<int>(A.T);
   if (A.batch == 0 || static_cast<int64_t>(tile) * kTile >= A.T) return -1;
   const int q0 = tile * kTile, first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
@@ -24,7 +37,7 @@ __device__ __forceinline__ int first_of(const PackArgs& A, int tile) {
   int v1 = q0 + kTile < last ? q0 + kTile : last;
   v1 = v1 < T ? v1 : T;
   if (v0 >= v1) return -1;
-  const int lo = doc_of(A.cu, A.batch, T, v0).lo;
+  const int lo = doc_near(A, near, v0).lo;
   return A.window ? lo : lo / kTile;
 }
 // Key tiles of token tile `tile`, of which first_of said `first`.
@@ -36,7 +49,7 @@ __device__ __forceinline__ int tiles_met(const PackArgs& A, int tile, int first)
 }
 
 // Last query tile that key tile `tile` meets, or tile - 1.
-__device__ __forceinline__ int last_tile_of(const PackArgs& A, int tile) {
+__device__ __forceinline__ int last_tile_of(const PackArgs& A, const int32_t* near, int tile) {
   const int T = static_cast<int>(A.T);
   if (A.batch == 0) return tile - 1;
   const int k0 = tile * kTile, first = __ldg(A.cu), last = __ldg(A.cu + A.batch);
@@ -44,7 +57,7 @@ __device__ __forceinline__ int last_tile_of(const PackArgs& A, int tile) {
   int v1 = k0 + kTile < last ? k0 + kTile : last;
   v1 = v1 < T ? v1 : T;
   if (v0 >= v1) return tile - 1;
-  const DocRange doc = doc_of(A.cu, A.batch, T, v1 - 1);
+  const DocRange doc = doc_near(A, near, v1 - 1);
   return A.window ? last_query_tile<true>(A, doc, k0, v1) : last_query_tile<false>(A, doc, k0, v1);
 }
 
@@ -70,6 +83,79 @@ __device__ __forceinline__ void to_places(int* hist, int* warp_tot) {
 __device__ __forceinline__ int work_class(int work, int shift) {
   const int c = work >> shift;
   return c < kPlanThreads ? c : kPlanThreads - 1;
+}
+
+// Lays the key tiles end to end and cuts the line.  Every thread calls it; scan holds 33 values.
+__device__ __forceinline__ void lay_out(const PackArgs& A, const PackPlan& P, const int32_t* near, long long* scan, int* joins,
+                                        unsigned long long* whole) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long* before = P.kv_before;
+  long long done = 0;
+  for (int t0 = 0; t0 < P.tiles; t0 += kPlanThreads) {
+    const int t = t0 + tid;
+    const long long mine =
+        t < P.tiles ? P.cost + static_cast<long long>(last_tile_of(A, near, t) - t + 1) * A.grp : 0;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    long long base = done;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) base += scan[w];
+      done += scan[w];
+    }
+    if (t < P.tiles) before[t] = base + inc - mine;
+  }
+  if (tid == 0) {
+    before[P.tiles] = done;
+    *joins = 0;
+    *whole = 0;
+  }
+  __syncthreads();
+  // How long whole tiles take at least: some block gets k + 1 of the k blocks + 1 longest.
+  const long long items = P.kv_list ? static_cast<long long>(P.tiles) * P.lanes : 0;
+  for (long long k = tid; k * P.share_blocks < items; k += kPlanThreads) {
+    const int4 e = P.kv_list[2 * (k * P.share_blocks / P.lanes)];
+    atomicMax(whole, static_cast<unsigned long long>((k + 1) * (P.cost + e.w - e.z)));
+  }
+  __syncthreads();
+  const long long total = done * P.lanes;
+  const long long most = total / kLeastShare;
+  const int blocks = most < P.share_blocks ? (most < 1 ? 1 : static_cast<int>(most)) : P.share_blocks;
+  KvShares* S = P.kv_shares;
+  if (tid < blocks) {
+    const long long p = total * tid / blocks;
+    const int head = static_cast<int>(p / done);
+    const long long r = p - head * done;
+    int l = 0, h = P.tiles;              // before[l] <= r < before[h]
+    while (h - l > 1) {
+      const int m = (l + h) >> 1;
+      if (before[m] <= r) l = m; else h = m;
+    }
+    S->first[tid] = make_int4(head, l, 0, 0);
+    // The border cuts tile l where some steps lie on both sides.  Of the borders that cut it the first one lists it.
+    const long long at = head * done + before[l], steps = before[l + 1] - before[l] - P.cost;
+    const long long cut = p - at - P.cost;
+    if (tid > 0 && cut > 0 && total * (tid - 1) / blocks - at - P.cost <= 0) {
+      int parts = 2;
+      while (tid + parts - 1 < blocks && total * (tid + parts - 1) / blocks - at - P.cost < steps) ++parts;
+      P.join_list[atomicAdd(joins, 1)] = make_int4(l, 2 * tid - 1, parts, head);
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    S->head = done;
+    S->total = total;
+    // (a share's part more, and the launch of the join)
+    const bool keep = P.kv_list && *whole * blocks <= static_cast<unsigned long long>(total + static_cast<long long>(2 * P.cost) * blocks);
+    S->blocks = keep ? 0 : blocks;
+    S->joins = keep ? 0 : *joins;
+  }
 }
 
 // D of one token of one shard, all its heads, by a warp: 256 columns at a time, d / 8 lanes for each head.
@@ -104,24 +190,31 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
   __shared__ int warp_tot[32];
   __shared__ unsigned long long total;
   __shared__ int taken, joins, longest;
+  __shared__ long long scan[kPlanThreads / 32];
+  __shared__ int32_t near[kNearDocs + 1];
   const int tid = threadIdx.x;
-  if (blockIdx.x > 0) {
-    const unsigned shard = (blockIdx.x - 1) / blocks;
-    const int64_t i = static_cast<int64_t>(blockIdx.x - 1 - shard * blocks) * (kPlanThreads / 32) + (tid >> 5);
+  if (blockIdx.x > 1) {
+    const unsigned shard = (blockIdx.x - 2) / blocks;
+    const int64_t i = static_cast<int64_t>(blockIdx.x - 2 - shard * blocks) * (kPlanThreads / 32) + (tid >> 5);
     if (i < A.T) {
       if (d == 128) row_dots<128>(A, static_cast<int>(shard), i);
       else row_dots<64>(A, static_cast<int>(shard), i);
     }
     return;
   }
-  if (P.q_list) {
+  if (A.batch <= kNearDocs) {
+    for (int i = tid; i <= A.batch; i += kPlanThreads) near[i] = __ldg(A.cu + i);
+  }
+  __syncthreads();
+  // block 0 the query tiles, block 1 the key tiles
+  if (P.q_list && blockIdx.x == 0) {
     if (tid == 0) *P.q_taken = 0;
     hist[tid] = 0;
     __syncthreads();
     for (int pass = 0; pass < 2; ++pass) {
       for (int u = tid; u < P.q_units; u += kPlanThreads) {
         const int t0 = u * P.q_per;
-        const int a = first_of(A, t0), b = P.q_per == 2 ? first_of(A, t0 + 1) : -1;
+        const int a = first_of(A, near, t0), b = P.q_per == 2 ? first_of(A, near, t0 + 1) : -1;
         const int work = tiles_met(A, t0, a) + tiles_met(A, t0 + 1, b);
         const int at = atomicAdd(&hist[work_class(work, q_shift)], 1);
         if (pass) P.q_list[at] = make_int4(u, a, b, 0);
@@ -130,7 +223,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     }
     __syncthreads();
   }
-  if (P.kv_list) {
+  if (P.kv_list && blockIdx.x == 1) {
     hist[tid] = 0;
     if (tid == 0) {
       total = 0;
@@ -140,12 +233,14 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     unsigned long long sum = 0;
     int most_here = 0;
     for (int t = tid; t < P.tiles; t += kPlanThreads) {
-      const int steps = (last_tile_of(A, t) - t + 1) * A.grp;
+      const int steps = (last_tile_of(A, near, t) - t + 1) * A.grp;
       sum += static_cast<unsigned long long>(steps);
       most_here = steps > most_here ? steps : most_here;
     }
-    atomicAdd(&total, sum);
-    atomicMax(&longest, most_here);
+    if (sum) {
+      atomicAdd(&total, sum);
+      atomicMax(&longest, most_here);
+    }
     __syncthreads();
     // Where a whole key tile would be more than an SM's share of all steps, no item is longer than a third of
     // that share.  (A part costs a write and a read of its fp32 sums: with every tile below the share,
@@ -157,7 +252,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     }
     for (int pass = 0; pass < 2; ++pass) {
       for (int t = tid; t < P.tiles; t += kPlanThreads) {
-        const int last = last_tile_of(A, t);
+        const int last = last_tile_of(A, near, t);
         const int steps = (last - t + 1) * A.grp;
         const int parts = steps > 0 ? static_cast<int>((steps + most - 1) / most) : 1;
         const int len = (steps + parts - 1) / parts;
@@ -184,18 +279,20 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     // the number of entries: all places given out
     int entries = 0;
     for (int t = tid; t < P.tiles; t += kPlanThreads) {
-      const int steps = (last_tile_of(A, t) - t + 1) * A.grp;
+      const int steps = (last_tile_of(A, near, t) - t + 1) * A.grp;
       entries += steps > 0 ? static_cast<int>((steps + most - 1) / most) : 1;
     }
     if (tid == 0) taken = 0;
     __syncthreads();
-    atomicAdd(&taken, entries);
+    if (entries) atomicAdd(&taken, entries);
     __syncthreads();
     if (tid == 0) {
       P.kv_head[0] = taken;
       *P.kv_taken = 0;
     }
+    __syncthreads();
   }
+  if (P.kv_shares && blockIdx.x == 1) lay_out(A, P, near, scan, &joins, &total);
 }
 
 }  // namespace
@@ -209,7 +306,7 @@ int pack_attn_plan_launch(const PackArgs& A, const PackPlan& plan, int d, cudaSt
   const int64_t rows = d > 0 ? A.t * A.T : 0;
   TraceScope trace(stream, TTL_K_OTHER, 0.0, 32.0 * tiles + 4.0 * rows * A.nql * d);
   const unsigned blocks = d > 0 ? static_cast<unsigned>((A.T + kPlanThreads / 32 - 1) / (kPlanThreads / 32)) : 0;
-  const unsigned grid = 1 + blocks * A.t;
+  const unsigned grid = 2 + blocks * A.t;
   pack_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(A, plan, q_shift, kv_shift, d, blocks);
   return cuda_check(cudaGetLastError(), "pack_plan_kernel launch");
 }
