@@ -336,6 +336,57 @@ __device__ __forceinline__ uint32_t bits_between(int a, int b) {
   return m;
 }
 
+// Bit e of a word as a mask of element e: bit 8 j + k stands in the sign of byte j of the word shifted left by 7 - k, which
+// one byte permutation spreads.
+struct SeenBits {
+  uint32_t y[8];
+  __device__ __forceinline__ explicit SeenBits(uint32_t see) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = see << (7 - k);
+  }
+  __device__ __forceinline__ static uint32_t spread(uint32_t a, uint32_t b, uint32_t select) {
+    uint32_t m;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m) : "r"(a), "r"(b), "r"(select));
+    return m;
+  }
+  // Elements e (even) and e + 1 as halves of a word.
+  __device__ __forceinline__ uint32_t pair(int e) const {
+    return spread(y[e & 7], y[(e & 7) + 1], 0xcc88u + 0x1111u * static_cast<uint32_t>(e >> 3));
+  }
+  // Element e as a word.
+  __device__ __forceinline__ uint32_t word(int e) const {
+    return spread(y[e & 7], 0, 0x8888u + 0x1111u * static_cast<uint32_t>(e >> 3));
+  }
+};
+// Makes the hidden ones of 32 bf16 values 0.
+__device__ __forceinline__ void hide_pairs(uint32_t (&pk)[16], uint32_t see) {
+  const SeenBits seen(see);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) pk[e >> 1] &= seen.pair(e);
+}
+
+// A row's 32 values times f, or 0 where the row is none (`all`: every row of the warp is one); bad becomes NaN in both
+// halves' sum with the first that is not finite.
+__device__ __forceinline__ void scale_row(uint32_t (&o)[32], float f, bool in, bool all, uint64_t& bad) {
+  if (!all && !in) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = 0;
+  }
+  const uint64_t f2 = f2_pack(f, f);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const uint64_t v = fmul2(f2_pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), f2);
+    bad = ffma2(v, 0, bad);
+    const float2 w = f2_unpack(v);
+    o[e] = __float_as_uint(w.x);
+    o[e + 1] = __float_as_uint(w.y);
+  }
+}
+__device__ __forceinline__ bool is_bad(uint64_t bad) {
+  const float2 b = f2_unpack(bad);
+  return b.x + b.y != 0.0f;
+}
+
 // 32 rows of 32 fp32 values, a row a thread, as bf16 to rows of stride ld (16-byte aligned), of which the first `rows`
 // exist.  Groups of four lanes exchange their rows' 16-byte words, so that a store instruction covers 64 bytes of
 // eight rows.  (32 bytes of 32 rows at a time: 84 cycles an instruction, 2700 for a query tile's dQ of 128 columns.)

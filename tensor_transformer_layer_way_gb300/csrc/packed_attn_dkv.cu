@@ -539,12 +539,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         }
         // hidden queries: P and, whatever dP and D hold, dS are 0
         const uint32_t see = masked ? bits_between(lo - q0, hi - q0) : 0xffffffffu;
-        auto hide = [&]() {
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            pk[e >> 1] &= ((see >> e) & 1u ? 0x0000ffffu : 0u) | ((see >> (e + 1)) & 1u ? 0xffff0000u : 0u);
-        };
-        if (masked) hide();
+        if (masked) hide_pairs(pk, see);
         tmem_st_32x32b_x16(lane_base + w * 32, pk);   // over this thread's own columns of S^T
         tmem_st_wait();
         tc_fence_before_sync();
@@ -571,7 +566,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           pk[e >> 1] = pack_bf16x2(u.x, u.y);
           pk[(e >> 1) + 1] = pack_bf16x2(v.x, v.y);
         }
-        if (masked) hide();
+        if (masked) hide_pairs(pk, see);
         tmem_st_32x32b_x16(lane_base + T_DP + w * 32, pk);
         tmem_st_wait();
         tc_fence_before_sync();
@@ -594,7 +589,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
         ++ni;
         tc_fence_after_sync();
       }
-      float bad = 0.0f;   // becomes NaN with the first value that is not finite
+      uint64_t bad = 0;
       const float f = kind || it.slot >= 0 ? 1.0f : A.scale;
       const int row0 = it.k0 + quad * 32;
       const int64_t ld = kind ? A.lddv : A.lddk;
@@ -610,12 +605,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
           tmem_ld_32x32b_x32(lane_base + (kind ? T_DV : T_DK) + col + u * 32, o);
           tmem_ld_wait();
         }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float v = in ? __uint_as_float(o[e]) * f : 0.0f;
-          bad = fmaf(v, 0.0f, bad);
-          o[e] = __float_as_uint(v);
-        }
+        scale_row(o, f, in, hi_min >= 0, bad);
         if (it.slot >= 0) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) st_global_v8(part + (u * 32 + q * 8) * kTile, o + q * 8);
@@ -626,7 +616,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) pack_dkv_kernel(const __grid_co
       tc_fence_before_sync();
       // A row is listed, by one of its two warpgroups, if either found its columns not finite.  (All sixteen warps
       // meet, with a bounded wait, unlike a hardware barrier.)
-      const unsigned mine = __ballot_sync(0xffffffffu, in && bad != 0.0f && it.slot < 0);
+      const unsigned mine = __ballot_sync(0xffffffffu, in && is_bad(bad) && it.slot < 0);
       if (mine && lane == 0) atomicOr(&flags[kind * 4 + quad], mine);
       __syncwarp();
       if (lane == 0) mbar_arrive(x_bar);

@@ -503,10 +503,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         }
         const int k0 = j * kTile + g * 32;
         if (k0 < lo_max || k0 + 31 > hi_min) {   // some row of the warp does not see every key: its dS is 0
-          const uint32_t see = bits_between(near - k0, hi - k0) | (W ? bits_between(lo - k0, sink - 1 - k0) : 0u);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            ds[e >> 1] &= ((see >> e) & 1u ? 0x0000ffffu : 0u) | ((see >> (e + 1)) & 1u ? 0xffff0000u : 0u);
+          hide_pairs(ds, bits_between(near - k0, hi - k0) | (W ? bits_between(lo - k0, sink - 1 - k0) : 0u));
         }
         const int b = pos & 1;
         ok = mbar_wait(&ds_empty[b], (static_cast<uint32_t>(pos >> 1) & 1u) ^ 1u, abort_flag, status, tmo);
@@ -532,7 +529,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         ++no;
         tc_fence_after_sync();
       }
-      float bad = 0.0f;   // becomes NaN with the first value that is not finite
+      uint64_t bad = 0;
       if (g < D / 32) {   // 32 of the head's columns
         uint32_t o[32];
 #pragma unroll
@@ -541,12 +538,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
           tmem_ld_32x32b_x32(lane_base + T_DQ + g * 32, o);
           tmem_ld_wait();
         }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float v = in ? __uint_as_float(o[e]) * A.scale : 0.0f;
-          bad = fmaf(v, 0.0f, bad);
-          o[e] = __float_as_uint(v);
-        }
+        scale_row(o, A.scale, in, hi_min >= 0, bad);
         const int row0 = it.q0 + quad * 32;
         if (row0 < T) store_rows_bf16x32(S.dq + row0 * A.lddq + it.c * D + g * 32, A.lddq, T - row0, o);
       }
@@ -556,7 +548,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) pack_dq_kernel(const __grid_con
         if (lane == 0) mbar_arrive_relaxed(dq_empty);
       }
       // A row is listed, by the first warpgroup, if any found its columns not finite.
-      const unsigned mine = __ballot_sync(0xffffffffu, in && bad != 0.0f);
+      const unsigned mine = __ballot_sync(0xffffffffu, in && is_bad(bad));
       if (mine && lane == 0) atomicOr(&flags[quad], mine);
       if (!(ok = meet())) break;
       if (g == 0) {

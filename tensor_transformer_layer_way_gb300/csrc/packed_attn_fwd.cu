@@ -522,8 +522,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
                 const int c0 = k0 + u * 32;
                 if (live(u) && (c0 < lo_max || c0 + 31 > hi_min)) {
                   const uint32_t see = bits_between(near - c0, hi - c0) | (W ? bits_between(lo - c0, sink - 1 - c0) : 0u);
+                  const SeenBits seen(see);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) s[u][e] = (see >> e) & 1u ? s[u][e] : 0xff800000u;
+                  for (int e = 0; e < 32; ++e) {
+                    const uint32_t keep = seen.word(e);
+                    s[u][e] = (s[u][e] & keep) | (0xff800000u & ~keep);
+                  }
                 }
               }
             }
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         ++no;
         tc_fence_after_sync();
       }
-      float bad = 0.0f;   // becomes NaN with the first value that is not finite
+      uint64_t bad = 0;
       // 64 columns at a time: a row per thread into the warp's swizzled tile, which a TMA store takes to memory (rows
       // past T are clipped).  Stored by the threads, 64 bytes of 32 different rows at a time, it took 3100
       // cycles an item.
@@ -626,6 +630,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
           tmem_ld_32x32b_x32(o_col + h * 64 + 32, o[1]);
           tmem_ld_wait();
         }
+        scale_row(o[0], inv, in, hi_min >= 0, bad);
+        scale_row(o[1], inv, in, hi_min >= 0, bad);
         if (lane == 0) bulk_wait_group_read<0>();   // the tile's last store has read it
         __syncwarp();
 #pragma unroll
@@ -634,10 +640,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int c = u * 8 + 2 * e;
-            const float lo_v = in ? __uint_as_float(o[c >> 5][c & 31]) * inv : 0.0f;
-            const float hi_v = in ? __uint_as_float(o[c >> 5][(c & 31) + 1]) * inv : 0.0f;
-            bad = fmaf(lo_v, 0.0f, fmaf(hi_v, 0.0f, bad));
-            w[e] = pack_bf16x2(lo_v, hi_v);
+            w[e] = pack_bf16x2(__uint_as_float(o[c >> 5][c & 31]), __uint_as_float(o[c >> 5][(c & 31) + 1]));
           }
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
@@ -649,7 +652,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
         }
       }
       tc_fence_before_sync();
-      const unsigned again = __ballot_sync(0xffffffffu, in && bad != 0.0f);
+      const unsigned again = __ballot_sync(0xffffffffu, in && is_bad(bad));
       if (again && lane == 0) redo_later(A.redo, redo_list, redo_slot(shard * A.nql + qt.c, A.T, qt.q0, quad), again);
     }
     if (lane == 0) bulk_wait_group_all();   // every store complete before the CTA's shared memory goes away
