@@ -353,10 +353,6 @@ struct SeenBits {
   __device__ __forceinline__ uint32_t pair(int e) const {
     return spread(y[e & 7], y[(e & 7) + 1], 0xcc88u + 0x1111u * static_cast<uint32_t>(e >> 3));
   }
-  // Element e as a word.
-  __device__ __forceinline__ uint32_t word(int e) const {
-    return spread(y[e & 7], 0, 0x8888u + 0x1111u * static_cast<uint32_t>(e >> 3));
-  }
 };
 // Makes the hidden ones of 32 bf16 values 0.
 __device__ __forceinline__ void hide_pairs(uint32_t (&pk)[16], uint32_t see) {

@@ -522,35 +522,38 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
                 const int c0 = k0 + u * 32;
                 if (live(u) && (c0 < lo_max || c0 + 31 > hi_min)) {
                   const uint32_t see = bits_between(near - c0, hi - c0) | (W ? bits_between(lo - c0, sink - 1 - c0) : 0u);
-                  const SeenBits seen(see);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) {
-                    const uint32_t keep = seen.word(e);
-                    s[u][e] = (s[u][e] & keep) | (0xff800000u & ~keep);
-                  }
+                  for (int e = 0; e < 32; ++e) s[u][e] = (see >> e) & 1u ? s[u][e] : 0xff800000u;
                 }
               }
             }
           };
-          read_scores();
-          float mxs[4];
+          // Once more where the accumulator had to be rescaled, as the scores' registers are O's meanwhile.  (With a window, whose
+          // tiles are of both kinds in turn, from one copy of the code: 12 documents 105.6 -> 101.2 us; without, whose tiles
+          // are whole for long, behind the first reading: one document of 32768 tokens 665 -> 648 us.)
+#pragma unroll 1
+          for (bool again = true; again;) {
+            read_scores();
+            float mxs[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            mxs[u] = -INFINITY;
-            if (live(u)) {
+            for (int u = 0; u < 4; ++u) {
+              mxs[u] = -INFINITY;
+              if (live(u)) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                mxs[u] = fmax3(mxs[u], __uint_as_float(s[u][e]), __uint_as_float(s[u][e + 1]));
+                for (int e = 0; e < 32; e += 2)
+                  mxs[u] = fmax3(mxs[u], __uint_as_float(s[u][e]), __uint_as_float(s[u][e + 1]));
+              }
             }
-          }
-          const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * k2;
-          const bool move = mx > m + kLazy || (m == -INFINITY && mx > m);
-          if (__any_sync(0xffffffffu, move)) {
+            const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * k2;
+            const bool move = mx > m + kLazy || (m == -INFINITY && mx > m);
+            again = __any_sync(0xffffffffu, move);   // (not the second time: m is the maximum)
+            if (!again) break;
             const float mn = move ? mx : m;
             const float f = move ? ex2_approx(m - mn) : 1.0f;
             l *= f;
             m = mn;
-            if (j > qt.jbeg) {
+            again = j > qt.jbeg;
+            if (again) {
               // O_x holds the products up to key tile j - 1: they were issued before S_x(j), which is complete.
 #pragma unroll 1
               for (int u = 0; u < D / 32; ++u) {
@@ -561,7 +564,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
                 for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                 tmem_st_32x32b_x32(o_col + u * 32, o);
               }
-              read_scores();   // again: their registers are O's meanwhile
+            }
+            if constexpr (!W) {
+              if (again) read_scores();
+              break;
             }
           }
           const float nm = m == -INFINITY ? 0.0f : -m;
