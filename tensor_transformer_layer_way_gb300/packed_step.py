@@ -12,6 +12,9 @@ norm writes in place, and the reduce-scatter behind W_O is ``shard_reduce_scatte
     x1 = x0 + a, n2 = norm(x1)             z = sequence-parallel MLP(n2)
     x2 = x1 + z, n3 = norm(x2)             loss = cross-entropy(n3 W^T, target)
 
+Where asked for, the heads of q and k are normalised and rotated by position before the attention, and the
+attention sees a window of each document and its first tokens.
+
 Only the order of the calls lives here: every step is a call into the C library, on the current
 stream, into buffers that are allocated once per shape; a step can be captured into a CUDA graph.
 Run as a module it trains a small model on synthetic packs and prints the loss.
@@ -25,9 +28,10 @@ import torch
 from . import _binding as ttl
 
 
-def init_weights(t, h, f, n_q, n_kv, d, V, *, seed=0, device="cuda"):
+def init_weights(t, h, f, n_q, n_kv, d, V, *, head_norm=False, seed=0, device="cuda"):
     """Random weights of one block in the shards' layout: E and W [V/t, h], Wqkv [h, (n_q + 2 n_kv)/t d],
-    Wo [n_q/t d, h], A and A_up [h, f/t], B [f/t, h], and the three norms' gamma and beta [h]."""
+    Wo [n_q/t d, h], A and A_up [h, f/t], B [f/t, h], and the three norms' gamma and beta [h]; with head_norm
+    the heads' gamma_q and gamma_k [d] too."""
     g = torch.Generator().manual_seed(seed)
 
     def mats(rows, cols, std):
@@ -39,13 +43,17 @@ def init_weights(t, h, f, n_q, n_kv, d, V, *, seed=0, device="cuda"):
     for n in ("1", "2", "3"):
         w["gamma" + n] = torch.ones(h, dtype=torch.bfloat16, device=device)
         w["beta" + n] = torch.zeros(h, dtype=torch.bfloat16, device=device)
+    if head_norm:
+        w["gamma_q"] = torch.ones(d, dtype=torch.bfloat16, device=device)
+        w["gamma_k"] = torch.ones(d, dtype=torch.bfloat16, device=device)
     return w
 
 
 class PackedStep:
-    """Buffers and call order of the step for T tokens (a multiple of 128 t) in `batch` documents."""
+    """Buffers and call order of the step for T tokens (a multiple of 128 t) in `batch` documents.  Weights gamma_q and
+    gamma_k normalise the heads, a `Rotary` rotates them, `window` (with `sinks`) limits what they see."""
 
-    def __init__(self, weights, T, batch, *, n_q, n_kv, d, device="cuda"):
+    def __init__(self, weights, T, batch, *, n_q, n_kv, d, rotary=None, window=None, sinks=0, device="cuda"):
         self.w = weights
         self.t = t = len(weights["E"])
         self.heads = dict(n_q=n_q, n_kv=n_kv, d=d)
@@ -74,7 +82,22 @@ class PackedStep:
         self.norm3 = dict(ttl.layer_norm_fwd_buffers(t, slab, h, residual=True, device=device), Y=slabs(self.n3))
         self.qkv = each(T, qc + 2 * kc)
         self.q, self.k, self.v = qkv(self.qkv)
-        self.attn = ttl.packed_attn_fwd_buffers(t, T, n_q, n_kv, d, batch, device)
+        # what the attention reads of q and k: the projection's columns, or normalised and rotated copies
+        self.head_norm = dict(gamma_q=weights.get("gamma_q"), gamma_k=weights.get("gamma_k"))
+        self.rotary = ttl.Rotary(()) if rotary is None and "gamma_q" in weights else rotary
+        self.seen = {"Q": self.q, "K": self.k}
+        if self.rotary is not None:
+            self.seen = ttl.head_norm_rotary_fwd_buffers(t, T, n_q, n_kv, d, device)
+        if window is None:
+            self.view = {}
+            self.attn_fwd, self.attn_bwd_of = ttl.packed_attn_fwd, ttl.packed_attn_bwd
+            self.attn = ttl.packed_attn_fwd_buffers(t, T, n_q, n_kv, d, batch, device)
+            attn_bwd = ttl.packed_attn_bwd_buffers(t, T, n_q, n_kv, d, batch, device)
+        else:
+            self.view = dict(window=window, sinks=sinks)
+            self.attn_fwd, self.attn_bwd_of = ttl.packed_window_attn_fwd, ttl.packed_window_attn_bwd
+            self.attn = ttl.packed_window_attn_fwd_buffers(t, T, n_q, n_kv, d, batch, window, sinks, device)
+            attn_bwd = ttl.packed_window_attn_bwd_buffers(t, T, n_q, n_kv, d, batch, window, sinks, device)
         self.partial = each(T, h)              # per-shard sums over its heads, forward and backward
         self.partial_slabs = [p[i * slab:(i + 1) * slab] for i, p in enumerate(self.partial)]
         self.mlp = None                        # allocated by the first call
@@ -89,21 +112,32 @@ class PackedStep:
         self.dO = each(T, qc)
         self.dqkv = each(T, qc + 2 * kc)
         dq, dk, dv = qkv(self.dqkv)
-        self.attn_bwd = dict(ttl.packed_attn_bwd_buffers(t, T, n_q, n_kv, d, batch, device), dQ=dq, dK=dk, dV=dv)
+        self.attn_bwd = dict(attn_bwd, dQ=dq, dK=dk, dV=dv)
+        self.rotary_bwd = None
+        if self.rotary is not None:            # in place: the columns of dqkv that the attention's gradients are in
+            self.rotary_bwd = dict(ttl.head_norm_rotary_bwd_buffers(t, 0, n_q, n_kv, d, "gamma_q" in weights, device),
+                                   dQ=dq, dK=dk)
+            if "gamma_q" in weights:
+                ws = int(ttl.lib().ttl_head_norm_rotary_bwd_workspace_size(t, T, n_q, n_kv, d))
+                self.rotary_bwd["ws"] = torch.empty(ws, dtype=torch.uint8, device=device)
         self.dW = each(Vs, h, dtype=torch.float32)
         self.dWo = each(qc, h, dtype=torch.float32)
         self.dWqkv = each(h, qc + 2 * kc, dtype=torch.float32)
         self.dE = each(Vs, h, dtype=torch.float32)
         self.embed_ws = ttl.embedding_sorted_bwd_workspace(t, T, h, V, device)
 
-    def forward(self, ids, target, cu_seqlens):
-        """The mean loss over all tokens (a tensor of one fp32 value)."""
+    def forward(self, ids, target, cu_seqlens, positions=None):
+        """The mean loss over all tokens (a tensor of one fp32 value).  `positions` (int32, [axes, T]) are the rotation's;
+        by default a token's place in its document."""
         w = self.w
         ttl.vocab_parallel_embedding_scaled_fwd(ids, w["E"], self.scale, out=self.x0)
         ttl.layer_norm_fwd(self.x0_slabs, w["gamma1"], w["beta1"], out=self.norm1)
         for i in range(self.t):
             ttl.gemm(self.n1, w["Wqkv"][i], self.qkv[i], b_kmajor=False)
-        ttl.packed_attn_fwd(self.q, self.k, self.v, cu_seqlens, out=self.attn, **self.heads)
+        if self.rotary is not None:
+            ttl.head_norm_rotary_fwd(self.q, self.k, self.rotary, positions=positions, cu_seqlens=cu_seqlens,
+                                     out=self.seen, **self.heads, **self.head_norm)
+        self.attn_fwd(self.seen["Q"], self.seen["K"], self.v, cu_seqlens, out=self.attn, **self.heads, **self.view)
         for i in range(self.t):
             ttl.gemm(self.attn["O"][i], w["Wo"][i], self.partial[i], b_kmajor=False)
         ttl.shard_reduce_scatter(self.partial)
@@ -113,8 +147,8 @@ class PackedStep:
         ttl.vocab_parallel_ce(self.n3, w["W"], target, out=self.ce)
         return self.ce["loss"]
 
-    def backward(self, ids, cu_seqlens):
-        """Every weight's gradient, under the weight's name; after forward() on the same pack."""
+    def backward(self, ids, cu_seqlens, positions=None):
+        """Every weight's gradient, under the weight's name; after forward() on the same pack (and positions)."""
         w, out = self.w, {}
         tn = dict(a_kmajor=False, b_kmajor=False)
         for i in range(self.t):
@@ -127,7 +161,12 @@ class PackedStep:
         for i in range(self.t):
             ttl.gemm(self.g1, w["Wo"][i], self.dO[i])
             ttl.gemm(self.attn["O"][i], self.g1, self.dWo[i], **tn)
-        ttl.packed_attn_bwd(self.dO, self.q, self.k, self.v, self.attn, cu_seqlens, out=self.attn_bwd, **self.heads)
+        self.attn_bwd_of(self.dO, self.seen["Q"], self.seen["K"], self.v, self.attn, cu_seqlens, out=self.attn_bwd,
+                         **self.heads, **self.view)
+        if self.rotary is not None:
+            ttl.head_norm_rotary_bwd(self.attn_bwd["dQ"], self.attn_bwd["dK"], self.rotary, Q=self.q, K=self.k,
+                                     positions=positions, cu_seqlens=cu_seqlens, out=self.rotary_bwd, **self.heads,
+                                     **self.head_norm)
         for i in range(self.t):
             ttl.gemm(self.dqkv[i], w["Wqkv"][i], self.partial[i])
             ttl.gemm(self.n1, self.dqkv[i], self.dWqkv[i], **tn)
@@ -138,6 +177,8 @@ class PackedStep:
                    A_up=self.mlp_bwd["dA_up"], B=self.mlp_bwd["dB"])
         for n, b in (("1", self.bwd1), ("2", self.bwd2), ("3", self.bwd3)):
             out["gamma" + n], out["beta" + n] = b["dgamma"], b["dbeta"]
+        if "gamma_q" in w:
+            out["gamma_q"], out["gamma_k"] = self.rotary_bwd["dgamma_q"], self.rotary_bwd["dgamma_k"]
         return out
 
 
@@ -152,11 +193,13 @@ def synthetic_pack(T, batch, V, *, seed, device="cuda"):
     return ids.to(device), ((ids + 1) % V).to(device), cu.to(torch.int32).to(device)
 
 
-def main(steps=20, lr=0.2):
+def main(steps=20, lr=0.2, rotated=False, window=None, sinks=0):
+    """Trains; `rotated` with normalised and rotated heads, `window` and `sinks` as PackedStep takes them."""
     t, T, h, f, n_q, n_kv, d, V, batch = 2, 1024, 256, 512, 4, 2, 64, 512, 6
-    w = init_weights(t, h, f, n_q, n_kv, d, V)
+    w = init_weights(t, h, f, n_q, n_kv, d, V, head_norm=rotated)
     master = {n: [p.float() for p in (m if isinstance(m, list) else [m])] for n, m in w.items()}
-    step = PackedStep(w, T, batch, n_q=n_q, n_kv=n_kv, d=d)
+    rotary = ttl.Rotary(ttl.rotary_freqs(d)) if rotated else None
+    step = PackedStep(w, T, batch, n_q=n_q, n_kv=n_kv, d=d, rotary=rotary, window=window, sinks=sinks)
     losses = []
     for s in range(steps):
         ids, target, cu = synthetic_pack(T, batch, V, seed=s)
@@ -174,4 +217,9 @@ def main(steps=20, lr=0.2):
 
 
 if __name__ == "__main__":
-    main()
+    import argparse
+    parser = argparse.ArgumentParser(description="Trains a small model on synthetic packs.")
+    parser.add_argument("--rotated", action="store_true", help="normalised and rotated heads")
+    parser.add_argument("--window", type=int, help="keys that a query sees up to itself")
+    parser.add_argument("--sinks", type=int, default=0, help="first tokens of a document that stay visible")
+    main(**vars(parser.parse_args()))
