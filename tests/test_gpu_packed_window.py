@@ -168,6 +168,25 @@ def test_more_items_than_sms(t, T, n_q, n_kv, d, lens, W, S):
     _check(x, fwd, bwd, t, T, n_q, n_kv, d, lens, W, S)
 
 
+# Wide windows over few heads: heads and token tiles paired, documents that begin late, sinks of several tiles, rows behind
+# the documents, key tiles in shares of more items than blocks and of fewer.
+WIDE = [
+    (1, 5000, 2, 1, 128, [4990], 1500, 4), (1, 5000, 3, 1, 64, [700, 4200], 1300, 300), (1, 9000, 1, 1, 64, [9000], 2000, 0),
+    (2, 4500, 8, 2, 64, [50, 4400], 1100, 1), (1, 4100, 20, 20, 64, [4100], 2000, 2), (1, 4300, 16, 8, 128, [4290], 1100, 0),
+    (1, 3000, 5, 5, 128, [60] * 10 + [2300], 1900, 130),
+]
+
+
+@pytest.mark.parametrize("t,T,n_q,n_kv,d,lens,W,S", WIDE)
+def test_wide_windows_over_few_heads(t, T, n_q, n_kv, d, lens, W, S):
+    x = _inputs(t, T, n_q, n_kv, d, lens, T)
+    fwd, bwd = _run(x, n_q, n_kv, d, W, S)
+    _check(x, fwd, bwd, t, T, n_q, n_kv, d, lens, W, S)
+    f2, b2 = _run(x, n_q, n_kv, d, W, S)
+    for a, b in ((fwd, f2), (bwd, b2)):
+        assert all(torch.equal(p, q) for n in a if n != "ws" for p, q in zip(a[n], b[n]))
+
+
 @pytest.mark.parametrize("W,S", [(500, 0), (10 ** 12, 0), (1, 499), (400, 10 ** 12), (200, 300)])
 def test_a_window_that_hides_nothing(W, S):
     """Window and sinks together hold every document: the bits of packed_attn."""
@@ -202,7 +221,8 @@ def test_growing_and_falling_scores():
 
 
 BESIDE = [(1, 700, 2, 1, 64, [100, 530, 60], 90, 4), (1, 2600, 16, 4, 128, [130, 2100, 300], 300, 0),
-          (1, 2600, 6, 2, 64, [2, 2500, 60], 128, 140), (1, 3000, 16, 1, 128, [2800, 150], 100, 2), (1, 700, 1, 1, 128, [690], 40, 1)]
+          (1, 2600, 6, 2, 64, [2, 2500, 60], 128, 140), (1, 3000, 16, 1, 128, [2800, 150], 100, 2), (1, 700, 1, 1, 128, [690], 40, 1),
+          (1, 3200, 2, 1, 128, [100, 3000], 1200, 4), (1, 3200, 3, 1, 64, [3000, 100], 1300, 200)]
 
 
 @pytest.mark.parametrize("t,T,n_q,n_kv,d,lens,W,S", BESIDE)
@@ -261,7 +281,8 @@ def test_a_value_that_is_not_finite_reaches_what_sees_it_and_nothing_else(t, T, 
 
 
 @pytest.mark.parametrize("t,T,n_q,n_kv,d,lens,W,S,left", [(1, 2000, 16, 4, 128, [900, 700], 200, 4, 150),
-                                                          (2, 1000, 4, 2, 64, [500, 300], 60, 0, 77), (1, 3000, 4, 1, 64, [2500], 128, 130, 201)])
+                                                          (2, 1000, 4, 2, 64, [500, 300], 60, 0, 77), (1, 3000, 4, 1, 64, [2500], 128, 130, 201),
+                                                          (1, 3000, 2, 1, 128, [2600], 1200, 5, 130)])
 @pytest.mark.parametrize("bad", [float("nan"), float("-inf"), -3.3e38])
 def test_rows_of_no_document_hold_anything(t, T, n_q, n_kv, d, lens, W, S, left, bad):
     """Uninitialised rows before and behind the documents."""
@@ -284,16 +305,16 @@ def test_rows_of_no_document_hold_anything(t, T, n_q, n_kv, d, lens, W, S, left,
             assert torch.count_nonzero(b2[n][i][:left]) == 0 and torch.count_nonzero(b2[n][i][used:]) == 0
 
 
-@pytest.mark.parametrize("T,n_q,n_kv", [(200, 2, 1), (3000, 16, 4), (3000, 9, 3)])
+@pytest.mark.parametrize("T,n_q,n_kv,W", [(200, 2, 1, 30), (3000, 16, 4, 30), (3000, 9, 3, 30), (3000, 3, 1, 1300), (3000, 2, 1, 1300)])
 @pytest.mark.parametrize("S", [0, 4, 140])
-def test_bad_document_bounds_are_reported(T, n_q, n_kv, S):
+def test_bad_document_bounds_are_reported(T, n_q, n_kv, W, S):
     d = 64
     x = _inputs(1, T, n_q, n_kv, d, [T], 0)
     for cu in ([0, T * 3 // 4, T // 2, T], [-5, T // 3, T * 2 // 3], [0, T // 3, 25 * T], [T + 100, T + 200], [T, 0],
                [0, T // 4, 7, T // 2, 3, T]):
         y = dict(x, cu=torch.tensor(cu, dtype=torch.int32, device="cuda"))
-        _run(y, n_q, n_kv, d, 30, S, status=ttl.TTL_ERR_DEVICE)
-    _run(x, n_q, n_kv, d, 30, S)
+        _run(y, n_q, n_kv, d, W, S, status=ttl.TTL_ERR_DEVICE)
+    _run(x, n_q, n_kv, d, W, S)
 
 
 def test_fused_projection_strides_and_wider_results():
