@@ -608,6 +608,7 @@ def tp_attn_bwd(X, dY, Wq, Wk, Wv, Wo, fwd, *, n_q, n_kv, d, out=None, stream=No
 # is looked at once, and the slow path that words an error runs only when there is one.
 
 _ARRS = [None] + [ctypes.c_void_p * n for n in range(1, TTL_MAX_SHARDS + 1)]
+_Tensor = torch.Tensor
 
 
 def _refuse(x, name, dtype, shape):
@@ -638,36 +639,33 @@ def _ptr(x, name, dtype, shape):
 def _ptrs(ts, name, n, dtype, shape):
     """The pointers of n contiguous CUDA tensors as a host array."""
     _list_of(ts, name, n)
-    out = _ARRS[n]()
-    for i, x in enumerate(ts):
-        if (not isinstance(x, torch.Tensor) or x.dtype != dtype or x.shape != shape or not x.is_cuda
+    at = []
+    for x in ts:
+        if (not isinstance(x, _Tensor) or x.dtype != dtype or x.shape != shape or not x.is_cuda
                 or not x.is_contiguous()):
             _refuse(x, name, dtype, shape)
-        out[i] = x.data_ptr()
-    return out
+        at.append(x.data_ptr())
+    return _ARRS[n](*at)
 
 
 def _rows(ts, name, n, dtype, rows, cols):
     """The pointers of n CUDA matrices [rows, cols] whose rows are contiguous and share one row
     stride, and that stride in elements."""
     _list_of(ts, name, n)
-    out = _ARRS[n]()
-    shape = (rows, cols)
-    ld = None
-    for i, x in enumerate(ts):
-        if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.shape != shape or not x.is_cuda:
+    shape, ld = (rows, cols), None
+    at = []
+    for x in ts:
+        if not isinstance(x, _Tensor) or x.dtype != dtype or x.shape != shape or not x.is_cuda:
             _refuse(x, name, dtype, shape)
         step, col = x.stride()
         if col != 1 and cols > 1:
             raise ValueError(f"{name}: rows must be contiguous")
-        if rows <= 1:
-            step = cols
         if ld is None:
             ld = step
-        elif step != ld:
+        elif step != ld and rows > 1:
             raise ValueError(f"{name}: the tensors must share one row stride")
-        out[i] = x.data_ptr()
-    return out, ld
+        at.append(x.data_ptr())
+    return _ARRS[n](*at), ld if rows > 1 else cols
 
 
 def _space(ws):
@@ -984,8 +982,8 @@ class Rotary:
         self.rot = 2 * len(freqs)
         self.axes = 1 + max(axes, default=0)
         self.interleaved = bool(interleaved)
-        self._freqs = (ctypes.c_double * len(freqs))(*freqs)
-        self._pair_axis = (ctypes.c_int32 * len(axes))(*axes)
+        self._kept = (ctypes.c_double * len(freqs))(*freqs), (ctypes.c_int32 * len(axes))(*axes)
+        self._freqs, self._pair_axis = (ctypes.addressof(a) for a in self._kept)
 
 
 def _rotary_args(rotary, T, d, n_q, n_kv, t, gamma_q, gamma_k, eps, positions, cu_seqlens):

@@ -522,7 +522,8 @@ int check_rotary(HeadArgs& A, int rot, int neighbours, const double* freqs, cons
     // (2^20 radians a position: beyond any use, and small enough for the fraction below)
     if (!(std::fabs(freqs[i]) <= 1048576.0)) return set_error(TTL_ERR_ARG, "%s: freqs[%d] is not a frequency", name, i);
     const double turns = std::fabs(freqs[i]) / 6.283185307179586476925;
-    const uint64_t part = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));   // (below 2^64: both steps are exact)
+    const double fraction = turns - static_cast<double>(static_cast<int64_t>(turns));
+    const uint64_t part = static_cast<uint64_t>(fraction * 18446744073709551616.0);   // (2^64; both steps are exact)
     A.turns[i] = freqs[i] < 0.0 ? 0 - part : part;
     const int axis = pair_axis ? pair_axis[i] : 0;
     if (axis < 0 || axis >= axes) return set_error(TTL_ERR_ARG, "%s: pair %d is on axis %d of %d", name, i, axis, axes);
