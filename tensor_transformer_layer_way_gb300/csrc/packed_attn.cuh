@@ -796,4 +796,68 @@ struct KeyEdges {
   }
 };
 
+// The same with a window.  For query rows, masked places are in the tile of the document's first token, the last one with
+// sinks, the two that the window of the tile's rows begins in, and the own one.
+struct WindowQueryEdges {
+  BadRows at[5];
+  int k0[5];
+  template <int D>
+  __device__ __forceinline__ void look(const PackArgs& A, const __nv_bfloat16* m, int64_t ld, int col, int lo, int row0, int lane) {
+    const int own = row0 / kTile;
+    const TileRange r = key_tiles(A, own * kTile, lo);
+    k0[0] = r.beg;
+    k0[1] = max(r.beg, r.gap - 1);
+    k0[2] = r.wbeg;
+    k0[3] = min(r.wbeg + 1, own);
+    k0[4] = own;
+#pragma unroll 1
+    for (int k = 0; k < 5; ++k) {
+      k0[k] *= kTile;
+      at[k] = BadRows{{0, 0, 0, 0}};
+      add_bad_rows<D>(at[k], m, ld, col, k0[k], A.T, lane);
+    }
+  }
+  __device__ __forceinline__ bool met(const PackArgs& A, int lo, int i) const {
+    const int near = near_key(A, lo, i), sink = sink_end(A, lo, near);
+    uint32_t hit = 0;
+#pragma unroll 1
+    for (int k = 0; k < 5; ++k)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c0 = k0[k] + u * 32;
+        hit |= at[k].w[u] & ~(bits_between(near - c0, i - c0) | bits_between(lo - c0, sink - 1 - c0));
+      }
+    return hit != 0;
+  }
+};
+// For key rows: queries before row j in its own tile, queries from its end on in the last two that the tile meets (of a key
+// that ends before these, beside sinks, without a look).
+struct WindowKeyEdges {
+  BadRows own, last[2];
+  int own0, last0[2];
+  template <int D>
+  __device__ __forceinline__ void look(const PackArgs& A, const PackShard& S, int g, int row0, bool want_k, int lane) {
+    const __nv_bfloat16* m = want_k ? S.q : S.dO;
+    const int64_t ld = want_k ? A.ldq : A.lddo;
+    own0 = row0 / kTile * kTile;
+    const int T = static_cast<int>(A.T), end = min(min(own0 + kTile, __ldg(A.cu + A.batch)), T);
+    const int tile = last_query_tile<true>(A, doc_of(A.cu, A.batch, T, end - 1), own0, end);
+    last0[0] = max(own0, (tile - 1) * kTile);
+    last0[1] = max(own0, tile * kTile);
+    own = last[0] = last[1] = BadRows{{0, 0, 0, 0}};
+    for (int c = g * A.grp; c < (g + 1) * A.grp; ++c) {
+      add_bad_rows<D>(own, m, ld, c * D, own0, A.T, lane);
+      add_bad_rows<D>(last[0], m, ld, c * D, last0[0], A.T, lane);
+      add_bad_rows<D>(last[1], m, ld, c * D, last0[1], A.T, lane);
+    }
+  }
+  __device__ __forceinline__ bool met(int j, int end) const {
+    return end < last0[0] || own.any(0, j - own0) || last[0].any(end - last0[0], kTile) || last[1].any(end - last0[1], kTile);
+  }
+};
+template <bool W>
+using QueryLook = typename std::conditional<W, WindowQueryEdges, QueryEdges>::type;
+template <bool W>
+using KeyLook = typename std::conditional<W, WindowKeyEdges, KeyEdges>::type;
+
 }  // namespace ttl

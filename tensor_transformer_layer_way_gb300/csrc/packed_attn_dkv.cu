@@ -130,9 +130,9 @@ __device__ __forceinline__ KvItem first_item(const KvParams& P, int total, bool 
 }
 
 // Those of the rows j of dK (want_k) or dV, whose sums are not finite, that masked places may have made so, again.
-// `edges` are looked at once for the rows of a tile.  (With a window without that look, as in the forward pass.)
+// `edges` are looked at once for the rows of a tile.
 template <int D, bool W, int R>
-__device__ __noinline__ void redo_keys(const PackArgs& A, int shard, int g, int (&j)[R], bool want_k, KeyEdges& edges,
+__device__ __noinline__ void redo_keys(const PackArgs& A, int shard, int g, int (&j)[R], bool want_k, KeyLook<W>& edges,
                                           bool& looked, int lane) {
   const PackShard& S = A.s[shard];
   const int T = static_cast<int>(A.T), row0 = j[0] & ~31;
@@ -140,9 +140,13 @@ __device__ __noinline__ void redo_keys(const PackArgs& A, int shard, int g, int 
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int hi = query_end<W>(A, doc_of(A.cu, A.batch, T, j[r]), j[r]);
-    bool met = W || hi - j[r] < kRedoShort;
+    bool met = hi - j[r] < kRedoShort;
     if (!met) {
-      if (!looked) edges.look<D>(A, S, g, row0, hi, want_k, lane);
+      if constexpr (W) {
+        if (!looked) edges.template look<D>(A, S, g, row0, want_k, lane);
+      } else {
+        if (!looked) edges.template look<D>(A, S, g, row0, hi, want_k, lane);
+      }
       looked = true;
       met = edges.met(j[r], hi);
     }
@@ -165,7 +169,7 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
     const RedoEntry e = A.redo[slot];
     const RedoPlace at = redo_place(slot, A.T);
     const int kv = at.head >> 1;
-    KeyEdges edges;
+    KeyLook<W> edges;
     bool looked = false;
     for (uint32_t rows = e.rows; rows;) {
       int j[kRedoRows];
@@ -699,7 +703,7 @@ __global__ void __launch_bounds__(2 * D) pack_join_kernel(const __grid_constant_
     if (bad && lane == 0) atomicOr(&redo, bad);
     __syncthreads();                 // (and all rows are stored)
     uint32_t again = redo;
-    KeyEdges edges;
+    KeyLook<W> edges;
     bool looked = false;
     for (int k = 0; again; ++k) {
       int j[kRedoRows];

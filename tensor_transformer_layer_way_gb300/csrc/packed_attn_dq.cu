@@ -106,7 +106,6 @@ __device__ __forceinline__ DqItem<W> first_item(const DqParams& P) {
 }
 
 // The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
-// (With a window without a look at the masked places, as in the forward pass.)
 template <int D, bool W>
 __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, int warps, int lane) {
   const uint32_t slots = redo_slots(A.t * A.nql, A.T);
@@ -116,7 +115,7 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
     const RedoPlace at = redo_place(slot, A.T);
     const int shard = at.head / A.nql, c = at.head % A.nql;
     const PackShard& S = A.s[shard];
-    QueryEdges edges;
+    QueryLook<W> edges;
     bool looked = false;
     for (uint32_t rows = e.rows; rows;) {
       int i[kRedoRows], lo[kRedoRows];
@@ -126,11 +125,16 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
 #pragma unroll
       for (int r = 0; r < kRedoRows; ++r) {
         const int first = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
-        bool met = W || i[r] - first < kRedoShort;
+        bool met = i[r] - first < kRedoShort;
         if (!met) {
-          if (!looked) edges.look<D>(S.k, A.ldk, c / A.grp * D, first, at.row0, A.T, lane);
+          if constexpr (W) {
+            if (!looked) edges.template look<D>(A, S.k, A.ldk, c / A.grp * D, first, at.row0, lane);
+            met = edges.met(A, first, i[r]);
+          } else {
+            if (!looked) edges.template look<D>(S.k, A.ldk, c / A.grp * D, first, at.row0, A.T, lane);
+            met = edges.met(first, i[r]);
+          }
           looked = true;
-          met = edges.met(first, i[r]);
         }
         if (met) again |= 1u << (i[r] - at.row0);
       }

@@ -182,8 +182,6 @@ __device__ __forceinline__ int first_token(const RowDocs<W>& d, int q0, int r) {
 }
 
 // The listed rows again, by `warps` warps, of which this is number w: the rows of an entry in groups, the groups in turn.
-// (With a window, whose tiles have masked places at both ends and among the sinks, without a look at them: a row's
-// keys are few.)
 template <int D, bool W>
 __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, int warps, int lane) {
   const uint32_t slots = redo_slots(A.t * A.nql, A.T);
@@ -193,7 +191,7 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
     const RedoPlace at = redo_place(slot, A.T);
     const PackShard& S = A.s[at.head / A.nql];
     const int c = at.head % A.nql;
-    QueryEdges edges;
+    QueryLook<W> edges;
     bool looked = false;
     for (uint32_t rows = e.rows; rows;) {
       int i[kRedoRows], lo[kRedoRows];
@@ -203,11 +201,16 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
 #pragma unroll
       for (int r = 0; r < kRedoRows; ++r) {
         const int first = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
-        bool met = W || i[r] - first < kRedoShort;
+        bool met = i[r] - first < kRedoShort;
         if (!met) {
-          if (!looked) edges.look<D>(S.v, A.ldv, c / A.grp * D, first, at.row0, A.T, lane);
+          if constexpr (W) {
+            if (!looked) edges.template look<D>(A, S.v, A.ldv, c / A.grp * D, first, at.row0, lane);
+            met = edges.met(A, first, i[r]);
+          } else {
+            if (!looked) edges.template look<D>(S.v, A.ldv, c / A.grp * D, first, at.row0, A.T, lane);
+            met = edges.met(first, i[r]);
+          }
           looked = true;
-          met = edges.met(first, i[r]);
         }
         if (met) again |= 1u << (i[r] - at.row0);
       }
