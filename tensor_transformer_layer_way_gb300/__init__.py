@@ -3,7 +3,8 @@
 The t tensor-parallel shards of the method are t device buffers on one GPU; the hot path
 (column/row-parallel GEMMs with fused activations, the partial-sum all-reduce, the GTP_remat
 weight path, vocab-parallel cross-entropy and embedding, the head-split attention block, layer
-norm on token slabs, attention over packed documents) runs in the hand-written CUDA kernels of
+norm on token slabs, norm and rotation of heads, attention over packed documents or windows of
+them) runs in the hand-written CUDA kernels of
 ``_lib/libttl.so`` behind the C ABI in ``include/ttl.h``.
 This package is the thin Python binding over that ABI.
 """

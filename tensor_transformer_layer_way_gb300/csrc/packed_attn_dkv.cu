@@ -13,13 +13,17 @@
 // tensor pipe busy: S(n+1), dK(n), dP(n+1), dV(n+1), S(n+2), ...  While the elementwise warps turn S(n+1)
 // into P, dK(n) and dP(n+1) run; while they form dS(n+1), dV(n+1) and S(n+2) do.
 //
-// What bounds it: the turns of tensor pipe and elementwise warps, 3000 cycles a step where the products need 2050.
-// Measured: one document of 16384 tokens, 4 query heads and 1 KV head of 128: 370 us, 1490 TFLOP/s.  P^T and dS^T are
-// rounded to bf16 once, the type of dO and Q in their products.
+// What bounds it: the turns of tensor pipe and elementwise warps, 2700 cycles a step where the products need 2050.
+// Measured: one document of 16384 tokens, 4 query heads and 1 KV head of 128: 359 us, 1530 TFLOP/s, window 2048 92 us;
+// 8192 tokens, 16 and 4 heads of 64, window 200: 45 us.  P^T and dS^T are rounded to bf16 once, the type of dO and Q in
+// their products.
 //
 // Blocks take items from the list, heaviest first, as they get to them; warp 0 takes one while its last tiles wait for
 // a place, and announces it to the others.  (Dealt out beforehand, in turn and back: 188 us for 12 documents of
-// 8192 tokens together, 32 and 8 heads over 8 shards; taken: 145 to 149.)
+// 8192 tokens together, 32 and 8 heads over 8 shards; taken: 134 to 149.)
+//
+// With a window a key tile meets the query tiles up to a window behind it, or to its document's end where it holds sinks.
+// Blocks then work on even shares of all steps in a line (KvShares), unless whole tiles should end as soon.
 //
 // Roles (640 threads, persistent): warp 0 the TMA loads, warp 1 the MMAs, warp 2 brings each step's lse and D to
 // shared memory, warp 3 the documents of the coming item's keys, warps 4..19 the elementwise work: a key row per

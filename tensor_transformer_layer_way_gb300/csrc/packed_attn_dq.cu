@@ -13,9 +13,10 @@
 // longer over a tile than the products they run under).
 // S, dP and dQ take 384 columns of tensor memory and two dS buffers the rest.
 //
-// What bounds it: the products' reads of shared memory, 1750 of the 2340 cycles a key tile takes.  Measured: one
-// document of 16384 tokens, 4 query heads and 1 KV head of 128: 273 us, 1510 TFLOP/s; 8192 tokens in 12
-// documents, 32 and 8 heads over 8 shards: 129 us.  dS is rounded to bf16 once, the type of K in their product (error of
+// What bounds it: the products' reads of shared memory, 1750 of the 2050 cycles a key tile takes, and 4400 cycles an item
+// beside its key tiles (first row data 550, the last product 700, dQ 2700).  Measured: one document of 16384 tokens, 4
+// query heads and 1 KV head of 128: 259 us, 1590 TFLOP/s, window 2048 83 us; 8192 tokens in 12 documents, 32 and 8 heads
+// over 8 shards: 117 us, window 1024 114 us; 8192 tokens, 16 and 4 heads of 64, window 200: 40 us.  dS is rounded to bf16 once, the type of K in their product (error of
 // the gradients against 64 bits 2.5e-3, with P and dS in fp32 1.8e-3).
 
 #include "packed_attn.cuh"

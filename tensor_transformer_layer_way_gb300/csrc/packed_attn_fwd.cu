@@ -26,10 +26,16 @@
 //
 // What bounds it: the turn of a tile, 2700 cycles (clock stamps: softmax 1300, product and next scores 1100, the rest
 // hand-overs), which the other tile's turn fills up to the products' 2050; tensor memory has no columns left in
-// which the next scores could wait.  Measured: one document of 32768 tokens, 4 query heads and 1 KV head of 128: 665 to 705 us,
-// 1560 to 1650 TFLOP/s; 8192 tokens in 12 documents, 32 query and 8 KV heads over 8 shards: 94 us (with items
-// dealt out beforehand 5 more); 16384 tokens, 8 and 2 heads of 64: 292 us.  With many short documents an
-// item costs about 10000 cycles beside its key tiles (masks, the wait for the last product, the result).
+// which the next scores could wait.  Measured: one document of 32768 tokens, 4 query heads and 1 KV head of 128: 645 to 705 us,
+// 1560 to 1700 TFLOP/s; 8192 tokens in 12 documents, 32 query and 8 KV heads over 8 shards: 92 to 94 us (with items
+// dealt out beforehand 5 more); 16384 tokens, 8 and 2 heads of 64: 292 us.  An item costs 4500 to 5000 cycles beside
+// its key tiles: its rows' documents 900, the wait for the last product 1100, the result 2500.
+//
+// With a window (W) an item's key tiles are its window's and its document's sinks.  Measured: 32768 tokens, 4 query heads and 1
+// KV head of 128, window 4096: 204 us (64% of the burst rate; 3.4 items of 34 key tiles a block leave a sixth of it idle at the
+// end: cut into parts that a second kernel joins they took 209); the 12 documents with window 1024: 101 us; 16384 tokens,
+// 16 and 4 heads of 64, window 128: 52 us, where an item is two masked key tiles of 3000 to 4000 cycles each: the
+// turn from scores to product and back, with nothing to fill it but the other tile's.
 //
 // A masked place enters the product as P = 0, and 0 times an infinite or NaN value is NaN: a row whose
 // result is not finite for that reason is computed again over its own keys alone when the block's items are done.
