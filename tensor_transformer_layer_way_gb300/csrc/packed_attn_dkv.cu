@@ -76,7 +76,8 @@ __device__ __forceinline__ KvItem listed_item(const KvParams& P, int at) {
 }
 
 // The block's item in its share of the line at or behind key tile `tile` of KV head `head` (which become the place behind
-// it); shard < 0: none.
+// it); shard < 0: none.  Whatever the line holds (a workspace that two calls write at once), an item is of a tile and
+// head that there are and no longer than a tile can be.
 template <int D>
 __device__ __forceinline__ KvItem share_item(const KvParams& P, int& head, int& tile) {
   constexpr int kCost = tile_cost(D);
@@ -86,7 +87,7 @@ __device__ __forceinline__ KvItem share_item(const KvParams& P, int& head, int& 
   const int b = static_cast<int>(blockIdx.x), blocks = __ldg(&S.blocks);
   const long long total = __ldg(&S.total), per = __ldg(&S.head);
   const long long p0 = total * b / blocks, p1 = total * (b + 1) / blocks;
-  while (b < blocks && head < P.lanes) {
+  while (b < blocks && head >= 0 && head < P.lanes && tile >= 0 && tile < P.tiles) {
     const long long at = head * per + __ldg(before + tile), end = head * per + __ldg(before + tile + 1);
     if (at >= p1) break;
     const int k = tile, ln = head;
@@ -96,8 +97,10 @@ __device__ __forceinline__ KvItem share_item(const KvParams& P, int& head, int& 
     }
     // the share's steps of the tile; a tile without steps belongs to the share in which it begins
     const long long from = p0 - at - kCost, to = (p1 < end ? p1 : end) - at - kCost;
-    const int steps = static_cast<int>(end - at - kCost);
-    const int s0 = from > 0 ? static_cast<int>(from < steps ? from : steps) : 0, s1 = to > 0 ? static_cast<int>(to) : 0;
+    const long long whole = end - at - kCost, most = static_cast<long long>(P.tiles - k) * A.grp;
+    const int steps = static_cast<int>(whole < 0 ? 0 : (whole < most ? whole : most));
+    const int s0 = from > 0 ? static_cast<int>(from < steps ? from : steps) : 0;
+    const int s1 = to > 0 ? static_cast<int>(to < steps ? to : steps) : 0;
     if (steps == 0 ? p0 <= at : s1 > s0) {
       const int slot = s0 > 0 ? 2 * b : (s1 < steps ? 2 * b + 1 : -1);
       return KvItem{ln / A.nkvl, ln % A.nkvl, k * kTile, k + steps / A.grp - 1, s0, s1 - s0, slot};
@@ -666,6 +669,7 @@ __global__ void __launch_bounds__(2 * D) pack_join_kernel(const __grid_constant_
     const int64_t at = w >> 3;
     const int4 e = __ldg(A.join_list + (shares ? at : at / lanes));
     const int ln = shares ? e.w : static_cast<int>(at % lanes);
+    if (shares && (ln < 0 || ln >= lanes || e.x < 0 || e.y < 0 || e.y + 2 * e.z > 2 * kShareBlocks + 1)) continue;
     const int key0 = e.x * kTile + r0, key = key0 + lane;
     const int shard = ln / A.nkvl, g = ln % A.nkvl;
     const PackShard& S = A.s[shard];

@@ -85,7 +85,7 @@ __device__ __forceinline__ int work_class(int work, int shift) {
   return c < kPlanThreads ? c : kPlanThreads - 1;
 }
 
-// Lays the key tiles end to end and cuts the line.  Every thread calls it; scan holds 33 values.
+// Lays the key tiles end to end and cuts the line.  Every thread calls it; scan holds a value a warp.
 __device__ __forceinline__ void lay_out(const PackArgs& A, const PackPlan& P, const int32_t* near, long long* scan, int* joins,
                                         unsigned long long* whole) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

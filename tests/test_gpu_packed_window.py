@@ -386,3 +386,48 @@ def test_gradient_against_differences():
     # 2-norm is at most 3 half steps of the gradient's, and a random direction sees 4 sigma of it.
     size = sum((bwd["d" + n][0].to(F8).square().sum()) for n in ("Q", "K", "V")).sqrt()
     assert (got - want).abs() <= 4 * 3 * HALF * size
+
+
+def test_two_graphs_that_share_buffers_and_a_workspace():
+    """Replayed in turn they give what each gives alone: nothing of the other's plan is left."""
+    T, n_q, n_kv, d, W, S = 4000, 8, 8, 64, 300, 5
+    kw = dict(n_q=n_q, n_kv=n_kv, d=d, window=W, sinks=S)
+    packs = [_inputs(1, T, n_q, n_kv, d, lens, 40 + len(lens)) for lens in ([4000], [100, 900, 2500])]
+    out_f = ttl.packed_window_attn_fwd_buffers(1, T, n_q, n_kv, d, 3, W, S)
+    out_b = ttl.packed_window_attn_bwd_buffers(1, T, n_q, n_kv, d, 3, W, S)
+    want, graphs = [], []
+    for x in packs:
+        f = ttl.packed_window_attn_fwd(x["Q"], x["K"], x["V"], x["cu"], **kw)
+        want.append((f, ttl.packed_window_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], f, x["cu"], **kw)))
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            ttl.packed_window_attn_fwd(x["Q"], x["K"], x["V"], x["cu"], out=out_f, **kw)
+            ttl.packed_window_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], out_f, x["cu"], out=out_b, **kw)
+        graphs.append(graph)
+    for i in (0, 1, 0, 0, 1):
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        f, b = want[i]
+        assert torch.equal(out_f["O"][0], f["O"][0]) and torch.equal(out_f["lse"][0], f["lse"][0])
+        assert all(torch.equal(out_b[n][0], b[n][0]) for n in ("dQ", "dK", "dV"))
+    assert ttl.device_status() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    T, n_q, n_kv, d, W, S = 3000, 16, 4, 128, 500, 4
+    kw = dict(n_q=n_q, n_kv=n_kv, d=d, window=W, sinks=S)
+    x, y = (_inputs(1, T, n_q, n_kv, d, lens, 50 + len(lens)) for lens in ([3000], [1200, 1700]))
+    want = [_run(v, n_q, n_kv, d, W, S) for v in (x, y)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(3):
+        for i, (v, s) in enumerate(zip((x, y), streams)):
+            f = ttl.packed_window_attn_fwd(v["Q"], v["K"], v["V"], v["cu"], stream=s, **kw)
+            got[i].append((f, ttl.packed_window_attn_bwd(v["dO"], v["Q"], v["K"], v["V"], f, v["cu"], stream=s, **kw)))
+    torch.cuda.synchronize()
+    assert ttl.device_status() == 0
+    for (f, b), runs in zip(want, got):
+        for f2, b2 in runs:
+            assert torch.equal(f["O"][0], f2["O"][0]) and all(torch.equal(b[n][0], b2[n][0]) for n in ("dQ", "dK", "dV"))
