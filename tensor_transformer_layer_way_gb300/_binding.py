@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -984,6 +985,10 @@ class Rotary:
         self.interleaved = bool(interleaved)
         self._kept = (ctypes.c_double * len(freqs))(*freqs), (ctypes.c_int32 * len(axes))(*axes)
         self._freqs, self._pair_axis = (ctypes.addressof(a) for a in self._kept)
+
+    def __reduce__(self):                  # a copy has arrays, and addresses, of its own
+        make = functools.partial(Rotary, axes=list(self._kept[1]), interleaved=self.interleaved)
+        return make, (list(self._kept[0]),)
 
 
 def _rotary_args(rotary, T, d, n_q, n_kv, t, gamma_q, gamma_k, eps, positions, cu_seqlens):

@@ -147,3 +147,15 @@ def test_binding_refusals(lib):
     r = ttl.Rotary(ttl.rotary_freqs(32), axes=[0] * 8 + [1] * 4 + [2] * 4)
     assert (r.rot, r.axes) == (32, 3) and ttl.Rotary([]).rot == 0
     assert ttl.rotary_freqs(4, 100.0) == [1.0, 0.1]
+
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle"])
+def test_a_copy_of_a_rotary_reads_its_own_arrays(how):
+    import copy
+    import pickle
+    import tensor_transformer_layer_way_gb300 as ttl
+    r = ttl.Rotary([1.0, 0.5, -0.25], axes=[0, 1, 1], interleaved=True)
+    c = pickle.loads(pickle.dumps(r)) if how == "pickle" else getattr(copy, how)(r)
+    assert (c.rot, c.axes, c.interleaved) == (6, 2, True)
+    assert list(c._kept[0]) == [1.0, 0.5, -0.25] and list(c._kept[1]) == [0, 1, 1]
+    assert (c._freqs, c._pair_axis) == tuple(ctypes.addressof(a) for a in c._kept)
