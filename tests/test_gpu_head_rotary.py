@@ -339,3 +339,62 @@ def test_rows_beyond_32_bits():
     ttl.head_norm_rotary_fwd([q], [k], rotary, out={"Q": [q], "K": [k]}, **kw)
     assert ttl.device_status() == 0
     assert torch.equal(q[-300:], want["Q"][0]) and torch.equal(k[-300:], want["K"][0])
+
+
+# ---------------------------------------------------------------------------- values that are not finite
+
+def _same(got, ref, bound, name):
+    """NaN where the formula's result is NaN, its infinities, and everything else as near as without them."""
+    got = got.to(F8)
+    nan, inf = torch.isnan(ref), torch.isinf(ref)
+    assert torch.equal(torch.isnan(got), nan), f"{name}: NaN at {torch.nonzero(torch.isnan(got) != nan)[:4].tolist()}"
+    assert torch.equal(got[inf], ref[inf]), f"{name}: infinities"
+    rest = ~(nan | inf)
+    over = (got - ref).abs()[rest] - bound[rest] * 1.01 - 1e-37
+    assert (over <= 0).all(), f"{name}: beyond the bound"
+
+
+def _check_same(x, f, b, T, d, cos, sin, inter):
+    inside = torch.ones(T, dtype=torch.bool, device="cuda")
+    for n in ("Q", "K"):
+        w = x["gamma_" + n.lower()]
+        y, e = _ref_fwd(x[n][0], w, d, cos, sin, inside, inter, 1e-6)
+        _same(f[n][0].view(T, -1, d), y, e, n)
+        dx, e, dg, ge = _ref_bwd(x["d" + n][0], x[n][0], w, d, cos, sin, inside, inter, 1e-6)
+        _same(b["d" + n][0].view(T, -1, d), dx, e, "d" + n)
+        if w is not None:
+            _same(b["dgamma_" + n.lower()], dg, ge, "dgamma_" + n.lower())
+
+
+# columns, rotated ones and weights: parts of a head, none, all, and slots of 16 that leave lanes idle
+MIXED = [(128, 64, None), (128, 64, torch.bfloat16), (64, 0, None), (64, 0, torch.float32), (80, 48, None), (256, 16, torch.float32),
+         (64, 64, None), (128, 128, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("d,rot,norm", MIXED)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_value_that_is_not_finite_stays_in_its_pair(d, rot, norm, inter, bad):
+    """In each column of a head, of the inputs or of the gradients: it reaches the column that it turns with, and through the norm its
+    head; columns that do not turn keep theirs to themselves."""
+    freqs = ttl.rotary_freqs(rot)
+    rotary = ttl.Rotary(freqs, interleaved=inter)
+    turned = lambda T: (torch.arange(T, dtype=F8, device="cuda")[:, None]   # noqa: E731
+                        * torch.tensor(freqs, dtype=F8, device="cuda"))
+    # every column, a token each
+    for names in (("Q", "K"), ("dQ", "dK")):
+        x = _inputs(1, d + 3, 2, 1, d, norm, d + rot)
+        for n in names:
+            for c in range(d):
+                x[n][0][c + 1, c] = bad
+        f, b = _run(x, rotary, 1, d + 3, 2, 1, d)
+        a = turned(d + 3)
+        _check_same(x, f, b, d + 3, d, a.cos(), a.sin(), inter)
+    # one column alone, for the sums over tokens
+    for c in sorted({0, 7, rot // 2, max(rot - 1, 0), min(rot, d - 1), min(rot + 8, d - 1), d - 9, d - 1}):
+        for n in ("Q", "dQ"):
+            x = _inputs(1, 6, 2, 1, d, norm, c)
+            x[n][0][3, c] = bad
+            f, b = _run(x, rotary, 1, 6, 2, 1, d)
+            a = turned(6)
+            _check_same(x, f, b, 6, d, a.cos(), a.sin(), inter)
