@@ -9,8 +9,8 @@
 // Backward, g = the incoming gradient turned back:  dgamma = sum g n, h = g gamma, dx = r (h - n mean(h n)).
 //
 // Angles.  A position times a frequency needs more than 32 bits before its whole turns are dropped.  The host
-// gives turns per position as a 64-bit fraction of a turn; the integer product with the position wraps at whole turns
-// by itself, exactly, for positions of either sign, and its upper 32 bits are the angle to 2^-32 turns.
+// gives turns per position as a 64-bit fraction of a turn, to 2^-64; the integer product with the position wraps at whole turns
+// by itself, for positions of either sign, and its upper 32 bits are the angle to 2^-31 turns.
 //
 // Layout.  A lane holds 16 columns of a head as two 16-byte words whose columns pair up (columns c.. and rot/2 + c..,
 // or 16 neighbours), so a rotation exchanges nothing; the 1 to 16 lanes of a head share a token and join their squares
@@ -515,6 +515,18 @@ int check_shape(int t, int64_t T, int n_q, int n_kv, int d, const char* name) {
   return TTL_OK;
 }
 
+// f / 2 pi without its whole turns, in units of 2^-64 turns, to one of them (0 <= f <= 2^20): a position of 2^31 leaves
+// 2^-33 turns of that.  The quotient in doubles alone is off by up to 2^-36 turns, which such a position makes a thirtieth
+// of a turn; so the division's remainder is divided too, by 2 pi as a sum of two doubles.
+uint64_t turns_of(double f) {
+  constexpr double kTwoPi = 0x1.921fb54442d18p+2, kTwoPiRest = 0x1.1a62633145c07p-52;
+  const double q = f / kTwoPi;
+  const double rest = std::fma(-q, kTwoPiRest, std::fma(-q, kTwoPi, f)) / kTwoPi;   // (the inner one is exact)
+  const double fraction = q - static_cast<double>(static_cast<int64_t>(q));
+  // (2^64; the first product is exact but for what lies below a unit)
+  return static_cast<uint64_t>(fraction * 18446744073709551616.0) + static_cast<uint64_t>(std::llrint(rest * 18446744073709551616.0));
+}
+
 // What both directions say about positions: fills A.
 int check_rotary(HeadArgs& A, int rot, int neighbours, const double* freqs, const int32_t* pair_axis, int axes,
                  const int32_t* positions, int batch, const int32_t* cu, const char* name) {
@@ -530,9 +542,7 @@ int check_rotary(HeadArgs& A, int rot, int neighbours, const double* freqs, cons
   for (int i = 0; i < rot / 2; ++i) {
     // (2^20 radians a position: beyond any use, and small enough for the fraction below)
     if (!(std::fabs(freqs[i]) <= 1048576.0)) return set_error(TTL_ERR_ARG, "%s: freqs[%d] is not a frequency", name, i);
-    const double turns = std::fabs(freqs[i]) / 6.283185307179586476925;
-    const double fraction = turns - static_cast<double>(static_cast<int64_t>(turns));
-    const uint64_t part = static_cast<uint64_t>(fraction * 18446744073709551616.0);   // (2^64; both steps are exact)
+    const uint64_t part = turns_of(std::fabs(freqs[i]));
     A.turns[i] = freqs[i] < 0.0 ? 0 - part : part;
     const int axis = pair_axis ? pair_axis[i] : 0;
     if (axis < 0 || axis >= axes) return set_error(TTL_ERR_ARG, "%s: pair %d is on axis %d of %d", name, i, axis, axes);

@@ -398,3 +398,59 @@ def test_a_value_that_is_not_finite_stays_in_its_pair(d, rot, norm, inter, bad):
             f, b = _run(x, rotary, 1, 6, 2, 1, d)
             a = turned(6)
             _check_same(x, f, b, 6, d, a.cos(), a.sin(), inter)
+
+
+# ---------------------------------------------------------------------------- large frequencies at far positions
+
+_PI_BITS = 400
+
+
+def _two_pi():
+    """2 pi 2^400 as a whole number: 8 (4 atan(1/5) - atan(1/239))."""
+    one = 1 << (_PI_BITS + 40)
+
+    def atan_of(n):
+        term, total, k = one // n, 0, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+
+    return 8 * (4 * atan_of(5) - atan_of(239)) >> 40
+
+
+def _reduced(freqs, positions):
+    """Angles in (-2 pi, 2 pi) of each position and frequency, whole turns dropped in whole numbers."""
+    turn = _two_pi()
+    rows = []
+    for p in positions:
+        row = []
+        for f in freqs:
+            num, den = float(f).as_integer_ratio()        # (den a power of two)
+            angle = p * num * (1 << _PI_BITS) % (turn * den)
+            row.append(angle / (den << _PI_BITS))
+        rows.append(row)
+    return torch.tensor(rows, dtype=F8, device="cuda")
+
+
+@pytest.mark.parametrize("start", [2 ** 24 - 40, 2 ** 31 - 81, -(2 ** 31), 10 ** 9 + 7])
+@pytest.mark.parametrize("inter", [False, True])
+def test_large_frequencies_at_far_positions(start, inter):
+    """An angle of any accepted frequency and position, to the bound that holds for small ones."""
+    t, T, n_q, n_kv, d = 1, 80, 2, 1, 64
+    x = _inputs(t, T, n_q, n_kv, d, torch.float32, 31)
+    freqs = [1.0, 100.0, -100.0, 12345.678, 99999.9, 2.0 ** 20, -(2.0 ** 20) + 0.37, math.pi * 1000, 1048575.999, 3e5, 1e-3, 0.1] * 3
+    freqs = freqs[:32]
+    positions = [start + i for i in range(T)]
+    f, b = _run(x, ttl.Rotary(freqs, interleaved=inter), t, T, n_q, n_kv, d, None,
+                torch.tensor(positions, dtype=torch.int32, device="cuda"))
+    angle = _reduced(freqs, positions)
+    inside = torch.ones(T, dtype=torch.bool, device="cuda")
+    for n in ("Q", "K"):
+        w = x["gamma_" + n.lower()]
+        y, e = _ref_fwd(x[n][0], w, d, angle.cos(), angle.sin(), inside, inter, 1e-6)
+        _near(f[n][0].view(T, -1, d), y, e, n)
+        dx, e, dg, ge = _ref_bwd(x["d" + n][0], x[n][0], w, d, angle.cos(), angle.sin(), inside, inter, 1e-6)
+        _near(b["d" + n][0].view(T, -1, d), dx, e, "d" + n)
+        _near(b["dgamma_" + n.lower()], dg, ge, "dgamma_" + n.lower())
