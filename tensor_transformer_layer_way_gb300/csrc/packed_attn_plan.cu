@@ -85,16 +85,23 @@ __device__ __forceinline__ int work_class(int work, int shift) {
   return c < kPlanThreads ? c : kPlanThreads - 1;
 }
 
-// Lays the key tiles end to end and cuts the line.  Every thread calls it; scan holds a value a warp.
-__device__ __forceinline__ void lay_out(const PackArgs& A, const PackPlan& P, const int32_t* near, long long* scan, int* joins,
-                                        unsigned long long* whole) {
+// Lays the key tiles end to end and cuts the line.  Every thread calls it; scan holds a value a warp, least one for each work
+// class.
+__device__ __forceinline__ void lay_out(const PackArgs& A, const PackPlan& P, const int32_t* near, int kv_shift, long long* scan,
+                                        int* least, int* joins, unsigned long long* whole) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long* before = P.kv_before;
   long long done = 0;
+  least[tid] = 0x7fffffff;
+  __syncthreads();
   for (int t0 = 0; t0 < P.tiles; t0 += kPlanThreads) {
     const int t = t0 + tid;
-    const long long mine =
-        t < P.tiles ? P.cost + static_cast<long long>(last_tile_of(A, near, t) - t + 1) * A.grp : 0;
+    long long mine = 0;
+    if (t < P.tiles) {
+      const int steps = (last_tile_of(A, near, t) - t + 1) * A.grp;
+      atomicMin(&least[work_class(steps, kv_shift)], steps);
+      mine = P.cost + steps;
+    }
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -117,11 +124,13 @@ __device__ __forceinline__ void lay_out(const PackArgs& A, const PackPlan& P, co
     *whole = 0;
   }
   __syncthreads();
-  // How long whole tiles take at least: some block gets k + 1 of the k blocks + 1 longest.
+  // How long whole tiles take at least: some block gets k + 1 of the k blocks + 1 longest.  (The list is in order by class alone, so
+  // which of a class's tiles stands at a place may differ from run to run, and with it whether tiles are summed in parts: the
+  // shortest of the class speaks for all of them.)
   const long long items = P.kv_list ? static_cast<long long>(P.tiles) * P.lanes : 0;
   for (long long k = tid; k * P.share_blocks < items; k += kPlanThreads) {
     const int4 e = P.kv_list[2 * (k * P.share_blocks / P.lanes)];
-    atomicMax(whole, static_cast<unsigned long long>((k + 1) * (P.cost + e.w - e.z)));
+    atomicMax(whole, static_cast<unsigned long long>((k + 1) * (P.cost + least[work_class(e.w - e.z, kv_shift)])));
   }
   __syncthreads();
   const long long total = done * P.lanes;
@@ -292,7 +301,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const __grid_co
     }
     __syncthreads();
   }
-  if (P.kv_shares && blockIdx.x == 1) lay_out(A, P, near, scan, &joins, &total);
+  if (P.kv_shares && blockIdx.x == 1) lay_out(A, P, near, kv_shift, scan, hist, &joins, &total);
 }
 
 }  // namespace
