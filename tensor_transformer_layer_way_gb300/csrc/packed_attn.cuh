@@ -469,6 +469,26 @@ __device__ __forceinline__ int redo_take(uint32_t& mask, int row0, int (&i)[R]) 
   return n;
 }
 
+// Up to R query rows in `mask`, taken out of it, and the first tokens of their documents.  With a window rows of one document at
+// a time: between the sinks (or windows) of two lies the length of a document that none of the rows sees.
+template <bool W, int R>
+__device__ __forceinline__ int redo_take_queries(const PackArgs& A, uint32_t& mask, int row0, int (&i)[R], int (&lo)[R]) {
+  const int T = static_cast<int>(A.T);
+  uint32_t taken = mask;
+  if constexpr (W) {
+    const int first = doc_of(A.cu, A.batch, T, row0 + __ffs(mask) - 1).lo;
+    taken = 0;
+    for (uint32_t rest = mask; rest; rest &= rest - 1)
+      if (doc_of(A.cu, A.batch, T, row0 + __ffs(rest) - 1).lo == first) taken |= rest & (0u - rest);
+    mask &= ~taken;
+  }
+  const int n = redo_take(taken, row0, i);
+  mask = W ? mask | taken : taken;
+#pragma unroll
+  for (int r = 0; r < R; ++r) lo[r] = doc_of(A.cu, A.batch, T, i[r]).lo;
+  return n;
+}
+
 // The work of one warp: kRedoRows rows together, 32 keys (or queries) at a time.  A lane takes the scores of one of
 // them, and lane l sums columns [l D/32, (l + 1) D/32) of the results.  The rows' ranges differ by a few places (or a
 // document); what a row does not see is left out of its sums, not multiplied by 0.

@@ -455,3 +455,33 @@ def test_long_packs_give_the_same_bits_again(T, docs, n_kv, grp, W, seed):
         same += [(first[n][0] == again[n][0]).all() for n in ("dQ", "dK", "dV")]
     assert torch.stack(same).all()
     assert ttl.device_status() == 0
+
+
+@pytest.mark.parametrize("S", [0, 4])
+def test_a_value_that_is_not_finite_beside_a_border_costs_a_window(S):
+    """Rows of two documents are computed again together: what they read goes with the window, not with the first document."""
+    T, d, W, border = 33000, 64, 64, 32007
+    x = _inputs(1, T, 1, 1, d, [border, 900], 77)
+    kw = dict(n_q=1, n_kv=1, d=d, window=W, sinks=S)
+
+    def times(at):
+        y = {k: [v.clone() for v in m] if k != "cu" else m for k, m in x.items()}
+        for n in ("K", "V"):
+            y[n][0][at, 3] = float("nan")
+        out_f = ttl.packed_window_attn_fwd_buffers(1, T, 1, 1, d, 2, W, S)
+        out_b = ttl.packed_window_attn_bwd_buffers(1, T, 1, 1, d, 2, W, S)
+        best = [math.inf, math.inf]
+        for _ in range(6):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(3)]
+            e[0].record()
+            ttl.packed_window_attn_fwd(y["Q"], y["K"], y["V"], y["cu"], out=out_f, **kw)
+            e[1].record()
+            ttl.packed_window_attn_bwd(y["dO"], y["Q"], y["K"], y["V"], out_f, y["cu"], out=out_b, **kw)
+            e[2].record()
+            torch.cuda.synchronize()
+            best = [min(best[0], e[0].elapsed_time(e[1])), min(best[1], e[1].elapsed_time(e[2]))]
+        return best
+
+    inside, beside = times(20005), times(border - 2)
+    assert ttl.device_status() == 0
+    assert all(b <= 4 * a for a, b in zip(inside, beside)), (inside, beside)
