@@ -27,6 +27,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "head_deal.h"
 #include "launch_after.cuh"
 #include "operands.h"
 #include "pack_docs.h"
@@ -40,7 +41,7 @@ constexpr int kMaxHead = 256;
 constexpr int kMaxPairs = kMaxHead / 2;
 constexpr int kMaxAxes = 8;
 constexpr int kNearDocs = 512;   // document bounds that a block keeps in shared memory
-constexpr int kWarps = 8;
+constexpr int kWarps = kHeadWarps;
 
 enum Mode : int {
   kTurn = 0,      // the rotation alone (backward: by the angles' negatives)
@@ -461,29 +462,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) head_join_kernel(const float*
   }
 }
 
-int lanes_of(int d) {
-  int l = 1;
-  while (l * 16 < d) l *= 2;
-  return l;
-}
-
-// Blocks of a launch, at most: all that the card holds at once.
-template <int MODE>
-constexpr int kMaxBlocks = kResident<MODE> * 152;
-
-// Deals out the work (fills A): returns the blocks.
-template <int MODE>
-unsigned deal(HeadArgs& A) {
-  const int tokens = 32 / lanes_of(A.d);
-  A.groups = (A.T + tokens - 1) / tokens;
-  const int64_t pairs = A.groups * A.t * (A.heads[0] + A.heads[1]), most = static_cast<int64_t>(kMaxBlocks<MODE>) * kWarps;
-  A.warps = pairs < most ? pairs : most;
-  return static_cast<unsigned>((A.warps + kWarps - 1) / kWarps);
-}
-
 template <int MODE>
 int launch(HeadArgs& A, bool neighbours, unsigned& grid, cudaStream_t s) {
-  grid = deal<MODE>(A);
+  const HeadDeal deal = head_deal(A.T, static_cast<int64_t>(A.t) * (A.heads[0] + A.heads[1]), A.d, kResident<MODE>, num_sms());
+  A.groups = deal.groups;
+  A.warps = deal.warps;
+  grid = deal.blocks;
   const double size = static_cast<double>(A.T) * A.t * (A.heads[0] + A.heads[1]) * A.d;
   TraceScope trace(s, TTL_K_NORM, 0.0, size * (MODE == kBackward ? 6.0 : 4.0));
   auto go = [&](auto lanes) {
@@ -495,7 +479,7 @@ int launch(HeadArgs& A, bool neighbours, unsigned& grid, cudaStream_t s) {
     if (rc) return rc;
     return neighbours ? run(head_rotary_kernel<L, true, MODE>) : run(head_rotary_kernel<L, false, MODE>);
   };
-  switch (lanes_of(A.d)) {
+  switch (head_lanes(A.d)) {
     case 1: return go(std::integral_constant<int, 1>{});
     case 2: return go(std::integral_constant<int, 2>{});
     case 4: return go(std::integral_constant<int, 4>{});
@@ -659,7 +643,7 @@ extern "C" int ttl_head_norm_rotary_fwd(int t, int64_t T, int n_q, int n_kv, int
 
 extern "C" size_t ttl_head_norm_rotary_bwd_workspace_size(int t, int64_t T, int n_q, int n_kv, int d) {
   if (check_shape(t, T, n_q, n_kv, d, "ttl_head_norm_rotary_bwd_workspace_size")) return 0;
-  return static_cast<size_t>(kMaxBlocks<kBackward>) * 2 * d * 4;
+  return static_cast<size_t>(kResident<kBackward> * kHeadMostSms) * 2 * d * 4;
 }
 
 extern "C" int ttl_head_norm_rotary_bwd(int t, int64_t T, int n_q, int n_kv, int d, int rot, int interleaved,
