@@ -54,6 +54,8 @@ class PackedStep:
     gamma_k normalise the heads, a `Rotary` rotates them, `window` (with `sinks`) limits what they see."""
 
     def __init__(self, weights, T, batch, *, n_q, n_kv, d, rotary=None, window=None, sinks=0, device="cuda"):
+        if window is None and sinks:
+            raise ValueError("sinks are the first tokens that stay visible behind a window: they need one")
         self.w = weights
         self.t = t = len(weights["E"])
         self.heads = dict(n_q=n_q, n_kv=n_kv, d=d)
@@ -221,5 +223,5 @@ if __name__ == "__main__":
     parser = argparse.ArgumentParser(description="Trains a small model on synthetic packs.")
     parser.add_argument("--rotated", action="store_true", help="normalised and rotated heads")
     parser.add_argument("--window", type=int, help="keys that a query sees up to itself")
-    parser.add_argument("--sinks", type=int, default=0, help="first tokens of a document that stay visible")
+    parser.add_argument("--sinks", type=int, default=0, help="first tokens of a document that stay visible behind the window")
     main(**vars(parser.parse_args()))
