@@ -128,9 +128,14 @@ class PackedStep:
         self.dE = each(Vs, h, dtype=torch.float32)
         self.embed_ws = ttl.embedding_sorted_bwd_workspace(t, T, h, V, device)
 
+    def _check_positions(self, positions):
+        if positions is not None and (self.rotary is None or self.rotary.rot == 0):
+            raise ValueError("positions are the rotation's: this step has none")
+
     def forward(self, ids, target, cu_seqlens, positions=None):
         """The mean loss over all tokens (a tensor of one fp32 value).  `positions` (int32, [axes, T]) are the rotation's;
         by default a token's place in its document."""
+        self._check_positions(positions)
         w = self.w
         ttl.vocab_parallel_embedding_scaled_fwd(ids, w["E"], self.scale, out=self.x0)
         ttl.layer_norm_fwd(self.x0_slabs, w["gamma1"], w["beta1"], out=self.norm1)
@@ -151,6 +156,7 @@ class PackedStep:
 
     def backward(self, ids, cu_seqlens, positions=None):
         """Every weight's gradient, under the weight's name; after forward() on the same pack (and positions)."""
+        self._check_positions(positions)
         w, out = self.w, {}
         tn = dict(a_kmajor=False, b_kmajor=False)
         for i in range(self.t):

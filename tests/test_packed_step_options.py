@@ -28,3 +28,15 @@ def test_the_example_refuses_sinks_without_a_window(ps, monkeypatch):
     monkeypatch.setattr(ps, "init_weights", lambda *a, **k: weights(*a, **dict(k, device="cpu")))
     with pytest.raises(ValueError, match="window"):
         ps.main(steps=1, sinks=4)
+
+
+@pytest.mark.parametrize("head_norm", [False, True])
+def test_positions_need_a_rotation(ps, head_norm):
+    """Without one they would be dropped; with one they go on to the kernels (which take no CPU tensors)."""
+    import torch
+    positions = torch.zeros(1, 128, dtype=torch.int32)
+    w = ps.init_weights(1, 128, 128, 2, 1, 64, 256, head_norm=head_norm, device="cpu")
+    step = ps.PackedStep(w, 128, 2, n_q=2, n_kv=1, d=64, device="cpu")
+    for call in (lambda: step.forward(None, None, None, positions), lambda: step.backward(None, None, positions)):
+        with pytest.raises(ValueError, match="rotation"):
+            call()
