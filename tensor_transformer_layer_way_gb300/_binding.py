@@ -883,17 +883,18 @@ def packed_attn_bwd(dO, Q, K, V, fwd, cu_seqlens, *, n_q, n_kv, d, scale=None, o
 
 # ------------------------------------------------------------------ packed attention over a window
 
-def _window_size(entry, t, T, n_q, n_kv, d, batch, window, sinks):
+def _window_size(size, entry, *shape):
     """The workspace's bytes; raises what is wrong with the arguments."""
-    ws = int(entry(t, T, n_q, n_kv, d, batch, window, sinks))
-    if ws == 0:
-        raise TTLError(TTL_ERR_ARG, last_error())
+    ws = int(size(*shape))
+    if ws == 0:                            # the entry point refuses the same, before it looks at its pointers, and says how
+        raise TTLError(entry(*shape, *[0] * (len(entry.argtypes) - len(shape))), last_error())
     return ws
 
 
 def packed_window_attn_fwd_buffers(t, T, n_q, n_kv, d, batch, window, sinks=0, device="cuda"):
     """Output and workspace buffers of packed_window_attn_fwd."""
-    ws = _window_size(lib().ttl_packed_window_attn_fwd_workspace_size, t, T, n_q, n_kv, d, batch, window, sinks)
+    ws = _window_size(lib().ttl_packed_window_attn_fwd_workspace_size, lib().ttl_packed_window_attn_fwd, t, T, n_q, n_kv, d, batch,
+                      window, sinks)
     return {"O": [torch.empty(T, n_q // t * d, device=device, dtype=torch.bfloat16) for _ in range(t)],
             "lse": [torch.empty(n_q // t, T, device=device) for _ in range(t)],
             "ws": torch.empty(ws, dtype=torch.uint8, device=device)}
@@ -927,7 +928,8 @@ def packed_window_attn_bwd_buffers(t, T, n_q, n_kv, d, batch, window, sinks=0, d
     """Gradient and workspace buffers of packed_window_attn_bwd."""
     qc, kc = n_q // t * d, n_kv // t * d
     e = dict(device=device, dtype=torch.bfloat16)
-    ws = _window_size(lib().ttl_packed_window_attn_bwd_workspace_size, t, T, n_q, n_kv, d, batch, window, sinks)
+    ws = _window_size(lib().ttl_packed_window_attn_bwd_workspace_size, lib().ttl_packed_window_attn_bwd, t, T, n_q, n_kv, d, batch,
+                      window, sinks)
     return {"dQ": [torch.empty(T, qc, **e) for _ in range(t)], "dK": [torch.empty(T, kc, **e) for _ in range(t)],
             "dV": [torch.empty(T, kc, **e) for _ in range(t)], "ws": torch.empty(ws, dtype=torch.uint8, device=device)}
 

@@ -109,3 +109,14 @@ def test_binding_refusals(lib):
         ttl.packed_window_attn_fwd([x], [x], [x], torch.zeros(2, dtype=torch.int32), window=2, n_q=1, n_kv=1, d=64)
     out = ttl.packed_window_attn_fwd_buffers(1, 16, 2, 1, 64, 1, 4, 1, device="cpu")
     assert out["O"][0].shape == (16, 128) and out["lse"][0].shape == (2, 16) and out["ws"].numel() > 0
+
+
+@pytest.mark.parametrize("shape,code", [((1, 16, 2, 1, 96, 1, 4, 0), 2), ((3, 16, 4, 2, 64, 1, 4, 0), 2), ((1, 1 << 28, 2, 1, 64, 1, 4, 0), 2),
+                                        ((1, 16, 3, 2, 64, 1, 4, 0), 2), ((17, 16, 17, 17, 64, 1, 4, 0), 1),
+                                        ((1, 16, 2, 1, 64, -1, 4, 0), 1), ((1, 16, 2, 1, 64, 1, 0, 0), 1), ((1, 16, 2, 1, 64, 1, 4, -1), 1)])
+def test_buffers_raise_the_codes_of_the_entry_points(lib, shape, code):
+    import tensor_transformer_layer_way_gb300 as ttl
+    for buffers in (ttl.packed_window_attn_fwd_buffers, ttl.packed_window_attn_bwd_buffers):
+        with pytest.raises(ttl.TTLError) as e:
+            buffers(*shape, device="cpu")
+        assert e.value.code == code and "ttl_packed_window_attn_" in str(e.value)
