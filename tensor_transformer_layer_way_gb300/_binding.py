@@ -883,6 +883,11 @@ def packed_attn_bwd(dO, Q, K, V, fwd, cu_seqlens, *, n_q, n_kv, d, scale=None, o
 
 # ------------------------------------------------------------------ packed attention over a window
 
+def _view(window, sinks):
+    """Window and sinks as 64-bit integers, in which larger ones would wrap: 2^62 is longer than any document."""
+    return max(-1, min(window, 1 << 62)), max(-1, min(sinks, 1 << 62))
+
+
 def _window_size(size, entry, *shape):
     """The workspace's bytes; raises what is wrong with the arguments."""
     ws = int(size(*shape))
@@ -894,7 +899,7 @@ def _window_size(size, entry, *shape):
 def packed_window_attn_fwd_buffers(t, T, n_q, n_kv, d, batch, window, sinks=0, device="cuda"):
     """Output and workspace buffers of packed_window_attn_fwd."""
     ws = _window_size(lib().ttl_packed_window_attn_fwd_workspace_size, lib().ttl_packed_window_attn_fwd, t, T, n_q, n_kv, d, batch,
-                      window, sinks)
+                      *_view(window, sinks))
     return {"O": [torch.empty(T, n_q // t * d, device=device, dtype=torch.bfloat16) for _ in range(t)],
             "lse": [torch.empty(n_q // t, T, device=device) for _ in range(t)],
             "ws": torch.empty(ws, dtype=torch.uint8, device=device)}
@@ -917,7 +922,7 @@ def packed_window_attn_fwd(Q, K, V, cu_seqlens, *, window, sinks=0, n_q, n_kv, d
         with _made_on(stream):
             out = packed_window_attn_fwd_buffers(t, T, n_q, n_kv, d, bounds - 1, window, sinks, Q[0].device)
     o, ldo = _rows(out["O"], "O", t, bf16, T, qc)
-    _check(lib().ttl_packed_window_attn_fwd(t, T, n_q, n_kv, d, bounds - 1, window, sinks, cu,
+    _check(lib().ttl_packed_window_attn_fwd(t, T, n_q, n_kv, d, bounds - 1, *_view(window, sinks), cu,
                                             d ** -0.5 if scale is None else scale, q, ldq, k, ldk, v, ldv, o, ldo,
                                             _ptrs(out["lse"], "lse", t, torch.float32, (nql, T)), *_space(out["ws"]),
                                             _queue(Q[0], stream)))
@@ -929,7 +934,7 @@ def packed_window_attn_bwd_buffers(t, T, n_q, n_kv, d, batch, window, sinks=0, d
     qc, kc = n_q // t * d, n_kv // t * d
     e = dict(device=device, dtype=torch.bfloat16)
     ws = _window_size(lib().ttl_packed_window_attn_bwd_workspace_size, lib().ttl_packed_window_attn_bwd, t, T, n_q, n_kv, d, batch,
-                      window, sinks)
+                      *_view(window, sinks))
     return {"dQ": [torch.empty(T, qc, **e) for _ in range(t)], "dK": [torch.empty(T, kc, **e) for _ in range(t)],
             "dV": [torch.empty(T, kc, **e) for _ in range(t)], "ws": torch.empty(ws, dtype=torch.uint8, device=device)}
 
@@ -956,7 +961,7 @@ def packed_window_attn_bwd(dO, Q, K, V, fwd, cu_seqlens, *, window, sinks=0, n_q
     dq, lddq = _rows(out["dQ"], "dQ", t, bf16, T, qc)
     dk, lddk = _rows(out["dK"], "dK", t, bf16, T, kc)
     dv, lddv = _rows(out["dV"], "dV", t, bf16, T, kc)
-    _check(lib().ttl_packed_window_attn_bwd(t, T, n_q, n_kv, d, bounds - 1, window, sinks, cu,
+    _check(lib().ttl_packed_window_attn_bwd(t, T, n_q, n_kv, d, bounds - 1, *_view(window, sinks), cu,
                                             d ** -0.5 if scale is None else scale, do, lddo, q, ldq, k, ldk, v, ldv, o, ldo,
                                             _ptrs(fwd["lse"], "lse", t, torch.float32, (nql, T)), dq, lddq, dk, lddk,
                                             dv, lddv, *_space(out["ws"]), _queue(Q[0], stream)))

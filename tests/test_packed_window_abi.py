@@ -120,3 +120,16 @@ def test_buffers_raise_the_codes_of_the_entry_points(lib, shape, code):
         with pytest.raises(ttl.TTLError) as e:
             buffers(*shape, device="cpu")
         assert e.value.code == code and "ttl_packed_window_attn_" in str(e.value)
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 64 + 5, 0), (2 ** 63, 2 ** 64), (5, 2 ** 64), (10 ** 30, 10 ** 30)])
+def test_windows_beyond_64_bits_hide_nothing(lib, window, sinks):
+    """Any size is taken: what the C integer cannot hold is longer than every document."""
+    import tensor_transformer_layer_way_gb300 as ttl
+    from tensor_transformer_layer_way_gb300 import _binding
+    shape = (1, 40000, 32, 32, 64, 1)
+    ws = ttl.lib().ttl_packed_attn_bwd_workspace_size(*shape)
+    got = _binding._window_size(lib.ttl_packed_window_attn_bwd_workspace_size, lib.ttl_packed_window_attn_bwd, *shape,
+                                *_binding._view(window, sinks))
+    assert got == ws
+    assert _binding._view(7, 3) == (7, 3) and _binding._view(-2 ** 70, -2 ** 70) == (-1, -1)
