@@ -454,3 +454,23 @@ def test_large_frequencies_at_far_positions(start, inter):
         dx, e, dg, ge = _ref_bwd(x["d" + n][0], x[n][0], w, d, angle.cos(), angle.sin(), inside, inter, 1e-6)
         _near(b["d" + n][0].view(T, -1, d), dx, e, "d" + n)
         _near(b["dgamma_" + n.lower()], dg, ge, "dgamma_" + n.lower())
+
+
+def _with_empty(total, n, seed):
+    """n lengths, `total` tokens together: some fifty of any size, the rest empty, in any order."""
+    g = torch.Generator().manual_seed(seed)
+    cuts = torch.randint(0, total + 1, (49,), generator=g).sort()[0].tolist()
+    lens = [b - a for a, b in zip([0] + cuts, cuts + [total])] + [0] * (n - 50)
+    return [lens[i] for i in torch.randperm(n, generator=g).tolist()]
+
+
+@pytest.mark.parametrize("n", [512, 513, 2000])
+@pytest.mark.parametrize("norm", [None, torch.bfloat16])
+def test_many_documents(n, norm):
+    """As many as a block keeps in shared memory, one more, and far more: empty ones among them."""
+    t, T, n_q, n_kv, d = 2, 3100, 4, 2, 64
+    cu = [5] + [5 + c for c in torch.tensor(_with_empty(3000, n, n)).cumsum(0).tolist()]
+    x = _inputs(t, T, n_q, n_kv, d, norm, n)
+    freqs = ttl.rotary_freqs(d)
+    f, b = _run(x, ttl.Rotary(freqs), t, T, n_q, n_kv, d, cu)
+    _check(x, f, b, t, T, n_q, n_kv, d, freqs, [0] * (d // 2), False, cu, None)

@@ -555,3 +555,13 @@ def test_the_first_kernel_of_a_call_waits_for_the_callers(T, n_q, n_kv, d, types
     call = lambda: ttl.packed_attn_fwd(x["Q"], x["K"], x["V"], x["cu"], n_q=n_q, n_kv=n_kv, d=d, out=out)   # noqa: E731
     call()
     assert sorted(_edges_into_the_last_kernel(call)) == types
+
+
+@pytest.mark.parametrize("n", [1024, 1025, 1500])
+@pytest.mark.parametrize("T,n_q,n_kv,d", [(4000, 10, 10, 64), (3000, 16, 4, 128)])
+def test_many_documents_and_more_items_than_sms(n, T, n_q, n_kv, d):
+    """As many documents as the plan keeps in shared memory, one more, and far more: some fifty of any size, the rest empty."""
+    lens = _ragged(T - 77, 50, n + T) + [0] * (n - 50)
+    lens = [lens[i] for i in torch.randperm(n, generator=torch.Generator().manual_seed(n)).tolist()]
+    x, fwd, bwd = _run(1, T, n_q, n_kv, d, lens, seed=n)
+    _check(x, fwd, bwd, 1, T, n_q, n_kv, d, lens)

@@ -485,3 +485,19 @@ def test_a_value_that_is_not_finite_beside_a_border_costs_a_window(S):
     inside, beside = times(20005), times(border - 2)
     assert ttl.device_status() == 0
     assert all(b <= 4 * a for a, b in zip(inside, beside)), (inside, beside)
+
+
+def _with_empty(total, n, seed):
+    """n lengths, `total` tokens together: some fifty of any size, the rest empty, in any order."""
+    lens = _ragged(total, 50, seed) + [0] * (n - 50)
+    return [lens[i] for i in torch.randperm(n, generator=torch.Generator().manual_seed(seed)).tolist()]
+
+
+@pytest.mark.parametrize("n", [1024, 1025, 1500])
+@pytest.mark.parametrize("T,n_q,n_kv,d,W,S", [(4000, 10, 10, 64, 70, 3), (3000, 16, 4, 128, 200, 0)])
+def test_many_documents_and_more_items_than_sms(n, T, n_q, n_kv, d, W, S):
+    """As many documents as the plan keeps in shared memory, one more, and far more: empty ones among them."""
+    lens = _with_empty(T - 77, n, n + T)
+    x = _inputs(1, T, n_q, n_kv, d, lens, n)
+    fwd, bwd = _run(x, n_q, n_kv, d, W, S)
+    _check(x, fwd, bwd, 1, T, n_q, n_kv, d, lens, W, S)
