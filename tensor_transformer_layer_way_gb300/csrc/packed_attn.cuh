@@ -469,24 +469,20 @@ __device__ __forceinline__ int redo_take(uint32_t& mask, int row0, int (&i)[R]) 
   return n;
 }
 
-// Up to R query rows in `mask`, taken out of it, and the first tokens of their documents.  With a window rows of one document at
-// a time: between the sinks (or windows) of two lies the length of a document that none of the rows sees.
+// Up to R query rows in `mask`, taken out of it.  With a window those of one document: between the sinks (or windows) of two lies
+// the length of a document that none of the rows sees.
 template <bool W, int R>
-__device__ __forceinline__ int redo_take_queries(const PackArgs& A, uint32_t& mask, int row0, int (&i)[R], int (&lo)[R]) {
-  const int T = static_cast<int>(A.T);
-  uint32_t taken = mask;
+__device__ __forceinline__ void redo_take_queries(const PackArgs& A, uint32_t& mask, int row0, int (&i)[R]) {
   if constexpr (W) {
-    const int first = doc_of(A.cu, A.batch, T, row0 + __ffs(mask) - 1).lo;
-    taken = 0;
-    for (uint32_t rest = mask; rest; rest &= rest - 1)
-      if (doc_of(A.cu, A.batch, T, row0 + __ffs(rest) - 1).lo == first) taken |= rest & (0u - rest);
-    mask &= ~taken;
+    const int at = __ffs(mask) - 1;
+    const DocRange doc = doc_of(A.cu, A.batch, static_cast<int>(A.T), row0 + at);
+    uint32_t same = mask & (bits_between(doc.lo - row0, doc.hi - 1 - row0) | 1u << at);
+    mask &= ~same;
+    redo_take(same, row0, i);
+    mask |= same;
+  } else {
+    redo_take(mask, row0, i);
   }
-  const int n = redo_take(taken, row0, i);
-  mask = W ? mask | taken : taken;
-#pragma unroll
-  for (int r = 0; r < R; ++r) lo[r] = doc_of(A.cu, A.batch, T, i[r]).lo;
-  return n;
 }
 
 // The work of one warp: kRedoRows rows together, 32 keys (or queries) at a time.  A lane takes the scores of one of

@@ -120,7 +120,7 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
     bool looked = false;
     for (uint32_t rows = e.rows; rows;) {
       int i[kRedoRows], lo[kRedoRows];
-      redo_take(rows, at.row0, i);
+      redo_take_queries<W>(A, rows, at.row0, i);
       if (turn++ % warps != w) continue;
       uint32_t again = 0;
 #pragma unroll
@@ -139,10 +139,11 @@ __device__ __noinline__ void redo_rows(const PackArgs& A, RedoList list, int w, 
         }
         if (met) again |= 1u << (i[r] - at.row0);
       }
-      while (again) {
-        const int n = redo_take_queries<W>(A, again, at.row0, i, lo);
-        dq_rows<D, W>(A, S, shard, c, i, lo, n, lane);
-      }
+      if (again == 0) continue;
+      const int n = redo_take(again, at.row0, i);
+#pragma unroll
+      for (int r = 0; r < kRedoRows; ++r) lo[r] = doc_of(A.cu, A.batch, static_cast<int>(A.T), i[r]).lo;
+      dq_rows<D, W>(A, S, shard, c, i, lo, n, lane);
     }
     slot = e.next;
   }
