@@ -206,6 +206,15 @@ __device__ __forceinline__ DocRange doc_of_warp(const int32_t* cu, int batch, in
   return doc_at_warp(cu, batch, T, tok).range;
 }
 
+// Lane l has read the bound c of number b + l, all of them below `end`.  The number, b at least, that 32 stand before the next to
+// read: where all are the same, of documents without tokens, the rest of the run is passed by bisection.  (Out of line: rare, and
+// its code in the kernels cost them 2%.)
+static __device__ __noinline__ int pass_empty(const int32_t* cu, int batch, int b, int c, int end) {
+  const int least = __shfl_sync(0xffffffffu, c, 0);
+  if (least != __shfl_sync(0xffffffffu, c, 31)) return b;
+  return max(b, doc_at_warp(cu, batch, end, least).doc - 31);
+}
+
 // Bit r of begins: a document begins at row r of the tile at q0, v0 < q0 + r < v1, where token v0 is of document `doc`.  By
 // a whole warp: 32 bounds at a time.  (A row's own bisection each took 2000 to 4000 cycles for the tile.)
 __device__ __forceinline__ void begins_in_tile(const int32_t* cu, int batch, int doc, int q0, int v0, int v1,
@@ -220,6 +229,7 @@ __device__ __forceinline__ void begins_in_tile(const int32_t* cu, int batch, int
       begins[u] |= __reduce_or_sync(0xffffffffu, c > v0 && c < v1 && r >= 0 && r < 32 ? 1u << r : 0u);
     }
     go = __all_sync(0xffffffffu, c < v1);
+    if (go) b = pass_empty(cu, batch, b, c, v1);
   }
 }
 

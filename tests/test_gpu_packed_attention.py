@@ -565,3 +565,33 @@ def test_many_documents_and_more_items_than_sms(n, T, n_q, n_kv, d):
     lens = [lens[i] for i in torch.randperm(n, generator=torch.Generator().manual_seed(n)).tolist()]
     x, fwd, bwd = _run(1, T, n_q, n_kv, d, lens, seed=n)
     _check(x, fwd, bwd, 1, T, n_q, n_kv, d, lens)
+
+
+@pytest.mark.parametrize("n", [31, 32, 33, 64, 95, 1000])
+def test_runs_of_empty_documents_inside_a_tile(n):
+    for T, n_q, n_kv, d in ((600, 4, 2, 64), (2000, 24, 8, 128)):
+        lens = [140] + [0] * n + [9] + [0] * 40 + [3, 1, 20] + [0] * n + [T - 200]
+        x, fwd, bwd = _run(1, T, n_q, n_kv, d, lens, seed=n)
+        _check(x, fwd, bwd, 1, T, n_q, n_kv, d, lens)
+
+
+def test_thousands_of_empty_documents_cost_no_reading_of_each():
+    T, n_q, n_kv, d = 8192, 32, 8, 128
+    kw = dict(n_q=n_q, n_kv=n_kv, d=d)
+
+    def best(empty):
+        x = _inputs(1, T, n_q, n_kv, d, [700, 2303] + [0] * empty + [997, 2000, 2192], 4)
+        out = ttl.packed_attn_fwd(x["Q"], x["K"], x["V"], x["cu"], **kw)
+        times = []
+        for _ in range(8):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            torch.cuda._sleep(1000000)
+            a.record()
+            ttl.packed_attn_fwd(x["Q"], x["K"], x["V"], x["cu"], out=out, **kw)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    few, many = best(0), best(20000)
+    assert many <= 2 * few, (few, many)
