@@ -21,7 +21,8 @@
 //
 // What bounds it: bytes, of which it moves 86% (forward) and 80% (backward) of what a plain copy of as many does.
 // Measured: 8192 tokens, 32 and 8 heads of 128 over 8 shards, forward 33 us (5.0 TB/s; one head's words a lane at a time
-// through registers took 51), backward with the weights' gradients 51 us, 3 of them the join of the blocks' sums.  A
+// through registers took 51), backward with the weights' gradients 51 us, 4 of them the join of the blocks' sums (alone on an idle
+// card it takes 6.6).  A
 // look-up of a token's document in memory cost each token group microseconds: the bounds are in shared memory.
 
 #include <cmath>

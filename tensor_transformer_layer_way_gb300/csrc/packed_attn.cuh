@@ -496,8 +496,8 @@ __device__ __forceinline__ void redo_take_queries(const PackArgs& A, uint32_t& m
 }
 
 // The work of one warp: kRedoRows rows together, 32 keys (or queries) at a time.  A lane takes the scores of one of
-// them, and lane l sums columns [l D/32, (l + 1) D/32) of the results.  The rows' ranges differ by a few places (or a
-// document); what a row does not see is left out of its sums, not multiplied by 0.
+// them, and lane l sums columns [l D/32, (l + 1) D/32) of the results.  The rows' ranges differ by a few places (or,
+// without a window, a document); what a row does not see is left out of its sums, not multiplied by 0.
 constexpr int kRedoRows = 4;
 
 template <int D>

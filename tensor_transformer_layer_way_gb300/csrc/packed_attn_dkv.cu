@@ -9,7 +9,8 @@
 // operands; the Q and dO tiles are read K-major for the scores and MN-major for the sums.  Nothing but
 // the four operand tiles passes through shared memory.
 //
-// S^T, dP^T, dK and dV fill tensor memory (4 x 128 columns), so the order of the products is what keeps the
+// S^T, dP^T, dK and dV fill tensor memory (4 x 128 columns; with heads of 64 dK and dV use half of theirs, and 128 columns
+// stay idle), so the order of the products is what keeps the
 // tensor pipe busy: S(n+1), dK(n), dP(n+1), dV(n+1), S(n+2), ...  While the elementwise warps turn S(n+1)
 // into P, dK(n) and dP(n+1) run; while they form dS(n+1), dV(n+1) and S(n+2) do.
 //

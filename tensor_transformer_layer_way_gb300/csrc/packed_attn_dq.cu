@@ -11,7 +11,7 @@
 // form dS_j; warps 2 and 3 bring lse, D and the first key of the coming item's rows to shared memory; warps 4..19
 // form dS: a row per thread, each of the four warpgroups on 32 of the keys (on 64 each, two warpgroups took
 // longer over a tile than the products they run under).
-// S, dP and dQ take 384 columns of tensor memory and two dS buffers the rest.
+// S, dP and dQ take 384 columns of tensor memory (with heads of 64 the half of dQ's stays idle) and two dS buffers the rest.
 //
 // What bounds it: the products' reads of shared memory, 1750 of the 2050 cycles a key tile takes, and 4400 cycles an item
 // beside its key tiles (first row data 550, the last product 700, dQ 2700).  Measured: one document of 16384 tokens, 4

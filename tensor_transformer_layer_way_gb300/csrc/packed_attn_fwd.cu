@@ -25,8 +25,8 @@
 // long document then takes 3200 cycles, with 208 it takes 2700.)
 //
 // What bounds it: the turn of a tile, 2700 cycles (clock stamps: softmax 1300, product and next scores 1100, the rest
-// hand-overs), which the other tile's turn fills up to the products' 2050; tensor memory has no columns left in
-// which the next scores could wait.  Measured: one document of 32768 tokens, 4 query heads and 1 KV head of 128: 645 to 705 us,
+// hand-overs), which the other tile's turn fills up to the products' 2050; with heads of 128 tensor memory has no columns left in
+// which the next scores could wait (with heads of 64 there are 128, not used).  Measured: one document of 32768 tokens, 4 query heads and 1 KV head of 128: 645 to 705 us,
 // 1560 to 1700 TFLOP/s; 8192 tokens in 12 documents, 32 query and 8 KV heads over 8 shards: 92 to 94 us (with items
 // dealt out beforehand 5 more); 16384 tokens, 8 and 2 heads of 64: 292 us.  An item costs 4500 to 5000 cycles beside
 // its key tiles: its rows' documents 900, the wait for the last product 1100, the result 2500.
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) pack_fwd_kernel(const __grid_c
             }
           };
           // Once more where the accumulator had to be rescaled, as the scores' registers are O's meanwhile.  (With a window, whose
-          // tiles are of both kinds in turn, from one copy of the code: 12 documents 105.6 -> 101.2 us; without, whose tiles
+          // tiles are of both kinds in turn, from one copy of the code: 12 documents 102 us, from two 104.5; without, whose tiles
           // are whole for long, behind the first reading: one document of 32768 tokens 665 -> 648 us.)
 #pragma unroll 1
           for (bool again = true; again;) {

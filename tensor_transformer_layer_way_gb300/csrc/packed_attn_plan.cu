@@ -11,7 +11,8 @@
 // With a window key tiles are also laid end to end and cut into even shares (KvShares): most are as long as the window,
 // so whole tiles may leave a part of the SMs idle at the end, and those with sinks are far longer.  Where whole
 // tiles in the list's order should end sooner than shares, which cost each block a part more, they are kept (8192
-// tokens in 12 documents, window 1024: 286 us, in shares 306; 16384 tokens of one, window 2048: 237 us, in shares 203).
+// tokens in 12 documents, window 1024: 286 us, in shares 306; 16384 tokens of one, window 2048: 237 us, in shares 203).  The
+// choice decides in which order dK and dV are summed, so it hangs on lengths alone, on nothing that atomics order.
 
 #include "packed_attn.cuh"
 
