@@ -323,11 +323,11 @@ __global__ void __launch_bounds__(kWarps * 32, kResident<MODE>) head_rotary_kern
       if (n <= 0) continue;
       Pairs ga;
       if constexpr (MODE != kTurn) {
-        float g[16];                              // (idle lanes: what is not used)
+        float g[16];                              // (idle lanes: 0, as of their zeros a weight that is infinite would make NaN)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<float4*>(g + i * 4) =
-              *reinterpret_cast<const float4*>(gamma[kind] + (mine ? c0 + (i & 1) * 4 + (i >> 1) * step : i * 4));
+              mine ? *reinterpret_cast<const float4*>(gamma[kind] + c0 + (i & 1) * 4 + (i >> 1) * step) : make_float4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           ga.a[i] = NEIGHBOURS ? f2_pack(g[4 * i], g[4 * i + 2]) : f2_pack(g[2 * i], g[2 * i + 1]);

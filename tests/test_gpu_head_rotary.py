@@ -474,3 +474,16 @@ def test_many_documents(n, norm):
     freqs = ttl.rotary_freqs(d)
     f, b = _run(x, ttl.Rotary(freqs), t, T, n_q, n_kv, d, cu)
     _check(x, f, b, t, T, n_q, n_kv, d, freqs, [0] * (d // 2), False, cu, None)
+
+
+@pytest.mark.parametrize("d,rot", [(48, 0), (80, 48), (112, 112), (64, 64)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_a_weight_that_is_infinite(d, rot, inter):
+    """Widths that leave lanes idle among them: these add nothing to a head's sums."""
+    freqs = ttl.rotary_freqs(rot)
+    angle = torch.arange(9, dtype=F8, device="cuda")[:, None] * torch.tensor(freqs, dtype=F8, device="cuda")
+    for c in (3, d - 5):
+        x = _inputs(1, 9, 2, 1, d, torch.float32, c)
+        x["gamma_q"][c], x["gamma_k"][c] = math.inf, -math.inf
+        f, b = _run(x, ttl.Rotary(freqs, interleaved=inter), 1, 9, 2, 1, d)
+        _check_same(x, f, b, 9, d, angle.cos(), angle.sin(), inter)
